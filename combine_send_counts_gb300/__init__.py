@@ -26,6 +26,11 @@ The lower-case helpers after them allocate outputs with torch and call the
   options), ``expert_capacity``, ``batched_combine``;
 - ``indices_to_multihot``: the NeMo token dispatchers' routing map and dense
   probabilities;
+- the layer that a decode step runs around the routing, for a few tokens:
+  ``RouterTopk`` / ``router_topk`` (logits, top-k and weights), ``MoeDecode`` /
+  ``moe_decode`` (the experts, bf16 or 4-bit weights, without dispatched
+  rows), ``w4_quantize`` / ``w4_dequantize`` / ``W4`` (4-bit codes with group
+  scales) and ``w4_matvec`` (their product with a few rows);
 - ``workspace``, ``combine_ws``, ``error_word``: scratch and the device error
   word, allocated the way the entry points expect.
 """
@@ -98,6 +103,15 @@ _SIGNATURES = {
     "ep_indices_to_multihot": (_I32, [_VP, _VP, _I64, _I32, _I32, _VP, _VP, _VP, _VP]),
     "ep_dispatch_nosync": (_I32, [_VP, _VP, _VP, _I64, _I32, _I32, _I32, _I32, _I64, _I32, _VP, _VP, _VP, _VP, _VP,
                                   _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP]),
+    "ep_w4_quantize": (_I32, [_VP, _I64, _I64, _I32, _VP, _VP, _VP, _VP]),
+    "ep_w4_dequantize": (_I32, [_VP, _VP, _VP, _I64, _I64, _I32, _VP, _I32, _VP]),
+    "ep_w4_matvec": (_I32, [_VP, _I64, _VP, _VP, _VP, _I64, _I64, _I32, _VP, _I32, _VP]),
+    "ep_router_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "ep_router_topk": (_I32, [_VP, _I64, _I32, _VP, _I32, _I32, _VP, _I32, _I32, _I32, ctypes.c_float, _VP, _VP, _VP,
+                              _VP, _SZ, _VP]),
+    "ep_moe_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "ep_moe_decode": (_I32, [_VP, _VP, _VP, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _SZ,
+                             _VP, _VP]),
 }
 
 EP_SCALE_ROW_F32, EP_SCALE_COL_F32, EP_SCALE_COL_UE8M0 = 0, 1, 2
@@ -125,6 +139,16 @@ class EPPipelineBuffers(ctypes.Structure):
     _fields_ = [("dest", _VP), ("is_in_rank", _VP), ("send_counts", _VP), ("rank_offsets", _VP),
                 ("token_pos", _VP), ("max_rows", _I64), ("n_sets", _I32), ("sets", EPRowSet * 2),
                 ("ws", _VP), ("ws_bytes", _SZ), ("combine_ws", _VP)]
+
+
+EP_W_BF16, EP_W_INT4 = 0, 1
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_MOE_MAX_SLOTS = 1024
+
+
+class EPMatrix(ctypes.Structure):
+    """ep_matrix of include/ep.h."""
+    _fields_ = [("data", _VP), ("scale", _VP), ("zero", _VP), ("format", _I32), ("group", _I32)]
 
 
 LOCAL_KERNEL_DEV_FN = ctypes.CFUNCTYPE(_I32, _VP, _I32, _I64, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP)
@@ -821,3 +845,272 @@ def dispatch_chunked_forward_nosync(x, topk_idx, topk_weights, *, num_local_expe
     out = f(x, topk_idx, topk_weights, err=err, stream=stream)
     torch.cuda.synchronize(x.device)   # the buffers of f die with this call
     return out
+
+
+# ------------------------------------------------ experts for a few tokens --
+def ep_w4_quantize(w, N, K, group, q, scale, zero, stream=None):
+    _check(load().ep_w4_quantize(_p(w), int(N), int(K), int(group), _p(q), _p(scale), _p(zero), _stream(stream)),
+           "ep_w4_quantize")
+
+
+def ep_w4_dequantize(q, scale, zero, N, K, group, w, out_dtype, stream=None):
+    _check(load().ep_w4_dequantize(_p(q), _p(scale), _p(zero), int(N), int(K), int(group), _p(w), int(out_dtype),
+                                   _stream(stream)), "ep_w4_dequantize")
+
+
+def ep_w4_matvec(x, M, q, scale, zero, N, K, group, y, out_dtype, stream=None):
+    _check(load().ep_w4_matvec(_p(x), int(M), _p(q), _p(scale), _p(zero), int(N), int(K), int(group), _p(y),
+                               int(out_dtype), _stream(stream)), "ep_w4_matvec")
+
+
+def ep_router_workspace_size(T: int, H: int, E: int) -> int:
+    return int(load().ep_router_workspace_size(int(T), int(H), int(E)))
+
+
+def ep_router_topk(x, T, H, w, w_dtype, E, bias, K, scoring, renormalize, scale, topk_idx, topk_weights, logits, ws,
+                   stream=None):
+    _check(load().ep_router_topk(_p(x), int(T), int(H), _p(w), int(w_dtype), int(E), _p(bias), int(K), int(scoring),
+                                 int(renormalize), float(scale), _p(topk_idx), _p(topk_weights), _p(logits), _p(ws),
+                                 _nbytes(ws), _stream(stream)), "ep_router_topk")
+
+
+def ep_moe_workspace_size(T: int, K: int, I: int) -> int:
+    return int(load().ep_moe_workspace_size(int(T), int(K), int(I)))
+
+
+def ep_moe_decode(x, topk_idx, topk_weights, T, K, H, I, E, E_local, rank, w13: EPMatrix, w2: EPMatrix, out, out_dtype,
+                  ws, err, stream=None):
+    _check(load().ep_moe_decode(_p(x), _p(topk_idx), _p(topk_weights), int(T), int(K), int(H), int(I), int(E),
+                                int(E_local), int(rank), ctypes.byref(w13), ctypes.byref(w2), _p(out), int(out_dtype),
+                                _p(ws), _nbytes(ws), _p(err), _stream(stream)), "ep_moe_decode")
+
+
+_OUT_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _out_code(where: str, dtype) -> int:
+    if dtype not in _OUT_DTYPES:
+        raise TypeError(f"{where}: out_dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    return _OUT_DTYPES[dtype]
+
+
+def _ready(where: str, name: str, t: torch.Tensor, dtype, shape):
+    """The pointer of a contiguous device tensor of this dtype and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name}: device tensor expected")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name}: contiguous tensor expected")
+    return t.data_ptr()
+
+
+def _on(stream, device):
+    """The context in which `stream` (a stream, a raw handle, or None) is current."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream`: allocated for that stream, so that memory
+    which earlier work of another stream still uses is not handed out."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+class W4:
+    """A weight matrix [..., N, K] in 4-bit codes (EP_W_INT4 of include/ep.h):
+    q [..., N, K/2] uint8 with code 2j of a row in the low half of byte j, scale
+    [..., N, K/group] bf16, zero [..., N, K/group] uint8 (0..15) or None for 8."""
+    __slots__ = ("q", "scale", "zero", "group", "shape", "matrix")
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor], group: int):
+        _expect("W4", q=(q, torch.uint8), scale=(scale, torch.bfloat16), zero=(zero, torch.uint8))
+        if group not in (32, 64, 128):
+            raise ValueError(f"W4: group must be 32, 64 or 128, got {group}")
+        K = 2 * q.shape[-1]
+        want = (*q.shape[:-1], K // group)
+        if q.dim() < 2 or K % group != 0 or tuple(scale.shape) != want or (zero is not None and tuple(zero.shape) != want):
+            raise ValueError(f"W4: q {tuple(q.shape)} in groups of {group} needs scale and zero of {want}")
+        for t in (q, scale, zero):
+            if t is not None and not t.is_contiguous():
+                raise ValueError("W4: contiguous tensor expected")
+        self.q, self.scale, self.zero, self.group = q, scale, zero, group
+        self.shape = torch.Size((*q.shape[:-1], K))
+        self.matrix = EPMatrix(q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(), EP_W_INT4,
+                               group)
+
+    def __getitem__(self, i) -> "W4":
+        """The i-th matrix of a stack of them."""
+        if self.q.dim() < 3:
+            raise IndexError("W4: not a stack of matrices")
+        return W4(self.q[i], self.scale[i], None if self.zero is None else self.zero[i], self.group)
+
+
+def w4_quantize(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=None) -> W4:
+    """4-bit codes of bf16 weights [..., N, K], K % group == 0; zeros: with a zero
+    point for each group instead of codes around 8."""
+    if w.dim() < 2:
+        raise ValueError("w4_quantize: a matrix or a stack of matrices expected")
+    src = _ready("w4_quantize", "w", w, torch.bfloat16, w.shape)
+    K = w.shape[-1]
+    if group not in (32, 64, 128) or K % group != 0 or K == 0:
+        raise ValueError(f"w4_quantize: group must be 32, 64 or 128 and divide {K}, got {group}")
+    N = w.numel() // K
+    q = _empty((*w.shape[:-1], K // 2), torch.uint8, w.device, stream)
+    s = _empty((*w.shape[:-1], K // group), torch.bfloat16, w.device, stream)
+    z = _empty(s.shape, torch.uint8, w.device, stream) if zeros else None
+    _check(load().ep_w4_quantize(src, N, K, group, q.data_ptr(), s.data_ptr(), None if z is None else z.data_ptr(),
+                                 _raw_stream(stream, w.device)), "w4_quantize")
+    return W4(q, s, z, group)
+
+
+def w4_dequantize(w: W4, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values that 4-bit weights stand for, in the shape of the matrices."""
+    code = _out_code("w4_dequantize", out_dtype)
+    out = _empty(w.shape, out_dtype, w.q.device, stream)
+    K = w.shape[-1]
+    m = w.matrix
+    _check(load().ep_w4_dequantize(m.data, m.scale, m.zero, out.numel() // K, K, w.group, out.data_ptr(), code,
+                                   _raw_stream(stream, w.q.device)), "w4_dequantize")
+    return out
+
+
+def w4_matvec(x: torch.Tensor, w: W4, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """x [M,K] bf16 (or one row [K]) times a 4-bit matrix [N,K]: [M,N] (or [N])."""
+    if len(w.shape) != 2:
+        raise ValueError("w4_matvec: one matrix expected")
+    N, K = w.shape
+    M = x.shape[0] if x.dim() == 2 else 1
+    src = _ready("w4_matvec", "x", x, torch.bfloat16, (M, K) if x.dim() != 1 else (K,))
+    code = _out_code("w4_matvec", out_dtype)
+    y = _empty((M, N) if x.dim() == 2 else (N,), out_dtype, x.device, stream)
+    m = w.matrix
+    _check(load().ep_w4_matvec(src, M, m.data, m.scale, m.zero, N, K, w.group, y.data_ptr(), code,
+                               _raw_stream(stream, x.device)), "w4_matvec")
+    return y
+
+
+class RouterTopk:
+    """The router of up to max_tokens tokens: w [E,H] bf16 or fp32, its workspace kept
+    for repeated (or graph-captured) calls, which must not overlap on the GPU.
+
+    scoring: "softmax" or "sigmoid"; bias [E] fp32 is added to the scores to
+    choose experts, not to the weights; renormalize divides the K weights by
+    their sum; scale multiplies them."""
+
+    def __init__(self, w: torch.Tensor, topk: int, *, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
+                 renormalize: bool = True, scale: float = 1.0, max_tokens: int = 128):
+        if scoring not in ("softmax", "sigmoid"):
+            raise ValueError(f"RouterTopk: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+        _expect("RouterTopk", w=(w, (torch.bfloat16, torch.float32)), bias=(bias, torch.float32))
+        E, H = w.shape
+        self._wp = _ready("RouterTopk", "w", w, w.dtype, (E, H))
+        self._bp = None if bias is None else _ready("RouterTopk", "bias", bias, torch.float32, (E,))
+        if not 1 <= topk <= min(E, 32):
+            raise ValueError(f"RouterTopk: topk must be 1 .. min(E, 32), got {topk}")
+        self.w, self.bias, self.E, self.H, self.topk = w, bias, E, H, topk
+        self.scoring, self.renormalize, self.scale, self.max_tokens = scoring, renormalize, float(scale), max_tokens
+        self._tail = (0 if w.dtype == torch.bfloat16 else 1, E, self._bp, topk,
+                      EP_SCORE_SIGMOID if scoring == "sigmoid" else EP_SCORE_SOFTMAX, int(renormalize), self.scale)
+        self.ws = torch.empty(max(ep_router_workspace_size(max_tokens, H, E), 256), dtype=torch.uint8, device=w.device)
+        self._ws = (self.ws.data_ptr(), self.ws.numel())
+
+    def __call__(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None, stream=None):
+        """x [T,H] bf16 -> (topk_idx [T,K] int64, topk_weights [T,K] fp32); logits
+        [T,E] fp32 receives the logits."""
+        T = x.shape[0]
+        src = _ready("RouterTopk", "x", x, torch.bfloat16, (T, self.H))
+        if T > self.max_tokens:
+            raise ValueError(f"RouterTopk: at most {self.max_tokens} tokens, got {T}")
+        lp = None if logits is None else _ready("RouterTopk", "logits", logits, torch.float32, (T, self.E))
+        idx = _empty((T, self.topk), torch.int64, x.device, stream)
+        wts = _empty((T, self.topk), torch.float32, x.device, stream)
+        _check(load().ep_router_topk(src, T, self.H, self._wp, *self._tail, idx.data_ptr(), wts.data_ptr(), lp,
+                                     *self._ws, _raw_stream(stream, x.device)), "RouterTopk")
+        return idx, wts
+
+
+def router_topk(x: torch.Tensor, w: torch.Tensor, topk: int, *, scoring: str = "softmax",
+                bias: Optional[torch.Tensor] = None, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """One call of the router (see RouterTopk): (topk_idx [T,K], topk_weights [T,K])."""
+    with _on(stream, x.device):   # the workspace dies with this call, on the stream that uses it
+        return RouterTopk(w, topk, scoring=scoring, bias=bias, renormalize=renormalize, scale=scale,
+                          max_tokens=x.shape[0])(x)
+
+
+class MoeDecode:
+    """The experts of a mixture-of-experts layer for a few tokens (T * topk <=
+    EP_MOE_MAX_SLOTS): this rank's weights, with a workspace kept for repeated (or
+    graph-captured) calls, which must not overlap on the GPU.
+
+    w13 [E_local, 2*I, H] (gate rows, then up rows) and w2 [E_local, H, I]: bf16
+    tensors, or both W4.  num_experts: experts of all ranks (default: E_local)."""
+
+    def __init__(self, w13, w2, *, topk: int, num_experts: Optional[int] = None, rank: int = 0, max_tokens: int = 64,
+                 out_dtype=torch.bfloat16):
+        if isinstance(w13, W4) != isinstance(w2, W4):
+            raise TypeError("MoeDecode: w13 and w2 must both be W4 or both bf16 tensors")
+        if len(w13.shape) != 3 or len(w2.shape) != 3:
+            raise ValueError("MoeDecode: w13 and w2 must be stacks of one matrix per expert")
+        El, I2, H = w13.shape
+        if I2 % 2 != 0 or tuple(w2.shape) != (El, H, I2 // 2):
+            raise ValueError(f"MoeDecode: w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not belong together")
+        I = I2 // 2
+        if isinstance(w13, W4):
+            self._m13, self._m2, dev = w13.matrix, w2.matrix, w13.q.device
+        else:
+            self._m13 = EPMatrix(_ready("MoeDecode", "w13", w13, torch.bfloat16, (El, I2, H)), None, None, EP_W_BF16, 0)
+            self._m2 = EPMatrix(_ready("MoeDecode", "w2", w2, torch.bfloat16, (El, H, I)), None, None, EP_W_BF16, 0)
+            dev = w13.device
+        E = El if num_experts is None else int(num_experts)
+        if topk < 1 or max_tokens * topk > EP_MOE_MAX_SLOTS:
+            raise ValueError(f"MoeDecode: max_tokens * topk must be at most {EP_MOE_MAX_SLOTS}")
+        self.w13, self.w2, self.E, self.E_local, self.H, self.I = w13, w2, E, El, H, I
+        self.rank, self.topk, self.max_tokens, self.out_dtype = rank, topk, max_tokens, out_dtype
+        self._code = _out_code("MoeDecode", out_dtype)
+        self.err = error_word(dev)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()   # the word is clear before a call on any stream
+        self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, I), 256), dtype=torch.uint8, device=dev)
+        self._mid = (H, I, E, El, rank, ctypes.addressof(self._m13), ctypes.addressof(self._m2))
+        self._ws = (self.ws.data_ptr(), self.ws.numel())
+
+    def __call__(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, out=None, err=None,
+                 stream=None) -> torch.Tensor:
+        """x [T,H] bf16, topk_idx [T,topk] int64, topk_weights [T,topk] fp32 -> this rank's
+        partial [T,H].  Device errors go to err (default: this object's err)."""
+        T, K = x.shape[0], self.topk
+        xp = _ready("MoeDecode", "x", x, torch.bfloat16, (T, self.H))
+        ip = _ready("MoeDecode", "topk_idx", topk_idx, torch.int64, (T, K))
+        wp = _ready("MoeDecode", "topk_weights", topk_weights, torch.float32, (T, K))
+        if T > self.max_tokens:
+            raise ValueError(f"MoeDecode: at most {self.max_tokens} tokens, got {T}")
+        if out is None:
+            out = _empty((T, self.H), self.out_dtype, x.device, stream)
+            op = out.data_ptr()
+        else:
+            op = _ready("MoeDecode", "out", out, self.out_dtype, (T, self.H))
+        _check(load().ep_moe_decode(xp, ip, wp, T, K, *self._mid, op, self._code, *self._ws,
+                                    (self.err if err is None else err).data_ptr(), _raw_stream(stream, x.device)),
+               "MoeDecode")
+        return out
+
+
+def moe_decode(x, topk_idx, topk_weights, w13, w2, *, num_experts: Optional[int] = None, rank: int = 0,
+               out_dtype=torch.bfloat16, err=None, stream=None) -> torch.Tensor:
+    """One call of the experts for a few tokens (see MoeDecode)."""
+    with _on(stream, x.device):   # the workspace dies with this call, on the stream that uses it
+        return MoeDecode(w13, w2, topk=topk_idx.shape[1], num_experts=num_experts, rank=rank, max_tokens=x.shape[0],
+                         out_dtype=out_dtype)(x, topk_idx, topk_weights, err=err)

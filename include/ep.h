@@ -522,6 +522,115 @@ int ep_compute_send_counts_noalloc(const int64_t *topk_idx, int64_t T, int K, in
                                    int32_t *rank_offsets, int32_t *tokens_per_expert,
                                    int32_t *err, ep_stream_t stream);
 
+/* ------------------------------------------------- experts for a few tokens --
+ * The layer that a decode step runs around the routing above, for as many
+ * tokens as a decode batch has: the router that makes topk_idx and
+ * topk_weights, the experts themselves (bf16 or 4-bit weights), and the 4-bit
+ * matrix-vector product for the projections beside them.  Inference only.
+ *
+ * A weight matrix [N, K] is row-major, in one of two formats:
+ *   EP_W_BF16: data [N,K] bf16; scale, zero NULL, group 0.  K % 8 == 0.
+ *   EP_W_INT4: 4-bit codes with one scale for each group of `group` columns
+ *     (32, 64 or 128; K % group == 0): data [N, K/2] uint8 holds code 2j of a
+ *     row in the low and code 2j+1 in the high half of byte j; scale
+ *     [N, K/group] bf16; zero [N, K/group] uint8, values 0..15, or NULL for 8
+ *     everywhere.  w[n,k] = (q[n,k] - zero[n,k/group]) * scale[n,k/group].
+ * data must start 16-byte aligned; scale and zero need their type's own
+ * alignment.  A matrix per expert is stored one after the other. */
+#define EP_W_BF16 0
+#define EP_W_INT4 1
+
+typedef struct ep_matrix {
+    const void *data;
+    const void *scale;
+    const uint8_t *zero;
+    int format;                /* EP_W_BF16 or EP_W_INT4 */
+    int group;                 /* 32, 64 or 128 for EP_W_INT4, else 0 */
+} ep_matrix;
+
+/* 4-bit codes of a bf16 matrix w [N,K] (several matrices of K columns may be
+ * passed as one).  Per group, in fp32 with each operation rounded to nearest:
+ *   zero == NULL: s = bf16(max|w| / 7), q = clamp(rint(w / s), -8, 7) + 8;
+ *   else lo = min(min w, 0), hi = max(max w, 0), s = bf16(hi/15 - lo/15),
+ *     zero = clamp(rint(-lo / s), 0, 15), q = clamp(rint(w / s) + zero, 0, 15).
+ * A group with s == 0 gets the codes of zero (zero point 8 or 0).  A group
+ * that holds a NaN or an infinity gets s = +inf and codes equal to its zero
+ * point (8 or 0), so that it reads back as NaN instead of as numbers. */
+int ep_w4_quantize(const void *w, int64_t N, int64_t K, int group, uint8_t *q, void *scale, uint8_t *zero,
+                   ep_stream_t stream);
+
+/* The values that 4-bit codes stand for: w [N,K], bf16 (out_dtype 0, the
+ * exact product rounded once) or fp32 (out_dtype 1, exact). */
+int ep_w4_dequantize(const uint8_t *q, const void *scale, const uint8_t *zero, int64_t N, int64_t K, int group,
+                     void *w, int out_dtype, ep_stream_t stream);
+
+/* y[m,n] = sum over k of x[m,k] * w[n,k] for a 4-bit matrix w [N,K]:
+ *   x [M,K] bf16, y [M,N] bf16 (out_dtype 0) or fp32 (out_dtype 1).
+ * Sums are fp32: a group's codes are summed first, then scaled, and rounded
+ * once at the end.  Any M >= 0; the weights are read once for each 32 rows of
+ * x, so it is meant for a few rows.  The same call on the same inputs gives
+ * the same bits. */
+int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const void *scale, const uint8_t *zero, int64_t N,
+                 int64_t K, int group, void *y, int out_dtype, ep_stream_t stream);
+
+/* The router: logits l[t,e] = sum over h of x[t,h] * w[e,h] (fp32 sums), and
+ * the K experts of each token with their weights, as every call above takes
+ * them.
+ *   x [T,H] bf16, H % 8 == 0; w [E,H] bf16 (w_dtype 0) or fp32 (w_dtype 1).
+ *   scoring EP_SCORE_SOFTMAX: score = softmax of the token's logits over all E;
+ *           EP_SCORE_SIGMOID: score = 1 / (1 + exp(-l)).
+ *   bias [E] fp32 or NULL: experts are chosen by key = score + bias[e], or by
+ *     key = l without a bias; it never enters the weights.  Keys of NaN or
+ *     -inf are never chosen (a bias of -inf masks an expert); a NaN logit
+ *     counts as -inf.
+ *   topk_idx [T,K] int64, topk_weights [T,K] fp32: the K largest keys in
+ *     descending order, the lower expert id first on equal keys; -1 with
+ *     weight +0 where fewer than K experts can be chosen.
+ *   topk_weights = score, divided by the sum of the K chosen scores when
+ *     renormalize != 0 (+0 where that sum is 0), times `scale`.
+ *   logits [T,E] fp32 or NULL.
+ *   ws: ep_router_workspace_size(T, H, E) bytes, 256-byte aligned, scratch.
+ *     Calls that overlap on the GPU must not share it.
+ * The same call on the same inputs gives the same bits.
+ * 1 <= K <= min(E, 32), E <= 8192. */
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+size_t ep_router_workspace_size(int64_t T, int H, int E);
+int ep_router_topk(const void *x, int64_t T, int H, const void *w, int w_dtype, int E, const float *bias, int K,
+                   int scoring, int renormalize, float scale, int64_t *topk_idx, float *topk_weights,
+                   float *logits, void *ws, size_t ws_bytes, ep_stream_t stream);
+
+/* The experts of a mixture-of-experts layer for a few tokens, without a
+ * dispatched copy of any row: this rank's partial
+ *   out[t] = sum over k ascending, for topk_idx[t,k] naming a local expert
+ *            e_l = topk_idx[t,k] - rank*E_local, of topk_weights[t,k] * y_k,
+ *   y_k = W2[e_l] h_k,   h_k = silu(Wg[e_l] x[t]) * (Wu[e_l] x[t]),
+ * where silu(a) = a / (1 + exp(-a)), sums are fp32 and the result is rounded
+ * once.  Only the experts that some token names are read, each once for every
+ * 32 slots that name it.  With E_local = E (rank 0) it is the whole layer;
+ * else the ranks' partials add up to it, like those of ep_batched_combine.
+ *   x [T,H] bf16, topk_idx [T,K] int64 (-1 = unrouted), topk_weights [T,K] fp32.
+ *   w13: per local expert [2*I, H], the I rows of Wg before the I rows of Wu;
+ *   w2: per local expert [H, I]; both in the same format and group.  H % 8 ==
+ *     0 and I % 8 == 0, and a 4-bit group divides both.  Weights must be
+ *     finite (a slot's infinite or NaN sums stay its own).
+ *   out [T,H]: bf16 (out_dtype 0) or fp32 (out_dtype 1); tokens without a local
+ *     expert give +0.  Weights of slots that name no local expert are not read
+ *     as numbers.
+ *   T * K <= EP_MOE_MAX_SLOTS (else EP_ERR_UNSUPPORTED: larger batches take the
+ *     dispatch and combine calls).
+ *   ws: ep_moe_workspace_size(T, K, I) bytes, 256-byte aligned, scratch.  Calls
+ *     that overlap on the GPU must not share it.
+ * The same call on the same inputs gives the same bits.  The sums' order
+ * depends on the batch, so a token's last bits may differ between batches.
+ * Device errors: EP_ERR_INVALID_EXPERT (an id outside [-1, E): the slot is
+ * ignored). */
+#define EP_MOE_MAX_SLOTS 1024
+size_t ep_moe_workspace_size(int64_t T, int K, int I);
+int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weights, int64_t T, int K, int H,
+                  int I, int E, int E_local, int rank, const ep_matrix *w13, const ep_matrix *w2, void *out,
+                  int out_dtype, void *ws, size_t ws_bytes, int32_t *err, ep_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
