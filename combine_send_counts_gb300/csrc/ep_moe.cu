@@ -5,21 +5,24 @@
 //   down:  out[t] = sum over k of w[t,k] * (W2 h[t,k]).
 //
 // Each expert that some token names has its matrices read once for all its
-// slots (up to 32 at a time), by products of 16 weight rows with the slots as
-// columns (ep_skinny.cuh).  No row of x is copied to an expert and no list is
-// made on the host: every block derives the experts in use and their slots
-// from topk_idx, which a graph replay may have changed.
+// slots (32 at a time), by products of 16 weight rows with the slots as columns
+// (ep_skinny.cuh).  No row of x is copied to an expert and no list is made on
+// the host: every block derives the experts in use and their slots from
+// topk_idx, which a graph replay may have changed.
 //
-// up's 16 rows are 8 gate rows and the 8 up rows of the same elements, which
-// the matrix step's accumulators hold in the same lane; a block is one of a
-// resident wave and takes (expert, 8 elements) units, whose columns S of its
-// warps share, S chosen so that the units fill the wave evenly.
+// up: the elements of h of all experts in use, laid end to end, are dealt to
+// one block per SM in equal runs.  An item is 8 elements: their 8 gate rows and
+// 8 up rows are the 16 rows of a matrix step, whose accumulators hold gate and
+// up of an element in the same lane.
 //
-// down gives 16 rows of the output to a thread-block cluster, whose warps
-// share the experts (and their columns when there are fewer experts than
-// warps).  Each slot's 16 partial results stay in the shared memory of the
-// block that made them and are weighted and added from there in ascending k,
-// so nothing but out is written and nothing depends on the order of arrival.
+// down: each block owns an equal share of the output's rows and adds up all
+// experts for them.  An item is up to 16 of its rows of one expert.  Every
+// slot's results stay in shared memory and are weighted and added from there in
+// ascending k, so nothing but out is written.
+//
+// In both the block's items are shared evenly by its warps, whose runs may stop
+// inside an item; the pieces of a divided item are added in the order of their
+// columns.  Nothing depends on the order of arrival.
 //
 // h is kept as the bf16 terms of a sum (two terms, or three for fp32 results:
 // 16 or 24 significant bits), which is what the matrix step takes; one bf16
@@ -33,17 +36,11 @@
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBlocks8 = 4;          // blocks of 8 slots in one pass over the weights
+constexpr int kThreads = kSkinnyThreads;
+constexpr int kWarps = kSkinnyWarps;
 constexpr int kMaxSlots = EP_MOE_MAX_SLOTS;
-constexpr int kRow = 20;                // floats between slots in shared memory: 16 rows, no bank conflicts
-
-struct Weights {
-    const uint8_t *data;
-    const uint16_t *scale;
-    const uint8_t *zero;
-};
+constexpr int kMaxDim = 65536;   // H and I: a block's units are counted in 32 bits
+constexpr int kRow = 17;   // floats between slots in shared memory, for 16 rows
 
 struct Routing {
     const int64_t *idx;
@@ -64,102 +61,114 @@ struct Routing {
     }
 };
 
-// The experts in use and the slots of each, in shared memory.
+// The experts in use, in entries of up to 32 slots each, in shared memory.
 struct Lists {
-    int active;                       // experts in use
-    int warp_sum[kWarps], warp_used[kWarps];
-    uint16_t expert[kMaxSlots];       // [active]
-    uint16_t begin[kMaxSlots + 1];    // slots of the j-th: slot[begin[j] .. begin[j+1])
+    int entries, big;
+    int scan[3][kWarps];
+    uint16_t big_expert[kMaxSlots / kMaxCols];   // experts of more than one entry
+    int cost[kMaxSlots + 1];          // exclusive sums of the entries' costs per weight row
+    uint16_t expert[kMaxSlots];
+    uint16_t begin[kMaxSlots + 1];    // slots of entry q: slot[begin[q] .. begin[q+1])
     uint16_t slot[kMaxSlots];
-    int16_t use[kMaxSlots];           // slot -> j, or -1
-    uint16_t place[kMaxSlots];
+    int16_t use[kMaxSlots];           // slot -> its entry, or -1
+    uint16_t place[kMaxSlots];        // slot -> its place among its expert's slots
 };
 
-// All threads of the block; count: E_local ints of shared memory.
-__device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *count, int32_t *err)
+__device__ __forceinline__ int blocks_of(int cols) { return (cols + 7) >> 3; }
+
+// All threads of the block; count: E_local ints of shared memory.  An entry of
+// nb column blocks costs item_cost + nb for each row.
+__device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *count, int item_cost, int32_t *err)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < r.E_local; e += kThreads)
         count[e] = 0;
+    if (tid == 0)
+        l.big = 0;
     __syncthreads();
     for (int s = tid; s < r.n; s += kThreads) {
         const int e = r.local(s, err);
         l.use[s] = (int16_t)e;
         if (e >= 0)
-            l.place[s] = (uint16_t)atomicAdd(&count[e], 1);   // the order within an expert moves no result
+            l.place[s] = (uint16_t)atomicAdd(&count[e], 1);
     }
     __syncthreads();
-    // each thread owns a run of experts; scan of (experts in use, slots)
+    // each thread owns a run of experts; scan of (entries, slots, cost)
     const int per = (r.E_local + kThreads - 1) / kThreads;
     const int e0 = min(tid * per, r.E_local), e1 = min(e0 + per, r.E_local);
-    int used = 0, slots = 0;
+    int own[3] = {0, 0, 0};
     for (int e = e0; e < e1; ++e) {
-        used += count[e] > 0;
-        slots += count[e];
+        const int c = count[e], full = c / kMaxCols, rest = c % kMaxCols;
+        own[0] += full + (rest > 0);
+        own[1] += c;
+        own[2] += full * (item_cost + kMaxCols / 8) + (rest > 0 ? item_cost + blocks_of(rest) : 0);
     }
-    int su = used, ss = slots;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(kFull, su, o), b = __shfl_up_sync(kFull, ss, o);
-        if (lane >= o) {
-            su += a;
-            ss += b;
+    int sum[3] = {own[0], own[1], own[2]};
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int v = __shfl_up_sync(kFull, sum[i], o);
+            if (lane >= o)
+                sum[i] += v;
         }
-    }
-    if (lane == 31) {
-        l.warp_used[warp] = su;
-        l.warp_sum[warp] = ss;
-    }
+    if (lane == 31)
+        for (int i = 0; i < 3; ++i)
+            l.scan[i][warp] = sum[i];
     __syncthreads();
-    int j = su - used, at = ss - slots;
-    for (int w = 0; w < warp; ++w) {
-        j += l.warp_used[w];
-        at += l.warp_sum[w];
+    for (int i = 0; i < 3; ++i) {
+        sum[i] -= own[i];
+        for (int w = 0; w < warp; ++w)
+            sum[i] += l.scan[i][w];
     }
+    int q = sum[0], at = sum[1], cost = sum[2];
     for (int e = e0; e < e1; ++e) {
         const int c = count[e];
-        if (c > 0) {
-            l.expert[j] = (uint16_t)e;
-            l.begin[j] = (uint16_t)at;
-            count[e] = j++;
-            at += c;
+        count[e] = q;
+        if (c > kMaxCols)
+            l.big_expert[atomicAdd(&l.big, 1)] = (uint16_t)e;
+        for (int b = 0; b < c; b += kMaxCols) {
+            const int cols = min(c - b, kMaxCols);
+            l.expert[q] = (uint16_t)e;
+            l.begin[q] = (uint16_t)(at + b);
+            l.cost[q] = cost;
+            cost += item_cost + blocks_of(cols);
+            ++q;
         }
+        at += c;
     }
     if (tid == kThreads - 1) {
-        l.active = j;
-        l.begin[j] = (uint16_t)at;
+        l.entries = q;
+        l.begin[q] = (uint16_t)at;
+        l.cost[q] = cost;
     }
     __syncthreads();
+    // The order of slots within an entry moves no result, but every block must put the same slots into an
+    // entry: where an expert has several, its slots take their places in ascending order.
+    if (l.big > 0) {
+        for (int b = warp; b < l.big; b += kWarps) {
+            const int e = l.big_expert[b];
+            int before = 0;
+            for (int s0 = 0; s0 < r.n; s0 += 32) {
+                const int s = s0 + lane;
+                const bool hit = s < r.n && l.use[s] == e;
+                const unsigned m = __ballot_sync(kFull, hit);
+                if (hit)
+                    l.place[s] = (uint16_t)(before + __popc(m & lanemask_lt()));
+                before += __popc(m);
+            }
+        }
+        __syncthreads();
+    }
     for (int s = tid; s < r.n; s += kThreads) {
         const int e = l.use[s];
         if (e >= 0) {
-            const int jj = count[e];
-            l.slot[l.begin[jj] + l.place[s]] = (uint16_t)s;
-            l.use[s] = (int16_t)jj;
+            const int p = l.place[s], f = count[e];
+            l.slot[l.begin[f] + p] = (uint16_t)s;
+            l.use[s] = (int16_t)(f + p / kMaxCols);
         }
     }
     __syncthreads();
 }
-
-// The weight format of a kernel: G = 0 for bf16, else the group of 4-bit codes.
-template <int G, bool PERMUTED>
-struct Format {
-    using Rows = RowsW4<G, PERMUTED>;
-    static __device__ __forceinline__ Rows rows(const Weights &w, int64_t a, int64_t b, int K)
-    {
-        const int64_t bytes = K / 2, groups = K / G;
-        return Rows{w.data + a * bytes, w.data + b * bytes, w.scale + a * groups, w.scale + b * groups,
-                    w.zero != nullptr ? w.zero + a * groups : nullptr, w.zero != nullptr ? w.zero + b * groups : nullptr};
-    }
-};
-template <bool PERMUTED>
-struct Format<0, PERMUTED> {
-    using Rows = RowsBf16;
-    static __device__ __forceinline__ Rows rows(const Weights &w, int64_t a, int64_t b, int K)
-    {
-        const int64_t bytes = (int64_t)K * 2;
-        return Rows{w.data + a * bytes, w.data + b * bytes};
-    }
-};
 
 struct Planes {
     uint8_t *h;            // [PLANES][n][I] bf16
@@ -186,34 +195,26 @@ __device__ __forceinline__ void store_planes(const Planes &p, int slot, int i, f
     }
 }
 
-// (the truncated form above would turn a NaN whose payload sits in the low half into an infinity)
-__device__ __forceinline__ float quiet(float v) { return isnan(v) ? __int_as_float(0x7fffffff) : v; }
-
-__device__ __forceinline__ void group_sync(int id, int threads)
+// silu(gate) * up; a NaN keeps its set bits in the upper half, where the terms above look
+__device__ __forceinline__ float activate(float gate, float up)
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+    const float h = __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up);
+    return isnan(h) ? __int_as_float(0x7fffffff) : h;
 }
 
-// slots [base, base + 8*NT) of the list [first, end) times 16 rows, one warp's columns [u0, u1)
-template <class F, int PLANES, int NT>
-__device__ __forceinline__ void pass(const F &f, const Lists &l, int first, int end, const uint8_t *cols,
-                                     int64_t row_bytes, int slots_per_row, int64_t plane_bytes, int u0, int u1, int K,
-                                     float (&acc)[NT][4])
+template <int NT, int PLANES>
+__device__ __forceinline__ void set_columns(const Lists &l, int q, const uint8_t *rows, int64_t row_bytes,
+                                            int slots_per_row, Columns<NT, PLANES> &x)
 {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    Columns<NT, PLANES> x;
-    x.plane_bytes = plane_bytes;
+    const int g = (threadIdx.x & 31) >> 2, first = l.begin[q], end = l.begin[q + 1];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int q = first + nt * 8 + g;
-        x.p[nt] = q < end ? cols + (int64_t)(l.slot[q] / slots_per_row) * row_bytes : nullptr;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            acc[nt][c] = 0.0f;
+        const int s = first + nt * 8 + g;
+        x.p[nt] = s < end ? rows + (int64_t)(l.slot[s] / slots_per_row) * row_bytes : nullptr;
     }
-    skinny<F, NT, PLANES>(f, u0, u1, K, t, x, acc);
 }
 
+// ------------------------------------------------------------------------ up --
 struct UpArgs {
     const uint8_t *x;
     Routing r;
@@ -223,98 +224,163 @@ struct UpArgs {
     int32_t *err;
 };
 
-template <int G, int PLANES, int NT>
-__device__ __forceinline__ void up_unit(const UpArgs &a, const Lists &l, int j, int tile, int base, int S, int part,
-                                        int sub, float *red)
-{
-    using F = typename Format<G, false>::Rows;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int first = l.begin[j] + base, end = l.begin[j + 1];
-    const int64_t row = (int64_t)l.expert[j] * 2 * a.I + tile * 8 + g;
-    const F f = Format<G, false>::rows(a.w, row, row + a.I, a.H);
-    const int units = (a.H + F::kUnit - 1) / F::kUnit;
-    float acc[NT][4];
-    pass<F, 1, NT>(f, l, first, end, a.x, (int64_t)a.H * 2, a.r.K, 0, units * part / S, units * (part + 1) / S, a.H,
-                   acc);
-    auto emit = [&](int q, float gate, float up) {
-        const float h = quiet(__fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up));
-        return h;
-    };
-    if (S == 1) {
+// A block's elements: from element i0 of entry q0 to element i1 of entry q1
+// (exclusive), in items of 8 elements that do not cross entries.
+template <int G, int PLANES>
+struct UpItems {
+    using F = typename FormatOf<G, false>::F;
+    const UpArgs &a;
+    const Lists &l;
+    int q0, i0, q1, i1;
+    int head, body;        // items of the first entry, items of each further one
+    float *side;           // this warp's kept piece of an item that another warp began
+    float *open;           // its kept piece of an item that it began and another goes on with
+
+    __device__ __forceinline__ int count() const
+    {
+        return q1 > q0 ? head + (q1 - q0 - 1) * body + (i1 + 7) / 8 : head;
+    }
+
+    __device__ __forceinline__ void where(int item, int &q, int &i, int &end) const
+    {
+        if (item < head) {
+            q = q0;
+            i = i0 + item * 8;
+        } else {
+            const int v = item - head;
+            q = q0 + 1 + v / body;
+            i = v % body * 8;
+        }
+        end = min(i + 8, q == q1 ? i1 : a.I);
+    }
+
+    __device__ __forceinline__ RowPtrs rows(int item) const
+    {
+        int q, i, end;
+        where(item, q, i, end);
+        i += (threadIdx.x & 31) >> 2;
+        const int64_t row = (int64_t)l.expert[q] * 2 * a.I + i;
+        return F::rows(a.w, row, row + a.I, i < end, i < end, a.H);
+    }
+
+    __device__ __forceinline__ int blocks(int item) const
+    {
+        int q, i, end;
+        where(item, q, i, end);
+        return blocks_of(l.begin[q + 1] - l.begin[q]);
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void columns(int item, Columns<NT, 1> &x) const
+    {
+        int q, i, end;
+        where(item, q, i, end);
+        x.plane_bytes = 0;
+        set_columns<NT, 1>(l, q, a.x, (int64_t)a.H * 2, a.r.K, x);
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void done(int item, bool first, bool last, float (&acc)[NT][4]) const
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        if (!first || !last) {
+            float *keep = first ? open : side;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                *reinterpret_cast<float4 *>(keep + (nt * 32 + lane) * 4) =
+                    make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+            return;
+        }
+        int q, i, end;
+        where(item, q, i, end);
+        if (i + g >= end)
+            return;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int q = first + nt * 8 + 2 * t + c;
-                if (q < end)
-                    store_planes<PLANES, (G > 0)>(a.out, l.slot[q], tile * 8 + g, emit(q, acc[nt][c], acc[nt][2 + c]));
+                const int s = l.begin[q] + nt * 8 + 2 * t + c;
+                if (s < l.begin[q + 1])
+                    store_planes<PLANES, (G > 0)>(a.out, l.slot[s], i + g, activate(acc[nt][c], acc[nt][2 + c]));
             }
-        return;
     }
-    // the S warps' partial sums, added in ascending order of their columns
-    float *mine = red + (size_t)part * NT * 128;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<float4 *>(mine + (nt * 32 + lane) * 4) =
-            make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-    group_sync(1 + sub, 32 * S);
-    for (int v = part * 32 + lane; v < NT * 64; v += 32 * S) {
-        // v: (block, lane that held it, which of its two columns)
-        const int c = v & 1, src = (v >> 1) & 31, nt = v >> 6;
-        const int q = first + nt * 8 + 2 * (src & 3) + c;
-        if (q < end) {
-            float gate = 0.0f, up = 0.0f;
-            for (int s = 0; s < S; ++s) {
-                const float *p = red + ((size_t)s * NT * 32 + nt * 32 + src) * 4;
-                gate = __fadd_rn(gate, p[c]);
-                up = __fadd_rn(up, p[2 + c]);
-            }
-            store_planes<PLANES, (G > 0)>(a.out, l.slot[q], tile * 8 + (src >> 2), emit(q, gate, up));
-        }
+};
+
+// the entry and element at position pos of the costs laid end to end
+__device__ __forceinline__ void find(const Lists &l, int I, int64_t pos, int &q, int &i)
+{
+    int lo = 0, hi = l.entries;   // cost[lo] * I <= pos < cost[hi] * I
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)l.cost[mid] * I <= pos)
+            lo = mid;
+        else
+            hi = mid;
     }
-    group_sync(1 + sub, 32 * S);   // the sums are read before the next unit's overwrite them
+    q = lo;
+    i = (int)((pos - (int64_t)l.cost[lo] * I) / (l.cost[lo + 1] - l.cost[lo]));
 }
 
 template <int G, int PLANES>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
 moe_up_kernel(UpArgs a)
 {
-    extern __shared__ __align__(16) uint8_t dynamic[];
+    extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
     __shared__ Lists l;
-    int *count = reinterpret_cast<int *>(dynamic);
-    float *red = reinterpret_cast<float *>(dynamic);   // after the lists are built
+    using F = typename FormatOf<G, false>::F;
     grid_dependency_wait();
     allow_dependents();
-    build_lists(a.r, l, count, blockIdx.x == 0 ? a.err : nullptr);
-    const int warp = threadIdx.x >> 5;
-    const int tiles = a.I / 8;
-    const int64_t units = (int64_t)l.active * tiles;
-    // S warps to a unit: the S in 1, 2, 4, 8 that leaves the fullest last wave, the smaller on a tie
-    const int64_t W = (int64_t)gridDim.x * kWarps;
-    int S = 1;
-    int64_t best = (units + W - 1) / W * kWarps;   // rounds, in eighths of a unit's time
-    for (int s = 2; s <= kWarps; s *= 2) {
-        const int64_t cost = (units * s + W - 1) / W * (kWarps / s);
-        if (cost < best) {
-            best = cost;
-            S = s;
-        }
+    build_lists(a.r, l, reinterpret_cast<int *>(dynamic), F::kItemCost, blockIdx.x == 0 ? a.err : nullptr);
+    if (l.entries == 0)
+        return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *sides = dynamic + kRingBytes;
+    UpItems<G, PLANES> items{a, l};
+    const int64_t total = (int64_t)l.cost[l.entries] * a.I;
+    find(l, a.I, total * blockIdx.x / gridDim.x, items.q0, items.i0);
+    if (blockIdx.x + 1 < gridDim.x) {
+        find(l, a.I, total * (blockIdx.x + 1) / gridDim.x, items.q1, items.i1);
+    } else {
+        items.q1 = l.entries;
+        items.i1 = 0;
     }
-    const int sub = warp / S, part = warp % S, subs = kWarps / S;
-    float *mine = red + (size_t)sub * S * kMaxBlocks8 * 128;
-    for (int64_t u = (int64_t)blockIdx.x * subs + sub; u < units; u += (int64_t)gridDim.x * subs) {
-        const int j = (int)(u / tiles), tile = (int)(u % tiles);
-        const int m = l.begin[j + 1] - l.begin[j];
-        int base = 0;
-        for (; m - base > 16; base += 32)
-            up_unit<G, PLANES, 4>(a, l, j, tile, base, S, part, sub, mine);
-        if (m - base > 8)
-            up_unit<G, PLANES, 2>(a, l, j, tile, base, S, part, sub, mine);
-        else if (m - base > 0)
-            up_unit<G, PLANES, 1>(a, l, j, tile, base, S, part, sub, mine);
+    items.head = ((items.q1 > items.q0 ? a.I : items.i1) - items.i0 + 7) / 8;
+    items.body = (a.I + 7) / 8;
+    items.side = reinterpret_cast<float *>(sides + warp * kSideBytes);
+    items.open = reinterpret_cast<float *>(dynamic + warp * (kStages * kStageBytes));   // the ring is idle by then
+    const int n = items.count();
+    if (n == 0)
+        return;
+    Stream<F, 1, UpItems<G, PLANES>> stream(items, a.H, n, smem_u32(dynamic));
+    stream.start();
+    stream.run();
+    __syncthreads();
+    // the warp that began an item which others went on with adds up its pieces
+    const int per = (a.H + F::kUnit - 1) / F::kUnit;
+    const int begin = run_begin(n, per, warp), end = run_begin(n, per, warp + 1);
+    const int item = (end - 1) / per;
+    if (begin == end || end % per == 0 || item * per < begin)
+        return;
+    int q, i, stop;
+    items.where(item, q, i, stop);
+    const int first = l.begin[q], cols = l.begin[q + 1] - first;
+    for (int v = lane; v < 8 * cols; v += 32) {
+        const int g = v & 7, c = v >> 3;
+        if (i + g >= stop)
+            continue;
+        float gate = items.open[side_index(g, c)], up = items.open[side_index(g + 8, c)];
+        for (int w = warp + 1; w < kWarps && run_begin(n, per, w) < (item + 1) * per; ++w) {
+            if (run_begin(n, per, w) == run_begin(n, per, w + 1))
+                continue;
+            const float *p = reinterpret_cast<const float *>(sides + w * kSideBytes);
+            gate = __fadd_rn(gate, p[side_index(g, c)]);
+            up = __fadd_rn(up, p[side_index(g + 8, c)]);
+        }
+        store_planes<PLANES, (G > 0)>(a.out, l.slot[first + c], i + g, activate(gate, up));
     }
 }
 
+// ---------------------------------------------------------------------- down --
 struct DownArgs {
     Routing r;
     const float *weights;
@@ -323,112 +389,138 @@ struct DownArgs {
     Planes h;
     void *out;
     int out_f32;
-    int max_slices;    // column slices per expert that the shared memory has room for
+    int blocks;        // row blocks that the shared memory has room for at a time
 };
 
-template <int G, int PLANES, int NT>
-__device__ __forceinline__ void down_unit(const DownArgs &a, const Lists &l, int j, int64_t r0, int64_t r1, int base,
-                                          int u0, int u1, float *y)
-{
-    using F = typename Format<G, (G > 0)>::Rows;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int first = l.begin[j] + base, end = l.begin[j + 1];
-    const F f = Format<G, (G > 0)>::rows(a.w, r0, r1, a.I);
-    float acc[NT][4];
-    pass<F, PLANES, NT>(f, l, first, end, a.h.h, (int64_t)a.I * 2, 1, a.h.plane_bytes, u0, u1, a.I, acc);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int q = first + nt * 8 + 2 * t + c;
-            if (q < end) {
-                float *p = y + (int)l.slot[q] * kRow + g;
-                p[0] = acc[nt][c];
-                p[8] = acc[nt][2 + c];
-            }
-        }
-}
+// Row blocks [0, nb) of `rows` rows each from row0 on, times all entries.
+template <int G, int PLANES>
+struct DownItems {
+    using F = typename FormatOf<G, (G > 0)>::F;
+    const DownArgs &a;
+    const Lists &l;
+    int row0, row1, rows_per;
+    float *y;              // [nb][n][kRow]
+    float *side;
 
-__device__ __forceinline__ float ld_dsmem_f32(const float *p, uint32_t rank)
-{
-    return __int_as_float(ld_dsmem_s32(reinterpret_cast<const int32_t *>(p), rank));
-}
+    __device__ __forceinline__ RowPtrs rows(int item) const
+    {
+        const int b = item / l.entries, q = item - b * l.entries, g = (threadIdx.x & 31) >> 2;
+        const int r = row0 + b * rows_per, end = min(r + rows_per, row1);
+        const int64_t row = (int64_t)l.expert[q] * a.H + r + g;
+        return F::rows(a.w, row, row + 8, r + g < end, r + g + 8 < end, a.I);
+    }
+
+    __device__ __forceinline__ int blocks(int item) const
+    {
+        const int q = item % l.entries;
+        return blocks_of(l.begin[q + 1] - l.begin[q]);
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void columns(int item, Columns<NT, PLANES> &x) const
+    {
+        x.plane_bytes = a.h.plane_bytes;
+        set_columns<NT, PLANES>(l, item % l.entries, a.h.h, (int64_t)a.I * 2, 1, x);
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void done(int item, bool first, bool, float (&acc)[NT][4]) const
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int b = item / l.entries, q = item - b * l.entries;
+        if (!first) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                *reinterpret_cast<float4 *>(side + (nt * 32 + lane) * 4) =
+                    make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+            return;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int s = l.begin[q] + nt * 8 + 2 * t + c;
+                if (s < l.begin[q + 1]) {
+                    float *p = y + ((size_t)b * a.r.n + l.slot[s]) * kRow + g;
+                    p[0] = acc[nt][c];
+                    p[8] = acc[nt][2 + c];
+                }
+            }
+    }
+};
 
 template <int G, int PLANES>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
 moe_down_kernel(DownArgs a)
 {
-    extern __shared__ __align__(16) uint8_t dynamic[];
+    extern __shared__ __align__(16) uint8_t dynamic[];   // ring, one side block per warp, y
     __shared__ Lists l;
-    float *y = reinterpret_cast<float *>(dynamic);   // [slices][n][kRow], after the lists are built
+    using F = typename FormatOf<G, (G > 0)>::F;
     // topk_idx was complete before the up kernel began; h is complete after the wait
-    build_lists(a.r, l, reinterpret_cast<int *>(dynamic), nullptr);
-    grid_dependency_wait();
-    allow_dependents();
-    using F = typename Format<G, (G > 0)>::Rows;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    const int C = (int)cluster_nctarank(), c = (int)cluster_ctarank();
-    const int row0 = (int)(blockIdx.x / C) * 16;
-    // column slices of an expert: enough units for every warp of the cluster
-    const int W = C * kWarps, cols = (a.I + F::kUnit - 1) / F::kUnit;
-    int S = 1;
-    while (l.active * S < W && 2 * S <= a.max_slices && 2 * S <= cols)
-        S *= 2;
-    const int units = l.active * S;
-    // unit u belongs to warp u % W of the cluster, block (u % W) % C
-    for (int u = warp * C + c; u < units; u += W) {
-        const int j = u / S, s = u % S;
-        const int64_t base_row = (int64_t)l.expert[j] * a.H;
-        // rows past H are read as the last one and not stored
-        const int64_t r0 = base_row + min(row0 + g, a.H - 1), r1 = base_row + min(row0 + g + 8, a.H - 1);
-        const int u0 = cols * s / S, u1 = cols * (s + 1) / S;
-        float *ys = y + (size_t)s * a.r.n * kRow;
-        const int m = l.begin[j + 1] - l.begin[j];
-        int base = 0;
-        for (; m - base > 16; base += 32)
-            down_unit<G, PLANES, 4>(a, l, j, r0, r1, base, u0, u1, ys);
-        if (m - base > 8)
-            down_unit<G, PLANES, 2>(a, l, j, r0, r1, base, u0, u1, ys);
-        else if (m - base > 0)
-            down_unit<G, PLANES, 1>(a, l, j, r0, r1, base, u0, u1, ys);
-    }
-    if (C > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    // weighted sums over k; the blocks of the cluster share the tokens
-    const int rows = min(16, a.H - row0), K = a.r.K;
-    for (int v = threadIdx.x + c * kThreads; v < a.T * 16; v += kThreads * C) {
-        const int tok = v >> 4, i = v & 15;
-        if (i >= rows)
-            continue;
-        float sum = 0.0f;
-        for (int k = 0; k < K; ++k) {
-            const int slot = tok * K + k;
-            const int j = l.use[slot];
-            if (j < 0)
-                continue;
-            float p = 0.0f;
-            for (int s = 0; s < S; ++s) {
-                const float *at = y + ((size_t)s * a.r.n + slot) * kRow + i;
-                const int owner = (j * S + s) % W % C;
-                p = __fadd_rn(p, owner == c ? *at : ld_dsmem_f32(at, owner));
-            }
-            sum = __fmaf_rn(a.weights[slot], p, sum);
+    build_lists(a.r, l, reinterpret_cast<int *>(dynamic), F::kItemCost, nullptr);
+    const int warp = threadIdx.x >> 5;
+    uint8_t *sides = dynamic + kRingBytes;
+    const int row0 = (int)((int64_t)a.H * blockIdx.x / gridDim.x);
+    const int row1 = (int)((int64_t)a.H * (blockIdx.x + 1) / gridDim.x);
+    const int all = (row1 - row0 + 15) / 16;       // row blocks, of equal size up to one row
+    const int per = (a.I + F::kUnit - 1) / F::kUnit, K = a.r.K;
+    DownItems<G, PLANES> items{a, l};
+    items.rows_per = (row1 - row0 + all - 1) / all;
+    items.row1 = row1;
+    items.y = reinterpret_cast<float *>(sides + kWarps * kSideBytes);
+    items.side = reinterpret_cast<float *>(sides + warp * kSideBytes);
+    for (int b0 = 0; b0 < all; b0 += a.blocks) {
+        const int nb = min(a.blocks, all - b0);
+        const int n = nb * l.entries;
+        items.row0 = row0 + b0 * items.rows_per;
+        Stream<F, PLANES, DownItems<G, PLANES>> stream(items, a.I, n, smem_u32(dynamic));
+        if (n > 0)
+            stream.start();
+        if (b0 == 0) {
+            grid_dependency_wait();
+            allow_dependents();
         }
-        const int64_t o = (int64_t)tok * a.H + row0 + i;
-        if (a.out_f32)
-            static_cast<float *>(a.out)[o] = sum;
-        else
-            static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(sum);
+        if (n > 0)
+            stream.run();
+        __syncthreads();
+        // weighted sums over k; a slot's divided items are added in the order of their columns
+        const int rows = min(nb * items.rows_per, row1 - items.row0);
+        for (int v = threadIdx.x; v < a.T * rows; v += kThreads) {
+            const int tok = v / rows, rr = v - tok * rows;
+            const int b = rr / items.rows_per, i = rr - b * items.rows_per;
+            float sum = 0.0f;
+            for (int k = 0; k < K; ++k) {
+                const int slot = tok * K + k;
+                const int q = l.use[slot];
+                if (q < 0)
+                    continue;
+                float p = items.y[((size_t)b * a.r.n + slot) * kRow + i];
+                const int item = b * l.entries + q;
+                // warps whose run begins inside the item
+                int w = (int)((int64_t)item * per * kWarps / ((int64_t)n * per));
+                const int col = l.place[slot] % kMaxCols;
+                for (; w < kWarps; ++w) {
+                    const int at = run_begin(n, per, w);
+                    if (at >= (item + 1) * per)
+                        break;
+                    if (at > item * per && at < run_begin(n, per, w + 1))
+                        p = __fadd_rn(p, reinterpret_cast<const float *>(sides + w * kSideBytes)[side_index(i, col)]);
+                }
+                sum = __fmaf_rn(a.weights[slot], p, sum);
+            }
+            const int64_t o = (int64_t)tok * a.H + items.row0 + rr;
+            if (a.out_f32)
+                static_cast<float *>(a.out)[o] = sum;
+            else
+                static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(sum);
+        }
+        __syncthreads();   // y and the sides are read before the next row blocks overwrite them
     }
-    if (C > 1)
-        cluster_sync();   // no block leaves while another reads its shared memory
 }
 
 // ------------------------------------------------------------ launch policy --
-constexpr size_t kStaticSmem = sizeof(Lists) + 1024;
-constexpr size_t kSmemPerBlock = 227 * 1024 / 2 - kStaticSmem;   // two blocks to an SM
+constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - 64;   // dynamic shared memory of a block that owns an SM
+static_assert(kRingBytes + kWarps * kSideBytes + (size_t)kMaxSlots * kRow * sizeof(float) <= kMaxSmem, "one row block fits");
 
 template <class Kernel>
 int raise_smem(Kernel kernel, size_t smem, PerDevice &set)
@@ -445,22 +537,18 @@ int raise_smem(Kernel kernel, size_t smem, PerDevice &set)
 }
 
 template <class Kernel, class Args>
-int launch_dependent(Kernel kernel, unsigned grid, size_t smem, unsigned cluster, cudaStream_t stream, const Args &a)
+int launch_dependent(Kernel kernel, unsigned grid, size_t smem, cudaStream_t stream, const Args &a)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
         cudaGetLastError();
         return EP_ERR_CUDA;
@@ -472,42 +560,29 @@ template <int G, int PLANES>
 int launch(const UpArgs &up, DownArgs down, cudaStream_t stream)
 {
     const int sms = device_sm_count();
-    const int used = std::min(up.r.n, up.r.E_local);   // experts in use, at most
-    const size_t counts = align_up((size_t)up.r.E_local * sizeof(int), 16);
+    const size_t fixed = kRingBytes + kWarps * kSideBytes;
+    static_assert(EP_MAX_EXPERTS * sizeof(int) <= kRingBytes, "the experts' counters use the ring before it starts");
     {
         static PerDevice set;
-        const size_t smem = std::max(counts, (size_t)kWarps * kMaxBlocks8 * 128 * sizeof(float));
-        int rc = raise_smem(moe_up_kernel<G, PLANES>, smem, set);
+        int rc = raise_smem(moe_up_kernel<G, PLANES>, fixed, set);
         if (rc != EP_OK)
             return rc;
-        // one resident wave, or fewer blocks when every unit already has a block's eight warps
-        const int64_t units = (int64_t)used * (up.I / 8);
-        rc = launch_dependent(moe_up_kernel<G, PLANES>, (unsigned)std::min<int64_t>(units, 2 * sms), smem, 1, stream, up);
+        // one block per SM, or one per element where there are fewer
+        const int64_t elements = (int64_t)std::min(up.r.n, up.r.E_local) * up.I;
+        rc = launch_dependent(moe_up_kernel<G, PLANES>, (unsigned)std::min<int64_t>(elements, sms), fixed, stream, up);
         if (rc != EP_OK)
             return rc;
     }
     static PerDevice set;
-    const size_t slice = (size_t)up.r.n * kRow * sizeof(float);
-    // blocks of a cluster: the count that leaves the fullest last wave of two blocks to an SM
-    const int tiles = (int)ceil_div(up.H, 16), wave = 2 * sms;
-    int C = 1;
-    int64_t best = INT64_MAX;
-    for (int c = 1; c <= 8; c *= 2) {
-        const int64_t cost = ceil_div((int64_t)tiles * c, wave) * (8 / c);
-        if (cost < best) {
-            best = cost;
-            C = c;
-        }
-    }
-    int slices = 1;
-    while (slices < kWarps * C && (size_t)(2 * slices) * slice <= kSmemPerBlock)
-        slices *= 2;
-    down.max_slices = slices;
-    const size_t smem = std::max(counts, slices * slice);
+    const int grid = std::min(sms, up.H);
+    const size_t block = (size_t)up.r.n * kRow * sizeof(float);   // results of 16 rows
+    const int all = (int)ceil_div(ceil_div(up.H, grid), 16);
+    down.blocks = (int)std::min<size_t>(all, std::max<size_t>(1, (kMaxSmem - fixed) / block));
+    const size_t smem = fixed + down.blocks * block;
     const int rc = raise_smem(moe_down_kernel<G, PLANES>, smem, set);
     if (rc != EP_OK)
         return rc;
-    return launch_dependent(moe_down_kernel<G, PLANES>, (unsigned)(tiles * C), smem, (unsigned)C, stream, down);
+    return launch_dependent(moe_down_kernel<G, PLANES>, (unsigned)grid, smem, stream, down);
 }
 
 bool matrix_ok(const ep_matrix *m)
@@ -551,7 +626,7 @@ extern "C" int ep_moe_decode(const void *x, const int64_t *topk_idx, const float
         if ((g != 32 && g != 64 && g != 128) || H % g != 0 || I % g != 0)
             return EP_ERR_INVALID_ARG;
     }
-    if (T > kMaxSlots || T * K > kMaxSlots || H >= (1 << 20) || I >= (1 << 20))
+    if (T > kMaxSlots || T * K > kMaxSlots || H > kMaxDim || I > kMaxDim)
         return EP_ERR_UNSUPPORTED;
     if (T == 0)
         return EP_OK;

@@ -1,18 +1,21 @@
-// Products of a streamed weight matrix with a few columns (internal): one warp
-// sums 16 weight rows times up to 8*NT columns over a range of K.
+// Products of a streamed weight matrix with a few columns (internal).
 //
 // With a few tokens every weight is used a handful of times, so these products
-// are bound by reading the weights from HBM.  Each lane loads its weights
-// straight from the row-major matrix into the registers of an m16n8k16 matrix
-// instruction, 16 bytes per row and load; nothing is staged in shared memory,
-// so no barrier stands between a load and its use.  The sum over k does not
-// care about the order of k: lane (g, t) takes whole 16-byte pieces of rows g
-// and g+8 and offers the same columns of x, whatever k the instruction's
-// layout gives those positions.  The columns (tokens) are the instruction's
-// N = 8 side, so one token costs what eight do, which is still nothing beside
-// the weight stream.
+// are bound by reading the weights from HBM, and what counts is that enough of
+// them is in flight all the time.  A block owns an SM and a share of the weight
+// rows; its 16 warps share that work in equal runs of K, each streaming its own
+// 16 rows at a time through a ring of its own in shared memory:
 //
-// Accumulators: the matrix instruction's fp32 sums run over at most 128 columns
+//   - cp.async copies 16 bytes of a row to the slot of the very lane that will
+//     use them, so a lane waits for its own copies only: no barrier stands
+//     between the copy and its use, and the ring runs across items;
+//   - lane (g, t) holds rows g and g+8 of an m16n8k16 matrix step and takes
+//     whole 16-byte pieces of them, offering the same columns of x for the
+//     instruction's k positions: a sum over k does not care about its order;
+//   - the columns (tokens) are the instruction's N = 8 side, so one token costs
+//     what eight do, which is nothing beside the weight stream.
+//
+// Accumulators: the matrix step's fp32 sums run over at most 128 columns of K
 // (one group of 4-bit weights); these partial sums are then scaled and added
 // with IEEE fp32 operations.
 #pragma once
@@ -22,6 +25,15 @@
 #include "ep_device.cuh"
 
 namespace ep {
+
+constexpr int kSkinnyWarps = 16;
+constexpr int kSkinnyThreads = 32 * kSkinnyWarps;
+constexpr int kGroupUnits = 2;       // units (1 KB: 16 rows) of one ring stage
+constexpr int kStages = 3;           // stages in flight per warp: 96 KB per SM, twice what 45 KB/us x 1 us needs
+constexpr int kStageBytes = kGroupUnits * 1024;
+constexpr int kRingBytes = kSkinnyWarps * kStages * kStageBytes;
+constexpr int kMaxCols = 32;         // columns of one pass over the weights: 4 blocks of 8
+constexpr int kSideBytes = 16 * kMaxCols * 4;   // one 16 x 32 block of partial sums
 
 // D += A (16x16, row) * B (16x8, col), bf16 in, fp32 sums.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -40,9 +52,25 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-__device__ __forceinline__ uint4 ld_cached(const void *p)
+// 16 bytes to shared memory, zeros where !ok (src is then not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok)
 {
-    return __ldg(reinterpret_cast<const uint4 *>(p));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
 }
 
 // The columns of the product, bf16, for this lane: column g of each of NT
@@ -57,61 +85,65 @@ struct Columns {
     {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (p[nt] != nullptr && k < K)
-            v = ld_cached(p[nt] + plane * plane_bytes + (int64_t)k * 2);
+            v = __ldg(reinterpret_cast<const uint4 *>(p[nt] + plane * plane_bytes + (int64_t)k * 2));
         return v;
     }
 };
 
-// bf16 weights.  A unit of work is 32 columns: lane (g, t) holds columns 8t ..
-// 8t+7 of rows g and g+8, which are two k16 steps.
-struct RowsBf16 {
+// Where a lane's two rows lie.  A row past the end of its block has a null data
+// pointer: it is not read, and its sums are not used.
+struct RowPtrs {
+    const uint8_t *r0, *r1;     // data of rows g and g+8
+    const uint16_t *s0, *s1;    // 4-bit: scales (bf16 bits)
+    const uint8_t *z0, *z1;     // 4-bit: zero points, or null
+};
+
+struct Weights {
+    const uint8_t *data;
+    const uint16_t *scale;
+    const uint8_t *zero;
+};
+
+// bf16 weights.  A unit is 32 columns: lane (g, t) holds columns 8t .. 8t+7 of
+// rows g and g+8, two k16 steps.
+struct FormatBf16 {
     static constexpr int kUnit = 32;
-    static constexpr int kBatch = 4;    // units loaded together: 128 columns, 4 KB per warp
     static constexpr bool kPermuted = false;
-    const uint8_t *r0, *r1;             // rows g and g+8 of this lane
+    // what an item costs beside one n-block's columns: 1 KB of weights to 0.5 KB of x
+    static constexpr int kItemCost = 4;
+    struct Extra {};
 
-    struct Regs {
-        uint4 a0[kBatch], a1[kBatch];
-    };
-
-    __device__ __forceinline__ void load(Regs &r, int u0, int u1, int K, int t) const
+    static __device__ __forceinline__ RowPtrs rows(const Weights &w, int64_t a, int64_t b, bool has_a, bool has_b, int K)
     {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int k = (u0 + i) * kUnit + 8 * t;
-            if (u0 + i < u1 && k < K) {
-                r.a0[i] = ld_stream(reinterpret_cast<const uint4 *>(r0 + (int64_t)k * 2));
-                r.a1[i] = ld_stream(reinterpret_cast<const uint4 *>(r1 + (int64_t)k * 2));
-            } else {
-                r.a0[i] = r.a1[i] = make_uint4(0, 0, 0, 0);
-            }
-        }
+        const int64_t bytes = (int64_t)K * 2;
+        RowPtrs r = {};
+        r.r0 = has_a ? w.data + a * bytes : nullptr;
+        r.r1 = has_b ? w.data + b * bytes : nullptr;
+        return r;
     }
 
+    static __device__ __forceinline__ int column(int u, int t) { return u * kUnit + 8 * t; }
+    static __device__ __forceinline__ int64_t offset(int k) { return (int64_t)k * 2; }
+    static __device__ __forceinline__ Extra extra(const RowPtrs &, int, int, int) { return Extra{}; }
+
     template <int NT, int PLANES>
-    __device__ __forceinline__ void compute(const Regs &r, int u0, int u1, int K, int t,
-                                            const Columns<NT, PLANES> &x, float (&acc)[NT][4]) const
+    static __device__ __forceinline__ void unit(const uint4 &a, const uint4 &b, const Extra &, int u, int K, int t,
+                                                const Columns<NT, PLANES> &x, float (&acc)[NT][4])
     {
-        float part[NT][4] = {};
+        const int k = column(u, t);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (u0 + i >= u1)
-                break;
-            const int k = (u0 + i) * kUnit + 8 * t;
+        for (int nt = 0; nt < NT; ++nt) {
+            float part[4] = {};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int p = 0; p < PLANES; ++p) {
-                    const uint4 b = x.load(nt, p, k, K);
-                    mma_bf16(part[nt], r.a0[i].x, r.a1[i].x, r.a0[i].y, r.a1[i].y, b.x, b.y);
-                    mma_bf16(part[nt], r.a0[i].z, r.a1[i].z, r.a0[i].w, r.a1[i].w, b.z, b.w);
-                }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int p = 0; p < PLANES; ++p) {
+                const uint4 v = x.load(nt, p, k, K);
+                mma_bf16(part, a.x, b.x, a.y, b.y, v.x, v.y);
+                mma_bf16(part, a.z, b.z, a.w, b.w, v.z, v.w);
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                acc[nt][c] = __fadd_rn(acc[nt][c], part[nt][c]);
+                acc[nt][c] = __fadd_rn(acc[nt][c], part[c]);
+        }
     }
 };
 
@@ -121,46 +153,57 @@ struct RowsBf16 {
 // 128 + zero.  Word bits 4j hold code j, so masking 0x000f000f takes codes
 // (j, j+4) as a pair; x's columns are paired the same way (by the stored order
 // where PERMUTED, else by byte permutes).  With G < 128 a lane's words belong
-// to different groups than its neighbours', so the four lanes of a row trade
-// words until each matrix step stays in one group.
+// to other groups than its neighbours', so the four lanes of a row trade words
+// until each matrix step stays in one group.
 template <int G, bool PERMUTED>
-struct RowsW4 {
+struct FormatW4 {
     static constexpr int kUnit = 128;
-    static constexpr int kBatch = 2;    // 256 columns, 2 KB per warp
     static constexpr bool kPermuted = PERMUTED;
-    const uint8_t *r0, *r1;
-    const uint16_t *s0, *s1;            // scales (bf16 bits) of rows g and g+8
-    const uint8_t *z0, *z1;             // zero points, or null
-
-    struct Regs {
-        uint4 a0[kBatch], a1[kBatch];
-        uint32_t q0[kBatch], q1[kBatch];   // scale in the high half, bf16(128 + zero) in the low half
+    static constexpr int kItemCost = 2;
+    struct Extra {
+        uint32_t q0, q1;    // scale in the high half, bf16(128 + zero) in the low half
     };
 
-    __device__ __forceinline__ uint32_t group(const uint16_t *s, const uint8_t *z, int gi) const
+    static __device__ __forceinline__ RowPtrs rows(const Weights &w, int64_t a, int64_t b, bool has_a, bool has_b, int K)
+    {
+        const int64_t bytes = K / 2, groups = K / G;
+        RowPtrs r = {};
+        if (has_a) {
+            r.r0 = w.data + a * bytes;
+            r.s0 = w.scale + a * groups;
+            r.z0 = w.zero != nullptr ? w.zero + a * groups : nullptr;
+        }
+        if (has_b) {
+            r.r1 = w.data + b * bytes;
+            r.s1 = w.scale + b * groups;
+            r.z1 = w.zero != nullptr ? w.zero + b * groups : nullptr;
+        }
+        return r;
+    }
+
+    static __device__ __forceinline__ int column(int u, int t) { return u * kUnit + 32 * t; }
+    static __device__ __forceinline__ int64_t offset(int k) { return k >> 1; }
+
+    static __device__ __forceinline__ uint32_t group(const uint16_t *s, const uint8_t *z, int gi)
     {
         const uint32_t zero = z != nullptr ? (uint32_t)__ldg(z + gi) : 8u;
         return ((uint32_t)__ldg(s + gi) << 16) | 0x4300u | zero;
     }
 
-    __device__ __forceinline__ void load(Regs &r, int u0, int u1, int K, int t) const
+    static __device__ __forceinline__ Extra extra(const RowPtrs &r, int u, int K, int t)
     {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int k = (u0 + i) * kUnit + 32 * t;
-            r.a0[i] = r.a1[i] = make_uint4(0, 0, 0, 0);
-            r.q0[i] = r.q1[i] = 0x4308u;
-            if (u0 + i < u1 && k < K) {
-                r.a0[i] = ld_stream(reinterpret_cast<const uint4 *>(r0 + (k >> 1)));
-                r.a1[i] = ld_stream(reinterpret_cast<const uint4 *>(r1 + (k >> 1)));
-                r.q0[i] = group(s0, z0, k / G);
-                r.q1[i] = group(s1, z1, k / G);
-            }
+        const int k = column(u, t);
+        Extra e{0x4308u, 0x4308u};
+        if (k < K) {
+            if (r.s0 != nullptr)
+                e.q0 = group(r.s0, r.z0, k / G);
+            if (r.s1 != nullptr)
+                e.q1 = group(r.s1, r.z1, k / G);
         }
+        return e;
     }
 
-    // the words a lane sends to lane ^ mask are replaced by those it gets:
-    // (a, b) -> low lane keeps a and gets the partner's a; high lane keeps b
+    // (a, b) -> the low lane keeps a and gets its partner's a, the high lane keeps b and gets b
     static __device__ __forceinline__ void trade(uint32_t &a, uint32_t &b, int mask, bool high)
     {
         const uint32_t out = high ? a : b;
@@ -169,7 +212,7 @@ struct RowsW4 {
         b = high ? b : in;
     }
 
-    // after it, word i of lane t lies in columns column(i, t) of the unit
+    // after it, word i of lane t lies in columns word_column(i, t) of the unit
     static __device__ __forceinline__ void arrange(uint4 &w, int t)
     {
         if (G == 64) {
@@ -183,7 +226,7 @@ struct RowsW4 {
         }
     }
 
-    static __device__ __forceinline__ int column(int i, int t)
+    static __device__ __forceinline__ int word_column(int i, int t)
     {
         if (G == 128)
             return 32 * t + 8 * i;
@@ -198,61 +241,64 @@ struct RowsW4 {
     }
 
     template <int NT, int PLANES>
-    __device__ __forceinline__ void compute(const Regs &r, int u0, int u1, int K, int t,
-                                            const Columns<NT, PLANES> &x, float (&acc)[NT][4]) const
+    static __device__ __forceinline__ void unit(uint4 wa, uint4 wb, const Extra &e, int u, int K, int t,
+                                                const Columns<NT, PLANES> &x, float (&acc)[NT][4])
     {
         constexpr int kWords = G / 32;   // words of a lane in one group
+        arrange(wa, t);
+        arrange(wb, t);
+        const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (u0 + i >= u1)
-                break;
-            const int k0 = (u0 + i) * kUnit;
-            uint4 wa = r.a0[i], wb = r.a1[i];
-            arrange(wa, t);
-            arrange(wb, t);
-            const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
+        for (int gi = 0; gi < 4 / kWords; ++gi) {
+            uint32_t q0 = e.q0, q1 = e.q1;
+            if (G < 128) {   // the lane of this row that loaded this group's scale
+                const int from = (threadIdx.x & 28) | (gi * kWords);
+                q0 = __shfl_sync(kFull, q0, from);
+                q1 = __shfl_sync(kFull, q1, from);
+            }
+            const uint32_t zz0 = __byte_perm(q0, q0, 0x1010), zz1 = __byte_perm(q1, q1, 0x1010);
+            float part[NT][4] = {};
 #pragma unroll
-            for (int gi = 0; gi < 4 / kWords; ++gi) {
-                uint32_t q0 = r.q0[i], q1 = r.q1[i];
-                if (G < 128) {   // the lane of this row that loaded this group's scale
-                    const int from = (threadIdx.x & 28) | (gi * kWords);
-                    q0 = __shfl_sync(kFull, q0, from);
-                    q1 = __shfl_sync(kFull, q1, from);
-                }
-                const uint32_t zz0 = __byte_perm(q0, q0, 0x1010), zz1 = __byte_perm(q1, q1, 0x1010);
-                float part[NT][4] = {};
+            for (int j = 0; j < kWords; ++j) {
+                const int w = gi * kWords + j;
+                const int k = u * kUnit + word_column(w, t);
+                const uint32_t a = va[w], b = vb[w];
+                const uint32_t a0 = codes(a, zz0), a1 = codes(a >> 4, zz0), a2 = codes(a >> 8, zz0),
+                               a3 = codes(a >> 12, zz0);
+                const uint32_t c0 = codes(b, zz1), c1 = codes(b >> 4, zz1), c2 = codes(b >> 8, zz1),
+                               c3 = codes(b >> 12, zz1);
 #pragma unroll
-                for (int j = 0; j < kWords; ++j) {
-                    const int w = gi * kWords + j;
-                    const int k = k0 + column(w, t);
-                    const uint32_t a = va[w], b = vb[w];
-                    const uint32_t a0 = codes(a, zz0), a1 = codes(a >> 4, zz0), a2 = codes(a >> 8, zz0),
-                                   a3 = codes(a >> 12, zz0);
-                    const uint32_t c0 = codes(b, zz1), c1 = codes(b >> 4, zz1), c2 = codes(b >> 8, zz1),
-                                   c3 = codes(b >> 12, zz1);
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int p = 0; p < PLANES; ++p) {
+                        uint4 v = x.load(nt, p, k, K);
+                        if (!PERMUTED)   // columns (0,4) (1,5) (2,6) (3,7)
+                            v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                           __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+                        mma_bf16(part[nt], a0, c0, a1, c1, v.x, v.y);
+                        mma_bf16(part[nt], a2, c2, a3, c3, v.z, v.w);
+                    }
+            }
+            const float f0 = __uint_as_float(q0 & 0xffff0000u), f1 = __uint_as_float(q1 & 0xffff0000u);
 #pragma unroll
-                        for (int p = 0; p < PLANES; ++p) {
-                            uint4 v = x.load(nt, p, k, K);
-                            if (!PERMUTED)   // columns (0,4) (1,5) (2,6) (3,7)
-                                v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-                            mma_bf16(part[nt], a0, c0, a1, c1, v.x, v.y);
-                            mma_bf16(part[nt], a2, c2, a3, c3, v.z, v.w);
-                        }
-                }
-                const float f0 = __uint_as_float(q0 & 0xffff0000u), f1 = __uint_as_float(q1 & 0xffff0000u);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    acc[nt][0] = __fmaf_rn(part[nt][0], f0, acc[nt][0]);
-                    acc[nt][1] = __fmaf_rn(part[nt][1], f0, acc[nt][1]);
-                    acc[nt][2] = __fmaf_rn(part[nt][2], f1, acc[nt][2]);
-                    acc[nt][3] = __fmaf_rn(part[nt][3], f1, acc[nt][3]);
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                acc[nt][0] = __fmaf_rn(part[nt][0], f0, acc[nt][0]);
+                acc[nt][1] = __fmaf_rn(part[nt][1], f0, acc[nt][1]);
+                acc[nt][2] = __fmaf_rn(part[nt][2], f1, acc[nt][2]);
+                acc[nt][3] = __fmaf_rn(part[nt][3], f1, acc[nt][3]);
             }
         }
     }
+};
+
+// The weight format of a kernel: G = 0 for bf16, else the group of 4-bit codes.
+template <int G, bool PERMUTED>
+struct FormatOf {
+    using F = FormatW4<G, PERMUTED>;
+};
+template <bool PERMUTED>
+struct FormatOf<0, PERMUTED> {
+    using F = FormatBf16;
 };
 
 // Where column j of a block of 8 stands in memory, for a producer of columns.
@@ -262,21 +308,146 @@ __device__ __forceinline__ int column_place(int j)
     return PERMUTED ? ((j & 3) << 1) | (j >> 2) : j;
 }
 
-// acc += the 16 rows of f times the columns x, over units [u0, u1) of K.
-// acc[nt]: rows g, g, g+8, g+8; columns 8*nt + 2t, +1, +0, +1.
-template <class F, int NT, int PLANES>
-__device__ __forceinline__ void skinny(const F &f, int u0, int u1, int K, int t, const Columns<NT, PLANES> &x,
-                                       float (&acc)[NT][4])
+// A warp's sums of one item as they are kept: [block of 8 columns][lane] float4.
+__device__ __forceinline__ int side_index(int row, int col)   // in floats
 {
-    typename F::Regs a, b;
-    f.load(a, u0, u1, K, t);
-    // the next batch is in flight while one is used
-    for (int u = u0; u < u1; u += 2 * F::kBatch) {
-        f.load(b, u + F::kBatch, u1, K, t);
-        f.compute(a, u, u1, K, t, x, acc);
-        f.load(a, u + 2 * F::kBatch, u1, K, t);
-        f.compute(b, u + F::kBatch, u1, K, t, x, acc);
+    const int lane = ((row & 7) << 2) | ((col & 7) >> 1);
+    return (((col >> 3) * 32 + lane) << 2) | ((row >> 3) << 1) | (col & 1);
+}
+
+// One warp's run of a block's items.  Items are numbered 0 .. items-1; each is
+// 16 rows times all of K (`per` units).  The run is units [begin, end) of the
+// items laid end to end: it may start or stop inside an item.
+//
+// Items is the kernel's view of its work: rows(item) gives this lane's RowPtrs,
+// blocks(item) the number of 8-column blocks (1 .. 4), columns<NT>(item, x)
+// sets the column pointers, and done<NT>(item, first, last, acc) takes the sums
+// of a piece; first / last say whether the piece holds the item's first and
+// last unit.
+template <class F, int PLANES, class Items>
+class Stream {
+public:
+    __device__ __forceinline__ Stream(Items &items, int K, int n_items, uint32_t ring)
+        : items_(items), K_(K), per_((K + F::kUnit - 1) / F::kUnit)
+    {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        t_ = lane & 3;
+        const int64_t total = (int64_t)n_items * per_;
+        begin_ = (int)(total * warp / kSkinnyWarps);
+        end_ = (int)(total * (warp + 1) / kSkinnyWarps);
+        slot_ = ring + warp * (kStages * kStageBytes) + lane * 16;
+        ahead_ = begin_;
+        item_ahead_ = begin_ / per_;
+        u_ahead_ = begin_ - item_ahead_ * per_;
+        stage_ahead_ = stage_ = 0;
+        fresh_ = true;
     }
+
+    // the first copies of the run; they read weights only
+    __device__ __forceinline__ void start()
+    {
+#pragma unroll
+        for (int s = 0; s < kStages; ++s)
+            issue();
+    }
+
+    __device__ __forceinline__ void run()
+    {
+        int at = begin_;
+        while (at < end_) {
+            const int item = at / per_, u0 = at - item * per_;
+            const int u1 = min(per_, u0 + end_ - at);
+            const int nb = items_.blocks(item);
+            if (nb <= 1)
+                piece<1>(item, u0, u1);
+            else if (nb == 2)
+                piece<2>(item, u0, u1);
+            else
+                piece<4>(item, u0, u1);
+            at += u1 - u0;
+        }
+    }
+
+private:
+    __device__ __forceinline__ void issue()
+    {
+        if (ahead_ < end_) {
+            if (fresh_) {
+                src_ = items_.rows(item_ahead_);
+                fresh_ = false;
+            }
+            const int left = min(per_ - u_ahead_, end_ - ahead_);
+            const uint32_t dst = slot_ + stage_ahead_ * kStageBytes;
+#pragma unroll
+            for (int i = 0; i < kGroupUnits; ++i)
+                if (i < left) {
+                    const int k = F::column(u_ahead_ + i, t_);
+                    const bool ok = k < K_;
+                    const int64_t off = ok ? F::offset(k) : 0;
+                    if (src_.r0 != nullptr)
+                        cp_async16(dst + i * 1024, src_.r0 + off, ok);
+                    if (src_.r1 != nullptr)
+                        cp_async16(dst + i * 1024 + 512, src_.r1 + off, ok);
+                }
+            const int n = min(left, kGroupUnits);
+            ahead_ += n;
+            u_ahead_ += n;
+            if (u_ahead_ == per_) {
+                u_ahead_ = 0;
+                ++item_ahead_;
+                fresh_ = true;
+            }
+        }
+        cp_async_commit();
+        stage_ahead_ = stage_ahead_ == kStages - 1 ? 0 : stage_ahead_ + 1;
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void piece(int item, int u0, int u1)
+    {
+        Columns<NT, PLANES> x;
+        items_.template columns<NT>(item, x);
+        const RowPtrs rows = items_.rows(item);
+        float acc[NT][4] = {};
+        typename F::Extra e[kGroupUnits];
+#pragma unroll
+        for (int i = 0; i < kGroupUnits; ++i)
+            e[i] = F::extra(rows, u0 + i, K_, t_);
+        for (int u = u0; u < u1; u += kGroupUnits) {
+            cp_async_wait<kStages - 1>();
+            const uint32_t src = slot_ + stage_ * kStageBytes;
+            uint4 a[kGroupUnits], b[kGroupUnits];
+            typename F::Extra f[kGroupUnits];
+#pragma unroll
+            for (int i = 0; i < kGroupUnits; ++i) {
+                a[i] = ld_shared16(src + i * 1024);
+                b[i] = ld_shared16(src + i * 1024 + 512);
+                f[i] = e[i];
+                e[i] = F::extra(rows, u + kGroupUnits + i, K_, t_);
+            }
+            issue();
+#pragma unroll
+            for (int i = 0; i < kGroupUnits; ++i)
+                if (u + i < u1)
+                    F::template unit<NT, PLANES>(a[i], b[i], f[i], u + i, K_, t_, x, acc);
+            stage_ = stage_ == kStages - 1 ? 0 : stage_ + 1;
+        }
+        items_.template done<NT>(item, u0 == 0, u1 == per_, acc);
+    }
+
+    Items &items_;
+    RowPtrs src_;
+    int K_, per_, t_;
+    int begin_, end_, ahead_, item_ahead_, u_ahead_;
+    int stage_ahead_, stage_;
+    uint32_t slot_;
+    bool fresh_;
+};
+
+// The first unit of warp w's run (see Stream), for whoever adds up the pieces.
+__device__ __forceinline__ int run_begin(int n_items, int per, int w)
+{
+    return (int)((int64_t)n_items * per * w / kSkinnyWarps);
 }
 
 }  // namespace ep

@@ -617,8 +617,8 @@ int ep_router_topk(const void *x, int64_t T, int H, const void *w, int w_dtype, 
  *   out [T,H]: bf16 (out_dtype 0) or fp32 (out_dtype 1); tokens without a local
  *     expert give +0.  Weights of slots that name no local expert are not read
  *     as numbers.
- *   T * K <= EP_MOE_MAX_SLOTS (else EP_ERR_UNSUPPORTED: larger batches take the
- *     dispatch and combine calls).
+ *   T * K <= EP_MOE_MAX_SLOTS and H, I <= 65536 (else EP_ERR_UNSUPPORTED: larger
+ *     batches take the dispatch and combine calls).
  *   ws: ep_moe_workspace_size(T, K, I) bytes, 256-byte aligned, scratch.  Calls
  *     that overlap on the GPU must not share it.
  * The same call on the same inputs gives the same bits.  The sums' order
