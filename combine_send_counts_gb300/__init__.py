@@ -109,7 +109,7 @@ _SIGNATURES = {
     "ep_router_workspace_size": (_SZ, [_I64, _I32, _I32]),
     "ep_router_topk": (_I32, [_VP, _I64, _I32, _VP, _I32, _I32, _VP, _I32, _I32, _I32, ctypes.c_float, _VP, _VP, _VP,
                               _VP, _SZ, _VP]),
-    "ep_moe_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "ep_moe_workspace_size": (_SZ, [_I64, _I32, _I32, _I32]),
     "ep_moe_decode": (_I32, [_VP, _VP, _VP, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _SZ,
                              _VP, _VP]),
 }
@@ -874,8 +874,8 @@ def ep_router_topk(x, T, H, w, w_dtype, E, bias, K, scoring, renormalize, scale,
                                  _nbytes(ws), _stream(stream)), "ep_router_topk")
 
 
-def ep_moe_workspace_size(T: int, K: int, I: int) -> int:
-    return int(load().ep_moe_workspace_size(int(T), int(K), int(I)))
+def ep_moe_workspace_size(T: int, K: int, H: int, I: int) -> int:
+    return int(load().ep_moe_workspace_size(int(T), int(K), int(H), int(I)))
 
 
 def ep_moe_decode(x, topk_idx, topk_weights, T, K, H, I, E, E_local, rank, w13: EPMatrix, w2: EPMatrix, out, out_dtype,
@@ -1083,7 +1083,7 @@ class MoeDecode:
         self.err = error_word(dev)
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(dev).synchronize()   # the word is clear before a call on any stream
-        self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, I), 256), dtype=torch.uint8, device=dev)
+        self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, H, I), 256), dtype=torch.uint8, device=dev)
         self._mid = (H, I, E, El, rank, ctypes.addressof(self._m13), ctypes.addressof(self._m2))
         self._ws = (self.ws.data_ptr(), self.ws.numel())
 

@@ -1,0 +1,626 @@
+// The experts of a mixture-of-experts layer for a few tokens, in two kernels
+// (internal; the entry point is in ep_moe.cu).
+//
+//   up:    h[s] = silu(Wg x) * (Wu x) for every slot s = (t, k) that names a
+//          local expert;
+//   down:  out[t] = sum over k of w[t,k] * (W2 h[t,k]).
+//
+// Each expert that some token names has its matrices read from HBM once for all
+// its slots, by products of blocks of 16 weight rows with 16 slots at a time as
+// columns (ep_skinny.cuh).  No row of x is copied to an expert and no list is made on
+// the host: every block derives the experts in use and their slots from
+// topk_idx, which a graph replay may have changed.
+//
+// up: the elements of h of all experts in use, laid end to end, are dealt to
+// one block per SM in equal runs.  An item is up to 32 elements: 8 gate rows and
+// the 8 up rows of the same elements are the 16 rows of a matrix step, whose accumulators hold gate and
+// up of an element in the same lane.
+//
+// down: each block owns an equal share of the output's rows and adds up all
+// experts for them.  An item is up to 48 of its rows of one expert.  Every
+// slot's results stay in shared memory (in the workspace, which means in L2,
+// when there are too many) and are weighted and added by the same block in
+// ascending k.
+//
+// In both the block's items are shared evenly by its warps, whose runs may stop
+// inside an item; the pieces of a divided item are added in the order of their
+// columns.  Nothing depends on the order of arrival.
+//
+// h is kept as the bf16 terms of a sum (two terms, or three for fp32 results:
+// 16 or 24 significant bits), which is what the matrix step takes; one bf16
+// would add an error as large as the rounding of the result itself.
+#pragma once
+
+#include <algorithm>
+
+#include "ep_device.cuh"
+#include "ep_internal.h"
+#include "ep_skinny.cuh"
+
+namespace ep {
+
+constexpr int kThreads = kSkinnyThreads;
+constexpr int kWarps = kSkinnyWarps;
+constexpr int kMaxSlots = EP_MOE_MAX_SLOTS;
+constexpr int kMaxDim = 65536;   // H and I: a block's units are counted in 32 bits
+
+struct Routing {
+    const int64_t *idx;
+    int n;           // slots: T * K
+    int K, E, E_local;
+    int64_t first;   // first local expert
+
+    // local expert of slot s, or -1
+    __device__ __forceinline__ int local(int s, int32_t *err) const
+    {
+        const int64_t v = idx[s];
+        if (v < -1 || v >= E) {
+            raise(err, EP_ERR_INVALID_EXPERT);
+            return -1;
+        }
+        const int64_t l = v - first;
+        return v >= 0 && l >= 0 && l < E_local ? (int)l : -1;
+    }
+};
+
+__device__ __forceinline__ int passes_of(int slots) { return (slots + kMaxCols - 1) / kMaxCols; }
+
+// The experts in use and their slots, in shared memory.  An expert has an entry
+// for each pass over its weights, of up to 16 slots.
+struct Lists {
+    int experts, entries, big;
+    int scan[3][kWarps];
+    int cost[kMaxSlots + 1];          // exclusive sums over the experts of the cost of a weight row
+    uint16_t id[kMaxSlots];           // expert j's local id
+    uint16_t entry[kMaxSlots + 1];    // its first entry: it has entry[j] .. entry[j+1]
+    uint16_t owner[kMaxSlots];        // entry -> j
+    uint16_t begin[kMaxSlots + 1];    // slots of entry q: slot[begin[q] .. begin[q+1])
+    uint16_t slot[kMaxSlots];
+    int16_t use[kMaxSlots];           // slot -> its entry, or -1
+    uint16_t place[kMaxSlots];        // slot -> its place among its expert's slots
+    uint16_t big_expert[kMaxSlots / kMaxCols];   // experts of more than one entry
+};
+
+// All threads of the block; count: E_local ints of shared memory.
+__device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *count, int32_t *err)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < r.E_local; e += kThreads)
+        count[e] = 0;
+    if (tid == 0)
+        l.big = 0;
+    __syncthreads();
+    for (int s = tid; s < r.n; s += kThreads) {
+        const int e = r.local(s, err);
+        l.use[s] = (int16_t)e;
+        if (e >= 0)
+            l.place[s] = (uint16_t)atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    // each thread owns a run of experts; scans of (experts in use, entries, slots)
+    const int per = (r.E_local + kThreads - 1) / kThreads;
+    const int e0 = min(tid * per, r.E_local), e1 = min(e0 + per, r.E_local);
+    int own[3] = {0, 0, 0};
+    for (int e = e0; e < e1; ++e) {
+        const int c = count[e];
+        own[0] += c > 0;
+        own[1] += passes_of(c);
+        own[2] += c;
+    }
+    int sum[3] = {own[0], own[1], own[2]};
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int v = __shfl_up_sync(kFull, sum[i], o);
+            if (lane >= o)
+                sum[i] += v;
+        }
+    if (lane == 31)
+        for (int i = 0; i < 3; ++i)
+            l.scan[i][warp] = sum[i];
+    __syncthreads();
+    for (int i = 0; i < 3; ++i) {
+        sum[i] -= own[i];
+        for (int w = 0; w < warp; ++w)
+            sum[i] += l.scan[i][w];
+    }
+    int j = sum[0], q = sum[1], at = sum[2];
+    for (int e = e0; e < e1; ++e) {
+        const int c = count[e];
+        count[e] = q;
+        if (c == 0)
+            continue;
+        if (c > kMaxCols)
+            l.big_expert[atomicAdd(&l.big, 1)] = (uint16_t)e;
+        l.id[j] = (uint16_t)e;
+        l.entry[j] = (uint16_t)q;
+        // one pass reads a row from HBM, each further one from L2, at about twice the rate
+        l.cost[j] = j + q;
+        for (int b = 0; b < c; b += kMaxCols) {
+            l.owner[q] = (uint16_t)j;
+            l.begin[q++] = (uint16_t)(at + b);
+        }
+        ++j;
+        at += c;
+    }
+    if (tid == kThreads - 1) {
+        l.experts = j;
+        l.entries = q;
+        l.entry[j] = (uint16_t)q;
+        l.begin[q] = (uint16_t)at;
+        l.cost[j] = j + q;
+    }
+    __syncthreads();
+    // The order of slots within an entry moves no result, but every block must put the same slots into an
+    // entry: where an expert has several, its slots take their places in ascending order.
+    if (l.big > 0) {
+        for (int b = warp; b < l.big; b += kWarps) {
+            const int e = l.big_expert[b];
+            int before = 0;
+            for (int s0 = 0; s0 < r.n; s0 += 32) {
+                const int s = s0 + lane;
+                const bool hit = s < r.n && l.use[s] == e;
+                const unsigned m = __ballot_sync(kFull, hit);
+                if (hit)
+                    l.place[s] = (uint16_t)(before + __popc(m & lanemask_lt()));
+                before += __popc(m);
+            }
+        }
+        __syncthreads();
+    }
+    for (int s = tid; s < r.n; s += kThreads) {
+        const int e = l.use[s];
+        if (e >= 0) {
+            const int p = l.place[s], f = count[e];
+            l.slot[l.begin[f] + p] = (uint16_t)s;
+            l.use[s] = (int16_t)(f + p / kMaxCols);
+        }
+    }
+    __syncthreads();
+}
+
+struct Planes {
+    uint8_t *h;            // [planes][n][I] bf16
+    int64_t plane_bytes;
+    int I, planes;
+};
+
+// h as a sum of bf16 terms; an infinity or NaN is its own first term
+template <bool PERMUTED>
+__device__ __forceinline__ void store_planes(const Planes &p, int slot, int i, float h)
+{
+    const int place = (i & ~7) | column_place<PERMUTED>(i & 7);
+    uint8_t *at = p.h + ((int64_t)slot * p.I + place) * 2;
+    float rest = h;
+    for (int q = 0; q < p.planes; ++q) {
+        // toward zero, so that a term never rounds up to infinity; the last to nearest
+        const bool last = q == p.planes - 1;
+        const float term = last ? __bfloat162float(__float2bfloat16_rn(rest))
+                                : __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+        *reinterpret_cast<uint16_t *>(at + q * p.plane_bytes) = (uint16_t)(__float_as_uint(term) >> 16);
+        const float left = __fsub_rn(rest, term);
+        rest = isfinite(h) ? left : 0.0f;
+    }
+}
+
+// silu(gate) * up; a NaN keeps its set bits in the upper half, where the terms above look
+__device__ __forceinline__ float activate(float gate, float up)
+{
+    const float h = __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up);
+    return isnan(h) ? __int_as_float(0x7fffffff) : h;
+}
+
+template <int NT, int PLANES>
+__device__ __forceinline__ void set_columns(const Lists &l, int q, const uint8_t *rows, int64_t row_bytes,
+                                            int slots_per_row, Columns<NT, PLANES> &x)
+{
+    const int g = (threadIdx.x & 31) >> 2, first = l.begin[q], end = l.begin[q + 1];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int s = first + nt * 8 + g;
+        x.p[nt] = s < end ? rows + (int64_t)(l.slot[s] / slots_per_row) * row_bytes : nullptr;
+    }
+}
+
+// ------------------------------------------------------------------------ up --
+struct UpArgs {
+    const uint8_t *x;
+    Routing r;
+    int H, I;
+    Weights w;
+    Planes out;
+    int32_t *err;
+};
+
+// `n` elements cut into items of up to 8*RB, as equal as blocks of 8 allow.
+template <int RB>
+struct Cut {
+    int items, size;   // items, elements of each but the last
+
+    __device__ __forceinline__ explicit Cut(int n)
+    {
+        const int blocks = (n + 7) / 8, most = (blocks + RB - 1) / RB;
+        size = most > 0 ? (blocks + most - 1) / most * 8 : 8;
+        items = (n + size - 1) / size;
+    }
+};
+
+// A block's elements: from element i0 of expert j0 to element i1 of expert j1
+// (exclusive), in items that do not cross experts; the passes over an item's
+// weights follow one another, so that all but the first find them in L2.
+template <int G, int RB>
+struct UpItems {
+    using F = typename FormatOf<G, false>::F;
+    static constexpr int kStep = 8;
+    const UpArgs &a;
+    const Lists &l;
+    int j0, i0, j1, i1;
+    Cut<RB> head, body, tail;   // of the first expert, each whole one, and the last
+    int head_items;             // of all passes
+    float *side;           // this warp's kept piece of an item that another warp began
+    float *open;           // its kept piece of an item that it began and another goes on with
+
+    __device__ __forceinline__ int passes(int j) const { return l.entry[j + 1] - l.entry[j]; }
+
+    __device__ __forceinline__ UpItems(const UpArgs &args, const Lists &lists, int ja, int ia, int jb, int ib)
+        : a(args), l(lists), j0(ja), i0(ia), j1(jb), i1(ib), head((jb > ja ? args.I : ib) - ia), body(args.I), tail(ib)
+    {
+        head_items = head.items > 0 ? head.items * passes(j0) : 0;
+    }
+
+    __device__ __forceinline__ int count() const
+    {
+        int n = head_items;
+        if (j1 > j0) {
+            n += body.items * (l.entry[j1] - l.entry[j0 + 1]);
+            if (i1 > 0)
+                n += tail.items * passes(j1);
+        }
+        return n;
+    }
+
+    // item -> its entry, expert, and elements [i, end)
+    __device__ __forceinline__ void where(int item, int &q, int &j, int &i, int &end) const
+    {
+        int v = item, size = head.size;
+        j = j0;
+        i = i0;
+        if (item >= head_items) {
+            const int q1 = l.entry[j0 + 1];
+            v -= head_items;
+            j = l.owner[q1 + v / body.items];
+            v -= body.items * (l.entry[j] - q1);
+            i = 0;
+            size = j == j1 ? tail.size : body.size;
+        }
+        const int n = passes(j);
+        i += v / n * size;
+        q = l.entry[j] + v % n;
+        end = min(i + size, j == j1 ? i1 : a.I);
+    }
+
+    __device__ __forceinline__ RowRange rows(int item) const
+    {
+        int q, j, i, end;
+        where(item, q, j, i, end);
+        const int64_t row = (int64_t)l.id[j] * 2 * a.I + i;
+        return RowRange{row, row + a.I, end - i, end - i};
+    }
+
+    __device__ __forceinline__ int cols(int item) const
+    {
+        int q, j, i, end;
+        where(item, q, j, i, end);
+        return l.begin[q + 1] - l.begin[q];
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void columns(int item, Columns<NT, 1> &x) const
+    {
+        int q, j, i, end;
+        where(item, q, j, i, end);
+        x.plane_bytes = 0;
+        set_columns<NT, 1>(l, q, a.x, (int64_t)a.H * 2, a.r.K, x);
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void done(int item, bool first, bool last, const float (&acc)[RB][NT][4]) const
+    {
+        if (!first || !last) {
+            keep<RB, NT>(first ? open : side, acc);
+            return;
+        }
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        int q, j, i, end;
+        where(item, q, j, i, end);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int s = l.begin[q] + nt * 8 + 2 * t + c;
+                if (s < l.begin[q + 1])
+#pragma unroll
+                    for (int r = 0; r < RB; ++r)
+                        if (i + 8 * r + g < end)
+                            store_planes<(G > 0)>(a.out, l.slot[s], i + 8 * r + g,
+                                                  activate(acc[r][nt][c], acc[r][nt][2 + c]));
+            }
+    }
+};
+
+// the expert and element at position pos of the costs laid end to end
+__device__ __forceinline__ void find(const Lists &l, int I, int64_t pos, int &j, int &i)
+{
+    int lo = 0, hi = l.experts;   // cost[lo] * I <= pos < cost[hi] * I
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)l.cost[mid] * I <= pos)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    j = lo;
+    i = (int)((pos - (int64_t)l.cost[lo] * I) / (l.cost[lo + 1] - l.cost[lo]));
+}
+
+template <int G, int RB>
+__global__ void __launch_bounds__(kThreads, 1)
+moe_up_kernel(UpArgs a)
+{
+    extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
+    __shared__ Lists l;
+    using F = typename FormatOf<G, false>::F;
+    grid_dependency_wait();
+    allow_dependents();
+    build_lists(a.r, l, reinterpret_cast<int *>(dynamic), blockIdx.x == 0 ? a.err : nullptr);
+    if (l.experts == 0)
+        return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *sides = dynamic + Room<RB>::kRing;
+    const int64_t total = (int64_t)l.cost[l.experts] * a.I;
+    int j0, i0, j1 = l.experts, i1 = 0;
+    find(l, a.I, total * blockIdx.x / gridDim.x, j0, i0);
+    if (blockIdx.x + 1 < gridDim.x)
+        find(l, a.I, total * (blockIdx.x + 1) / gridDim.x, j1, i1);
+    UpItems<G, RB> items(a, l, j0, i0, j1, i1);
+    items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
+    items.open = reinterpret_cast<float *>(dynamic + warp * kWarpRing);   // the ring is idle by then
+    const int n = items.count();
+    if (n == 0)
+        return;
+    Stream<F, RB, 1, UpItems<G, RB>> stream(items, a.w, a.H, n, smem_u32(dynamic));
+    stream.start();
+    stream.run();
+    __syncthreads();
+    // the warp that began an item which others went on with adds up its pieces
+    const int per = (a.H + F::kUnit - 1) / F::kUnit;
+    const int begin = run_begin(n, per, warp), end = run_begin(n, per, warp + 1);
+    const int item = (end - 1) / per;
+    if (begin == end || end % per == 0 || item * per < begin)
+        return;
+    int q, j, i, stop;
+    items.where(item, q, j, i, stop);
+    const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
+    for (int v = lane; v < 8 * RB * cols; v += 32) {
+        const int e = v % (8 * RB), c = v / (8 * RB);
+        if (i + e >= stop)
+            continue;
+        const int ga = side_index(e >> 3, e & 7, nb, c), ua = side_index(e >> 3, (e & 7) + 8, nb, c);
+        const float gate = add_pieces<RB>(items.open[ga], sides, n, per, item, ga);
+        const float up = add_pieces<RB>(items.open[ua], sides, n, per, item, ua);
+        store_planes<(G > 0)>(a.out, l.slot[first + c], i + e, activate(gate, up));
+    }
+}
+
+// ---------------------------------------------------------------------- down --
+struct DownArgs {
+    Routing r;
+    const float *weights;
+    int T, H, I;
+    Weights w;
+    Planes h;
+    void *out;
+    int out_f32;
+    float *y;          // [n][H] of the workspace, or null where the slots' results fit in shared memory
+};
+
+// A block's output rows [row0, row1) in groups of up to 16*RB, times all entries.
+template <int G, int PLANES, int RB>
+struct DownItems {
+    using F = typename FormatOf<G, (G > 0)>::F;
+    static constexpr int kStep = 16;
+    const DownArgs &a;
+    const Lists &l;
+    int row0, row1;
+    float *y;              // [n], `stride` floats apart: the block's rows of each slot
+    int stride;
+    float *side;
+
+    __device__ __forceinline__ RowRange rows(int item) const
+    {
+        const int b = item / l.entries, q = item - b * l.entries;
+        const int r = row0 + b * (16 * RB), n = min(row1 - r, 16 * RB);
+        const int64_t row = (int64_t)l.id[l.owner[q]] * a.H + r;
+        return RowRange{row, row + 8, n, n - 8};
+    }
+
+    __device__ __forceinline__ int cols(int item) const
+    {
+        const int q = item % l.entries;
+        return l.begin[q + 1] - l.begin[q];
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void columns(int item, Columns<NT, PLANES> &x) const
+    {
+        x.plane_bytes = a.h.plane_bytes;
+        set_columns<NT, PLANES>(l, item % l.entries, a.h.h, (int64_t)a.I * 2, 1, x);
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void done(int item, bool first, bool, const float (&acc)[RB][NT][4]) const
+    {
+        if (!first) {
+            keep<RB, NT>(side, acc);
+            return;
+        }
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int b = item / l.entries, q = item - b * l.entries, rows = row1 - row0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int s = l.begin[q] + nt * 8 + 2 * t + c;
+                if (s < l.begin[q + 1]) {
+                    float *p = y + (int64_t)l.slot[s] * stride;
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) {
+                        const int i = (b * RB + r) * 16 + g;
+                        if (i < rows)
+                            p[i] = acc[r][nt][c];
+                        if (i + 8 < rows)
+                            p[i + 8] = acc[r][nt][2 + c];
+                    }
+                }
+            }
+    }
+};
+
+template <int G, int PLANES, int RB>
+__global__ void __launch_bounds__(kThreads, 1)
+moe_down_kernel(DownArgs a)
+{
+    extern __shared__ __align__(16) uint8_t dynamic[];   // ring, one side block per warp, y if it fits
+    __shared__ Lists l;
+    using F = typename FormatOf<G, (G > 0)>::F;
+    // topk_idx was complete before the up kernel began; h is complete after the wait
+    build_lists(a.r, l, reinterpret_cast<int *>(dynamic), nullptr);
+    const int warp = threadIdx.x >> 5;
+    uint8_t *sides = dynamic + Room<RB>::kRing;
+    DownItems<G, PLANES, RB> items{a, l};
+    items.row0 = (int)((int64_t)a.H * blockIdx.x / gridDim.x);
+    items.row1 = (int)((int64_t)a.H * (blockIdx.x + 1) / gridDim.x);
+    const int rows = items.row1 - items.row0;
+    items.y = a.y != nullptr ? a.y + items.row0 : reinterpret_cast<float *>(dynamic + Room<RB>::kFixed);
+    items.stride = a.y != nullptr ? a.H : rows | 1;
+    items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
+    const int n = (rows + 16 * RB - 1) / (16 * RB) * l.entries;
+    const int per = (a.I + F::kUnit - 1) / F::kUnit, K = a.r.K;
+    Stream<F, RB, PLANES, DownItems<G, PLANES, RB>> stream(items, a.w, a.I, n, smem_u32(dynamic));
+    stream.start();
+    grid_dependency_wait();
+    allow_dependents();
+    stream.run();
+    __syncthreads();
+    // weighted sums over k; a slot's divided items are added in the order of their columns
+    for (int v = threadIdx.x; v < a.T * rows; v += kThreads) {
+        const int tok = v / rows, i = v - tok * rows;
+        const int b = i / (16 * RB), ib = i - b * (16 * RB);
+        float sum = 0.0f;
+        for (int k = 0; k < K; ++k) {
+            const int slot = tok * K + k;
+            const int q = l.use[slot];
+            if (q < 0)
+                continue;
+            const int nb = l.begin[q + 1] - l.begin[q] <= 8 ? 1 : 2;
+            const int at = side_index(ib >> 4, ib & 15, nb, l.place[slot] % kMaxCols);
+            const float p = add_pieces<RB>(items.y[(int64_t)slot * items.stride + i], sides, n, per,
+                                           b * l.entries + q, at);
+            sum = __fmaf_rn(a.weights[slot], p, sum);
+        }
+        const int64_t o = (int64_t)tok * a.H + items.row0 + i;
+        if (a.out_f32)
+            static_cast<float *>(a.out)[o] = sum;
+        else
+            static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(sum);
+    }
+}
+
+// ------------------------------------------------------------ launch policy --
+constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - 64;   // dynamic shared memory of a block that owns an SM
+
+template <class Kernel>
+inline int raise_smem(Kernel kernel, size_t smem, PerDevice &set)
+{
+    const int dev = current_device();
+    if ((int)smem > set.get(dev)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+            cudaGetLastError();
+            return EP_ERR_CUDA;
+        }
+        set.put(dev, (int)smem);
+    }
+    return EP_OK;
+}
+
+template <class Kernel, class Args>
+int launch_dependent(Kernel kernel, unsigned grid, size_t smem, cudaStream_t stream, const Args &a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return EP_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+template <int G, int RB>
+int launch_up(const UpArgs &a, int64_t elements, cudaStream_t stream)
+{
+    static_assert(EP_MAX_EXPERTS * sizeof(int) <= (size_t)Room<RB>::kRing, "the experts' counters use the ring before it starts");
+    static PerDevice set;
+    const int rc = raise_smem(moe_up_kernel<G, RB>, Room<RB>::kFixed, set);
+    if (rc != EP_OK)
+        return rc;
+    const unsigned grid = (unsigned)std::min<int64_t>(elements, device_sm_count());
+    return launch_dependent(moe_up_kernel<G, RB>, grid, Room<RB>::kFixed, stream, a);
+}
+
+template <int G, int PLANES, int RB>
+int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
+{
+    static PerDevice set;
+    // the slots' results stay in shared memory where there is room for them
+    const size_t y = (size_t)a.r.n * ((size_t)ceil_div(a.H, grid) | 1) * sizeof(float);
+    size_t smem = Room<RB>::kFixed;
+    if (smem + y <= kMaxSmem) {
+        smem += y;
+        a.y = nullptr;
+    }
+    const int rc = raise_smem(moe_down_kernel<G, PLANES, RB>, smem, set);
+    if (rc != EP_OK)
+        return rc;
+    return launch_dependent(moe_down_kernel<G, PLANES, RB>, grid, smem, stream, a);
+}
+
+// The two kernels.  A warp takes as many blocks of 16 rows at a time as its
+// block has rows for: each x it loads serves all of them.
+template <int G>
+int launch(const UpArgs &up, const DownArgs &down, cudaStream_t stream)
+{
+    const int sms = device_sm_count();
+    const int64_t elements = (int64_t)std::min(up.r.n, up.r.E_local) * up.I;   // at most: the experts in use are not known here
+    const int64_t mine = ceil_div(elements, sms);
+    int rc = mine > 16 ? launch_up<G, 4>(up, elements, stream)
+             : mine > 8 ? launch_up<G, 2>(up, elements, stream) : launch_up<G, 1>(up, elements, stream);
+    if (rc != EP_OK)
+        return rc;
+    const unsigned grid = (unsigned)std::min(sms, down.H);
+    const int64_t rows = ceil_div(down.H, grid);
+    if (down.out_f32)
+        return rows > 32 ? launch_down<G, 3, 3>(down, grid, stream)
+               : rows > 16 ? launch_down<G, 3, 2>(down, grid, stream) : launch_down<G, 3, 1>(down, grid, stream);
+    return rows > 32 ? launch_down<G, 2, 3>(down, grid, stream)
+           : rows > 16 ? launch_down<G, 2, 2>(down, grid, stream) : launch_down<G, 2, 1>(down, grid, stream);
+}
+
+}  // namespace ep

@@ -1,0 +1,8 @@
+// The few-token experts' kernels for 4-bit weights in groups of 128.
+#include "ep_moe.cuh"
+
+namespace ep {
+
+template int launch<128>(const UpArgs &, const DownArgs &, cudaStream_t);
+
+}  // namespace ep

@@ -3,17 +3,22 @@
 // With a few tokens every weight is used a handful of times, so these products
 // are bound by reading the weights from HBM, and what counts is that enough of
 // them is in flight all the time.  A block owns an SM and a share of the weight
-// rows; its 16 warps share that work in equal runs of K, each streaming its own
-// 16 rows at a time through a ring of its own in shared memory:
+// rows; its 8 warps share that work in equal runs of K, each streaming up to 64
+// rows at a time through a ring of its own in shared memory:
 //
-//   - cp.async copies 16 bytes of a row to the slot of the very lane that will
-//     use them, so a lane waits for its own copies only: no barrier stands
-//     between the copy and its use, and the ring runs across items;
+//   - cp.async brings 16 rows times 256 bytes (4-bit: 128) to a stage of the
+//     ring, whole row pieces by neighbouring lanes.  No block barrier stands
+//     between a copy and its use, and the ring runs on across items.  (Copied
+//     in pieces of 64, 128, 256 and 512 bytes, a plain stream of rows ran at
+//     6.1, 6.4, 6.9 and 7.1 TB/s.)
 //   - lane (g, t) holds rows g and g+8 of an m16n8k16 matrix step and takes
 //     whole 16-byte pieces of them, offering the same columns of x for the
 //     instruction's k positions: a sum over k does not care about its order;
 //   - the columns (tokens) are the instruction's N = 8 side, so one token costs
-//     what eight do, which is nothing beside the weight stream.
+//     what eight do, which is nothing beside the weight stream;
+//   - x comes through L1 and L2 into registers, one unit of K ahead, and serves
+//     all of the warp's row blocks.  (With 16 rows a warp and x loaded where it
+//     is used, eight tokens ran at 3.5 TB/s, waiting for x.)
 //
 // Accumulators: the matrix step's fp32 sums run over at most 128 columns of K
 // (one group of 4-bit weights); these partial sums are then scaled and added
@@ -26,14 +31,19 @@
 
 namespace ep {
 
-constexpr int kSkinnyWarps = 16;
+constexpr int kSkinnyWarps = 8;
 constexpr int kSkinnyThreads = 32 * kSkinnyWarps;
-constexpr int kGroupUnits = 2;       // units (1 KB: 16 rows) of one ring stage
-constexpr int kStages = 3;           // stages in flight per warp: 96 KB per SM, twice what 45 KB/us x 1 us needs
-constexpr int kStageBytes = kGroupUnits * 1024;
-constexpr int kRingBytes = kSkinnyWarps * kStages * kStageBytes;
-constexpr int kMaxCols = 32;         // columns of one pass over the weights: 4 blocks of 8
-constexpr int kSideBytes = 16 * kMaxCols * 4;   // one 16 x 32 block of partial sums
+constexpr int kMaxCols = 16;         // columns of one pass over the weights: 2 blocks of 8
+
+constexpr int kWarpRing = 16 * 1024;   // 128 KB per SM in flight; 45 KB/us times about 1 us are needed
+
+// The shared memory of a block whose warps take up to RB blocks of 16 rows at a time.
+template <int RB>
+struct Room {
+    static constexpr int kRing = kSkinnyWarps * kWarpRing;
+    static constexpr int kSide = RB * 16 * kMaxCols * 4;   // one warp's kept sums
+    static constexpr int kFixed = kRing + kSkinnyWarps * kSide;
+};
 
 // D += A (16x16, row) * B (16x8, col), bf16 in, fp32 sums.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -90,12 +100,12 @@ struct Columns {
     }
 };
 
-// Where a lane's two rows lie.  A row past the end of its block has a null data
-// pointer: it is not read, and its sums are not used.
-struct RowPtrs {
-    const uint8_t *r0, *r1;     // data of rows g and g+8
-    const uint16_t *s0, *s1;    // 4-bit: scales (bf16 bits)
-    const uint8_t *z0, *z1;     // 4-bit: zero points, or null
+// An item's rows: block r takes rows a + r*step .. +7 (the first n of a's rows
+// exist) and b + r*step .. +7 (the first m of b's), as rows 0-7 and 8-15 of the
+// matrix step.  Rows that do not exist are not read, and their sums not used.
+struct RowRange {
+    int64_t a, b;
+    int n, m;
 };
 
 struct Weights {
@@ -104,103 +114,89 @@ struct Weights {
     const uint8_t *zero;
 };
 
-// bf16 weights.  A unit is 32 columns: lane (g, t) holds columns 8t .. 8t+7 of
-// rows g and g+8, two k16 steps.
+// bf16 weights.  A unit is 128 columns; word j of lane (g, t) are columns
+// 32j + 8t .. +7 of its rows, two k16 steps.
 struct FormatBf16 {
-    static constexpr int kUnit = 32;
+    static constexpr int kUnit = 128;
+    static constexpr int kRowPiece = 256;    // bytes of a row in a unit
+    static constexpr int kWordsX = 4;        // 8-column words of x that a lane holds for a unit
     static constexpr bool kPermuted = false;
-    // what an item costs beside one n-block's columns: 1 KB of weights to 0.5 KB of x
-    static constexpr int kItemCost = 4;
-    struct Extra {};
+    static constexpr int kPieces = 4;        // 16-byte pieces of a lane's row in a stage
 
-    static __device__ __forceinline__ RowPtrs rows(const Weights &w, int64_t a, int64_t b, bool has_a, bool has_b, int K)
+    static __device__ __forceinline__ int64_t row_bytes(int K) { return (int64_t)K * 2; }
+    static __device__ __forceinline__ int column(int u, int w, int t) { return u * kUnit + 32 * w + 8 * t; }
+    static __device__ __forceinline__ uint4 pair(uint4 v) { return v; }
+
+    template <int RB>
+    struct Scales {
+        __device__ __forceinline__ void begin(const Weights &, const RowRange &, int, int, int) {}
+        __device__ __forceinline__ void load(int, int, int, int) {}
+    };
+
+    // acc += block r of the unit; next(w) is called once word w of x is used up
+    template <int RB, int NT, int PLANES, class Next>
+    static __device__ __forceinline__ void block(const uint4 (&a)[kPieces], const uint4 (&b)[kPieces], int,
+                                                 const Scales<RB> &, const uint4 (&x)[kWordsX][NT][PLANES], int,
+                                                 float (&acc)[NT][4], Next next)
     {
-        const int64_t bytes = (int64_t)K * 2;
-        RowPtrs r = {};
-        r.r0 = has_a ? w.data + a * bytes : nullptr;
-        r.r1 = has_b ? w.data + b * bytes : nullptr;
-        return r;
-    }
-
-    static __device__ __forceinline__ int column(int u, int t) { return u * kUnit + 8 * t; }
-    static __device__ __forceinline__ int64_t offset(int k) { return (int64_t)k * 2; }
-    static __device__ __forceinline__ Extra extra(const RowPtrs &, int, int, int) { return Extra{}; }
-
-    template <int NT, int PLANES>
-    static __device__ __forceinline__ void unit(const uint4 &a, const uint4 &b, const Extra &, int u, int K, int t,
-                                                const Columns<NT, PLANES> &x, float (&acc)[NT][4])
-    {
-        const int k = column(u, t);
+        float part[NT][4] = {};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float part[4] = {};
+        for (int j = 0; j < 4; ++j) {
 #pragma unroll
-            for (int p = 0; p < PLANES; ++p) {
-                const uint4 v = x.load(nt, p, k, K);
-                mma_bf16(part, a.x, b.x, a.y, b.y, v.x, v.y);
-                mma_bf16(part, a.z, b.z, a.w, b.w, v.z, v.w);
-            }
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                acc[nt][c] = __fadd_rn(acc[nt][c], part[c]);
+                for (int p = 0; p < PLANES; ++p) {
+                    const uint4 v = x[j][nt][p];
+                    mma_bf16(part[nt], a[j].x, b[j].x, a[j].y, b[j].y, v.x, v.y);
+                    mma_bf16(part[nt], a[j].z, b[j].z, a[j].w, b[j].w, v.z, v.w);
+                }
+            next(j);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[nt][i] = __fadd_rn(acc[nt][i], part[nt][i]);
     }
 };
 
-// 4-bit weights with a scale (and zero point) per G columns.  A unit is 128
-// columns: lane (g, t) loads the 32 codes of columns 32t .. 32t+31 of rows g
-// and g+8.  Codes become bf16 integers exactly: 0x4300 | q is 128 + q, less
-// 128 + zero.  Word bits 4j hold code j, so masking 0x000f000f takes codes
+// 4-bit weights with a scale (and zero point) per G columns.  A unit is 256
+// columns, two halves: lane (g, t) reads the 32 codes of columns 32t .. 32t+31
+// of each half.  Codes become bf16 integers exactly: 0x4300 | q is 128 + q,
+// less 128 + zero.  Word bits 4j hold code j, so masking 0x000f000f takes codes
 // (j, j+4) as a pair; x's columns are paired the same way (by the stored order
-// where PERMUTED, else by byte permutes).  With G < 128 a lane's words belong
-// to other groups than its neighbours', so the four lanes of a row trade words
+// where PERMUTED, else by byte permutes).  With G < 128 a lane's words belong to
+// other groups than its neighbours', so the four lanes of a row trade words
 // until each matrix step stays in one group.
 template <int G, bool PERMUTED>
 struct FormatW4 {
-    static constexpr int kUnit = 128;
+    static constexpr int kUnit = 256;
+    static constexpr int kRowPiece = 128;
+    static constexpr int kWordsX = 8;
     static constexpr bool kPermuted = PERMUTED;
-    static constexpr int kItemCost = 2;
-    struct Extra {
-        uint32_t q0, q1;    // scale in the high half, bf16(128 + zero) in the low half
-    };
+    static constexpr int kPieces = 2;
+    static constexpr int kWords = G / 32;   // words of a lane in one group
 
-    static __device__ __forceinline__ RowPtrs rows(const Weights &w, int64_t a, int64_t b, bool has_a, bool has_b, int K)
+    static __device__ __forceinline__ int64_t row_bytes(int K) { return K / 2; }
+
+    // word w of lane t once the lanes have traded
+    static __device__ __forceinline__ int column(int u, int w, int t)
     {
-        const int64_t bytes = K / 2, groups = K / G;
-        RowPtrs r = {};
-        if (has_a) {
-            r.r0 = w.data + a * bytes;
-            r.s0 = w.scale + a * groups;
-            r.z0 = w.zero != nullptr ? w.zero + a * groups : nullptr;
-        }
-        if (has_b) {
-            r.r1 = w.data + b * bytes;
-            r.s1 = w.scale + b * groups;
-            r.z1 = w.zero != nullptr ? w.zero + b * groups : nullptr;
-        }
-        return r;
+        const int base = u * kUnit + 128 * (w >> 2), i = w & 3;
+        if (G == 128)
+            return base + 32 * t + 8 * i;
+        if (G == 64)
+            return base + 64 * (i >> 1) + 32 * (t & 1) + 16 * (t >> 1) + 8 * (i & 1);
+        return base + 32 * i + 8 * t;
     }
 
-    static __device__ __forceinline__ int column(int u, int t) { return u * kUnit + 32 * t; }
-    static __device__ __forceinline__ int64_t offset(int k) { return k >> 1; }
-
-    static __device__ __forceinline__ uint32_t group(const uint16_t *s, const uint8_t *z, int gi)
+    static __device__ __forceinline__ uint4 pair(uint4 v)
     {
-        const uint32_t zero = z != nullptr ? (uint32_t)__ldg(z + gi) : 8u;
-        return ((uint32_t)__ldg(s + gi) << 16) | 0x4300u | zero;
-    }
-
-    static __device__ __forceinline__ Extra extra(const RowPtrs &r, int u, int K, int t)
-    {
-        const int k = column(u, t);
-        Extra e{0x4308u, 0x4308u};
-        if (k < K) {
-            if (r.s0 != nullptr)
-                e.q0 = group(r.s0, r.z0, k / G);
-            if (r.s1 != nullptr)
-                e.q1 = group(r.s1, r.z1, k / G);
-        }
-        return e;
+        if (PERMUTED)
+            return v;
+        // columns (0,4) (1,5) (2,6) (3,7)
+        return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                          __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
     }
 
     // (a, b) -> the low lane keeps a and gets its partner's a, the high lane keeps b and gets b
@@ -212,27 +208,17 @@ struct FormatW4 {
         b = high ? b : in;
     }
 
-    // after it, word i of lane t lies in columns word_column(i, t) of the unit
-    static __device__ __forceinline__ void arrange(uint4 &w, int t)
+    static __device__ __forceinline__ void arrange(uint32_t (&w)[4], int t)
     {
         if (G == 64) {
-            trade(w.x, w.z, 2, t & 2);
-            trade(w.y, w.w, 2, t & 2);
+            trade(w[0], w[2], 2, t & 2);
+            trade(w[1], w[3], 2, t & 2);
         } else if (G == 32) {
-            trade(w.x, w.y, 1, t & 1);
-            trade(w.z, w.w, 1, t & 1);
-            trade(w.x, w.z, 2, t & 2);
-            trade(w.y, w.w, 2, t & 2);
+            trade(w[0], w[1], 1, t & 1);
+            trade(w[2], w[3], 1, t & 1);
+            trade(w[0], w[2], 2, t & 2);
+            trade(w[1], w[3], 2, t & 2);
         }
-    }
-
-    static __device__ __forceinline__ int word_column(int i, int t)
-    {
-        if (G == 128)
-            return 32 * t + 8 * i;
-        if (G == 64)
-            return 64 * (i >> 1) + 32 * (t & 1) + 16 * (t >> 1) + 8 * (i & 1);
-        return 32 * i + 8 * t;
     }
 
     static __device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t zz)
@@ -240,52 +226,88 @@ struct FormatW4 {
         return sub_bf16x2((w & 0x000f000fu) | 0x43004300u, zz);
     }
 
-    template <int NT, int PLANES>
-    static __device__ __forceinline__ void unit(uint4 wa, uint4 wb, const Extra &e, int u, int K, int t,
-                                                const Columns<NT, PLANES> &x, float (&acc)[NT][4])
+    // a lane's scales and zero points of the unit, for its rows of every block: the scale in the high half,
+    // bf16(128 + zero) in the low half
+    template <int RB>
+    struct Scales {
+        uint32_t q[RB][2][2];
+        const uint16_t *s0, *s1;
+        const uint8_t *z0, *z1;
+        int n, m, step;
+        int64_t per_row;
+
+        __device__ __forceinline__ void begin(const Weights &w, const RowRange &rows, int row_step, int K, int g)
+        {
+            per_row = K / G;
+            s0 = w.scale + (rows.a + g) * per_row;
+            s1 = w.scale + (rows.b + g) * per_row;
+            z0 = w.zero != nullptr ? w.zero + (rows.a + g) * per_row : nullptr;
+            z1 = w.zero != nullptr ? w.zero + (rows.b + g) * per_row : nullptr;
+            n = rows.n - g;
+            m = rows.m - g;
+            step = row_step;
+        }
+
+        __device__ __forceinline__ void load(int r, int u, int K, int t)
+        {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = u * kUnit + 128 * h + 32 * t;
+                const int64_t at = r * step * per_row + k / G;
+                q[r][h][0] = q[r][h][1] = 0x4308u;
+                if (k < K && r * step < n)
+                    q[r][h][0] = ((uint32_t)__ldg(s0 + at) << 16) | 0x4300u | (z0 != nullptr ? (uint32_t)__ldg(z0 + at) : 8u);
+                if (k < K && r * step < m)
+                    q[r][h][1] = ((uint32_t)__ldg(s1 + at) << 16) | 0x4300u | (z1 != nullptr ? (uint32_t)__ldg(z1 + at) : 8u);
+            }
+        }
+    };
+
+    template <int RB, int NT, int PLANES, class Next>
+    static __device__ __forceinline__ void block(const uint4 (&va)[kPieces], const uint4 (&vb)[kPieces], int r,
+                                                 const Scales<RB> &s, const uint4 (&x)[kWordsX][NT][PLANES], int t,
+                                                 float (&acc)[NT][4], Next next)
     {
-        constexpr int kWords = G / 32;   // words of a lane in one group
-        arrange(wa, t);
-        arrange(wb, t);
-        const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-        for (int gi = 0; gi < 4 / kWords; ++gi) {
-            uint32_t q0 = e.q0, q1 = e.q1;
-            if (G < 128) {   // the lane of this row that loaded this group's scale
-                const int from = (threadIdx.x & 28) | (gi * kWords);
-                q0 = __shfl_sync(kFull, q0, from);
-                q1 = __shfl_sync(kFull, q1, from);
-            }
-            const uint32_t zz0 = __byte_perm(q0, q0, 0x1010), zz1 = __byte_perm(q1, q1, 0x1010);
-            float part[NT][4] = {};
+        for (int h = 0; h < 2; ++h) {
+            uint32_t a[4] = {va[h].x, va[h].y, va[h].z, va[h].w}, b[4] = {vb[h].x, vb[h].y, vb[h].z, vb[h].w};
+            arrange(a, t);
+            arrange(b, t);
 #pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-                const int w = gi * kWords + j;
-                const int k = u * kUnit + word_column(w, t);
-                const uint32_t a = va[w], b = vb[w];
-                const uint32_t a0 = codes(a, zz0), a1 = codes(a >> 4, zz0), a2 = codes(a >> 8, zz0),
-                               a3 = codes(a >> 12, zz0);
-                const uint32_t c0 = codes(b, zz1), c1 = codes(b >> 4, zz1), c2 = codes(b >> 8, zz1),
-                               c3 = codes(b >> 12, zz1);
+            for (int gi = 0; gi < 4 / kWords; ++gi) {
+                uint32_t q0 = s.q[r][h][0], q1 = s.q[r][h][1];
+                if (G < 128) {   // the lane of this row that loaded this group's scale
+                    const int from = (threadIdx.x & 28) | (gi * kWords);
+                    q0 = __shfl_sync(kFull, q0, from);
+                    q1 = __shfl_sync(kFull, q1, from);
+                }
+                const uint32_t zz0 = __byte_perm(q0, q0, 0x1010), zz1 = __byte_perm(q1, q1, 0x1010);
+                float part[NT][4] = {};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int j = 0; j < kWords; ++j) {
+                    const int i = gi * kWords + j, w = 4 * h + i;
+                    const uint32_t a0 = codes(a[i], zz0), a1 = codes(a[i] >> 4, zz0), a2 = codes(a[i] >> 8, zz0),
+                                   a3 = codes(a[i] >> 12, zz0);
+                    const uint32_t b0 = codes(b[i], zz1), b1 = codes(b[i] >> 4, zz1), b2 = codes(b[i] >> 8, zz1),
+                                   b3 = codes(b[i] >> 12, zz1);
 #pragma unroll
-                    for (int p = 0; p < PLANES; ++p) {
-                        uint4 v = x.load(nt, p, k, K);
-                        if (!PERMUTED)   // columns (0,4) (1,5) (2,6) (3,7)
-                            v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                           __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-                        mma_bf16(part[nt], a0, c0, a1, c1, v.x, v.y);
-                        mma_bf16(part[nt], a2, c2, a3, c3, v.z, v.w);
-                    }
-            }
-            const float f0 = __uint_as_float(q0 & 0xffff0000u), f1 = __uint_as_float(q1 & 0xffff0000u);
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                acc[nt][0] = __fmaf_rn(part[nt][0], f0, acc[nt][0]);
-                acc[nt][1] = __fmaf_rn(part[nt][1], f0, acc[nt][1]);
-                acc[nt][2] = __fmaf_rn(part[nt][2], f1, acc[nt][2]);
-                acc[nt][3] = __fmaf_rn(part[nt][3], f1, acc[nt][3]);
+                        for (int p = 0; p < PLANES; ++p) {
+                            const uint4 v = x[w][nt][p];
+                            mma_bf16(part[nt], a0, b0, a1, b1, v.x, v.y);
+                            mma_bf16(part[nt], a2, b2, a3, b3, v.z, v.w);
+                        }
+                    next(w);
+                }
+                const float f0 = __uint_as_float(q0 & 0xffff0000u), f1 = __uint_as_float(q1 & 0xffff0000u);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    acc[nt][0] = __fmaf_rn(part[nt][0], f0, acc[nt][0]);
+                    acc[nt][1] = __fmaf_rn(part[nt][1], f0, acc[nt][1]);
+                    acc[nt][2] = __fmaf_rn(part[nt][2], f1, acc[nt][2]);
+                    acc[nt][3] = __fmaf_rn(part[nt][3], f1, acc[nt][3]);
+                }
             }
         }
     }
@@ -308,37 +330,61 @@ __device__ __forceinline__ int column_place(int j)
     return PERMUTED ? ((j & 3) << 1) | (j >> 2) : j;
 }
 
-// A warp's sums of one item as they are kept: [block of 8 columns][lane] float4.
-__device__ __forceinline__ int side_index(int row, int col)   // in floats
+// A warp's sums of one item as they are kept: [row block][column block][lane] float4.
+__device__ __forceinline__ int side_index(int block, int row, int nt_blocks, int col)   // in floats
 {
     const int lane = ((row & 7) << 2) | ((col & 7) >> 1);
-    return (((col >> 3) * 32 + lane) << 2) | ((row >> 3) << 1) | (col & 1);
+    return (((block * nt_blocks + (col >> 3)) * 32 + lane) << 2) | ((row >> 3) << 1) | (col & 1);
+}
+
+template <int RB, int NT>
+__device__ __forceinline__ void keep(float *side, const float (&acc)[RB][NT][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            *reinterpret_cast<float4 *>(side + ((r * NT + nt) * 32 + lane) * 4) =
+                make_float4(acc[r][nt][0], acc[r][nt][1], acc[r][nt][2], acc[r][nt][3]);
 }
 
 // One warp's run of a block's items.  Items are numbered 0 .. items-1; each is
-// 16 rows times all of K (`per` units).  The run is units [begin, end) of the
-// items laid end to end: it may start or stop inside an item.
+// up to 16*RB rows times all of K (`per` units).  The run is units [begin, end)
+// of the items laid end to end: it may start or stop inside an item.
 //
-// Items is the kernel's view of its work: rows(item) gives this lane's RowPtrs,
-// blocks(item) the number of 8-column blocks (1 .. 4), columns<NT>(item, x)
-// sets the column pointers, and done<NT>(item, first, last, acc) takes the sums
-// of a piece; first / last say whether the piece holds the item's first and
-// last unit.
-template <class F, int PLANES, class Items>
+// Items is the kernel's view of its work: rows(item) gives its rows, kStep the
+// rows from one block to the next, cols(item) the number of columns,
+// columns<NT>(item, x) sets this lane's column pointers, and done<NT>(item,
+// first, last, acc) takes the sums of a piece; first / last say whether the
+// piece holds the item's first and last unit.
+template <class F, int RB, int PLANES, class Items>
 class Stream {
 public:
-    __device__ __forceinline__ Stream(Items &items, int K, int n_items, uint32_t ring)
-        : items_(items), K_(K), per_((K + F::kUnit - 1) / F::kUnit)
+    static constexpr int kStageBytes = 16 * F::kRowPiece;
+    static constexpr int kStages = kWarpRing / kStageBytes;
+    static constexpr int kLanes = F::kRowPiece / 16;   // lanes that copy one row
+    static constexpr int kAtOnce = 32 / kLanes;        // rows of one copy instruction
+
+    __device__ __forceinline__ Stream(const Items &items, const Weights &w, int K, int n_items, uint32_t ring)
+        : items_(items), w_(w), K_(K), per_((K + F::kUnit - 1) / F::kUnit)
     {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        g_ = lane >> 2;
         t_ = lane & 3;
         const int64_t total = (int64_t)n_items * per_;
         begin_ = (int)(total * warp / kSkinnyWarps);
         end_ = (int)(total * (warp + 1) / kSkinnyWarps);
-        slot_ = ring + warp * (kStages * kStageBytes) + lane * 16;
+        ring_ = ring + warp * kWarpRing;
+        // a row's 16-byte pieces are swapped in groups of four on odd rows, so that the eight lanes of a
+        // quarter warp, which read two rows, meet all 32 banks
+        const int row = lane / kLanes, piece = lane % kLanes;
+        put_ = row * F::kRowPiece + (piece ^ ((row & 1) << 2)) * 16;
+        get_ = g_ * F::kRowPiece + t_ * 16;
         ahead_ = begin_;
         item_ahead_ = begin_ / per_;
         u_ahead_ = begin_ - item_ahead_ * per_;
+        r_ahead_ = 0;
         stage_ahead_ = stage_ = 0;
         fresh_ = true;
     }
@@ -357,45 +403,53 @@ public:
         while (at < end_) {
             const int item = at / per_, u0 = at - item * per_;
             const int u1 = min(per_, u0 + end_ - at);
-            const int nb = items_.blocks(item);
-            if (nb <= 1)
+            if (items_.cols(item) <= 8)
                 piece<1>(item, u0, u1);
-            else if (nb == 2)
-                piece<2>(item, u0, u1);
             else
-                piece<4>(item, u0, u1);
+                piece<2>(item, u0, u1);
             at += u1 - u0;
         }
     }
 
 private:
+    static __device__ __forceinline__ int blocks(const RowRange &r) { return (r.n + Items::kStep - 1) / Items::kStep; }
+
+    // the next stage's copies: one block of 16 rows, one unit of K
     __device__ __forceinline__ void issue()
     {
         if (ahead_ < end_) {
+            const int64_t bytes = F::row_bytes(K_);
+            const int lane = threadIdx.x & 31, row = lane / kLanes;
             if (fresh_) {
-                src_ = items_.rows(item_ahead_);
+                const RowRange r = items_.rows(item_ahead_);
+                const int64_t mine = row * bytes + (lane % kLanes) * 16;
+                pa_ = w_.data + r.a * bytes + mine;
+                pb_ = w_.data + r.b * bytes + mine;
+                n_ = r.n - row;
+                m_ = r.m - row;
+                blocks_ahead_ = blocks(r);
                 fresh_ = false;
             }
-            const int left = min(per_ - u_ahead_, end_ - ahead_);
-            const uint32_t dst = slot_ + stage_ahead_ * kStageBytes;
+            const uint32_t dst = ring_ + stage_ahead_ * kStageBytes + put_;
+            const int64_t k = (int64_t)u_ahead_ * F::kRowPiece;
+            const bool in = k + (lane % kLanes) * 16 < bytes;   // past the row: zeros
+            const int first = r_ahead_ * Items::kStep;
+            const uint8_t *a = pa_ + first * bytes + (in ? k : 0), *b = pb_ + first * bytes + (in ? k : 0);
 #pragma unroll
-            for (int i = 0; i < kGroupUnits; ++i)
-                if (i < left) {
-                    const int k = F::column(u_ahead_ + i, t_);
-                    const bool ok = k < K_;
-                    const int64_t off = ok ? F::offset(k) : 0;
-                    if (src_.r0 != nullptr)
-                        cp_async16(dst + i * 1024, src_.r0 + off, ok);
-                    if (src_.r1 != nullptr)
-                        cp_async16(dst + i * 1024 + 512, src_.r1 + off, ok);
+            for (int i = 0; i < 8 / kAtOnce; ++i) {
+                if (first + i * kAtOnce < n_)
+                    cp_async16(dst + i * kAtOnce * F::kRowPiece, a + i * kAtOnce * bytes, in);
+                if (first + i * kAtOnce < m_)
+                    cp_async16(dst + (8 + i * kAtOnce) * F::kRowPiece, b + i * kAtOnce * bytes, in);
+            }
+            if (++r_ahead_ == blocks_ahead_) {
+                r_ahead_ = 0;
+                ++ahead_;
+                if (++u_ahead_ == per_) {
+                    u_ahead_ = 0;
+                    ++item_ahead_;
+                    fresh_ = true;
                 }
-            const int n = min(left, kGroupUnits);
-            ahead_ += n;
-            u_ahead_ += n;
-            if (u_ahead_ == per_) {
-                u_ahead_ = 0;
-                ++item_ahead_;
-                fresh_ = true;
             }
         }
         cp_async_commit();
@@ -405,42 +459,63 @@ private:
     template <int NT>
     __device__ __forceinline__ void piece(int item, int u0, int u1)
     {
-        Columns<NT, PLANES> x;
-        items_.template columns<NT>(item, x);
-        const RowPtrs rows = items_.rows(item);
-        float acc[NT][4] = {};
-        typename F::Extra e[kGroupUnits];
+        Columns<NT, PLANES> c;
+        items_.template columns<NT>(item, c);
+        const RowRange rows = items_.rows(item);
+        const int nb = blocks(rows);
+        float acc[RB][NT][4] = {};
+        typename F::template Scales<RB> scales;
+        uint4 x[F::kWordsX][NT][PLANES];
+        auto load_x = [&](int w, int u) {
 #pragma unroll
-        for (int i = 0; i < kGroupUnits; ++i)
-            e[i] = F::extra(rows, u0 + i, K_, t_);
-        for (int u = u0; u < u1; u += kGroupUnits) {
-            cp_async_wait<kStages - 1>();
-            const uint32_t src = slot_ + stage_ * kStageBytes;
-            uint4 a[kGroupUnits], b[kGroupUnits];
-            typename F::Extra f[kGroupUnits];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < kGroupUnits; ++i) {
-                a[i] = ld_shared16(src + i * 1024);
-                b[i] = ld_shared16(src + i * 1024 + 512);
-                f[i] = e[i];
-                e[i] = F::extra(rows, u + kGroupUnits + i, K_, t_);
+                for (int p = 0; p < PLANES; ++p)
+                    x[w][nt][p] = F::pair(c.load(nt, p, F::column(u, w, t_), K_));
+        };
+        scales.begin(w_, rows, Items::kStep, K_, g_);
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+            scales.load(r, u0, K_, t_);
+#pragma unroll
+        for (int w = 0; w < F::kWordsX; ++w)
+            load_x(w, u0);
+        for (int u = u0; u < u1; ++u) {
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                if (r < nb) {
+                    cp_async_wait<kStages - 1>();
+                    __syncwarp();   // every lane's copies have arrived
+                    const uint32_t src = ring_ + stage_ * kStageBytes + get_;
+                    uint4 a[F::kPieces], b[F::kPieces];
+#pragma unroll
+                    for (int j = 0; j < F::kPieces; ++j) {
+                        a[j] = ld_shared16(src + ((j ^ (g_ & 1)) << 6));
+                        b[j] = ld_shared16(src + ((j ^ (g_ & 1)) << 6) + 8 * F::kRowPiece);
+                    }
+                    __syncwarp();   // every lane has read the stage
+                    issue();
+                    const bool last = r == nb - 1;
+                    F::template block<RB, NT, PLANES>(a, b, r, scales, x, t_, acc[r], [&](int w) {
+                        if (last)
+                            load_x(w, u + 1);
+                    });
+                    scales.load(r, u + 1, K_, t_);
+                    stage_ = stage_ == kStages - 1 ? 0 : stage_ + 1;
+                }
             }
-            issue();
-#pragma unroll
-            for (int i = 0; i < kGroupUnits; ++i)
-                if (u + i < u1)
-                    F::template unit<NT, PLANES>(a[i], b[i], f[i], u + i, K_, t_, x, acc);
-            stage_ = stage_ == kStages - 1 ? 0 : stage_ + 1;
         }
         items_.template done<NT>(item, u0 == 0, u1 == per_, acc);
     }
 
-    Items &items_;
-    RowPtrs src_;
-    int K_, per_, t_;
-    int begin_, end_, ahead_, item_ahead_, u_ahead_;
-    int stage_ahead_, stage_;
-    uint32_t slot_;
+    const Items &items_;
+    const Weights &w_;
+    int K_, per_, g_, t_;
+    int begin_, end_, ahead_, item_ahead_, u_ahead_, r_ahead_, blocks_ahead_;
+    int stage_ahead_, stage_, put_, get_;
+    uint32_t ring_;
+    const uint8_t *pa_, *pb_;
+    int n_, m_;
     bool fresh_;
 };
 
@@ -448,6 +523,22 @@ private:
 __device__ __forceinline__ int run_begin(int n_items, int per, int w)
 {
     return (int)((int64_t)n_items * per * w / kSkinnyWarps);
+}
+
+// Sum of the pieces of `item` that later warps than its first kept in their
+// side blocks (`sides`, bytes per warp), in ascending order of K, added to v.
+template <int RB>
+__device__ __forceinline__ float add_pieces(float v, const uint8_t *sides, int n_items, int per, int item, int at)
+{
+    // the first warp whose run can begin inside the item
+    for (int w = (int)((int64_t)item * kSkinnyWarps / n_items); w < kSkinnyWarps; ++w) {
+        const int b = run_begin(n_items, per, w);
+        if (b >= (item + 1) * per)
+            break;
+        if (b > item * per && b < run_begin(n_items, per, w + 1))
+            v = __fadd_rn(v, reinterpret_cast<const float *>(sides + w * Room<RB>::kSide)[at]);
+    }
+    return v;
 }
 
 }  // namespace ep

@@ -606,8 +606,8 @@ int ep_router_topk(const void *x, int64_t T, int H, const void *w, int w_dtype, 
  *            e_l = topk_idx[t,k] - rank*E_local, of topk_weights[t,k] * y_k,
  *   y_k = W2[e_l] h_k,   h_k = silu(Wg[e_l] x[t]) * (Wu[e_l] x[t]),
  * where silu(a) = a / (1 + exp(-a)), sums are fp32 and the result is rounded
- * once.  Only the experts that some token names are read, each once for every
- * 32 slots that name it.  With E_local = E (rank 0) it is the whole layer;
+ * once.  Only the experts that some token names are read, their weights once from HBM
+ * for all slots that name them.  With E_local = E (rank 0) it is the whole layer;
  * else the ranks' partials add up to it, like those of ep_batched_combine.
  *   x [T,H] bf16, topk_idx [T,K] int64 (-1 = unrouted), topk_weights [T,K] fp32.
  *   w13: per local expert [2*I, H], the I rows of Wg before the I rows of Wu;
@@ -619,14 +619,14 @@ int ep_router_topk(const void *x, int64_t T, int H, const void *w, int w_dtype, 
  *     as numbers.
  *   T * K <= EP_MOE_MAX_SLOTS and H, I <= 65536 (else EP_ERR_UNSUPPORTED: larger
  *     batches take the dispatch and combine calls).
- *   ws: ep_moe_workspace_size(T, K, I) bytes, 256-byte aligned, scratch.  Calls
+ *   ws: ep_moe_workspace_size(T, K, H, I) bytes, 256-byte aligned, scratch.  Calls
  *     that overlap on the GPU must not share it.
  * The same call on the same inputs gives the same bits.  The sums' order
  * depends on the batch, so a token's last bits may differ between batches.
  * Device errors: EP_ERR_INVALID_EXPERT (an id outside [-1, E): the slot is
  * ignored). */
 #define EP_MOE_MAX_SLOTS 1024
-size_t ep_moe_workspace_size(int64_t T, int K, int I);
+size_t ep_moe_workspace_size(int64_t T, int K, int H, int I);
 int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weights, int64_t T, int K, int H,
                   int I, int E, int E_local, int rank, const ep_matrix *w13, const ep_matrix *w2, void *out,
                   int out_dtype, void *ws, size_t ws_bytes, int32_t *err, ep_stream_t stream);

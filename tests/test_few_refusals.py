@@ -88,7 +88,7 @@ def test_moe(lib):
     assert moe(lib, T=0, x=None) == ep.EP_OK
     assert lib.ep_moe_decode(P, P, P, 2, 2, 64, 64, 8, 4, 1, None, None, P, 0, P, 1 << 20, None, None) \
         == ep.EP_ERR_INVALID_ARG
-    assert ep.ep_moe_workspace_size(4, 2, 64) > 0 and ep.ep_moe_workspace_size(4, 0, 64) == 0
+    assert ep.ep_moe_workspace_size(4, 2, 64, 64) > 0 and ep.ep_moe_workspace_size(4, 0, 64, 64) == 0
     with pytest.raises(ep.EPError, match="EP_ERR_UNSUPPORTED"):
         ep._check(moe(lib, T=513), "moe")
 
