@@ -384,7 +384,7 @@ moe_up_kernel(UpArgs a)
         find(l, a.I, total * (blockIdx.x + 1) / gridDim.x, j1, i1);
     UpItems<G, RB> items(a, l, j0, i0, j1, i1);
     items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
-    items.open = reinterpret_cast<float *>(dynamic + warp * kWarpRing);   // the ring is idle by then
+    items.open = reinterpret_cast<float *>(dynamic + warp * Room<RB>::kWarpRing);   // the ring is idle by then
     const int n = items.count();
     if (n == 0)
         return;

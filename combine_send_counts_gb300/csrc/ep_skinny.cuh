@@ -35,11 +35,11 @@ constexpr int kSkinnyWarps = 8;
 constexpr int kSkinnyThreads = 32 * kSkinnyWarps;
 constexpr int kMaxCols = 16;         // columns of one pass over the weights: 2 blocks of 8
 
-constexpr int kWarpRing = 16 * 1024;   // 128 KB per SM in flight; 45 KB/us times about 1 us are needed
-
-// The shared memory of a block whose warps take up to RB blocks of 16 rows at a time.
+// The shared memory of a block whose warps take RB blocks of 16 rows at a time:
+// 96 or 128 KB are in flight per SM, and 45 KB/us times about 1 us are needed.
 template <int RB>
 struct Room {
+    static constexpr int kWarpRing = (RB == 3 ? 12 : 16) * 1024;
     static constexpr int kRing = kSkinnyWarps * kWarpRing;
     static constexpr int kSide = RB * 16 * kMaxCols * 4;   // one warp's kept sums
     static constexpr int kFixed = kRing + kSkinnyWarps * kSide;
@@ -49,7 +49,7 @@ struct Room {
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -127,16 +127,16 @@ struct FormatBf16 {
     static __device__ __forceinline__ int column(int u, int w, int t) { return u * kUnit + 32 * w + 8 * t; }
     static __device__ __forceinline__ uint4 pair(uint4 v) { return v; }
 
-    template <int RB>
+    template <int RB, int STEP>
     struct Scales {
-        __device__ __forceinline__ void begin(const Weights &, const RowRange &, int, int, int) {}
+        __device__ __forceinline__ void begin(const Weights &, const RowRange &, int, int) {}
         __device__ __forceinline__ void load(int, int, int, int) {}
     };
 
     // acc += block r of the unit; next(w) is called once word w of x is used up
-    template <int RB, int NT, int PLANES, class Next>
+    template <int RB, int STEP, int NT, int PLANES, class Next>
     static __device__ __forceinline__ void block(const uint4 (&a)[kPieces], const uint4 (&b)[kPieces], int,
-                                                 const Scales<RB> &, const uint4 (&x)[kWordsX][NT][PLANES], int,
+                                                 const Scales<RB, STEP> &, uint4 (&x)[kWordsX][NT][PLANES], int,
                                                  float (&acc)[NT][4], Next next)
     {
         float part[NT][4] = {};
@@ -228,44 +228,51 @@ struct FormatW4 {
 
     // a lane's scales and zero points of the unit, for its rows of every block: the scale in the high half,
     // bf16(128 + zero) in the low half
-    template <int RB>
+    template <int RB, int STEP>
     struct Scales {
         uint32_t q[RB][2][2];
         const uint16_t *s0, *s1;
         const uint8_t *z0, *z1;
-        int n, m, step;
-        int64_t per_row;
+        int n, m, per_row;
 
-        __device__ __forceinline__ void begin(const Weights &w, const RowRange &rows, int row_step, int K, int g)
+        __device__ __forceinline__ void begin(const Weights &w, const RowRange &rows, int K, int g)
         {
             per_row = K / G;
-            s0 = w.scale + (rows.a + g) * per_row;
-            s1 = w.scale + (rows.b + g) * per_row;
-            z0 = w.zero != nullptr ? w.zero + (rows.a + g) * per_row : nullptr;
-            z1 = w.zero != nullptr ? w.zero + (rows.b + g) * per_row : nullptr;
+            const int64_t a = (rows.a + g) * per_row, b = (rows.b + g) * per_row;
+            s0 = w.scale + a;
+            s1 = w.scale + b;
+            z0 = w.zero != nullptr ? w.zero + a : nullptr;
+            z1 = w.zero != nullptr ? w.zero + b : nullptr;
             n = rows.n - g;
             m = rows.m - g;
-            step = row_step;
         }
 
         __device__ __forceinline__ void load(int r, int u, int K, int t)
         {
+            const int at = r * STEP * per_row + (u * kUnit + 32 * t) / G;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int k = u * kUnit + 128 * h + 32 * t;
-                const int64_t at = r * step * per_row + k / G;
-                q[r][h][0] = q[r][h][1] = 0x4308u;
-                if (k < K && r * step < n)
-                    q[r][h][0] = ((uint32_t)__ldg(s0 + at) << 16) | 0x4300u | (z0 != nullptr ? (uint32_t)__ldg(z0 + at) : 8u);
-                if (k < K && r * step < m)
-                    q[r][h][1] = ((uint32_t)__ldg(s1 + at) << 16) | 0x4300u | (z1 != nullptr ? (uint32_t)__ldg(z1 + at) : 8u);
+                const bool in = u * kUnit + 128 * h + 32 * t < K;
+                uint32_t v0 = 0, v1 = 0, y0 = 8, y1 = 8;
+                if (in && r * STEP < n) {
+                    v0 = __ldg(s0 + at + h * (128 / G));
+                    if (z0 != nullptr)
+                        y0 = __ldg(z0 + at + h * (128 / G));
+                }
+                if (in && r * STEP < m) {
+                    v1 = __ldg(s1 + at + h * (128 / G));
+                    if (z0 != nullptr)
+                        y1 = __ldg(z1 + at + h * (128 / G));
+                }
+                q[r][h][0] = v0 << 16 | 0x4300u | y0;
+                q[r][h][1] = v1 << 16 | 0x4300u | y1;
             }
         }
     };
 
-    template <int RB, int NT, int PLANES, class Next>
+    template <int RB, int STEP, int NT, int PLANES, class Next>
     static __device__ __forceinline__ void block(const uint4 (&va)[kPieces], const uint4 (&vb)[kPieces], int r,
-                                                 const Scales<RB> &s, const uint4 (&x)[kWordsX][NT][PLANES], int t,
+                                                 const Scales<RB, STEP> &s, uint4 (&x)[kWordsX][NT][PLANES], int t,
                                                  float (&acc)[NT][4], Next next)
     {
 #pragma unroll
@@ -358,13 +365,17 @@ __device__ __forceinline__ void keep(float *side, const float (&acc)[RB][NT][4])
 // columns<NT>(item, x) sets this lane's column pointers, and done<NT>(item,
 // first, last, acc) takes the sums of a piece; first / last say whether the
 // piece holds the item's first and last unit.
+//
+// The ring holds whole units, one stage for each of the RB row blocks; the
+// stages of blocks that an item does not have stay unread.
 template <class F, int RB, int PLANES, class Items>
 class Stream {
 public:
     static constexpr int kStageBytes = 16 * F::kRowPiece;
-    static constexpr int kStages = kWarpRing / kStageBytes;
+    static constexpr int kUnits = Room<RB>::kWarpRing / (RB * kStageBytes);   // units in the ring
     static constexpr int kLanes = F::kRowPiece / 16;   // lanes that copy one row
     static constexpr int kAtOnce = 32 / kLanes;        // rows of one copy instruction
+    static_assert(kUnits >= 1, "the ring holds a unit");
 
     __device__ __forceinline__ Stream(const Items &items, const Weights &w, int K, int n_items, uint32_t ring)
         : items_(items), w_(w), K_(K), per_((K + F::kUnit - 1) / F::kUnit)
@@ -375,26 +386,27 @@ public:
         const int64_t total = (int64_t)n_items * per_;
         begin_ = (int)(total * warp / kSkinnyWarps);
         end_ = (int)(total * (warp + 1) / kSkinnyWarps);
-        ring_ = ring + warp * kWarpRing;
         // a row's 16-byte pieces are swapped in groups of four on odd rows, so that the eight lanes of a
         // quarter warp, which read two rows, meet all 32 banks
         const int row = lane / kLanes, piece = lane % kLanes;
-        put_ = row * F::kRowPiece + (piece ^ ((row & 1) << 2)) * 16;
-        get_ = g_ * F::kRowPiece + t_ * 16;
-        ahead_ = begin_;
+        put_ = ring + warp * Room<RB>::kWarpRing + row * F::kRowPiece + (piece ^ ((row & 1) << 2)) * 16;
+        get_ = ring + warp * Room<RB>::kWarpRing + g_ * F::kRowPiece + t_ * 16;
+        left_ = end_ - begin_;
         item_ahead_ = begin_ / per_;
         u_ahead_ = begin_ - item_ahead_ * per_;
-        r_ahead_ = 0;
-        stage_ahead_ = stage_ = 0;
+        slot_ahead_ = slot_ = 0;
         fresh_ = true;
     }
 
     // the first copies of the run; they read weights only
     __device__ __forceinline__ void start()
     {
+        for (int s = 0; s < kUnits; ++s) {
+            open();
 #pragma unroll
-        for (int s = 0; s < kStages; ++s)
-            issue();
+            for (int r = 0; r < RB; ++r)
+                issue(r);
+        }
     }
 
     __device__ __forceinline__ void run()
@@ -412,48 +424,52 @@ public:
     }
 
 private:
-    static __device__ __forceinline__ int blocks(const RowRange &r) { return (r.n + Items::kStep - 1) / Items::kStep; }
-
-    // the next stage's copies: one block of 16 rows, one unit of K
-    __device__ __forceinline__ void issue()
+    // moves on to the next unit to copy
+    __device__ __forceinline__ void open()
     {
-        if (ahead_ < end_) {
-            const int64_t bytes = F::row_bytes(K_);
-            const int lane = threadIdx.x & 31, row = lane / kLanes;
-            if (fresh_) {
-                const RowRange r = items_.rows(item_ahead_);
-                const int64_t mine = row * bytes + (lane % kLanes) * 16;
-                pa_ = w_.data + r.a * bytes + mine;
-                pb_ = w_.data + r.b * bytes + mine;
-                n_ = r.n - row;
-                m_ = r.m - row;
-                blocks_ahead_ = blocks(r);
-                fresh_ = false;
-            }
-            const uint32_t dst = ring_ + stage_ahead_ * kStageBytes + put_;
-            const int64_t k = (int64_t)u_ahead_ * F::kRowPiece;
-            const bool in = k + (lane % kLanes) * 16 < bytes;   // past the row: zeros
-            const int first = r_ahead_ * Items::kStep;
-            const uint8_t *a = pa_ + first * bytes + (in ? k : 0), *b = pb_ + first * bytes + (in ? k : 0);
+        live_ = left_ > 0;
+        if (!live_)
+            return;
+        --left_;
+        const int row_bytes = (int)F::row_bytes(K_), lane = threadIdx.x & 31;
+        if (fresh_) {
+            const RowRange r = items_.rows(item_ahead_);
+            const int row = lane / kLanes;
+            const int64_t mine = (int64_t)row * row_bytes;
+            pa_ = w_.data + r.a * row_bytes + mine;
+            pb_ = w_.data + r.b * row_bytes + mine;
+            n_ = r.n - row;
+            m_ = r.m - row;
+            fresh_ = false;
+        }
+        off_ = u_ahead_ * F::kRowPiece + (lane % kLanes) * 16;
+        in_ = off_ < row_bytes;   // past the row: zeros
+        off_ = in_ ? off_ : 0;
+        if (++u_ahead_ == per_) {
+            u_ahead_ = 0;
+            ++item_ahead_;
+            fresh_ = true;
+        }
+    }
+
+    // its copies of row block r
+    __device__ __forceinline__ void issue(int r)
+    {
+        if (live_) {
+            const int row_bytes = (int)F::row_bytes(K_);
+            const uint32_t dst = put_ + (slot_ahead_ + r) * kStageBytes;
 #pragma unroll
             for (int i = 0; i < 8 / kAtOnce; ++i) {
-                if (first + i * kAtOnce < n_)
-                    cp_async16(dst + i * kAtOnce * F::kRowPiece, a + i * kAtOnce * bytes, in);
-                if (first + i * kAtOnce < m_)
-                    cp_async16(dst + (8 + i * kAtOnce) * F::kRowPiece, b + i * kAtOnce * bytes, in);
-            }
-            if (++r_ahead_ == blocks_ahead_) {
-                r_ahead_ = 0;
-                ++ahead_;
-                if (++u_ahead_ == per_) {
-                    u_ahead_ = 0;
-                    ++item_ahead_;
-                    fresh_ = true;
-                }
+                const int row = r * Items::kStep + i * kAtOnce, off = off_ + row * row_bytes;
+                if (row < n_)
+                    cp_async16(dst + i * kAtOnce * F::kRowPiece, pa_ + off, in_);
+                if (row < m_)
+                    cp_async16(dst + (8 + i * kAtOnce) * F::kRowPiece, pb_ + off, in_);
             }
         }
         cp_async_commit();
-        stage_ahead_ = stage_ahead_ == kStages - 1 ? 0 : stage_ahead_ + 1;
+        if (r == RB - 1)
+            slot_ahead_ = slot_ahead_ == (kUnits - 1) * RB ? 0 : slot_ahead_ + RB;
     }
 
     template <int NT>
@@ -461,10 +477,8 @@ private:
     {
         Columns<NT, PLANES> c;
         items_.template columns<NT>(item, c);
-        const RowRange rows = items_.rows(item);
-        const int nb = blocks(rows);
         float acc[RB][NT][4] = {};
-        typename F::template Scales<RB> scales;
+        typename F::template Scales<RB, Items::kStep> scales;
         uint4 x[F::kWordsX][NT][PLANES];
         auto load_x = [&](int w, int u) {
 #pragma unroll
@@ -473,7 +487,7 @@ private:
                 for (int p = 0; p < PLANES; ++p)
                     x[w][nt][p] = F::pair(c.load(nt, p, F::column(u, w, t_), K_));
         };
-        scales.begin(w_, rows, Items::kStep, K_, g_);
+        scales.begin(w_, items_.rows(item), K_, g_);
 #pragma unroll
         for (int r = 0; r < RB; ++r)
             scales.load(r, u0, K_, t_);
@@ -481,29 +495,27 @@ private:
         for (int w = 0; w < F::kWordsX; ++w)
             load_x(w, u0);
         for (int u = u0; u < u1; ++u) {
+            open();
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
-                if (r < nb) {
-                    cp_async_wait<kStages - 1>();
-                    __syncwarp();   // every lane's copies have arrived
-                    const uint32_t src = ring_ + stage_ * kStageBytes + get_;
-                    uint4 a[F::kPieces], b[F::kPieces];
+                cp_async_wait<kUnits * RB - 1>();
+                __syncwarp();   // every lane's copies have arrived
+                const uint32_t src = get_ + (slot_ + r) * kStageBytes;
+                uint4 a[F::kPieces], b[F::kPieces];
 #pragma unroll
-                    for (int j = 0; j < F::kPieces; ++j) {
-                        a[j] = ld_shared16(src + ((j ^ (g_ & 1)) << 6));
-                        b[j] = ld_shared16(src + ((j ^ (g_ & 1)) << 6) + 8 * F::kRowPiece);
-                    }
-                    __syncwarp();   // every lane has read the stage
-                    issue();
-                    const bool last = r == nb - 1;
-                    F::template block<RB, NT, PLANES>(a, b, r, scales, x, t_, acc[r], [&](int w) {
-                        if (last)
-                            load_x(w, u + 1);
-                    });
-                    scales.load(r, u + 1, K_, t_);
-                    stage_ = stage_ == kStages - 1 ? 0 : stage_ + 1;
+                for (int j = 0; j < F::kPieces; ++j) {
+                    a[j] = ld_shared16(src + ((j ^ (g_ & 1)) << 6));
+                    b[j] = ld_shared16(src + ((j ^ (g_ & 1)) << 6) + 8 * F::kRowPiece);
                 }
+                __syncwarp();   // every lane has read the stage
+                issue(r);
+                F::template block<RB, Items::kStep, NT, PLANES>(a, b, r, scales, x, t_, acc[r], [&](int w) {
+                    if (r == RB - 1)
+                        load_x(w, u + 1);
+                });
+                scales.load(r, u + 1, K_, t_);
             }
+            slot_ = slot_ == (kUnits - 1) * RB ? 0 : slot_ + RB;
         }
         items_.template done<NT>(item, u0 == 0, u1 == per_, acc);
     }
@@ -511,12 +523,12 @@ private:
     const Items &items_;
     const Weights &w_;
     int K_, per_, g_, t_;
-    int begin_, end_, ahead_, item_ahead_, u_ahead_, r_ahead_, blocks_ahead_;
-    int stage_ahead_, stage_, put_, get_;
-    uint32_t ring_;
+    int begin_, end_, left_, item_ahead_, u_ahead_;
+    int slot_ahead_, slot_, off_;
+    uint32_t put_, get_;
     const uint8_t *pa_, *pb_;
     int n_, m_;
-    bool fresh_;
+    bool fresh_, live_, in_;
 };
 
 // The first unit of warp w's run (see Stream), for whoever adds up the pieces.
