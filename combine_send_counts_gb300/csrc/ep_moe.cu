@@ -22,7 +22,7 @@ bool matrix_ok(const ep_matrix *m)
 
 Weights weights_of(const ep_matrix *m)
 {
-    return Weights{static_cast<const uint8_t *>(m->data), static_cast<const uint16_t *>(m->scale), m->zero};
+    return Weights{static_cast<const uint8_t *>(m->data), static_cast<const uint16_t *>(m->scale), m->zero, kMagic};
 }
 
 }  // namespace

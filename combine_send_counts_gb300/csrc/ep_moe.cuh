@@ -218,7 +218,7 @@ __device__ __forceinline__ void set_columns(const Lists &l, int q, const uint8_t
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int s = first + nt * 8 + g;
-        x.p[nt] = s < end ? rows + (int64_t)(l.slot[s] / slots_per_row) * row_bytes : nullptr;
+        x.set(nt, s < end ? rows + (int64_t)(l.slot[s] / slots_per_row) * row_bytes : nullptr, (int)(row_bytes / 2));
     }
 }
 

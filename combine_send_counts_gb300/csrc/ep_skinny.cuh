@@ -85,17 +85,24 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a)
 
 // The columns of the product, bf16, for this lane: column g of each of NT
 // blocks of 8.  PLANES copies of the columns (a value split into a sum of bf16
-// terms) lie plane_bytes apart.  A null pointer is a column of zeros.
+// terms) lie plane_bytes apart.
 template <int NT, int PLANES>
 struct Columns {
     const uint8_t *p[NT];
     int64_t plane_bytes;
+    int end[NT];          // K, or 0 for a column of zeros
 
-    __device__ __forceinline__ uint4 load(int nt, int plane, int k, int K) const
+    __device__ __forceinline__ void set(int nt, const uint8_t *column, int K)
+    {
+        p[nt] = column;
+        end[nt] = column != nullptr ? K : 0;
+    }
+
+    __device__ __forceinline__ uint4 load(int nt, int plane, int k) const
     {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (p[nt] != nullptr && k < K)
-            v = __ldg(reinterpret_cast<const uint4 *>(p[nt] + plane * plane_bytes + (int64_t)k * 2));
+        if (k < end[nt])
+            v = __ldg(reinterpret_cast<const uint4 *>(p[nt] + plane * plane_bytes + (uint32_t)k * 2));
         return v;
     }
 };
@@ -112,7 +119,11 @@ struct Weights {
     const uint8_t *data;
     const uint16_t *scale;
     const uint8_t *zero;
+    // 0x43004300, the bf16 pair 128, 128.  As an argument it stays in a register and a code pair takes one
+    // and-or; as a constant the compiler spent a second instruction on it (302 -> XXX).
+    uint32_t magic;
 };
+constexpr uint32_t kMagic = 0x43004300u;
 
 // bf16 weights.  A unit is 128 columns; word j of lane (g, t) are columns
 // 32j + 8t .. +7 of its rows, two k16 steps.
@@ -129,8 +140,8 @@ struct FormatBf16 {
 
     template <int RB, int STEP>
     struct Scales {
-        __device__ __forceinline__ void begin(const Weights &, const RowRange &, int, int) {}
-        __device__ __forceinline__ void load(int, int, int, int) {}
+        __device__ __forceinline__ void begin(const Weights &, const RowRange &, int, int, int) {}
+        __device__ __forceinline__ void load(int) {}
     };
 
     // acc += block r of the unit; next(w) is called once word w of x is used up
@@ -221,52 +232,54 @@ struct FormatW4 {
         }
     }
 
-    static __device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t zz)
+    static __device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t magic, uint32_t zz)
     {
-        return sub_bf16x2((w & 0x000f000fu) | 0x43004300u, zz);
+        return sub_bf16x2((w & 0x000f000fu) | magic, zz);
     }
 
-    // a lane's scales and zero points of the unit, for its rows of every block: the scale in the high half,
-    // bf16(128 + zero) in the low half
+    // The scales and zero points of a unit: lane (g, t) keeps those of rows g and g+8 of row block t, the scale in
+    // the high half and bf16(128 + zero) in the low half of a word per group, and hands them out when that
+    // block's turn comes.
     template <int RB, int STEP>
     struct Scales {
-        uint32_t q[RB][2][2];
-        const uint16_t *s0, *s1;
+        static_assert(RB <= 4, "a lane of a row for each block");
+        static constexpr int kGroups = kUnit / G;
+        uint32_t q[2][kGroups];
+        uint32_t magic;
+        const uint16_t *s0, *s1;    // the lane's rows, or null
         const uint8_t *z0, *z1;
-        int n, m, per_row;
+        int groups;                 // of a row
 
-        __device__ __forceinline__ void begin(const Weights &w, const RowRange &rows, int K, int g)
+        __device__ __forceinline__ void begin(const Weights &w, const RowRange &rows, int K, int g, int t)
         {
-            per_row = K / G;
-            const int64_t a = (rows.a + g) * per_row, b = (rows.b + g) * per_row;
-            s0 = w.scale + a;
-            s1 = w.scale + b;
-            z0 = w.zero != nullptr ? w.zero + a : nullptr;
-            z1 = w.zero != nullptr ? w.zero + b : nullptr;
-            n = rows.n - g;
-            m = rows.m - g;
+            groups = K / G;
+            magic = w.magic;
+            const int i = t * STEP + g;
+            const int64_t a = (rows.a + i) * groups, b = (rows.b + i) * groups;
+            const bool mine = t < RB;
+            s0 = mine && i < rows.n ? w.scale + a : nullptr;
+            s1 = mine && i < rows.m ? w.scale + b : nullptr;
+            z0 = s0 != nullptr && w.zero != nullptr ? w.zero + a : nullptr;
+            z1 = s1 != nullptr && w.zero != nullptr ? w.zero + b : nullptr;
         }
 
-        __device__ __forceinline__ void load(int r, int u, int K, int t)
+        __device__ __forceinline__ void load(int u)
         {
-            const int at = r * STEP * per_row + (u * kUnit + 32 * t) / G;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool in = u * kUnit + 128 * h + 32 * t < K;
-                uint32_t v0 = 0, v1 = 0, y0 = 8, y1 = 8;
-                if (in && r * STEP < n) {
-                    v0 = __ldg(s0 + at + h * (128 / G));
-                    if (z0 != nullptr)
-                        y0 = __ldg(z0 + at + h * (128 / G));
-                }
-                if (in && r * STEP < m) {
-                    v1 = __ldg(s1 + at + h * (128 / G));
-                    if (z0 != nullptr)
-                        y1 = __ldg(z1 + at + h * (128 / G));
-                }
-                q[r][h][0] = v0 << 16 | 0x4300u | y0;
-                q[r][h][1] = v1 << 16 | 0x4300u | y1;
+            for (int i = 0; i < kGroups; ++i) {
+                const int at = u * kGroups + i;
+                const bool in = at < groups;
+                const uint32_t v0 = in && s0 != nullptr ? __ldg(s0 + at) : 0, v1 = in && s1 != nullptr ? __ldg(s1 + at) : 0;
+                const uint32_t y0 = in && z0 != nullptr ? __ldg(z0 + at) : 8, y1 = in && z1 != nullptr ? __ldg(z1 + at) : 8;
+                q[0][i] = v0 << 16 | 0x4300u | y0;
+                q[1][i] = v1 << 16 | 0x4300u | y1;
             }
+        }
+
+        // of group i of row block r, for the lane's row g + 8*half
+        __device__ __forceinline__ uint32_t get(int r, int half, int i) const
+        {
+            return __shfl_sync(kFull, q[half][i], (threadIdx.x & 28) | r);
         }
     };
 
@@ -282,21 +295,16 @@ struct FormatW4 {
             arrange(b, t);
 #pragma unroll
             for (int gi = 0; gi < 4 / kWords; ++gi) {
-                uint32_t q0 = s.q[r][h][0], q1 = s.q[r][h][1];
-                if (G < 128) {   // the lane of this row that loaded this group's scale
-                    const int from = (threadIdx.x & 28) | (gi * kWords);
-                    q0 = __shfl_sync(kFull, q0, from);
-                    q1 = __shfl_sync(kFull, q1, from);
-                }
+                const uint32_t q0 = s.get(r, 0, h * (128 / G) + gi), q1 = s.get(r, 1, h * (128 / G) + gi);
                 const uint32_t zz0 = __byte_perm(q0, q0, 0x1010), zz1 = __byte_perm(q1, q1, 0x1010);
                 float part[NT][4] = {};
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
                     const int i = gi * kWords + j, w = 4 * h + i;
-                    const uint32_t a0 = codes(a[i], zz0), a1 = codes(a[i] >> 4, zz0), a2 = codes(a[i] >> 8, zz0),
-                                   a3 = codes(a[i] >> 12, zz0);
-                    const uint32_t b0 = codes(b[i], zz1), b1 = codes(b[i] >> 4, zz1), b2 = codes(b[i] >> 8, zz1),
-                                   b3 = codes(b[i] >> 12, zz1);
+                    const uint32_t a0 = codes(a[i], s.magic, zz0), a1 = codes(a[i] >> 4, s.magic, zz0), a2 = codes(a[i] >> 8, s.magic, zz0),
+                                   a3 = codes(a[i] >> 12, s.magic, zz0);
+                    const uint32_t b0 = codes(b[i], s.magic, zz1), b1 = codes(b[i] >> 4, s.magic, zz1), b2 = codes(b[i] >> 8, s.magic, zz1),
+                                   b3 = codes(b[i] >> 12, s.magic, zz1);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -485,12 +493,10 @@ private:
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int p = 0; p < PLANES; ++p)
-                    x[w][nt][p] = F::pair(c.load(nt, p, F::column(u, w, t_), K_));
+                    x[w][nt][p] = F::pair(c.load(nt, p, F::column(u, w, t_)));
         };
-        scales.begin(w_, items_.rows(item), K_, g_);
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-            scales.load(r, u0, K_, t_);
+        scales.begin(w_, items_.rows(item), K_, g_, t_);
+        scales.load(u0);
 #pragma unroll
         for (int w = 0; w < F::kWordsX; ++w)
             load_x(w, u0);
@@ -513,8 +519,8 @@ private:
                     if (r == RB - 1)
                         load_x(w, u + 1);
                 });
-                scales.load(r, u + 1, K_, t_);
             }
+            scales.load(u + 1);
             slot_ = slot_ == (kUnits - 1) * RB ? 0 : slot_ + RB;
         }
         items_.template done<NT>(item, u0 == 0, u1 == per_, acc);
