@@ -35,6 +35,7 @@
 
 #include "ep_device.cuh"
 #include "ep_internal.h"
+#include "ep_launch.cuh"
 #include "ep_skinny.cuh"
 
 namespace ep {
@@ -539,40 +540,6 @@ moe_down_kernel(DownArgs a)
 // ------------------------------------------------------------ launch policy --
 constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - 64;   // dynamic shared memory of a block that owns an SM
 
-template <class Kernel>
-inline int raise_smem(Kernel kernel, size_t smem, PerDevice &set)
-{
-    const int dev = current_device();
-    if ((int)smem > set.get(dev)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-            cudaGetLastError();
-            return EP_ERR_CUDA;
-        }
-        set.put(dev, (int)smem);
-    }
-    return EP_OK;
-}
-
-template <class Kernel, class Args>
-int launch_dependent(Kernel kernel, unsigned grid, size_t smem, cudaStream_t stream, const Args &a)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
-        cudaGetLastError();
-        return EP_ERR_CUDA;
-    }
-    return launch_status();
-}
-
 template <int G, int RB>
 int launch_up(const UpArgs &a, int64_t elements, cudaStream_t stream)
 {
@@ -582,7 +549,7 @@ int launch_up(const UpArgs &a, int64_t elements, cudaStream_t stream)
     if (rc != EP_OK)
         return rc;
     const unsigned grid = (unsigned)std::min<int64_t>(elements, device_sm_count());
-    return launch_dependent(moe_up_kernel<G, RB>, grid, Room<RB>::kFixed, stream, a);
+    return launch_dependent(moe_up_kernel<G, RB>, grid, kThreads, Room<RB>::kFixed, stream, a);
 }
 
 template <int G, int PLANES, int RB>
@@ -599,7 +566,7 @@ int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
     const int rc = raise_smem(moe_down_kernel<G, PLANES, RB>, smem, set);
     if (rc != EP_OK)
         return rc;
-    return launch_dependent(moe_down_kernel<G, PLANES, RB>, grid, smem, stream, a);
+    return launch_dependent(moe_down_kernel<G, PLANES, RB>, grid, kThreads, smem, stream, a);
 }
 
 // The two kernels.  A warp takes as many blocks of 16 rows at a time as its

@@ -6,98 +6,321 @@
 
 #include "ep_device.cuh"
 #include "ep_internal.h"
+#include "ep_launch.cuh"
+#include "ep_skinny.cuh"
 
 namespace ep {
 namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float bf16_f(const __nv_bfloat16 *p, int64_t i) { return __bfloat162float(p[i]); }
+// ----------------------------------------------------- quantise, read back --
+// Both are bound by HBM (2.5 bytes a weight and the scales); what matters is
+// that the arithmetic between stays under it, about a dozen instructions per
+// weight.  A lane holds 8 consecutive weights; G/8 neighbouring lanes share a
+// group and find its extremes with shuffles of bf16 pairs.  kVectors
+// independent 16-byte loads per lane keep enough in flight.
+constexpr int kVectors = 4;
 
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b)   // NaN if either is
+{
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// 1.5 * 2^23: adding it leaves the nearest integer (ties to even) of a small number in the low mantissa bits.
+constexpr float kRound = 12582912.0f;
+constexpr uint32_t kRoundBits = 0x4b400000u;
+
+// rint(w / s) for bf16 values w and s whose quotient is small, s normal and rs
+// = 1/s to nearest.  The first guess c = rint(w * rs) can differ from the
+// rounded quotient at ties only: w / s, a ratio of two 8-bit significands, is
+// either a tie or at least 2^-11 away from one, and w * rs is off by 2^-20 at
+// most.  The remainder w - c*s is exact (5 + 8 bits), so a tie shows as a
+// remainder of s/2; there an odd c moves to its even neighbour on w's side.
+// Returns the integer added to kRoundBits.
+__device__ __forceinline__ uint32_t round_quotient(float w, float s, float rs)
+{
+    const float t = __fmaf_rn(w, rs, kRound);
+    const float c = __fsub_rn(t, kRound), d = __fmaf_rn(-c, s, w);
+    uint32_t n = __float_as_uint(t);
+    if (__fadd_rn(fabsf(d), fabsf(d)) == s && (n & 1))
+        n += d > 0.0f ? 1 : -1;
+    return n;
+}
+
+template <int G, bool ZERO>
 __global__ void __launch_bounds__(kThreads)
-w4_quantize_kernel(const __nv_bfloat16 *__restrict__ w, int64_t groups, int G, uint8_t *__restrict__ q,
+w4_quantize_kernel(const uint4 *__restrict__ w, int64_t vectors, uint32_t *__restrict__ q,
                    __nv_bfloat16 *__restrict__ scale, uint8_t *__restrict__ zero)
 {
-    const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (g >= groups)
-        return;
-    const __nv_bfloat16 *src = w + g * G;
-    float lo = 0.0f, hi = 0.0f;
-    bool finite = true;
-    for (int i = 0; i < G; ++i) {
-        const float v = bf16_f(src, i);
-        finite = finite && isfinite(v);
-        lo = fminf(lo, v);
-        hi = fmaxf(hi, v);
-    }
-    const bool asym = zero != nullptr;
-    const float wide = asym ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
-    const __nv_bfloat16 sb = finite ? __float2bfloat16_rn(wide) : __float2bfloat16_rn(__int_as_float(0x7f800000));
-    const float s = __bfloat162float(sb);
-    const bool plain = finite && s > 0.0f;
-    const float z = asym ? (plain ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f) : 0.0f) : 8.0f;
-    scale[g] = sb;
-    if (asym)
-        zero[g] = (uint8_t)z;
-    for (int i = 0; i < G; i += 2) {
-        unsigned b = 0;
-        for (int j = 0; j < 2; ++j) {
-            const float r = plain ? rintf(__fdiv_rn(bf16_f(src, i + j), s)) : 0.0f;
-            b |= (unsigned)fminf(fmaxf(__fadd_rn(r, z), 0.0f), 15.0f) << (4 * j);
+    constexpr int kLanes = G / 8;
+    const int64_t first = (int64_t)blockIdx.x * (kThreads * kVectors) + threadIdx.x;
+    grid_dependency_wait();
+    allow_dependents();
+    uint4 v[kVectors];
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i)
+        if (first + i * kThreads < vectors)
+            v[i] = ld_stream(w + first + i * kThreads);
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+        const int64_t at = first + i * kThreads;
+        // a group's lanes are in or out together (K is a multiple of G)
+        const unsigned in = __ballot_sync(kFull, at < vectors);
+        if (at >= vectors)
+            return;
+        const uint32_t p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t lo2 = p[0], hi2 = p[0];
+#pragma unroll
+        for (int j = 1; j < 4; ++j) {
+            lo2 = min_bf16x2(lo2, p[j]);
+            hi2 = max_bf16x2(hi2, p[j]);
         }
-        q[(g * G + i) >> 1] = (uint8_t)b;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) {
+            lo2 = min_bf16x2(lo2, __shfl_xor_sync(in, lo2, o));
+            hi2 = max_bf16x2(hi2, __shfl_xor_sync(in, hi2, o));
+        }
+        lo2 = min_bf16x2(lo2, __byte_perm(lo2, lo2, 0x1032));
+        hi2 = max_bf16x2(hi2, __byte_perm(hi2, hi2, 0x1032));
+        const bool finite = isfinite(bf16_lo(lo2)) && isfinite(bf16_lo(hi2));
+        const float lo = fminf(bf16_lo(lo2), 0.0f), hi = fmaxf(bf16_lo(hi2), 0.0f);
+        const float wide = ZERO ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+        const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? wide : __int_as_float(0x7f800000));
+        const float s = __bfloat162float(sb);
+        const bool plain = finite && s > 0.0f;
+        const float z = ZERO ? (plain ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f) : 0.0f) : 8.0f;
+        if (threadIdx.x % kLanes == 0) {
+            scale[at / kLanes] = sb;
+            if (ZERO)
+                zero[at / kLanes] = (uint8_t)z;
+        }
+        const int zi = (int)z;
+        uint32_t code[8];
+        if (s >= 1.1754944e-38f && finite) {
+            const float rs = __fdiv_rn(1.0f, s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                code[j] = round_quotient(j & 1 ? bf16_hi(p[j >> 1]) : bf16_lo(p[j >> 1]), s, rs) - kRoundBits + zi;
+        } else {   // no scale, or one so small that its reciprocal overflows
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float x = j & 1 ? bf16_hi(p[j >> 1]) : bf16_lo(p[j >> 1]);
+                code[j] = (plain ? (int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -64.0f), 64.0f) : 0) + zi;
+            }
+        }
+        uint32_t out = 0;
+#pragma unroll
+        for (int j = 7; j >= 0; --j)
+            out = out << 4 | (uint32_t)min(max((int)code[j], 0), 15);
+        q[at] = out;
     }
 }
 
-template <bool F32>
+template <int G, bool F32>
 __global__ void __launch_bounds__(kThreads)
-w4_dequantize_kernel(const uint8_t *__restrict__ q, const __nv_bfloat16 *__restrict__ scale,
-                     const uint8_t *__restrict__ zero, int64_t pairs, int G, void *__restrict__ out)
+w4_dequantize_kernel(const uint32_t *__restrict__ q, const __nv_bfloat16 *__restrict__ scale,
+                     const uint8_t *__restrict__ zero, int64_t vectors, void *__restrict__ out)
 {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= pairs)
-        return;
-    const int64_t g = 2 * i / G;
-    const float s = __bfloat162float(scale[g]), z = zero != nullptr ? (float)zero[g] : 8.0f;
-    const unsigned b = q[i];
-    const float v0 = __fmul_rn((float)(b & 15) - z, s), v1 = __fmul_rn((float)(b >> 4) - z, s);
-    if (F32)
-        reinterpret_cast<float2 *>(out)[i] = make_float2(v0, v1);
-    else
-        reinterpret_cast<uint32_t *>(out)[i] = pack_bf16x2(v0, v1);
+    const int64_t first = (int64_t)blockIdx.x * (kThreads * kVectors) + threadIdx.x;
+    grid_dependency_wait();
+    allow_dependents();
+    uint32_t v[kVectors], zz[kVectors];
+    float s[kVectors];
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+        const int64_t at = first + i * kThreads;
+        if (at < vectors) {
+            v[i] = __ldg(q + at);
+            s[i] = __bfloat162float(scale[at / (G / 8)]);
+            zz[i] = (0x4300u | (zero != nullptr ? (uint32_t)zero[at / (G / 8)] : 8u)) * 0x10001u;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+        const int64_t at = first + i * kThreads;
+        if (at >= vectors)
+            return;
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // codes j and j + 4 as bf16 integers, less the zero point: exact
+            const uint32_t c = sub_bf16x2(((v[i] >> (4 * j)) & 0x000f000fu) | kMagic, zz[i]);
+            const float2 p = mul2_rn(make_float2(bf16_lo(c), bf16_hi(c)), make_float2(s[i], s[i]));
+            f[j] = p.x;
+            f[j + 4] = p.y;
+        }
+        if (F32) {
+            float4 *o = static_cast<float4 *>(out) + 2 * at;
+            o[0] = make_float4(f[0], f[1], f[2], f[3]);
+            o[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            st_stream(static_cast<uint4 *>(out) + at, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                                 pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+        }
+    }
 }
 
-// one warp for each (row of w, row of x)
-template <bool F32>
-__global__ void __launch_bounds__(kThreads)
-w4_matvec_kernel(const __nv_bfloat16 *__restrict__ x, const uint8_t *__restrict__ q,
-                 const __nv_bfloat16 *__restrict__ scale, const uint8_t *__restrict__ zero, int64_t M, int64_t N,
-                 int64_t K, int G, void *__restrict__ y)
+template <int G>
+int quantize(const void *w, int64_t vectors, unsigned blocks, uint8_t *q, void *scale, uint8_t *zero, cudaStream_t stream)
 {
-    const int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    const int lane = threadIdx.x & 31;
-    if (u >= M * N)
-        return;
-    const int64_t n = u % N, m = u / N;
-    const int64_t ng = K / G;
-    float acc = 0.0f;
-    for (int64_t g = 0; g < ng; ++g) {
-        const float z = zero != nullptr ? (float)zero[n * ng + g] : 8.0f;
-        float part = 0.0f;
-        for (int64_t k = g * G + lane; k < (g + 1) * G; k += 32) {
-            const unsigned b = q[(n * K + k) >> 1];
-            part = __fmaf_rn(bf16_f(x, m * K + k), (float)((b >> (4 * (k & 1))) & 15) - z, part);
+    const auto *src = static_cast<const uint4 *>(w);
+    auto *dst = reinterpret_cast<uint32_t *>(q);
+    auto *s = static_cast<__nv_bfloat16 *>(scale);
+    if (zero != nullptr)
+        return launch_dependent(w4_quantize_kernel<G, true>, blocks, kThreads, 0, stream, src, vectors, dst, s, zero);
+    return launch_dependent(w4_quantize_kernel<G, false>, blocks, kThreads, 0, stream, src, vectors, dst, s, zero);
+}
+
+template <int G>
+int dequantize(const uint8_t *q, const void *scale, const uint8_t *zero, int64_t vectors, unsigned blocks, void *w,
+               int out_dtype, cudaStream_t stream)
+{
+    const auto *src = reinterpret_cast<const uint32_t *>(q);
+    const auto *s = static_cast<const __nv_bfloat16 *>(scale);
+    if (out_dtype == 1)
+        return launch_dependent(w4_dequantize_kernel<G, true>, blocks, kThreads, 0, stream, src, s, zero, vectors, w);
+    return launch_dependent(w4_dequantize_kernel<G, false>, blocks, kThreads, 0, stream, src, s, zero, vectors, w);
+}
+
+// ------------------------------------------------------------------ product --
+// y[m,n]: each block owns an equal share of the rows of w, in groups of up to
+// 16*RB, which its warps share evenly (ep_skinny.cuh); the passes over a group
+// of rows (16 rows of x each, up to four of them in one block) follow one
+// another, so that all but the first find the codes in L2.
+struct MatvecArgs {
+    const uint8_t *x;
+    int M, N, K;
+    Weights w;
+    void *y;
+    int out_f32;
+};
+
+constexpr int kMaxPasses = 4;
+
+template <int G, int RB>
+struct MatvecItems {
+    using F = FormatW4<G, false>;
+    static constexpr int kStep = 16;
+    const MatvecArgs &a;
+    int row0, row1, m0, passes;
+    float *side, *open;    // this warp's kept pieces: of an item begun by another, and of one it began
+
+    __device__ __forceinline__ int row(int item) const { return row0 + item / passes * (16 * RB); }
+    __device__ __forceinline__ int col(int item) const { return m0 + item % passes * kMaxCols; }
+
+    __device__ __forceinline__ RowRange rows(int item) const
+    {
+        const int r = row(item), n = min(row1 - r, 16 * RB);
+        return RowRange{r, r + 8, n, n - 8};
+    }
+
+    __device__ __forceinline__ int cols(int item) const { return min(a.M - col(item), kMaxCols); }
+
+    template <int NT>
+    __device__ __forceinline__ void columns(int item, Columns<NT, 1> &x) const
+    {
+        x.plane_bytes = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int m = col(item) + nt * 8 + ((threadIdx.x & 31) >> 2);
+            x.set(nt, m < a.M ? a.x + (int64_t)m * a.K * 2 : nullptr, a.K);
         }
-        acc = __fmaf_rn(part, bf16_f(scale, n * ng + g), acc);
     }
-    for (int o = 16; o > 0; o >>= 1)
-        acc = __fadd_rn(acc, __shfl_xor_sync(kFull, acc, o));
-    if (lane == 0) {
-        if (F32)
-            static_cast<float *>(y)[m * N + n] = acc;
-        else
-            static_cast<__nv_bfloat16 *>(y)[m * N + n] = __float2bfloat16_rn(acc);
+
+    __device__ __forceinline__ void store(int m, int n, float v) const
+    {
+        if (m < a.M && n < row1) {
+            if (a.out_f32)
+                static_cast<float *>(a.y)[(int64_t)m * a.N + n] = v;
+            else
+                static_cast<__nv_bfloat16 *>(a.y)[(int64_t)m * a.N + n] = __float2bfloat16_rn(v);
+        }
     }
+
+    template <int NT>
+    __device__ __forceinline__ void done(int item, bool first, bool last, const float (&acc)[RB][NT][4]) const
+    {
+        if (!first || !last) {
+            keep<RB, NT>(first ? open : side, acc);
+            return;
+        }
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int n = row(item) + g, m = col(item) + 2 * t;
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    store(m + nt * 8 + (c & 1), n + r * 16 + (c >> 1) * 8, acc[r][nt][c]);
+    }
+};
+
+template <int G, int RB>
+__global__ void __launch_bounds__(kSkinnyThreads, 1)
+w4_matvec_kernel(MatvecArgs a)
+{
+    extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
+    using F = FormatW4<G, false>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *sides = dynamic + Room<RB>::kRing;
+    MatvecItems<G, RB> items{a};
+    items.row0 = (int)((int64_t)a.N * blockIdx.x / gridDim.x);
+    items.row1 = (int)((int64_t)a.N * (blockIdx.x + 1) / gridDim.x);
+    items.m0 = blockIdx.y * (kMaxPasses * kMaxCols);
+    items.passes = min((a.M - items.m0 + kMaxCols - 1) / kMaxCols, kMaxPasses);
+    items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
+    items.open = reinterpret_cast<float *>(dynamic + warp * Room<RB>::kWarpRing);   // the ring is idle by then
+    const int n = (items.row1 - items.row0 + 16 * RB - 1) / (16 * RB) * items.passes;
+    const int per = (a.K + F::kUnit - 1) / F::kUnit;
+    Stream<F, RB, 1, MatvecItems<G, RB>> stream(items, a.w, a.K, n, smem_u32(dynamic));
+    grid_dependency_wait();
+    allow_dependents();
+    stream.start();
+    stream.run();
+    __syncthreads();
+    // the warp that began an item which others went on with adds up its pieces
+    const int begin = run_begin(n, per, warp), end = run_begin(n, per, warp + 1);
+    const int item = (end - 1) / per;
+    if (begin == end || end % per == 0 || item * per < begin)
+        return;
+    const int cols = items.cols(item), nb = cols <= 8 ? 1 : 2;
+    for (int v = lane; v < 16 * RB * cols; v += 32) {
+        const int r = v % (16 * RB), c = v / (16 * RB), at = side_index(r >> 4, r & 15, nb, c);
+        items.store(items.col(item) + c, items.row(item) + r,
+                    add_pieces<RB>(items.open[at], sides, n, per, item, at));
+    }
+}
+
+template <int G, int RB>
+int launch_matvec(const MatvecArgs &a, dim3 grid, cudaStream_t stream)
+{
+    static PerDevice set;
+    const int rc = raise_smem(w4_matvec_kernel<G, RB>, Room<RB>::kFixed, set);
+    if (rc != EP_OK)
+        return rc;
+    return launch_dependent(w4_matvec_kernel<G, RB>, grid, kSkinnyThreads, Room<RB>::kFixed, stream, a);
+}
+
+template <int G>
+int matvec(const MatvecArgs &a, cudaStream_t stream)
+{
+    const int sms = std::min(device_sm_count(), a.N);
+    const dim3 grid(sms, (unsigned)ceil_div(a.M, kMaxPasses * kMaxCols));
+    // a warp takes as many blocks of 16 rows at a time as its block has rows for: each x it loads serves them all
+    const int64_t rows = ceil_div(a.N, sms);
+    if (rows > 32)
+        return launch_matvec<G, 4>(a, grid, stream);
+    return rows > 16 ? launch_matvec<G, 2>(a, grid, stream) : launch_matvec<G, 1>(a, grid, stream);
 }
 
 bool w4_shape_ok(int64_t N, int64_t K, int group)
@@ -121,12 +344,14 @@ extern "C" int ep_w4_quantize(const void *w, int64_t N, int64_t K, int group, ui
         return EP_OK;
     if (w == nullptr || q == nullptr || scale == nullptr || !aligned(w, 16) || !aligned(q, 16) || !aligned(scale, 2))
         return EP_ERR_INVALID_ARG;
-    const int64_t groups = N * (K / group), blocks = ceil_div(groups, kThreads);
+    const int64_t vectors = N * (K / 8), blocks = ceil_div(vectors, kThreads * kVectors);
     if (blocks >= ((int64_t)1 << 31))
         return EP_ERR_UNSUPPORTED;
-    w4_quantize_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(static_cast<const __nv_bfloat16 *>(w), groups, group,
-                                                                 q, static_cast<__nv_bfloat16 *>(scale), zero);
-    return launch_status();
+    switch (group) {
+    case 32: return quantize<32>(w, vectors, (unsigned)blocks, q, scale, zero, stream);
+    case 64: return quantize<64>(w, vectors, (unsigned)blocks, q, scale, zero, stream);
+    default: return quantize<128>(w, vectors, (unsigned)blocks, q, scale, zero, stream);
+    }
 }
 
 extern "C" int ep_w4_dequantize(const uint8_t *q, const void *scale, const uint8_t *zero, int64_t N, int64_t K,
@@ -141,15 +366,14 @@ extern "C" int ep_w4_dequantize(const uint8_t *q, const void *scale, const uint8
         return EP_OK;
     if (w == nullptr || q == nullptr || scale == nullptr || !aligned(w, 16) || !aligned(q, 16) || !aligned(scale, 2))
         return EP_ERR_INVALID_ARG;
-    const int64_t pairs = N * K / 2, blocks = ceil_div(pairs, kThreads);
+    const int64_t vectors = N * (K / 8), blocks = ceil_div(vectors, kThreads * kVectors);
     if (blocks >= ((int64_t)1 << 31))
         return EP_ERR_UNSUPPORTED;
-    const auto *s = static_cast<const __nv_bfloat16 *>(scale);
-    if (out_dtype == 1)
-        w4_dequantize_kernel<true><<<(unsigned)blocks, kThreads, 0, stream>>>(q, s, zero, pairs, group, w);
-    else
-        w4_dequantize_kernel<false><<<(unsigned)blocks, kThreads, 0, stream>>>(q, s, zero, pairs, group, w);
-    return launch_status();
+    switch (group) {
+    case 32: return dequantize<32>(q, scale, zero, vectors, (unsigned)blocks, w, out_dtype, stream);
+    case 64: return dequantize<64>(q, scale, zero, vectors, (unsigned)blocks, w, out_dtype, stream);
+    default: return dequantize<128>(q, scale, zero, vectors, (unsigned)blocks, w, out_dtype, stream);
+    }
 }
 
 extern "C" int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const void *scale, const uint8_t *zero,
@@ -165,14 +389,15 @@ extern "C" int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const vo
     if (x == nullptr || q == nullptr || scale == nullptr || y == nullptr || !aligned(x, 16) || !aligned(q, 16) ||
         !aligned(scale, 2) || !aligned(y, 16))
         return EP_ERR_INVALID_ARG;
-    const int64_t blocks = ceil_div(M * N, kThreads / 32);
-    if (M >= ((int64_t)1 << 20) || N >= ((int64_t)1 << 31) || blocks >= ((int64_t)1 << 31))
+    // a block's units of work are counted in 32 bits
+    const int64_t units = ceil_div(N, (int64_t)16 * device_sm_count()) * kMaxPasses * ceil_div(K, 256);
+    if (M >= ((int64_t)1 << 20) || N >= ((int64_t)1 << 31) || K >= ((int64_t)1 << 25) || units >= ((int64_t)1 << 30))
         return EP_ERR_UNSUPPORTED;
-    const auto *xb = static_cast<const __nv_bfloat16 *>(x);
-    const auto *s = static_cast<const __nv_bfloat16 *>(scale);
-    if (out_dtype == 1)
-        w4_matvec_kernel<true><<<(unsigned)blocks, kThreads, 0, stream>>>(xb, q, s, zero, M, N, K, group, y);
-    else
-        w4_matvec_kernel<false><<<(unsigned)blocks, kThreads, 0, stream>>>(xb, q, s, zero, M, N, K, group, y);
-    return launch_status();
+    const MatvecArgs a{static_cast<const uint8_t *>(x), (int)M, (int)N, (int)K,
+                       Weights{q, static_cast<const uint16_t *>(scale), zero, kMagic}, y, out_dtype};
+    switch (group) {
+    case 32: return matvec<32>(a, stream);
+    case 64: return matvec<64>(a, stream);
+    default: return matvec<128>(a, stream);
+    }
 }

@@ -567,8 +567,9 @@ int ep_w4_dequantize(const uint8_t *q, const void *scale, const uint8_t *zero, i
 /* y[m,n] = sum over k of x[m,k] * w[n,k] for a 4-bit matrix w [N,K]:
  *   x [M,K] bf16, y [M,N] bf16 (out_dtype 0) or fp32 (out_dtype 1).
  * Sums are fp32: a group's codes are summed first, then scaled, and rounded
- * once at the end.  Any M >= 0; the weights are read once for each 32 rows of
- * x, so it is meant for a few rows.  The same call on the same inputs gives
+ * once at the end.  The weights are read once for each 64 rows of x, so it is
+ * meant for a few rows (M < 2^20, N < 2^31, K < 2^25).
+ * The same call on the same inputs gives
  * the same bits. */
 int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const void *scale, const uint8_t *zero, int64_t N,
                  int64_t K, int group, void *y, int out_dtype, ep_stream_t stream);
