@@ -82,9 +82,64 @@ struct Lists {
     uint16_t big_expert[kMaxSlots / kMaxCols];   // experts of more than one entry
 };
 
+// build_lists for up to 32 slots, by the first warp: one slot to a lane.  The
+// experts come in the order of their first slots.
+__device__ __forceinline__ void build_few(const Routing &r, Lists &l, int32_t *err)
+{
+    if (threadIdx.x < 32) {
+        const int s = threadIdx.x;
+        const int e = s < r.n ? r.local(s, err) : -1;
+        const unsigned lt = lanemask_lt(), peers = __match_any_sync(kFull, e), before = peers & lt;
+        const int c = __popc(peers);
+        const unsigned leaders = __ballot_sync(kFull, e >= 0 && before == 0);
+        const unsigned twice = __ballot_sync(kFull, e >= 0 && before == 0 && c > kMaxCols);   // 32 slots are two passes at most
+        const int leader = __ffs(peers) - 1;
+        const unsigned earlier = e >= 0 ? (1u << leader) - 1 : 0;   // lanes below this expert's first
+        const int j = __popc(leaders & earlier), q = j + __popc(twice & earlier);
+        int at = 0;   // slots of the experts before
+        for (unsigned m = leaders; m != 0; m &= m - 1) {
+            const int o = __ffs(m) - 1, n = __shfl_sync(kFull, c, o);
+            if (earlier >> o & 1)
+                at += n;
+        }
+        const int place = __popc(before);
+        if (s < r.n) {
+            l.use[s] = e >= 0 ? (int16_t)(q + place / kMaxCols) : (int16_t)-1;
+            l.place[s] = (uint16_t)place;
+        }
+        if (e >= 0) {
+            l.slot[at + place] = (uint16_t)s;
+            if (before == 0) {
+                l.id[j] = (uint16_t)e;
+                l.entry[j] = (uint16_t)q;
+                l.cost[j] = j + q;
+                for (int p = 0; p < passes_of(c); ++p) {
+                    l.owner[q + p] = (uint16_t)j;
+                    l.begin[q + p] = (uint16_t)(at + p * kMaxCols);
+                }
+            }
+        }
+        if (s == 0) {
+            const int experts = __popc(leaders), entries = experts + __popc(twice);
+            l.experts = experts;
+            l.entries = entries;
+            l.entry[experts] = (uint16_t)entries;
+            l.cost[experts] = experts + entries;
+        }
+        const int slots = __popc(__ballot_sync(kFull, e >= 0));
+        if (s == 0)
+            l.begin[__popc(leaders) + __popc(twice)] = (uint16_t)slots;
+    }
+    __syncthreads();
+}
+
 // All threads of the block; count: E_local ints of shared memory.
 __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *count, int32_t *err)
 {
+    if (r.n <= 32) {
+        build_few(r, l, err);
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < r.E_local; e += kThreads)
         count[e] = 0;
@@ -349,19 +404,22 @@ struct UpItems {
     }
 };
 
-// the expert and element at position pos of the costs laid end to end
-__device__ __forceinline__ void find(const Lists &l, int I, int64_t pos, int &j, int &i)
+// The expert and element where block b's share of the costs laid end to end
+// begins.  (At most 2 * kMaxSlots * kMaxDim = 2^27 in all.)
+__device__ __forceinline__ void share_begin(const Lists &l, int I, int b, int blocks, int &j, int &i)
 {
+    const int total = l.cost[l.experts] * I;
+    const int pos = total / blocks * b + min(b, total % blocks);
     int lo = 0, hi = l.experts;   // cost[lo] * I <= pos < cost[hi] * I
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((int64_t)l.cost[mid] * I <= pos)
+        if (l.cost[mid] * I <= pos)
             lo = mid;
         else
             hi = mid;
     }
     j = lo;
-    i = (int)((pos - (int64_t)l.cost[lo] * I) / (l.cost[lo + 1] - l.cost[lo]));
+    i = (pos - l.cost[lo] * I) / (l.cost[lo + 1] - l.cost[lo]);
 }
 
 template <int G, int RB>
@@ -370,19 +428,19 @@ moe_up_kernel(UpArgs a)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
     __shared__ Lists l;
+    __shared__ Splits splits;
     using F = typename FormatOf<G, false>::F;
     grid_dependency_wait();
     allow_dependents();
     build_lists(a.r, l, reinterpret_cast<int *>(dynamic), blockIdx.x == 0 ? a.err : nullptr);
     if (l.experts == 0)
         return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     uint8_t *sides = dynamic + Room<RB>::kRing;
-    const int64_t total = (int64_t)l.cost[l.experts] * a.I;
     int j0, i0, j1 = l.experts, i1 = 0;
-    find(l, a.I, total * blockIdx.x / gridDim.x, j0, i0);
+    share_begin(l, a.I, blockIdx.x, gridDim.x, j0, i0);
     if (blockIdx.x + 1 < gridDim.x)
-        find(l, a.I, total * (blockIdx.x + 1) / gridDim.x, j1, i1);
+        share_begin(l, a.I, blockIdx.x + 1, gridDim.x, j1, i1);
     UpItems<G, RB> items(a, l, j0, i0, j1, i1);
     items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
     items.open = reinterpret_cast<float *>(dynamic + warp * Room<RB>::kWarpRing);   // the ring is idle by then
@@ -392,24 +450,20 @@ moe_up_kernel(UpArgs a)
     Stream<F, RB, 1, UpItems<G, RB>> stream(items, a.w, a.H, n, smem_u32(dynamic));
     stream.start();
     stream.run();
-    __syncthreads();
-    // the warp that began an item which others went on with adds up its pieces
-    const int per = (a.H + F::kUnit - 1) / F::kUnit;
-    const int begin = run_begin(n, per, warp), end = run_begin(n, per, warp + 1);
-    const int item = (end - 1) / per;
-    if (begin == end || end % per == 0 || item * per < begin)
-        return;
-    int q, j, i, stop;
-    items.where(item, q, j, i, stop);
-    const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
-    for (int v = lane; v < 8 * RB * cols; v += 32) {
-        const int e = v % (8 * RB), c = v / (8 * RB);
-        if (i + e >= stop)
+    find_splits(splits, n, (a.H + F::kUnit - 1) / F::kUnit);
+    for (int w = 0; w < kWarps; ++w) {
+        if (splits.item[w] < 0)
             continue;
-        const int ga = side_index(e >> 3, e & 7, nb, c), ua = side_index(e >> 3, (e & 7) + 8, nb, c);
-        const float gate = add_pieces<RB>(items.open[ga], sides, n, per, item, ga);
-        const float up = add_pieces<RB>(items.open[ua], sides, n, per, item, ua);
-        store_planes<(G > 0)>(a.out, l.slot[first + c], i + e, activate(gate, up));
+        int q, j, i, stop;
+        items.where(splits.item[w], q, j, i, stop);
+        const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
+        for (int v = threadIdx.x; v < 8 * RB * cols; v += kThreads) {
+            const int e = v % (8 * RB), c = v / (8 * RB);
+            if (i + e < stop)
+                store_planes<(G > 0)>(a.out, l.slot[first + c], i + e,
+                                      activate(add_pieces<RB>(splits, dynamic, w, side_index(e >> 3, e & 7, nb, c)),
+                                               add_pieces<RB>(splits, dynamic, w, side_index(e >> 3, (e & 7) + 8, nb, c))));
+        }
     }
 }
 
@@ -435,7 +489,7 @@ struct DownItems {
     int row0, row1;
     float *y;              // [n], `stride` floats apart: the block's rows of each slot
     int stride;
-    float *side;
+    float *side, *open;    // this warp's kept pieces: of an item begun by another, and of one it began
 
     __device__ __forceinline__ RowRange rows(int item) const
     {
@@ -459,10 +513,10 @@ struct DownItems {
     }
 
     template <int NT>
-    __device__ __forceinline__ void done(int item, bool first, bool, const float (&acc)[RB][NT][4]) const
+    __device__ __forceinline__ void done(int item, bool first, bool last, const float (&acc)[RB][NT][4]) const
     {
-        if (!first) {
-            keep<RB, NT>(side, acc);
+        if (!first || !last) {
+            keep<RB, NT>(first ? open : side, acc);
             return;
         }
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -493,6 +547,7 @@ moe_down_kernel(DownArgs a)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, one side block per warp, y if it fits
     __shared__ Lists l;
+    __shared__ Splits splits;
     using F = typename FormatOf<G, (G > 0)>::F;
     // topk_idx was complete before the up kernel began; h is complete after the wait
     build_lists(a.r, l, reinterpret_cast<int *>(dynamic), nullptr);
@@ -505,29 +560,34 @@ moe_down_kernel(DownArgs a)
     items.y = a.y != nullptr ? a.y + items.row0 : reinterpret_cast<float *>(dynamic + Room<RB>::kFixed);
     items.stride = a.y != nullptr ? a.H : rows | 1;
     items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
+    items.open = reinterpret_cast<float *>(dynamic + warp * Room<RB>::kWarpRing);
     const int n = (rows + 16 * RB - 1) / (16 * RB) * l.entries;
-    const int per = (a.I + F::kUnit - 1) / F::kUnit, K = a.r.K;
     Stream<F, RB, PLANES, DownItems<G, PLANES, RB>> stream(items, a.w, a.I, n, smem_u32(dynamic));
     stream.start();
     grid_dependency_wait();
     allow_dependents();
     stream.run();
+    find_splits(splits, n, (a.I + F::kUnit - 1) / F::kUnit);
+    for (int w = 0; w < kWarps; ++w) {
+        if (splits.item[w] < 0)
+            continue;
+        const int b = splits.item[w] / l.entries, q = splits.item[w] - b * l.entries;
+        const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
+        for (int v = threadIdx.x; v < 16 * RB * cols; v += kThreads) {
+            const int r = v % (16 * RB), c = v / (16 * RB), i = b * (16 * RB) + r;
+            if (i < rows)
+                items.y[(int64_t)l.slot[first + c] * items.stride + i] =
+                    add_pieces<RB>(splits, dynamic, w, side_index(r >> 4, r & 15, nb, c));
+        }
+    }
     __syncthreads();
-    // weighted sums over k; a slot's divided items are added in the order of their columns
     for (int v = threadIdx.x; v < a.T * rows; v += kThreads) {
         const int tok = v / rows, i = v - tok * rows;
-        const int b = i / (16 * RB), ib = i - b * (16 * RB);
         float sum = 0.0f;
-        for (int k = 0; k < K; ++k) {
-            const int slot = tok * K + k;
-            const int q = l.use[slot];
-            if (q < 0)
-                continue;
-            const int nb = l.begin[q + 1] - l.begin[q] <= 8 ? 1 : 2;
-            const int at = side_index(ib >> 4, ib & 15, nb, l.place[slot] % kMaxCols);
-            const float p = add_pieces<RB>(items.y[(int64_t)slot * items.stride + i], sides, n, per,
-                                           b * l.entries + q, at);
-            sum = __fmaf_rn(a.weights[slot], p, sum);
+        for (int k = 0; k < a.r.K; ++k) {
+            const int slot = tok * a.r.K + k;
+            if (l.use[slot] >= 0)
+                sum = __fmaf_rn(a.weights[slot], items.y[(int64_t)slot * items.stride + i], sum);
         }
         const int64_t o = (int64_t)tok * a.H + items.row0 + i;
         if (a.out_f32)
@@ -538,7 +598,7 @@ moe_down_kernel(DownArgs a)
 }
 
 // ------------------------------------------------------------ launch policy --
-constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - 64;   // dynamic shared memory of a block that owns an SM
+constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - sizeof(Splits) - 64;   // dynamic shared memory of a block that owns an SM
 
 template <int G, int RB>
 int launch_up(const UpArgs &a, int64_t elements, cudaStream_t stream)

@@ -150,7 +150,7 @@ struct FormatBf16 {
                                                  const Scales<RB, STEP> &, uint4 (&x)[kWordsX][NT][PLANES], int,
                                                  float (&acc)[NT][4], Next next)
     {
-        float part[NT][4] = {};
+        float part[2][NT][4] = {};   // two chains, so that a matrix step need not wait for the one before
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -158,8 +158,8 @@ struct FormatBf16 {
 #pragma unroll
                 for (int p = 0; p < PLANES; ++p) {
                     const uint4 v = x[j][nt][p];
-                    mma_bf16(part[nt], a[j].x, b[j].x, a[j].y, b[j].y, v.x, v.y);
-                    mma_bf16(part[nt], a[j].z, b[j].z, a[j].w, b[j].w, v.z, v.w);
+                    mma_bf16(part[0][nt], a[j].x, b[j].x, a[j].y, b[j].y, v.x, v.y);
+                    mma_bf16(part[1][nt], a[j].z, b[j].z, a[j].w, b[j].w, v.z, v.w);
                 }
             next(j);
         }
@@ -167,7 +167,7 @@ struct FormatBf16 {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                acc[nt][i] = __fadd_rn(acc[nt][i], part[nt][i]);
+                acc[nt][i] = __fadd_rn(acc[nt][i], __fadd_rn(part[0][nt][i], part[1][nt][i]));
     }
 };
 
@@ -297,7 +297,7 @@ struct FormatW4 {
             for (int gi = 0; gi < 4 / kWords; ++gi) {
                 const uint32_t q0 = s.get(r, 0, h * (128 / G) + gi), q1 = s.get(r, 1, h * (128 / G) + gi);
                 const uint32_t zz0 = __byte_perm(q0, q0, 0x1010), zz1 = __byte_perm(q1, q1, 0x1010);
-                float part[NT][4] = {};
+                float part[2][NT][4] = {};   // two chains, so that a matrix step need not wait for the one before
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
                     const int i = gi * kWords + j, w = 4 * h + i;
@@ -310,18 +310,18 @@ struct FormatW4 {
 #pragma unroll
                         for (int p = 0; p < PLANES; ++p) {
                             const uint4 v = x[w][nt][p];
-                            mma_bf16(part[nt], a0, b0, a1, b1, v.x, v.y);
-                            mma_bf16(part[nt], a2, b2, a3, b3, v.z, v.w);
+                            mma_bf16(part[0][nt], a0, b0, a1, b1, v.x, v.y);
+                            mma_bf16(part[1][nt], a2, b2, a3, b3, v.z, v.w);
                         }
                     next(w);
                 }
                 const float f0 = __uint_as_float(q0 & 0xffff0000u), f1 = __uint_as_float(q1 & 0xffff0000u);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    acc[nt][0] = __fmaf_rn(part[nt][0], f0, acc[nt][0]);
-                    acc[nt][1] = __fmaf_rn(part[nt][1], f0, acc[nt][1]);
-                    acc[nt][2] = __fmaf_rn(part[nt][2], f1, acc[nt][2]);
-                    acc[nt][3] = __fmaf_rn(part[nt][3], f1, acc[nt][3]);
+                    acc[nt][0] = __fmaf_rn(__fadd_rn(part[0][nt][0], part[1][nt][0]), f0, acc[nt][0]);
+                    acc[nt][1] = __fmaf_rn(__fadd_rn(part[0][nt][1], part[1][nt][1]), f0, acc[nt][1]);
+                    acc[nt][2] = __fmaf_rn(__fadd_rn(part[0][nt][2], part[1][nt][2]), f1, acc[nt][2]);
+                    acc[nt][3] = __fmaf_rn(__fadd_rn(part[0][nt][3], part[1][nt][3]), f1, acc[nt][3]);
                 }
             }
         }
@@ -543,19 +543,47 @@ __device__ __forceinline__ int run_begin(int n_items, int per, int w)
     return (int)((int64_t)n_items * per * w / kSkinnyWarps);
 }
 
-// Sum of the pieces of `item` that later warps than its first kept in their
-// side blocks (`sides`, bytes per warp), in ascending order of K, added to v.
-template <int RB>
-__device__ __forceinline__ float add_pieces(float v, const uint8_t *sides, int n_items, int per, int item, int at)
+// The items of a block that are divided among warps: item[w] is the one that
+// warp w began and did not finish (-1: none); it kept its piece at the start of
+// its ring, which is idle by then, and warps w+1 .. end[w]-1 kept theirs in
+// their side blocks (those with work).
+struct Splits {
+    int item[kSkinnyWarps], end[kSkinnyWarps];
+    unsigned busy;      // bit w: warp w had work
+};
+
+// All threads, after their run; holds a barrier, after which the kept pieces
+// may be read.
+__device__ __forceinline__ void find_splits(Splits &s, int n_items, int per)
 {
-    // the first warp whose run can begin inside the item
-    for (int w = (int)((int64_t)item * kSkinnyWarps / n_items); w < kSkinnyWarps; ++w) {
-        const int b = run_begin(n_items, per, w);
-        if (b >= (item + 1) * per)
-            break;
-        if (b > item * per && b < run_begin(n_items, per, w + 1))
-            v = __fadd_rn(v, reinterpret_cast<const float *>(sides + w * Room<RB>::kSide)[at]);
+    const int w = threadIdx.x;
+    if (w < 32) {
+        const int begin = run_begin(n_items, per, min(w, kSkinnyWarps)), end = run_begin(n_items, per, min(w + 1, kSkinnyWarps));
+        const unsigned busy = __ballot_sync(kFull, begin < end);
+        if (w < kSkinnyWarps) {
+            const int item = end > 0 ? (end - 1) / per : 0;
+            const bool open = begin < end && item * per >= begin && (item + 1) * per > end;
+            int last = w + 1;
+            while (open && last < kSkinnyWarps && run_begin(n_items, per, last) < (item + 1) * per)
+                ++last;
+            s.item[w] = open ? item : -1;
+            s.end[w] = last;
+        }
+        if (w == 0)
+            s.busy = busy;
     }
+    __syncthreads();
+}
+
+// The sum at place `at` of the item that warp w began: its pieces in the order
+// of K.  `dynamic`: the ring, then the side blocks.
+template <int RB>
+__device__ __forceinline__ float add_pieces(const Splits &s, const uint8_t *dynamic, int w, int at)
+{
+    float v = reinterpret_cast<const float *>(dynamic + w * Room<RB>::kWarpRing)[at];
+    for (int o = w + 1; o < s.end[w]; ++o)
+        if (s.busy >> o & 1)
+            v = __fadd_rn(v, reinterpret_cast<const float *>(dynamic + Room<RB>::kRing + o * Room<RB>::kSide)[at]);
     return v;
 }
 

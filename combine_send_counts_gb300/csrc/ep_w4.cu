@@ -270,8 +270,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
 w4_matvec_kernel(MatvecArgs a)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
+    __shared__ Splits splits;
     using F = FormatW4<G, false>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     uint8_t *sides = dynamic + Room<RB>::kRing;
     MatvecItems<G, RB> items{a};
     items.row0 = (int)((int64_t)a.N * blockIdx.x / gridDim.x);
@@ -281,23 +282,22 @@ w4_matvec_kernel(MatvecArgs a)
     items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
     items.open = reinterpret_cast<float *>(dynamic + warp * Room<RB>::kWarpRing);   // the ring is idle by then
     const int n = (items.row1 - items.row0 + 16 * RB - 1) / (16 * RB) * items.passes;
-    const int per = (a.K + F::kUnit - 1) / F::kUnit;
     Stream<F, RB, 1, MatvecItems<G, RB>> stream(items, a.w, a.K, n, smem_u32(dynamic));
     grid_dependency_wait();
     allow_dependents();
     stream.start();
     stream.run();
-    __syncthreads();
-    // the warp that began an item which others went on with adds up its pieces
-    const int begin = run_begin(n, per, warp), end = run_begin(n, per, warp + 1);
-    const int item = (end - 1) / per;
-    if (begin == end || end % per == 0 || item * per < begin)
-        return;
-    const int cols = items.cols(item), nb = cols <= 8 ? 1 : 2;
-    for (int v = lane; v < 16 * RB * cols; v += 32) {
-        const int r = v % (16 * RB), c = v / (16 * RB), at = side_index(r >> 4, r & 15, nb, c);
-        items.store(items.col(item) + c, items.row(item) + r,
-                    add_pieces<RB>(items.open[at], sides, n, per, item, at));
+    find_splits(splits, n, (a.K + F::kUnit - 1) / F::kUnit);
+    for (int w = 0; w < kSkinnyWarps; ++w) {
+        const int item = splits.item[w];
+        if (item < 0)
+            continue;
+        const int cols = items.cols(item), nb = cols <= 8 ? 1 : 2;
+        for (int v = threadIdx.x; v < 16 * RB * cols; v += kSkinnyThreads) {
+            const int r = v % (16 * RB), c = v / (16 * RB);
+            items.store(items.col(item) + c, items.row(item) + r,
+                        add_pieces<RB>(splits, dynamic, w, side_index(r >> 4, r & 15, nb, c)));
+        }
     }
 }
 
