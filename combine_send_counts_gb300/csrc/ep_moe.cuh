@@ -636,9 +636,11 @@ int launch(const UpArgs &up, const DownArgs &down, cudaStream_t stream)
 {
     const int sms = device_sm_count();
     const int64_t elements = (int64_t)std::min(up.r.n, up.r.E_local) * up.I;   // at most: the experts in use are not known here
-    const int64_t mine = ceil_div(elements, sms);
-    int rc = mine > 16 ? launch_up<G, 4>(up, elements, stream)
-             : mine > 8 ? launch_up<G, 2>(up, elements, stream) : launch_up<G, 1>(up, elements, stream);
+    const int mine = (int)ceil_div(ceil_div(elements, sms), 8);             // blocks of 8 elements
+    const int at_once = (int)ceil_div(mine, ceil_div(mine, 4));             // in equal items of up to four
+    int rc = at_once == 1   ? launch_up<G, 1>(up, elements, stream)
+             : at_once == 2 ? launch_up<G, 2>(up, elements, stream)
+             : at_once == 3 ? launch_up<G, 3>(up, elements, stream) : launch_up<G, 4>(up, elements, stream);
     if (rc != EP_OK)
         return rc;
     const unsigned grid = (unsigned)std::min(sms, down.H);

@@ -98,11 +98,12 @@ struct Columns {
         end[nt] = column != nullptr ? K : 0;
     }
 
-    __device__ __forceinline__ uint4 load(int nt, int plane, int k) const
+    // columns k + offset .. +7; the offset is a constant
+    __device__ __forceinline__ uint4 load(int nt, int plane, int k, int offset) const
     {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (k < end[nt])
-            v = __ldg(reinterpret_cast<const uint4 *>(p[nt] + plane * plane_bytes + (uint32_t)k * 2));
+        if (k + offset < end[nt])
+            v = __ldg(reinterpret_cast<const uint4 *>(p[nt] + plane * plane_bytes + (uint32_t)k * 2 + offset * 2));
         return v;
     }
 };
@@ -130,12 +131,14 @@ constexpr uint32_t kMagic = 0x43004300u;
 struct FormatBf16 {
     static constexpr int kUnit = 128;
     static constexpr int kRowPiece = 256;    // bytes of a row in a unit
-    static constexpr int kWordsX = 4;        // 8-column words of x that a lane holds for a unit
+    static constexpr int kWordsX = 4;        // 8-column words of a unit that a lane holds
     static constexpr bool kPermuted = false;
     static constexpr int kPieces = 4;        // 16-byte pieces of a lane's row in a stage
 
     static __device__ __forceinline__ int64_t row_bytes(int K) { return (int64_t)K * 2; }
-    static __device__ __forceinline__ int column(int u, int w, int t) { return u * kUnit + 32 * w + 8 * t; }
+    // word w of lane t are columns lane_column(t) + word_column(w) .. +7 of the unit
+    static __device__ __forceinline__ int lane_column(int t) { return 8 * t; }
+    static __device__ __forceinline__ constexpr int word_column(int w) { return 32 * w; }
     static __device__ __forceinline__ uint4 pair(uint4 v) { return v; }
 
     template <int RB, int STEP>
@@ -190,15 +193,14 @@ struct FormatW4 {
 
     static __device__ __forceinline__ int64_t row_bytes(int K) { return K / 2; }
 
-    // word w of lane t once the lanes have traded
-    static __device__ __forceinline__ int column(int u, int w, int t)
+    // word w of lane t, once the lanes have traded, are columns lane_column(t) + word_column(w) .. +7 of the unit
+    static __device__ __forceinline__ int lane_column(int t)
     {
-        const int base = u * kUnit + 128 * (w >> 2), i = w & 3;
-        if (G == 128)
-            return base + 32 * t + 8 * i;
-        if (G == 64)
-            return base + 64 * (i >> 1) + 32 * (t & 1) + 16 * (t >> 1) + 8 * (i & 1);
-        return base + 32 * i + 8 * t;
+        return G == 128 ? 32 * t : G == 64 ? 32 * (t & 1) + 16 * (t >> 1) : 8 * t;
+    }
+    static __device__ __forceinline__ constexpr int word_column(int w)
+    {
+        return 128 * (w >> 2) + (G == 128 ? 8 * (w & 3) : G == 64 ? 64 * ((w & 3) >> 1) + 8 * (w & 1) : 32 * (w & 3));
     }
 
     static __device__ __forceinline__ uint4 pair(uint4 v)
@@ -451,8 +453,8 @@ private:
             fresh_ = false;
         }
         off_ = u_ahead_ * F::kRowPiece + (lane % kLanes) * 16;
-        in_ = off_ < row_bytes;   // past the row: zeros
-        off_ = in_ ? off_ : 0;
+        if (off_ >= row_bytes)    // past the row: zeros
+            n_ = m_ = 0;
         if (++u_ahead_ == per_) {
             u_ahead_ = 0;
             ++item_ahead_;
@@ -460,7 +462,7 @@ private:
         }
     }
 
-    // its copies of row block r
+    // its copies of row block r (zeros for rows that it does not have)
     __device__ __forceinline__ void issue(int r)
     {
         if (live_) {
@@ -469,15 +471,14 @@ private:
 #pragma unroll
             for (int i = 0; i < 8 / kAtOnce; ++i) {
                 const int row = r * Items::kStep + i * kAtOnce, off = off_ + row * row_bytes;
-                if (row < n_)
-                    cp_async16(dst + i * kAtOnce * F::kRowPiece, pa_ + off, in_);
-                if (row < m_)
-                    cp_async16(dst + (8 + i * kAtOnce) * F::kRowPiece, pb_ + off, in_);
+                cp_async16(dst + i * kAtOnce * F::kRowPiece, pa_ + off, row < n_);
+                cp_async16(dst + (8 + i * kAtOnce) * F::kRowPiece, pb_ + off, row < m_);
             }
         }
-        cp_async_commit();
-        if (r == RB - 1)
+        if (r == RB - 1) {
+            cp_async_commit();
             slot_ahead_ = slot_ahead_ == (kUnits - 1) * RB ? 0 : slot_ahead_ + RB;
+        }
     }
 
     template <int NT>
@@ -493,7 +494,7 @@ private:
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int p = 0; p < PLANES; ++p)
-                    x[w][nt][p] = F::pair(c.load(nt, p, F::column(u, w, t_)));
+                    x[w][nt][p] = F::pair(c.load(nt, p, u * F::kUnit + F::lane_column(t_), F::word_column(w)));
         };
         scales.begin(w_, items_.rows(item), K_, g_, t_);
         scales.load(u0);
@@ -502,10 +503,10 @@ private:
             load_x(w, u0);
         for (int u = u0; u < u1; ++u) {
             open();
+            cp_async_wait<kUnits - 1>();
+            __syncwarp();   // every lane's copies of the unit have arrived
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
-                cp_async_wait<kUnits * RB - 1>();
-                __syncwarp();   // every lane's copies have arrived
                 const uint32_t src = get_ + (slot_ + r) * kStageBytes;
                 uint4 a[F::kPieces], b[F::kPieces];
 #pragma unroll
@@ -534,7 +535,7 @@ private:
     uint32_t put_, get_;
     const uint8_t *pa_, *pb_;
     int n_, m_;
-    bool fresh_, live_, in_;
+    bool fresh_, live_;
 };
 
 // The first unit of warp w's run (see Stream), for whoever adds up the pieces.

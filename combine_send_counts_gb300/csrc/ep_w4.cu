@@ -318,9 +318,13 @@ int matvec(const MatvecArgs &a, cudaStream_t stream)
     const dim3 grid(sms, (unsigned)ceil_div(a.M, kMaxPasses * kMaxCols));
     // a warp takes as many blocks of 16 rows at a time as its block has rows for: each x it loads serves them all
     const int64_t rows = ceil_div(a.N, sms);
-    if (rows > 32)
-        return launch_matvec<G, 4>(a, grid, stream);
-    return rows > 16 ? launch_matvec<G, 2>(a, grid, stream) : launch_matvec<G, 1>(a, grid, stream);
+    const int blocks = (int)ceil_div(rows, 16), at_once = (int)ceil_div(blocks, ceil_div(blocks, 4));
+    switch (at_once) {
+    case 1: return launch_matvec<G, 1>(a, grid, stream);
+    case 2: return launch_matvec<G, 2>(a, grid, stream);
+    case 3: return launch_matvec<G, 3>(a, grid, stream);
+    default: return launch_matvec<G, 4>(a, grid, stream);
+    }
 }
 
 bool w4_shape_ok(int64_t N, int64_t K, int group)
