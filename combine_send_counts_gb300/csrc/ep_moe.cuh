@@ -349,9 +349,9 @@ struct UpItems {
             i = 0;
             size = j == j1 ? tail.size : body.size;
         }
-        const int n = passes(j);
-        i += v / n * size;
-        q = l.entry[j] + v % n;
+        const int n = passes(j), block = n == 1 ? v : v / n;
+        i += block * size;
+        q = l.entry[j] + v - block * n;
         end = min(i + size, j == j1 ? i1 : a.I);
     }
 

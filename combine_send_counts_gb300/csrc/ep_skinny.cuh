@@ -248,21 +248,23 @@ struct FormatW4 {
         static constexpr int kGroups = kUnit / G;
         uint32_t q[2][kGroups];
         uint32_t magic;
-        const uint16_t *s0, *s1;    // the lane's rows, or null
+        const uint16_t *s0, *s1;    // the lane's rows
         const uint8_t *z0, *z1;
-        int groups;                 // of a row
+        int n0, n1, y0, y1;         // their groups and zero points to load: all of K's, or none
 
         __device__ __forceinline__ void begin(const Weights &w, const RowRange &rows, int K, int g, int t)
         {
-            groups = K / G;
-            magic = w.magic;
-            const int i = t * STEP + g;
+            const int groups = K / G, i = t * STEP + g;
             const int64_t a = (rows.a + i) * groups, b = (rows.b + i) * groups;
-            const bool mine = t < RB;
-            s0 = mine && i < rows.n ? w.scale + a : nullptr;
-            s1 = mine && i < rows.m ? w.scale + b : nullptr;
-            z0 = s0 != nullptr && w.zero != nullptr ? w.zero + a : nullptr;
-            z1 = s1 != nullptr && w.zero != nullptr ? w.zero + b : nullptr;
+            magic = w.magic;
+            s0 = w.scale + a;
+            s1 = w.scale + b;
+            z0 = w.zero + a;
+            z1 = w.zero + b;
+            n0 = t < RB && i < rows.n ? groups : 0;
+            n1 = t < RB && i < rows.m ? groups : 0;
+            y0 = w.zero != nullptr ? n0 : 0;
+            y1 = w.zero != nullptr ? n1 : 0;
         }
 
         __device__ __forceinline__ void load(int u)
@@ -270,11 +272,10 @@ struct FormatW4 {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 const int at = u * kGroups + i;
-                const bool in = at < groups;
-                const uint32_t v0 = in && s0 != nullptr ? __ldg(s0 + at) : 0, v1 = in && s1 != nullptr ? __ldg(s1 + at) : 0;
-                const uint32_t y0 = in && z0 != nullptr ? __ldg(z0 + at) : 8, y1 = in && z1 != nullptr ? __ldg(z1 + at) : 8;
-                q[0][i] = v0 << 16 | 0x4300u | y0;
-                q[1][i] = v1 << 16 | 0x4300u | y1;
+                const uint32_t v0 = at < n0 ? __ldg(s0 + at) : 0, v1 = at < n1 ? __ldg(s1 + at) : 0;
+                const uint32_t w0 = at < y0 ? __ldg(z0 + at) : 8, w1 = at < y1 ? __ldg(z1 + at) : 8;
+                q[0][i] = v0 << 16 | 0x4300u | w0;
+                q[1][i] = v1 << 16 | 0x4300u | w1;
             }
         }
 
@@ -400,9 +401,9 @@ public:
         // quarter warp, which read two rows, meet all 32 banks
         const int row = lane / kLanes, piece = lane % kLanes;
         put_ = ring + warp * Room<RB>::kWarpRing + row * F::kRowPiece + (piece ^ ((row & 1) << 2)) * 16;
-        get_ = ring + warp * Room<RB>::kWarpRing + g_ * F::kRowPiece + t_ * 16;
+        get_ = ring + warp * Room<RB>::kWarpRing + g_ * F::kRowPiece + (g_ & 1) * 64 + t_ * 16;
         left_ = end_ - begin_;
-        item_ahead_ = begin_ / per_;
+        item_ahead_ = first_item_ = begin_ / per_;
         u_ahead_ = begin_ - item_ahead_ * per_;
         slot_ahead_ = slot_ = 0;
         fresh_ = true;
@@ -421,15 +422,16 @@ public:
 
     __device__ __forceinline__ void run()
     {
-        int at = begin_;
-        while (at < end_) {
-            const int item = at / per_, u0 = at - item * per_;
-            const int u1 = min(per_, u0 + end_ - at);
+        int item = first_item_, u0 = begin_ - item * per_, left = end_ - begin_;
+        while (left > 0) {
+            const int u1 = min(per_, u0 + left);
             if (items_.cols(item) <= 8)
                 piece<1>(item, u0, u1);
             else
                 piece<2>(item, u0, u1);
-            at += u1 - u0;
+            left -= u1 - u0;
+            ++item;
+            u0 = 0;
         }
     }
 
@@ -467,7 +469,7 @@ private:
     {
         if (live_) {
             const int row_bytes = (int)F::row_bytes(K_);
-            const uint32_t dst = put_ + (slot_ahead_ + r) * kStageBytes;
+            const uint32_t dst = put_ + slot_ahead_ + r * kStageBytes;
 #pragma unroll
             for (int i = 0; i < 8 / kAtOnce; ++i) {
                 const int row = r * Items::kStep + i * kAtOnce, off = off_ + row * row_bytes;
@@ -477,7 +479,7 @@ private:
         }
         if (r == RB - 1) {
             cp_async_commit();
-            slot_ahead_ = slot_ahead_ == (kUnits - 1) * RB ? 0 : slot_ahead_ + RB;
+            slot_ahead_ = slot_ahead_ == (kUnits - 1) * RB * kStageBytes ? 0 : slot_ahead_ + RB * kStageBytes;
         }
     }
 
@@ -505,14 +507,15 @@ private:
             open();
             cp_async_wait<kUnits - 1>();
             __syncwarp();   // every lane's copies of the unit have arrived
+            const uint32_t even = get_ + slot_, odd = even + 64 - 128 * (g_ & 1);
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
-                const uint32_t src = get_ + (slot_ + r) * kStageBytes;
                 uint4 a[F::kPieces], b[F::kPieces];
 #pragma unroll
-                for (int j = 0; j < F::kPieces; ++j) {
-                    a[j] = ld_shared16(src + ((j ^ (g_ & 1)) << 6));
-                    b[j] = ld_shared16(src + ((j ^ (g_ & 1)) << 6) + 8 * F::kRowPiece);
+                for (int j = 0; j < F::kPieces; ++j) {   // 64-byte piece j of a row stands at j ^ (row & 1)
+                    const uint32_t at = (j & 1 ? odd : even) + r * kStageBytes + (j & ~1) * 64;
+                    a[j] = ld_shared16(at);
+                    b[j] = ld_shared16(at + 8 * F::kRowPiece);
                 }
                 __syncwarp();   // every lane has read the stage
                 issue(r);
@@ -522,7 +525,7 @@ private:
                 });
             }
             scales.load(u + 1);
-            slot_ = slot_ == (kUnits - 1) * RB ? 0 : slot_ + RB;
+            slot_ = slot_ == (kUnits - 1) * RB * kStageBytes ? 0 : slot_ + RB * kStageBytes;
         }
         items_.template done<NT>(item, u0 == 0, u1 == per_, acc);
     }
@@ -530,7 +533,7 @@ private:
     const Items &items_;
     const Weights &w_;
     int K_, per_, g_, t_;
-    int begin_, end_, left_, item_ahead_, u_ahead_;
+    int begin_, end_, left_, first_item_, item_ahead_, u_ahead_;
     int slot_ahead_, slot_, off_;
     uint32_t put_, get_;
     const uint8_t *pa_, *pb_;
