@@ -44,4 +44,25 @@ inline int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, s
     return EP_OK;
 }
 
+// How many of a block's `blocks` row blocks a warp takes at a time, up to four
+// (`most`): each x it loads serves them all, but an item that has fewer still
+// takes the time of all, which counts where the codes' arithmetic is what takes
+// time (4-bit weights; a stage of it is about 270 instructions, and a unit's x
+// 40).  bf16: the largest equal items.
+inline int blocks_at_once(int64_t blocks, int most, bool w4)
+{
+    int best = (int)ceil_div(blocks, ceil_div(blocks, most));
+    if (w4) {
+        int64_t least = INT64_MAX;
+        for (int n = most; n >= 1; --n) {
+            const int64_t cost = ceil_div(blocks, n) * (270 * n + 40);
+            if (cost < least) {
+                least = cost;
+                best = n;
+            }
+        }
+    }
+    return best;
+}
+
 }  // namespace ep

@@ -40,8 +40,7 @@
 
 namespace ep {
 
-constexpr int kThreads = kSkinnyThreads;
-constexpr int kWarps = kSkinnyWarps;
+constexpr int kMostWarps = 16;
 constexpr int kMaxSlots = EP_MOE_MAX_SLOTS;
 constexpr int kMaxDim = 65536;   // H and I: a block's units are counted in 32 bits
 
@@ -70,7 +69,7 @@ __device__ __forceinline__ int passes_of(int slots) { return (slots + kMaxCols -
 // for each pass over its weights, of up to 16 slots.
 struct Lists {
     int experts, entries, big;
-    int scan[3][kWarps];
+    int scan[3][kMostWarps];
     int cost[kMaxSlots + 1];          // exclusive sums over the experts of the cost of a weight row
     uint16_t id[kMaxSlots];           // expert j's local id
     uint16_t entry[kMaxSlots + 1];    // its first entry: it has entry[j] .. entry[j+1]
@@ -133,7 +132,8 @@ __device__ __forceinline__ void build_few(const Routing &r, Lists &l, int32_t *e
     __syncthreads();
 }
 
-// All threads of the block; count: E_local ints of shared memory.
+// All threads of the block, WARPS warps; count: E_local ints of shared memory.
+template <int WARPS>
 __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *count, int32_t *err)
 {
     if (r.n <= 32) {
@@ -141,12 +141,12 @@ __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *cou
         return;
     }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < r.E_local; e += kThreads)
+    for (int e = tid; e < r.E_local; e += (32 * WARPS))
         count[e] = 0;
     if (tid == 0)
         l.big = 0;
     __syncthreads();
-    for (int s = tid; s < r.n; s += kThreads) {
+    for (int s = tid; s < r.n; s += (32 * WARPS)) {
         const int e = r.local(s, err);
         l.use[s] = (int16_t)e;
         if (e >= 0)
@@ -154,7 +154,7 @@ __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *cou
     }
     __syncthreads();
     // each thread owns a run of experts; scans of (experts in use, entries, slots)
-    const int per = (r.E_local + kThreads - 1) / kThreads;
+    const int per = (r.E_local + (32 * WARPS) - 1) / (32 * WARPS);
     const int e0 = min(tid * per, r.E_local), e1 = min(e0 + per, r.E_local);
     int own[3] = {0, 0, 0};
     for (int e = e0; e < e1; ++e) {
@@ -199,7 +199,7 @@ __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *cou
         ++j;
         at += c;
     }
-    if (tid == kThreads - 1) {
+    if (tid == (32 * WARPS) - 1) {
         l.experts = j;
         l.entries = q;
         l.entry[j] = (uint16_t)q;
@@ -210,7 +210,7 @@ __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *cou
     // The order of slots within an entry moves no result, but every block must put the same slots into an
     // entry: where an expert has several, its slots take their places in ascending order.
     if (l.big > 0) {
-        for (int b = warp; b < l.big; b += kWarps) {
+        for (int b = warp; b < l.big; b += WARPS) {
             const int e = l.big_expert[b];
             int before = 0;
             for (int s0 = 0; s0 < r.n; s0 += 32) {
@@ -224,7 +224,7 @@ __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *cou
         }
         __syncthreads();
     }
-    for (int s = tid; s < r.n; s += kThreads) {
+    for (int s = tid; s < r.n; s += (32 * WARPS)) {
         const int e = l.use[s];
         if (e >= 0) {
             const int p = l.place[s], f = count[e];
@@ -423,27 +423,27 @@ __device__ __forceinline__ void share_begin(const Lists &l, int I, int b, int bl
 }
 
 template <int G, int RB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(32 * FormatOf<G, false>::F::kWarps, 1)
 moe_up_kernel(UpArgs a)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
     __shared__ Lists l;
-    __shared__ Splits splits;
     using F = typename FormatOf<G, false>::F;
+    __shared__ Splits<F> splits;
     grid_dependency_wait();
     allow_dependents();
-    build_lists(a.r, l, reinterpret_cast<int *>(dynamic), blockIdx.x == 0 ? a.err : nullptr);
+    build_lists<F::kWarps>(a.r, l, reinterpret_cast<int *>(dynamic), blockIdx.x == 0 ? a.err : nullptr);
     if (l.experts == 0)
         return;
     const int warp = threadIdx.x >> 5;
-    uint8_t *sides = dynamic + Room<RB>::kRing;
+    uint8_t *sides = dynamic + Room<F, RB>::kRing;
     int j0, i0, j1 = l.experts, i1 = 0;
     share_begin(l, a.I, blockIdx.x, gridDim.x, j0, i0);
     if (blockIdx.x + 1 < gridDim.x)
         share_begin(l, a.I, blockIdx.x + 1, gridDim.x, j1, i1);
     UpItems<G, RB> items(a, l, j0, i0, j1, i1);
-    items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
-    items.open = reinterpret_cast<float *>(dynamic + warp * Room<RB>::kWarpRing);   // the ring is idle by then
+    items.side = reinterpret_cast<float *>(sides + warp * Room<F, RB>::kSide);
+    items.open = reinterpret_cast<float *>(dynamic + warp * Room<F, RB>::kWarpRing);   // the ring is idle by then
     const int n = items.count();
     if (n == 0)
         return;
@@ -451,18 +451,18 @@ moe_up_kernel(UpArgs a)
     stream.start();
     stream.run();
     find_splits(splits, n, (a.H + F::kUnit - 1) / F::kUnit);
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < F::kWarps; ++w) {
         if (splits.item[w] < 0)
             continue;
         int q, j, i, stop;
         items.where(splits.item[w], q, j, i, stop);
         const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
-        for (int v = threadIdx.x; v < 8 * RB * cols; v += kThreads) {
+        for (int v = threadIdx.x; v < 8 * RB * cols; v += 32 * F::kWarps) {
             const int e = v % (8 * RB), c = v / (8 * RB);
             if (i + e < stop)
                 store_planes<(G > 0)>(a.out, l.slot[first + c], i + e,
-                                      activate(add_pieces<RB>(splits, dynamic, w, side_index(e >> 3, e & 7, nb, c)),
-                                               add_pieces<RB>(splits, dynamic, w, side_index(e >> 3, (e & 7) + 8, nb, c))));
+                                      activate(add_pieces<F, RB>(splits, dynamic, w, side_index(e >> 3, e & 7, nb, c)),
+                                               add_pieces<F, RB>(splits, dynamic, w, side_index(e >> 3, (e & 7) + 8, nb, c))));
         }
     }
 }
@@ -542,25 +542,25 @@ struct DownItems {
 };
 
 template <int G, int PLANES, int RB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(32 * FormatOf<G, (G > 0)>::F::kWarps, 1)
 moe_down_kernel(DownArgs a)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, one side block per warp, y if it fits
     __shared__ Lists l;
-    __shared__ Splits splits;
     using F = typename FormatOf<G, (G > 0)>::F;
+    __shared__ Splits<F> splits;
     // topk_idx was complete before the up kernel began; h is complete after the wait
-    build_lists(a.r, l, reinterpret_cast<int *>(dynamic), nullptr);
+    build_lists<F::kWarps>(a.r, l, reinterpret_cast<int *>(dynamic), nullptr);
     const int warp = threadIdx.x >> 5;
-    uint8_t *sides = dynamic + Room<RB>::kRing;
+    uint8_t *sides = dynamic + Room<F, RB>::kRing;
     DownItems<G, PLANES, RB> items{a, l};
     items.row0 = (int)((int64_t)a.H * blockIdx.x / gridDim.x);
     items.row1 = (int)((int64_t)a.H * (blockIdx.x + 1) / gridDim.x);
     const int rows = items.row1 - items.row0;
-    items.y = a.y != nullptr ? a.y + items.row0 : reinterpret_cast<float *>(dynamic + Room<RB>::kFixed);
+    items.y = a.y != nullptr ? a.y + items.row0 : reinterpret_cast<float *>(dynamic + Room<F, RB>::kFixed);
     items.stride = a.y != nullptr ? a.H : rows | 1;
-    items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
-    items.open = reinterpret_cast<float *>(dynamic + warp * Room<RB>::kWarpRing);
+    items.side = reinterpret_cast<float *>(sides + warp * Room<F, RB>::kSide);
+    items.open = reinterpret_cast<float *>(dynamic + warp * Room<F, RB>::kWarpRing);
     const int n = (rows + 16 * RB - 1) / (16 * RB) * l.entries;
     Stream<F, RB, PLANES, DownItems<G, PLANES, RB>> stream(items, a.w, a.I, n, smem_u32(dynamic));
     stream.start();
@@ -568,20 +568,20 @@ moe_down_kernel(DownArgs a)
     allow_dependents();
     stream.run();
     find_splits(splits, n, (a.I + F::kUnit - 1) / F::kUnit);
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < F::kWarps; ++w) {
         if (splits.item[w] < 0)
             continue;
         const int b = splits.item[w] / l.entries, q = splits.item[w] - b * l.entries;
         const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
-        for (int v = threadIdx.x; v < 16 * RB * cols; v += kThreads) {
+        for (int v = threadIdx.x; v < 16 * RB * cols; v += 32 * F::kWarps) {
             const int r = v % (16 * RB), c = v / (16 * RB), i = b * (16 * RB) + r;
             if (i < rows)
                 items.y[(int64_t)l.slot[first + c] * items.stride + i] =
-                    add_pieces<RB>(splits, dynamic, w, side_index(r >> 4, r & 15, nb, c));
+                    add_pieces<F, RB>(splits, dynamic, w, side_index(r >> 4, r & 15, nb, c));
         }
     }
     __syncthreads();
-    for (int v = threadIdx.x; v < a.T * rows; v += kThreads) {
+    for (int v = threadIdx.x; v < a.T * rows; v += 32 * F::kWarps) {
         const int tok = v / rows, i = v - tok * rows;
         float sum = 0.0f;
         for (int k = 0; k < a.r.K; ++k) {
@@ -598,27 +598,31 @@ moe_down_kernel(DownArgs a)
 }
 
 // ------------------------------------------------------------ launch policy --
-constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - sizeof(Splits) - 64;   // dynamic shared memory of a block that owns an SM
+constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - sizeof(Splits<FormatW4<128, false>>) - 64;   // dynamic shared memory of a block that owns an SM
 
 template <int G, int RB>
 int launch_up(const UpArgs &a, int64_t elements, cudaStream_t stream)
 {
-    static_assert(EP_MAX_EXPERTS * sizeof(int) <= (size_t)Room<RB>::kRing, "the experts' counters use the ring before it starts");
+    using F = typename FormatOf<G, false>::F;
+    constexpr int kSmem = Room<F, RB>::kFixed;
+    static_assert(EP_MAX_EXPERTS * sizeof(int) <= Room<F, RB>::kRing, "the experts' counters use the ring before it starts");
+    static_assert(kSmem <= kMaxSmem, "a block fits");
     static PerDevice set;
-    const int rc = raise_smem(moe_up_kernel<G, RB>, Room<RB>::kFixed, set);
+    const int rc = raise_smem(moe_up_kernel<G, RB>, kSmem, set);
     if (rc != EP_OK)
         return rc;
     const unsigned grid = (unsigned)std::min<int64_t>(elements, device_sm_count());
-    return launch_dependent(moe_up_kernel<G, RB>, grid, kThreads, Room<RB>::kFixed, stream, a);
+    return launch_dependent(moe_up_kernel<G, RB>, grid, 32 * F::kWarps, kSmem, stream, a);
 }
 
 template <int G, int PLANES, int RB>
 int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
 {
+    using F = typename FormatOf<G, (G > 0)>::F;
     static PerDevice set;
     // the slots' results stay in shared memory where there is room for them
     const size_t y = (size_t)a.r.n * ((size_t)ceil_div(a.H, grid) | 1) * sizeof(float);
-    size_t smem = Room<RB>::kFixed;
+    size_t smem = Room<F, RB>::kFixed;
     if (smem + y <= kMaxSmem) {
         smem += y;
         a.y = nullptr;
@@ -626,30 +630,44 @@ int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
     const int rc = raise_smem(moe_down_kernel<G, PLANES, RB>, smem, set);
     if (rc != EP_OK)
         return rc;
-    return launch_dependent(moe_down_kernel<G, PLANES, RB>, grid, kThreads, smem, stream, a);
+    return launch_dependent(moe_down_kernel<G, PLANES, RB>, grid, 32 * F::kWarps, smem, stream, a);
 }
 
-// The two kernels.  A warp takes as many blocks of 16 rows at a time as its
-// block has rows for: each x it loads serves all of them.
+template <int G, int RB = FormatOf<G, false>::F::kMaxBlocks>
+int launch_up_blocks(const UpArgs &a, int64_t elements, int blocks, cudaStream_t stream)
+{
+    if constexpr (RB > 1) {
+        if (blocks < RB)
+            return launch_up_blocks<G, RB - 1>(a, elements, blocks, stream);
+    }
+    return launch_up<G, RB>(a, elements, stream);
+}
+
+constexpr int kMostDown = 3;   // row blocks of down at a time: 48 rows are a block's share up to H = 7296
+
+template <int G, int PLANES, int RB>
+int launch_down_blocks(const DownArgs &a, unsigned grid, int blocks, cudaStream_t stream)
+{
+    if constexpr (RB > 1) {
+        if (blocks < RB)
+            return launch_down_blocks<G, PLANES, RB - 1>(a, grid, blocks, stream);
+    }
+    return launch_down<G, PLANES, RB>(a, grid, stream);
+}
+
 template <int G>
 int launch(const UpArgs &up, const DownArgs &down, cudaStream_t stream)
 {
+    constexpr int kMost = FormatOf<G, false>::F::kMaxBlocks, kDown = kMost < kMostDown ? kMost : kMostDown;
     const int sms = device_sm_count();
     const int64_t elements = (int64_t)std::min(up.r.n, up.r.E_local) * up.I;   // at most: the experts in use are not known here
-    const int mine = (int)ceil_div(ceil_div(elements, sms), 8);             // blocks of 8 elements
-    const int at_once = (int)ceil_div(mine, ceil_div(mine, 4));             // in equal items of up to four
-    int rc = at_once == 1   ? launch_up<G, 1>(up, elements, stream)
-             : at_once == 2 ? launch_up<G, 2>(up, elements, stream)
-             : at_once == 3 ? launch_up<G, 3>(up, elements, stream) : launch_up<G, 4>(up, elements, stream);
+    const int rc = launch_up_blocks<G>(up, elements, blocks_at_once(ceil_div(ceil_div(elements, sms), 8), kMost, G > 0), stream);
     if (rc != EP_OK)
         return rc;
     const unsigned grid = (unsigned)std::min(sms, down.H);
-    const int64_t rows = ceil_div(down.H, grid);
-    if (down.out_f32)
-        return rows > 32 ? launch_down<G, 3, 3>(down, grid, stream)
-               : rows > 16 ? launch_down<G, 3, 2>(down, grid, stream) : launch_down<G, 3, 1>(down, grid, stream);
-    return rows > 32 ? launch_down<G, 2, 3>(down, grid, stream)
-           : rows > 16 ? launch_down<G, 2, 2>(down, grid, stream) : launch_down<G, 2, 1>(down, grid, stream);
+    const int blocks = blocks_at_once(ceil_div(ceil_div(down.H, grid), 16), kDown, G > 0);
+    return down.out_f32 ? launch_down_blocks<G, 3, kDown>(down, grid, blocks, stream)
+                        : launch_down_blocks<G, 2, kDown>(down, grid, blocks, stream);
 }
 
 }  // namespace ep

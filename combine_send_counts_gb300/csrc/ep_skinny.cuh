@@ -3,7 +3,7 @@
 // With a few tokens every weight is used a handful of times, so these products
 // are bound by reading the weights from HBM, and what counts is that enough of
 // them is in flight all the time.  A block owns an SM and a share of the weight
-// rows; its 8 warps share that work in equal runs of K, each streaming up to 64
+// rows; its warps share that work in equal runs of K, each streaming up to 64
 // rows at a time through a ring of its own in shared memory:
 //
 //   - cp.async brings 16 rows times 256 bytes (4-bit: 128) to a stage of the
@@ -31,18 +31,20 @@
 
 namespace ep {
 
-constexpr int kSkinnyWarps = 8;
-constexpr int kSkinnyThreads = 32 * kSkinnyWarps;
 constexpr int kMaxCols = 16;         // columns of one pass over the weights: 2 blocks of 8
 
 // The shared memory of a block whose warps take RB blocks of 16 rows at a time:
-// 96 or 128 KB are in flight per SM, and 45 KB/us times about 1 us are needed.
-template <int RB>
+// 96 to 128 KB of weights are in flight per SM, and 45 KB/us times about 1 us
+// are needed.
+template <class F, int RB>
 struct Room {
-    static constexpr int kWarpRing = (RB == 3 ? 12 : 16) * 1024;
-    static constexpr int kRing = kSkinnyWarps * kWarpRing;
-    static constexpr int kSide = RB * 16 * kMaxCols * 4;   // one warp's kept sums
-    static constexpr int kFixed = kRing + kSkinnyWarps * kSide;
+    static constexpr int kStage = 16 * F::kRowPiece;                         // one row block, one unit of K
+    static constexpr int kUnits = 128 * 1024 / F::kWarps / (RB * kStage);    // units in a warp's ring
+    static constexpr int kWarpRing = kUnits * RB * kStage;
+    static constexpr int kRing = F::kWarps * kWarpRing;
+    static constexpr int kSide = RB * 16 * kMaxCols * 4;                     // one warp's kept sums
+    static constexpr int kFixed = kRing + F::kWarps * kSide;
+    static_assert(kUnits >= 1 && kSide <= kWarpRing, "the ring holds a unit, and kept sums after the run");
 };
 
 // D += A (16x16, row) * B (16x8, col), bf16 in, fp32 sums.
@@ -129,6 +131,8 @@ constexpr uint32_t kMagic = 0x43004300u;
 // bf16 weights.  A unit is 128 columns; word j of lane (g, t) are columns
 // 32j + 8t .. +7 of its rows, two k16 steps.
 struct FormatBf16 {
+    static constexpr int kWarps = 8;
+    static constexpr int kMaxBlocks = 4;     // row blocks that a warp takes at a time
     static constexpr int kUnit = 128;
     static constexpr int kRowPiece = 256;    // bytes of a row in a unit
     static constexpr int kWordsX = 4;        // 8-column words of a unit that a lane holds
@@ -184,6 +188,8 @@ struct FormatBf16 {
 // until each matrix step stays in one group.
 template <int G, bool PERMUTED>
 struct FormatW4 {
+    static constexpr int kWarps = 8;
+    static constexpr int kMaxBlocks = 4;
     static constexpr int kUnit = 256;
     static constexpr int kRowPiece = 128;
     static constexpr int kWordsX = 8;
@@ -382,11 +388,10 @@ __device__ __forceinline__ void keep(float *side, const float (&acc)[RB][NT][4])
 template <class F, int RB, int PLANES, class Items>
 class Stream {
 public:
-    static constexpr int kStageBytes = 16 * F::kRowPiece;
-    static constexpr int kUnits = Room<RB>::kWarpRing / (RB * kStageBytes);   // units in the ring
+    static constexpr int kStageBytes = Room<F, RB>::kStage;
+    static constexpr int kUnits = Room<F, RB>::kUnits;
     static constexpr int kLanes = F::kRowPiece / 16;   // lanes that copy one row
     static constexpr int kAtOnce = 32 / kLanes;        // rows of one copy instruction
-    static_assert(kUnits >= 1, "the ring holds a unit");
 
     __device__ __forceinline__ Stream(const Items &items, const Weights &w, int K, int n_items, uint32_t ring)
         : items_(items), w_(w), K_(K), per_((K + F::kUnit - 1) / F::kUnit)
@@ -395,13 +400,13 @@ public:
         g_ = lane >> 2;
         t_ = lane & 3;
         const int64_t total = (int64_t)n_items * per_;
-        begin_ = (int)(total * warp / kSkinnyWarps);
-        end_ = (int)(total * (warp + 1) / kSkinnyWarps);
+        begin_ = (int)(total * warp / F::kWarps);
+        end_ = (int)(total * (warp + 1) / F::kWarps);
         // a row's 16-byte pieces are swapped in groups of four on odd rows, so that the eight lanes of a
         // quarter warp, which read two rows, meet all 32 banks
         const int row = lane / kLanes, piece = lane % kLanes;
-        put_ = ring + warp * Room<RB>::kWarpRing + row * F::kRowPiece + (piece ^ ((row & 1) << 2)) * 16;
-        get_ = ring + warp * Room<RB>::kWarpRing + g_ * F::kRowPiece + (g_ & 1) * 64 + t_ * 16;
+        put_ = ring + warp * Room<F, RB>::kWarpRing + row * F::kRowPiece + (piece ^ ((row & 1) << 2)) * 16;
+        get_ = ring + warp * Room<F, RB>::kWarpRing + g_ * F::kRowPiece + (g_ & 1) * 64 + t_ * 16;
         left_ = end_ - begin_;
         item_ahead_ = first_item_ = begin_ / per_;
         u_ahead_ = begin_ - item_ahead_ * per_;
@@ -542,33 +547,36 @@ private:
 };
 
 // The first unit of warp w's run (see Stream), for whoever adds up the pieces.
+template <class F>
 __device__ __forceinline__ int run_begin(int n_items, int per, int w)
 {
-    return (int)((int64_t)n_items * per * w / kSkinnyWarps);
+    return (int)((int64_t)n_items * per * w / F::kWarps);
 }
 
 // The items of a block that are divided among warps: item[w] is the one that
 // warp w began and did not finish (-1: none); it kept its piece at the start of
 // its ring, which is idle by then, and warps w+1 .. end[w]-1 kept theirs in
 // their side blocks (those with work).
+template <class F>
 struct Splits {
-    int item[kSkinnyWarps], end[kSkinnyWarps];
+    int item[F::kWarps], end[F::kWarps];
     unsigned busy;      // bit w: warp w had work
 };
 
 // All threads, after their run; holds a barrier, after which the kept pieces
 // may be read.
-__device__ __forceinline__ void find_splits(Splits &s, int n_items, int per)
+template <class F>
+__device__ __forceinline__ void find_splits(Splits<F> &s, int n_items, int per)
 {
     const int w = threadIdx.x;
     if (w < 32) {
-        const int begin = run_begin(n_items, per, min(w, kSkinnyWarps)), end = run_begin(n_items, per, min(w + 1, kSkinnyWarps));
+        const int begin = run_begin<F>(n_items, per, min(w, F::kWarps)), end = run_begin<F>(n_items, per, min(w + 1, F::kWarps));
         const unsigned busy = __ballot_sync(kFull, begin < end);
-        if (w < kSkinnyWarps) {
+        if (w < F::kWarps) {
             const int item = end > 0 ? (end - 1) / per : 0;
             const bool open = begin < end && item * per >= begin && (item + 1) * per > end;
             int last = w + 1;
-            while (open && last < kSkinnyWarps && run_begin(n_items, per, last) < (item + 1) * per)
+            while (open && last < F::kWarps && run_begin<F>(n_items, per, last) < (item + 1) * per)
                 ++last;
             s.item[w] = open ? item : -1;
             s.end[w] = last;
@@ -581,13 +589,13 @@ __device__ __forceinline__ void find_splits(Splits &s, int n_items, int per)
 
 // The sum at place `at` of the item that warp w began: its pieces in the order
 // of K.  `dynamic`: the ring, then the side blocks.
-template <int RB>
-__device__ __forceinline__ float add_pieces(const Splits &s, const uint8_t *dynamic, int w, int at)
+template <class F, int RB>
+__device__ __forceinline__ float add_pieces(const Splits<F> &s, const uint8_t *dynamic, int w, int at)
 {
-    float v = reinterpret_cast<const float *>(dynamic + w * Room<RB>::kWarpRing)[at];
+    float v = reinterpret_cast<const float *>(dynamic + w * Room<F, RB>::kWarpRing)[at];
     for (int o = w + 1; o < s.end[w]; ++o)
         if (s.busy >> o & 1)
-            v = __fadd_rn(v, reinterpret_cast<const float *>(dynamic + Room<RB>::kRing + o * Room<RB>::kSide)[at]);
+            v = __fadd_rn(v, reinterpret_cast<const float *>(dynamic + Room<F, RB>::kRing + o * Room<F, RB>::kSide)[at]);
     return v;
 }
 

@@ -266,21 +266,21 @@ struct MatvecItems {
 };
 
 template <int G, int RB>
-__global__ void __launch_bounds__(kSkinnyThreads, 1)
+__global__ void __launch_bounds__(32 * FormatW4<G, false>::kWarps, 1)
 w4_matvec_kernel(MatvecArgs a)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
-    __shared__ Splits splits;
     using F = FormatW4<G, false>;
+    __shared__ Splits<F> splits;
     const int warp = threadIdx.x >> 5;
-    uint8_t *sides = dynamic + Room<RB>::kRing;
+    uint8_t *sides = dynamic + Room<F, RB>::kRing;
     MatvecItems<G, RB> items{a};
     items.row0 = (int)((int64_t)a.N * blockIdx.x / gridDim.x);
     items.row1 = (int)((int64_t)a.N * (blockIdx.x + 1) / gridDim.x);
     items.m0 = blockIdx.y * (kMaxPasses * kMaxCols);
     items.passes = min((a.M - items.m0 + kMaxCols - 1) / kMaxCols, kMaxPasses);
-    items.side = reinterpret_cast<float *>(sides + warp * Room<RB>::kSide);
-    items.open = reinterpret_cast<float *>(dynamic + warp * Room<RB>::kWarpRing);   // the ring is idle by then
+    items.side = reinterpret_cast<float *>(sides + warp * Room<F, RB>::kSide);
+    items.open = reinterpret_cast<float *>(dynamic + warp * Room<F, RB>::kWarpRing);   // the ring is idle by then
     const int n = (items.row1 - items.row0 + 16 * RB - 1) / (16 * RB) * items.passes;
     Stream<F, RB, 1, MatvecItems<G, RB>> stream(items, a.w, a.K, n, smem_u32(dynamic));
     grid_dependency_wait();
@@ -288,43 +288,41 @@ w4_matvec_kernel(MatvecArgs a)
     stream.start();
     stream.run();
     find_splits(splits, n, (a.K + F::kUnit - 1) / F::kUnit);
-    for (int w = 0; w < kSkinnyWarps; ++w) {
+    for (int w = 0; w < F::kWarps; ++w) {
         const int item = splits.item[w];
         if (item < 0)
             continue;
         const int cols = items.cols(item), nb = cols <= 8 ? 1 : 2;
-        for (int v = threadIdx.x; v < 16 * RB * cols; v += kSkinnyThreads) {
+        for (int v = threadIdx.x; v < 16 * RB * cols; v += 32 * F::kWarps) {
             const int r = v % (16 * RB), c = v / (16 * RB);
             items.store(items.col(item) + c, items.row(item) + r,
-                        add_pieces<RB>(splits, dynamic, w, side_index(r >> 4, r & 15, nb, c)));
+                        add_pieces<F, RB>(splits, dynamic, w, side_index(r >> 4, r & 15, nb, c)));
         }
     }
 }
 
 template <int G, int RB>
-int launch_matvec(const MatvecArgs &a, dim3 grid, cudaStream_t stream)
+int launch_matvec(const MatvecArgs &a, int blocks, dim3 grid, cudaStream_t stream)
 {
+    if constexpr (RB > 1) {
+        if (blocks < RB)
+            return launch_matvec<G, RB - 1>(a, blocks, grid, stream);
+    }
+    using F = FormatW4<G, false>;
     static PerDevice set;
-    const int rc = raise_smem(w4_matvec_kernel<G, RB>, Room<RB>::kFixed, set);
+    const int rc = raise_smem(w4_matvec_kernel<G, RB>, Room<F, RB>::kFixed, set);
     if (rc != EP_OK)
         return rc;
-    return launch_dependent(w4_matvec_kernel<G, RB>, grid, kSkinnyThreads, Room<RB>::kFixed, stream, a);
+    return launch_dependent(w4_matvec_kernel<G, RB>, grid, 32 * F::kWarps, Room<F, RB>::kFixed, stream, a);
 }
 
 template <int G>
 int matvec(const MatvecArgs &a, cudaStream_t stream)
 {
+    constexpr int kMost = FormatW4<G, false>::kMaxBlocks;
     const int sms = std::min(device_sm_count(), a.N);
     const dim3 grid(sms, (unsigned)ceil_div(a.M, kMaxPasses * kMaxCols));
-    // a warp takes as many blocks of 16 rows at a time as its block has rows for: each x it loads serves them all
-    const int64_t rows = ceil_div(a.N, sms);
-    const int blocks = (int)ceil_div(rows, 16), at_once = (int)ceil_div(blocks, ceil_div(blocks, 4));
-    switch (at_once) {
-    case 1: return launch_matvec<G, 1>(a, grid, stream);
-    case 2: return launch_matvec<G, 2>(a, grid, stream);
-    case 3: return launch_matvec<G, 3>(a, grid, stream);
-    default: return launch_matvec<G, 4>(a, grid, stream);
-    }
+    return launch_matvec<G, kMost>(a, blocks_at_once(ceil_div(ceil_div(a.N, sms), 16), kMost, true), grid, stream);
 }
 
 bool w4_shape_ok(int64_t N, int64_t K, int group)
