@@ -894,14 +894,18 @@ def _out_code(where: str, dtype) -> int:
     return _OUT_DTYPES[dtype]
 
 
-def _ready(where: str, name: str, t: torch.Tensor, dtype, shape):
-    """The pointer of a contiguous device tensor of this dtype and shape."""
-    if t.dtype != dtype:
+def _ready(where: str, name: str, t: torch.Tensor, dtype, shape, index: Optional[int] = None) -> int:
+    """The pointer of a contiguous device tensor of this dtype, shape and (if
+    given) device index."""
+    if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda:
+    on = t.get_device()
+    if on < 0:
         raise ValueError(f"{where}: {name}: device tensor expected")
+    if index is not None and on != index:
+        raise ValueError(f"{where}: {name} must be on device {index}, got {on}")
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name}: contiguous tensor expected")
     return t.data_ptr()
@@ -923,9 +927,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _raw_stream(stream, device) -> int:
+# the current stream's handle by device index: the attribute look-up of torch.cuda.current_stream costs 2 us
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _raw_stream(stream, index: int) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return _current_raw(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -933,7 +942,7 @@ class W4:
     """A weight matrix [..., N, K] in 4-bit codes (EP_W_INT4 of include/ep.h):
     q [..., N, K/2] uint8 with code 2j of a row in the low half of byte j, scale
     [..., N, K/group] bf16, zero [..., N, K/group] uint8 (0..15) or None for 8."""
-    __slots__ = ("q", "scale", "zero", "group", "shape", "matrix")
+    __slots__ = ("q", "scale", "zero", "group", "shape", "_p")
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor], group: int):
         _expect("W4", q=(q, torch.uint8), scale=(scale, torch.bfloat16), zero=(zero, torch.uint8))
@@ -946,10 +955,19 @@ class W4:
         for t in (q, scale, zero):
             if t is not None and not t.is_contiguous():
                 raise ValueError("W4: contiguous tensor expected")
+            if t is not None and t.device != q.device:
+                raise ValueError("W4: q, scale and zero must be on one device")
+        self._set(q, scale, zero, group)
+
+    def _set(self, q, scale, zero, group):
         self.q, self.scale, self.zero, self.group = q, scale, zero, group
-        self.shape = torch.Size((*q.shape[:-1], K))
-        self.matrix = EPMatrix(q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(), EP_W_INT4,
-                               group)
+        self.shape = torch.Size((*q.shape[:-1], 2 * q.shape[-1]))
+        self._p = (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
+        return self
+
+    @property
+    def matrix(self) -> EPMatrix:
+        return EPMatrix(*self._p, EP_W_INT4, self.group)
 
     def __getitem__(self, i) -> "W4":
         """The i-th matrix of a stack of them."""
@@ -961,29 +979,31 @@ class W4:
 def w4_quantize(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=None) -> W4:
     """4-bit codes of bf16 weights [..., N, K], K % group == 0; zeros: with a zero
     point for each group instead of codes around 8."""
-    if w.dim() < 2:
+    shape = w.shape
+    if len(shape) < 2:
         raise ValueError("w4_quantize: a matrix or a stack of matrices expected")
-    src = _ready("w4_quantize", "w", w, torch.bfloat16, w.shape)
-    K = w.shape[-1]
+    src = _ready("w4_quantize", "w", w, torch.bfloat16, shape)
+    lead, K, dev = shape[:-1], shape[-1], w.device
     if group not in (32, 64, 128) or K % group != 0 or K == 0:
         raise ValueError(f"w4_quantize: group must be 32, 64 or 128 and divide {K}, got {group}")
-    N = w.numel() // K
-    q = _empty((*w.shape[:-1], K // 2), torch.uint8, w.device, stream)
-    s = _empty((*w.shape[:-1], K // group), torch.bfloat16, w.device, stream)
-    z = _empty(s.shape, torch.uint8, w.device, stream) if zeros else None
-    _check(load().ep_w4_quantize(src, N, K, group, q.data_ptr(), s.data_ptr(), None if z is None else z.data_ptr(),
-                                 _raw_stream(stream, w.device)), "w4_quantize")
-    return W4(q, s, z, group)
+    q = _empty((*lead, K // 2), torch.uint8, dev, stream)
+    s = _empty((*lead, K // group), torch.bfloat16, dev, stream)
+    z = _empty((*lead, K // group), torch.uint8, dev, stream) if zeros else None
+    out = W4.__new__(W4)._set(q, s, z, group)
+    _check(load().ep_w4_quantize(src, w.numel() // K, K, group, *out._p, _raw_stream(stream, w.get_device())),
+           "w4_quantize")
+    return out
 
 
 def w4_dequantize(w: W4, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values that 4-bit weights stand for, in the shape of the matrices."""
     code = _out_code("w4_dequantize", out_dtype)
+    if not w.q.is_cuda:
+        raise ValueError("w4_dequantize: w: device tensors expected")
     out = _empty(w.shape, out_dtype, w.q.device, stream)
     K = w.shape[-1]
-    m = w.matrix
-    _check(load().ep_w4_dequantize(m.data, m.scale, m.zero, out.numel() // K, K, w.group, out.data_ptr(), code,
-                                   _raw_stream(stream, w.q.device)), "w4_dequantize")
+    _check(load().ep_w4_dequantize(*w._p, out.numel() // K, K, w.group, out.data_ptr(), code,
+                                   _raw_stream(stream, w.q.get_device())), "w4_dequantize")
     return out
 
 
@@ -992,13 +1012,16 @@ def w4_matvec(x: torch.Tensor, w: W4, out_dtype=torch.bfloat16, stream=None) -> 
     if len(w.shape) != 2:
         raise ValueError("w4_matvec: one matrix expected")
     N, K = w.shape
-    M = x.shape[0] if x.dim() == 2 else 1
-    src = _ready("w4_matvec", "x", x, torch.bfloat16, (M, K) if x.dim() != 1 else (K,))
+    shape = x.shape
+    M = shape[0] if len(shape) == 2 else 1
+    src = _ready("w4_matvec", "x", x, torch.bfloat16, (M, K) if len(shape) != 1 else (K,))
     code = _out_code("w4_matvec", out_dtype)
-    y = _empty((M, N) if x.dim() == 2 else (N,), out_dtype, x.device, stream)
-    m = w.matrix
-    _check(load().ep_w4_matvec(src, M, m.data, m.scale, m.zero, N, K, w.group, y.data_ptr(), code,
-                               _raw_stream(stream, x.device)), "w4_matvec")
+    index = x.get_device()
+    if w.q.get_device() != index:
+        raise ValueError("w4_matvec: x and w must be on one device")
+    y = _empty((M, N) if len(shape) == 2 else (N,), out_dtype, x.device, stream)
+    _check(load().ep_w4_matvec(src, M, *w._p, N, K, w.group, y.data_ptr(), code, _raw_stream(stream, index)),
+           "w4_matvec")
     return y
 
 
@@ -1016,29 +1039,30 @@ class RouterTopk:
             raise ValueError(f"RouterTopk: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
         _expect("RouterTopk", w=(w, (torch.bfloat16, torch.float32)), bias=(bias, torch.float32))
         E, H = w.shape
-        self._wp = _ready("RouterTopk", "w", w, w.dtype, (E, H))
-        self._bp = None if bias is None else _ready("RouterTopk", "bias", bias, torch.float32, (E,))
+        wp = _ready("RouterTopk", "w", w, w.dtype, (E, H))
+        bp = None if bias is None else _ready("RouterTopk", "bias", bias, torch.float32, (E,))
         if not 1 <= topk <= min(E, 32):
             raise ValueError(f"RouterTopk: topk must be 1 .. min(E, 32), got {topk}")
         self.w, self.bias, self.E, self.H, self.topk = w, bias, E, H, topk
         self.scoring, self.renormalize, self.scale, self.max_tokens = scoring, renormalize, float(scale), max_tokens
-        self._tail = (0 if w.dtype == torch.bfloat16 else 1, E, self._bp, topk,
-                      EP_SCORE_SIGMOID if scoring == "sigmoid" else EP_SCORE_SOFTMAX, int(renormalize), self.scale)
         self.ws = torch.empty(max(ep_router_workspace_size(max_tokens, H, E), 256), dtype=torch.uint8, device=w.device)
+        self._mid = (H, wp, 0 if w.dtype == torch.bfloat16 else 1, E, bp, topk,
+                     EP_SCORE_SIGMOID if scoring == "sigmoid" else EP_SCORE_SOFTMAX, int(renormalize), self.scale)
         self._ws = (self.ws.data_ptr(), self.ws.numel())
+        self._index = w.get_device()
 
     def __call__(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None, stream=None):
         """x [T,H] bf16 -> (topk_idx [T,K] int64, topk_weights [T,K] fp32); logits
         [T,E] fp32 receives the logits."""
-        T = x.shape[0]
-        src = _ready("RouterTopk", "x", x, torch.bfloat16, (T, self.H))
+        T, dev = x.shape[0], x.device
+        src = _ready("RouterTopk", "x", x, torch.bfloat16, (T, self.H), self._index)
         if T > self.max_tokens:
             raise ValueError(f"RouterTopk: at most {self.max_tokens} tokens, got {T}")
-        lp = None if logits is None else _ready("RouterTopk", "logits", logits, torch.float32, (T, self.E))
-        idx = _empty((T, self.topk), torch.int64, x.device, stream)
-        wts = _empty((T, self.topk), torch.float32, x.device, stream)
-        _check(load().ep_router_topk(src, T, self.H, self._wp, *self._tail, idx.data_ptr(), wts.data_ptr(), lp,
-                                     *self._ws, _raw_stream(stream, x.device)), "RouterTopk")
+        lp = None if logits is None else _ready("RouterTopk", "logits", logits, torch.float32, (T, self.E), self._index)
+        idx = _empty((T, self.topk), torch.int64, dev, stream)
+        wts = _empty((T, self.topk), torch.float32, dev, stream)
+        _check(load().ep_router_topk(src, T, *self._mid, idx.data_ptr(), wts.data_ptr(), lp, *self._ws,
+                                     _raw_stream(stream, self._index)), "RouterTopk")
         return idx, wts
 
 
@@ -1068,42 +1092,47 @@ class MoeDecode:
         if I2 % 2 != 0 or tuple(w2.shape) != (El, H, I2 // 2):
             raise ValueError(f"MoeDecode: w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not belong together")
         I = I2 // 2
-        if isinstance(w13, W4):
-            self._m13, self._m2, dev = w13.matrix, w2.matrix, w13.q.device
-        else:
-            self._m13 = EPMatrix(_ready("MoeDecode", "w13", w13, torch.bfloat16, (El, I2, H)), None, None, EP_W_BF16, 0)
-            self._m2 = EPMatrix(_ready("MoeDecode", "w2", w2, torch.bfloat16, (El, H, I)), None, None, EP_W_BF16, 0)
-            dev = w13.device
-        E = El if num_experts is None else int(num_experts)
         if topk < 1 or max_tokens * topk > EP_MOE_MAX_SLOTS:
             raise ValueError(f"MoeDecode: max_tokens * topk must be at most {EP_MOE_MAX_SLOTS}")
+        if isinstance(w13, W4):
+            if not w13.q.is_cuda or w2.q.device != w13.q.device:
+                raise ValueError("MoeDecode: w13 and w2: tensors of one device expected")
+            self._m13, self._m2, on = w13.matrix, w2.matrix, w13.q
+        else:
+            self._m13 = EPMatrix(_ready("MoeDecode", "w13", w13, torch.bfloat16, (El, I2, H)), None, None, EP_W_BF16, 0)
+            self._m2 = EPMatrix(_ready("MoeDecode", "w2", w2, torch.bfloat16, (El, H, I), w13.get_device()), None, None,
+                                EP_W_BF16, 0)
+            on = w13
+        E = El if num_experts is None else int(num_experts)
         self.w13, self.w2, self.E, self.E_local, self.H, self.I = w13, w2, E, El, H, I
         self.rank, self.topk, self.max_tokens, self.out_dtype = rank, topk, max_tokens, out_dtype
         self._code = _out_code("MoeDecode", out_dtype)
-        self.err = error_word(dev)
+        self.err = error_word(on.device)
         if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream(dev).synchronize()   # the word is clear before a call on any stream
-        self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, H, I), 256), dtype=torch.uint8, device=dev)
-        self._mid = (H, I, E, El, rank, ctypes.addressof(self._m13), ctypes.addressof(self._m2))
+            torch.cuda.current_stream(on.device).synchronize()   # the word is clear before a call on any stream
+        self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, H, I), 256), dtype=torch.uint8,
+                              device=on.device)
+        self._mid = (topk, H, I, E, El, rank, ctypes.addressof(self._m13), ctypes.addressof(self._m2))
         self._ws = (self.ws.data_ptr(), self.ws.numel())
+        self._index = on.get_device()
 
     def __call__(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, out=None, err=None,
                  stream=None) -> torch.Tensor:
         """x [T,H] bf16, topk_idx [T,topk] int64, topk_weights [T,topk] fp32 -> this rank's
         partial [T,H].  Device errors go to err (default: this object's err)."""
-        T, K = x.shape[0], self.topk
-        xp = _ready("MoeDecode", "x", x, torch.bfloat16, (T, self.H))
-        ip = _ready("MoeDecode", "topk_idx", topk_idx, torch.int64, (T, K))
-        wp = _ready("MoeDecode", "topk_weights", topk_weights, torch.float32, (T, K))
+        T, index = x.shape[0], self._index
+        xp = _ready("MoeDecode", "x", x, torch.bfloat16, (T, self.H), index)
+        ip = _ready("MoeDecode", "topk_idx", topk_idx, torch.int64, (T, self.topk), index)
+        wp = _ready("MoeDecode", "topk_weights", topk_weights, torch.float32, (T, self.topk), index)
         if T > self.max_tokens:
             raise ValueError(f"MoeDecode: at most {self.max_tokens} tokens, got {T}")
         if out is None:
             out = _empty((T, self.H), self.out_dtype, x.device, stream)
             op = out.data_ptr()
         else:
-            op = _ready("MoeDecode", "out", out, self.out_dtype, (T, self.H))
-        _check(load().ep_moe_decode(xp, ip, wp, T, K, *self._mid, op, self._code, *self._ws,
-                                    (self.err if err is None else err).data_ptr(), _raw_stream(stream, x.device)),
+            op = _ready("MoeDecode", "out", out, self.out_dtype, (T, self.H), index)
+        _check(load().ep_moe_decode(xp, ip, wp, T, *self._mid, op, self._code, *self._ws,
+                                    (self.err if err is None else err).data_ptr(), _raw_stream(stream, index)),
                "MoeDecode")
         return out
 

@@ -593,7 +593,7 @@ int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const void *scale, 
  *   ws: ep_router_workspace_size(T, H, E) bytes, 256-byte aligned, scratch.
  *     Calls that overlap on the GPU must not share it.
  * The same call on the same inputs gives the same bits.
- * 1 <= K <= min(E, 32), E <= 8192. */
+ * 1 <= K <= min(E, 32), E <= 8192, T <= 2^20. */
 #define EP_SCORE_SOFTMAX 0
 #define EP_SCORE_SIGMOID 1
 size_t ep_router_workspace_size(int64_t T, int H, int E);

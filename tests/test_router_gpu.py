@@ -159,3 +159,15 @@ def test_another_stream_and_graph():
     torch.cuda.synchronize()
     want = r(x)
     assert torch.equal(idx, want[0]) and torch.equal(wts, want[1])
+
+
+@pytest.mark.parametrize("E", [17, 64, 256, 1000])
+def test_one_workspace_serves_every_smaller_batch(E):
+    g = f.gen(4)
+    w = f.randn((E, 2048), g, 2048 ** -0.5)
+    r = ep.RouterTopk(w, 2, max_tokens=300)
+    x = f.randn((300, 2048), g)
+    for T in (1, 7, 8, 9, 16, 17, 31, 32, 33, 64, 100, 152, 153, 200, 299, 300):
+        assert r(x[:T])[0].shape == (T, 2)
+    sizes = [ep.ep_router_workspace_size(T, 2048, E) for T in range(1, 400)]
+    assert sizes == sorted(sizes)
