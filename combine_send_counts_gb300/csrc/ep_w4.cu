@@ -16,10 +16,9 @@ constexpr int kThreads = 256;
 
 // ----------------------------------------------------- quantise, read back --
 // Both are bound by HBM (2.5 bytes a weight and the scales); what matters is
-// that the arithmetic between stays under it, about a dozen instructions per
-// weight.  A lane holds 8 consecutive weights; G/8 neighbouring lanes share a
-// group and find its extremes with shuffles of bf16 pairs.  kVectors
-// independent 16-byte loads per lane keep enough in flight.
+// that the arithmetic between stays under it.  A lane holds 8 consecutive
+// weights of kVectors groups; G/8 neighbouring lanes share a group and find its
+// extremes with shuffles of bf16 pairs.
 constexpr int kVectors = 4;
 
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b)   // NaN if either is
@@ -40,21 +39,36 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
 constexpr float kRound = 12582912.0f;
 constexpr uint32_t kRoundBits = 0x4b400000u;
 
-// rint(w / s) for bf16 values w and s whose quotient is small, s normal and rs
-// = 1/s to nearest.  The first guess c = rint(w * rs) can differ from the
-// rounded quotient at ties only: w / s, a ratio of two 8-bit significands, is
-// either a tie or at least 2^-11 away from one, and w * rs is off by 2^-20 at
-// most.  The remainder w - c*s is exact (5 + 8 bits), so a tie shows as a
-// remainder of s/2; there an odd c moves to its even neighbour on w's side.
-// Returns the integer added to kRoundBits.
-__device__ __forceinline__ uint32_t round_quotient(float w, float s, float rs)
+// rint(w / s) + kRound of two weights.  With rs the correctly rounded 1/s, q0 = w * rs and the exact remainder r =
+// w - q0 * s, q0 + r * rs rounds to the correctly rounded quotient (Markstein, 1990), so that ties are exact and go
+// to even.  Two per instruction.
+__device__ __forceinline__ float2 round_quotients(float2 w, float s, float rs)
 {
-    const float t = __fmaf_rn(w, rs, kRound);
-    const float c = __fsub_rn(t, kRound), d = __fmaf_rn(-c, s, w);
-    uint32_t n = __float_as_uint(t);
-    if (__fadd_rn(fabsf(d), fabsf(d)) == s && (n & 1))
-        n += d > 0.0f ? 1 : -1;
-    return n;
+    const float2 rs2 = make_float2(rs, rs);
+    const float2 q0 = mul2_rn(w, rs2);
+    const float2 r = fma2_rn(q0, make_float2(-s, -s), w);
+    const float2 q = fma2_rn(r, rs2, q0);
+    return fma2_rn(q, make_float2(1.0f, 1.0f), make_float2(kRound, kRound));
+}
+
+// a group's scale, its reciprocal (0: the codes take the slow way) and its zero point
+struct GroupScale {
+    float s, rs, z;
+};
+
+template <bool ZERO>
+__device__ __forceinline__ GroupScale group_scale(float least, float most)   // NaN where the group holds one
+{
+    const bool finite = isfinite(least) && isfinite(most);
+    const float lo = fminf(least, 0.0f), hi = fmaxf(most, 0.0f);
+    const float wide = ZERO ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+    GroupScale g;
+    g.s = __bfloat162float(__float2bfloat16_rn(finite ? wide : __int_as_float(0x7f800000)));
+    const bool plain = finite && g.s > 0.0f;
+    g.z = ZERO ? (plain ? fminf(fmaxf(rintf(__fdiv_rn(-lo, g.s)), 0.0f), 15.0f) : 0.0f) : 8.0f;
+    // where nothing above over- or underflows
+    g.rs = finite && g.s >= 7.9e-31f && g.s <= 1.2e30f ? __fdiv_rn(1.0f, g.s) : 0.0f;
+    return g;
 }
 
 template <int G, bool ZERO>
@@ -63,65 +77,75 @@ w4_quantize_kernel(const uint4 *__restrict__ w, int64_t vectors, uint32_t *__res
                    __nv_bfloat16 *__restrict__ scale, uint8_t *__restrict__ zero)
 {
     constexpr int kLanes = G / 8;
+    static_assert(kVectors == 4 && kLanes % kVectors == 0, "a lane of each group for each of a lane's groups");
     const int64_t first = (int64_t)blockIdx.x * (kThreads * kVectors) + threadIdx.x;
+    const int lane = threadIdx.x & 31;
     grid_dependency_wait();
     allow_dependents();
     uint4 v[kVectors];
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i)
-        if (first + i * kThreads < vectors)
+    for (int i = 0; i < kVectors; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (first + i * kThreads < vectors)   // a group's lanes are in or out together
             v[i] = ld_stream(w + first + i * kThreads);
+    }
+    uint32_t lo2[kVectors], hi2[kVectors];
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) {
-        const int64_t at = first + i * kThreads;
-        // a group's lanes are in or out together (K is a multiple of G)
-        const unsigned in = __ballot_sync(kFull, at < vectors);
-        if (at >= vectors)
-            return;
-        const uint32_t p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t lo2 = p[0], hi2 = p[0];
-#pragma unroll
-        for (int j = 1; j < 4; ++j) {
-            lo2 = min_bf16x2(lo2, p[j]);
-            hi2 = max_bf16x2(hi2, p[j]);
-        }
+        lo2[i] = min_bf16x2(min_bf16x2(v[i].x, v[i].y), min_bf16x2(v[i].z, v[i].w));
+        hi2[i] = max_bf16x2(max_bf16x2(v[i].x, v[i].y), max_bf16x2(v[i].z, v[i].w));
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) {
-            lo2 = min_bf16x2(lo2, __shfl_xor_sync(in, lo2, o));
-            hi2 = max_bf16x2(hi2, __shfl_xor_sync(in, hi2, o));
+            lo2[i] = min_bf16x2(lo2[i], __shfl_xor_sync(kFull, lo2[i], o));
+            hi2[i] = max_bf16x2(hi2[i], __shfl_xor_sync(kFull, hi2[i], o));
         }
-        lo2 = min_bf16x2(lo2, __byte_perm(lo2, lo2, 0x1032));
-        hi2 = max_bf16x2(hi2, __byte_perm(hi2, hi2, 0x1032));
-        const bool finite = isfinite(bf16_lo(lo2)) && isfinite(bf16_lo(hi2));
-        const float lo = fminf(bf16_lo(lo2), 0.0f), hi = fmaxf(bf16_lo(hi2), 0.0f);
-        const float wide = ZERO ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
-        const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? wide : __int_as_float(0x7f800000));
-        const float s = __bfloat162float(sb);
-        const bool plain = finite && s > 0.0f;
-        const float z = ZERO ? (plain ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f) : 0.0f) : 8.0f;
+    }
+    // the divisions: lane i of each four for the lane's i-th group
+    const int mine = lane & 3;
+    uint32_t l2 = mine & 2 ? (mine & 1 ? lo2[3] : lo2[2]) : (mine & 1 ? lo2[1] : lo2[0]);
+    uint32_t h2 = mine & 2 ? (mine & 1 ? hi2[3] : hi2[2]) : (mine & 1 ? hi2[1] : hi2[0]);
+    l2 = min_bf16x2(l2, __byte_perm(l2, l2, 0x1032));
+    h2 = max_bf16x2(h2, __byte_perm(h2, h2, 0x1032));
+    const GroupScale own = group_scale<ZERO>(bf16_lo(l2), bf16_lo(h2));
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+        const int from = (lane & 28) | i;
+        GroupScale g;
+        g.s = __shfl_sync(kFull, own.s, from);
+        g.rs = __shfl_sync(kFull, own.rs, from);
+        g.z = ZERO ? __shfl_sync(kFull, own.z, from) : 8.0f;
+        const int64_t at = first + i * kThreads;
+        if (at >= vectors)
+            continue;
         if (threadIdx.x % kLanes == 0) {
-            scale[at / kLanes] = sb;
+            scale[at / kLanes] = __float2bfloat16_rn(g.s);
             if (ZERO)
-                zero[at / kLanes] = (uint8_t)z;
+                zero[at / kLanes] = (uint8_t)g.z;
         }
-        const int zi = (int)z;
-        uint32_t code[8];
-        if (s >= 1.1754944e-38f && finite) {
-            const float rs = __fdiv_rn(1.0f, s);
+        const uint32_t p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t out = 0;
+        if (g.rs != 0.0f) {
+            // codes as integers added to kRoundBits; only zero points can push one out of range (|w| / s <= 7.03)
+            const float least = kRound - g.z, most = kRound + 15.0f - g.z;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                code[j] = round_quotient(j & 1 ? bf16_hi(p[j >> 1]) : bf16_lo(p[j >> 1]), s, rs) - kRoundBits + zi;
-        } else {   // no scale, or one so small that its reciprocal overflows
+            for (int j = 3; j >= 0; --j) {
+                float2 t = round_quotients(make_float2(bf16_lo(p[j]), bf16_hi(p[j])), g.s, g.rs);
+                if (ZERO)
+                    t = make_float2(fminf(fmaxf(t.x, least), most), fminf(fmaxf(t.y, least), most));
+                out = out * 16 + __float_as_uint(t.y);
+                out = out * 16 + __float_as_uint(t.x);
+            }
+            // sum of (kRoundBits - z) * 16^j modulo 2^32; kRoundBits ends in 22 zeros
+            out += (uint32_t)(int)g.z * 0x11111111u - kRoundBits * 0x11111111u;
+        } else {   // no scale, or one out of the range of the above
+            const bool plain = g.s > 0.0f && g.s < __int_as_float(0x7f800000);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 7; j >= 0; --j) {
                 const float x = j & 1 ? bf16_hi(p[j >> 1]) : bf16_lo(p[j >> 1]);
-                code[j] = (plain ? (int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -64.0f), 64.0f) : 0) + zi;
+                const float r = plain ? fminf(fmaxf(rintf(__fdiv_rn(x, g.s)), -64.0f), 64.0f) : 0.0f;
+                out = out << 4 | (uint32_t)fminf(fmaxf(__fadd_rn(r, g.z), 0.0f), 15.0f);
             }
         }
-        uint32_t out = 0;
-#pragma unroll
-        for (int j = 7; j >= 0; --j)
-            out = out << 4 | (uint32_t)min(max((int)code[j], 0), 15);
         q[at] = out;
     }
 }
