@@ -78,6 +78,7 @@ struct Lists {
     uint16_t slot[kMaxSlots];
     int16_t use[kMaxSlots];           // slot -> its entry, or -1
     uint16_t place[kMaxSlots];        // slot -> its place among its expert's slots
+    float weight[kMaxSlots];          // down: the slots' weights
     uint16_t big_expert[kMaxSlots / kMaxCols];   // experts of more than one entry
 };
 
@@ -296,8 +297,8 @@ struct Cut {
     __device__ __forceinline__ explicit Cut(int n)
     {
         const int blocks = (n + 7) / 8, most = (blocks + RB - 1) / RB;
-        size = most > 0 ? (blocks + most - 1) / most * 8 : 8;
-        items = (n + size - 1) / size;
+        size = most > 1 ? quick_div(blocks + most - 1, most) * 8 : 8 * RB;
+        items = most > 1 ? quick_div(n + size - 1, size) : most;
     }
 };
 
@@ -344,12 +345,12 @@ struct UpItems {
         if (item >= head_items) {
             const int q1 = l.entry[j0 + 1];
             v -= head_items;
-            j = l.owner[q1 + v / body.items];
+            j = l.owner[q1 + quick_div(v, body.items)];
             v -= body.items * (l.entry[j] - q1);
             i = 0;
             size = j == j1 ? tail.size : body.size;
         }
-        const int n = passes(j), block = n == 1 ? v : v / n;
+        const int n = passes(j), block = n == 1 ? v : quick_div(v, n);
         i += block * size;
         q = l.entry[j] + v - block * n;
         end = min(i + size, j == j1 ? i1 : a.I);
@@ -404,12 +405,14 @@ struct UpItems {
     }
 };
 
-// The expert and element where block b's share of the costs laid end to end
-// begins.  (At most 2 * kMaxSlots * kMaxDim = 2^27 in all.)
-__device__ __forceinline__ void share_begin(const Lists &l, int I, int b, int blocks, int &j, int &i)
+// The expert and element where the shares of blocks b and b + 1 of the costs
+// laid end to end begin, by lanes 0 and 1 of every warp.  (At most 2 *
+// kMaxSlots * kMaxDim = 2^27 in all.)
+__device__ __forceinline__ void share(const Lists &l, int I, int b, int blocks, int &j0, int &i0, int &j1, int &i1)
 {
-    const int total = l.cost[l.experts] * I;
-    const int pos = total / blocks * b + min(b, total % blocks);
+    const int total = l.cost[l.experts] * I, each = quick_div(total, blocks), rest = total - each * blocks;
+    b += threadIdx.x & 1;
+    const int pos = each * b + min(b, rest);
     int lo = 0, hi = l.experts;   // cost[lo] * I <= pos < cost[hi] * I
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -418,8 +421,16 @@ __device__ __forceinline__ void share_begin(const Lists &l, int I, int b, int bl
         else
             hi = mid;
     }
-    j = lo;
-    i = (pos - l.cost[lo] * I) / (l.cost[lo + 1] - l.cost[lo]);
+    const int at = l.cost[lo], cost = l.cost[lo + 1] - at;
+    int i = quick_div(pos - at * I, cost);
+    if (b == blocks) {
+        lo = l.experts;
+        i = 0;
+    }
+    j0 = __shfl_sync(kFull, lo, 0);
+    i0 = __shfl_sync(kFull, i, 0);
+    j1 = __shfl_sync(kFull, lo, 1);
+    i1 = __shfl_sync(kFull, i, 1);
 }
 
 template <int G, int RB>
@@ -429,7 +440,7 @@ moe_up_kernel(UpArgs a)
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
     __shared__ Lists l;
     using F = typename FormatOf<G, false>::F;
-    __shared__ Splits<F> splits;
+    __shared__ int begins[F::kWarps + 1];
     grid_dependency_wait();
     allow_dependents();
     build_lists<F::kWarps>(a.r, l, reinterpret_cast<int *>(dynamic), blockIdx.x == 0 ? a.err : nullptr);
@@ -437,10 +448,8 @@ moe_up_kernel(UpArgs a)
         return;
     const int warp = threadIdx.x >> 5;
     uint8_t *sides = dynamic + Room<F, RB>::kRing;
-    int j0, i0, j1 = l.experts, i1 = 0;
-    share_begin(l, a.I, blockIdx.x, gridDim.x, j0, i0);
-    if (blockIdx.x + 1 < gridDim.x)
-        share_begin(l, a.I, blockIdx.x + 1, gridDim.x, j1, i1);
+    int j0, i0, j1, i1;
+    share(l, a.I, blockIdx.x, gridDim.x, j0, i0, j1, i1);
     UpItems<G, RB> items(a, l, j0, i0, j1, i1);
     items.side = reinterpret_cast<float *>(sides + warp * Room<F, RB>::kSide);
     items.open = reinterpret_cast<float *>(dynamic + warp * Room<F, RB>::kWarpRing);   // the ring is idle by then
@@ -450,19 +459,17 @@ moe_up_kernel(UpArgs a)
     Stream<F, RB, 1, UpItems<G, RB>> stream(items, a.w, a.H, n, smem_u32(dynamic));
     stream.start();
     stream.run();
-    find_splits(splits, n, (a.H + F::kUnit - 1) / F::kUnit);
-    for (int w = 0; w < F::kWarps; ++w) {
-        if (splits.item[w] < 0)
-            continue;
+    stream.meet(begins);
+    if (stream.open_item >= 0) {
         int q, j, i, stop;
-        items.where(splits.item[w], q, j, i, stop);
+        items.where(stream.open_item, q, j, i, stop);
         const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
-        for (int v = threadIdx.x; v < 8 * RB * cols; v += 32 * F::kWarps) {
+        for (int v = threadIdx.x & 31; v < 8 * RB * cols; v += 32) {
             const int e = v % (8 * RB), c = v / (8 * RB);
             if (i + e < stop)
                 store_planes<(G > 0)>(a.out, l.slot[first + c], i + e,
-                                      activate(add_pieces<F, RB>(splits, dynamic, w, side_index(e >> 3, e & 7, nb, c)),
-                                               add_pieces<F, RB>(splits, dynamic, w, side_index(e >> 3, (e & 7) + 8, nb, c))));
+                                      activate(stream.add_pieces(begins, dynamic, side_index(e >> 3, e & 7, nb, c)),
+                                               stream.add_pieces(begins, dynamic, side_index(e >> 3, (e & 7) + 8, nb, c))));
         }
     }
 }
@@ -548,8 +555,10 @@ moe_down_kernel(DownArgs a)
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, one side block per warp, y if it fits
     __shared__ Lists l;
     using F = typename FormatOf<G, (G > 0)>::F;
-    __shared__ Splits<F> splits;
+    __shared__ int begins[F::kWarps + 1];
     // topk_idx was complete before the up kernel began; h is complete after the wait
+    for (int s = threadIdx.x; s < a.r.n; s += 32 * F::kWarps)
+        l.weight[s] = a.weights[s];
     build_lists<F::kWarps>(a.r, l, reinterpret_cast<int *>(dynamic), nullptr);
     const int warp = threadIdx.x >> 5;
     uint8_t *sides = dynamic + Room<F, RB>::kRing;
@@ -567,17 +576,15 @@ moe_down_kernel(DownArgs a)
     grid_dependency_wait();
     allow_dependents();
     stream.run();
-    find_splits(splits, n, (a.I + F::kUnit - 1) / F::kUnit);
-    for (int w = 0; w < F::kWarps; ++w) {
-        if (splits.item[w] < 0)
-            continue;
-        const int b = splits.item[w] / l.entries, q = splits.item[w] - b * l.entries;
+    stream.meet(begins);
+    if (stream.open_item >= 0) {
+        const int b = stream.open_item / l.entries, q = stream.open_item - b * l.entries;
         const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
-        for (int v = threadIdx.x; v < 16 * RB * cols; v += 32 * F::kWarps) {
+        for (int v = threadIdx.x & 31; v < 16 * RB * cols; v += 32) {
             const int r = v % (16 * RB), c = v / (16 * RB), i = b * (16 * RB) + r;
             if (i < rows)
                 items.y[(int64_t)l.slot[first + c] * items.stride + i] =
-                    add_pieces<F, RB>(splits, dynamic, w, side_index(r >> 4, r & 15, nb, c));
+                    stream.add_pieces(begins, dynamic, side_index(r >> 4, r & 15, nb, c));
         }
     }
     __syncthreads();
@@ -587,7 +594,7 @@ moe_down_kernel(DownArgs a)
         for (int k = 0; k < a.r.K; ++k) {
             const int slot = tok * a.r.K + k;
             if (l.use[slot] >= 0)
-                sum = __fmaf_rn(a.weights[slot], items.y[(int64_t)slot * items.stride + i], sum);
+                sum = __fmaf_rn(l.weight[slot], items.y[(int64_t)slot * items.stride + i], sum);
         }
         const int64_t o = (int64_t)tok * a.H + items.row0 + i;
         if (a.out_f32)
@@ -598,7 +605,7 @@ moe_down_kernel(DownArgs a)
 }
 
 // ------------------------------------------------------------ launch policy --
-constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - sizeof(Splits<FormatW4<128, false>>) - 64;   // dynamic shared memory of a block that owns an SM
+constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - (kMostWarps + 1) * sizeof(int) - 64;   // dynamic shared memory of a block that owns an SM
 
 template <int G, int RB>
 int launch_up(const UpArgs &a, int64_t elements, cudaStream_t stream)

@@ -47,6 +47,17 @@ struct Room {
     static_assert(kUnits >= 1 && kSide <= kWarpRing, "the ring holds a unit, and kept sums after the run");
 };
 
+// n / d for 0 <= n < 2^27, 0 < d and a quotient below 2^22, by a float reciprocal put right by the remainder: a third
+// of the general division's latency, of which the kernels' prologues had a microsecond.
+__device__ __forceinline__ int quick_div(int n, int d)
+{
+    int q = (int)(__int2float_rz(n) * __frcp_rz(__int2float_rn(d)));
+    int r = n - q * d;
+    q += r >= d ? 1 : r < 0 ? -1 : 0;
+    r = n - q * d;
+    return q + (r >= d ? 1 : r < 0 ? -1 : 0);
+}
+
 // D += A (16x16, row) * B (16x8, col), bf16 in, fp32 sums.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
@@ -408,7 +419,7 @@ public:
         put_ = ring + warp * Room<F, RB>::kWarpRing + row * F::kRowPiece + (piece ^ ((row & 1) << 2)) * 16;
         get_ = ring + warp * Room<F, RB>::kWarpRing + g_ * F::kRowPiece + (g_ & 1) * 64 + t_ * 16;
         left_ = end_ - begin_;
-        item_ahead_ = first_item_ = begin_ / per_;
+        item_ahead_ = first_item_ = quick_div(begin_, per_);
         u_ahead_ = begin_ - item_ahead_ * per_;
         slot_ahead_ = slot_ = 0;
         fresh_ = true;
@@ -428,8 +439,11 @@ public:
     __device__ __forceinline__ void run()
     {
         int item = first_item_, u0 = begin_ - item * per_, left = end_ - begin_;
+        open_item = -1;
         while (left > 0) {
             const int u1 = min(per_, u0 + left);
+            if (u0 == 0 && u1 < per_)
+                open_item = item;
             if (items_.cols(item) <= 8)
                 piece<1>(item, u0, u1);
             else
@@ -439,6 +453,39 @@ public:
             u0 = 0;
         }
     }
+
+    // All threads, after their run: holds a barrier, after which the kept pieces may be read.  begins: F::kWarps + 1
+    // ints of shared memory.
+    __device__ __forceinline__ void meet(int *begins)
+    {
+        if ((threadIdx.x & 31) == 0) {
+            const int warp = threadIdx.x >> 5;
+            begins[warp] = begin_;
+            if (warp == F::kWarps - 1)
+                begins[F::kWarps] = end_;
+        }
+        __syncthreads();
+        // warps 1 + this one .. last_ - 1 went on with the item that it began
+        int last = (threadIdx.x >> 5) + 1;
+        const int stop = (open_item + 1) * per_;
+        while (last < F::kWarps && begins[last] < stop)
+            ++last;
+        last_ = last;
+    }
+
+    // The sum at place `at` of the item that this warp began and others went on with: the pieces in the order of K.
+    // `dynamic`: the ring, whose warps' parts hold the pieces that begin an item, then the side blocks.
+    __device__ __forceinline__ float add_pieces(const int *begins, const uint8_t *dynamic, int at) const
+    {
+        const int warp = threadIdx.x >> 5;
+        float v = reinterpret_cast<const float *>(dynamic + warp * Room<F, RB>::kWarpRing)[at];
+        for (int o = warp + 1; o < last_; ++o)
+            if (begins[o] < begins[o + 1])
+                v = __fadd_rn(v, reinterpret_cast<const float *>(dynamic + Room<F, RB>::kRing + o * Room<F, RB>::kSide)[at]);
+        return v;
+    }
+
+    int open_item;   // the item that this warp's run began and did not finish, or -1
 
 private:
     // moves on to the next unit to copy
@@ -538,65 +585,12 @@ private:
     const Items &items_;
     const Weights &w_;
     int K_, per_, g_, t_;
-    int begin_, end_, left_, first_item_, item_ahead_, u_ahead_;
+    int begin_, end_, last_, left_, first_item_, item_ahead_, u_ahead_;
     int slot_ahead_, slot_, off_;
     uint32_t put_, get_;
     const uint8_t *pa_, *pb_;
     int n_, m_;
     bool fresh_, live_;
 };
-
-// The first unit of warp w's run (see Stream), for whoever adds up the pieces.
-template <class F>
-__device__ __forceinline__ int run_begin(int n_items, int per, int w)
-{
-    return (int)((int64_t)n_items * per * w / F::kWarps);
-}
-
-// The items of a block that are divided among warps: item[w] is the one that
-// warp w began and did not finish (-1: none); it kept its piece at the start of
-// its ring, which is idle by then, and warps w+1 .. end[w]-1 kept theirs in
-// their side blocks (those with work).
-template <class F>
-struct Splits {
-    int item[F::kWarps], end[F::kWarps];
-    unsigned busy;      // bit w: warp w had work
-};
-
-// All threads, after their run; holds a barrier, after which the kept pieces
-// may be read.
-template <class F>
-__device__ __forceinline__ void find_splits(Splits<F> &s, int n_items, int per)
-{
-    const int w = threadIdx.x;
-    if (w < 32) {
-        const int begin = run_begin<F>(n_items, per, min(w, F::kWarps)), end = run_begin<F>(n_items, per, min(w + 1, F::kWarps));
-        const unsigned busy = __ballot_sync(kFull, begin < end);
-        if (w < F::kWarps) {
-            const int item = end > 0 ? (end - 1) / per : 0;
-            const bool open = begin < end && item * per >= begin && (item + 1) * per > end;
-            int last = w + 1;
-            while (open && last < F::kWarps && run_begin<F>(n_items, per, last) < (item + 1) * per)
-                ++last;
-            s.item[w] = open ? item : -1;
-            s.end[w] = last;
-        }
-        if (w == 0)
-            s.busy = busy;
-    }
-    __syncthreads();
-}
-
-// The sum at place `at` of the item that warp w began: its pieces in the order
-// of K.  `dynamic`: the ring, then the side blocks.
-template <class F, int RB>
-__device__ __forceinline__ float add_pieces(const Splits<F> &s, const uint8_t *dynamic, int w, int at)
-{
-    float v = reinterpret_cast<const float *>(dynamic + w * Room<F, RB>::kWarpRing)[at];
-    for (int o = w + 1; o < s.end[w]; ++o)
-        if (s.busy >> o & 1)
-            v = __fadd_rn(v, reinterpret_cast<const float *>(dynamic + Room<F, RB>::kRing + o * Room<F, RB>::kSide)[at]);
-    return v;
-}
 
 }  // namespace ep

@@ -295,8 +295,8 @@ w4_matvec_kernel(MatvecArgs a)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
     using F = FormatW4<G, false>;
-    __shared__ Splits<F> splits;
-    const int warp = threadIdx.x >> 5;
+    __shared__ int begins[F::kWarps + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *sides = dynamic + Room<F, RB>::kRing;
     MatvecItems<G, RB> items{a};
     items.row0 = (int)((int64_t)a.N * blockIdx.x / gridDim.x);
@@ -311,16 +311,14 @@ w4_matvec_kernel(MatvecArgs a)
     allow_dependents();
     stream.start();
     stream.run();
-    find_splits(splits, n, (a.K + F::kUnit - 1) / F::kUnit);
-    for (int w = 0; w < F::kWarps; ++w) {
-        const int item = splits.item[w];
-        if (item < 0)
-            continue;
+    stream.meet(begins);
+    const int item = stream.open_item;
+    if (item >= 0) {
         const int cols = items.cols(item), nb = cols <= 8 ? 1 : 2;
-        for (int v = threadIdx.x; v < 16 * RB * cols; v += 32 * F::kWarps) {
+        for (int v = lane; v < 16 * RB * cols; v += 32) {
             const int r = v % (16 * RB), c = v / (16 * RB);
             items.store(items.col(item) + c, items.row(item) + r,
-                        add_pieces<F, RB>(splits, dynamic, w, side_index(r >> 4, r & 15, nb, c)));
+                        stream.add_pieces(begins, dynamic, side_index(r >> 4, r & 15, nb, c)));
         }
     }
 }
