@@ -5,7 +5,9 @@
 
 namespace ep {
 
-// Allows `kernel` up to smem bytes of dynamic shared memory on the current device.
+// Allows `kernel` up to smem bytes of dynamic shared memory on the current
+// device.  smem is the same in every call for one kernel, so that concurrent
+// first calls cannot lower it.
 template <class Kernel>
 inline int raise_smem(Kernel kernel, size_t smem, PerDevice &set)
 {

@@ -634,7 +634,7 @@ int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
         smem += y;
         a.y = nullptr;
     }
-    const int rc = raise_smem(moe_down_kernel<G, PLANES, RB>, smem, set);
+    const int rc = raise_smem(moe_down_kernel<G, PLANES, RB>, kMaxSmem, set);
     if (rc != EP_OK)
         return rc;
     return launch_dependent(moe_down_kernel<G, PLANES, RB>, grid, 32 * F::kWarps, smem, stream, a);

@@ -101,7 +101,7 @@ router_logits_kernel(LogitsArgs a)
 {
     __shared__ __align__(16) float red[kWarps][RB * NT * 32 * 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int e0 = blockIdx.x * (16 * RB), t0 = blockIdx.y * (8 * NT), z = blockIdx.z;
+    const int t0 = blockIdx.x * (8 * NT), e0 = blockIdx.y * (16 * RB), z = blockIdx.z;
     const int units = (a.H + kUnit - 1) / kUnit, parts = a.slices * kWarps, part = z * kWarps + warp;
     const int u0 = (int)((int64_t)units * part / parts), u1 = (int)((int64_t)units * (part + 1) / parts);
     const int64_t row_bytes = (int64_t)a.H * (TERMS == 1 ? 2 : 4);
@@ -300,16 +300,12 @@ int slices_of(int64_t T, int H, int E)
 template <int TERMS>
 int launch_logits(const LogitsArgs &a, cudaStream_t stream)
 {
+    const unsigned e16 = (unsigned)ceil_div(a.E, 16), e64 = (unsigned)ceil_div(a.E, 64), t16 = (unsigned)ceil_div(a.T, 16);
     if (a.T <= 8)
-        return launch_dependent(router_logits_kernel<TERMS, 1, 1>, dim3((unsigned)ceil_div(a.E, 16), 1, a.slices),
-                                kThreads, 0, stream, a);
+        return launch_dependent(router_logits_kernel<TERMS, 1, 1>, dim3(1, e16, a.slices), kThreads, 0, stream, a);
     if (a.T <= kFewTokens)
-        return launch_dependent(router_logits_kernel<TERMS, 1, 2>,
-                                dim3((unsigned)ceil_div(a.E, 16), (unsigned)ceil_div(a.T, 16), a.slices), kThreads, 0,
-                                stream, a);
-    return launch_dependent(router_logits_kernel<TERMS, 4, 2>,
-                            dim3((unsigned)ceil_div(a.E, 64), (unsigned)ceil_div(a.T, 16), a.slices), kThreads, 0,
-                            stream, a);
+        return launch_dependent(router_logits_kernel<TERMS, 1, 2>, dim3(t16, e16, a.slices), kThreads, 0, stream, a);
+    return launch_dependent(router_logits_kernel<TERMS, 4, 2>, dim3(t16, e64, a.slices), kThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -351,7 +347,7 @@ extern "C" int ep_router_topk(const void *x, int64_t T, int H, const void *w, in
     const size_t smem = 2 * (size_t)E * sizeof(float);
     static PerDevice set;
     if (smem > 48 * 1024) {
-        const int rs = raise_smem(router_select_kernel, smem, set);
+        const int rs = raise_smem(router_select_kernel, 2 * EP_MAX_EXPERTS * sizeof(float), set);
         if (rs != EP_OK)
             return rs;
     }

@@ -415,7 +415,7 @@ extern "C" int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const vo
         return EP_ERR_INVALID_ARG;
     // a block's units of work are counted in 32 bits
     const int64_t units = ceil_div(N, (int64_t)16 * device_sm_count()) * kMaxPasses * ceil_div(K, 256);
-    if (M >= ((int64_t)1 << 20) || N >= ((int64_t)1 << 31) || K >= ((int64_t)1 << 25) || units >= ((int64_t)1 << 30))
+    if (M >= ((int64_t)1 << 20) || N >= ((int64_t)1 << 31) || K >= ((int64_t)1 << 25) || units >= ((int64_t)1 << 28))
         return EP_ERR_UNSUPPORTED;
     const MatvecArgs a{static_cast<const uint8_t *>(x), (int)M, (int)N, (int)K,
                        Weights{q, static_cast<const uint16_t *>(scale), zero, kMagic}, y, out_dtype};
