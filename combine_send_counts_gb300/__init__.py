@@ -942,7 +942,7 @@ class W4:
     """A weight matrix [..., N, K] in 4-bit codes (EP_W_INT4 of include/ep.h):
     q [..., N, K/2] uint8 with code 2j of a row in the low half of byte j, scale
     [..., N, K/group] bf16, zero [..., N, K/group] uint8 (0..15) or None for 8."""
-    __slots__ = ("q", "scale", "zero", "group", "shape", "_p")
+    __slots__ = ("q", "scale", "zero", "group", "shape", "_p", "_index")
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor], group: int):
         _expect("W4", q=(q, torch.uint8), scale=(scale, torch.bfloat16), zero=(zero, torch.uint8))
@@ -963,6 +963,7 @@ class W4:
         self.q, self.scale, self.zero, self.group = q, scale, zero, group
         self.shape = torch.Size((*q.shape[:-1], 2 * q.shape[-1]))
         self._p = (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
+        self._index = q.get_device()
         return self
 
     @property
@@ -1012,16 +1013,21 @@ def w4_matvec(x: torch.Tensor, w: W4, out_dtype=torch.bfloat16, stream=None) -> 
     if len(w.shape) != 2:
         raise ValueError("w4_matvec: one matrix expected")
     N, K = w.shape
-    shape = x.shape
-    M = shape[0] if len(shape) == 2 else 1
-    src = _ready("w4_matvec", "x", x, torch.bfloat16, (M, K) if len(shape) != 1 else (K,))
-    code = _out_code("w4_matvec", out_dtype)
-    index = x.get_device()
-    if w.q.get_device() != index:
-        raise ValueError("w4_matvec: x and w must be on one device")
-    y = _empty((M, N) if len(shape) == 2 else (N,), out_dtype, x.device, stream)
-    _check(load().ep_w4_matvec(src, M, *w._p, N, K, w.group, y.data_ptr(), code, _raw_stream(stream, index)),
-           "w4_matvec")
+    shape, index = x.shape, x.get_device()
+    if len(shape) == 2:
+        M, out = shape[0], (shape[0], N)
+    else:
+        M, out = 1, (N,)
+    src = _ready("w4_matvec", "x", x, torch.bfloat16, (K,) if len(shape) == 1 else (M, K), w._index)
+    if out_dtype not in _OUT_DTYPES:
+        _out_code("w4_matvec", out_dtype)
+    if stream is None:
+        y, raw = torch.empty(out, dtype=out_dtype, device=x.device), _current_raw(index)
+    else:
+        y, raw = _empty(out, out_dtype, x.device, stream), _raw_stream(stream, index)
+    rc = load().ep_w4_matvec(src, M, *w._p, N, K, w.group, y.data_ptr(), _OUT_DTYPES[out_dtype], raw)
+    if rc:
+        _check(rc, "w4_matvec")
     return y
 
 
@@ -1059,10 +1065,17 @@ class RouterTopk:
         if T > self.max_tokens:
             raise ValueError(f"RouterTopk: at most {self.max_tokens} tokens, got {T}")
         lp = None if logits is None else _ready("RouterTopk", "logits", logits, torch.float32, (T, self.E), self._index)
-        idx = _empty((T, self.topk), torch.int64, dev, stream)
-        wts = _empty((T, self.topk), torch.float32, dev, stream)
-        _check(load().ep_router_topk(src, T, *self._mid, idx.data_ptr(), wts.data_ptr(), lp, *self._ws,
-                                     _raw_stream(stream, self._index)), "RouterTopk")
+        if stream is None:
+            idx = torch.empty((T, self.topk), dtype=torch.int64, device=dev)
+            wts = torch.empty((T, self.topk), dtype=torch.float32, device=dev)
+            raw = _current_raw(self._index)
+        else:
+            idx = _empty((T, self.topk), torch.int64, dev, stream)
+            wts = _empty((T, self.topk), torch.float32, dev, stream)
+            raw = _raw_stream(stream, self._index)
+        rc = load().ep_router_topk(src, T, *self._mid, idx.data_ptr(), wts.data_ptr(), lp, *self._ws, raw)
+        if rc:
+            _check(rc, "RouterTopk")
         return idx, wts
 
 
@@ -1112,6 +1125,7 @@ class MoeDecode:
             torch.cuda.current_stream(on.device).synchronize()   # the word is clear before a call on any stream
         self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, H, I), 256), dtype=torch.uint8,
                               device=on.device)
+        self._err = self.err.data_ptr()
         self._mid = (topk, H, I, E, El, rank, ctypes.addressof(self._m13), ctypes.addressof(self._m2))
         self._ws = (self.ws.data_ptr(), self.ws.numel())
         self._index = on.get_device()
@@ -1127,13 +1141,16 @@ class MoeDecode:
         if T > self.max_tokens:
             raise ValueError(f"MoeDecode: at most {self.max_tokens} tokens, got {T}")
         if out is None:
-            out = _empty((T, self.H), self.out_dtype, x.device, stream)
+            out = (torch.empty((T, self.H), dtype=self.out_dtype, device=x.device) if stream is None else
+                   _empty((T, self.H), self.out_dtype, x.device, stream))
             op = out.data_ptr()
         else:
             op = _ready("MoeDecode", "out", out, self.out_dtype, (T, self.H), index)
-        _check(load().ep_moe_decode(xp, ip, wp, T, *self._mid, op, self._code, *self._ws,
-                                    (self.err if err is None else err).data_ptr(), _raw_stream(stream, index)),
-               "MoeDecode")
+        rc = load().ep_moe_decode(xp, ip, wp, T, *self._mid, op, self._code, *self._ws,
+                                  self._err if err is None else err.data_ptr(),
+                                  _current_raw(index) if stream is None else _raw_stream(stream, index))
+        if rc:
+            _check(rc, "MoeDecode")
         return out
 
 
