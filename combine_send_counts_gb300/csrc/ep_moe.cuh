@@ -70,7 +70,6 @@ __device__ __forceinline__ int passes_of(int slots) { return (slots + kMaxCols -
 struct Lists {
     int experts, entries, big;
     int scan[3][kMostWarps];
-    int cost[kMaxSlots + 1];          // exclusive sums over the experts of the cost of a weight row
     uint16_t id[kMaxSlots];           // expert j's local id
     uint16_t entry[kMaxSlots + 1];    // its first entry: it has entry[j] .. entry[j+1]
     uint16_t owner[kMaxSlots];        // entry -> j
@@ -112,7 +111,6 @@ __device__ __forceinline__ void build_few(const Routing &r, Lists &l, int32_t *e
             if (before == 0) {
                 l.id[j] = (uint16_t)e;
                 l.entry[j] = (uint16_t)q;
-                l.cost[j] = j + q;
                 for (int p = 0; p < passes_of(c); ++p) {
                     l.owner[q + p] = (uint16_t)j;
                     l.begin[q + p] = (uint16_t)(at + p * kMaxCols);
@@ -124,7 +122,6 @@ __device__ __forceinline__ void build_few(const Routing &r, Lists &l, int32_t *e
             l.experts = experts;
             l.entries = entries;
             l.entry[experts] = (uint16_t)entries;
-            l.cost[experts] = experts + entries;
         }
         const int slots = __popc(__ballot_sync(kFull, e >= 0));
         if (s == 0)
@@ -191,8 +188,6 @@ __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *cou
             l.big_expert[atomicAdd(&l.big, 1)] = (uint16_t)e;
         l.id[j] = (uint16_t)e;
         l.entry[j] = (uint16_t)q;
-        // one pass reads a row from HBM, each further one from L2, at about twice the rate
-        l.cost[j] = j + q;
         for (int b = 0; b < c; b += kMaxCols) {
             l.owner[q] = (uint16_t)j;
             l.begin[q++] = (uint16_t)(at + b);
@@ -205,7 +200,6 @@ __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *cou
         l.entries = q;
         l.entry[j] = (uint16_t)q;
         l.begin[q] = (uint16_t)at;
-        l.cost[j] = j + q;
     }
     __syncthreads();
     // The order of slots within an entry moves no result, but every block must put the same slots into an
@@ -304,7 +298,7 @@ struct Cut {
 
 // A block's elements: from element i0 of expert j0 to element i1 of expert j1
 // (exclusive), in items that do not cross experts; the passes over an item's
-// weights follow one another, so that all but the first find them in L2.
+// weights follow one another.
 template <int G, int RB>
 struct UpItems {
     using F = typename FormatOf<G, false>::F;
@@ -405,23 +399,23 @@ struct UpItems {
     }
 };
 
-// The expert and element where the shares of blocks b and b + 1 of the costs
-// laid end to end begin, by lanes 0 and 1 of every warp.  (At most 2 *
-// kMaxSlots * kMaxDim = 2^27 in all.)
+// The expert and element where the shares of blocks b and b + 1 begin, by lanes 0
+// and 1 of every warp: an element costs its expert's passes, each of which reads
+// its rows again.  (At most kMaxSlots * kMaxDim = 2^26 in all.)
 __device__ __forceinline__ void share(const Lists &l, int I, int b, int blocks, int &j0, int &i0, int &j1, int &i1)
 {
-    const int total = l.cost[l.experts] * I, each = quick_div(total, blocks), rest = total - each * blocks;
+    const int total = l.entry[l.experts] * I, each = quick_div(total, blocks), rest = total - each * blocks;
     b += threadIdx.x & 1;
     const int pos = each * b + min(b, rest);
-    int lo = 0, hi = l.experts;   // cost[lo] * I <= pos < cost[hi] * I
+    int lo = 0, hi = l.experts;   // entry[lo] * I <= pos < entry[hi] * I
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (l.cost[mid] * I <= pos)
+        if (l.entry[mid] * I <= pos)
             lo = mid;
         else
             hi = mid;
     }
-    const int at = l.cost[lo], cost = l.cost[lo + 1] - at;
+    const int at = l.entry[lo], cost = l.entry[lo + 1] - at;
     int i = quick_div(pos - at * I, cost);
     if (b == blocks) {
         lo = l.experts;
