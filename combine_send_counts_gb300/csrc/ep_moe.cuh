@@ -283,19 +283,6 @@ struct UpArgs {
     int32_t *err;
 };
 
-// `n` elements cut into items of up to 8*RB, as equal as blocks of 8 allow.
-template <int RB>
-struct Cut {
-    int items, size;   // items, elements of each but the last
-
-    __device__ __forceinline__ explicit Cut(int n)
-    {
-        const int blocks = (n + 7) / 8, most = (blocks + RB - 1) / RB;
-        size = most > 1 ? quick_div(blocks + most - 1, most) * 8 : 8 * RB;
-        items = most > 1 ? quick_div(n + size - 1, size) : most;
-    }
-};
-
 // A block's elements: from element i0 of expert j0 to element i1 of expert j1
 // (exclusive), in items that do not cross experts; the passes over an item's
 // weights follow one another.
@@ -306,26 +293,31 @@ struct UpItems {
     const UpArgs &a;
     const Lists &l;
     int j0, i0, j1, i1;
-    Cut<RB> head, body, tail;   // of the first expert, each whole one, and the last
-    int head_items;             // of all passes
+    int head, body;        // items of the first expert, all passes; of a whole expert in one pass
     float *side;           // this warp's kept piece of an item that another warp began
     float *open;           // its kept piece of an item that it began and another goes on with
 
     __device__ __forceinline__ int passes(int j) const { return l.entry[j + 1] - l.entry[j]; }
 
+    mutable int open_q, open_i, open_end;   // the item that it began: its entry and elements
+
+    static __device__ __forceinline__ int cut(int elements) { return (elements + 8 * RB - 1) / (8 * RB); }
+
     __device__ __forceinline__ UpItems(const UpArgs &args, const Lists &lists, int ja, int ia, int jb, int ib)
-        : a(args), l(lists), j0(ja), i0(ia), j1(jb), i1(ib), head((jb > ja ? args.I : ib) - ia), body(args.I), tail(ib)
+        : a(args), l(lists), j0(ja), i0(ia), j1(jb), i1(ib)
     {
-        head_items = head.items > 0 ? head.items * passes(j0) : 0;
+        const int first = (j1 > j0 ? a.I : i1) - i0;
+        head = first > 0 ? cut(first) * passes(j0) : 0;
+        body = cut(a.I);
     }
 
     __device__ __forceinline__ int count() const
     {
-        int n = head_items;
+        int n = head;
         if (j1 > j0) {
-            n += body.items * (l.entry[j1] - l.entry[j0 + 1]);
+            n += body * (l.entry[j1] - l.entry[j0 + 1]);
             if (i1 > 0)
-                n += tail.items * passes(j1);
+                n += cut(i1) * passes(j1);
         }
         return n;
     }
@@ -333,21 +325,20 @@ struct UpItems {
     // item -> its entry, expert, and elements [i, end)
     __device__ __forceinline__ void where(int item, int &q, int &j, int &i, int &end) const
     {
-        int v = item, size = head.size;
+        int v = item;
         j = j0;
         i = i0;
-        if (item >= head_items) {
+        if (item >= head) {
             const int q1 = l.entry[j0 + 1];
-            v -= head_items;
-            j = l.owner[q1 + quick_div(v, body.items)];
-            v -= body.items * (l.entry[j] - q1);
+            v -= head;
+            j = l.owner[q1 + quick_div(v, body)];
+            v -= body * (l.entry[j] - q1);
             i = 0;
-            size = j == j1 ? tail.size : body.size;
         }
         const int n = passes(j), block = n == 1 ? v : quick_div(v, n);
-        i += block * size;
+        i += block * (8 * RB);
         q = l.entry[j] + v - block * n;
-        end = min(i + size, j == j1 ? i1 : a.I);
+        end = min(i + 8 * RB, j == j1 ? i1 : a.I);
     }
 
     __device__ __forceinline__ RowRange rows(int item) const
@@ -377,13 +368,18 @@ struct UpItems {
     template <int NT>
     __device__ __forceinline__ void done(int item, bool first, bool last, const float (&acc)[RB][NT][4]) const
     {
-        if (!first || !last) {
-            keep<RB, NT>(first ? open : side, acc);
-            return;
-        }
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         int q, j, i, end;
         where(item, q, j, i, end);
+        if (!first || !last) {
+            keep<RB, NT>(first ? open : side, acc);
+            if (first) {
+                open_q = q;
+                open_i = i;
+                open_end = end;
+            }
+            return;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -455,15 +451,14 @@ moe_up_kernel(UpArgs a)
     stream.run();
     stream.meet(begins);
     if (stream.open_item >= 0) {
-        int q, j, i, stop;
-        items.where(stream.open_item, q, j, i, stop);
-        const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
+        const int first = l.begin[items.open_q], cols = l.begin[items.open_q + 1] - first, nb = cols <= 8 ? 1 : 2;
         for (int v = threadIdx.x & 31; v < 8 * RB * cols; v += 32) {
-            const int e = v % (8 * RB), c = v / (8 * RB);
-            if (i + e < stop)
-                store_planes<(G > 0)>(a.out, l.slot[first + c], i + e,
-                                      activate(stream.add_pieces(begins, dynamic, side_index(e >> 3, e & 7, nb, c)),
-                                               stream.add_pieces(begins, dynamic, side_index(e >> 3, (e & 7) + 8, nb, c))));
+            const int e = v % (8 * RB), c = v / (8 * RB), i = items.open_i + e;
+            const int at[2] = {side_index(e >> 3, e & 7, nb, c), side_index(e >> 3, (e & 7) + 8, nb, c)};
+            float sum[2];
+            stream.template add_pieces<2>(dynamic, at, sum);
+            if (i < items.open_end)
+                store_planes<(G > 0)>(a.out, l.slot[first + c], i, activate(sum[0], sum[1]));
         }
     }
 }
@@ -494,7 +489,7 @@ struct DownItems {
 
     __device__ __forceinline__ RowRange rows(int item) const
     {
-        const int b = item / l.entries, q = item - b * l.entries;
+        const int b = quick_div(item, l.entries), q = item - b * l.entries;
         const int r = row0 + b * (16 * RB), n = min(row1 - r, 16 * RB);
         const int64_t row = (int64_t)l.id[l.owner[q]] * a.H + r;
         return RowRange{row, row + 8, n, n - 8};
@@ -502,7 +497,7 @@ struct DownItems {
 
     __device__ __forceinline__ int cols(int item) const
     {
-        const int q = item % l.entries;
+        const int q = item - quick_div(item, l.entries) * l.entries;
         return l.begin[q + 1] - l.begin[q];
     }
 
@@ -510,7 +505,7 @@ struct DownItems {
     __device__ __forceinline__ void columns(int item, Columns<NT, PLANES> &x) const
     {
         x.plane_bytes = a.h.plane_bytes;
-        set_columns<NT, PLANES>(l, item % l.entries, a.h.h, (int64_t)a.I * 2, 1, x);
+        set_columns<NT, PLANES>(l, item - quick_div(item, l.entries) * l.entries, a.h.h, (int64_t)a.I * 2, 1, x);
     }
 
     template <int NT>
@@ -551,9 +546,11 @@ moe_down_kernel(DownArgs a)
     using F = typename FormatOf<G, (G > 0)>::F;
     __shared__ int begins[F::kWarps + 1];
     // topk_idx was complete before the up kernel began; h is complete after the wait
-    for (int s = threadIdx.x; s < a.r.n; s += 32 * F::kWarps)
-        l.weight[s] = a.weights[s];
+    const float weight = threadIdx.x < a.r.n ? a.weights[threadIdx.x] : 0.0f;   // in flight while the lists are built
     build_lists<F::kWarps>(a.r, l, reinterpret_cast<int *>(dynamic), nullptr);
+    l.weight[threadIdx.x] = weight;
+    for (int s = threadIdx.x + 32 * F::kWarps; s < a.r.n; s += 32 * F::kWarps)
+        l.weight[s] = a.weights[s];
     const int warp = threadIdx.x >> 5;
     uint8_t *sides = dynamic + Room<F, RB>::kRing;
     DownItems<G, PLANES, RB> items{a, l};
@@ -572,18 +569,21 @@ moe_down_kernel(DownArgs a)
     stream.run();
     stream.meet(begins);
     if (stream.open_item >= 0) {
-        const int b = stream.open_item / l.entries, q = stream.open_item - b * l.entries;
+        const int b = quick_div(stream.open_item, l.entries), q = stream.open_item - b * l.entries;
         const int first = l.begin[q], cols = l.begin[q + 1] - first, nb = cols <= 8 ? 1 : 2;
         for (int v = threadIdx.x & 31; v < 16 * RB * cols; v += 32) {
             const int r = v % (16 * RB), c = v / (16 * RB), i = b * (16 * RB) + r;
-            if (i < rows)
-                items.y[(int64_t)l.slot[first + c] * items.stride + i] =
-                    stream.add_pieces(begins, dynamic, side_index(r >> 4, r & 15, nb, c));
+            if (i < rows) {
+                const int at[1] = {side_index(r >> 4, r & 15, nb, c)};
+                float sum[1];
+                stream.template add_pieces<1>(dynamic, at, sum);
+                items.y[(int64_t)l.slot[first + c] * items.stride + i] = sum[0];
+            }
         }
     }
     __syncthreads();
     for (int v = threadIdx.x; v < a.T * rows; v += 32 * F::kWarps) {
-        const int tok = v / rows, i = v - tok * rows;
+        const int tok = quick_div(v, rows), i = v - tok * rows;
         float sum = 0.0f;
         for (int k = 0; k < a.r.K; ++k) {
             const int slot = tok * a.r.K + k;

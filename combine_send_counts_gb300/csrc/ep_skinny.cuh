@@ -49,15 +49,19 @@ struct Room {
     static_assert(kUnits >= 1 && kSide <= kWarpRing, "the ring holds a unit, and kept sums after the run");
 };
 
-// n / d for 0 <= n < 2^27, 0 < d and a quotient below 2^22, by a float reciprocal put right by the remainder: a third
-// of the general division's latency, of which the kernels' prologues had a microsecond.
+// n / d for 0 <= n < 2^30, 0 < d and a quotient below 2^22: by the approximate
+// reciprocal, put right by the remainder (the estimate is off by two at most).
+// The general division and the exact reciprocal cost the kernels' prologues a
+// microsecond.
 __device__ __forceinline__ int quick_div(int n, int d)
 {
-    int q = (int)(__int2float_rz(n) * __frcp_rz(__int2float_rn(d)));
-    int r = n - q * d;
-    q += r >= d ? 1 : r < 0 ? -1 : 0;
-    r = n - q * d;
-    return q + (r >= d ? 1 : r < 0 ? -1 : 0);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__int2float_rn(d)));
+    int q = __float2int_rz(__fmul_rn(__int2float_rn(n), r));
+    int left = n - q * d;
+    q += left >= d ? 1 : left < 0 ? -1 : 0;
+    left = n - q * d;
+    return q + (left >= d ? 1 : left < 0 ? -1 : 0);
 }
 
 // D += A (16x16, row) * B (16x8, col), bf16 in, fp32 sums.
@@ -467,24 +471,32 @@ public:
                 begins[F::kWarps] = end_;
         }
         __syncthreads();
-        // warps 1 + this one .. last_ - 1 went on with the item that it began
-        int last = (threadIdx.x >> 5) + 1;
-        const int stop = (open_item + 1) * per_;
-        while (last < F::kWarps && begins[last] < stop)
-            ++last;
-        last_ = last;
+        // the warps (a bit each) that went on with the item that this one began
+        unsigned more = 0;
+        if (open_item >= 0) {
+            const int stop = (open_item + 1) * per_;
+#pragma unroll
+            for (int o = 1; o < F::kWarps; ++o)
+                more |= (unsigned)(o > (threadIdx.x >> 5) && begins[o] < stop && begins[o] < begins[o + 1]) << o;
+        }
+        more_ = more;
     }
 
-    // The sum at place `at` of the item that this warp began and others went on with: the pieces in the order of K.
+    // The sums at places `at` of the item that this warp began and others went on with: the pieces in the order of K.
     // `dynamic`: the ring, whose warps' parts hold the pieces that begin an item, then the side blocks.
-    __device__ __forceinline__ float add_pieces(const int *begins, const uint8_t *dynamic, int at) const
+    template <int N>
+    __device__ __forceinline__ void add_pieces(const uint8_t *dynamic, const int (&at)[N], float (&v)[N]) const
     {
         const int warp = threadIdx.x >> 5;
-        float v = reinterpret_cast<const float *>(dynamic + warp * Room<F, RB>::kWarpRing)[at];
-        for (int o = warp + 1; o < last_; ++o)
-            if (begins[o] < begins[o + 1])
-                v = __fadd_rn(v, reinterpret_cast<const float *>(dynamic + Room<F, RB>::kRing + o * Room<F, RB>::kSide)[at]);
-        return v;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = reinterpret_cast<const float *>(dynamic + warp * Room<F, RB>::kWarpRing)[at[i]];
+        for (unsigned m = more_; m != 0; m &= m - 1) {
+            const float *p = reinterpret_cast<const float *>(dynamic + Room<F, RB>::kRing + (__ffs(m) - 1) * Room<F, RB>::kSide);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] = __fadd_rn(v[i], p[at[i]]);
+        }
     }
 
     int open_item;   // the item that this warp's run began and did not finish, or -1
@@ -587,7 +599,8 @@ private:
     const Items &items_;
     const Weights &w_;
     int K_, per_, g_, t_;
-    int begin_, end_, last_, left_, first_item_, item_ahead_, u_ahead_;
+    unsigned more_;
+    int begin_, end_, left_, first_item_, item_ahead_, u_ahead_;
     int slot_ahead_, slot_, off_;
     uint32_t put_, get_;
     const uint8_t *pa_, *pb_;

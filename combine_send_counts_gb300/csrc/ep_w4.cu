@@ -317,8 +317,10 @@ w4_matvec_kernel(MatvecArgs a)
         const int cols = items.cols(item), nb = cols <= 8 ? 1 : 2;
         for (int v = lane; v < 16 * RB * cols; v += 32) {
             const int r = v % (16 * RB), c = v / (16 * RB);
-            items.store(items.col(item) + c, items.row(item) + r,
-                        stream.add_pieces(begins, dynamic, side_index(r >> 4, r & 15, nb, c)));
+            const int at[1] = {side_index(r >> 4, r & 15, nb, c)};
+            float sum[1];
+            stream.template add_pieces<1>(dynamic, at, sum);
+            items.store(items.col(item) + c, items.row(item) + r, sum[0]);
         }
     }
 }
