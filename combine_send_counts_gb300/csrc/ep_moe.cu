@@ -69,8 +69,8 @@ extern "C" int ep_moe_decode(const void *x, const int64_t *topk_idx, const float
     const Routing r{topk_idx, n, K, E, E_local, (int64_t)rank * E_local};
     const Planes h{static_cast<uint8_t *>(ws), (int64_t)planes_bytes(n, I), I, out_dtype == 1 ? 3 : 2};
     const UpArgs up{static_cast<const uint8_t *>(x), r, H, I, weights_of(w13), h, err};
-    const DownArgs down{r,   topk_weights, (int)T, H, I, weights_of(w2), h,
-                        out, out_dtype,    reinterpret_cast<float *>(h.h + 3 * h.plane_bytes)};
+    const DownArgs down{r, topk_weights, (int)T, H, I, weights_of(w2), h, out, out_dtype, 0, 0,
+                        reinterpret_cast<float *>(h.h + 3 * h.plane_bytes)};
     switch (w13->group) {
     case 0: return launch<0>(up, down, stream);
     case 32: return launch<32>(up, down, stream);

@@ -472,6 +472,7 @@ struct DownArgs {
     Planes h;
     void *out;
     int out_f32;
+    int each, rest;    // output rows of a block; the first `rest` blocks have one more
     float *y;          // [n][H] of the workspace, or null where the slots' results fit in shared memory
 };
 
@@ -554,8 +555,8 @@ moe_down_kernel(DownArgs a)
     const int warp = threadIdx.x >> 5;
     uint8_t *sides = dynamic + Room<F, RB>::kRing;
     DownItems<G, PLANES, RB> items{a, l};
-    items.row0 = (int)((int64_t)a.H * blockIdx.x / gridDim.x);
-    items.row1 = (int)((int64_t)a.H * (blockIdx.x + 1) / gridDim.x);
+    items.row0 = a.each * blockIdx.x + min((int)blockIdx.x, a.rest);
+    items.row1 = items.row0 + a.each + ((int)blockIdx.x < a.rest ? 1 : 0);
     const int rows = items.row1 - items.row0;
     items.y = a.y != nullptr ? a.y + items.row0 : reinterpret_cast<float *>(dynamic + Room<F, RB>::kFixed);
     items.stride = a.y != nullptr ? a.H : rows | 1;
@@ -620,6 +621,8 @@ template <int G, int PLANES, int RB>
 int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
 {
     using F = typename FormatOf<G, (G > 0)>::F;
+    a.each = a.H / (int)grid;
+    a.rest = a.H % (int)grid;
     static PerDevice set;
     // the slots' results stay in shared memory where there is room for them
     const size_t y = (size_t)a.r.n * ((size_t)ceil_div(a.H, grid) | 1) * sizeof(float);

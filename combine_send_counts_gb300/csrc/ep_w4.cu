@@ -223,6 +223,7 @@ int dequantize(const uint8_t *q, const void *scale, const uint8_t *zero, int64_t
 struct MatvecArgs {
     const uint8_t *x;
     int M, N, K;
+    int each, rest;    // rows of a block; the first `rest` blocks have one more
     Weights w;
     void *y;
     int out_f32;
@@ -238,8 +239,9 @@ struct MatvecItems {
     int row0, row1, m0, passes;
     float *side, *open;    // this warp's kept pieces: of an item begun by another, and of one it began
 
-    __device__ __forceinline__ int row(int item) const { return row0 + item / passes * (16 * RB); }
-    __device__ __forceinline__ int col(int item) const { return m0 + item % passes * kMaxCols; }
+    __device__ __forceinline__ int group(int item) const { return passes == 1 ? item : quick_div(item, passes); }
+    __device__ __forceinline__ int row(int item) const { return row0 + group(item) * (16 * RB); }
+    __device__ __forceinline__ int col(int item) const { return m0 + (item - group(item) * passes) * kMaxCols; }
 
     __device__ __forceinline__ RowRange rows(int item) const
     {
@@ -299,8 +301,8 @@ w4_matvec_kernel(MatvecArgs a)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *sides = dynamic + Room<F, RB>::kRing;
     MatvecItems<G, RB> items{a};
-    items.row0 = (int)((int64_t)a.N * blockIdx.x / gridDim.x);
-    items.row1 = (int)((int64_t)a.N * (blockIdx.x + 1) / gridDim.x);
+    items.row0 = a.each * blockIdx.x + min((int)blockIdx.x, a.rest);
+    items.row1 = items.row0 + a.each + ((int)blockIdx.x < a.rest ? 1 : 0);
     items.m0 = blockIdx.y * (kMaxPasses * kMaxCols);
     items.passes = min((a.M - items.m0 + kMaxCols - 1) / kMaxCols, kMaxPasses);
     items.side = reinterpret_cast<float *>(sides + warp * Room<F, RB>::kSide);
@@ -341,10 +343,12 @@ int launch_matvec(const MatvecArgs &a, int blocks, dim3 grid, cudaStream_t strea
 }
 
 template <int G>
-int matvec(const MatvecArgs &a, cudaStream_t stream)
+int matvec(MatvecArgs a, cudaStream_t stream)
 {
     constexpr int kMost = FormatW4<G, false>::kMaxBlocks;
     const int sms = std::min(device_sm_count(), a.N);
+    a.each = a.N / sms;
+    a.rest = a.N % sms;
     const dim3 grid(sms, (unsigned)ceil_div(a.M, kMaxPasses * kMaxCols));
     return launch_matvec<G, kMost>(a, blocks_at_once(ceil_div(ceil_div(a.N, sms), 16), kMost, true), grid, stream);
 }
@@ -419,7 +423,7 @@ extern "C" int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const vo
     const int64_t units = ceil_div(N, (int64_t)16 * device_sm_count()) * kMaxPasses * ceil_div(K, 256);
     if (M >= ((int64_t)1 << 20) || N >= ((int64_t)1 << 31) || K >= ((int64_t)1 << 25) || units >= ((int64_t)1 << 28))
         return EP_ERR_UNSUPPORTED;
-    const MatvecArgs a{static_cast<const uint8_t *>(x), (int)M, (int)N, (int)K,
+    const MatvecArgs a{static_cast<const uint8_t *>(x), (int)M, (int)N, (int)K, 0, 0,
                        Weights{q, static_cast<const uint16_t *>(scale), zero, kMagic}, y, out_dtype};
     switch (group) {
     case 32: return matvec<32>(a, stream);
