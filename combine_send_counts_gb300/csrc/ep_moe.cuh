@@ -427,7 +427,7 @@ template <int G, int RB>
 __global__ void __launch_bounds__(32 * FormatOf<G, false>::F::kWarps, 1)
 moe_up_kernel(UpArgs a)
 {
-    extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
+    extern __shared__ __align__(128) uint8_t dynamic[];   // ring, then one side block per warp
     __shared__ Lists l;
     using F = typename FormatOf<G, false>::F;
     __shared__ int begins[F::kWarps + 1];
@@ -542,7 +542,7 @@ template <int G, int PLANES, int RB>
 __global__ void __launch_bounds__(32 * FormatOf<G, (G > 0)>::F::kWarps, 1)
 moe_down_kernel(DownArgs a)
 {
-    extern __shared__ __align__(16) uint8_t dynamic[];   // ring, one side block per warp, y if it fits
+    extern __shared__ __align__(128) uint8_t dynamic[];   // ring, one side block per warp, y if it fits
     __shared__ Lists l;
     using F = typename FormatOf<G, (G > 0)>::F;
     __shared__ int begins[F::kWarps + 1];

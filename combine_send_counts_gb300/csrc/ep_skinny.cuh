@@ -102,6 +102,20 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a)
     return v;
 }
 
+__device__ __forceinline__ uint2 ld_shared8(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_shared4(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
 // The columns of the product, bf16, for this lane: column g of each of NT
 // blocks of 8.  PLANES copies of the columns (a value split into a sum of bf16
 // terms) lie plane_bytes apart.
@@ -157,6 +171,18 @@ struct FormatBf16 {
     static constexpr int kPieces = 4;        // 16-byte pieces of a lane's row in a stage
 
     static __device__ __forceinline__ int64_t row_bytes(int K) { return (int64_t)K * 2; }
+
+    // 16-byte piece p of a row stands at p ^ fold(row) in its stage, so that the lanes of a load meet all banks
+    static __device__ __forceinline__ int fold(int row) { return (row & 1) << 2; }
+    static __device__ __forceinline__ constexpr uint32_t refold(int) { return 0; }
+    // a lane's 16 of 64 bytes come by kReads loads, the i-th at place(g, t) ^ i * kReadStep
+    static constexpr int kReads = 1, kReadStep = 0;
+    static __device__ __forceinline__ int place(int, int t) { return 16 * t; }
+    static __device__ __forceinline__ uint4 read(const uint32_t (&at)[kReads], int offset)
+    {
+        return ld_shared16(at[0] + offset);
+    }
+
     // word w of lane t are columns lane_column(t) + word_column(w) .. +7 of the unit
     static __device__ __forceinline__ int lane_column(int t) { return 8 * t; }
     static __device__ __forceinline__ constexpr int word_column(int w) { return 32 * w; }
@@ -196,13 +222,10 @@ struct FormatBf16 {
 };
 
 // 4-bit weights with a scale (and zero point) per G columns.  A unit is 256
-// columns, two halves: lane (g, t) reads the 32 codes of columns 32t .. 32t+31
-// of each half.  Codes become bf16 integers exactly: 0x4300 | q is 128 + q,
+// columns, two halves; of each lane (g, t) reads 32 codes of its rows.  Codes become bf16 integers exactly: 0x4300 | q is 128 + q,
 // less 128 + zero.  Word bits 4j hold code j, so masking 0x000f000f takes codes
 // (j, j+4) as a pair; x's columns are paired the same way (by the stored order
-// where PERMUTED, else by byte permutes).  With G < 128 a lane's words belong to
-// other groups than its neighbours', so the four lanes of a row trade words
-// until each matrix step stays in one group.
+// where PERMUTED, else by byte permutes).
 template <int G, bool PERMUTED>
 struct FormatW4 {
     static constexpr int kWarps = 8;
@@ -216,7 +239,32 @@ struct FormatW4 {
 
     static __device__ __forceinline__ int64_t row_bytes(int K) { return K / 2; }
 
-    // word w of lane t, once the lanes have traded, are columns lane_column(t) + word_column(w) .. +7 of the unit
+    // A half's 64 bytes of a row are four 16-byte pieces of 32 codes.  A matrix step takes codes of one group: with
+    // G = 128 a lane takes a whole piece, with 64 half of each of two pieces, with 32 a word of each of the four.
+    // Piece p of a row stands at p ^ fold(row) in its stage, so that the lanes of each of these loads meet all banks.
+    static __device__ __forceinline__ int fold(int row) { return (row & 1) << 2 | (G == 128 ? 0 : row >> 1 & 3); }
+    // what fold(4i + row) changes in an address against fold(row), for rows below 4
+    static __device__ __forceinline__ constexpr uint32_t refold(int i) { return G == 128 ? 0 : 32 * i; }
+    static constexpr int kReads = 128 / G, kReadStep = G == 64 ? 32 : 16;
+    static __device__ __forceinline__ int place(int g, int t)
+    {
+        const int low = (fold(g) & 3) << 4;
+        return G == 128 ? 16 * t : G == 64 ? (16 * (t & 1) ^ low) + 8 * (t >> 1) : low + 4 * t;
+    }
+    static __device__ __forceinline__ uint4 read(const uint32_t (&at)[kReads], int offset)
+    {
+        if constexpr (G == 128) {
+            return ld_shared16(at[0] + offset);
+        } else if constexpr (G == 64) {
+            const uint2 a = ld_shared8(at[0] + offset), b = ld_shared8(at[1] + offset);
+            return make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            return make_uint4(ld_shared4(at[0] + offset), ld_shared4(at[1] + offset), ld_shared4(at[2] + offset),
+                              ld_shared4(at[3] + offset));
+        }
+    }
+
+    // word w of lane t are columns lane_column(t) + word_column(w) .. +7 of the unit
     static __device__ __forceinline__ int lane_column(int t)
     {
         return G == 128 ? 32 * t : G == 64 ? 32 * (t & 1) + 16 * (t >> 1) : 8 * t;
@@ -233,28 +281,6 @@ struct FormatW4 {
         // columns (0,4) (1,5) (2,6) (3,7)
         return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                           __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-    }
-
-    // (a, b) -> the low lane keeps a and gets its partner's a, the high lane keeps b and gets b
-    static __device__ __forceinline__ void trade(uint32_t &a, uint32_t &b, int mask, bool high)
-    {
-        const uint32_t out = high ? a : b;
-        const uint32_t in = __shfl_xor_sync(kFull, out, mask);
-        a = high ? in : a;
-        b = high ? b : in;
-    }
-
-    static __device__ __forceinline__ void arrange(uint32_t (&w)[4], int t)
-    {
-        if (G == 64) {
-            trade(w[0], w[2], 2, t & 2);
-            trade(w[1], w[3], 2, t & 2);
-        } else if (G == 32) {
-            trade(w[0], w[1], 1, t & 1);
-            trade(w[2], w[3], 1, t & 1);
-            trade(w[0], w[2], 2, t & 2);
-            trade(w[1], w[3], 2, t & 2);
-        }
     }
 
     static __device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t magic, uint32_t zz)
@@ -274,6 +300,7 @@ struct FormatW4 {
         const uint16_t *s0, *s1;    // the lane's rows
         const uint8_t *z0, *z1;
         int n0, n1, y0, y1;         // their groups and zero points to load: all of K's, or none
+        bool wide;
 
         __device__ __forceinline__ void begin(const Weights &w, const RowRange &rows, int K, int g, int t)
         {
@@ -288,17 +315,71 @@ struct FormatW4 {
             n1 = t < RB && i < rows.m ? groups : 0;
             y0 = w.zero != nullptr ? n0 : 0;
             y1 = w.zero != nullptr ? n1 : 0;
+            wide = groups % kGroups == 0 && reinterpret_cast<uintptr_t>(w.scale) % (2 * kGroups) == 0 &&
+                   reinterpret_cast<uintptr_t>(w.zero) % kGroups == 0;
         }
 
+        // unit u's: in one load per row where every row's start allows it (eight loads of a group each, of as many
+        // lines as rows, took most of the time of a product with groups of 32)
         __device__ __forceinline__ void load(int u)
         {
+            const int first = u * kGroups;
+            if (G < 128 && wide) {
+                uint32_t v[2][kGroups / 2], y[2][(kGroups + 3) / 4];
+                fetch(v[0], s0 + first, first < n0);
+                fetch(v[1], s1 + first, first < n1);
+                fetch_zero(y[0], z0 + first, first < y0);
+                fetch_zero(y[1], z1 + first, first < y1);
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        q[k][i] = (i & 1 ? v[k][i / 2] & 0xffff0000u : v[k][i / 2] << 16) | 0x4300u |
+                                  (y[k][i / 4] >> (8 * (i % 4)) & 0xff);
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
-                const int at = u * kGroups + i;
+                const int at = first + i;
                 const uint32_t v0 = at < n0 ? __ldg(s0 + at) : 0, v1 = at < n1 ? __ldg(s1 + at) : 0;
                 const uint32_t w0 = at < y0 ? __ldg(z0 + at) : 8, w1 = at < y1 ? __ldg(z1 + at) : 8;
                 q[0][i] = v0 << 16 | 0x4300u | w0;
                 q[1][i] = v1 << 16 | 0x4300u | w1;
+            }
+        }
+
+        static __device__ __forceinline__ void fetch(uint32_t (&v)[kGroups / 2], const uint16_t *p, bool in)
+        {
+#pragma unroll
+            for (int i = 0; i < kGroups / 2; ++i)
+                v[i] = 0;
+            if (!in)
+                return;
+            if constexpr (kGroups == 2) {
+                v[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+            } else if constexpr (kGroups == 4) {
+                const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
+                v[0] = t.x, v[1] = t.y;
+            } else {
+                const uint4 t = __ldg(reinterpret_cast<const uint4 *>(p));
+                v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+            }
+        }
+
+        static __device__ __forceinline__ void fetch_zero(uint32_t (&y)[(kGroups + 3) / 4], const uint8_t *p, bool in)
+        {
+#pragma unroll
+            for (int i = 0; i < (kGroups + 3) / 4; ++i)
+                y[i] = 0x08080808u;
+            if (!in)
+                return;
+            if constexpr (kGroups == 2) {
+                y[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+            } else if constexpr (kGroups == 4) {
+                y[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+            } else {
+                const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
+                y[0] = t.x, y[1] = t.y;
             }
         }
 
@@ -316,9 +397,7 @@ struct FormatW4 {
     {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t a[4] = {va[h].x, va[h].y, va[h].z, va[h].w}, b[4] = {vb[h].x, vb[h].y, vb[h].z, vb[h].w};
-            arrange(a, t);
-            arrange(b, t);
+            const uint32_t a[4] = {va[h].x, va[h].y, va[h].z, va[h].w}, b[4] = {vb[h].x, vb[h].y, vb[h].z, vb[h].w};
 #pragma unroll
             for (int gi = 0; gi < 4 / kWords; ++gi) {
                 const uint32_t q0 = s.get(r, 0, h * (128 / G) + gi), q1 = s.get(r, 1, h * (128 / G) + gi);
@@ -419,11 +498,9 @@ public:
         const int64_t total = (int64_t)n_items * per_;
         begin_ = (int)(total * warp / F::kWarps);
         end_ = (int)(total * (warp + 1) / F::kWarps);
-        // a row's 16-byte pieces are swapped in groups of four on odd rows, so that the eight lanes of a
-        // quarter warp, which read two rows, meet all 32 banks
         const int row = lane / kLanes, piece = lane % kLanes;
-        put_ = ring + warp * Room<F, RB>::kWarpRing + row * F::kRowPiece + (piece ^ ((row & 1) << 2)) * 16;
-        get_ = ring + warp * Room<F, RB>::kWarpRing + g_ * F::kRowPiece + (g_ & 1) * 64 + t_ * 16;
+        put_ = ring + warp * Room<F, RB>::kWarpRing + row * F::kRowPiece + (piece ^ F::fold(row)) * 16;
+        get_ = ring + warp * Room<F, RB>::kWarpRing + g_ * F::kRowPiece + (g_ & 1) * 64 + F::place(g_, t_);
         left_ = end_ - begin_;
         item_ahead_ = first_item_ = quick_div(begin_, per_);
         u_ahead_ = begin_ - item_ahead_ * per_;
@@ -535,12 +612,12 @@ private:
     {
         if (live_) {
             const int row_bytes = (int)F::row_bytes(K_);
-            const uint32_t dst = put_ + slot_ahead_ + r * kStageBytes;
 #pragma unroll
             for (int i = 0; i < 8 / kAtOnce; ++i) {
                 const int row = r * Items::kStep + i * kAtOnce, off = off_ + row * row_bytes;
-                cp_async16(dst + i * kAtOnce * F::kRowPiece, pa_ + off, row < n_);
-                cp_async16(dst + (8 + i * kAtOnce) * F::kRowPiece, pb_ + off, row < m_);
+                const uint32_t dst = (put_ ^ F::refold(i)) + slot_ahead_ + r * kStageBytes + i * kAtOnce * F::kRowPiece;
+                cp_async16(dst, pa_ + off, row < n_);
+                cp_async16(dst + 8 * F::kRowPiece, pb_ + off, row < m_);
             }
         }
         if (r == RB - 1) {
@@ -573,15 +650,20 @@ private:
             open();
             cp_async_wait<kUnits - 1>();
             __syncwarp();   // every lane's copies of the unit have arrived
-            const uint32_t even = get_ + slot_, odd = even + 64 - 128 * (g_ & 1);
+            uint32_t even[F::kReads], odd[F::kReads];
+#pragma unroll
+            for (int i = 0; i < F::kReads; ++i) {
+                even[i] = (get_ ^ i * F::kReadStep) + slot_;
+                odd[i] = even[i] + 64 - 128 * (g_ & 1);
+            }
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
                 uint4 a[F::kPieces], b[F::kPieces];
 #pragma unroll
-                for (int j = 0; j < F::kPieces; ++j) {   // 64-byte piece j of a row stands at j ^ (row & 1)
-                    const uint32_t at = (j & 1 ? odd : even) + r * kStageBytes + (j & ~1) * 64;
-                    a[j] = ld_shared16(at);
-                    b[j] = ld_shared16(at + 8 * F::kRowPiece);
+                for (int j = 0; j < F::kPieces; ++j) {   // 64 bytes of a row: those of odd rows change places
+                    const int offset = r * kStageBytes + (j & ~1) * 64;
+                    a[j] = F::read(j & 1 ? odd : even, offset);
+                    b[j] = F::read(j & 1 ? odd : even, offset + 8 * F::kRowPiece);
                 }
                 __syncwarp();   // every lane has read the stage
                 issue(r);

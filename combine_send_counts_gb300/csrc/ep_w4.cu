@@ -295,7 +295,7 @@ template <int G, int RB>
 __global__ void __launch_bounds__(32 * FormatW4<G, false>::kWarps, 1)
 w4_matvec_kernel(MatvecArgs a)
 {
-    extern __shared__ __align__(16) uint8_t dynamic[];   // ring, then one side block per warp
+    extern __shared__ __align__(128) uint8_t dynamic[];   // ring, then one side block per warp
     using F = FormatW4<G, false>;
     __shared__ int begins[F::kWarps + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
