@@ -335,10 +335,16 @@ struct UpItems {
             v -= body * (l.entry[j] - q1);
             i = 0;
         }
-        const int n = passes(j), block = n == 1 ? v : quick_div(v, n);
+        const int stop = j == j1 ? i1 : a.I;
+        int pass = 0, block = v;
+        if (passes(j) > 1) {
+            const int blocks = cut(stop - i);
+            pass = quick_div(v, blocks);
+            block = v - pass * blocks;
+        }
         i += block * (8 * RB);
-        q = l.entry[j] + v - block * n;
-        end = min(i + 8 * RB, j == j1 ? i1 : a.I);
+        q = l.entry[j] + pass;
+        end = min(i + 8 * RB, stop);
     }
 
     __device__ __forceinline__ RowRange rows(int item) const

@@ -390,6 +390,16 @@ struct FormatW4 {
         }
     };
 
+    // Chains of matrix steps whose sums are added at a group's end, so that a step need not wait for the one before.
+    // A group of 32 is two steps, too short for that: with one chain 24x7168x4096 took 24.2 us, with two 27.8; groups
+    // of 64 lost 1% with one.
+    static constexpr int kChains = G == 32 ? 1 : 2;
+    template <int NT>
+    static __device__ __forceinline__ float sum_of(const float (&part)[kChains][NT][4], int nt, int i)
+    {
+        return kChains == 1 ? part[0][nt][i] : __fadd_rn(part[0][nt][i], part[kChains - 1][nt][i]);
+    }
+
     template <int RB, int STEP, int NT, int PLANES, class Next>
     static __device__ __forceinline__ void block(const uint4 (&va)[kPieces], const uint4 (&vb)[kPieces], int r,
                                                  const Scales<RB, STEP> &s, uint4 (&x)[kWordsX][NT][PLANES], int t,
@@ -402,7 +412,7 @@ struct FormatW4 {
             for (int gi = 0; gi < 4 / kWords; ++gi) {
                 const uint32_t q0 = s.get(r, 0, h * (128 / G) + gi), q1 = s.get(r, 1, h * (128 / G) + gi);
                 const uint32_t zz0 = __byte_perm(q0, q0, 0x1010), zz1 = __byte_perm(q1, q1, 0x1010);
-                float part[2][NT][4] = {};   // two chains, so that a matrix step need not wait for the one before
+                float part[kChains][NT][4] = {};
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
                     const int i = gi * kWords + j, w = 4 * h + i;
@@ -416,17 +426,17 @@ struct FormatW4 {
                         for (int p = 0; p < PLANES; ++p) {
                             const uint4 v = x[w][nt][p];
                             mma_bf16(part[0][nt], a0, b0, a1, b1, v.x, v.y);
-                            mma_bf16(part[1][nt], a2, b2, a3, b3, v.z, v.w);
+                            mma_bf16(part[kChains - 1][nt], a2, b2, a3, b3, v.z, v.w);
                         }
                     next(w);
                 }
                 const float f0 = __uint_as_float(q0 & 0xffff0000u), f1 = __uint_as_float(q1 & 0xffff0000u);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    acc[nt][0] = __fmaf_rn(__fadd_rn(part[0][nt][0], part[1][nt][0]), f0, acc[nt][0]);
-                    acc[nt][1] = __fmaf_rn(__fadd_rn(part[0][nt][1], part[1][nt][1]), f0, acc[nt][1]);
-                    acc[nt][2] = __fmaf_rn(__fadd_rn(part[0][nt][2], part[1][nt][2]), f1, acc[nt][2]);
-                    acc[nt][3] = __fmaf_rn(__fadd_rn(part[0][nt][3], part[1][nt][3]), f1, acc[nt][3]);
+                    acc[nt][0] = __fmaf_rn(sum_of(part, nt, 0), f0, acc[nt][0]);
+                    acc[nt][1] = __fmaf_rn(sum_of(part, nt, 1), f0, acc[nt][1]);
+                    acc[nt][2] = __fmaf_rn(sum_of(part, nt, 2), f1, acc[nt][2]);
+                    acc[nt][3] = __fmaf_rn(sum_of(part, nt, 3), f1, acc[nt][3]);
                 }
             }
         }
@@ -574,6 +584,31 @@ public:
             for (int i = 0; i < N; ++i)
                 v[i] = __fadd_rn(v[i], p[at[i]]);
         }
+    }
+
+    // The same for all of the item's sums, as the lanes hold them: four of a lane by one load.  For an item of many
+    // columns: each sum by itself took 8 of the 24 us of 24x7168x4096.  The experts' entries have few columns, and
+    // there the sums by themselves are faster (64 experts' pieces for 13 tokens: 70 us, so 76).
+    template <int NT>
+    __device__ __forceinline__ void join(const uint8_t *dynamic, float (&acc)[RB][NT][4]) const
+    {
+        const int lane = threadIdx.x & 31;
+        const auto add = [&](const uint8_t *kept, bool more) {
+            const float4 *p = reinterpret_cast<const float4 *>(kept) + lane;
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float4 v = p[(r * NT + nt) * 32];
+                    acc[r][nt][0] = more ? __fadd_rn(acc[r][nt][0], v.x) : v.x;
+                    acc[r][nt][1] = more ? __fadd_rn(acc[r][nt][1], v.y) : v.y;
+                    acc[r][nt][2] = more ? __fadd_rn(acc[r][nt][2], v.z) : v.z;
+                    acc[r][nt][3] = more ? __fadd_rn(acc[r][nt][3], v.w) : v.w;
+                }
+        };
+        add(dynamic + (threadIdx.x >> 5) * Room<F, RB>::kWarpRing, false);
+        for (unsigned m = more_; m != 0; m &= m - 1)
+            add(dynamic + Room<F, RB>::kRing + (__ffs(m) - 1) * Room<F, RB>::kSide, true);
     }
 
     int open_item;   // the item that this warp's run began and did not finish, or -1

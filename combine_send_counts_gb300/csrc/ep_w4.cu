@@ -316,13 +316,14 @@ w4_matvec_kernel(MatvecArgs a)
     stream.meet(begins);
     const int item = stream.open_item;
     if (item >= 0) {
-        const int cols = items.cols(item), nb = cols <= 8 ? 1 : 2;
-        for (int v = lane; v < 16 * RB * cols; v += 32) {
-            const int r = v % (16 * RB), c = v / (16 * RB);
-            const int at[1] = {side_index(r >> 4, r & 15, nb, c)};
-            float sum[1];
-            stream.template add_pieces<1>(dynamic, at, sum);
-            items.store(items.col(item) + c, items.row(item) + r, sum[0]);
+        if (items.cols(item) <= 8) {
+            float acc[RB][1][4];
+            stream.template join<1>(dynamic, acc);
+            items.template done<1>(item, true, true, acc);
+        } else {
+            float acc[RB][2][4];
+            stream.template join<2>(dynamic, acc);
+            items.template done<2>(item, true, true, acc);
         }
     }
 }
