@@ -40,7 +40,7 @@
 
 namespace ep {
 
-constexpr int kMostWarps = 16;
+constexpr int kMostWarps = 8;    // of a block, in either format
 constexpr int kMaxSlots = EP_MOE_MAX_SLOTS;
 constexpr int kMaxDim = 65536;   // H and I: a block's units are counted in 32 bits
 
@@ -606,7 +606,9 @@ moe_down_kernel(DownArgs a)
 }
 
 // ------------------------------------------------------------ launch policy --
-constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - (kMostWarps + 1) * sizeof(int) - 64;   // dynamic shared memory of a block that owns an SM
+// Dynamic shared memory of a block that owns an SM: all but the static part, both rounded up to the dynamic one's
+// alignment of 128 bytes.
+constexpr size_t kMaxSmem = 227 * 1024 - sizeof(Lists) - (kMostWarps + 1) * sizeof(int) - 256;
 
 template <int G, int RB>
 int launch_up(const UpArgs &a, int64_t elements, cudaStream_t stream)

@@ -9,11 +9,13 @@
 // microsecond of HBM.
 //
 //   logits: matrix steps of 16 experts with 8 tokens as columns, weights loaded
-//   straight into their registers.  A block has 16 or 64 experts, 8 or 16
-//   tokens and one of `slices` parts of the columns, its 8 warps an eighth of
-//   that each; there are as many slices as fill the GPU once, so that a warp
-//   has one or two rounds of loads.  The slices' sums are left in the
-//   workspace.
+//   straight into their registers.  A block has 16 experts, 8 or 16 tokens and
+//   one of `slices` parts of the columns, its 8 warps an eighth of that each;
+//   there are as many slices as fill the GPU once, so that a warp has one or
+//   two rounds of loads.  The slices' sums are left in the workspace.  (Blocks
+//   of 64 experts, which read x a quarter as often, took 25.9 us instead of
+//   16.6 for 200 tokens, 256 experts and 7168 columns, 170 instead of 126 for
+//   4096 tokens, and 611 instead of 678 only at 16384.)
 //   select: a block per token adds the slices in ascending order and scores;
 //   its first warp takes the K experts, each lane keeping the best of its own
 //   keys so that a round is two reductions and one lane's rescan.
@@ -31,7 +33,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnit = 32;             // columns of a lane's 16-byte pieces: two k16 steps
 constexpr int kSelectThreads = 128;
-constexpr int kFewTokens = 32;        // up to here 16 experts to a block, else 64
 
 struct LogitsArgs {
     const uint8_t *x, *w;
@@ -95,33 +96,30 @@ struct Piece {
     }
 };
 
-template <int TERMS, int RB, int NT>
+template <int TERMS, int NT>
 __global__ void __launch_bounds__(kThreads)
 router_logits_kernel(LogitsArgs a)
 {
-    __shared__ __align__(16) float red[kWarps][RB * NT * 32 * 4];
+    __shared__ __align__(16) float red[kWarps][NT * 32 * 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int t0 = blockIdx.x * (8 * NT), e0 = blockIdx.y * (16 * RB), z = blockIdx.z;
+    const int t0 = blockIdx.x * (8 * NT), e0 = blockIdx.y * 16, z = blockIdx.z;
     const int units = (a.H + kUnit - 1) / kUnit, parts = a.slices * kWarps, part = z * kWarps + warp;
     const int u0 = (int)((int64_t)units * part / parts), u1 = (int)((int64_t)units * (part + 1) / parts);
     const int64_t row_bytes = (int64_t)a.H * (TERMS == 1 ? 2 : 4);
-    constexpr int kBatch = RB == 1 ? 4 / (TERMS == 1 ? 1 : 2) : 1;   // units loaded together
+    constexpr int kBatch = TERMS == 1 ? 4 : 2;   // units loaded together
     grid_dependency_wait();
     allow_dependents();
-    float acc[RB][NT][4] = {};
+    float acc[1][NT][4] = {};
     for (int u = u0; u < u1; u += kBatch) {
-        Piece<TERMS> pa[kBatch][RB], pb[kBatch][RB];
+        Piece<TERMS> pa[kBatch], pb[kBatch];
         uint4 x[kBatch][NT];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int k = (u + i) * kUnit + 8 * t;
             const bool in = u + i < u1 && k < a.H;
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const int e = e0 + r * 16 + g;
-                pa[i][r].load(a.w + e * row_bytes, k, in && e < a.E);
-                pb[i][r].load(a.w + (e + 8) * row_bytes, k, in && e + 8 < a.E);
-            }
+            const int e = e0 + g;
+            pa[i].load(a.w + e * row_bytes, k, in && e < a.E);
+            pb[i].load(a.w + (e + 8) * row_bytes, k, in && e + 8 < a.E);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int tok = t0 + n * 8 + g;
@@ -130,33 +128,30 @@ router_logits_kernel(LogitsArgs a)
                     x[i][n] = __ldg(reinterpret_cast<const uint4 *>(a.x + ((int64_t)tok * a.H + k) * 2));
             }
         }
+        float sum[NT][4] = {};   // of at most 128 columns, then added with IEEE operations
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            float sum[NT][4] = {};   // of at most 128 columns, then added with IEEE operations
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                uint4 wa[TERMS], wb[TERMS];
-                pa[i][r].split(wa);
-                pb[i][r].split(wb);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int s = TERMS - 1; s >= 0; --s) {
-                        mma_bf16(sum[n], wa[s].x, wb[s].x, wa[s].y, wb[s].y, x[i][n].x, x[i][n].y);
-                        mma_bf16(sum[n], wa[s].z, wb[s].z, wa[s].w, wb[s].w, x[i][n].z, x[i][n].w);
-                    }
-            }
+        for (int i = 0; i < kBatch; ++i) {
+            uint4 wa[TERMS], wb[TERMS];
+            pa[i].split(wa);
+            pb[i].split(wb);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    acc[r][n][c] = __fadd_rn(acc[r][n][c], sum[n][c]);
+                for (int s = TERMS - 1; s >= 0; --s) {
+                    mma_bf16(sum[n], wa[s].x, wb[s].x, wa[s].y, wb[s].y, x[i][n].x, x[i][n].y);
+                    mma_bf16(sum[n], wa[s].z, wb[s].z, wa[s].w, wb[s].w, x[i][n].z, x[i][n].w);
+                }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                acc[0][n][c] = __fadd_rn(acc[0][n][c], sum[n][c]);
     }
-    keep<RB, NT>(red[warp], acc);
+    keep<1, NT>(red[warp], acc);
     __syncthreads();
-    for (int v = threadIdx.x; v < 16 * RB * 8 * NT; v += kThreads) {
-        const int r = v % (16 * RB), c = v / (16 * RB), at = side_index(r >> 4, r & 15, NT, c);
+    for (int v = threadIdx.x; v < 16 * 8 * NT; v += kThreads) {
+        const int r = v % 16, c = v / 16, at = side_index(0, r, NT, c);
         float s = red[0][at];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w)
@@ -291,8 +286,7 @@ router_select_kernel(Select a)
 // As many slices of the columns as fill 152 SMs with blocks, at least a unit to a warp.
 int slices_of(int64_t T, int H, int E)
 {
-    const int64_t blocks = T <= kFewTokens ? ceil_div(E, 16) * ceil_div(T, T <= 8 ? 8 : 16)
-                                           : ceil_div(E, 64) * ceil_div(T, 16);
+    const int64_t blocks = ceil_div(E, 16) * ceil_div(T, T <= 8 ? 8 : 16);
     const int64_t most = std::max<int64_t>(1, ceil_div(H, kUnit * kWarps));
     return (int)std::max<int64_t>(1, std::min<int64_t>(most, 152 / std::max<int64_t>(1, blocks)));
 }
@@ -300,12 +294,11 @@ int slices_of(int64_t T, int H, int E)
 template <int TERMS>
 int launch_logits(const LogitsArgs &a, cudaStream_t stream)
 {
-    const unsigned e16 = (unsigned)ceil_div(a.E, 16), e64 = (unsigned)ceil_div(a.E, 64), t16 = (unsigned)ceil_div(a.T, 16);
+    const unsigned experts = (unsigned)ceil_div(a.E, 16);
     if (a.T <= 8)
-        return launch_dependent(router_logits_kernel<TERMS, 1, 1>, dim3(1, e16, a.slices), kThreads, 0, stream, a);
-    if (a.T <= kFewTokens)
-        return launch_dependent(router_logits_kernel<TERMS, 1, 2>, dim3(t16, e16, a.slices), kThreads, 0, stream, a);
-    return launch_dependent(router_logits_kernel<TERMS, 4, 2>, dim3(t16, e64, a.slices), kThreads, 0, stream, a);
+        return launch_dependent(router_logits_kernel<TERMS, 1>, dim3(1, experts, a.slices), kThreads, 0, stream, a);
+    return launch_dependent(router_logits_kernel<TERMS, 2>, dim3((unsigned)ceil_div(a.T, 16), experts, a.slices), kThreads, 0,
+                            stream, a);
 }
 
 }  // namespace
@@ -319,7 +312,7 @@ extern "C" size_t ep_router_workspace_size(int64_t T, int H, int E)
         return 0;
     // slices_of(t) * t is at most this for every t <= T, so that a workspace serves smaller batches too
     const size_t most = (size_t)std::max<int64_t>(1, ceil_div(H, kUnit * kWarps)) * T;
-    const size_t rows = std::min(most, std::max((size_t)T, (size_t)(152 * 16 / ceil_div(E, 64))));
+    const size_t rows = std::min(most, std::max((size_t)T, (size_t)(152 * 16 / ceil_div(E, 16))));
     return align_up(rows * E * sizeof(float), kWsAlign) + kWsAlign;
 }
 
