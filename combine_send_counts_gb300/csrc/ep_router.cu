@@ -33,6 +33,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnit = 32;             // columns of a lane's 16-byte pieces: two k16 steps
 constexpr int kSelectThreads = 128;
+constexpr int kAtOnce = 8;            // slices whose sums select loads together
 
 struct LogitsArgs {
     const uint8_t *x, *w;
@@ -210,8 +211,16 @@ router_select_kernel(Select a)
     float mx = neg_inf();
     for (int e = threadIdx.x; e < a.E; e += kSelectThreads) {
         float v = a.sums[t * a.E + e];
-        for (int z = 1; z < a.slices; ++z)
-            v = __fadd_rn(v, a.sums[((int64_t)z * a.T + t) * a.E + e]);
+        for (int z = 1; z < a.slices; z += kAtOnce) {
+            float part[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                part[i] = z + i < a.slices ? a.sums[((int64_t)(z + i) * a.T + t) * a.E + e] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (z + i < a.slices)
+                    v = __fadd_rn(v, part[i]);
+        }
         if (a.logits != nullptr)
             a.logits[t * a.E + e] = v;
         l[e] = v;
