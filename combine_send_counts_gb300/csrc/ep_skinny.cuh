@@ -23,6 +23,13 @@
 // Accumulators: the matrix step's fp32 sums run over at most 128 columns of K
 // (one group of 4-bit weights); these partial sums are then scaled and added
 // with IEEE fp32 operations.
+//
+// What bounds them, by the counters of a profile: bf16 weights, HBM (128 tokens
+// of 128 experts 4096x1536 read 4.8 GB in 781 us, 6.2 TB/s, 0.91 of what a copy
+// reaches); 4-bit weights, the instructions that make bf16 of the codes (50021
+// rows of 7168: 4.4 TB/s, with the ALU pipe at 59% and the warps' waits short).
+// Kernels that end before 20 us are latency: the first weights, the first x,
+// the join and the launch take 3 us or so whatever the size.
 #pragma once
 
 #include <cstdint>
@@ -98,7 +105,10 @@ __device__ __forceinline__ void cp_async_wait()
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a)
 {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
 }
 
@@ -154,7 +164,8 @@ struct Weights {
     const uint16_t *scale;
     const uint8_t *zero;
     // 0x43004300, the bf16 pair 128, 128.  As an argument it stays in a register and a code pair takes one
-    // and-or; as a constant the compiler spent a second instruction on it (302 -> XXX).
+    // and-or; as a constant it took a second instruction.  (With the scales shared by a row's lanes: 522 -> 383
+    // instructions of a warp per stage, one token of 4-bit experts 95 -> 68 us.)
     uint32_t magic;
 };
 constexpr uint32_t kMagic = 0x43004300u;
@@ -222,10 +233,11 @@ struct FormatBf16 {
 };
 
 // 4-bit weights with a scale (and zero point) per G columns.  A unit is 256
-// columns, two halves; of each lane (g, t) reads 32 codes of its rows.  Codes become bf16 integers exactly: 0x4300 | q is 128 + q,
-// less 128 + zero.  Word bits 4j hold code j, so masking 0x000f000f takes codes
-// (j, j+4) as a pair; x's columns are paired the same way (by the stored order
-// where PERMUTED, else by byte permutes).
+// columns, two halves; lane (g, t) reads 32 codes of each for each of its rows.
+// Codes become bf16 integers exactly: 0x4300 | q is 128 + q, less 128 + zero.
+// Word bits 4j hold code j, so masking 0x000f000f takes codes (j, j+4) as a
+// pair; x's columns are paired the same way (by the stored order where
+// PERMUTED, else by byte permutes).
 template <int G, bool PERMUTED>
 struct FormatW4 {
     static constexpr int kWarps = 8;
@@ -319,8 +331,9 @@ struct FormatW4 {
                    reinterpret_cast<uintptr_t>(w.zero) % kGroups == 0;
         }
 
-        // unit u's: in one load per row where every row's start allows it (eight loads of a group each, of as many
-        // lines as rows, took most of the time of a product with groups of 32)
+        // unit u's: in one load per row where every row's start allows it (eight loads of a row took 37.7 us for
+        // 24x7168x4096 with groups of 32, one 27.7; for the two of a group of 128 it is not worth its selects: 43.4
+        // instead of 42.1 us for 50021x7168, and loads a unit ahead were no better)
         __device__ __forceinline__ void load(int u)
         {
             const int first = u * kGroups;
@@ -416,10 +429,10 @@ struct FormatW4 {
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
                     const int i = gi * kWords + j, w = 4 * h + i;
-                    const uint32_t a0 = codes(a[i], s.magic, zz0), a1 = codes(a[i] >> 4, s.magic, zz0), a2 = codes(a[i] >> 8, s.magic, zz0),
-                                   a3 = codes(a[i] >> 12, s.magic, zz0);
-                    const uint32_t b0 = codes(b[i], s.magic, zz1), b1 = codes(b[i] >> 4, s.magic, zz1), b2 = codes(b[i] >> 8, s.magic, zz1),
-                                   b3 = codes(b[i] >> 12, s.magic, zz1);
+                    const uint32_t a0 = codes(a[i], s.magic, zz0), a1 = codes(a[i] >> 4, s.magic, zz0),
+                                   a2 = codes(a[i] >> 8, s.magic, zz0), a3 = codes(a[i] >> 12, s.magic, zz0);
+                    const uint32_t b0 = codes(b[i], s.magic, zz1), b1 = codes(b[i] >> 4, s.magic, zz1),
+                                   b2 = codes(b[i] >> 8, s.magic, zz1), b3 = codes(b[i] >> 12, s.magic, zz1);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -579,7 +592,8 @@ public:
         for (int i = 0; i < N; ++i)
             v[i] = reinterpret_cast<const float *>(dynamic + warp * Room<F, RB>::kWarpRing)[at[i]];
         for (unsigned m = more_; m != 0; m &= m - 1) {
-            const float *p = reinterpret_cast<const float *>(dynamic + Room<F, RB>::kRing + (__ffs(m) - 1) * Room<F, RB>::kSide);
+            const uint8_t *kept = dynamic + Room<F, RB>::kRing + (__ffs(m) - 1) * Room<F, RB>::kSide;
+            const float *p = reinterpret_cast<const float *>(kept);
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 v[i] = __fadd_rn(v[i], p[at[i]]);

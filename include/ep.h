@@ -567,10 +567,9 @@ int ep_w4_dequantize(const uint8_t *q, const void *scale, const uint8_t *zero, i
 /* y[m,n] = sum over k of x[m,k] * w[n,k] for a 4-bit matrix w [N,K]:
  *   x [M,K] bf16, y [M,N] bf16 (out_dtype 0) or fp32 (out_dtype 1).
  * Sums are fp32: a group's codes are summed first, then scaled, and rounded
- * once at the end.  The weights are read once for each 64 rows of x, so it is
- * meant for a few rows (M < 2^20, N < 2^31, K < 2^25).
- * The same call on the same inputs gives
- * the same bits. */
+ * once at the end.  The weights are gone over once for each 16 rows of x, so it
+ * is meant for a few rows (M < 2^20, N < 2^31, K < 2^25).  The same call on the
+ * same inputs gives the same bits. */
 int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const void *scale, const uint8_t *zero, int64_t N,
                  int64_t K, int group, void *y, int out_dtype, ep_stream_t stream);
 
@@ -607,9 +606,9 @@ int ep_router_topk(const void *x, int64_t T, int H, const void *w, int w_dtype, 
  *            e_l = topk_idx[t,k] - rank*E_local, of topk_weights[t,k] * y_k,
  *   y_k = W2[e_l] h_k,   h_k = silu(Wg[e_l] x[t]) * (Wu[e_l] x[t]),
  * where silu(a) = a / (1 + exp(-a)), sums are fp32 and the result is rounded
- * once.  Only the experts that some token names are read, their weights once from HBM
- * for all slots that name them.  With E_local = E (rank 0) it is the whole layer;
- * else the ranks' partials add up to it, like those of ep_batched_combine.
+ * once.  Only the experts that some token names are read, their weights once
+ * for every 16 slots that name them.  With E_local = E (rank 0) it is the whole
+ * layer; else the ranks' partials add up to it, like those of ep_batched_combine.
  *   x [T,H] bf16, topk_idx [T,K] int64 (-1 = unrouted), topk_weights [T,K] fp32.
  *   w13: per local expert [2*I, H], the I rows of Wg before the I rows of Wu;
  *   w2: per local expert [H, I]; both in the same format and group.  H % 8 ==
