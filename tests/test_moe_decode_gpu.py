@@ -57,6 +57,12 @@ def test_routings(how, fmt, T, K):
     check(T, 192, 128, 12, 12, 0, K, fmt, how, torch.bfloat16, seed=K)
 
 
+@pytest.mark.parametrize("fmt,H,I", [("bf16", 520, 1000), (32, 544, 1024), (64, 576, 960), (128, 640, 1152)])
+@pytest.mark.parametrize("T,how", [(20, "repeats"), (60, "repeats"), (60, "one"), (90, "distinct")])
+def test_several_passes_over_divided_experts(fmt, H, I, T, how):
+    check(T, H, I, 6, 6, 0, 4, fmt, how, torch.float32, seed=T)
+
+
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("fmt", ["bf16", 32])
 @pytest.mark.parametrize("rank", [0, 1, 3])

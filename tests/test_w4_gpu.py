@@ -174,6 +174,32 @@ def test_views_of_larger_buffers():
     assert torch.equal(ep.w4_dequantize(odd), ep.w4_dequantize(w))
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("at,zero_at", [(0, 0), (1, 0), (0, 1), (2, 2), (3, 5), (4, 4), (8, 8)])
+def test_scales_at_any_element(group, at, zero_at):
+    """Rows of whole units, whose scales are loaded together where their start allows it."""
+    g = f.gen(at + 10 * zero_at)
+    w = f.w4_random((), 333, 1024, group, True, g)
+    n = w.scale.numel()
+    s = torch.full((n + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    z = torch.full((n + 16,), 255, dtype=torch.uint8, device="cuda")
+    s[at:at + n], z[zero_at:zero_at + n] = w.scale.flatten(), w.zero.flatten()
+    moved = ep.W4(w.q, s[at:at + n].view(w.scale.shape), z[zero_at:zero_at + n].view(w.zero.shape), group)
+    x = f.randn((5, 1024), g)
+    got = ep.w4_matvec(x, moved, out_dtype=torch.float32)
+    v = f.values64(w)
+    f.assert_close(got, x.double() @ v.t(), f.SUM * (x.double().abs() @ v.abs().t()))
+    assert torch.equal(got, ep.w4_matvec(x, w, out_dtype=torch.float32))
+    assert torch.equal(ep.w4_dequantize(moved), ep.w4_dequantize(w))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [9, 24, 40, 70])
+@pytest.mark.parametrize("N", [2500, 9731])
+def test_matvec_passes_over_divided_rows(group, M, N):
+    check_matvec(M, N, 512, group, True, torch.bfloat16, seed=M + N)
+
+
 def test_offsets_past_32_bits():
     # codes past 2^31 bytes: the last rows against 64 bits, and the whole by one column of x
     N, K = 640_000, 7168
