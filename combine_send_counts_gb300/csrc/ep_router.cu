@@ -268,25 +268,24 @@ router_select_kernel(Select a)
         }
     };
     scan();
-    float mine = 0.0f, chosen = 0.0f;   // lane k holds slot k
-    int mine_e = -1;
+    int mine_e = -1;   // lane k holds slot k
     for (int k = 0; k < a.K; ++k) {
         const uint32_t top = __reduce_max_sync(kFull, best);
         if (top == none)
             break;
         const int e = (int)__reduce_min_sync(kFull, best == top ? (uint32_t)at : 0xffffffffu);
-        const float s = score(l[e]);
-        chosen = __fadd_rn(chosen, s);
-        if (lane == k) {
-            mine = s;
+        if (lane == k)
             mine_e = e;
-        }
         if (lane == (e & 31)) {
             key[e] = neg_inf();
             scan();
         }
         __syncwarp();
     }
+    const float mine = mine_e >= 0 ? score(l[mine_e]) : 0.0f;
+    float chosen = 0.0f;   // the scores are positive or +0: those of empty slots change nothing
+    for (int k = 0; k < a.K; ++k)
+        chosen = __fadd_rn(chosen, __shfl_sync(kFull, mine, k));
     if (lane < a.K) {
         float w = mine;
         if (a.renormalize)
