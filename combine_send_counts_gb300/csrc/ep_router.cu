@@ -20,8 +20,8 @@
 //   its first warp takes the K experts, each lane keeping the best of its own
 //   keys so that a round is two reductions and one lane's rescan.
 //
-// Measured: one token, 256 experts of 7168, 6.8 us; 200 tokens, 64 experts of
-// 2048, 6.1 us; 1024 tokens, 256 experts of 7168, 38 us.  Two launches, the first
+// Measured: one token, 256 experts of 7168, 6.5 us; 200 tokens, 64 experts of
+// 2048, 5.8 us; 1024 tokens, 256 experts of 7168, 38 us.  Two launches, the first
 // loads and K rounds of reductions are what is left of the small ones.
 #include <algorithm>
 
