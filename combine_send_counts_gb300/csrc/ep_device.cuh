@@ -120,6 +120,47 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 
 __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Loads of what the kernel before may still be writing when this one starts,
+// for use after grid_dependency_wait().  The read-only path (__ldg, ld.global.nc,
+// which const __restrict__ invites too) is for memory that nobody writes while
+// the kernel lives, and a compiler may move such a load ahead of the wait; a
+// volatile asm stays behind the wait's.
+template <class T>
+__device__ __forceinline__ T ld_global(const T *p)
+{
+    T v;
+    if constexpr (sizeof(T) == 16) {
+        uint4 u;
+        asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "l"(p));
+        v = u;
+    } else if constexpr (sizeof(T) == 8) {
+        uint2 u;
+        asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(p));
+        v = u;
+    } else if constexpr (sizeof(T) == 4) {
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    } else if constexpr (sizeof(T) == 2) {
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    } else {
+        uint32_t u;
+        asm volatile("ld.global.u8 %0, [%1];" : "=r"(u) : "l"(p));
+        v = (T)u;
+    }
+    return v;
+}
+
+// ld_stream for such memory.
+__device__ __forceinline__ uint4 ld_global_stream(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // ------------------------------------------------------ shared-memory addresses --
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {

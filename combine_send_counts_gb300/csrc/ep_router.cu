@@ -66,7 +66,7 @@ struct Piece {
         for (int i = 0; i < (TERMS == 1 ? 1 : 2); ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
             if (ok)
-                v[i] = __ldg(reinterpret_cast<const uint4 *>(row + (int64_t)k * (TERMS == 1 ? 2 : 4)) + i);
+                v[i] = ld_global(reinterpret_cast<const uint4 *>(row + (int64_t)k * (TERMS == 1 ? 2 : 4)) + i);
         }
     }
 
@@ -130,7 +130,7 @@ router_logits_kernel(LogitsArgs a)
                 const int tok = t0 + n * 8 + g;
                 x[i][n] = make_uint4(0, 0, 0, 0);
                 if (in && tok < a.T)
-                    x[i][n] = __ldg(reinterpret_cast<const uint4 *>(a.x + ((int64_t)tok * a.H + k) * 2));
+                    x[i][n] = ld_global(reinterpret_cast<const uint4 *>(a.x + ((int64_t)tok * a.H + k) * 2));
             }
         }
         float sum[NT][4] = {};   // of at most 128 columns, then added with IEEE operations

@@ -146,7 +146,7 @@ struct Columns {
     {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (k + offset < end[nt])
-            v = __ldg(reinterpret_cast<const uint4 *>(p[nt] + plane * plane_bytes + (uint32_t)k * 2 + offset * 2));
+            v = ld_global(reinterpret_cast<const uint4 *>(p[nt] + plane * plane_bytes + (uint32_t)k * 2 + offset * 2));
         return v;
     }
 };
@@ -354,8 +354,8 @@ struct FormatW4 {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 const int at = first + i;
-                const uint32_t v0 = at < n0 ? __ldg(s0 + at) : 0, v1 = at < n1 ? __ldg(s1 + at) : 0;
-                const uint32_t w0 = at < y0 ? __ldg(z0 + at) : 8, w1 = at < y1 ? __ldg(z1 + at) : 8;
+                const uint32_t v0 = at < n0 ? ld_global(s0 + at) : 0, v1 = at < n1 ? ld_global(s1 + at) : 0;
+                const uint32_t w0 = at < y0 ? ld_global(z0 + at) : 8, w1 = at < y1 ? ld_global(z1 + at) : 8;
                 q[0][i] = v0 << 16 | 0x4300u | w0;
                 q[1][i] = v1 << 16 | 0x4300u | w1;
             }
@@ -369,12 +369,12 @@ struct FormatW4 {
             if (!in)
                 return;
             if constexpr (kGroups == 2) {
-                v[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+                v[0] = ld_global(reinterpret_cast<const uint32_t *>(p));
             } else if constexpr (kGroups == 4) {
-                const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
+                const uint2 t = ld_global(reinterpret_cast<const uint2 *>(p));
                 v[0] = t.x, v[1] = t.y;
             } else {
-                const uint4 t = __ldg(reinterpret_cast<const uint4 *>(p));
+                const uint4 t = ld_global(reinterpret_cast<const uint4 *>(p));
                 v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
             }
         }
@@ -387,11 +387,11 @@ struct FormatW4 {
             if (!in)
                 return;
             if constexpr (kGroups == 2) {
-                y[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+                y[0] = ld_global(reinterpret_cast<const uint16_t *>(p));
             } else if constexpr (kGroups == 4) {
-                y[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+                y[0] = ld_global(reinterpret_cast<const uint32_t *>(p));
             } else {
-                const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
+                const uint2 t = ld_global(reinterpret_cast<const uint2 *>(p));
                 y[0] = t.x, y[1] = t.y;
             }
         }

@@ -74,8 +74,7 @@ __device__ __forceinline__ GroupScale group_scale(float least, float most)   // 
 
 template <int G, bool ZERO>
 __global__ void __launch_bounds__(kThreads)
-w4_quantize_kernel(const uint4 *__restrict__ w, int64_t vectors, uint32_t *__restrict__ q,
-                   __nv_bfloat16 *__restrict__ scale, uint8_t *__restrict__ zero)
+w4_quantize_kernel(const uint4 *w, int64_t vectors, uint32_t *q, __nv_bfloat16 *scale, uint8_t *zero)
 {
     constexpr int kLanes = G / 8;
     static_assert(kVectors == 4 && kLanes % kVectors == 0, "a lane of each group for each of a lane's groups");
@@ -88,7 +87,7 @@ w4_quantize_kernel(const uint4 *__restrict__ w, int64_t vectors, uint32_t *__res
     for (int i = 0; i < kVectors; ++i) {
         v[i] = make_uint4(0, 0, 0, 0);
         if (first + i * kThreads < vectors)   // a group's lanes are in or out together
-            v[i] = ld_stream(w + first + i * kThreads);
+            v[i] = ld_global_stream(w + first + i * kThreads);
     }
     uint32_t lo2[kVectors], hi2[kVectors];
 #pragma unroll
@@ -153,8 +152,7 @@ w4_quantize_kernel(const uint4 *__restrict__ w, int64_t vectors, uint32_t *__res
 
 template <int G, bool F32>
 __global__ void __launch_bounds__(kThreads)
-w4_dequantize_kernel(const uint32_t *__restrict__ q, const __nv_bfloat16 *__restrict__ scale,
-                     const uint8_t *__restrict__ zero, int64_t vectors, void *__restrict__ out)
+w4_dequantize_kernel(const uint32_t *q, const uint16_t *scale, const uint8_t *zero, int64_t vectors, void *out)
 {
     const int64_t first = (int64_t)blockIdx.x * (kThreads * kVectors) + threadIdx.x;
     grid_dependency_wait();
@@ -165,9 +163,9 @@ w4_dequantize_kernel(const uint32_t *__restrict__ q, const __nv_bfloat16 *__rest
     for (int i = 0; i < kVectors; ++i) {
         const int64_t at = first + i * kThreads;
         if (at < vectors) {
-            v[i] = __ldg(q + at);
-            s[i] = __bfloat162float(scale[at / (G / 8)]);
-            zz[i] = (0x4300u | (zero != nullptr ? (uint32_t)zero[at / (G / 8)] : 8u)) * 0x10001u;
+            v[i] = ld_global(q + at);
+            s[i] = __uint_as_float((uint32_t)ld_global(scale + at / (G / 8)) << 16);
+            zz[i] = (0x4300u | (zero != nullptr ? ld_global(zero + at / (G / 8)) : 8u)) * 0x10001u;
         }
     }
 #pragma unroll
@@ -211,7 +209,7 @@ int dequantize(const uint8_t *q, const void *scale, const uint8_t *zero, int64_t
                int out_dtype, cudaStream_t stream)
 {
     const auto *src = reinterpret_cast<const uint32_t *>(q);
-    const auto *s = static_cast<const __nv_bfloat16 *>(scale);
+    const auto *s = static_cast<const uint16_t *>(scale);
     if (out_dtype == 1)
         return launch_dependent(w4_dequantize_kernel<G, true>, blocks, kThreads, 0, stream, src, s, zero, vectors, w);
     return launch_dependent(w4_dequantize_kernel<G, false>, blocks, kThreads, 0, stream, src, s, zero, vectors, w);
