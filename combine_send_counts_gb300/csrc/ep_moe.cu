@@ -30,14 +30,14 @@ Weights weights_of(const ep_matrix *m)
 
 using namespace ep;
 
-// h as bf16 terms (up to three), then the slots' results
+// a term of h; the workspace holds the terms, then the slots' results
 static size_t planes_bytes(int64_t n, int I) { return align_up((size_t)n * I * 2, kWsAlign); }
 
 extern "C" size_t ep_moe_workspace_size(int64_t T, int K, int H, int I)
 {
     if (T < 0 || K < 1 || H < 1 || I < 1)
         return 0;
-    return 3 * planes_bytes(T * K, I) + align_up((size_t)T * K * H * sizeof(float), kWsAlign) + kWsAlign;
+    return kPlanes * planes_bytes(T * K, I) + align_up((size_t)T * K * H * sizeof(float), kWsAlign) + kWsAlign;
 }
 
 extern "C" int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weights, int64_t T, int K,
@@ -67,10 +67,10 @@ extern "C" int ep_moe_decode(const void *x, const int64_t *topk_idx, const float
         return EP_ERR_INVALID_ARG;
     const int n = (int)T * K;
     const Routing r{topk_idx, n, K, E, E_local, (int64_t)rank * E_local};
-    const Planes h{static_cast<uint8_t *>(ws), (int64_t)planes_bytes(n, I), I, out_dtype == 1 ? 3 : 2};
+    const Planes h{static_cast<uint8_t *>(ws), (int64_t)planes_bytes(n, I), I};
     const UpArgs up{static_cast<const uint8_t *>(x), r, H, I, weights_of(w13), h, err};
     const DownArgs down{r, topk_weights, (int)T, H, I, weights_of(w2), h, out, out_dtype, 0, 0,
-                        reinterpret_cast<float *>(h.h + 3 * h.plane_bytes)};
+                        reinterpret_cast<float *>(h.h + kPlanes * h.plane_bytes)};
     switch (w13->group) {
     case 0: return launch<0>(up, down, stream);
     case 32: return launch<32>(up, down, stream);

@@ -27,9 +27,10 @@
 // inside an item; the pieces of a divided item are added in the order of their
 // columns.  Nothing depends on the order of arrival.
 //
-// h is kept as the bf16 terms of a sum (two terms, or three for fp32 results:
-// 16 or 24 significant bits), which is what the matrix step takes; one bf16
-// would add an error as large as the rounding of the result itself.
+// h is kept whole: as the three bf16 terms of a sum (24 significant bits), which
+// is what the matrix step takes.  One bf16 would add an error as large as the
+// rounding of the result itself, and with two (16 bits) about one bf16 result
+// in 270 rounded the other way.
 //
 // Measured (up + down, of the bytes of the experts in use at 6.79 TB/s): one
 // token, 6 of 64 bf16 experts 2048x1024, 20.4 us (0.55); 128 tokens, 128 bf16
@@ -241,24 +242,26 @@ __device__ __forceinline__ void build_lists(const Routing &r, Lists &l, int *cou
     __syncthreads();
 }
 
+constexpr int kPlanes = 3;   // bf16 terms of h
+
 struct Planes {
-    uint8_t *h;            // [planes][n][I] bf16
+    uint8_t *h;            // [kPlanes][n][I] bf16
     int64_t plane_bytes;
-    int I, planes;
+    int I;
 };
 
-// h as a sum of bf16 terms; an infinity or NaN is its own first term
+// h as a sum of bf16 terms, each the next 8 of its 24 bits and toward zero, so
+// that a term never rounds up to infinity; an infinity or NaN is its own first
+// term
 template <bool PERMUTED>
 __device__ __forceinline__ void store_planes(const Planes &p, int slot, int i, float h)
 {
     const int place = (i & ~7) | column_place<PERMUTED>(i & 7);
     uint8_t *at = p.h + ((int64_t)slot * p.I + place) * 2;
     float rest = h;
-    for (int q = 0; q < p.planes; ++q) {
-        // toward zero, so that a term never rounds up to infinity; the last to nearest
-        const bool last = q == p.planes - 1;
-        const float term = last ? __bfloat162float(__float2bfloat16_rn(rest))
-                                : __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+#pragma unroll
+    for (int q = 0; q < kPlanes; ++q) {
+        const float term = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
         *reinterpret_cast<uint16_t *>(at + q * p.plane_bytes) = (uint16_t)(__float_as_uint(term) >> 16);
         const float left = __fsub_rn(rest, term);
         rest = isfinite(h) ? left : 0.0f;
@@ -497,7 +500,7 @@ struct DownArgs {
 };
 
 // A block's output rows [row0, row1) in groups of up to 16*RB, times all entries.
-template <int G, int PLANES, int RB>
+template <int G, int RB>
 struct DownItems {
     using F = typename FormatOf<G, (G > 0)>::F;
     static constexpr int kStep = 16;
@@ -523,10 +526,10 @@ struct DownItems {
     }
 
     template <int NT>
-    __device__ __forceinline__ void columns(int item, Columns<NT, PLANES> &x) const
+    __device__ __forceinline__ void columns(int item, Columns<NT, kPlanes> &x) const
     {
         x.plane_bytes = a.h.plane_bytes;
-        set_columns<NT, PLANES>(l, item - quick_div(item, l.entries) * l.entries, a.h.h, (int64_t)a.I * 2, 1, x);
+        set_columns<NT, kPlanes>(l, item - quick_div(item, l.entries) * l.entries, a.h.h, (int64_t)a.I * 2, 1, x);
     }
 
     template <int NT>
@@ -558,7 +561,7 @@ struct DownItems {
     }
 };
 
-template <int G, int PLANES, int RB>
+template <int G, int RB>
 __global__ void __launch_bounds__(32 * FormatOf<G, (G > 0)>::F::kWarps, 1)
 moe_down_kernel(DownArgs a)
 {
@@ -574,7 +577,7 @@ moe_down_kernel(DownArgs a)
         l.weight[s] = a.weights[s];
     const int warp = threadIdx.x >> 5;
     uint8_t *sides = dynamic + Room<F, RB>::kRing;
-    DownItems<G, PLANES, RB> items{a, l};
+    DownItems<G, RB> items{a, l};
     items.row0 = a.each * blockIdx.x + min((int)blockIdx.x, a.rest);
     items.row1 = items.row0 + a.each + ((int)blockIdx.x < a.rest ? 1 : 0);
     const int rows = items.row1 - items.row0;
@@ -583,7 +586,7 @@ moe_down_kernel(DownArgs a)
     items.side = reinterpret_cast<float *>(sides + warp * Room<F, RB>::kSide);
     items.open = reinterpret_cast<float *>(dynamic + warp * Room<F, RB>::kWarpRing);
     const int n = (rows + 16 * RB - 1) / (16 * RB) * l.entries;
-    Stream<F, RB, PLANES, DownItems<G, PLANES, RB>> stream(items, a.w, a.I, n, smem_u32(dynamic));
+    Stream<F, RB, kPlanes, DownItems<G, RB>> stream(items, a.w, a.I, n, smem_u32(dynamic));
     stream.start();
     grid_dependency_wait();
     allow_dependents();
@@ -640,7 +643,7 @@ int launch_up(const UpArgs &a, int64_t elements, cudaStream_t stream)
     return launch_dependent(moe_up_kernel<G, RB>, grid, 32 * F::kWarps, kSmem, stream, a);
 }
 
-template <int G, int PLANES, int RB>
+template <int G, int RB>
 int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
 {
     using F = typename FormatOf<G, (G > 0)>::F;
@@ -655,10 +658,10 @@ int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
         smem += y;
         a.y = nullptr;
     }
-    const int rc = raise_smem(moe_down_kernel<G, PLANES, RB>, kMaxSmem, set);
+    const int rc = raise_smem(moe_down_kernel<G, RB>, kMaxSmem, set);
     if (rc != EP_OK)
         return rc;
-    return launch_dependent(moe_down_kernel<G, PLANES, RB>, grid, 32 * F::kWarps, smem, stream, a);
+    return launch_dependent(moe_down_kernel<G, RB>, grid, 32 * F::kWarps, smem, stream, a);
 }
 
 template <int G, int RB = FormatOf<G, false>::F::kMaxBlocks>
@@ -673,14 +676,14 @@ int launch_up_blocks(const UpArgs &a, int64_t elements, int blocks, cudaStream_t
 
 constexpr int kMostDown = 3;   // row blocks of down at a time: 48 rows are a block's share up to H = 7296
 
-template <int G, int PLANES, int RB>
+template <int G, int RB>
 int launch_down_blocks(const DownArgs &a, unsigned grid, int blocks, cudaStream_t stream)
 {
     if constexpr (RB > 1) {
         if (blocks < RB)
-            return launch_down_blocks<G, PLANES, RB - 1>(a, grid, blocks, stream);
+            return launch_down_blocks<G, RB - 1>(a, grid, blocks, stream);
     }
-    return launch_down<G, PLANES, RB>(a, grid, stream);
+    return launch_down<G, RB>(a, grid, stream);
 }
 
 template <int G>
@@ -696,8 +699,7 @@ int launch(const UpArgs &up, const DownArgs &down, cudaStream_t stream)
         return rc;
     const unsigned grid = (unsigned)std::min(sms, down.H);
     const int blocks = blocks_at_once(ceil_div(ceil_div(down.H, grid), 16), kDown, G > 0);
-    return down.out_f32 ? launch_down_blocks<G, 3, kDown>(down, grid, blocks, stream)
-                        : launch_down_blocks<G, 2, kDown>(down, grid, blocks, stream);
+    return launch_down_blocks<G, kDown>(down, grid, blocks, stream);
 }
 
 }  // namespace ep
