@@ -43,3 +43,21 @@ def test_bits_of_h(fmt, out, T):
     y = ep.moe_decode(x.to(torch.bfloat16).cuda(), idx, torch.ones((T, 1), device="cuda"), a, b, out_dtype=out)
     off = (y.double() - 2.0 ** -11).abs()
     assert (off <= 8 * 2.0 ** -23 * 129 + (2.0 ** -8 if out == torch.bfloat16 else 2.0 ** -23) * 2.0 ** -11).all()
+
+
+def test_large_terms_that_cancel_take_no_bits_of_small_ones():
+    # h = 2^20 in elements 0 and 123, which cancel, and 1 + 2^-8 + 2^-16 in element 64 between them.  The first bf16
+    # terms are integers below 2^24, whose sum is exact; the others are summed apart from them, so the result is exact.
+    H, I = 24, 128
+    x = torch.zeros((1, H))
+    x[0, [0, 8, 16]] = 1.0
+    w13, w2 = torch.zeros((1, 2 * I, H)), torch.zeros((1, H, I))
+    w13[0, [0, 64, 123], 0] = 64.0
+    w13[0, [I, I + 123], 0] = 2.0 ** 14
+    w13[0, I + 64, [0, 8, 16]] = torch.tensor([2.0 ** -6, 2.0 ** -14, 2.0 ** -22])
+    w2[0, :, [0, 64]] = 1.0
+    w2[0, :, 123] = -1.0
+    y = ep.moe_decode(x.to(torch.bfloat16).cuda(), torch.zeros((1, 1), dtype=torch.int64, device="cuda"),
+                      torch.ones((1, 1), device="cuda"), w13.to(torch.bfloat16).cuda(), w2.to(torch.bfloat16).cuda(),
+                      out_dtype=torch.float32)
+    assert (y == 1 + 2.0 ** -8 + 2.0 ** -16).all()
