@@ -426,9 +426,13 @@ extern "C" int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const vo
     if (x == nullptr || q == nullptr || scale == nullptr || y == nullptr || !aligned(x, 16) || !aligned(q, 16) ||
         !aligned(scale, 2) || !aligned(y, 16))
         return EP_ERR_INVALID_ARG;
+    // rows are counted in 32 bits, and the last of a block's row blocks counts on past N before it is masked
+    constexpr int64_t kMostRows = ((int64_t)1 << 31) - 16 * FormatW4<32, false>::kMaxBlocks;
+    if (M >= ((int64_t)1 << 20) || N > kMostRows || K >= ((int64_t)1 << 25))
+        return EP_ERR_UNSUPPORTED;
     // a block's units of work are counted in 32 bits
     const int64_t units = ceil_div(N, (int64_t)16 * device_sm_count()) * kMaxPasses * ceil_div(K, 256);
-    if (M >= ((int64_t)1 << 20) || N >= ((int64_t)1 << 31) || K >= ((int64_t)1 << 25) || units >= ((int64_t)1 << 28))
+    if (units >= ((int64_t)1 << 28))
         return EP_ERR_UNSUPPORTED;
     const MatvecArgs a{static_cast<const uint8_t *>(x), (int)M, (int)N, (int)K, 0, 0,
                        Weights{q, static_cast<const uint16_t *>(scale), zero, kMagic}, y, out_dtype};

@@ -568,8 +568,8 @@ int ep_w4_dequantize(const uint8_t *q, const void *scale, const uint8_t *zero, i
  *   x [M,K] bf16, y [M,N] bf16 (out_dtype 0) or fp32 (out_dtype 1).
  * Sums are fp32: a group's codes are summed first, then scaled, and rounded
  * once at the end.  The weights are gone over once for each 16 rows of x, so it
- * is meant for a few rows (M < 2^20, N < 2^31, K < 2^25).  The same call on the
- * same inputs gives the same bits. */
+ * is meant for a few rows (M < 2^20, N <= 2^31 - 64, K < 2^25; else
+ * EP_ERR_UNSUPPORTED).  The same call on the same inputs gives the same bits. */
 int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const void *scale, const uint8_t *zero, int64_t N,
                  int64_t K, int group, void *y, int out_dtype, ep_stream_t stream);
 
