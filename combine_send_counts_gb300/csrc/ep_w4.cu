@@ -21,6 +21,7 @@ constexpr int kThreads = 256;
 // extremes with shuffles of bf16 pairs.  98304x4096 in groups of 128: 170 us to
 // codes and 164 back, 5.9 and 6.2 TB/s (0.88 and 0.91 of what a copy reaches).
 constexpr int kVectors = 4;
+constexpr int64_t kMostVectors = (((int64_t)1 << 31) - 1) * kThreads * kVectors;   // of a grid
 
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b)   // NaN if either is
 {
@@ -381,9 +382,9 @@ extern "C" int ep_w4_quantize(const void *w, int64_t N, int64_t K, int group, ui
         return EP_OK;
     if (w == nullptr || q == nullptr || scale == nullptr || !aligned(w, 16) || !aligned(q, 16) || !aligned(scale, 2))
         return EP_ERR_INVALID_ARG;
-    const int64_t vectors = N * (K / 8), blocks = ceil_div(vectors, kThreads * kVectors);
-    if (blocks >= ((int64_t)1 << 31))
+    if (N > kMostVectors / (K / 8))
         return EP_ERR_UNSUPPORTED;
+    const int64_t vectors = N * (K / 8), blocks = ceil_div(vectors, kThreads * kVectors);
     switch (group) {
     case 32: return quantize<32>(w, vectors, (unsigned)blocks, q, scale, zero, stream);
     case 64: return quantize<64>(w, vectors, (unsigned)blocks, q, scale, zero, stream);
@@ -403,9 +404,9 @@ extern "C" int ep_w4_dequantize(const uint8_t *q, const void *scale, const uint8
         return EP_OK;
     if (w == nullptr || q == nullptr || scale == nullptr || !aligned(w, 16) || !aligned(q, 16) || !aligned(scale, 2))
         return EP_ERR_INVALID_ARG;
-    const int64_t vectors = N * (K / 8), blocks = ceil_div(vectors, kThreads * kVectors);
-    if (blocks >= ((int64_t)1 << 31))
+    if (N > kMostVectors / (K / 8))
         return EP_ERR_UNSUPPORTED;
+    const int64_t vectors = N * (K / 8), blocks = ceil_div(vectors, kThreads * kVectors);
     switch (group) {
     case 32: return dequantize<32>(q, scale, zero, vectors, (unsigned)blocks, w, out_dtype, stream);
     case 64: return dequantize<64>(q, scale, zero, vectors, (unsigned)blocks, w, out_dtype, stream);

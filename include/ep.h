@@ -555,7 +555,8 @@ typedef struct ep_matrix {
  *     zero = clamp(rint(-lo / s), 0, 15), q = clamp(rint(w / s) + zero, 0, 15).
  * A group with s == 0 gets the codes of zero (zero point 8 or 0).  A group
  * that holds a NaN or an infinity gets s = +inf and codes equal to its zero
- * point (8 or 0), so that it reads back as NaN instead of as numbers. */
+ * point (8 or 0), so that it reads back as NaN instead of as numbers.
+ * N * K is at most 2^44 - 2^13 here and below (else EP_ERR_UNSUPPORTED). */
 int ep_w4_quantize(const void *w, int64_t N, int64_t K, int group, uint8_t *q, void *scale, uint8_t *zero,
                    ep_stream_t stream);
 
