@@ -343,20 +343,19 @@ extern "C" int ep_router_topk(const void *x, int64_t T, int H, const void *w, in
     if (x == nullptr || w == nullptr || topk_idx == nullptr || topk_weights == nullptr || !aligned(x, 16) ||
         !aligned(w, 16) || ws == nullptr || !aligned(ws, kWsAlign) || ws_bytes < ep_router_workspace_size(T, H, E))
         return EP_ERR_INVALID_ARG;
+    // for every E: the kernel's static part counts toward the 48 KB that need no raising
+    static PerDevice set;
+    int rc = raise_smem(router_select_kernel, 2 * EP_MAX_EXPERTS * sizeof(float), set);
+    if (rc != EP_OK)
+        return rc;
     const int slices = slices_of(T, H, E);
     float *sums = static_cast<float *>(ws);
     const LogitsArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), (int)T, H, E, slices, sums};
-    const int rc = w_dtype == 1 ? launch_logits<3>(a, stream) : launch_logits<1>(a, stream);
+    rc = w_dtype == 1 ? launch_logits<3>(a, stream) : launch_logits<1>(a, stream);
     if (rc != EP_OK)
         return rc;
-    const size_t smem = 2 * (size_t)E * sizeof(float);
-    static PerDevice set;
-    if (smem > 48 * 1024) {
-        const int rs = raise_smem(router_select_kernel, 2 * EP_MAX_EXPERTS * sizeof(float), set);
-        if (rs != EP_OK)
-            return rs;
-    }
     const Select s{sums, bias, (int)T, E, K, slices, scoring == EP_SCORE_SIGMOID, renormalize, scale, topk_idx,
                    topk_weights, logits};
-    return launch_dependent(router_select_kernel, dim3((unsigned)T), kSelectThreads, smem, stream, s);
+    return launch_dependent(router_select_kernel, dim3((unsigned)T), kSelectThreads, 2 * (size_t)E * sizeof(float), stream,
+                            s);
 }
