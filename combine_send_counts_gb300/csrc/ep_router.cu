@@ -101,6 +101,12 @@ struct Piece {
     }
 };
 
+// Two bf16 with 0 in place of an infinity or NaN.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v)
+{
+    return v & ~__vcmpeq2(v & 0x7f807f80u, 0x7f807f80u);
+}
+
 template <int TERMS, int NT>
 __global__ void __launch_bounds__(kThreads)
 router_logits_kernel(LogitsArgs a)
@@ -140,12 +146,21 @@ router_logits_kernel(LogitsArgs a)
             pa[i].split(wa);
             pb[i].split(wb);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                const uint4 v = x[i][n];
+                if (TERMS > 1) {
+                    // an infinite or NaN x meets the first term only: the later ones may be 0 where the weight is not
+                    const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z),
+                                               finite_bf16x2(v.w));
 #pragma unroll
-                for (int s = TERMS - 1; s >= 0; --s) {
-                    mma_bf16(sum[n], wa[s].x, wb[s].x, wa[s].y, wb[s].y, x[i][n].x, x[i][n].y);
-                    mma_bf16(sum[n], wa[s].z, wb[s].z, wa[s].w, wb[s].w, x[i][n].z, x[i][n].w);
+                    for (int s = TERMS - 1; s >= 1; --s) {
+                        mma_bf16(sum[n], wa[s].x, wb[s].x, wa[s].y, wb[s].y, f.x, f.y);
+                        mma_bf16(sum[n], wa[s].z, wb[s].z, wa[s].w, wb[s].w, f.z, f.w);
+                    }
                 }
+                mma_bf16(sum[n], wa[0].x, wb[0].x, wa[0].y, wb[0].y, v.x, v.y);
+                mma_bf16(sum[n], wa[0].z, wb[0].z, wa[0].w, wb[0].w, v.z, v.w);
+            }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)

@@ -578,6 +578,8 @@ int ep_w4_matvec(const void *x, int64_t M, const uint8_t *q, const void *scale, 
  * the K experts of each token with their weights, as every call above takes
  * them.
  *   x [T,H] bf16, H % 8 == 0; w [E,H] bf16 (w_dtype 0) or fp32 (w_dtype 1).
+ *     Infinities and NaN in either make the sums that fp32 arithmetic makes of
+ *     them; of an fp32 weight, what is below 2^-133 is dropped.
  *   scoring EP_SCORE_SOFTMAX: score = softmax of the token's logits over all E;
  *           EP_SCORE_SIGMOID: score = 1 / (1 + exp(-l)).
  *   bias [E] fp32 or NULL: experts are chosen by key = score + bias[e], or by
