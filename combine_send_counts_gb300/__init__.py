@@ -932,6 +932,17 @@ _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(index: int, fn, *args) -> int:
+    """fn(*args) with device `index` current, as the library launches on the current one."""
+    if _current_device() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
 def _raw_stream(stream, index: int) -> int:
     if stream is None:
         return _current_raw(index)
@@ -991,7 +1002,8 @@ def w4_quantize(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=N
     s = _empty((*lead, K // group), torch.bfloat16, dev, stream)
     z = _empty((*lead, K // group), torch.uint8, dev, stream) if zeros else None
     out = W4.__new__(W4)._set(q, s, z, group)
-    _check(load().ep_w4_quantize(src, w.numel() // K, K, group, *out._p, _raw_stream(stream, w.get_device())),
+    index = w.get_device()
+    _check(_call(index, load().ep_w4_quantize, src, w.numel() // K, K, group, *out._p, _raw_stream(stream, index)),
            "w4_quantize")
     return out
 
@@ -1003,8 +1015,8 @@ def w4_dequantize(w: W4, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         raise ValueError("w4_dequantize: w: device tensors expected")
     out = _empty(w.shape, out_dtype, w.q.device, stream)
     K = w.shape[-1]
-    _check(load().ep_w4_dequantize(*w._p, out.numel() // K, K, w.group, out.data_ptr(), code,
-                                   _raw_stream(stream, w.q.get_device())), "w4_dequantize")
+    _check(_call(w._index, load().ep_w4_dequantize, *w._p, out.numel() // K, K, w.group, out.data_ptr(), code,
+                 _raw_stream(stream, w._index)), "w4_dequantize")
     return out
 
 
@@ -1025,7 +1037,7 @@ def w4_matvec(x: torch.Tensor, w: W4, out_dtype=torch.bfloat16, stream=None) -> 
         y, raw = torch.empty(out, dtype=out_dtype, device=x.device), _current_raw(index)
     else:
         y, raw = _empty(out, out_dtype, x.device, stream), _raw_stream(stream, index)
-    rc = load().ep_w4_matvec(src, M, *w._p, N, K, w.group, y.data_ptr(), _OUT_DTYPES[out_dtype], raw)
+    rc = _call(index, load().ep_w4_matvec, src, M, *w._p, N, K, w.group, y.data_ptr(), _OUT_DTYPES[out_dtype], raw)
     if rc:
         _check(rc, "w4_matvec")
     return y
@@ -1073,7 +1085,8 @@ class RouterTopk:
             idx = _empty((T, self.topk), torch.int64, dev, stream)
             wts = _empty((T, self.topk), torch.float32, dev, stream)
             raw = _raw_stream(stream, self._index)
-        rc = load().ep_router_topk(src, T, *self._mid, idx.data_ptr(), wts.data_ptr(), lp, *self._ws, raw)
+        rc = _call(self._index, load().ep_router_topk, src, T, *self._mid, idx.data_ptr(), wts.data_ptr(), lp,
+                   *self._ws, raw)
         if rc:
             _check(rc, "RouterTopk")
         return idx, wts
@@ -1121,8 +1134,10 @@ class MoeDecode:
         self.rank, self.topk, self.max_tokens, self.out_dtype = rank, topk, max_tokens, out_dtype
         self._code = _out_code("MoeDecode", out_dtype)
         self.err = error_word(on.device)
-        if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream(on.device).synchronize()   # the word is clear before a call on any stream
+        stream = torch.cuda.current_stream(on.device)
+        with torch.cuda.stream(stream):   # its device too
+            if not torch.cuda.is_current_stream_capturing():
+                stream.synchronize()   # the word is clear before a call on any stream
         self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, H, I), 256), dtype=torch.uint8,
                               device=on.device)
         self._err = self.err.data_ptr()
@@ -1146,9 +1161,9 @@ class MoeDecode:
             op = out.data_ptr()
         else:
             op = _ready("MoeDecode", "out", out, self.out_dtype, (T, self.H), index)
-        rc = load().ep_moe_decode(xp, ip, wp, T, *self._mid, op, self._code, *self._ws,
-                                  self._err if err is None else err.data_ptr(),
-                                  _current_raw(index) if stream is None else _raw_stream(stream, index))
+        rc = _call(index, load().ep_moe_decode, xp, ip, wp, T, *self._mid, op, self._code, *self._ws,
+                   self._err if err is None else err.data_ptr(),
+                   _current_raw(index) if stream is None else _raw_stream(stream, index))
         if rc:
             _check(rc, "MoeDecode")
         return out
