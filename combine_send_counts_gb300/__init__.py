@@ -949,6 +949,31 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+class _Kept:
+    """An object that keeps scratch memory for its calls.  The memory belongs to the
+    stream that is current at construction; calls may be on any stream, one
+    after the other."""
+
+    def _keep(self, device, *scratch, wait=True):
+        """wait: for what the current stream still does with the memory, outside a capture."""
+        stream = torch.cuda.current_stream(device)
+        self._scratch, self._home, self._others = scratch, stream.cuda_stream, set()
+        with torch.cuda.stream(stream):   # its device too
+            if wait and not torch.cuda.is_current_stream_capturing():
+                stream.synchronize()
+
+    def _lend(self, stream, raw: int):
+        """Keeps the memory from other use, when this object dies, until the stream is done with it."""
+        device = self._scratch[0].device
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(raw, device=device)
+        for t in self._scratch:
+            t.record_stream(stream)
+        self._others.add(raw)
+
+
 class W4:
     """A weight matrix [..., N, K] in 4-bit codes (EP_W_INT4 of include/ep.h):
     q [..., N, K/2] uint8 with code 2j of a row in the low half of byte j, scale
@@ -1043,16 +1068,18 @@ def w4_matvec(x: torch.Tensor, w: W4, out_dtype=torch.bfloat16, stream=None) -> 
     return y
 
 
-class RouterTopk:
+class RouterTopk(_Kept):
     """The router of up to max_tokens tokens: w [E,H] bf16 or fp32, its workspace kept
     for repeated (or graph-captured) calls, which must not overlap on the GPU.
+    Making one waits for the current stream (outside a capture), so that calls may be
+    on any.
 
     scoring: "softmax" or "sigmoid"; bias [E] fp32 is added to the scores to
     choose experts, not to the weights; renormalize divides the K weights by
     their sum; scale multiplies them."""
 
     def __init__(self, w: torch.Tensor, topk: int, *, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
-                 renormalize: bool = True, scale: float = 1.0, max_tokens: int = 128):
+                 renormalize: bool = True, scale: float = 1.0, max_tokens: int = 128, _wait: bool = True):
         if scoring not in ("softmax", "sigmoid"):
             raise ValueError(f"RouterTopk: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
         _expect("RouterTopk", w=(w, (torch.bfloat16, torch.float32)), bias=(bias, torch.float32))
@@ -1068,6 +1095,7 @@ class RouterTopk:
                      EP_SCORE_SIGMOID if scoring == "sigmoid" else EP_SCORE_SOFTMAX, int(renormalize), self.scale)
         self._ws = (self.ws.data_ptr(), self.ws.numel())
         self._index = w.get_device()
+        self._keep(w.device, self.ws, wait=_wait)
 
     def __call__(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None, stream=None):
         """x [T,H] bf16 -> (topk_idx [T,K] int64, topk_weights [T,K] fp32); logits
@@ -1085,6 +1113,8 @@ class RouterTopk:
             idx = _empty((T, self.topk), torch.int64, dev, stream)
             wts = _empty((T, self.topk), torch.float32, dev, stream)
             raw = _raw_stream(stream, self._index)
+        if raw != self._home and raw not in self._others:
+            self._lend(stream, raw)
         rc = _call(self._index, load().ep_router_topk, src, T, *self._mid, idx.data_ptr(), wts.data_ptr(), lp,
                    *self._ws, raw)
         if rc:
@@ -1095,15 +1125,16 @@ class RouterTopk:
 def router_topk(x: torch.Tensor, w: torch.Tensor, topk: int, *, scoring: str = "softmax",
                 bias: Optional[torch.Tensor] = None, renormalize: bool = True, scale: float = 1.0, stream=None):
     """One call of the router (see RouterTopk): (topk_idx [T,K], topk_weights [T,K])."""
-    with _on(stream, x.device):   # the workspace dies with this call, on the stream that uses it
+    with _on(stream, x.device):   # the workspace lives and dies on the stream that uses it: nothing to wait for
         return RouterTopk(w, topk, scoring=scoring, bias=bias, renormalize=renormalize, scale=scale,
-                          max_tokens=x.shape[0])(x)
+                          max_tokens=x.shape[0], _wait=False)(x)
 
 
-class MoeDecode:
+class MoeDecode(_Kept):
     """The experts of a mixture-of-experts layer for a few tokens (T * topk <=
     EP_MOE_MAX_SLOTS): this rank's weights, with a workspace kept for repeated (or
-    graph-captured) calls, which must not overlap on the GPU.
+    graph-captured) calls, which must not overlap on the GPU.  Making one waits for
+    the current stream (outside a capture), so that calls may be on any.
 
     w13 [E_local, 2*I, H] (gate rows, then up rows) and w2 [E_local, H, I]: bf16
     tensors, or both W4.  num_experts: experts of all ranks (default: E_local)."""
@@ -1134,16 +1165,13 @@ class MoeDecode:
         self.rank, self.topk, self.max_tokens, self.out_dtype = rank, topk, max_tokens, out_dtype
         self._code = _out_code("MoeDecode", out_dtype)
         self.err = error_word(on.device)
-        stream = torch.cuda.current_stream(on.device)
-        with torch.cuda.stream(stream):   # its device too
-            if not torch.cuda.is_current_stream_capturing():
-                stream.synchronize()   # the word is clear before a call on any stream
         self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, H, I), 256), dtype=torch.uint8,
                               device=on.device)
         self._err = self.err.data_ptr()
         self._mid = (topk, H, I, E, El, rank, ctypes.addressof(self._m13), ctypes.addressof(self._m2))
         self._ws = (self.ws.data_ptr(), self.ws.numel())
         self._index = on.get_device()
+        self._keep(on.device, self.ws, self.err)
 
     def __call__(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, out=None, err=None,
                  stream=None) -> torch.Tensor:
@@ -1161,9 +1189,11 @@ class MoeDecode:
             op = out.data_ptr()
         else:
             op = _ready("MoeDecode", "out", out, self.out_dtype, (T, self.H), index)
+        raw = _current_raw(index) if stream is None else _raw_stream(stream, index)
+        if raw != self._home and raw not in self._others:
+            self._lend(stream, raw)
         rc = _call(index, load().ep_moe_decode, xp, ip, wp, T, *self._mid, op, self._code, *self._ws,
-                   self._err if err is None else err.data_ptr(),
-                   _current_raw(index) if stream is None else _raw_stream(stream, index))
+                   self._err if err is None else err.data_ptr(), raw)
         if rc:
             _check(rc, "MoeDecode")
         return out
