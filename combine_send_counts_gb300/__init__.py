@@ -1140,7 +1140,7 @@ class MoeDecode(_Kept):
     tensors, or both W4.  num_experts: experts of all ranks (default: E_local)."""
 
     def __init__(self, w13, w2, *, topk: int, num_experts: Optional[int] = None, rank: int = 0, max_tokens: int = 64,
-                 out_dtype=torch.bfloat16):
+                 out_dtype=torch.bfloat16, _once: bool = False):
         if isinstance(w13, W4) != isinstance(w2, W4):
             raise TypeError("MoeDecode: w13 and w2 must both be W4 or both bf16 tensors")
         if len(w13.shape) != 3 or len(w2.shape) != 3:
@@ -1164,14 +1164,15 @@ class MoeDecode(_Kept):
         self.w13, self.w2, self.E, self.E_local, self.H, self.I = w13, w2, E, El, H, I
         self.rank, self.topk, self.max_tokens, self.out_dtype = rank, topk, max_tokens, out_dtype
         self._code = _out_code("MoeDecode", out_dtype)
-        self.err = error_word(on.device)
+        # a single call has the caller's word or none, and its scratch lives and dies on the stream that uses it
+        self.err = None if _once else error_word(on.device)
         self.ws = torch.empty(max(ep_moe_workspace_size(max_tokens, topk, H, I), 256), dtype=torch.uint8,
                               device=on.device)
-        self._err = self.err.data_ptr()
+        self._err = None if _once else self.err.data_ptr()
         self._mid = (topk, H, I, E, El, rank, ctypes.addressof(self._m13), ctypes.addressof(self._m2))
         self._ws = (self.ws.data_ptr(), self.ws.numel())
         self._index = on.get_device()
-        self._keep(on.device, self.ws, self.err)
+        self._keep(on.device, self.ws, *(() if _once else (self.err,)), wait=not _once)
 
     def __call__(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, out=None, err=None,
                  stream=None) -> torch.Tensor:
@@ -1201,7 +1202,9 @@ class MoeDecode(_Kept):
 
 def moe_decode(x, topk_idx, topk_weights, w13, w2, *, num_experts: Optional[int] = None, rank: int = 0,
                out_dtype=torch.bfloat16, err=None, stream=None) -> torch.Tensor:
-    """One call of the experts for a few tokens (see MoeDecode)."""
-    with _on(stream, x.device):   # the workspace dies with this call, on the stream that uses it
+    """One call of the experts for a few tokens (see MoeDecode), without waiting for
+    anything.  Slots with an invalid expert id are ignored; they are reported in err
+    (an error_word()), so without one unseen."""
+    with _on(stream, x.device):
         return MoeDecode(w13, w2, topk=topk_idx.shape[1], num_experts=num_experts, rank=rank, max_tokens=x.shape[0],
-                         out_dtype=out_dtype)(x, topk_idx, topk_weights, err=err)
+                         out_dtype=out_dtype, _once=True)(x, topk_idx, topk_weights, err=err)
