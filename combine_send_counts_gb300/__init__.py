@@ -911,6 +911,17 @@ def _ready(where: str, name: str, t: torch.Tensor, dtype, shape, index: Optional
     return t.data_ptr()
 
 
+def _word(where: str, err: torch.Tensor, index: int) -> int:
+    """The pointer of a caller's error word: the first int32 of a tensor on this device."""
+    if err.dtype is not torch.int32:
+        raise TypeError(f"{where}: err must be torch.int32, got {err.dtype}")
+    if err.get_device() != index:
+        raise ValueError(f"{where}: err must be on device {index}, got {err.get_device()}")
+    if err.numel() == 0:
+        raise ValueError(f"{where}: err must hold a word")
+    return err.data_ptr()
+
+
 def _on(stream, device):
     """The context in which `stream` (a stream, a raw handle, or None) is current."""
     if stream is not None and not isinstance(stream, torch.cuda.Stream):
@@ -1177,7 +1188,7 @@ class MoeDecode(_Kept):
     def __call__(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, out=None, err=None,
                  stream=None) -> torch.Tensor:
         """x [T,H] bf16, topk_idx [T,topk] int64, topk_weights [T,topk] fp32 -> this rank's
-        partial [T,H].  Device errors go to err (default: this object's err)."""
+        partial [T,H].  Device errors go to err, an error_word() (default: this object's)."""
         T, index = x.shape[0], self._index
         xp = _ready("MoeDecode", "x", x, torch.bfloat16, (T, self.H), index)
         ip = _ready("MoeDecode", "topk_idx", topk_idx, torch.int64, (T, self.topk), index)
@@ -1190,11 +1201,11 @@ class MoeDecode(_Kept):
             op = out.data_ptr()
         else:
             op = _ready("MoeDecode", "out", out, self.out_dtype, (T, self.H), index)
+        ep = self._err if err is None else _word("MoeDecode", err, index)
         raw = _current_raw(index) if stream is None else _raw_stream(stream, index)
         if raw != self._home and raw not in self._others:
             self._lend(stream, raw)
-        rc = _call(index, load().ep_moe_decode, xp, ip, wp, T, *self._mid, op, self._code, *self._ws,
-                   self._err if err is None else err.data_ptr(), raw)
+        rc = _call(index, load().ep_moe_decode, xp, ip, wp, T, *self._mid, op, self._code, *self._ws, ep, raw)
         if rc:
             _check(rc, "MoeDecode")
         return out
