@@ -960,7 +960,20 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-class _Kept:
+class _Fixed:
+    """What the constructor sets stays: calls use pointers and values taken from it there."""
+    __slots__ = ()
+
+    def __setattr__(self, name, value):
+        if hasattr(self, name):
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed when the object is made")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__}.{name} is fixed when the object is made")
+
+
+class _Kept(_Fixed):
     """An object that keeps scratch memory for its calls.  The memory belongs to the
     stream that is current at construction; calls may be on any stream, one
     after the other."""
@@ -985,7 +998,7 @@ class _Kept:
         self._others.add(raw)
 
 
-class W4:
+class W4(_Fixed):
     """A weight matrix [..., N, K] in 4-bit codes (EP_W_INT4 of include/ep.h):
     q [..., N, K/2] uint8 with code 2j of a row in the low half of byte j, scale
     [..., N, K/group] bf16, zero [..., N, K/group] uint8 (0..15) or None for 8."""

@@ -33,3 +33,32 @@ def test_the_error_word_is_checked(monkeypatch, once):
     with pytest.raises(ValueError, match="err must be on device 1"):
         call(torch.zeros(1, dtype=torch.int32))
     assert len(lib.calls) == 3
+
+
+def test_fields_are_fixed(monkeypatch):
+    # a call takes its pointers from the constructor: a field set later would be ignored, or checked in its place
+    fake.install(monkeypatch, 1)
+    w = w4(N=8, K=64)
+    router = ep.RouterTopk(fake.on(E, H), K, bias=fake.on(E, dtype=torch.float32))
+    layer = experts()
+    for kept, names in ((w, ("q", "scale", "zero", "group", "shape")),
+                        (router, ("w", "bias", "topk", "scoring", "renormalize", "scale", "max_tokens", "ws")),
+                        (layer, ("w13", "w2", "rank", "topk", "max_tokens", "out_dtype", "err", "ws"))):
+        for name in names:
+            was = getattr(kept, name)
+            with pytest.raises(AttributeError, match="fixed"):
+                setattr(kept, name, None)
+            with pytest.raises(AttributeError, match="fixed"):
+                delattr(kept, name)
+            assert getattr(kept, name) is was
+    router.name = "of layer 3"   # a caller's own
+    assert router.name == "of layer 3"
+
+
+def test_w4_pointers_are_those_of_its_tensors(monkeypatch):
+    lib, _ = fake.install(monkeypatch, 1)
+    w = w4(N=8, K=64)
+    ep.w4_matvec(fake.on(T, 64), w)
+    ep.w4_dequantize(w)
+    for name, _, args in lib.calls:
+        assert w.q.data_ptr() in args and w.scale.data_ptr() in args, name
