@@ -978,6 +978,9 @@ class _Kept(_Fixed):
     stream that is current at construction; calls may be on any stream, one
     after the other."""
 
+    def __reduce_ex__(self, protocol):
+        raise TypeError(f"{type(self).__name__}: cannot be copied or pickled, make another of its weights")
+
     def _keep(self, device, *scratch, wait=True):
         """wait: for what the current stream still does with the memory, outside a capture."""
         stream = torch.cuda.current_stream(device)
@@ -1025,6 +1028,9 @@ class W4(_Fixed):
         self._p = (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
         self._index = q.get_device()
         return self
+
+    def __reduce__(self):   # a copy has pointers of its own
+        return W4, (self.q, self.scale, self.zero, self.group)
 
     @property
     def matrix(self) -> EPMatrix:

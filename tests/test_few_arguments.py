@@ -1,5 +1,8 @@
 """What the few-token objects check and keep fixed (on the host, with a recording
 library)."""
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -62,3 +65,21 @@ def test_w4_pointers_are_those_of_its_tensors(monkeypatch):
     ep.w4_dequantize(w)
     for name, _, args in lib.calls:
         assert w.q.data_ptr() in args and w.scale.data_ptr() in args, name
+
+
+@pytest.mark.parametrize("copied", [copy.deepcopy, copy.copy, lambda w: pickle.loads(pickle.dumps(w))])
+def test_a_copy_of_w4_points_to_its_own_tensors(copied):
+    w = ep.W4(torch.ones((8, 32), dtype=torch.uint8), torch.ones((8, 2), dtype=torch.bfloat16),
+              torch.ones((8, 2), dtype=torch.uint8), 32)
+    c = copied(w)
+    m = c.matrix
+    assert (m.data, m.scale, m.zero) == (c.q.data_ptr(), c.scale.data_ptr(), c.zero.data_ptr())
+    assert c.shape == w.shape and c.group == 32 and torch.equal(c.q, w.q) and torch.equal(c.zero, w.zero)
+
+
+@pytest.mark.parametrize("copied", [copy.deepcopy, copy.copy, pickle.dumps])
+def test_objects_with_scratch_are_not_copied(monkeypatch, copied):
+    fake.install(monkeypatch, 1)
+    for kept in (ep.RouterTopk(fake.on(E, H), K), experts()):
+        with pytest.raises(TypeError, match="make another"):
+            copied(kept)
