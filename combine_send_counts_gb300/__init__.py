@@ -1023,10 +1023,14 @@ class W4(_Fixed):
         self._set(q, scale, zero, group)
 
     def _set(self, q, scale, zero, group):
-        self.q, self.scale, self.zero, self.group = q, scale, zero, group
-        self.shape = torch.Size((*q.shape[:-1], 2 * q.shape[-1]))
-        self._p = (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
-        self._index = q.get_device()
+        put = object.__setattr__   # of a new object: nothing to ask for
+        put(self, "q", q)
+        put(self, "scale", scale)
+        put(self, "zero", zero)
+        put(self, "group", group)
+        put(self, "shape", torch.Size((*q.shape[:-1], 2 * q.shape[-1])))
+        put(self, "_p", (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr()))
+        put(self, "_index", q.get_device())
         return self
 
     def __reduce__(self):   # a copy has pointers of its own
