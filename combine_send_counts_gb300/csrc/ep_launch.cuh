@@ -51,8 +51,13 @@ inline int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, s
 // takes the time of all, which counts where the codes' arithmetic is what takes
 // time (4-bit weights; a stage of it is about 270 instructions, and a unit's x
 // 40: one row with 50021x7168 took 48 us in the largest equal items, 45 so).
-// bf16: the largest equal items (64 tokens of 31 experts 7168x2048 take 574 us,
-// 580 with the other rule).
+// bf16: the largest equal items (128 tokens of 128 experts 4096x1536: 814 us;
+// with three, two, one of up's blocks at a time 818, 829, 868, with one of down's
+// 980.  One token of 6 experts 2048x1024 would be 20.2 us with one of up's,
+// instead of 21.3).  The 270 instructions are those of groups of 128 and one
+// plane of x, but the choices hold for the others: with 1, 13 and 128 tokens and
+// groups of 32, 64 and 128, no other number of blocks in up or in down (three
+// planes) took 1.5% less, and most took 2 to 20% more.
 inline int blocks_at_once(int64_t blocks, int most, bool w4)
 {
     int best = (int)ceil_div(blocks, ceil_div(blocks, most));

@@ -33,11 +33,13 @@
 // in 270 rounded the other way.
 //
 // Measured (up + down, of the bytes of the experts in use at 6.79 TB/s): one
-// token, 6 of 64 bf16 experts 2048x1024, 20.4 us (0.55); 128 tokens, 128 bf16
-// experts 4096x1536, 781 us (0.91); 64 tokens, 31 of 32 bf16 experts 7168x2048
-// with 44 passes, 585 us (0.70); one token, 8 4-bit experts 7168x2048 in groups
-// of 128, 54.5 us (0.49); 13 tokens, 32 4-bit experts 4160x1472 in groups of 64,
-// 71 us (0.37).
+// token, 6 of 64 bf16 experts 2048x1024, 20.9 us (0.53); 128 tokens, 128 bf16
+// experts 4096x1536, 814 us (0.87); 64 tokens, 31 of 32 bf16 experts 7168x2048
+// with 44 passes, 588 us (0.70); one token, 8 4-bit experts 7168x2048 in groups
+// of 128, 59.3 us (0.45); 13 tokens, 32 4-bit experts 4160x1472 in groups of 64,
+// 68.3 us (0.38).  (With two terms of h these were 20.4, 781, 585 and 54.5 us;
+// the last had an fp32 result and three.)  4-bit down holds x of a unit in up to
+// 192 registers and spills in its loop.
 #pragma once
 
 #include <algorithm>
@@ -92,8 +94,8 @@ struct Lists {
 
 // build_lists for up to 32 slots, by the first warp: one slot to a lane.  The
 // experts come in the order of their first slots.  (One token of 6 bf16 experts
-// 2048x1024: 20.3 us, with the general lists 21.7; of 8 4-bit experts
-// 7168x2048: 54.5 and 58.5.)
+// 2048x1024: 20.9 us, with the general lists 22.0; of 8 4-bit experts
+// 7168x2048: 59.3 and 62.9.)
 __device__ __forceinline__ void build_few(const Routing &r, Lists &l, int32_t *err)
 {
     if (threadIdx.x < 32) {
@@ -650,8 +652,8 @@ int launch_down(DownArgs a, unsigned grid, cudaStream_t stream)
     a.each = a.H / (int)grid;
     a.rest = a.H % (int)grid;
     static PerDevice set;
-    // the slots' results stay in shared memory where there is room for them (128 tokens of 8 experts: 767 us, in the
-    // workspace 787; with fewer slots the two are alike)
+    // the slots' results stay in shared memory where there is room for them (128 tokens of 8 experts: 814 us, in the
+    // workspace 827; 64 tokens of 4: 448 and 457; one token: alike)
     const size_t y = (size_t)a.r.n * ((size_t)ceil_div(a.H, grid) | 1) * sizeof(float);
     size_t smem = Room<F, RB>::kFixed;
     if (smem + y <= kMaxSmem) {

@@ -20,9 +20,10 @@
 //   its first warp takes the K experts, each lane keeping the best of its own
 //   keys so that a round is two reductions and one lane's rescan.
 //
-// Measured: one token, 256 experts of 7168, 6.5 us; 200 tokens, 64 experts of
-// 2048, 5.8 us; 1024 tokens, 256 experts of 7168, 38 us.  Two launches, the first
-// loads and K rounds of reductions are what is left of the small ones.
+// Measured: one token, 256 experts of 7168, 6.6 us; 200 tokens, 64 experts of
+// 2048, 5.8 us; 1024 tokens, 256 experts of 7168, 40 us; 16384 tokens, 672 us.
+// Two launches, the first loads and K rounds of reductions are what is left of
+// the small ones; the large ones read x once for each 16 experts.
 #include <algorithm>
 
 #include "ep_device.cuh"
@@ -310,12 +311,15 @@ router_select_kernel(Select a)
     }
 }
 
-// As many slices of the columns as fill 152 SMs with blocks, at least a unit to a warp.
+// Blocks that fill the GPU once: a GB300's SMs.  A constant, so that the workspace has one size wherever it is asked.
+constexpr int kBlocks = 152;
+
+// As many slices of the columns as make that many blocks, at least a unit to a warp.
 int slices_of(int64_t T, int H, int E)
 {
     const int64_t blocks = ceil_div(E, 16) * ceil_div(T, T <= 8 ? 8 : 16);
     const int64_t most = std::max<int64_t>(1, ceil_div(H, kUnit * kWarps));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(most, 152 / std::max<int64_t>(1, blocks)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(most, kBlocks / std::max<int64_t>(1, blocks)));
 }
 
 template <int TERMS>
@@ -339,7 +343,7 @@ extern "C" size_t ep_router_workspace_size(int64_t T, int H, int E)
         return 0;
     // slices_of(t) * t is at most this for every t <= T, so that a workspace serves smaller batches too
     const size_t most = (size_t)std::max<int64_t>(1, ceil_div(H, kUnit * kWarps)) * T;
-    const size_t rows = std::min(most, std::max((size_t)T, (size_t)(152 * 16 / ceil_div(E, 16))));
+    const size_t rows = std::min(most, std::max((size_t)T, (size_t)(kBlocks * 16 / ceil_div(E, 16))));
     return align_up(rows * E * sizeof(float), kWsAlign) + kWsAlign;
 }
 

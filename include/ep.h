@@ -608,8 +608,8 @@ int ep_router_topk(const void *x, int64_t T, int H, const void *w, int w_dtype, 
  *   out[t] = sum over k ascending, for topk_idx[t,k] naming a local expert
  *            e_l = topk_idx[t,k] - rank*E_local, of topk_weights[t,k] * y_k,
  *   y_k = W2[e_l] h_k,   h_k = silu(Wg[e_l] x[t]) * (Wu[e_l] x[t]),
- * where silu(a) = a / (1 + exp(-a)), sums are fp32 and the result is rounded
- * once.  Only the experts that some token names are read, their weights once
+ * where silu(a) = a / (1 + exp(-a)), sums and h_k are fp32 and the result is
+ * rounded once.  Only the experts that some token names are read, their weights once
  * for every 16 slots that name them.  With E_local = E (rank 0) it is the whole
  * layer; else the ranks' partials add up to it, like those of ep_batched_combine.
  *   x [T,H] bf16, topk_idx [T,K] int64 (-1 = unrouted), topk_weights [T,K] fp32.
