@@ -31,6 +31,11 @@ The lower-case helpers after them allocate outputs with torch and call the
   ``moe_decode`` (the experts, bf16 or 4-bit weights, without dispatched
   rows), ``w4_quantize`` / ``w4_dequantize`` / ``W4`` (4-bit codes with group
   scales) and ``w4_matvec`` (their product with a few rows);
+- what stands next to the routing, for any number of tokens: ``add_rms_norm``
+  (the residual's addition, the norm, and its rows in 8 bits too) and
+  ``add_rms_norm_backward``, ``router_select`` (experts and weights from logits,
+  with groups) and ``router_select_backward``, ``LoraAdapters`` (low-rank
+  adapters of many requests beside a projection);
 - ``workspace``, ``combine_ws``, ``error_word``: scratch and the device error
   word, allocated the way the entry points expect.
 """
@@ -109,6 +114,20 @@ _SIGNATURES = {
     "ep_router_workspace_size": (_SZ, [_I64, _I32, _I32]),
     "ep_router_topk": (_I32, [_VP, _I64, _I32, _VP, _I32, _I32, _VP, _I32, _I32, _I32, ctypes.c_float, _VP, _VP, _VP,
                               _VP, _SZ, _VP]),
+    "ep_router_topk_groups": (_I32, [_VP, _I64, _I32, _VP, _I32, _I32, _VP, _I32, _I32, _I32, _I32, _I32, _I32,
+                                     ctypes.c_float, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "ep_router_select": (_I32, [_VP, _I32, _I64, _I32, _VP, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _VP,
+                                _VP, _VP]),
+    "ep_router_select_backward": (_I32, [_VP, _I32, _I64, _I32, _VP, _VP, _I32, _I32, _I32, ctypes.c_float, _VP, _VP,
+                                         _VP]),
+    "ep_add_rms_norm": (_I32, [_VP, _VP, _I32, _I64, _I32, _VP, _I32, ctypes.c_float, _VP, _VP, _VP, _VP, _I32, _I32,
+                               _VP]),
+    "ep_rms_norm_backward_workspace_size": (_SZ, [_I64, _I32]),
+    "ep_add_rms_norm_backward": (_I32, [_VP, _VP, _VP, _I32, _I64, _I32, _VP, _I32, ctypes.c_float, _VP, _VP, _VP, _VP,
+                                        _SZ, _VP]),
+    "ep_lora_workspace_size": (_SZ, [_I64, _I32]),
+    "ep_lora": (_I32, [_VP, _I64, _I32, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _VP, _I32, _VP, _I32, _VP, _SZ, _VP,
+                       _VP]),
     "ep_moe_workspace_size": (_SZ, [_I64, _I32, _I32, _I32]),
     "ep_moe_decode": (_I32, [_VP, _VP, _VP, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _SZ,
                              _VP, _VP]),
@@ -143,6 +162,7 @@ class EPPipelineBuffers(ctypes.Structure):
 
 EP_W_BF16, EP_W_INT4 = 0, 1
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_GROUP_MAX, EP_GROUP_TOP2 = 0, 1
 EP_MOE_MAX_SLOTS = 1024
 
 
@@ -874,6 +894,55 @@ def ep_router_topk(x, T, H, w, w_dtype, E, bias, K, scoring, renormalize, scale,
                                  _nbytes(ws), _stream(stream)), "ep_router_topk")
 
 
+def ep_router_topk_groups(x, T, H, w, w_dtype, E, bias, K, scoring, num_groups, topk_groups, group_score, renormalize,
+                          scale, topk_idx, topk_weights, logits, ws, stream=None):
+    _check(load().ep_router_topk_groups(_p(x), int(T), int(H), _p(w), int(w_dtype), int(E), _p(bias), int(K),
+                                        int(scoring), int(num_groups), int(topk_groups), int(group_score),
+                                        int(renormalize), float(scale), _p(topk_idx), _p(topk_weights), _p(logits),
+                                        _p(ws), _nbytes(ws), _stream(stream)), "ep_router_topk_groups")
+
+
+def ep_router_select(logits, dtype, T, E, bias, K, scoring, num_groups, topk_groups, group_score, renormalize, scale,
+                     topk_idx, topk_weights, stream=None):
+    _check(load().ep_router_select(_p(logits), int(dtype), int(T), int(E), _p(bias), int(K), int(scoring),
+                                   int(num_groups), int(topk_groups), int(group_score), int(renormalize), float(scale),
+                                   _p(topk_idx), _p(topk_weights), _stream(stream)), "ep_router_select")
+
+
+def ep_router_select_backward(logits, dtype, T, E, topk_idx, dweights, K, scoring, renormalize, scale, dlogits, err,
+                              stream=None):
+    _check(load().ep_router_select_backward(_p(logits), int(dtype), int(T), int(E), _p(topk_idx), _p(dweights), int(K),
+                                            int(scoring), int(renormalize), float(scale), _p(dlogits), _p(err),
+                                            _stream(stream)), "ep_router_select_backward")
+
+
+def ep_add_rms_norm(x, residual, res_dtype, T, H, w, w_dtype, eps, sum, y, q, scale, scale_fmt, round_scale,
+                    stream=None):
+    _check(load().ep_add_rms_norm(_p(x), _p(residual), int(res_dtype), int(T), int(H), _p(w), int(w_dtype), float(eps),
+                                  _p(sum), _p(y), _p(q), _p(scale), int(scale_fmt), int(round_scale), _stream(stream)),
+           "ep_add_rms_norm")
+
+
+def ep_rms_norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(load().ep_rms_norm_backward_workspace_size(int(T), int(H)))
+
+
+def ep_add_rms_norm_backward(dy, h, dresidual, res_dtype, T, H, w, w_dtype, eps, dh, dx, dw, ws, stream=None):
+    _check(load().ep_add_rms_norm_backward(_p(dy), _p(h), _p(dresidual), int(res_dtype), int(T), int(H), _p(w),
+                                           int(w_dtype), float(eps), _p(dh), _p(dx), _p(dw), _p(ws), _nbytes(ws),
+                                           _stream(stream)), "ep_add_rms_norm_backward")
+
+
+def ep_lora_workspace_size(M: int, R: int) -> int:
+    return int(load().ep_lora_workspace_size(int(M), int(R)))
+
+
+def ep_lora(x, M, K, ids, a, b, scaling, L, R, N, base, base_dtype, out, out_dtype, ws, err, stream=None):
+    _check(load().ep_lora(_p(x), int(M), int(K), _p(ids), _p(a), _p(b), _p(scaling), int(L), int(R), int(N), _p(base),
+                          int(base_dtype), _p(out), int(out_dtype), _p(ws), _nbytes(ws), _p(err), _stream(stream)),
+           "ep_lora")
+
+
 def ep_moe_workspace_size(T: int, K: int, H: int, I: int) -> int:
     return int(load().ep_moe_workspace_size(int(T), int(K), int(H), int(I)))
 
@@ -1102,6 +1171,20 @@ def w4_matvec(x: torch.Tensor, w: W4, out_dtype=torch.bfloat16, stream=None) -> 
     return y
 
 
+_GROUP_SCORES = {"max": EP_GROUP_MAX, "top2": EP_GROUP_TOP2}
+
+
+def _groups(where: str, E: int, num_groups: int, topk_groups: int, group_score: str):
+    """The arguments of a choice with groups, checked."""
+    if not 1 <= num_groups <= min(E, 64) or E % num_groups != 0:
+        raise ValueError(f"{where}: num_groups must be 1 .. 64 and divide {E}, got {num_groups}")
+    if not 1 <= topk_groups <= num_groups:
+        raise ValueError(f"{where}: topk_groups must be 1 .. num_groups, got {topk_groups}")
+    if group_score not in _GROUP_SCORES:
+        raise ValueError(f"{where}: group_score must be 'max' or 'top2', got {group_score!r}")
+    return num_groups, topk_groups, _GROUP_SCORES[group_score]
+
+
 class RouterTopk(_Kept):
     """The router of up to max_tokens tokens: w [E,H] bf16 or fp32, its workspace kept
     for repeated (or graph-captured) calls, which must not overlap on the GPU.
@@ -1110,10 +1193,12 @@ class RouterTopk(_Kept):
 
     scoring: "softmax" or "sigmoid"; bias [E] fp32 is added to the scores to
     choose experts, not to the weights; renormalize divides the K weights by
-    their sum; scale multiplies them."""
+    their sum; scale multiplies them; num_groups, topk_groups, group_score: see
+    router_select."""
 
     def __init__(self, w: torch.Tensor, topk: int, *, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
-                 renormalize: bool = True, scale: float = 1.0, max_tokens: int = 128, _wait: bool = True):
+                 renormalize: bool = True, scale: float = 1.0, max_tokens: int = 128, num_groups: int = 1,
+                 topk_groups: int = 1, group_score: str = "max", _wait: bool = True):
         if scoring not in ("softmax", "sigmoid"):
             raise ValueError(f"RouterTopk: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
         _expect("RouterTopk", w=(w, (torch.bfloat16, torch.float32)), bias=(bias, torch.float32))
@@ -1125,8 +1210,12 @@ class RouterTopk(_Kept):
         self.w, self.bias, self.E, self.H, self.topk = w, bias, E, H, topk
         self.scoring, self.renormalize, self.scale, self.max_tokens = scoring, renormalize, float(scale), max_tokens
         self.ws = torch.empty(max(ep_router_workspace_size(max_tokens, H, E), 256), dtype=torch.uint8, device=w.device)
+        self.num_groups, self.topk_groups, self.group_score = num_groups, topk_groups, group_score
+        groups = _groups("RouterTopk", E, num_groups, topk_groups, group_score)
+        self._grouped = num_groups > 1
         self._mid = (H, wp, 0 if w.dtype == torch.bfloat16 else 1, E, bp, topk,
-                     EP_SCORE_SIGMOID if scoring == "sigmoid" else EP_SCORE_SOFTMAX, int(renormalize), self.scale)
+                     EP_SCORE_SIGMOID if scoring == "sigmoid" else EP_SCORE_SOFTMAX,
+                     *(groups if self._grouped else ()), int(renormalize), self.scale)
         self._ws = (self.ws.data_ptr(), self.ws.numel())
         self._index = w.get_device()
         self._keep(w.device, self.ws, wait=_wait)
@@ -1149,19 +1238,22 @@ class RouterTopk(_Kept):
             raw = _raw_stream(stream, self._index)
         if raw != self._home and raw not in self._others:
             self._lend(stream, raw)
-        rc = _call(self._index, load().ep_router_topk, src, T, *self._mid, idx.data_ptr(), wts.data_ptr(), lp,
-                   *self._ws, raw)
+        lib = load()
+        rc = _call(self._index, lib.ep_router_topk_groups if self._grouped else lib.ep_router_topk, src, T, *self._mid,
+                   idx.data_ptr(), wts.data_ptr(), lp, *self._ws, raw)
         if rc:
             _check(rc, "RouterTopk")
         return idx, wts
 
 
 def router_topk(x: torch.Tensor, w: torch.Tensor, topk: int, *, scoring: str = "softmax",
-                bias: Optional[torch.Tensor] = None, renormalize: bool = True, scale: float = 1.0, stream=None):
+                bias: Optional[torch.Tensor] = None, renormalize: bool = True, scale: float = 1.0, stream=None,
+                num_groups: int = 1, topk_groups: int = 1, group_score: str = "max"):
     """One call of the router (see RouterTopk): (topk_idx [T,K], topk_weights [T,K])."""
     with _on(stream, x.device):   # the workspace lives and dies on the stream that uses it: nothing to wait for
         return RouterTopk(w, topk, scoring=scoring, bias=bias, renormalize=renormalize, scale=scale,
-                          max_tokens=x.shape[0], _wait=False)(x)
+                          max_tokens=x.shape[0], num_groups=num_groups, topk_groups=topk_groups,
+                          group_score=group_score, _wait=False)(x)
 
 
 class MoeDecode(_Kept):
@@ -1242,3 +1334,238 @@ def moe_decode(x, topk_idx, topk_weights, w13, w2, *, num_experts: Optional[int]
     with _on(stream, x.device):
         return MoeDecode(w13, w2, topk=topk_idx.shape[1], num_experts=num_experts, rank=rank, max_tokens=x.shape[0],
                          out_dtype=out_dtype, _once=True)(x, topk_idx, topk_weights, err=err)
+
+
+# ------------------------------------------------------- around the routing --
+_SCORINGS = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+_FLOATS = {torch.float32: 0, torch.bfloat16: 1}   # of logits
+_SCALE_FMTS = (EP_SCALE_ROW_F32, EP_SCALE_COL_F32, EP_SCALE_COL_UE8M0)
+
+
+def _matrix(where: str, name: str, t: torch.Tensor) -> tuple:
+    """The shape of a matrix."""
+    if t.dim() != 2:
+        raise ValueError(f"{where}: {name} must be a matrix, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _norm_weight(where: str, w: Optional[torch.Tensor], H: int, index: int):
+    if w is None:
+        return None, 0
+    if w.dtype not in _OUT_DTYPES:
+        raise TypeError(f"{where}: weight must be torch.bfloat16 or torch.float32, got {w.dtype}")
+    return _ready(where, "weight", w, w.dtype, (H,), index), _OUT_DTYPES[w.dtype]
+
+
+def _apart(where: str, name: str, t: torch.Tensor, **others):
+    """Refuses memory that t shares with another tensor, unless it is all of it."""
+    a, n = t.data_ptr(), t.numel() * t.element_size()
+    for other, o in others.items():
+        if o is None:
+            continue
+        b, m = o.data_ptr(), o.numel() * o.element_size()
+        if a < b + m and b < a + n:
+            raise ValueError(f"{where}: {name} must not overlap {other}")
+
+
+def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Optional[torch.Tensor] = None, *,
+                 eps: float = 1e-6, y: bool = True, fp8: bool = False, scale_fmt: int = EP_SCALE_ROW_F32,
+                 round_scale: bool = False, inplace: bool = False, stream=None) -> dict:
+    """h = x + residual and its root-mean-square norm times weight: x [T,H] bf16,
+    residual [T,H] bf16 or fp32 (or None: h is x), weight [H] bf16 or fp32 (or None).
+
+    -> dict(y [T,H] bf16, residual: h in the residual's type, q [T,H] uint8 (e4m3 codes of
+    y before its rounding), scale), None what is not asked for or without a
+    residual.  y=False: no y.  fp8: q and scale, whose layout scale_fmt names
+    (EP_SCALE_ROW_F32 [T,H/128], EP_SCALE_COL_F32 [H/128,T], EP_SCALE_COL_UE8M0
+    [H/512,T] int32); round_scale: scales that are powers of two.  inplace: h
+    is written over residual."""
+    where = "add_rms_norm"
+    T, H = _matrix(where, "x", x)
+    index, dev = x.get_device(), x.device
+    xp = _ready(where, "x", x, torch.bfloat16, (T, H), index)
+    wp, wd = _norm_weight(where, weight, H, index)
+    rp, rd, h, hp = None, 0, None, None
+    if residual is not None:
+        if residual.dtype not in _OUT_DTYPES:
+            raise TypeError(f"{where}: residual must be torch.bfloat16 or torch.float32, got {residual.dtype}")
+        rd = _OUT_DTYPES[residual.dtype]
+        rp = _ready(where, "residual", residual, residual.dtype, (T, H), index)
+        if inplace:
+            _apart(where, "residual", residual, x=x, weight=weight)
+        h = residual if inplace else _empty((T, H), residual.dtype, dev, stream)
+        hp = h.data_ptr()
+    elif inplace:
+        raise ValueError(f"{where}: inplace needs a residual")
+    if not y and not fp8 and residual is None:
+        raise ValueError(f"{where}: nothing is asked for")
+    out = _empty((T, H), torch.bfloat16, dev, stream) if y else None
+    q = scale = None
+    if fp8:
+        if scale_fmt not in _SCALE_FMTS:
+            raise ValueError(f"{where}: scale_fmt must be one of EP_SCALE_*, got {scale_fmt!r}")
+        q = _empty((T, H), torch.uint8, dev, stream)
+        scale = (_empty((T, H // 128), torch.float32, dev, stream) if scale_fmt == EP_SCALE_ROW_F32 else
+                 _empty((H // 128, T), torch.float32, dev, stream) if scale_fmt == EP_SCALE_COL_F32 else
+                 _empty((H // 512, T), torch.int32, dev, stream))
+    rc = _call(index, load().ep_add_rms_norm, xp, rp, rd, T, H, wp, wd, eps, hp, None if out is None else out.data_ptr(),
+               None if q is None else q.data_ptr(), None if scale is None else scale.data_ptr(), scale_fmt,
+               int(round_scale), _raw_stream(stream, index))
+    if rc:
+        _check(rc, where)
+    return dict(y=out, residual=h, q=q, scale=scale)
+
+
+def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor],
+                          dresidual: Optional[torch.Tensor] = None, *, eps: float = 1e-6, dweight: bool = True,
+                          stream=None) -> dict:
+    """The gradients of add_rms_norm from dy [T,H] bf16, that of y, and h [T,H] (what
+    it gave as residual, or x where there was none); dresidual [T,H], in h's type, is the
+    gradient that reaches h by another way.
+
+    -> dict(dresidual [T,H] in h's type, dx [T,H] bf16 (the same tensor where h is
+    bf16), dweight [H] fp32 or None)."""
+    where = "add_rms_norm_backward"
+    T, H = _matrix(where, "dy", dy)
+    index, dev = dy.get_device(), dy.device
+    gp = _ready(where, "dy", dy, torch.bfloat16, (T, H), index)
+    if h.dtype not in _OUT_DTYPES:
+        raise TypeError(f"{where}: h must be torch.bfloat16 or torch.float32, got {h.dtype}")
+    rd = _OUT_DTYPES[h.dtype]
+    hp = _ready(where, "h", h, h.dtype, (T, H), index)
+    rp = None if dresidual is None else _ready(where, "dresidual", dresidual, h.dtype, (T, H), index)
+    wp, wd = _norm_weight(where, weight, H, index)
+    dh = _empty((T, H), h.dtype, dev, stream)
+    dx = dh if rd == 0 else _empty((T, H), torch.bfloat16, dev, stream)
+    dw = ws = None
+    n = 0
+    if dweight:
+        dw = _empty((H,), torch.float32, dev, stream)
+        n = ep_rms_norm_backward_workspace_size(T, H)
+        ws = _empty((n,), torch.uint8, dev, stream)
+    rc = _call(index, load().ep_add_rms_norm_backward, gp, hp, rp, rd, T, H, wp, wd, eps, dh.data_ptr(),
+               None if rd == 0 else dx.data_ptr(), None if dw is None else dw.data_ptr(),
+               None if ws is None else ws.data_ptr(), n, _raw_stream(stream, index))
+    if rc:
+        _check(rc, where)
+    return dict(dresidual=dh, dx=dx, dweight=dw)
+
+
+def router_select(logits: torch.Tensor, topk: int, *, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
+                  num_groups: int = 1, topk_groups: int = 1, group_score: str = "max", renormalize: bool = True,
+                  scale: float = 1.0, stream=None):
+    """The experts of any number of tokens from their logits [T,E], fp32 or bf16:
+    (topk_idx [T,K] int64, topk_weights [T,K] fp32).  scoring, bias, renormalize and
+    scale as RouterTopk.
+
+    num_groups: runs of E / num_groups experts, of which the topk_groups best stay;
+    group_score: "max", a group's largest key, or "top2", the sum of its two largest."""
+    where = "router_select"
+    T, E = _matrix(where, "logits", logits)
+    dt = logits.dtype
+    if dt not in _FLOATS:
+        raise TypeError(f"{where}: logits must be torch.float32 or torch.bfloat16, got {dt}")
+    if scoring not in _SCORINGS:
+        raise ValueError(f"{where}: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+    if not 1 <= topk <= min(E, 32):
+        raise ValueError(f"{where}: topk must be 1 .. min(E, 32), got {topk}")
+    groups = _groups(where, E, num_groups, topk_groups, group_score)
+    index = logits.get_device()
+    lp = _ready(where, "logits", logits, dt, (T, E), index)
+    bp = None if bias is None else _ready(where, "bias", bias, torch.float32, (E,), index)
+    idx = _empty((T, topk), torch.int64, logits.device, stream)
+    wts = _empty((T, topk), torch.float32, logits.device, stream)
+    rc = _call(index, load().ep_router_select, lp, _FLOATS[dt], T, E, bp, topk, _SCORINGS[scoring], *groups,
+               int(renormalize), scale, idx.data_ptr(), wts.data_ptr(), _raw_stream(stream, index))
+    if rc:
+        _check(rc, where)
+    return idx, wts
+
+
+def router_select_backward(logits: torch.Tensor, topk_idx: torch.Tensor, dweights: torch.Tensor, *,
+                           scoring: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                           err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dlogits [T,E], in the logits' type, from dweights [T,K] fp32, the gradient of the
+    weights that router_select or RouterTopk gave with topk_idx [T,K]; the choice
+    itself is held fixed.  Slots with an invalid expert id are left out and
+    reported in err (an error_word()), so without one unseen."""
+    where = "router_select_backward"
+    T, E = _matrix(where, "logits", logits)
+    dt = logits.dtype
+    if dt not in _FLOATS:
+        raise TypeError(f"{where}: logits must be torch.float32 or torch.bfloat16, got {dt}")
+    if scoring not in _SCORINGS:
+        raise ValueError(f"{where}: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+    K = _matrix(where, "topk_idx", topk_idx)[1]
+    index = logits.get_device()
+    lp = _ready(where, "logits", logits, dt, (T, E), index)
+    ip = _ready(where, "topk_idx", topk_idx, torch.int64, (T, K), index)
+    gp = _ready(where, "dweights", dweights, torch.float32, (T, K), index)
+    wp = None if err is None else _word(where, err, index)
+    out = _empty((T, E), dt, logits.device, stream)
+    rc = _call(index, load().ep_router_select_backward, lp, _FLOATS[dt], T, E, ip, gp, K, _SCORINGS[scoring],
+               int(renormalize), scale, out.data_ptr(), wp, _raw_stream(stream, index))
+    if rc:
+        _check(rc, where)
+    return out
+
+
+class LoraAdapters(_Kept):
+    """Low-rank adapters of many requests beside a shared projection, for up to
+    max_tokens rows: a [L,R,K] and b [L,N,R] bf16 (a smaller rank is padded with zeros),
+    scaling [L] fp32 or None, with a workspace kept for repeated (or graph-captured)
+    calls, which must not overlap on the GPU.  Making one waits for the current
+    stream (outside a capture), so that calls may be on any."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scaling: Optional[torch.Tensor] = None, *,
+                 max_tokens: int = 128, out_dtype=torch.bfloat16):
+        if a.dim() != 3 or b.dim() != 3 or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+            raise ValueError(f"LoraAdapters: a {tuple(a.shape)} and b {tuple(b.shape)} do not belong together")
+        (L, R, K), N = a.shape, b.shape[1]
+        index = a.get_device()
+        ap = _ready("LoraAdapters", "a", a, torch.bfloat16, (L, R, K), index)
+        bp = _ready("LoraAdapters", "b", b, torch.bfloat16, (L, N, R), index)
+        sp = None if scaling is None else _ready("LoraAdapters", "scaling", scaling, torch.float32, (L,), index)
+        self._code = _out_code("LoraAdapters", out_dtype)
+        self.a, self.b, self.scaling, self.L, self.R, self.K, self.N = a, b, scaling, L, R, K, N
+        self.max_tokens, self.out_dtype = max_tokens, out_dtype
+        self.err = error_word(a.device)
+        self.ws = torch.empty(max(ep_lora_workspace_size(max_tokens, R), 256), dtype=torch.uint8, device=a.device)
+        self._err = self.err.data_ptr()
+        self._mid = (ap, bp, sp, L, R, N)
+        self._ws = (self.ws.data_ptr(), self.ws.numel())
+        self._index = index
+        self._keep(a.device, self.ws, self.err)
+
+    def __call__(self, x: torch.Tensor, ids: torch.Tensor, base: Optional[torch.Tensor] = None, out=None, err=None,
+                 stream=None) -> torch.Tensor:
+        """x [M,K] bf16, ids [M] int64 (the row's adapter, -1: none), base [M,N] bf16 or
+        fp32 (what the projection left; None: zeros) -> base + the adapters' part,
+        [M,N].  out may be base if the types are the same.  Device errors go to err, an
+        error_word() (default: this object's)."""
+        M, index = x.shape[0], self._index
+        xp = _ready("LoraAdapters", "x", x, torch.bfloat16, (M, self.K), index)
+        ip = _ready("LoraAdapters", "ids", ids, torch.int64, (M,), index)
+        if M > self.max_tokens:
+            raise ValueError(f"LoraAdapters: at most {self.max_tokens} rows, got {M}")
+        bp, bd = None, 0
+        if base is not None:
+            if base.dtype not in _OUT_DTYPES:
+                raise TypeError(f"LoraAdapters: base must be torch.bfloat16 or torch.float32, got {base.dtype}")
+            bd = _OUT_DTYPES[base.dtype]
+            bp = _ready("LoraAdapters", "base", base, base.dtype, (M, self.N), index)
+        if out is None:
+            out = _empty((M, self.N), self.out_dtype, x.device, stream)
+            op = out.data_ptr()
+        else:
+            op = _ready("LoraAdapters", "out", out, self.out_dtype, (M, self.N), index)
+            _apart("LoraAdapters", "out", out, x=x, ids=ids, a=self.a, b=self.b, scaling=self.scaling,
+                   base=None if op == bp and bd == self._code else base)
+        ep = self._err if err is None else _word("LoraAdapters", err, index)
+        raw = _current_raw(index) if stream is None else _raw_stream(stream, index)
+        if raw != self._home and raw not in self._others:
+            self._lend(stream, raw)
+        rc = _call(index, load().ep_lora, xp, M, self.K, ip, *self._mid, bp, bd, op, self._code, *self._ws, ep, raw)
+        if rc:
+            _check(rc, "LoraAdapters")
+        return out

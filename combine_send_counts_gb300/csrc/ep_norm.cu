@@ -1,0 +1,493 @@
+// Root-mean-square norm in front of a layer, with the residual's addition and
+// 8-bit rows, and its backward pass.
+//
+//   h = x + r;  y = h * (mean(h^2) + eps)^-1/2 * w
+//   dh = rs * (g w - n * mean(g w n)) + dr,  dw = sum over rows of g n,
+//   with rs = (mean(h^2) + eps)^-1/2, n = h rs, g = dy.
+//
+// Bound by HBM: every element is read once and written once, its row being
+// held in a block's registers between the sum of squares and its use.
+#include <algorithm>
+#include <type_traits>
+
+#include "ep_device.cuh"
+#include "ep_fp8.cuh"
+#include "ep_internal.h"
+#include "ep_launch.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kMaxH = 32768;
+constexpr int kMostVectors = 4;    // of 8 columns, a thread
+constexpr int kSMs = 152;          // a GB300's
+
+enum { kNone = 0, kBf16 = 1, kFp32 = 2 };
+
+// Eight neighbouring columns as loaded.
+template <int TYPE>
+struct Eight {
+    uint4 v[TYPE == kFp32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void *p, int64_t at, bool ok)
+    {
+        if constexpr (TYPE != kNone) {
+#pragma unroll
+            for (int i = 0; i < (TYPE == kFp32 ? 2 : 1); ++i) {
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (ok)
+                    v[i] = ld_global_stream(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) +
+                                                                            at * (TYPE == kFp32 ? 4 : 2)) + i);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        if (TYPE == kBf16) {
+            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = bf16_lo(w[i]);
+                f[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else if (TYPE == kFp32) {
+            const uint4 a = v[0], b = v[TYPE == kFp32];
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] = __uint_as_float(w[i]);
+        }
+    }
+
+    __device__ __forceinline__ void set(const float (&f)[8])
+    {
+        if (TYPE == kBf16) {
+            v[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                              pack_bf16x2(f[6], f[7]));
+        } else if (TYPE == kFp32) {
+            v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                              __float_as_uint(f[3]));
+            v[TYPE == kFp32] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                                          __float_as_uint(f[7]));
+        }
+    }
+
+    __device__ __forceinline__ void store(void *p, int64_t at) const
+    {
+#pragma unroll
+        for (int i = 0; i < (TYPE == kFp32 ? 2 : 1); ++i)
+            st_stream(reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p) + at * (TYPE == kFp32 ? 4 : 2)) + i, v[i]);
+    }
+};
+
+// Eight weights of either type; ones without.
+__device__ __forceinline__ void load_weights(const void *w, int w_dtype, int at, bool ok, float (&f)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[i] = 1.0f;
+    if (w == nullptr || !ok)
+        return;
+    if (w_dtype == 0) {
+        Eight<kBf16> e;
+        e.v[0] = ld_global(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(w) + (int64_t)at * 2));
+        e.get(f);
+    } else {
+        Eight<kFp32> e;
+        e.v[0] = ld_global(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(w) + (int64_t)at * 4));
+        e.v[1] = ld_global(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(w) + (int64_t)at * 4) + 1);
+        e.get(f);
+    }
+}
+
+// Sums of N values over the block, the same bits in every thread.  s: [2][32][N].
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float *s, int &phase)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        for (int o = 16; o > 0; o >>= 1)
+            v[i] = __fadd_rn(v[i], __shfl_xor_sync(kFull, v[i], o));
+    float *mine = s + phase * 32 * N;   // the other half may still be read
+    phase ^= 1;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            mine[(threadIdx.x >> 5) * N + i] = v[i];
+    __syncthreads();
+    const int warps = blockDim.x >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = mine[i];
+    for (int w = 1; w < warps; ++w)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = __fadd_rn(v[i], mine[w * N + i]);
+}
+
+__device__ __forceinline__ float inverse_root(float squares, int H, float eps)
+{
+    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, (float)H), eps)));
+}
+
+struct Norm {
+    const void *x, *residual, *w;
+    int64_t T;
+    int H, w_dtype;
+    float eps;
+    void *sum, *y;
+    uint8_t *q;
+    ScaleSpec scale;
+};
+
+// The largest magnitude of the 128 columns that 16 neighbouring lanes hold.
+__device__ __forceinline__ float half_warp_max(float m)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    return m;
+}
+
+// The scale of a group whose largest magnitude is m, its reciprocal and UE8M0 code.
+__device__ __forceinline__ void group_scale(float m, bool power_of_two, float &scale, float &inverse, uint32_t &code)
+{
+    const float a = fmaxf(m, 1e-4f);
+    scale = __fdiv_rn(a, 448.0f);
+    code = 0;
+    if (power_of_two) {
+        const uint32_t b = __float_as_uint(scale);
+        code = (b >> 23) + ((b & 0x7fffffu) != 0u);
+        scale = __uint_as_float(code << 23);
+        inverse = code < 255u ? __uint_as_float((254u - code) << 23) : 0.0f;
+    } else {
+        inverse = __fdiv_rn(448.0f, a);
+    }
+}
+
+template <int RES, int NV, int SF, int MOST>
+__global__ void __launch_bounds__(MOST)
+norm_kernel(Norm a)
+{
+    constexpr int SUM = RES == kNone ? kBf16 : RES;   // what the sum is held in
+    __shared__ float s[2 * 32];
+    const int64_t row = (int64_t)blockIdx.x * a.H;
+    grid_dependency_wait();
+    allow_dependents();
+    Eight<SUM> h[NV];
+    {
+        Eight<kBf16> x[NV];
+        Eight<RES> r[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * 8;
+            x[i].load(a.x, row + c, c < a.H);
+            r[i].load(a.residual, row + c, c < a.H);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[8], g[8];
+            x[i].get(f);
+            if (RES != kNone) {
+                r[i].get(g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[j] = __fadd_rn(f[j], g[j]);
+            }
+            h[i].set(f);
+        }
+    }
+    float squares[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * 8;
+        float f[8];
+        h[i].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            squares[0] = __fmaf_rn(f[j], f[j], squares[0]);
+        if (a.sum != nullptr && c < a.H)
+            h[i].store(a.sum, row + c);
+    }
+    int phase = 0;
+    block_sums(squares, s, phase);
+    const float rs = inverse_root(squares[0], a.H, a.eps);
+    const int groups = a.H >> 7;
+    const int64_t base = SF < 0 ? 0 : scale_row_base<SF < 0 ? 0 : SF>(a.scale, blockIdx.x, groups);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * 8;
+        float f[8], w[8];
+        h[i].get(f);
+        load_weights(a.w, a.w_dtype, c, c < a.H, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = __fmul_rn(__fmul_rn(f[j], rs), w[j]);
+        if (a.y != nullptr && c < a.H) {
+            Eight<kBf16> o;
+            o.set(f);
+            o.store(a.y, row + c);
+        }
+        if (SF >= 0) {
+            float m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                m = fmaxf(m, fabsf(f[j]));   // a NaN does not enter it
+            float scale, inverse;
+            uint32_t code;
+            group_scale(half_warp_max(m), a.scale.round != 0, scale, inverse, code);
+            uint32_t p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                p[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(
+                    mul2_rn(make_float2(f[2 * j], f[2 * j + 1]), make_float2(inverse, inverse)), __NV_SATFINITE,
+                    __NV_E4M3);
+            if (c < a.H) {
+                st_stream(reinterpret_cast<uint2 *>(a.q + row + c), make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16));
+                if ((threadIdx.x & 15) == 0)
+                    put_scale<SF < 0 ? 0 : SF>(a.scale, base, c >> 7, scale, code);
+            }
+        }
+    }
+}
+
+struct NormBackward {
+    const void *dy, *h, *dres, *w;
+    int64_t T;
+    int H, w_dtype;
+    float eps;
+    void *dh, *dx;
+    float *partial;     // [blocks][H], or null: no dw
+};
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; the block's part of dw stays in registers.
+template <int RES, int NV, int MOST>
+__global__ void __launch_bounds__(MOST)
+norm_backward_kernel(NormBackward a)
+{
+    __shared__ float s[2 * 32 * 2];
+    grid_dependency_wait();
+    allow_dependents();
+    float dw[NV][8] = {}, w[NV][8];
+    int phase = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * 8;
+        load_weights(a.w, a.w_dtype, c, c < a.H, w[i]);
+    }
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const int64_t row = t * a.H;
+        Eight<kBf16> g[NV];
+        Eight<RES> h[NV], r[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * 8;
+            g[i].load(a.dy, row + c, c < a.H);
+            h[i].load(a.h, row + c, c < a.H);
+            r[i].load(a.dres, row + c, c < a.H && a.dres != nullptr);
+        }
+        float sums[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float fg[8], fh[8];
+            g[i].get(fg);
+            h[i].get(fh);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sums[0] = __fmaf_rn(fh[j], fh[j], sums[0]);
+                sums[1] = __fmaf_rn(__fmul_rn(fg[j], w[i][j]), fh[j], sums[1]);
+            }
+        }
+        block_sums(sums, s, phase);
+        const float rs = inverse_root(sums[0], a.H, a.eps);
+        const float mean = __fdiv_rn(__fmul_rn(sums[1], rs), (float)a.H);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * 8;
+            float fg[8], fh[8], fr[8], d[8];
+            g[i].get(fg);
+            h[i].get(fh);
+            r[i].get(fr);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float n = __fmul_rn(fh[j], rs);
+                dw[i][j] = __fmaf_rn(fg[j], n, dw[i][j]);
+                d[j] = __fmaf_rn(rs, __fmaf_rn(-n, mean, __fmul_rn(fg[j], w[i][j])), fr[j]);
+            }
+            if (c < a.H) {
+                Eight<RES> o;
+                o.set(d);
+                if (a.dh != nullptr)
+                    o.store(a.dh, row + c);
+                if (a.dx != nullptr) {
+                    Eight<kBf16> b;
+                    b.set(d);
+                    b.store(a.dx, row + c);
+                }
+            }
+        }
+    }
+    if (a.partial == nullptr)
+        return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * 8;
+        if (c < a.H) {
+            float4 *p = reinterpret_cast<float4 *>(a.partial + (int64_t)blockIdx.x * a.H + c);
+            p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+            p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+        }
+    }
+}
+
+// dw: the blocks' parts added in their order, 32 columns to a block, 16 runs of parts side by side.
+constexpr int kJoinRuns = 16;
+
+__global__ void __launch_bounds__(32 * kJoinRuns)
+norm_join_kernel(const float *partial, int parts, int H, float *dw)
+{
+    __shared__ float s[kJoinRuns][32];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+    const int from = parts * run / kJoinRuns, to = parts * (run + 1) / kJoinRuns;
+    grid_dependency_wait();
+    allow_dependents();
+    float v = 0.0f;
+    if (c < H)
+        for (int p = from; p < to; ++p)
+            v = __fadd_rn(v, __uint_as_float(ld_global(reinterpret_cast<const uint32_t *>(partial) + (int64_t)p * H + c)));
+    s[run][threadIdx.x & 31] = v;
+    __syncthreads();
+    if (run == 0 && c < H) {
+        for (int i = 1; i < kJoinRuns; ++i)
+            v = __fadd_rn(v, s[i][threadIdx.x]);
+        dw[c] = v;
+    }
+}
+
+// Vectors of 8 columns a thread, and threads: one where rows are few or short, as a row's latency is all there.
+struct Shape {
+    int vectors, threads;
+};
+
+Shape shape_of(int H, bool few)
+{
+    const int v = H / 8;
+    const int n = v <= 1024 && (few || v <= 128) ? 1 : kMostVectors;
+    return {n, (int)align_up(ceil_div(v, n), 32)};
+}
+
+// f with the number of vectors and the most threads of its kernel as constants.
+template <class F>
+int with_shape(const Shape &s, F &&f)
+{
+    if (s.vectors == 1)
+        return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1024>());
+    if (s.threads <= 256)
+        return f(std::integral_constant<int, kMostVectors>(), std::integral_constant<int, 256>());
+    return f(std::integral_constant<int, kMostVectors>(), std::integral_constant<int, 1024>());
+}
+
+template <int RES>
+int launch_norm(const Norm &a, cudaStream_t stream)
+{
+    const Shape s = shape_of(a.H, a.T <= kSMs);
+    return with_shape(s, [&](auto nv, auto most) {
+        constexpr int NV = decltype(nv)::value, MOST = decltype(most)::value;
+        const dim3 grid((unsigned)a.T);
+        if (a.q == nullptr)
+            return launch_dependent(norm_kernel<RES, NV, -1, MOST>, grid, s.threads, 0, stream, a);
+        switch (a.scale.fmt) {
+        case EP_SCALE_ROW_F32:
+            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_ROW_F32, MOST>, grid, s.threads, 0, stream, a);
+        case EP_SCALE_COL_F32:
+            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_COL_F32, MOST>, grid, s.threads, 0, stream, a);
+        default:
+            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_COL_UE8M0, MOST>, grid, s.threads, 0, stream, a);
+        }
+    });
+}
+
+// Parts of dw: a constant, so that results do not depend on where they are computed.
+constexpr int kParts = 2 * kSMs;
+
+int parts_of(int64_t T) { return (int)std::min<int64_t>(T, kParts); }
+
+template <int RES>
+int launch_norm_backward(const NormBackward &a, cudaStream_t stream)
+{
+    const Shape s = shape_of(a.H, a.T <= kSMs);
+    return with_shape(s, [&](auto nv, auto most) {
+        return launch_dependent(norm_backward_kernel<RES, decltype(nv)::value, decltype(most)::value>,
+                                dim3((unsigned)parts_of(a.T)), s.threads, 0, stream, a);
+    });
+}
+
+bool rows_ok(const void *p) { return p == nullptr || aligned(p, 16); }
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_add_rms_norm(const void *x, const void *residual, int res_dtype, int64_t T, int H, const void *w,
+                               int w_dtype, float eps, void *sum, void *y, uint8_t *q, void *scale, int scale_fmt,
+                               int round_scale, ep_stream_t stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (T < 0 || H < 8 || H % 8 != 0 || !(eps >= 0.0f))
+        return EP_ERR_INVALID_ARG;
+    if (q != nullptr && (scale_fmt < EP_SCALE_ROW_F32 || scale_fmt > EP_SCALE_COL_UE8M0 ||
+                         (round_scale != 0 && round_scale != 1)))
+        return EP_ERR_INVALID_ARG;
+    if ((res_dtype != 0 && res_dtype != 1) || (w_dtype != 0 && w_dtype != 1) || H > kMaxH || T > INT32_MAX)
+        return EP_ERR_UNSUPPORTED;
+    if (q != nullptr && (H % 128 != 0 || (scale_fmt == EP_SCALE_COL_UE8M0 && (round_scale != 1 || H % 512 != 0))))
+        return EP_ERR_UNSUPPORTED;
+    if (T == 0)
+        return EP_OK;
+    if (x == nullptr || (y == nullptr && q == nullptr && sum == nullptr) || !rows_ok(x) || !rows_ok(residual) ||
+        !rows_ok(w) || !rows_ok(sum) || !rows_ok(y) || !rows_ok(q) ||
+        (q != nullptr && (scale == nullptr || !aligned(scale, 4))))
+        return EP_ERR_INVALID_ARG;
+    const Norm a{x, residual, w, T, H, w_dtype, eps, sum, y, q, ScaleSpec{scale, scale_fmt, round_scale, (int)T}};
+    if (residual == nullptr)
+        return launch_norm<kNone>(a, stream);
+    return res_dtype == 0 ? launch_norm<kBf16>(a, stream) : launch_norm<kFp32>(a, stream);
+}
+
+extern "C" size_t ep_rms_norm_backward_workspace_size(int64_t T, int H)
+{
+    if (T < 0 || H < 1)
+        return 0;
+    return align_up((size_t)parts_of(T) * H * sizeof(float), kWsAlign) + kWsAlign;
+}
+
+extern "C" int ep_add_rms_norm_backward(const void *dy, const void *h, const void *dresidual, int res_dtype, int64_t T,
+                                        int H, const void *w, int w_dtype, float eps, void *dh, void *dx, float *dw,
+                                        void *ws, size_t ws_bytes, ep_stream_t stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (T < 0 || H < 8 || H % 8 != 0 || !(eps >= 0.0f))
+        return EP_ERR_INVALID_ARG;
+    if ((res_dtype != 0 && res_dtype != 1) || (w_dtype != 0 && w_dtype != 1) || H > kMaxH || T > INT32_MAX)
+        return EP_ERR_UNSUPPORTED;
+    if (T == 0) {   // a sum of nothing
+        if (dw != nullptr && cudaMemsetAsync(dw, 0, (size_t)H * sizeof(float), stream) != cudaSuccess) {
+            cudaGetLastError();
+            return EP_ERR_CUDA;
+        }
+        return EP_OK;
+    }
+    if (dy == nullptr || h == nullptr || (dh == nullptr && dx == nullptr && dw == nullptr) || !rows_ok(dy) ||
+        !rows_ok(h) || !rows_ok(dresidual) || !rows_ok(w) || !rows_ok(dh) || !rows_ok(dx) || !aligned(dw, 4) ||
+        (dw != nullptr && (ws == nullptr || !aligned(ws, kWsAlign) ||
+                           ws_bytes < ep_rms_norm_backward_workspace_size(T, H))))
+        return EP_ERR_INVALID_ARG;
+    const NormBackward a{dy, h, dresidual, w, T, H, w_dtype, eps, dh, dx, dw == nullptr ? nullptr : static_cast<float *>(ws)};
+    const int rc = res_dtype == 0 ? launch_norm_backward<kBf16>(a, stream) : launch_norm_backward<kFp32>(a, stream);
+    if (rc != EP_OK || dw == nullptr)
+        return rc;
+    return launch_dependent(norm_join_kernel, dim3((unsigned)ceil_div(H, 32)), 32 * kJoinRuns, 0, stream,
+                            static_cast<const float *>(ws), parts_of(T), H, dw);
+}

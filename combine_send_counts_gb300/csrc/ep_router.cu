@@ -29,6 +29,7 @@
 #include "ep_device.cuh"
 #include "ep_internal.h"
 #include "ep_launch.cuh"
+#include "ep_select.cuh"
 #include "ep_skinny.cuh"
 
 namespace ep {
@@ -332,6 +333,13 @@ int launch_logits(const LogitsArgs &a, cudaStream_t stream)
     return launch_dependent(router_logits_kernel<TERMS, 2>, grid, kThreads, 0, stream, a);
 }
 
+int launch_logits(const void *x, int64_t T, int H, const void *w, int w_dtype, int E, int slices, float *sums,
+                  cudaStream_t stream)
+{
+    const LogitsArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), (int)T, H, E, slices, sums};
+    return w_dtype == 1 ? launch_logits<3>(a, stream) : launch_logits<1>(a, stream);
+}
+
 }  // namespace
 }  // namespace ep
 
@@ -347,34 +355,74 @@ extern "C" size_t ep_router_workspace_size(int64_t T, int H, int E)
     return align_up(rows * E * sizeof(float), kWsAlign) + kWsAlign;
 }
 
-extern "C" int ep_router_topk(const void *x, int64_t T, int H, const void *w, int w_dtype, int E, const float *bias,
-                              int K, int scoring, int renormalize, float scale, int64_t *topk_idx,
-                              float *topk_weights, float *logits, void *ws, size_t ws_bytes, ep_stream_t stream_)
+// Whether the call goes on: EP_OK with *done unset.
+static int router_arguments(const void *x, int64_t T, int H, const void *w, int w_dtype, int E, int K, int scoring,
+                            const int64_t *topk_idx, const float *topk_weights, const void *ws, size_t ws_bytes,
+                            bool *done)
 {
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (T < 0 || H < 8 || H % 8 != 0 || E < 1 || E > EP_MAX_EXPERTS || K < 1 || K > EP_MAX_TOPK || K > E ||
         (scoring != EP_SCORE_SOFTMAX && scoring != EP_SCORE_SIGMOID))
         return EP_ERR_INVALID_ARG;
     if ((w_dtype != 0 && w_dtype != 1) || T > (1 << 20))
         return EP_ERR_UNSUPPORTED;
-    if (T == 0)
+    if (T == 0) {
+        *done = true;
         return EP_OK;
+    }
     if (x == nullptr || w == nullptr || topk_idx == nullptr || topk_weights == nullptr || !aligned(x, 16) ||
         !aligned(w, 16) || ws == nullptr || !aligned(ws, kWsAlign) || ws_bytes < ep_router_workspace_size(T, H, E))
         return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+extern "C" int ep_router_topk(const void *x, int64_t T, int H, const void *w, int w_dtype, int E, const float *bias,
+                              int K, int scoring, int renormalize, float scale, int64_t *topk_idx,
+                              float *topk_weights, float *logits, void *ws, size_t ws_bytes, ep_stream_t stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    bool done = false;
+    int rc = router_arguments(x, T, H, w, w_dtype, E, K, scoring, topk_idx, topk_weights, ws, ws_bytes, &done);
+    if (rc != EP_OK || done)
+        return rc;
     // for every E: the kernel's static part counts toward the 48 KB that need no raising
     static PerDevice set;
-    int rc = raise_smem(router_select_kernel, 2 * EP_MAX_EXPERTS * sizeof(float), set);
+    rc = raise_smem(router_select_kernel, 2 * EP_MAX_EXPERTS * sizeof(float), set);
     if (rc != EP_OK)
         return rc;
     const int slices = slices_of(T, H, E);
     float *sums = static_cast<float *>(ws);
-    const LogitsArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), (int)T, H, E, slices, sums};
-    rc = w_dtype == 1 ? launch_logits<3>(a, stream) : launch_logits<1>(a, stream);
+    rc = launch_logits(x, T, H, w, w_dtype, E, slices, sums, stream);
     if (rc != EP_OK)
         return rc;
     const Select s{sums, bias, (int)T, E, K, slices, scoring == EP_SCORE_SIGMOID, renormalize, scale, topk_idx,
                    topk_weights, logits};
     return launch_dependent(router_select_kernel, dim3((unsigned)T), kSelectThreads, 2 * (size_t)E * sizeof(float), stream,
                             s);
+}
+
+extern "C" int ep_router_topk_groups(const void *x, int64_t T, int H, const void *w, int w_dtype, int E,
+                                     const float *bias, int K, int scoring, int num_groups, int topk_groups,
+                                     int group_score, int renormalize, float scale, int64_t *topk_idx,
+                                     float *topk_weights, float *logits, void *ws, size_t ws_bytes,
+                                     ep_stream_t stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    int rc = choice_status(E, K, scoring, num_groups, topk_groups, group_score);
+    if (rc != EP_OK)
+        return rc;
+    if (num_groups == 1)
+        return ep_router_topk(x, T, H, w, w_dtype, E, bias, K, scoring, renormalize, scale, topk_idx, topk_weights,
+                              logits, ws, ws_bytes, stream_);
+    bool done = false;
+    rc = router_arguments(x, T, H, w, w_dtype, E, K, scoring, topk_idx, topk_weights, ws, ws_bytes, &done);
+    if (rc != EP_OK || done)
+        return rc;
+    const int slices = slices_of(T, H, E);
+    float *sums = static_cast<float *>(ws);
+    rc = launch_logits(x, T, H, w, w_dtype, E, slices, sums, stream);
+    if (rc != EP_OK)
+        return rc;
+    const Choice c{sums, 0, slices, bias, (int)T, E, K, scoring == EP_SCORE_SIGMOID, num_groups, topk_groups,
+                   group_score == EP_GROUP_TOP2, renormalize, scale, topk_idx, topk_weights, logits};
+    return launch_choice(c, stream);
 }

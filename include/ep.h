@@ -634,6 +634,106 @@ int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weig
                   int I, int E, int E_local, int rank, const ep_matrix *w13, const ep_matrix *w2, void *out,
                   int out_dtype, void *ws, size_t ws_bytes, int32_t *err, ep_stream_t stream);
 
+/* ------------------------------------------------- around the routing --
+ * What stands next to the routing in a layer: the norm in front of it, the choice
+ * of experts where the logits are there already, and low-rank adapters beside a
+ * projection.  The norm and the choice have backward passes. */
+
+/* Root-mean-square norm with the residual's addition:
+ *   h = x + residual, rounded to the residual's type (h = x without one);
+ *   y = h * (mean(h^2) + eps)^(-1/2) * w, the mean over a row, in fp32.
+ *   x [T,H] bf16, H % 8 == 0, H <= 32768, T < 2^31 (else EP_ERR_UNSUPPORTED).
+ *   residual [T,H] bf16 (res_dtype 0) or fp32 (1), or NULL.
+ *   w [H] bf16 (w_dtype 0) or fp32 (1), or NULL for ones.
+ * Outputs, NULL where not wanted:
+ *   sum [T,H] in the residual's type (bf16 without one): h.  May be residual.
+ *   y [T,H] bf16.  May be x.
+ *   q [T,H] e4m3 codes of y before its rounding to bf16, with scale in scale_fmt, as
+ *     ep_batched_prepare_fp8 defines them (round_scale too), for one expert of T
+ *     rows: EP_SCALE_ROW_F32 [T,H/128], EP_SCALE_COL_F32 [H/128,T],
+ *     EP_SCALE_COL_UE8M0 int32 [H/512,T].  Needs H % 128 == 0 (UE8M0: round_scale = 1
+ *     and H % 512 == 0), else EP_ERR_UNSUPPORTED.
+ * Arrays that are not the same one must not overlap.  x, residual, w, sum, y and q
+ * start 16-byte aligned.  The same call on the same inputs gives the same bits. */
+int ep_add_rms_norm(const void *x, const void *residual, int res_dtype, int64_t T, int H, const void *w, int w_dtype,
+                    float eps, void *sum, void *y, uint8_t *q, void *scale, int scale_fmt, int round_scale,
+                    ep_stream_t stream);
+
+/* The backward pass of ep_add_rms_norm, from h (its `sum`; x without a residual),
+ * the gradient dy [T,H] bf16 of y, and dresidual, the gradient that reaches h by
+ * another way (the residual's own), in h's type (res_dtype), or NULL:
+ *   rs = (mean(h^2) + eps)^(-1/2),  n = h * rs,  g = dy * w,
+ *   dh = rs * (g - n * mean(g * n)) + dresidual,   dw = sum over rows of dy * n.
+ * dh is the gradient of both x and residual.  Outputs, NULL where not wanted:
+ *   dh [T,H] in h's type.  May be dresidual, or dy where h is bf16.
+ *   dx [T,H] bf16: dh rounded to x's type (for h in fp32).  May be dy.
+ *   dw [H] fp32, with ws of ep_rms_norm_backward_workspace_size(T, H) bytes, 256-byte
+ *     aligned, scratch (not used without dw).  Calls that overlap on the GPU must
+ *     not share it.  Rows are added in an order that the sizes alone decide.
+ * Sizes, types and alignments as ep_add_rms_norm. */
+size_t ep_rms_norm_backward_workspace_size(int64_t T, int H);
+int ep_add_rms_norm_backward(const void *dy, const void *h, const void *dresidual, int res_dtype, int64_t T, int H,
+                             const void *w, int w_dtype, float eps, void *dh, void *dx, float *dw, void *ws,
+                             size_t ws_bytes, ep_stream_t stream);
+
+/* The choice of experts of ep_router_topk from logits that are there already, for
+ * any number of tokens, with groups of experts.
+ *   logits [T,E] fp32 (dtype 0) or bf16 (1); scoring, bias, K, renormalize, scale,
+ *   topk_idx and topk_weights as ep_router_topk (NaN logits are never chosen).
+ *   num_groups: the experts are num_groups runs of E / num_groups.  A group's mark is
+ *     EP_GROUP_MAX: its largest key (score + bias, or the logit without a bias);
+ *     EP_GROUP_TOP2: the sum of its two largest, of score + bias, or of scores
+ *     without a bias (of one, where only one can be chosen).
+ *     Experts are chosen in the topk_groups groups of the largest marks, the lower
+ *     group on equal ones.  1 and 1: no groups.
+ * Keys and marks are compared as 64-bit arithmetic makes them of the logits.
+ * The same call on the same inputs gives the same bits.
+ * 1 <= K <= min(E, 32), E <= 8192, num_groups <= 64, T < 2^31. */
+#define EP_GROUP_MAX 0
+#define EP_GROUP_TOP2 1
+int ep_router_select(const void *logits, int dtype, int64_t T, int E, const float *bias, int K, int scoring,
+                     int num_groups, int topk_groups, int group_score, int renormalize, float scale, int64_t *topk_idx,
+                     float *topk_weights, ep_stream_t stream);
+
+/* ep_router_topk with the groups of ep_router_select (num_groups 1 and topk_groups
+ * 1 is ep_router_topk). */
+int ep_router_topk_groups(const void *x, int64_t T, int H, const void *w, int w_dtype, int E, const float *bias, int K,
+                          int scoring, int num_groups, int topk_groups, int group_score, int renormalize, float scale,
+                          int64_t *topk_idx, float *topk_weights, float *logits, void *ws, size_t ws_bytes,
+                          ep_stream_t stream);
+
+/* The gradient of the logits of ep_router_select (or ep_router_topk), whose choice
+ * is held fixed, from dweights [T,K] fp32, the gradient of topk_weights:
+ *   dlogits [T,E] in the logits' type, all of it written.
+ * Slots of -1 are left out; an expert that several slots name gets their sum.
+ * Logits of NaN and -inf get 0.  dlogits must not overlap the inputs.
+ * Device errors: EP_ERR_INVALID_EXPERT (an id outside [-1, E): the slot is left
+ * out). */
+int ep_router_select_backward(const void *logits, int dtype, int64_t T, int E, const int64_t *topk_idx,
+                              const float *dweights, int K, int scoring, int renormalize, float scale, void *dlogits,
+                              int32_t *err, ep_stream_t stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   out[m] = base[m] + scaling[i] * B[i] (A[i] x[m]),  i = ids[m];
+ *   out[m] = base[m] where ids[m] is -1.
+ *   x [M,K] bf16, ids [M] int64; a [L,R,K] and b [L,N,R] bf16, the L adapters (a
+ *     smaller rank is padded with zeros); scaling [L] fp32, or NULL for ones.
+ *   base [M,N] bf16 (base_dtype 0) or fp32 (1): what the projection left, or NULL for
+ *     zeros.  out [M,N] bf16 (out_dtype 0) or fp32 (1); may be base if the types
+ *     are the same.
+ * Sums are fp32; the result is rounded once.
+ *   K, N, R % 8 == 0, R <= 128; M, K, N <= 2^24 (else EP_ERR_UNSUPPORTED).
+ *   Up to 1024 rows may name adapters in any order; with more, rows of one adapter
+ *   are best neighbours (16 rows are gone over once for each adapter among them).
+ *   ws: ep_lora_workspace_size(M, R) bytes, 256-byte aligned, scratch.  Calls that
+ *     overlap on the GPU must not share it.
+ * The same call on the same inputs gives the same bits.
+ * Device errors: EP_ERR_INVALID_EXPERT (an id outside [-1, L): taken as -1). */
+size_t ep_lora_workspace_size(int64_t M, int R);
+int ep_lora(const void *x, int64_t M, int K, const int64_t *ids, const void *a, const void *b, const float *scaling,
+            int L, int R, int N, const void *base, int base_dtype, void *out, int out_dtype, void *ws, size_t ws_bytes,
+            int32_t *err, ep_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
