@@ -190,6 +190,410 @@ select_kernel(Choice c)
     }
 }
 
+// ------------------------------------------- up to 512 experts: a warp a token --
+// Lanes share the groups out evenly: `per` lanes (a power of two) to a group, C
+// neighbouring experts of it to a lane.  Keys are fp32 with a bound on what they
+// are off by; the K largest are taken one at a time, the warp's best by one
+// reduction.  Where two keys, or two marks, that decide something are nearer than
+// their bounds allow, the few candidates are compared in 64 bits.
+//
+// The bounds, in units u = 2^-24 (ex2.approx 4u of its result, rcp.approx 2u):
+//   sigmoid: an exponential off by 4u + 1.5 |l| u of itself moves the score by at
+//     most (1 + 0.34) u, as s (1 - s) <= 1/4 and |l| s (1 - s) <= 0.23; 1 + e
+//     and the reciprocal by 3u: below 8u in all.
+//   softmax: exponentials of x = l - max off by (4 + 2.6 |x|) u of themselves; their sum by
+//     (4 + 2.6 log E) u, as the mean of |x| is at most log E, and 21 u for its
+//     additions: below 64 u of the score, and u as |x| e^-|x| <= 0.37.
+//   the addition of the bias: u of the key.
+constexpr float kU = 1.0f / (1 << 24);
+
+__device__ __forceinline__ float exp2_quick(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float reciprocal_quick(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+constexpr float kLog2e = 1.44269504f;
+constexpr float kLeastLog = -745.0f;   // logarithm of the least score that 64 bits tell from 0
+
+// order-preserving map of floats to unsigned (-inf maps to kNone, +0 above -0)
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    const uint32_t b = __float_as_uint(v);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float unordered(uint32_t v)
+{
+    return __uint_as_float(v & 0x80000000u ? v & 0x7fffffffu : ~v);
+}
+
+constexpr uint32_t kNone = 0x007fffffu;
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+    for (int o = 16; o > 0; o >>= 1)
+        v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(kFull, ordered(v))); }
+
+__device__ __forceinline__ float warp_min(float v) { return unordered(__reduce_min_sync(kFull, ordered(v))); }
+
+__device__ __forceinline__ double warp_sum64(double v)
+{
+    for (int o = 16; o > 0; o >>= 1)
+        v += shfl_xor64(v, o);
+    return v;
+}
+
+// A token's 64-bit scores, for the comparisons that need them.
+__device__ __noinline__ Score64 scores64(const Choice &c, int64_t t, float mx)
+{
+    Score64 s{c.sigmoid, (double)mx, 1.0};
+    if (!c.sigmoid) {
+        double part = 0.0;
+        for (int e = threadIdx.x & 31; e < c.E; e += 32)
+            part += s(logit_of(c, t, e));
+        s.sum = warp_sum64(part);
+    }
+    return s;
+}
+
+__device__ __forceinline__ double key64(const Choice &c, const Score64 &score, float l, int e)
+{
+    const double k = isnan(l) ? neg_inf64() : c.bias != nullptr ? score(l) + (double)ld_float(c.bias + e) : (double)l;
+    return isnan(k) ? neg_inf64() : k + 0.0;
+}
+
+// A lane's experts.
+struct Share {
+    int first, count;   // neighbours, of group `group`
+    int group, per;     // lanes to a group
+};
+
+// Which groups stay, by marks in 64 bits: a bit for each group.
+__device__ __noinline__ uint32_t groups64(const Choice &c, int64_t t, float mx, Share mine)
+{
+    const Score64 score = scores64(c, t, mx);
+    const bool of_scores = c.top2 && c.bias == nullptr;
+    double a = neg_inf64(), b = neg_inf64();
+    for (int i = 0; i < mine.count; ++i) {
+        const float l = logit_of(c, t, mine.first + i);
+        double k = key64(c, score, l, mine.first + i);
+        if (k != neg_inf64() && of_scores)
+            k = score(l);
+        b = fmax(b, fmin(a, k));
+        a = fmax(a, k);
+    }
+    for (int o = 1; o < mine.per; o *= 2) {
+        const double a2 = shfl_xor64(a, o), b2 = shfl_xor64(b, o);
+        b = fmax(fmin(a, a2), fmax(b, b2));
+        a = fmax(a, a2);
+    }
+    const double mark = c.top2 && b != neg_inf64() ? a + b : a;
+    int ahead = 0;
+    for (int o = 0; o < c.groups; ++o) {
+        const double m = __shfl_sync(kFull, mark, o * mine.per);
+        ahead += m > mark || (m == mark && o < mine.group);
+    }
+    const bool stays = mine.group < c.groups && ahead < c.kept;
+    return __reduce_or_sync(kFull, stays ? 1u << mine.group : 0u);
+}
+
+// The K largest of the candidates (bit i of `mask`: this lane's expert first + i) by keys in 64 bits; lane k gets the
+// k-th, or -1.
+__device__ __noinline__ int choose64(const Choice &c, int64_t t, float mx, Share mine, uint32_t mask)
+{
+    const int lane = threadIdx.x & 31;
+    const Score64 score = scores64(c, t, mx);
+    int chosen = -1;
+    int before = 0, all = 0;   // candidates in the lanes before this one, and in all
+    for (int o = 0; o < 32; ++o) {
+        const int n = __popc(__shfl_sync(kFull, mask, o));
+        before += o < lane ? n : 0;
+        all += n;
+    }
+    if (all <= 32) {   // one to a lane, ranked
+        int e = -1;
+        for (int o = 0; o < 32; ++o) {
+            const uint32_t m = __shfl_sync(kFull, mask, o);
+            const int b = __shfl_sync(kFull, before, o), f = __shfl_sync(kFull, mine.first, o);
+            if (lane >= b && lane < b + __popc(m)) {
+                uint32_t left = m;
+                for (int skip = lane - b; skip > 0; --skip)
+                    left &= left - 1u;
+                e = f + __ffs(left) - 1;
+            }
+        }
+        const double k = e >= 0 ? key64(c, score, logit_of(c, t, e), e) : neg_inf64();
+        int ahead = 0;
+        for (int o = 0; o < all; ++o) {
+            const double u = __shfl_sync(kFull, k, o);
+            const int f = __shfl_sync(kFull, e, o);
+            ahead += u > k || (u == k && f < e);
+        }
+        for (int o = 0; o < all; ++o) {
+            const int place = __shfl_sync(kFull, ahead, o), f = __shfl_sync(kFull, e, o);
+            if (place == lane && place < c.K)
+                chosen = f;
+        }
+        return chosen;
+    }
+    for (int k = 0; k < c.K; ++k) {
+        double top = neg_inf64();
+        int at = -1;
+        for (int i = 0; i < mine.count; ++i)
+            if (mask >> i & 1u) {
+                const double u = key64(c, score, logit_of(c, t, mine.first + i), mine.first + i);
+                if (u > top) {
+                    top = u;
+                    at = mine.first + i;
+                }
+            }
+        int e = at;
+        for (int o = 16; o > 0; o >>= 1) {
+            const double u = shfl_xor64(top, o);
+            const int f = __shfl_xor_sync(kFull, e, o);
+            if (u > top || (u == top && (unsigned)f < (unsigned)e)) {
+                top = u;
+                e = f;
+            }
+        }
+        if (e < 0)
+            break;
+        if (e == at)
+            mask &= ~(1u << (e - mine.first));
+        if (lane == k)
+            chosen = e;
+    }
+    return chosen;
+}
+
+template <int C>
+__global__ void __launch_bounds__(kThreads)
+select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    grid_dependency_wait();
+    allow_dependents();
+    if (t >= c.T)
+        return;
+    const int size = c.E / c.groups, group = lane / per, in_group = (lane % per) * C;
+    const int count = group < c.groups ? max(0, min(C, size - in_group)) : 0;
+    const Share mine{group * size + in_group, count, group, per};
+
+    float l[C];
+    if (C % 4 == 0 && wide) {   // fours of experts, whole
+#pragma unroll
+        for (int i = 0; i < C; i += 4) {
+            if (C % 4 != 0)
+                break;
+            if (i < count) {
+                const int64_t at = t * c.E + mine.first + i;
+                if (c.dtype == 0) {
+                    const uint4 v = ld_global(reinterpret_cast<const uint4 *>(static_cast<const float *>(c.logits) + at));
+                    l[i] = __uint_as_float(v.x);
+                    l[(i + 1) % C] = __uint_as_float(v.y);
+                    l[(i + 2) % C] = __uint_as_float(v.z);
+                    l[(i + 3) % C] = __uint_as_float(v.w);
+                } else {
+                    const uint2 v = ld_global(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(c.logits) + at));
+                    l[i] = bf16_lo(v.x);
+                    l[(i + 1) % C] = bf16_hi(v.x);
+                    l[(i + 2) % C] = bf16_lo(v.y);
+                    l[(i + 3) % C] = bf16_hi(v.y);
+                }
+            } else {
+                l[i] = l[(i + 1) % C] = l[(i + 2) % C] = l[(i + 3) % C] = neg_inf();
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            l[i] = i < count ? logit_of(c, t, mine.first + i) : neg_inf();
+    }
+    if (c.sums != nullptr)
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (i < count)
+                c.sums[t * c.E + mine.first + i] = l[i];
+
+    const bool marks_of_scores = c.groups > 1 && c.top2 && c.bias == nullptr;
+    const bool scored = c.bias != nullptr || marks_of_scores;   // something compared is made of scores
+    float mx = 0.0f, sum = 1.0f, off = 8 * kU;   // off: of a score
+    if (!c.sigmoid) {
+        mx = neg_inf();
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            mx = fmaxf(mx, l[i]);
+        mx = warp_max(mx);
+        if (scored || !c.renormalize) {
+            float part = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const float p = l[i] == mx ? 1.0f : exp2_quick(__fmul_rn(__fsub_rn(l[i], mx), kLog2e));
+                part = __fadd_rn(part, i < count && !isnan(l[i]) ? p : 0.0f);
+            }
+            sum = warp_sum(part);
+            off = __fadd_rn(__fmul_rn(64 * kU, __fdividef(1.0f, sum)), kU);
+        }
+    }
+    auto score = [&](float v) {
+        if (c.sigmoid)
+            return reciprocal_quick(__fadd_rn(1.0f, exp2_quick(__fmul_rn(v, -kLog2e))));
+        return __fmul_rn(v == mx ? 1.0f : exp2_quick(__fmul_rn(__fsub_rn(v, mx), kLog2e)), reciprocal_quick(sum));
+    };
+    uint32_t key[C];
+    float s[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        s[i] = scored ? score(l[i]) : 0.0f;
+        float k = l[i];
+        if (c.bias != nullptr && i < count)
+            k = isnan(k) ? k : __fadd_rn(s[i], ld_float(c.bias + mine.first + i));
+        key[i] = isnan(k) || i >= count ? kNone : ordered(__fadd_rn(k, 0.0f));
+    }
+
+    if (c.groups > 1) {
+        float a = neg_inf(), b = neg_inf();
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const float k = marks_of_scores && key[i] != kNone ? s[i] : unordered(key[i]);
+            b = fmaxf(b, fminf(a, k));
+            a = fmaxf(a, k);
+        }
+        for (int o = 1; o < per; o *= 2) {
+            const float a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+            b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+            a = fmaxf(a, a2);
+        }
+        const bool both = c.top2 && b != neg_inf();
+        const float mark = both ? __fadd_rn(a, b) : a;
+        int ahead = 0;
+        for (int o = 0; o < c.groups; ++o) {
+            const float m = __shfl_sync(kFull, mark, o * per);
+            ahead += m > mark || (m == mark && o < group);
+        }
+        bool stays = group < c.groups && ahead < c.kept;
+        if (scored && c.kept < c.groups) {
+            const float wrong = __fadd_rn(both ? 2 * off : off, __fmul_rn(2 * kU, __fadd_rn(fabsf(a), both ? fabsf(b) : 0.0f)));
+            const float inf = -neg_inf();   // infinite marks are what they are
+            // the least that a group which stays may have, the most of one that goes
+            const float least = warp_min(stays && fabsf(mark) < inf ? __fsub_rn(mark, wrong) : inf);
+            const float most = warp_max(!stays && group < c.groups && mark > neg_inf() ? __fadd_rn(mark, wrong) : neg_inf());
+            if (most >= least)
+                stays = groups64(c, t, mx, mine) >> group & 1u;
+        }
+        if (!stays)
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                key[i] = kNone;
+    }
+
+    uint32_t best = kNone;   // this lane's best key and where it is
+    int at = 0;
+    auto scan = [&]() {
+        best = kNone;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+    };
+    scan();
+    uint32_t taken = 0, mine_key = kNone;   // of this lane's experts; lane k holds slot k
+    int mine_e = -1;
+    for (int k = 0; k < c.K; ++k) {
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        if (top == kNone)
+            break;
+        const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+        const int e = __shfl_sync(kFull, mine.first + at, owner);
+        if (lane == k) {
+            mine_e = e;
+            mine_key = top;
+        }
+        if (lane == owner) {
+            taken |= 1u << at;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                if (i == at)
+                    key[i] = kNone;
+            scan();
+        }
+    }
+    float mine_l = mine_e >= 0 ? logit_of(c, t, mine_e) : neg_inf();
+    if (c.bias != nullptr) {
+        // neighbours in the order that 32 bits give, unless they are the same score and bias
+        auto wrong = [&](float k) { return __fadd_rn(off, __fmul_rn(2 * kU, fabsf(k))); };
+        const float mine_b = mine_e >= 0 ? ld_float(c.bias + mine_e) : 0.0f;
+        const int chosen = __popc(__ballot_sync(kFull, mine_e >= 0));
+        const float k = unordered(mine_key), next = __shfl_down_sync(kFull, k, 1);
+        const float next_l = __shfl_down_sync(kFull, mine_l, 1), next_b = __shfl_down_sync(kFull, mine_b, 1);
+        bool near = lane + 1 < chosen && __fadd_rn(next, wrong(next)) >= __fsub_rn(k, wrong(k)) &&
+                    !(mine_l == next_l && mine_b == next_b);
+        // those left, against the last chosen
+        const int end = max(chosen - 1, 0);
+        const float last = __shfl_sync(kFull, k, end), least = __fsub_rn(last, wrong(last));
+        const float last_l = __shfl_sync(kFull, mine_l, end), last_b = __shfl_sync(kFull, mine_b, end);
+        const float rest = unordered(best);
+        if (best != kNone && chosen > 0 && __fadd_rn(rest, wrong(rest)) >= least)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const float u = unordered(key[i]);
+                if (key[i] != kNone && __fadd_rn(u, wrong(u)) >= least &&
+                    !(l[i] == last_l && ld_float(c.bias + mine.first + i) == last_b))
+                    near = true;
+            }
+        if (__any_sync(kFull, near)) {
+            uint32_t mask = taken;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const float u = unordered(key[i]);
+                if (key[i] != kNone && __fadd_rn(u, wrong(u)) >= least)
+                    mask |= 1u << i;
+            }
+            mine_e = choose64(c, t, mx, mine, mask);
+            mine_l = mine_e >= 0 ? logit_of(c, t, mine_e) : neg_inf();
+        }
+    }
+    // the weights: shares of the chosen ones' sum from a multiple of the scores that does not vanish
+    float w = 0.0f;
+    if (c.renormalize) {
+        const float top = warp_max(mine_l);
+        if (c.sigmoid) {
+            const float x = expf(-fabsf(mine_l));
+            if (mine_l >= kLeastLog)
+                w = __fdiv_rn(mine_l >= 0.0f ? 1.0f : expf(__fsub_rn(mine_l, fminf(top, 0.0f))), __fadd_rn(1.0f, x));
+        } else if (mine_e >= 0) {
+            w = mine_l == mx || (mine_l == top && __fsub_rn(top, mx) >= kLeastLog) ? 1.0f
+                : __fsub_rn(mine_l, mx) >= kLeastLog ? expf(__fsub_rn(mine_l, top)) : 0.0f;
+        }
+        const float all = warp_sum(w);
+        w = all > 0.0f ? __fdiv_rn(w, all) : 0.0f;
+    } else if (mine_e >= 0) {
+        const float x = expf(-fabsf(mine_l));
+        w = c.sigmoid ? __fdiv_rn(mine_l >= 0.0f ? 1.0f : x, __fadd_rn(1.0f, x))
+                      : __fdiv_rn(mine_l == mx ? 1.0f : expf(__fsub_rn(mine_l, mx)), sum);
+    }
+    if (lane < c.K) {
+        c.idx[t * c.K + lane] = mine_e;
+        c.weights[t * c.K + lane] = mine_e >= 0 ? __fmul_rn(w, c.scale) : 0.0f;
+    }
+}
+
 // ------------------------------------------------------------ backward pass --
 struct Backward {
     const void *logits;
@@ -200,20 +604,6 @@ struct Backward {
     void *out;
     int32_t *err;
 };
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-    for (int o = 16; o > 0; o >>= 1)
-        v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-}
-
-__device__ __forceinline__ float warp_max(float v)
-{
-    for (int o = 16; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-}
 
 __device__ __forceinline__ void st_logit(void *p, int dtype, int64_t at, float v)
 {
@@ -268,7 +658,7 @@ select_backward_kernel(Backward b)
     if (there && b.sigmoid) {
         const float x = expf(-fabsf(l)), d = __fdiv_rn(1.0f, __fadd_rn(1.0f, x)), m = __fmul_rn(x, d);
         rest = l >= 0.0f ? m : d;
-        s = l >= 0.0f ? d : b.renormalize && mx < 0.0f ? __fmul_rn(expf(__fsub_rn(l, mx)), d) : m;
+        s = l < kLeastLog ? 0.0f : l >= 0.0f ? d : b.renormalize && mx < 0.0f ? __fmul_rn(expf(__fsub_rn(l, mx)), d) : m;
     } else if (there) {
         s = __fdiv_rn(power(l), sum);
     }
@@ -314,6 +704,23 @@ int choice_status(int E, int K, int scoring, int num_groups, int topk_groups, in
 
 int launch_choice(const Choice &c, cudaStream_t stream)
 {
+    int per = 32;   // lanes to a group
+    while (per > 1 && per * c.groups > 32)
+        per /= 2;
+    const int size = c.E / c.groups, share = (int)ceil_div(size, per);
+    if (per * c.groups <= 32 && share <= 16) {
+        const dim3 grid((unsigned)ceil_div(c.T, kWarps));
+        const int wide = c.slices == 1 && size % 4 == 0 && aligned(c.logits, c.dtype == 0 ? 16 : 8);
+        if (share <= 1)
+            return launch_dependent(select_warp_kernel<1>, grid, kThreads, 0, stream, c, per, wide);
+        if (share <= 2)
+            return launch_dependent(select_warp_kernel<2>, grid, kThreads, 0, stream, c, per, wide);
+        if (share <= 4)
+            return launch_dependent(select_warp_kernel<4>, grid, kThreads, 0, stream, c, per, wide);
+        if (share <= 8)
+            return launch_dependent(select_warp_kernel<8>, grid, kThreads, 0, stream, c, per, wide);
+        return launch_dependent(select_warp_kernel<16>, grid, kThreads, 0, stream, c, per, wide);
+    }
     static PerDevice set;
     const int rc = raise_smem(select_kernel, EP_MAX_EXPERTS * (sizeof(double) + sizeof(float)), set);
     if (rc != EP_OK)
