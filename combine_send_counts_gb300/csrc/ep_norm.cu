@@ -14,6 +14,7 @@
 #include "ep_fp8.cuh"
 #include "ep_internal.h"
 #include "ep_launch.cuh"
+#include "ep_skinny.cuh"
 
 namespace ep {
 namespace {
@@ -21,6 +22,7 @@ namespace {
 constexpr int kMaxH = 32768;
 constexpr int kMostVectors = 4;    // of 8 columns, a thread
 constexpr int kSMs = 152;          // a GB300's
+constexpr size_t kMostShared = 224 * 1024;   // of a block, beside the static part
 
 enum { kNone = 0, kBf16 = 1, kFp32 = 2 };
 
@@ -116,14 +118,15 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float *s, int &phase)
         for (int i = 0; i < N; ++i)
             mine[(threadIdx.x >> 5) * N + i] = v[i];
     __syncthreads();
-    const int warps = blockDim.x >> 5;
+    // every warp adds the warps' sums, a lane to each: 28 reads and additions in a row took 784 cycles of a block's issue
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        v[i] = mine[i];
-    for (int w = 1; w < warps; ++w)
+        v[i] = lane < (int)(blockDim.x >> 5) ? mine[lane * N + i] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = __fadd_rn(v[i], mine[w * N + i]);
+    for (int i = 0; i < N; ++i)
+        for (int o = 16; o > 0; o >>= 1)
+            v[i] = __fadd_rn(v[i], __shfl_xor_sync(kFull, v[i], o));
 }
 
 __device__ __forceinline__ float inverse_root(float squares, int H, float eps)
@@ -341,6 +344,139 @@ norm_backward_kernel(NormBackward a)
     }
 }
 
+// The same for rows of up to 16384 columns: rows are copied ahead of their use into
+// a ring in shared memory, of which each thread fills and reads its own slots, so
+// that the copies go on through the block's sums.
+template <int RES>
+struct Slot {
+    static constexpr int kPieces = RES == kFp32 ? 5 : 3;   // 16 bytes each: dy, then h, then dres
+    static constexpr int kBytes = kPieces * 16;            // of eight columns of a row
+};
+
+// Two roundings at once, on the pairs of eight values.
+__device__ __forceinline__ float2 pair(const float (&f)[8], int j) { return make_float2(f[2 * j], f[2 * j + 1]); }
+
+template <int RES, int NV, int AHEAD, int MOST, int BLOCKS>
+__global__ void __launch_bounds__(MOST, BLOCKS)
+norm_backward_ring_kernel(NormBackward a)
+{
+    constexpr int kPieces = Slot<RES>::kPieces, kWide = RES == kFp32 ? 2 : 1;
+    extern __shared__ __align__(16) uint8_t ring[];   // [AHEAD][NV][kPieces][threads] of 16 bytes
+    __shared__ float s[2 * 32 * 2];
+    const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, piece = blockDim.x * 16;
+    grid_dependency_wait();
+    allow_dependents();
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < a.T) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * blockDim.x + threadIdx.x) * 8;
+                const bool in = c < a.H;
+                const uint32_t to = mine + (stage * NV + v) * kPieces * piece;
+                const int64_t at = t * a.H + (in ? c : 0);
+                cp_async16(to, static_cast<const uint8_t *>(a.dy) + at * 2, in);
+#pragma unroll
+                for (int i = 0; i < kWide; ++i) {
+                    cp_async16(to + (1 + i) * piece, static_cast<const uint8_t *>(a.h) + at * (2 * kWide) + 16 * i, in);
+                    if (a.dres != nullptr)
+                        cp_async16(to + (1 + kWide + i) * piece,
+                                   static_cast<const uint8_t *>(a.dres) + at * (2 * kWide) + 16 * i, in);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    float dw[NV][8] = {}, w[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * blockDim.x + threadIdx.x) * 8;
+        load_weights(a.w, a.w_dtype, c, c < a.H, w[v]);
+    }
+    int phase = 0, stage = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        cp_async_wait<AHEAD - 1>();
+        Eight<kBf16> g[NV];
+        Eight<RES> h[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const uint32_t from = mine + (stage * NV + v) * kPieces * piece;
+            g[v].v[0] = ld_shared16(from);
+#pragma unroll
+            for (int i = 0; i < kWide; ++i)
+                h[v].v[i] = ld_shared16(from + (1 + i) * piece);
+        }
+        float2 squares = make_float2(0.0f, 0.0f), products = squares;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float f[8], n[8];
+            g[v].get(f);
+            h[v].get(n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                squares = fma2_rn(pair(n, j), pair(n, j), squares);
+                products = fma2_rn(mul2_rn(pair(f, j), pair(w[v], j)), pair(n, j), products);
+            }
+        }
+        float sums[2] = {__fadd_rn(squares.x, squares.y), __fadd_rn(products.x, products.y)};
+        block_sums(sums, s, phase);
+        const float rs = inverse_root(sums[0], a.H, a.eps);
+        const float mean = __fdiv_rn(__fmul_rn(sums[1], rs), (float)a.H);
+        const float2 rs2 = make_float2(rs, rs), less = make_float2(-mean, -mean);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * blockDim.x + threadIdx.x) * 8;
+            if (c >= a.H)
+                continue;
+            float f[8], n[8], d[8];
+            Eight<RES> r;
+#pragma unroll
+            for (int i = 0; i < kWide; ++i)
+                r.v[i] = a.dres != nullptr ? ld_shared16(mine + ((stage * NV + v) * kPieces + 1 + kWide + i) * piece)
+                                           : make_uint4(0, 0, 0, 0);
+            g[v].get(f);
+            h[v].get(n);
+            r.get(d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 n2 = mul2_rn(pair(n, j), rs2), f2 = pair(f, j);
+                const float2 sum = fma2_rn(f2, n2, pair(dw[v], j));
+                dw[v][2 * j] = sum.x;
+                dw[v][2 * j + 1] = sum.y;
+                const float2 out = fma2_rn(rs2, fma2_rn(n2, less, mul2_rn(f2, pair(w[v], j))), pair(d, j));
+                d[2 * j] = out.x;
+                d[2 * j + 1] = out.y;
+            }
+            const int64_t at = t * a.H + c;
+            if (a.dh != nullptr) {
+                Eight<RES> o;
+                o.set(d);
+                o.store(a.dh, at);
+            }
+            if (a.dx != nullptr) {
+                Eight<kBf16> b;
+                b.set(d);
+                b.store(a.dx, at);
+            }
+        }
+        fetch(t + (int64_t)AHEAD * gridDim.x, stage);
+        stage = stage + 1 == AHEAD ? 0 : stage + 1;
+    }
+    if (a.partial == nullptr)
+        return;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * blockDim.x + threadIdx.x) * 8;
+        if (c < a.H) {
+            float4 *p = reinterpret_cast<float4 *>(a.partial + (int64_t)blockIdx.x * a.H + c);
+            p[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+            p[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+        }
+    }
+}
+
 // dw: the blocks' parts added in their order, 32 columns to a block, 16 runs of parts side by side.
 constexpr int kJoinRuns = 16;
 
@@ -408,19 +544,61 @@ int launch_norm(const Norm &a, cudaStream_t stream)
     });
 }
 
-// Parts of dw: a constant, so that results do not depend on where they are computed.
-constexpr int kParts = 2 * kSMs;
+// The ring's blocks: a thread for each eight columns, or for each sixteen of more
+// than 8192; as many blocks to an SM as make 1024 threads.  (Sixteen columns a
+// thread for 7168, in two blocks, spilled and took 242 us instead of 142.)  Three rows
+// ahead where they fit, or two.
+struct Ring {
+    int vectors, threads, blocks;
+};
 
-int parts_of(int64_t T) { return (int)std::min<int64_t>(T, kParts); }
+Ring ring_of(int H)
+{
+    const int n = H > 8192 ? 2 : 1, threads = (int)align_up(ceil_div(H / 8, n), 32);
+    return {n, threads, std::max(1, std::min(8, 1024 / threads))};
+}
+
+// Parts of dw, one to a block: by the sizes alone, so that results do not depend on where they are computed.
+int parts_of(int64_t T, int H) { return (int)std::min<int64_t>(T, ring_of(H).blocks * kSMs); }
+
+template <int RES, int NV, int AHEAD, int MOST, int BLOCKS>
+int launch_ring(const NormBackward &a, int threads, cudaStream_t stream)
+{
+    static PerDevice set;
+    constexpr size_t kThread = (size_t)Slot<RES>::kBytes * NV * AHEAD;
+    const int rc = raise_smem(norm_backward_ring_kernel<RES, NV, AHEAD, MOST, BLOCKS>,
+                              std::min<size_t>(kThread * MOST, kMostShared), set);
+    if (rc != EP_OK)
+        return rc;
+    return launch_dependent(norm_backward_ring_kernel<RES, NV, AHEAD, MOST, BLOCKS>, dim3((unsigned)parts_of(a.T, a.H)),
+                            threads, kThread * threads, stream, a);
+}
+
+template <int RES, int AHEAD>
+int launch_ring(const NormBackward &a, const Ring &r, cudaStream_t stream)
+{
+    if (r.vectors == 2)
+        return launch_ring<RES, 2, AHEAD, 1024, 1>(a, r.threads, stream);
+    if (r.blocks == 1)
+        return launch_ring<RES, 1, AHEAD, 1024, 1>(a, r.threads, stream);
+    if (r.threads > 256)
+        return launch_ring<RES, 1, AHEAD, 512, 2>(a, r.threads, stream);
+    if (r.threads > 128)
+        return launch_ring<RES, 1, AHEAD, 256, 4>(a, r.threads, stream);
+    return launch_ring<RES, 1, AHEAD, 128, 8>(a, r.threads, stream);
+}
 
 template <int RES>
 int launch_norm_backward(const NormBackward &a, cudaStream_t stream)
 {
-    const Shape s = shape_of(a.H, a.T <= kSMs);
-    return with_shape(s, [&](auto nv, auto most) {
-        return launch_dependent(norm_backward_kernel<RES, decltype(nv)::value, decltype(most)::value>,
-                                dim3((unsigned)parts_of(a.T)), s.threads, 0, stream, a);
-    });
+    const Ring r = ring_of(a.H);
+    const size_t row = (size_t)Slot<RES>::kBytes * r.vectors * r.threads;
+    if (a.H <= 16384 && 3 * row * r.blocks <= kMostShared)
+        return launch_ring<RES, 3>(a, r, stream);
+    if (a.H <= 16384 && 2 * row * r.blocks <= kMostShared)
+        return launch_ring<RES, 2>(a, r, stream);
+    return launch_dependent(norm_backward_kernel<RES, kMostVectors, 1024>, dim3((unsigned)parts_of(a.T, a.H)),
+                            shape_of(a.H, false).threads, 0, stream, a);
 }
 
 bool rows_ok(const void *p) { return p == nullptr || aligned(p, 16); }
@@ -460,7 +638,7 @@ extern "C" size_t ep_rms_norm_backward_workspace_size(int64_t T, int H)
 {
     if (T < 0 || H < 1)
         return 0;
-    return align_up((size_t)parts_of(T) * H * sizeof(float), kWsAlign) + kWsAlign;
+    return align_up((size_t)parts_of(T, H) * H * sizeof(float), kWsAlign) + kWsAlign;
 }
 
 extern "C" int ep_add_rms_norm_backward(const void *dy, const void *h, const void *dresidual, int res_dtype, int64_t T,
@@ -489,5 +667,5 @@ extern "C" int ep_add_rms_norm_backward(const void *dy, const void *h, const voi
     if (rc != EP_OK || dw == nullptr)
         return rc;
     return launch_dependent(norm_join_kernel, dim3((unsigned)ceil_div(H, 32)), 32 * kJoinRuns, 0, stream,
-                            static_cast<const float *>(ws), parts_of(T), H, dw);
+                            static_cast<const float *>(ws), parts_of(T, H), H, dw);
 }
