@@ -193,9 +193,10 @@ select_kernel(Choice c)
 // ------------------------------------------- up to 512 experts: a warp a token --
 // Lanes share the groups out evenly: `per` lanes (a power of two) to a group, C
 // neighbouring experts of it to a lane.  Keys are fp32 with a bound on what they
-// are off by; the K largest are taken one at a time, the warp's best by one
-// reduction.  Where two keys, or two marks, that decide something are nearer than
-// their bounds allow, the few candidates are compared in 64 bits.
+// are off by.  The K-th of the lanes' largest keys leaves a dozen candidates or so,
+// which are ranked one to a lane (more than 32 are taken one at a time).  Where
+// two keys, or two marks, that decide something are nearer than their bounds
+// allow, the few candidates are compared in 64 bits.
 //
 // The bounds, in units u = 2^-24 (ex2.approx 4u of its result, rcp.approx 2u):
 //   sigmoid: an exponential off by 4u + 1.5 |l| u of itself moves the score by at
@@ -224,7 +225,7 @@ __device__ __forceinline__ float reciprocal_quick(float v)
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLeastLog = -745.0f;   // logarithm of the least score that 64 bits tell from 0
 
-// order-preserving map of floats to unsigned (-inf maps to kNone, +0 above -0)
+// order-preserving map of floats to unsigned (+0 above -0)
 __device__ __forceinline__ uint32_t ordered(float v)
 {
     const uint32_t b = __float_as_uint(v);
@@ -235,8 +236,6 @@ __device__ __forceinline__ float unordered(uint32_t v)
 {
     return __uint_as_float(v & 0x80000000u ? v & 0x7fffffffu : ~v);
 }
-
-constexpr uint32_t kNone = 0x007fffffu;
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -310,45 +309,40 @@ __device__ __noinline__ uint32_t groups64(const Choice &c, int64_t t, float mx, 
     return __reduce_or_sync(kFull, stays ? 1u << mine.group : 0u);
 }
 
-// The K largest of the candidates (bit i of `mask`: this lane's expert first + i) by keys in 64 bits; lane k gets the
-// k-th, or -1.
+// The place of this lane's (key, expert) among the first n lanes': how many are larger, or equal with a lower id.
+template <class Key>
+__device__ __forceinline__ int place_of(Key k, int e, int n)
+{
+    int ahead = 0;
+    for (int o = 0; o < n; ++o) {
+        const Key u = __shfl_sync(kFull, k, o);
+        const int f = __shfl_sync(kFull, e, o);
+        ahead += u > k || (u == k && f < e);
+    }
+    return ahead;
+}
+
+// One candidate a lane, by keys in 64 bits: lane k gets the k-th expert.
+__device__ __noinline__ int order64(const Choice &c, int64_t t, float mx, int e, int n, int *room)
+{
+    const int lane = threadIdx.x & 31;
+    const Score64 score = scores64(c, t, mx);
+    const double k = lane < n ? key64(c, score, logit_of(c, t, e), e) : neg_inf64();
+    const int place = place_of(k, e, n);
+    __syncwarp();
+    if (lane < n)
+        room[place] = e;
+    __syncwarp();
+    return lane < n ? room[lane] : -1;
+}
+
+// The K largest of any number of candidates (bit i of `mask`: this lane's expert first + i) by keys in 64 bits, one at a
+// time; lane k gets the k-th, or -1.
 __device__ __noinline__ int choose64(const Choice &c, int64_t t, float mx, Share mine, uint32_t mask)
 {
     const int lane = threadIdx.x & 31;
     const Score64 score = scores64(c, t, mx);
     int chosen = -1;
-    int before = 0, all = 0;   // candidates in the lanes before this one, and in all
-    for (int o = 0; o < 32; ++o) {
-        const int n = __popc(__shfl_sync(kFull, mask, o));
-        before += o < lane ? n : 0;
-        all += n;
-    }
-    if (all <= 32) {   // one to a lane, ranked
-        int e = -1;
-        for (int o = 0; o < 32; ++o) {
-            const uint32_t m = __shfl_sync(kFull, mask, o);
-            const int b = __shfl_sync(kFull, before, o), f = __shfl_sync(kFull, mine.first, o);
-            if (lane >= b && lane < b + __popc(m)) {
-                uint32_t left = m;
-                for (int skip = lane - b; skip > 0; --skip)
-                    left &= left - 1u;
-                e = f + __ffs(left) - 1;
-            }
-        }
-        const double k = e >= 0 ? key64(c, score, logit_of(c, t, e), e) : neg_inf64();
-        int ahead = 0;
-        for (int o = 0; o < all; ++o) {
-            const double u = __shfl_sync(kFull, k, o);
-            const int f = __shfl_sync(kFull, e, o);
-            ahead += u > k || (u == k && f < e);
-        }
-        for (int o = 0; o < all; ++o) {
-            const int place = __shfl_sync(kFull, ahead, o), f = __shfl_sync(kFull, e, o);
-            if (place == lane && place < c.K)
-                chosen = f;
-        }
-        return chosen;
-    }
     for (int k = 0; k < c.K; ++k) {
         double top = neg_inf64();
         int at = -1;
@@ -379,12 +373,65 @@ __device__ __noinline__ int choose64(const Choice &c, int64_t t, float mx, Share
     return chosen;
 }
 
+// The 32 lanes' values in descending order.
+__device__ __forceinline__ float sort_lanes(float v)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int o = size / 2; o > 0; o /= 2) {
+            const float u = __shfl_xor_sync(kFull, v, o);
+            v = ((lane & o) == 0) == ((lane & size) == 0) ? fmaxf(v, u) : fminf(v, u);
+        }
+    return v;
+}
+
+// Four neighbouring values of type `dtype` (0 fp32, 1 bf16).
+__device__ __forceinline__ void ld_four(const void *p, int dtype, int64_t at, float (&f)[4])
+{
+    if (dtype == 0) {
+        const uint4 v = ld_global(reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + at));
+        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    } else {
+        const uint2 v = ld_global(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at));
+        f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+    }
+}
+
+// A lane's C values of a row of E; `none` where it has fewer.
+template <int C>
+__device__ __forceinline__ void ld_share(const void *p, int dtype, int64_t row, const Share &mine, bool wide, float none,
+                                         float (&f)[C])
+{
+    if (C >= 4 && wide) {   // whole fours
+#pragma unroll
+        for (int i = 0; i + 3 < C; i += 4) {
+            float v[4] = {none, none, none, none};
+            if (i < mine.count)
+                ld_four(p, dtype, row + mine.first + i, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[i + j] = v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            f[i] = i < mine.count ? ld_logit(p, dtype, row + mine.first + i) : none;
+    }
+}
+
+// What is compared is off by `off` and 2u of itself at most.
+__device__ __forceinline__ float most_of(float v, float off) { return __fadd_rn(v, __fmaf_rn(2 * kU, fabsf(v), off)); }
+__device__ __forceinline__ float least_of(float v, float off) { return __fsub_rn(v, __fmaf_rn(2 * kU, fabsf(v), off)); }
+
 template <int C>
 __global__ void __launch_bounds__(kThreads)
 select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    __shared__ float2 room[kWarps][32];   // candidates: key and expert
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     grid_dependency_wait();
     allow_dependents();
     if (t >= c.T)
@@ -393,36 +440,17 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
     const int count = group < c.groups ? max(0, min(C, size - in_group)) : 0;
     const Share mine{group * size + in_group, count, group, per};
 
-    float l[C];
-    if (C % 4 == 0 && wide) {   // fours of experts, whole
-#pragma unroll
-        for (int i = 0; i < C; i += 4) {
-            if (C % 4 != 0)
-                break;
-            if (i < count) {
-                const int64_t at = t * c.E + mine.first + i;
-                if (c.dtype == 0) {
-                    const uint4 v = ld_global(reinterpret_cast<const uint4 *>(static_cast<const float *>(c.logits) + at));
-                    l[i] = __uint_as_float(v.x);
-                    l[(i + 1) % C] = __uint_as_float(v.y);
-                    l[(i + 2) % C] = __uint_as_float(v.z);
-                    l[(i + 3) % C] = __uint_as_float(v.w);
-                } else {
-                    const uint2 v = ld_global(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(c.logits) + at));
-                    l[i] = bf16_lo(v.x);
-                    l[(i + 1) % C] = bf16_hi(v.x);
-                    l[(i + 2) % C] = bf16_lo(v.y);
-                    l[(i + 3) % C] = bf16_hi(v.y);
-                }
-            } else {
-                l[i] = l[(i + 1) % C] = l[(i + 2) % C] = l[(i + 3) % C] = neg_inf();
-            }
-        }
-    } else {
+    // none: -inf, and a NaN as it is
+    float l[C], key[C];
+    if (c.slices > 1) {
 #pragma unroll
         for (int i = 0; i < C; ++i)
             l[i] = i < count ? logit_of(c, t, mine.first + i) : neg_inf();
+    } else {
+        ld_share(c.logits, c.dtype, t * c.E, mine, wide & 1, neg_inf(), l);
     }
+    if (c.bias != nullptr)
+        ld_share(c.bias, 0, 0, mine, wide & 2, neg_inf(), key);
     if (c.sums != nullptr)
 #pragma unroll
         for (int i = 0; i < C; ++i)
@@ -446,30 +474,25 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
                 part = __fadd_rn(part, i < count && !isnan(l[i]) ? p : 0.0f);
             }
             sum = warp_sum(part);
-            off = __fadd_rn(__fmul_rn(64 * kU, __fdividef(1.0f, sum)), kU);
+            off = __fmaf_rn(64 * kU, reciprocal_quick(sum), kU);
         }
     }
-    auto score = [&](float v) {
-        if (c.sigmoid)
-            return reciprocal_quick(__fadd_rn(1.0f, exp2_quick(__fmul_rn(v, -kLog2e))));
-        return __fmul_rn(v == mx ? 1.0f : exp2_quick(__fmul_rn(__fsub_rn(v, mx), kLog2e)), reciprocal_quick(sum));
-    };
-    uint32_t key[C];
     float s[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        s[i] = scored ? score(l[i]) : 0.0f;
-        float k = l[i];
-        if (c.bias != nullptr && i < count)
-            k = isnan(k) ? k : __fadd_rn(s[i], ld_float(c.bias + mine.first + i));
-        key[i] = isnan(k) || i >= count ? kNone : ordered(__fadd_rn(k, 0.0f));
+        s[i] = 0.0f;
+        if (scored && c.sigmoid)
+            s[i] = reciprocal_quick(__fadd_rn(1.0f, exp2_quick(__fmul_rn(l[i], -kLog2e))));
+        else if (scored)
+            s[i] = __fmul_rn(l[i] == mx ? 1.0f : exp2_quick(__fmul_rn(__fsub_rn(l[i], mx), kLog2e)), reciprocal_quick(sum));
+        key[i] = fmaxf(c.bias != nullptr ? __fadd_rn(s[i], key[i]) : l[i], neg_inf());   // a NaN is no key
     }
 
     if (c.groups > 1) {
         float a = neg_inf(), b = neg_inf();
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const float k = marks_of_scores && key[i] != kNone ? s[i] : unordered(key[i]);
+            const float k = marks_of_scores && key[i] != neg_inf() ? s[i] : key[i];
             b = fmaxf(b, fminf(a, k));
             a = fmaxf(a, k);
         }
@@ -498,88 +521,129 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
         if (!stays)
 #pragma unroll
             for (int i = 0; i < C; ++i)
-                key[i] = kNone;
+                key[i] = neg_inf();
     }
 
-    uint32_t best = kNone;   // this lane's best key and where it is
-    int at = 0;
-    auto scan = [&]() {
-        best = kNone;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-    };
-    scan();
-    uint32_t taken = 0, mine_key = kNone;   // of this lane's experts; lane k holds slot k
+    // Candidates: no key below the K-th of the lanes' largest can be one of the K.
     int mine_e = -1;
-    for (int k = 0; k < c.K; ++k) {
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        if (top == kNone)
-            break;
-        const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-        const int e = __shfl_sync(kFull, mine.first + at, owner);
-        if (lane == k) {
-            mine_e = e;
-            mine_key = top;
+    float top = key[0];
+#pragma unroll
+    for (int i = 1; i < C; ++i)
+        top = fmaxf(top, key[i]);
+    const float kth = __shfl_sync(kFull, sort_lanes(top), c.K - 1);
+    const float least = c.bias != nullptr && kth != neg_inf() ? least_of(least_of(kth, off), off) : kth;
+    int n = 0;
+    float2 *const found = room[warp];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const bool is = key[i] >= least && key[i] > neg_inf();
+        const uint32_t lanes = __ballot_sync(kFull, is);
+        const int place = n + __popc(lanes & lanemask_lt());
+        if (is && place < 32)
+            found[place] = make_float2(key[i], __int_as_float(mine.first + i));
+        n += __popc(lanes);
+    }
+    if (n <= 32) {
+        __syncwarp();
+        float2 v = lane < n ? found[lane] : make_float2(neg_inf(), __int_as_float(INT32_MAX));
+        int place = 0;
+        for (int o = 0; o < n; ++o) {
+            const float2 u = found[o];
+            place += u.x > v.x || (u.x == v.x && __float_as_int(u.y) < __float_as_int(v.y));
         }
-        if (lane == owner) {
-            taken |= 1u << at;
+        __syncwarp();
+        if (lane < n)
+            found[place] = v;
+        __syncwarp();
+        if (lane < n)
+            v = found[lane];
+        mine_e = lane < n ? __float_as_int(v.y) : -1;
+        if (c.bias != nullptr) {
+            // neighbours in this order that are too near, up to the first that is not chosen
+            const float next = __shfl_down_sync(kFull, v.x, 1);
+            bool near = lane < c.K && lane + 1 < n && most_of(next, off) >= least_of(v.x, off);
+            if (__any_sync(kFull, near)) {
+                // the same score and bias are the same key; those left are held against the last chosen
+                const float my_l = lane < n ? logit_of(c, t, mine_e) : 0.0f, my_b = lane < n ? ld_float(c.bias + mine_e) : 0.0f;
+                const int other = lane < c.K ? min(lane + 1, 31) : c.K - 1;
+                const float key2 = __shfl_sync(kFull, v.x, other), l2 = __shfl_sync(kFull, my_l, other);
+                const float b2 = __shfl_sync(kFull, my_b, other);
+                near = lane < n && !(l2 == my_l && b2 == my_b) &&
+                       (lane < c.K ? lane + 1 < min(n, c.K) && most_of(key2, off) >= least_of(v.x, off)
+                                   : most_of(v.x, off) >= least_of(key2, off));
+                if (__any_sync(kFull, near))
+                    mine_e = order64(c, t, mx, mine_e, n, reinterpret_cast<int *>(found));
+            }
+        }
+        if (lane >= c.K)
+            mine_e = -1;
+    } else {   // one at a time
+        float best;   // this lane's best key and where it is
+        int at = 0;
+        auto scan = [&]() {
+            best = neg_inf();
 #pragma unroll
             for (int i = 0; i < C; ++i)
-                if (i == at)
-                    key[i] = kNone;
-            scan();
+                if (key[i] > best) {
+                    best = key[i];
+                    at = i;
+                }
+        };
+        scan();
+        uint32_t taken = 0;   // of this lane's experts
+        float last = 0.0f;
+        bool near = false;
+        for (int k = 0; k < c.K; ++k) {
+            const float up = warp_max(__fadd_rn(best, 0.0f));   // -0 and +0 are one key
+            if (up == neg_inf())
+                break;
+            const int owner = __ffs(__ballot_sync(kFull, best == up)) - 1;
+            const int e = __shfl_sync(kFull, mine.first + at, owner);
+            if (lane == k)
+                mine_e = e;
+            if (c.bias != nullptr && k > 0 && most_of(up, off) >= least_of(last, off))
+                near = true;   // unless they are the same, below
+            last = up;
+            if (lane == owner) {
+                taken |= 1u << at;
+#pragma unroll
+                for (int i = 0; i < C; ++i)
+                    if (i == at)
+                        key[i] = neg_inf();
+                scan();
+            }
         }
-    }
-    float mine_l = mine_e >= 0 ? logit_of(c, t, mine_e) : neg_inf();
-    if (c.bias != nullptr) {
-        // neighbours in the order that 32 bits give, unless they are the same score and bias
-        auto wrong = [&](float k) { return __fadd_rn(off, __fmul_rn(2 * kU, fabsf(k))); };
-        const float mine_b = mine_e >= 0 ? ld_float(c.bias + mine_e) : 0.0f;
-        const int chosen = __popc(__ballot_sync(kFull, mine_e >= 0));
-        const float k = unordered(mine_key), next = __shfl_down_sync(kFull, k, 1);
-        const float next_l = __shfl_down_sync(kFull, mine_l, 1), next_b = __shfl_down_sync(kFull, mine_b, 1);
-        bool near = lane + 1 < chosen && __fadd_rn(next, wrong(next)) >= __fsub_rn(k, wrong(k)) &&
-                    !(mine_l == next_l && mine_b == next_b);
-        // those left, against the last chosen
-        const int end = max(chosen - 1, 0);
-        const float last = __shfl_sync(kFull, k, end), least = __fsub_rn(last, wrong(last));
-        const float last_l = __shfl_sync(kFull, mine_l, end), last_b = __shfl_sync(kFull, mine_b, end);
-        const float rest = unordered(best);
-        if (best != kNone && chosen > 0 && __fadd_rn(rest, wrong(rest)) >= least)
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const float u = unordered(key[i]);
-                if (key[i] != kNone && __fadd_rn(u, wrong(u)) >= least &&
-                    !(l[i] == last_l && ld_float(c.bias + mine.first + i) == last_b))
-                    near = true;
-            }
-        if (__any_sync(kFull, near)) {
+        if (c.bias != nullptr) {
+            const int chosen = __popc(__ballot_sync(kFull, mine_e >= 0)), end = max(chosen - 1, 0);
+            const float my_l = mine_e >= 0 ? logit_of(c, t, mine_e) : 0.0f, my_b = mine_e >= 0 ? ld_float(c.bias + mine_e) : 0.0f;
+            const float last_l = __shfl_sync(kFull, my_l, end), last_b = __shfl_sync(kFull, my_b, end);
+            const float l2 = __shfl_down_sync(kFull, my_l, 1), b2 = __shfl_down_sync(kFull, my_b, 1);
+            near = __any_sync(kFull, near && lane + 1 < chosen && !(l2 == my_l && b2 == my_b));
             uint32_t mask = taken;
+            const float low = least_of(last, off);
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const float u = unordered(key[i]);
-                if (key[i] != kNone && __fadd_rn(u, wrong(u)) >= least)
+            for (int i = 0; i < C; ++i)
+                if (key[i] > neg_inf() && most_of(key[i], off) >= low) {
                     mask |= 1u << i;
-            }
-            mine_e = choose64(c, t, mx, mine, mask);
-            mine_l = mine_e >= 0 ? logit_of(c, t, mine_e) : neg_inf();
+                    near |= !(l[i] == last_l && ld_float(c.bias + mine.first + i) == last_b);
+                }
+            if (__any_sync(kFull, near))
+                mine_e = choose64(c, t, mx, mine, mask);
         }
     }
     // the weights: shares of the chosen ones' sum from a multiple of the scores that does not vanish
+    const float mine_l = mine_e >= 0 ? logit_of(c, t, mine_e) : neg_inf();
     float w = 0.0f;
     if (c.renormalize) {
-        const float top = warp_max(mine_l);
+        const float up = warp_max(mine_l);
         if (c.sigmoid) {
             const float x = expf(-fabsf(mine_l));
+            const float of = mine_l >= 0.0f ? 1.0f : up >= 0.0f ? x : expf(__fsub_rn(mine_l, up));
             if (mine_l >= kLeastLog)
-                w = __fdiv_rn(mine_l >= 0.0f ? 1.0f : expf(__fsub_rn(mine_l, fminf(top, 0.0f))), __fadd_rn(1.0f, x));
+                w = __fdiv_rn(of, __fadd_rn(1.0f, x));
         } else if (mine_e >= 0) {
-            w = mine_l == mx || (mine_l == top && __fsub_rn(top, mx) >= kLeastLog) ? 1.0f
-                : __fsub_rn(mine_l, mx) >= kLeastLog ? expf(__fsub_rn(mine_l, top)) : 0.0f;
+            w = mine_l == mx || (mine_l == up && __fsub_rn(up, mx) >= kLeastLog) ? 1.0f
+                : __fsub_rn(mine_l, mx) >= kLeastLog ? expf(__fsub_rn(mine_l, up)) : 0.0f;
         }
         const float all = warp_sum(w);
         w = all > 0.0f ? __fdiv_rn(w, all) : 0.0f;
@@ -613,43 +677,78 @@ __device__ __forceinline__ void st_logit(void *p, int dtype, int64_t at, float v
         static_cast<uint16_t *>(p)[at] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
 }
 
-// A warp per token, lane k with slot k.  First what every logit gets, then the chosen ones over it.
+// A warp per token, lane k with slot k.  First what every logit gets, then the
+// chosen ones over it.  PIECES > 0: the row stays in registers, four neighbours of
+// each 128 to a lane; 0: any number of experts, the row read as often as needed.
+template <int PIECES>
 __global__ void __launch_bounds__(kThreads)
 select_backward_kernel(Backward b)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), row = t * b.E;
     grid_dependency_wait();
     allow_dependents();
     if (t >= b.T)
         return;
+    // softmax divided by the chosen ones' sum: the others cancel
+    const bool whole = !b.sigmoid && !b.renormalize;
+    float all[PIECES > 0 ? PIECES : 1][4];
+    if (PIECES > 0 && whole)
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int at = (i * 32 + lane) * 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                all[i][j] = neg_inf();
+            if (at < b.E)
+                ld_four(b.logits, b.dtype, row + at, all[i]);
+        }
     int e = -1;
     float g = 0.0f;
     if (lane < b.K) {
         const uint2 w = ld_global(reinterpret_cast<const uint2 *>(b.idx) + t * b.K + lane);
         const int64_t id = (int64_t)((uint64_t)w.y << 32 | w.x);
+        g = __fmul_rn(ld_float(b.dw + t * b.K + lane), b.scale);
         if (id < -1 || id >= b.E)
             raise(b.err, EP_ERR_INVALID_EXPERT);
         else
             e = (int)id;
-        if (e >= 0)
-            g = __fmul_rn(ld_float(b.dw + t * b.K + lane), b.scale);
+        if (e < 0)
+            g = 0.0f;
     }
-    const float l = e >= 0 ? ld_logit(b.logits, b.dtype, t * b.E + e) : neg_inf();
+    const float l = e >= 0 ? ld_logit(b.logits, b.dtype, row + e) : neg_inf();
     const bool there = l > neg_inf();   // a logit of NaN or -inf gets nothing
-    // softmax divided by the chosen ones' sum: the others cancel
-    const bool whole = !b.sigmoid && !b.renormalize;
     float mx = there ? l : neg_inf();
-    if (whole)
-        for (int i = lane; i < b.E; i += 32)
-            mx = fmaxf(mx, ld_logit(b.logits, b.dtype, t * b.E + i));
-    mx = warp_max(mx);
+    if (whole) {
+        if constexpr (PIECES > 0) {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mx = fmaxf(mx, all[i][j]);
+        } else {
+            for (int i = lane; i < b.E; i += 32)
+                mx = fmaxf(mx, ld_logit(b.logits, b.dtype, row + i));
+        }
+    }
+    if (!b.sigmoid || b.renormalize)
+        mx = warp_max(mx);
     auto power = [&](float v) { return isnan(v) ? 0.0f : v == mx ? 1.0f : expf(__fsub_rn(v, mx)); };
     float sum = 1.0f;
     if (whole) {
         sum = 0.0f;
-        for (int i = lane; i < b.E; i += 32)
-            sum = __fadd_rn(sum, power(ld_logit(b.logits, b.dtype, t * b.E + i)));
+        if constexpr (PIECES > 0) {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    all[i][j] = (i * 32 + lane) * 4 < b.E ? power(all[i][j]) : 0.0f;
+                    sum = __fadd_rn(sum, all[i][j]);
+                }
+        } else {
+            for (int i = lane; i < b.E; i += 32)
+                sum = __fadd_rn(sum, power(ld_logit(b.logits, b.dtype, row + i)));
+        }
         sum = warp_sum(sum);
     }
     // s: the score, or, where only its share of the chosen ones' sum counts, a multiple of it that does
@@ -668,26 +767,45 @@ select_backward_kernel(Backward b)
         g = __fsub_rn(g, warp_sum(__fmul_rn(g, s)));
     }
     const float dot = whole ? warp_sum(__fmul_rn(g, s)) : 0.0f;
-    for (int i = lane; i < b.E; i += 32) {
-        float v = 0.0f;
-        if (whole)
-            v = -__fmul_rn(__fdiv_rn(power(ld_logit(b.logits, b.dtype, t * b.E + i)), sum), dot);
-        st_logit(b.out, b.dtype, t * b.E + i, v);
+    if constexpr (PIECES > 0) {
+        const float by = whole && sum > 0.0f ? -__fdiv_rn(dot, sum) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int at = (i * 32 + lane) * 4;
+            if (at >= b.E)
+                continue;
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = whole ? __fmul_rn(all[i][j], by) : 0.0f;
+            if (b.dtype == 0)
+                *reinterpret_cast<float4 *>(static_cast<float *>(b.out) + row + at) = make_float4(v[0], v[1], v[2], v[3]);
+            else
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(b.out) + row + at) =
+                    make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+    } else {
+        for (int i = lane; i < b.E; i += 32) {
+            float v = 0.0f;
+            if (whole && sum > 0.0f)
+                v = -__fmul_rn(__fdiv_rn(power(ld_logit(b.logits, b.dtype, row + i)), sum), dot);
+            st_logit(b.out, b.dtype, row + i, v);
+        }
     }
     // slots that name the same expert are added in their order, by the first
-    float total = 0.0f;
-    bool first = there;
-    for (int k = 0; k < b.K; ++k) {
-        const int o = __shfl_sync(kFull, e, k);
-        const float u = __shfl_sync(kFull, g, k);
-        if (o == e)
-            total = __fadd_rn(total, u);
-        if (o == e && k < lane)
-            first = false;
+    const uint32_t same = __match_any_sync(kFull, e);
+    float total = g;
+    if (__any_sync(kFull, e >= 0 && (same & (same - 1u)) != 0)) {
+        total = 0.0f;
+        for (int k = 0; k < b.K; ++k) {
+            const float u = __shfl_sync(kFull, g, k);
+            if (same >> k & 1u)
+                total = __fadd_rn(total, u);
+        }
     }
     __syncwarp();
-    if (first)
-        st_logit(b.out, b.dtype, t * b.E + e, __fmul_rn(__fmul_rn(s, rest), __fsub_rn(total, dot)));
+    if (there && (same & lanemask_lt()) == 0)
+        st_logit(b.out, b.dtype, row + e, __fmul_rn(__fmul_rn(s, rest), __fsub_rn(total, dot)));
 }
 
 }  // namespace
@@ -710,7 +828,7 @@ int launch_choice(const Choice &c, cudaStream_t stream)
     const int size = c.E / c.groups, share = (int)ceil_div(size, per);
     if (per * c.groups <= 32 && share <= 16) {
         const dim3 grid((unsigned)ceil_div(c.T, kWarps));
-        const int wide = c.slices == 1 && size % 4 == 0 && aligned(c.logits, c.dtype == 0 ? 16 : 8);
+        const int wide = size % 4 != 0 ? 0 : (aligned(c.logits, c.dtype == 0 ? 16 : 8) ? 1 : 0) | (aligned(c.bias, 16) ? 2 : 0);
         if (share <= 1)
             return launch_dependent(select_warp_kernel<1>, grid, kThreads, 0, stream, c, per, wide);
         if (share <= 2)
@@ -770,5 +888,13 @@ extern "C" int ep_router_select_backward(const void *logits, int dtype, int64_t 
         return EP_ERR_INVALID_ARG;
     const Backward b{logits, dtype, (int)T, E, K, scoring == EP_SCORE_SIGMOID, renormalize, scale, topk_idx, dweights,
                      dlogits, err};
-    return launch_dependent(select_backward_kernel, dim3((unsigned)ceil_div(T, kWarps)), kThreads, 0, stream, b);
+    const dim3 grid((unsigned)ceil_div(T, kWarps));
+    const size_t four = dtype == 0 ? 16 : 8;
+    if (E <= 512 && E % 4 == 0 && aligned(logits, four) && aligned(dlogits, four)) {
+        if (E <= 128)
+            return launch_dependent(select_backward_kernel<1>, grid, kThreads, 0, stream, b);
+        return E <= 256 ? launch_dependent(select_backward_kernel<2>, grid, kThreads, 0, stream, b)
+                        : launch_dependent(select_backward_kernel<4>, grid, kThreads, 0, stream, b);
+    }
+    return launch_dependent(select_backward_kernel<0>, grid, kThreads, 0, stream, b);
 }
