@@ -10,6 +10,7 @@
 // Keys and marks are compared as they come out in 64 bits: with a million
 // scores in a batch some two are nearer than fp32 tells apart.
 #include <algorithm>
+#include <type_traits>
 
 #include "ep_device.cuh"
 #include "ep_internal.h"
@@ -280,15 +281,17 @@ struct Share {
     int group, per;     // lanes to a group
 };
 
-// Which groups stay, by marks in 64 bits: a bit for each group.
-__device__ __noinline__ uint32_t groups64(const Choice &c, int64_t t, float mx, Share mine)
+// Which groups stay, by marks in 64 bits of the experts (bit i of `mask`: this lane's first + i) that a mark may be made
+// of: a bit for each group.
+__device__ __noinline__ uint32_t groups64(const Choice &c, int64_t t, float mx, Share mine, uint32_t mask)
 {
     const Score64 score = scores64(c, t, mx);
     const bool of_scores = c.top2 && c.bias == nullptr;
     double a = neg_inf64(), b = neg_inf64();
-    for (int i = 0; i < mine.count; ++i) {
-        const float l = logit_of(c, t, mine.first + i);
-        double k = key64(c, score, l, mine.first + i);
+    for (; mask != 0; mask &= mask - 1u) {
+        const int e = mine.first + __ffs(mask) - 1;
+        const float l = logit_of(c, t, e);
+        double k = key64(c, score, l, e);
         if (k != neg_inf64() && of_scores)
             k = score(l);
         b = fmax(b, fmin(a, k));
@@ -377,12 +380,13 @@ __device__ __noinline__ int choose64(const Choice &c, int64_t t, float mx, Share
 __device__ __forceinline__ float sort_lanes(float v)
 {
     const int lane = threadIdx.x & 31;
+    const bool bit[6] = {(lane & 1) != 0, (lane & 2) != 0, (lane & 4) != 0, (lane & 8) != 0, (lane & 16) != 0, false};
 #pragma unroll
-    for (int size = 2; size <= 32; size *= 2)
+    for (int size = 1; size <= 5; ++size)
 #pragma unroll
-        for (int o = size / 2; o > 0; o /= 2) {
-            const float u = __shfl_xor_sync(kFull, v, o);
-            v = ((lane & o) == 0) == ((lane & size) == 0) ? fmaxf(v, u) : fminf(v, u);
+        for (int o = size - 1; o >= 0; --o) {
+            const float u = __shfl_xor_sync(kFull, v, 1 << o);
+            v = bit[o] == bit[size] ? fmaxf(v, u) : fminf(v, u);
         }
     return v;
 }
@@ -425,9 +429,9 @@ __device__ __forceinline__ void ld_share(const void *p, int dtype, int64_t row, 
 __device__ __forceinline__ float most_of(float v, float off) { return __fadd_rn(v, __fmaf_rn(2 * kU, fabsf(v), off)); }
 __device__ __forceinline__ float least_of(float v, float off) { return __fsub_rn(v, __fmaf_rn(2 * kU, fabsf(v), off)); }
 
-template <int C>
-__global__ void __launch_bounds__(kThreads)
-select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
+template <int C, bool SIGMOID, bool BIAS>
+__global__ void __launch_bounds__(kThreads, C <= 8 ? 8 : 5)
+select_warp_kernel(const __grid_constant__ Choice c, int size, int log_per, int wide)
 {
     __shared__ float2 room[kWarps][32];   // candidates: key and expert
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -436,31 +440,32 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
     allow_dependents();
     if (t >= c.T)
         return;
-    const int size = c.E / c.groups, group = lane / per, in_group = (lane % per) * C;
+    const int per = 1 << log_per, group = lane >> log_per, in_group = (lane & (per - 1)) * C;
     const int count = group < c.groups ? max(0, min(C, size - in_group)) : 0;
     const Share mine{group * size + in_group, count, group, per};
 
     // none: -inf, and a NaN as it is
     float l[C], key[C];
-    if (c.slices > 1) {
+    if (c.slices > 1 || c.sums != nullptr) {
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            l[i] = i < count ? logit_of(c, t, mine.first + i) : neg_inf();
+        for (int i = 0; i < C; ++i) {
+            l[i] = neg_inf();
+            if (i < count) {
+                l[i] = logit_of(c, t, mine.first + i);
+                if (c.sums != nullptr)
+                    c.sums[t * c.E + mine.first + i] = l[i];
+            }
+        }
     } else {
         ld_share(c.logits, c.dtype, t * c.E, mine, wide & 1, neg_inf(), l);
     }
-    if (c.bias != nullptr)
+    if (BIAS)
         ld_share(c.bias, 0, 0, mine, wide & 2, neg_inf(), key);
-    if (c.sums != nullptr)
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (i < count)
-                c.sums[t * c.E + mine.first + i] = l[i];
 
-    const bool marks_of_scores = c.groups > 1 && c.top2 && c.bias == nullptr;
-    const bool scored = c.bias != nullptr || marks_of_scores;   // something compared is made of scores
+    const bool marks_of_scores = c.groups > 1 && c.top2 && !BIAS;
+    const bool scored = BIAS || marks_of_scores;   // something compared is made of scores
     float mx = 0.0f, sum = 1.0f, off = 8 * kU;   // off: of a score
-    if (!c.sigmoid) {
+    if (!SIGMOID) {
         mx = neg_inf();
 #pragma unroll
         for (int i = 0; i < C; ++i)
@@ -481,11 +486,11 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         s[i] = 0.0f;
-        if (scored && c.sigmoid)
+        if (scored && SIGMOID)
             s[i] = reciprocal_quick(__fadd_rn(1.0f, exp2_quick(__fmul_rn(l[i], -kLog2e))));
         else if (scored)
             s[i] = __fmul_rn(l[i] == mx ? 1.0f : exp2_quick(__fmul_rn(__fsub_rn(l[i], mx), kLog2e)), reciprocal_quick(sum));
-        key[i] = fmaxf(c.bias != nullptr ? __fadd_rn(s[i], key[i]) : l[i], neg_inf());   // a NaN is no key
+        key[i] = fmaxf(BIAS ? __fadd_rn(s[i], key[i]) : l[i], neg_inf());   // a NaN is no key
     }
 
     if (c.groups > 1) {
@@ -515,8 +520,15 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
             // the least that a group which stays may have, the most of one that goes
             const float least = warp_min(stays && fabsf(mark) < inf ? __fsub_rn(mark, wrong) : inf);
             const float most = warp_max(!stays && group < c.groups && mark > neg_inf() ? __fadd_rn(mark, wrong) : neg_inf());
-            if (most >= least)
-                stays = groups64(c, t, mx, mine) >> group & 1u;
+            if (most >= least) {
+                const float low = least_of(c.top2 ? b : a, off);   // of what the mark is made of; -inf: all
+                uint32_t mask = 0;
+#pragma unroll
+                for (int i = 0; i < C; ++i)
+                    if (key[i] != neg_inf() && !(most_of(marks_of_scores ? s[i] : key[i], off) < low))
+                        mask |= 1u << i;
+                stays = groups64(c, t, mx, mine, mask) >> group & 1u;
+            }
         }
         if (!stays)
 #pragma unroll
@@ -531,22 +543,30 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
     for (int i = 1; i < C; ++i)
         top = fmaxf(top, key[i]);
     const float kth = __shfl_sync(kFull, sort_lanes(top), c.K - 1);
-    const float least = c.bias != nullptr && kth != neg_inf() ? least_of(least_of(kth, off), off) : kth;
-    int n = 0;
+    const float least = BIAS && kth != neg_inf() ? least_of(least_of(kth, off), off) : kth;
     float2 *const found = room[warp];
+    int n = 0, place = 0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const bool is = key[i] >= least && key[i] > neg_inf();
-        const uint32_t lanes = __ballot_sync(kFull, is);
-        const int place = n + __popc(lanes & lanemask_lt());
-        if (is && place < 32)
-            found[place] = make_float2(key[i], __int_as_float(mine.first + i));
-        n += __popc(lanes);
+    for (int i = 0; i < C; ++i)
+        n += key[i] >= least && key[i] > neg_inf();
+    place = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int before = __shfl_up_sync(kFull, place, o);
+        place += lane >= o ? before : 0;
     }
+    const int end = place;
+    place -= n;
+    n = __shfl_sync(kFull, end, 31);
+    if (end <= 32 && place < end)
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (key[i] >= least && key[i] > neg_inf())
+                found[place++] = make_float2(key[i], __int_as_float(mine.first + i));
     if (n <= 32) {
         __syncwarp();
         float2 v = lane < n ? found[lane] : make_float2(neg_inf(), __int_as_float(INT32_MAX));
-        int place = 0;
+        place = 0;
         for (int o = 0; o < n; ++o) {
             const float2 u = found[o];
             place += u.x > v.x || (u.x == v.x && __float_as_int(u.y) < __float_as_int(v.y));
@@ -558,7 +578,7 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
         if (lane < n)
             v = found[lane];
         mine_e = lane < n ? __float_as_int(v.y) : -1;
-        if (c.bias != nullptr) {
+        if (BIAS) {
             // neighbours in this order that are too near, up to the first that is not chosen
             const float next = __shfl_down_sync(kFull, v.x, 1);
             bool near = lane < c.K && lane + 1 < n && most_of(next, off) >= least_of(v.x, off);
@@ -601,7 +621,7 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
             const int e = __shfl_sync(kFull, mine.first + at, owner);
             if (lane == k)
                 mine_e = e;
-            if (c.bias != nullptr && k > 0 && most_of(up, off) >= least_of(last, off))
+            if (BIAS && k > 0 && most_of(up, off) >= least_of(last, off))
                 near = true;   // unless they are the same, below
             last = up;
             if (lane == owner) {
@@ -613,7 +633,7 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
                 scan();
             }
         }
-        if (c.bias != nullptr) {
+        if (BIAS) {
             const int chosen = __popc(__ballot_sync(kFull, mine_e >= 0)), end = max(chosen - 1, 0);
             const float my_l = mine_e >= 0 ? logit_of(c, t, mine_e) : 0.0f, my_b = mine_e >= 0 ? ld_float(c.bias + mine_e) : 0.0f;
             const float last_l = __shfl_sync(kFull, my_l, end), last_b = __shfl_sync(kFull, my_b, end);
@@ -636,11 +656,11 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
     float w = 0.0f;
     if (c.renormalize) {
         const float up = warp_max(mine_l);
-        if (c.sigmoid) {
+        if (SIGMOID) {
             const float x = expf(-fabsf(mine_l));
             const float of = mine_l >= 0.0f ? 1.0f : up >= 0.0f ? x : expf(__fsub_rn(mine_l, up));
             if (mine_l >= kLeastLog)
-                w = __fdiv_rn(of, __fadd_rn(1.0f, x));
+                w = __fdividef(of, __fadd_rn(1.0f, x));
         } else if (mine_e >= 0) {
             w = mine_l == mx || (mine_l == up && __fsub_rn(up, mx) >= kLeastLog) ? 1.0f
                 : __fsub_rn(mine_l, mx) >= kLeastLog ? expf(__fsub_rn(mine_l, up)) : 0.0f;
@@ -649,7 +669,7 @@ select_warp_kernel(const __grid_constant__ Choice c, int per, int wide)
         w = all > 0.0f ? __fdiv_rn(w, all) : 0.0f;
     } else if (mine_e >= 0) {
         const float x = expf(-fabsf(mine_l));
-        w = c.sigmoid ? __fdiv_rn(mine_l >= 0.0f ? 1.0f : x, __fadd_rn(1.0f, x))
+        w = SIGMOID ? __fdiv_rn(mine_l >= 0.0f ? 1.0f : x, __fadd_rn(1.0f, x))
                       : __fdiv_rn(mine_l == mx ? 1.0f : expf(__fsub_rn(mine_l, mx)), sum);
     }
     if (lane < c.K) {
@@ -822,22 +842,28 @@ int choice_status(int E, int K, int scoring, int num_groups, int topk_groups, in
 
 int launch_choice(const Choice &c, cudaStream_t stream)
 {
-    int per = 32;   // lanes to a group
-    while (per > 1 && per * c.groups > 32)
-        per /= 2;
-    const int size = c.E / c.groups, share = (int)ceil_div(size, per);
-    if (per * c.groups <= 32 && share <= 16) {
+    int log_per = 5;   // lanes to a group
+    while (log_per > 0 && (c.groups << log_per) > 32)
+        --log_per;
+    const int size = c.E / c.groups, share = (int)ceil_div(size, 1 << log_per);
+    if ((c.groups << log_per) <= 32 && share <= 16) {
         const dim3 grid((unsigned)ceil_div(c.T, kWarps));
         const int wide = size % 4 != 0 ? 0 : (aligned(c.logits, c.dtype == 0 ? 16 : 8) ? 1 : 0) | (aligned(c.bias, 16) ? 2 : 0);
+        auto launch = [&](auto experts) {
+            constexpr int C = decltype(experts)::value;
+            if (c.bias != nullptr)
+                return launch_dependent(c.sigmoid ? select_warp_kernel<C, true, true> : select_warp_kernel<C, false, true>,
+                                        grid, kThreads, 0, stream, c, size, log_per, wide);
+            return launch_dependent(c.sigmoid ? select_warp_kernel<C, true, false> : select_warp_kernel<C, false, false>,
+                                    grid, kThreads, 0, stream, c, size, log_per, wide);
+        };
         if (share <= 1)
-            return launch_dependent(select_warp_kernel<1>, grid, kThreads, 0, stream, c, per, wide);
+            return launch(std::integral_constant<int, 1>());
         if (share <= 2)
-            return launch_dependent(select_warp_kernel<2>, grid, kThreads, 0, stream, c, per, wide);
+            return launch(std::integral_constant<int, 2>());
         if (share <= 4)
-            return launch_dependent(select_warp_kernel<4>, grid, kThreads, 0, stream, c, per, wide);
-        if (share <= 8)
-            return launch_dependent(select_warp_kernel<8>, grid, kThreads, 0, stream, c, per, wide);
-        return launch_dependent(select_warp_kernel<16>, grid, kThreads, 0, stream, c, per, wide);
+            return launch(std::integral_constant<int, 4>());
+        return share <= 8 ? launch(std::integral_constant<int, 8>()) : launch(std::integral_constant<int, 16>());
     }
     static PerDevice set;
     const int rc = raise_smem(select_kernel, EP_MAX_EXPERTS * (sizeof(double) + sizeof(float)), set);
