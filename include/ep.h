@@ -724,7 +724,7 @@ int ep_router_select_backward(const void *logits, int dtype, int64_t T, int E, c
  * Sums are fp32; the result is rounded once.
  *   K, N, R % 8 == 0, R <= 128; M, K, N <= 2^24 (else EP_ERR_UNSUPPORTED).
  *   Up to 1024 rows may name adapters in any order; with more, rows of one adapter
- *   are best neighbours (16 rows are gone over once for each adapter among them).
+ *   are best neighbours (128 rows are gone over once for each adapter among them).
  *   ws: ep_lora_workspace_size(M, R) bytes, 256-byte aligned, scratch.  Calls that
  *     overlap on the GPU must not share it.
  * The same call on the same inputs gives the same bits.

@@ -87,6 +87,20 @@ def test_bad_ids_and_rows_of_their_own(M):
     assert torch.equal(odd[other], want[other])
 
 
+@pytest.mark.parametrize("M", [40, 1200])
+@pytest.mark.parametrize("R", [16, 64, 128])
+def test_a_broken_adapter_harms_its_own_rows_alone(M, R):
+    g = f.gen(R)
+    x, ids, a, b, s, y = inputs(M, 264, 136, 5, R, "bf16", "random", g)
+    want = ep.LoraAdapters(a, b, s, max_tokens=M)(x, ids, y)
+    a2, b2 = a.clone(), b.clone()
+    a2[1], b2[3, :, 2] = float("inf"), float("nan")
+    got = ep.LoraAdapters(a2, b2, s, max_tokens=M)(x, ids, y)
+    whole = (ids != 1) & (ids != 3)
+    assert torch.equal(got[whole], want[whole])
+    assert not bool(torch.isfinite(got[ids == 3]).any()) and not bool(torch.isfinite(got[ids == 1]).all())
+
+
 def test_infinities():
     g = f.gen(8)
     x, _, a, b, s, y = inputs(4, 64, 64, 2, 16, "fp32", "random", g)
