@@ -21,6 +21,7 @@
 #include "ep_device.cuh"
 #include "ep_internal.h"
 #include "ep_launch.cuh"
+#include "ep_lora.cuh"
 #include "ep_skinny.cuh"
 
 namespace ep {
@@ -31,44 +32,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kUnit = 32;            // columns of a lane's 16-byte pieces: two k16 steps
 constexpr int kBatch = 4;            // units loaded together, and summed by matrix steps alone
 constexpr int kTile = 16;
-constexpr int kGatherRows = 1024;
-constexpr int kMaxRank = 128;
-constexpr int kMaxSplits = 16;
-constexpr int kBlocks = 2 * 152;     // that fill the GPU
-constexpr int kPlanes = 3;
-
-struct Lora {
-    const uint8_t *x, *a, *b;
-    const int64_t *ids;
-    const float *scaling;
-    const void *base;
-    void *out;
-    int64_t M;
-    int K, N, R, L, splits, base_dtype, out_dtype;
-    float *parts;                    // [splits][M][R]
-    int32_t *err;
-};
-
-// The adapter of a row, or -1.
-__device__ __forceinline__ int adapter_of(const Lora &p, int64_t m)
-{
-    const uint2 w = ld_global(reinterpret_cast<const uint2 *>(p.ids) + m);
-    const int64_t id = (int64_t)((uint64_t)w.y << 32 | w.x);
-    return id >= 0 && id < p.L ? (int)id : -1;
-}
-
-__device__ __forceinline__ bool bad_id(const Lora &p, int64_t m)
-{
-    const uint2 w = ld_global(reinterpret_cast<const uint2 *>(p.ids) + m);
-    const int64_t id = (int64_t)((uint64_t)w.y << 32 | w.x);
-    return id < -1 || id >= p.L;
-}
 
 // The tile that begins with row m: `mine` is the row index of this lane's slot (lane & 15), or -1; false if no tile
 // does.  A tile begins with every 16th row of an adapter.  All threads of the block.
 __device__ __forceinline__ bool gather_tile(const Lora &p, int m, int adapter, int &mine)
 {
-    __shared__ uint32_t same[kGatherRows / 32];
+    __shared__ uint32_t same[kLoraFewRows / 32];
     const int words = ((int)p.M + 31) / 32;
     for (int r = threadIdx.x; r < words * 32; r += kThreads) {
         const uint32_t bits = __ballot_sync(kFull, r < p.M && adapter_of(p, r) == adapter);
@@ -235,40 +204,6 @@ struct Ranks {
     }
 };
 
-// Ranks r and r + 1 of v of row m: the parts in their order, scaled.
-__device__ __forceinline__ float2 ranks_of(const Lora &p, int64_t m, int r, float scaling)
-{
-    float2 v = make_float2(0.0f, 0.0f);
-    if (m < 0 || r >= p.R)
-        return v;
-    const float2 *part = reinterpret_cast<const float2 *>(p.parts + m * p.R + r);
-    const int64_t next = p.M * p.R / 2;
-    for (int z = 0; z < p.splits; z += 4) {
-        float2 u[4];   // loaded together
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = z + i < p.splits ? part[(z + i) * next] : make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v.x = __fadd_rn(v.x, u[i].x);
-            v.y = __fadd_rn(v.y, u[i].y);
-        }
-    }
-    return make_float2(__fmul_rn(v.x, scaling), __fmul_rn(v.y, scaling));
-}
-
-// Two values as sums of kPlanes bf16 terms each.
-__device__ __forceinline__ void split(float2 v, uint32_t (&w)[kPlanes])
-{
-#pragma unroll
-    for (int i = 0; i < kPlanes; ++i) {
-        w[i] = pack_bf16x2(v.x, v.y);
-        // what is left of an infinity or NaN is nothing
-        v.x = isfinite(v.x) ? __fsub_rn(v.x, bf16_lo(w[i])) : 0.0f;
-        v.y = isfinite(v.y) ? __fsub_rn(v.y, bf16_hi(w[i])) : 0.0f;
-    }
-}
-
 // Eight columns of a row of the base as they are loaded, bf16 (in lo) or fp32.
 struct Base {
     uint4 lo, hi;
@@ -312,12 +247,6 @@ __device__ __forceinline__ void put(void *out, bool bf16_base, bool bf16_out, co
         static_cast<float4 *>(out)[0] = make_float4(f[0], f[1], f[2], f[3]);
         static_cast<float4 *>(out)[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
-}
-
-__device__ __forceinline__ float scaling_of(const Lora &p, int adapter)
-{
-    return adapter < 0 || p.scaling == nullptr
-               ? 1.0f : __uint_as_float(ld_global(reinterpret_cast<const uint32_t *>(p.scaling) + adapter));
 }
 
 // Few rows: a block per row (where a tile begins, or without an adapter) and 256
@@ -402,425 +331,36 @@ lora_expand_few_kernel(Lora p)
         put(at(m1), bf16_base, bf16_out, base1, {d[0][2], d[0][3], d[1][2], d[1][3], d[2][2], d[2][3], d[3][2], d[3][3]});
 }
 
-// ------------------------------------------------------------- many rows --
-// Tiles of 128 (or 64) neighbouring rows.  The adapters among a tile's rows, a few
-// at a time in ascending order, have their weights in the same stage of a ring
-// in shared memory (cp.async; rows 16 bytes apart from a multiple of 128, so that
-// the eight rows of a matrix load meet no bank twice).  A warp takes those that its rows
-// name, each for its own rows.
-__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(at)
-                 : "memory");
-}
-
-constexpr int kNoRow = 0x7fffffff;   // the adapter of a row past the end
-
-// The least adapter above `last` among `rows` in shared memory, kNoRow if there is none.  The same in every lane.
-__device__ __forceinline__ int adapter_after(const int *ids, int rows, int last)
-{
-    int least = kNoRow;
-    for (int i = threadIdx.x & 31; i < rows; i += 32)
-        least = ids[i] > last ? min(least, ids[i]) : least;
-    return __reduce_min_sync(kFull, least);
-}
-
-constexpr int kChunk = 64;                       // columns of x a stage
-constexpr int kRow = kChunk * 2 + 16;            // bytes of a row in shared memory
-
-template <int NT, int MW, int SLOTS, int STAGES, int THREADS>
-struct Shrink {
-    static constexpr int kRows = THREADS / 32 * 16 * MW, kRanks = NT * 8, kStages = STAGES;
-    static constexpr int kStage = (kRows + SLOTS * kRanks) * kRow;
-    static constexpr int kBytes = kStages * kStage;
-};
-
-// v: a warp has MW blocks of 16 rows and all ranks.
-template <int NT, int MW, int SLOTS, int STAGES, int THREADS>
-__global__ void __launch_bounds__(THREADS)
-lora_shrink_kernel(Lora p)
-{
-    using S = Shrink<NT, MW, SLOTS, STAGES, THREADS>;
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ int ids[S::kRows];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    const int64_t first = (int64_t)blockIdx.x * S::kRows;
-    grid_dependency_wait();
-    allow_dependents();
-    for (int r = threadIdx.x; r < S::kRows; r += THREADS) {
-        ids[r] = first + r < p.M ? adapter_of(p, first + r) : -1;
-        if (blockIdx.y == 0 && first + r < p.M && bad_id(p, first + r))
-            raise(p.err, EP_ERR_INVALID_EXPERT);
-    }
-    __syncthreads();
-    const int chunks = (p.K + kChunk - 1) / kChunk;
-    const int c0 = (int)((int64_t)chunks * blockIdx.y / p.splits), c1 = (int)((int64_t)chunks * (blockIdx.y + 1) / p.splits);
-    const uint32_t base = smem_u32(ring);
-    // this thread's pieces: of 16 bytes, at `piece` of rows r0, r0 + kStep, ...
-    const int r0 = threadIdx.x >> 3, piece = threadIdx.x & 7;
-    constexpr int kStep = THREADS / 8, kXPieces = S::kRows / kStep, kAPieces = (S::kRanks + kStep - 1) / kStep;
-    const int64_t x_row = (int64_t)p.K * 2 * kStep;   // from a piece to the next, in bytes
-    for (int now = adapter_after(ids, S::kRows, -1); now != kNoRow;) {
-        int slot_of[SLOTS];   // the adapters of this pass
-        int slots = 0;
-#pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-            slot_of[i] = now;
-            slots += now != kNoRow;
-            if (now != kNoRow)
-                now = adapter_after(ids, S::kRows, now);
-        }
-        uint32_t here = 0;   // rows of this thread's pieces that the pass is for
-#pragma unroll
-        for (int i = 0; i < kXPieces; ++i) {
-            const int id = ids[r0 + kStep * i];
-            here |= (id >= slot_of[0] && id < now && id != kNoRow ? 1u : 0u) << i;
-        }
-        uint32_t mine = 0;   // slots that this warp's rows name
-#pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-            bool any = false;
-#pragma unroll
-            for (int w = 0; w < MW; ++w)
-                any |= lane < 16 && ids[(warp * MW + w) * 16 + (lane & 15)] == slot_of[i];
-            if (__any_sync(kFull, any && slot_of[i] != kNoRow))
-                mine |= 1u << i;
-        }
-        const bool mixed = (mine & (mine - 1u)) != 0;
-        const uint8_t *x_at = p.x + ((first + r0) * p.K + piece * 8) * 2;
-        auto fetch = [&](int c) {
-            if (c < c1) {
-                const uint32_t to = base + (c % STAGES) * S::kStage + r0 * kRow + piece * 16;
-                const int64_t k = (int64_t)c * kChunk * 2;
-                const bool in = c * kChunk + piece * 8 < p.K;
-#pragma unroll
-                for (int i = 0; i < kXPieces; ++i) {
-                    const bool ok = in && (here >> i & 1u);
-                    cp_async16(to + i * kStep * kRow, ok ? x_at + i * x_row + k : p.x, ok);
-                }
-#pragma unroll
-                for (int i = 0; i < SLOTS; ++i) {
-                    if (i >= slots)
-                        break;
-                    const uint8_t *a_at = p.a + (((int64_t)slot_of[i] * p.R + r0) * p.K + piece * 8) * 2;
-#pragma unroll
-                    for (int j = 0; j < kAPieces; ++j) {
-                        const int r = r0 + kStep * j;
-                        const bool ok = in && r < p.R;
-                        if (r < S::kRanks)
-                            cp_async16(to + (S::kRows + i * S::kRanks + j * kStep) * kRow, ok ? a_at + j * x_row + k : p.a, ok);
-                    }
-                }
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i)
-            fetch(c0 + i);
-        float acc[MW][NT][4] = {}, sum[MW][NT][4] = {};   // sums of at most 128 columns are added with IEEE operations
-        for (int c = c0; c < c1; ++c) {
-            cp_async_wait<STAGES - 2>();
-            __syncthreads();
-            fetch(c + STAGES - 1);
-            const uint32_t stage = base + (c % STAGES) * S::kStage;
-            for (uint32_t todo = mine; todo != 0; todo &= todo - 1u) {
-                const int slot = __ffs(todo) - 1;
-                int now_id = slot_of[0];
-#pragma unroll
-                for (int i = 1; i < SLOTS; ++i)
-                    now_id = slot == i ? slot_of[i] : now_id;
-#pragma unroll
-                for (int k = 0; k < kChunk / 16; ++k) {
-                    uint32_t x[MW][4];
-#pragma unroll
-                    for (int i = 0; i < MW; ++i)
-                        load_matrices(x[i], stage + ((warp * MW + i) * 16 + (lane & 15)) * kRow + k * 32 + (lane >> 4) * 16);
-#pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
-                        uint32_t w[4];   // with one block of ranks the other half is not used
-                        const int row = NT > 1 ? n * 8 + (lane >> 4) * 8 + (lane & 7) : lane & 7;
-                        load_matrices(w, stage + (S::kRows + slot * S::kRanks + row) * kRow + k * 32 + (lane >> 3 & 1) * 16);
-#pragma unroll
-                        for (int i = 0; i < MW; ++i) {
-                            mma_bf16(sum[i][n], x[i][0], x[i][1], x[i][2], x[i][3], w[0], w[1]);
-                            if (NT > 1)
-                                mma_bf16(sum[i][(n + 1) % NT], x[i][0], x[i][1], x[i][2], x[i][3], w[2], w[3]);
-                        }
-                    }
-                }
-                // sums of one adapter go to its own rows: another's weights, were they infinite, would make NaN of zeros
-                if (mixed || (c - c0) % 2 == 1 || c + 1 == c1)
-#pragma unroll
-                    for (int i = 0; i < MW; ++i) {
-                        const bool own0 = !mixed || ids[(warp * MW + i) * 16 + g] == now_id;
-                        const bool own1 = !mixed || ids[(warp * MW + i) * 16 + g + 8] == now_id;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                if (v < 2 ? own0 : own1)
-                                    acc[i][n][v] = __fadd_rn(acc[i][n][v], sum[i][n][v]);
-                                sum[i][n][v] = 0.0f;
-                            }
-                    }
-            }
-        }
-        auto done = [&](int row) { return ids[row] >= slot_of[0] && ids[row] < now && ids[row] != kNoRow ? first + row : -1; };
-#pragma unroll
-        for (int i = 0; i < MW; ++i) {
-            const int row = (warp * MW + i) * 16 + g;
-            leave<NT>(p, acc[i], done(row), done(row + 8), blockIdx.y);
-        }
-        cp_async_wait<0>();
-        __syncthreads();
-    }
-}
-
-constexpr int kColumns = 64;     // of the output, a stage
-constexpr int kExpandRows = kWarps * kTile;
-constexpr int kExpandStages = 3;
-
-// Adapters whose B a stage holds, for KS steps of 16 ranks.
-__host__ __device__ constexpr int expand_slots(int ks) { return ks <= 2 ? 4 : 2; }
-
-__host__ __device__ constexpr int expand_stage(int ks, int base_bytes)
-{
-    return expand_slots(ks) * kColumns * (ks * 32 + 16) + kThreads * base_bytes;
-}
-
-// out: a warp has 16 rows, whose v it holds in registers, and the block `span`
-// columns.  A row of B's tile stands for a column as in the kernel for few rows; each
-// thread fetches the part of the base that it will add to.  WIDE: 1 for a bf16 base, 2 for fp32.
-template <int KS, int WIDE, bool BF16_OUT>
-__global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1)
-lora_expand_kernel(Lora p, int span)
-{
-    constexpr int kBRow = KS * 32 + 16, kSlots = expand_slots(KS), kBPieces = kColumns * KS * 2 / kThreads;
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ int ids[kExpandRows];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int64_t first = (int64_t)blockIdx.x * kExpandRows;
-    grid_dependency_wait();
-    allow_dependents();
-    for (int r = threadIdx.x; r < kExpandRows; r += kThreads)
-        ids[r] = first + r < p.M ? adapter_of(p, first + r) : kNoRow;
-    __syncthreads();
-    const int base_bytes = p.base == nullptr ? 0 : 64 * WIDE;
-    const int b_bytes = kSlots * kColumns * kBRow, stage_bytes = b_bytes + kThreads * base_bytes;
-    const int n_from = blockIdx.y * span, n_to = min(n_from + span, p.N);
-    const uint32_t ring_at = smem_u32(ring);
-    const int id0 = ids[warp * kTile + g], id1 = ids[warp * kTile + g + 8];
-    // this thread's pieces of a tile of B: rows b_row, b_row + kThreads / (2 KS), ...
-    const int b_piece = threadIdx.x % (KS * 2), b_row = threadIdx.x / (KS * 2);
-    const bool b_in = b_piece * 8 < p.R && b_row < kColumns;
-    for (int now = adapter_after(ids, kExpandRows, -2); now != kNoRow;) {
-        // rows without an adapter are a pass of their own, of nothing but the base
-        int slot_of[kSlots], slots = 0;
-        const int least = now;
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            slot_of[i] = now;
-            if (now != kNoRow && (i == 0 || least >= 0)) {
-                ++slots;
-                now = adapter_after(ids, kExpandRows, now);
-            }
-        }
-        const int64_t m0 = id0 >= least && id0 < now ? first + warp * kTile + g : -1;
-        const int64_t m1 = id1 >= least && id1 < now ? first + warp * kTile + g + 8 : -1;
-        const bool active = __any_sync(kFull, m0 >= 0 || m1 >= 0);
-        uint32_t mine = 0;   // slots that this warp's rows name
-        float scale0 = 1.0f, scale1 = 1.0f;
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-            if (i < slots && least >= 0) {
-                const bool in0 = id0 == slot_of[i], in1 = id1 == slot_of[i];
-                if (__any_sync(kFull, in0 || in1)) {
-                    mine |= 1u << i;
-                    const float scaling = scaling_of(p, slot_of[i]);
-                    scale0 = in0 ? scaling : scale0;
-                    scale1 = in1 ? scaling : scale1;
-                }
-            }
-        // 16 bytes of the base: row i (m0, m1), group of 32 columns j, part h of 32 bytes
-        const uint32_t own = ring_at + b_bytes + threadIdx.x * 16;
-        const uint8_t *base0 = static_cast<const uint8_t *>(p.base) + (m0 < 0 ? 0 : (m0 * p.N + 8 * t) * 2 * WIDE);
-        const uint8_t *base1 = static_cast<const uint8_t *>(p.base) + (m1 < 0 ? 0 : (m1 * p.N + 8 * t) * 2 * WIDE);
-        uint8_t *const out_at = static_cast<uint8_t *>(p.out) + (first + warp * kTile + g) * p.N * (BF16_OUT ? 2 : 4);
-        const int64_t rows_apart = (int64_t)8 * p.N * (BF16_OUT ? 2 : 4);
-        auto fetch = [&](int n0, int stage) {
-            if (n0 < n_to) {
-                const uint32_t to = ring_at + stage * stage_bytes;
-                if (least >= 0)
-#pragma unroll
-                    for (int z = 0; z < kSlots; ++z) {
-                        if (z >= slots)
-                            break;
-                        const uint8_t *b = p.b + (((int64_t)slot_of[z] * p.N + n0) * p.R + b_piece * 8) * 2;
-#pragma unroll
-                        for (int i = 0; i < (kBPieces > 0 ? kBPieces : 1); ++i) {
-                            const int row = b_row + i * (kThreads / (KS * 2));
-                            const int n = (row & 32) + 4 * (row & 6) + 2 * (row >> 3 & 3) + (row & 1);
-                            const bool ok = b_in && n0 + n < p.N;
-                            if (row < kColumns)
-                                cp_async16(to + (z * kColumns + row) * kBRow + b_piece * 16, ok ? b + n * p.R * 2 : p.b, ok);
-                        }
-                    }
-                if (p.base != nullptr) {
-                    const uint32_t slot = own + stage * stage_bytes;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int n = n0 + 32 * j;
-                        const bool in = n + 8 * t < p.N;
-#pragma unroll
-                        for (int h = 0; h < WIDE; ++h) {
-                            cp_async16(slot + (j * WIDE + h) * kThreads * 16, in ? base0 + n * 2 * WIDE + 16 * h : base0, in && m0 >= 0);
-                            cp_async16(slot + ((2 + j) * WIDE + h) * kThreads * 16, in ? base1 + n * 2 * WIDE + 16 * h : base1,
-                                       in && m1 >= 0);
-                        }
-                    }
-                }
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kExpandStages - 1; ++i)
-            fetch(n_from + i * kColumns, i);
-        uint32_t v[kPlanes][KS][4];
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t terms[kPlanes];
-                split(ranks_of(p, least < 0 ? -1 : w % 2 == 0 ? m0 : m1, k * 16 + (w / 2) * 8 + 2 * t, w % 2 == 0 ? scale0 : scale1),
-                      terms);
-#pragma unroll
-                for (int i = 0; i < kPlanes; ++i)
-                    v[i][k][w] = terms[i];
-            }
-        int stage = 0;
-        for (int n0 = n_from; n0 < n_to; n0 += kColumns) {
-            cp_async_wait<kExpandStages - 2>();
-            __syncthreads();
-            fetch(n0 + (kExpandStages - 1) * kColumns, stage == 0 ? kExpandStages - 1 : stage - 1);
-            if (active) {
-                // one adapter after the other, each for its own rows; without adapters, once for the base
-                for (uint32_t todo = least < 0 ? 1u : mine; todo != 0; todo &= todo - 1u) {
-                    const int slot = __ffs(todo) - 1;
-                    int id = slot_of[0];
-#pragma unroll
-                    for (int i = 1; i < kSlots; ++i)
-                        id = slot == i ? slot_of[i] : id;
-                    const float none = least >= 0 ? 0.0f : -0.0f;   // base + -0 is base
-                    float d[8][4];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        d[c][0] = d[c][1] = d[c][2] = d[c][3] = none;
-                    const uint32_t tile = ring_at + stage * stage_bytes +
-                                          (slot * kColumns + (lane >> 4) * 8 + (lane & 7)) * kBRow + (lane >> 3 & 1) * 16;
-                    if (least >= 0)
-#pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            uint32_t w[4][4];
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                load_matrices(w[c], tile + c * 16 * kBRow + k * 32);
-#pragma unroll
-                            for (int i = kPlanes - 1; i >= 0; --i)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    mma_bf16(d[c], v[i][k][0], v[i][k][1], v[i][k][2], v[i][k][3], w[c / 2][c % 2 * 2],
-                                             w[c / 2][c % 2 * 2 + 1]);
-                        }
-                    const uint32_t at = own + stage * stage_bytes;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int n = n0 + 32 * j + 8 * t;
-                        if (n >= p.N)
-                            continue;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if ((i == 0 ? id0 : id1) != id)
-                                continue;
-                            Base base{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                            if (p.base != nullptr) {
-                                base.lo = ld_shared16(at + (2 * i + j) * WIDE * kThreads * 16);
-                                if (WIDE == 2)
-                                    base.hi = ld_shared16(at + ((2 * i + j) * WIDE + 1) * kThreads * 16);
-                            }
-                            put(out_at + (i == 0 ? 0 : rows_apart) + (int64_t)n * (BF16_OUT ? 2 : 4), WIDE == 1, BF16_OUT, base,
-                                {d[4 * j][2 * i], d[4 * j][2 * i + 1], d[4 * j + 1][2 * i], d[4 * j + 1][2 * i + 1],
-                                 d[4 * j + 2][2 * i], d[4 * j + 2][2 * i + 1], d[4 * j + 3][2 * i], d[4 * j + 3][2 * i + 1]});
-                        }
-                    }
-                }
-            }
-            stage = stage + 1 == kExpandStages ? 0 : stage + 1;
-        }
-        cp_async_wait<0>();
-        __syncthreads();
-    }
-}
-
 // ---------------------------------------------------------------- launch --
-// Rows of a tile of many rows, 16 or 32 to a warp by what its registers hold.
-int tile_rows(int R) { return R <= 64 ? 128 : 64; }
-
-// Parts of K: as many as fill the GPU, at least a unit to a warp of each, or four
-// stages.  Tiles are estimated from the sizes alone.
-int splits_of(int64_t M, int K, int L, int R)
+// Parts of K: as many as fill the GPU, at least a unit to a warp of each, or 256
+// columns of many rows.  Tiles are estimated from the sizes alone.
+int splits_of(int64_t M, int K, int L)
 {
-    const bool few = M <= kGatherRows;
-    const int64_t tiles = few ? std::min<int64_t>(M, L + M / kTile) : ceil_div(M, tile_rows(R));
-    const int64_t most = std::min<int64_t>(kMaxSplits, ceil_div(K, few ? kUnit * kWarps : 4 * kChunk));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(most, kBlocks / std::max<int64_t>(1, tiles)));
+    const bool few = M <= kLoraFewRows;
+    const int64_t tiles = few ? std::min<int64_t>(M, L + M / kTile) : ceil_div(M, 128);
+    const int64_t most = std::min<int64_t>(kLoraMaxSplits, ceil_div(K, 256));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(most, kLoraBlocks / std::max<int64_t>(1, tiles)));
 }
 
-template <int NT, int MW, int SLOTS, int STAGES, int THREADS>
-int launch_shrink(const Lora &p, cudaStream_t stream)
+template <int NT, int UNITS, int WORDS>
+int launch_few(const Lora &p, cudaStream_t stream)
 {
-    if (p.M <= kGatherRows)
-        return launch_dependent(lora_shrink_few_kernel<NT>, dim3((unsigned)p.M, p.splits), kThreads, 0, stream, p);
-    using S = Shrink<NT, MW, SLOTS, STAGES, THREADS>;
-    static PerDevice set;
-    const int rc = raise_smem(lora_shrink_kernel<NT, MW, SLOTS, STAGES, THREADS>, S::kBytes, set);
+    const int rc = launch_dependent(lora_shrink_few_kernel<NT>, dim3((unsigned)p.M, p.splits), kThreads, 0, stream, p);
     if (rc != EP_OK)
         return rc;
-    return launch_dependent(lora_shrink_kernel<NT, MW, SLOTS, STAGES, THREADS>,
-                            dim3((unsigned)ceil_div(p.M, S::kRows), p.splits), THREADS, S::kBytes, stream, p);
-}
-
-template <int KS, int WIDE, bool BF16_OUT>
-int launch_expand_many(const Lora &p, cudaStream_t stream)
-{
-    static PerDevice set;
-    const int rc = raise_smem(lora_expand_kernel<KS, WIDE, BF16_OUT>, kExpandStages * expand_stage(KS, 64 * WIDE), set);
-    if (rc != EP_OK)
-        return rc;
-    const int64_t tiles = ceil_div(p.M, kExpandRows);
-    const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(ceil_div(p.N, kColumns), kBlocks / tiles));
-    const int span = (int)(ceil_div(ceil_div(p.N, pieces), kColumns) * kColumns);
-    return launch_dependent(lora_expand_kernel<KS, WIDE, BF16_OUT>, dim3((unsigned)tiles, (unsigned)ceil_div(p.N, span)),
-                            kThreads, (size_t)kExpandStages * expand_stage(KS, p.base == nullptr ? 0 : 64 * WIDE), stream, p,
-                            span);
-}
-
-template <int KS>
-int launch_expand_many(const Lora &p, cudaStream_t stream)
-{
-    if (p.base != nullptr && p.base_dtype != 0)
-        return p.out_dtype == 0 ? launch_expand_many<KS, 2, true>(p, stream) : launch_expand_many<KS, 2, false>(p, stream);
-    return p.out_dtype == 0 ? launch_expand_many<KS, 1, true>(p, stream) : launch_expand_many<KS, 1, false>(p, stream);
-}
-
-template <int UNITS, int WORDS>
-int launch_expand(const Lora &p, cudaStream_t stream)
-{
-    if (p.M > kGatherRows)
-        return launch_expand_many<UNITS * WORDS / 2>(p, stream);
     return launch_dependent(lora_expand_few_kernel<UNITS, WORDS>,
                             dim3((unsigned)p.M, (unsigned)ceil_div(p.N, 32 * kWarps)), kThreads, 0, stream, p);
+}
+
+int launch_few(const Lora &p, cudaStream_t stream)
+{
+    if (p.R <= 8)
+        return launch_few<1, 1, 2>(p, stream);
+    if (p.R <= 16)
+        return launch_few<2, 1, 2>(p, stream);
+    if (p.R <= 32)
+        return launch_few<4, 1, 4>(p, stream);
+    return p.R <= 64 ? launch_few<8, 2, 4>(p, stream) : launch_few<16, 4, 4>(p, stream);
 }
 
 }  // namespace
@@ -833,7 +373,7 @@ extern "C" size_t ep_lora_workspace_size(int64_t M, int R)
     if (M < 0 || R < 1)
         return 0;
     // splits_of(m) * m is at most this for every m <= M, so that a workspace serves smaller batches too
-    const int64_t rows = std::min<int64_t>(kMaxSplits * M, std::max<int64_t>(M, (int64_t)kBlocks * 128));
+    const int64_t rows = std::min<int64_t>(kLoraMaxSplits * M, std::max<int64_t>(M, (int64_t)kLoraBlocks * 128));
     return align_up((size_t)rows * R * sizeof(float), kWsAlign) + kWsAlign;
 }
 
@@ -844,7 +384,7 @@ extern "C" int ep_lora(const void *x, int64_t M, int K, const int64_t *ids, cons
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (M < 0 || K < 8 || K % 8 != 0 || N < 8 || N % 8 != 0 || R < 8 || R % 8 != 0 || L < 1)
         return EP_ERR_INVALID_ARG;
-    if ((out_dtype != 0 && out_dtype != 1) || (base != nullptr && base_dtype != 0 && base_dtype != 1) || R > kMaxRank ||
+    if ((out_dtype != 0 && out_dtype != 1) || (base != nullptr && base_dtype != 0 && base_dtype != 1) || R > kLoraMaxRank ||
         K > (1 << 24) || N > (1 << 24) || M > (1 << 24))
         return EP_ERR_UNSUPPORTED;
     if (M == 0)
@@ -855,16 +395,7 @@ extern "C" int ep_lora(const void *x, int64_t M, int K, const int64_t *ids, cons
         !aligned(ws, kWsAlign) || ws_bytes < ep_lora_workspace_size(M, R))
         return EP_ERR_INVALID_ARG;
     const Lora p{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(a), static_cast<const uint8_t *>(b), ids,
-                 scaling, base, out, M, K, N, R, L, splits_of(M, K, L, R), base_dtype, out_dtype, static_cast<float *>(ws),
+                 scaling, base, out, M, K, N, R, L, splits_of(M, K, L), base_dtype, out_dtype, static_cast<float *>(ws),
                  err};
-    const int rc = R <= 8 ? launch_shrink<1, 1, 4, 4, 256>(p, stream) : R <= 16 ? launch_shrink<2, 1, 4, 4, 256>(p, stream)
-                 : R <= 32 ? launch_shrink<4, 1, 4, 3, 256>(p, stream) : R <= 64 ? launch_shrink<8, 1, 2, 3, 256>(p, stream)
-                                                                                 : launch_shrink<16, 1, 1, 4, 128>(p, stream);
-    if (rc != EP_OK)
-        return rc;
-    if (R <= 16)
-        return launch_expand<1, 2>(p, stream);
-    if (R <= 32)
-        return launch_expand<1, 4>(p, stream);
-    return R <= 64 ? launch_expand<2, 4>(p, stream) : launch_expand<4, 4>(p, stream);
+    return M <= kLoraFewRows ? launch_few(p, stream) : launch_lora_many(p, stream);
 }

@@ -1,0 +1,591 @@
+// Low-rank adapters for many rows.
+//
+// Tiles of 128 neighbouring rows, on tcgen05 matrix steps of 128 x N.  A tile's rows may
+// name several adapters: they are taken a few at a time (a pass), side by side as N, so that
+// every row has a product with each of them, and each row keeps its own.  (One
+// adapter's infinities never meet another's rows.)  What a pass does not need is
+// not loaded.
+//
+//   shrink: x and the adapters' A come 64 columns at a time through a ring; the tensor
+//     memory's sums are taken into registers after every 128 columns and added there
+//     with IEEE operations, as a long chain of matrix steps loses bits.
+//   expand: v is made once for a tile, as three bf16 terms, and stays in shared
+//     memory; B comes 32 columns at a time; the base comes through a ring of each warp's
+//     own, where the sums are added to it and from where they leave in whole rows.
+//
+// Operands are copied by cp.async, which zeroes what is past the edges and takes any
+// alignment of 16 bytes; a thread that has waited for its copies makes them visible to
+// the matrix steps by a proxy fence.  Waits on barriers give up after a second
+// (EP_ERR_TIMEOUT).
+#include <algorithm>
+
+#include "ep_device.cuh"
+#include "ep_internal.h"
+#include "ep_launch.cuh"
+#include "ep_lora.cuh"
+#include "ep_skinny.cuh"
+#include "ep_tensor.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kRows = 128;           // of a tile
+constexpr int kNoRow = 0x7fffffff;   // the adapter of a row past the end
+constexpr uint64_t kLimitNs = 1000000000;
+
+// The least adapter above `last` among a tile's rows, kNoRow if there is none.  The same in every lane.
+__device__ __forceinline__ int adapter_after(const int *ids, int last)
+{
+    int least = kNoRow;
+#pragma unroll
+    for (int i = 0; i < kRows / 32; ++i) {
+        const int id = ids[i * 32 + (threadIdx.x & 31)];
+        least = id > last ? min(least, id) : least;
+    }
+    return __reduce_min_sync(kFull, least);
+}
+
+// The adapters of a pass: up to SLOTS in ascending order, and the first that is left for the next pass.
+template <int SLOTS>
+struct Pass {
+    int slot[SLOTS], slots, next;
+
+    __device__ __forceinline__ void set(const int *ids, int first)
+    {
+        next = first;
+        slots = 0;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            slot[i] = next;
+            if (next != kNoRow) {
+                ++slots;
+                next = adapter_after(ids, next);
+            }
+        }
+    }
+
+    __device__ __forceinline__ bool has(int id) const { return id >= slot[0] && id < next; }
+
+    // the slots that the lanes' adapters name
+    __device__ __forceinline__ uint32_t mask(int id) const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+            m |= (i < slots && id == slot[i] ? 1u : 0u) << i;
+        return __reduce_or_sync(kFull, m);
+    }
+
+    __device__ __forceinline__ int id_of(int i) const
+    {
+        int id = slot[0];
+#pragma unroll
+        for (int j = 1; j < SLOTS; ++j)
+            id = i == j ? slot[j] : id;
+        return id;
+    }
+};
+
+// Waits until the n-th use of a barrier that is completed once a use; false (once and for all) after a second.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, int n, volatile int *failed)
+{
+    if (mbar_wait(bar, n & 1, kLimitNs))
+        return true;
+    *failed = 1;
+    return false;
+}
+
+// ---------------------------------------------------------------- shrink --
+constexpr int kFlushWarps = 4, kLoadThreads = 128;
+constexpr int kShrinkThreads = kFlushWarps * 32 + kLoadThreads + 32;
+constexpr int kChunk = 64;      // columns of x a stage
+constexpr int kGroup = 2;       // stages of a sum
+
+template <int RP, int SLOTS, int STAGES>
+struct Shrink {
+    static constexpr int kX = kRows * 128, kN = SLOTS * RP, kStage = kX + kN * 128;
+    static constexpr int kColumns = 2 * kN;                      // of tensor memory
+    static constexpr int kBytes = STAGES * kStage + 1024;        // and room to align
+};
+
+template <int RP, int SLOTS, int STAGES>
+__global__ void __launch_bounds__(kShrinkThreads, RP <= 64 ? 2 : 1)
+lora_shrink_many_kernel(Lora p)
+{
+    using S = Shrink<RP, SLOTS, STAGES>;
+    constexpr int kLoad = RP < 32 ? RP : 32;   // columns of tensor memory a load
+    extern __shared__ uint8_t dynamic[];
+    __shared__ int ids[kRows];
+    __shared__ uint64_t full[STAGES], empty[STAGES], done[2], taken[2];
+    __shared__ uint32_t tensor;
+    __shared__ int failed;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = (int64_t)blockIdx.x * kRows;
+    const uint32_t ring = (smem_u32(dynamic) + 1023u) & ~1023u;
+    grid_dependency_wait();
+    allow_dependents();
+    if (threadIdx.x < kRows) {
+        const int64_t m = first + threadIdx.x;
+        ids[threadIdx.x] = m < p.M ? adapter_of(p, m) : -1;
+        if (blockIdx.y == 0 && m < p.M && bad_id(p, m))
+            raise(p.err, EP_ERR_INVALID_EXPERT);
+    }
+    if (threadIdx.x == 0) {
+        failed = 0;
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&full[i], kLoadThreads);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&taken[i], kFlushWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kFlushWarps + kLoadThreads / 32)
+        tensor_alloc(&tensor, S::kColumns);
+    tensor_fence_before();
+    __syncthreads();
+    tensor_fence_after();
+    const int chunks = (p.K + kChunk - 1) / kChunk;
+    const int c0 = (int)((int64_t)chunks * blockIdx.y / p.splits), c1 = (int)((int64_t)chunks * (blockIdx.y + 1) / p.splits);
+    int used = 0, summed = 0;   // stages and sums so far
+    Pass<SLOTS> pass;
+    if (warp < kFlushWarps) {
+        // a row to a thread
+        const int id = ids[threadIdx.x];
+        const int64_t m = first + threadIdx.x;
+        for (int now = adapter_after(ids, -1); now != kNoRow; now = pass.next) {
+            pass.set(ids, now);
+            const uint32_t mine = pass.mask(id);
+            float acc[RP] = {};
+            for (int c = c0; c < c1; c += kGroup, ++summed) {
+                const int buf = summed & 1;
+                if (!wait_for(&done[buf], summed >> 1, &failed))
+                    break;
+                tensor_fence_after();
+                for (uint32_t todo = mine; todo != 0; todo &= todo - 1u) {
+                    const int slot = __ffs(todo) - 1;
+                    const bool own = id == pass.id_of(slot);
+                    const uint32_t at = tensor + ((uint32_t)(warp * 32) << 16) + buf * S::kN + slot * RP;
+#pragma unroll
+                    for (int j = 0; j < RP; j += kLoad) {
+                        float f[kLoad];
+                        tensor_load<kLoad>(f, at + j);
+                        if (own)
+#pragma unroll
+                            for (int i = 0; i < kLoad; ++i)
+                                acc[j + i] = __fadd_rn(acc[j + i], f[i]);
+                    }
+                }
+                tensor_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&taken[buf]);
+            }
+            if (failed)
+                break;
+            if (pass.has(id)) {
+                float *to = p.parts + ((int64_t)blockIdx.y * p.M + m) * p.R;
+#pragma unroll
+                for (int r = 0; r < RP; r += 4)
+                    if (r < p.R)
+                        *reinterpret_cast<float4 *>(to + r) = make_float4(acc[r], acc[r + 1], acc[r + 2], acc[r + 3]);
+            }
+        }
+    } else if (warp < kFlushWarps + kLoadThreads / 32) {
+        // this thread's pieces: of 16 bytes, at `piece` of rows r0, r0 + 16, ...
+        const int t = threadIdx.x - kFlushWarps * 32, r0 = t >> 3, piece = t & 7;
+        constexpr int kAhead = STAGES - 1;   // stages copied before the first is waited for
+        int arrived = 0;
+        auto arrive = [&]() {
+            fence_async_shared();
+            mbar_arrive(&full[arrived++ % STAGES]);
+        };
+        for (int now = adapter_after(ids, -1); now != kNoRow; now = pass.next) {
+            pass.set(ids, now);
+            uint32_t here = 0;   // rows that the pass is for
+#pragma unroll
+            for (int i = 0; i < kRows / 16; ++i)
+                here |= (pass.has(ids[r0 + 16 * i]) ? 1u : 0u) << i;
+            const uint8_t *x_at = p.x + ((first + r0) * p.K + piece * 8) * 2;
+            const int64_t step = (int64_t)p.K * 2 * 16;   // from a piece to the next
+            for (int c = c0; c < c1; ++c, ++used) {
+                if (used >= STAGES && !wait_for(&empty[used % STAGES], used / STAGES - 1, &failed))
+                    break;
+                const uint32_t to = ring + (used % STAGES) * S::kStage;
+                const int64_t k = (int64_t)c * kChunk * 2;
+                const bool in = c * kChunk + piece * 8 < p.K;
+#pragma unroll
+                for (int i = 0; i < kRows / 16; ++i) {
+                    const bool ok = in && (here >> i & 1u);
+                    cp_async16(to + tile_offset(r0 + 16 * i, piece), ok ? x_at + i * step + k : p.x, ok);
+                }
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i)
+                    if (i < pass.slots) {
+                        const uint8_t *a_at = p.a + (((int64_t)pass.slot[i] * p.R + r0) * p.K + piece * 8) * 2;
+#pragma unroll
+                        for (int j = 0; j < RP / 16; ++j) {
+                            const bool ok = in && r0 + 16 * j < p.R;
+                            cp_async16(to + S::kX + tile_offset(i * RP + r0 + 16 * j, piece), ok ? a_at + j * step + k : p.a, ok);
+                        }
+                    }
+                cp_async_commit();
+                cp_async_wait<kAhead>();
+                if (used >= kAhead)
+                    arrive();
+            }
+            if (failed)
+                break;
+        }
+        cp_async_wait<0>();
+        while (arrived < used)
+            arrive();
+    } else {
+        for (int now = adapter_after(ids, -1); now != kNoRow; now = pass.next) {
+            pass.set(ids, now);
+            const uint32_t kind = step_kind(pass.slots * RP);
+            if (lane == 0)
+                for (int c = c0; c < c1; ++c, ++used) {
+                    const int at = (c - c0) % kGroup, buf = summed & 1;
+                    if ((at == 0 && summed >= 2 && !wait_for(&taken[buf], (summed >> 1) - 1, &failed)) ||
+                        !wait_for(&full[used % STAGES], used / STAGES, &failed))
+                        break;
+                    tensor_fence_after();
+                    const uint32_t stage = ring + (used % STAGES) * S::kStage;
+                    const uint64_t x = tile_descriptor(stage), a = tile_descriptor(stage + S::kX);
+#pragma unroll
+                    for (int k = 0; k < kChunk / 16; ++k)
+                        tensor_step(tensor + buf * S::kN, x + 2 * k, a + 2 * k, kind, at != 0 || k != 0);
+                    tensor_commit(&empty[used % STAGES]);
+                    if (at == kGroup - 1 || c + 1 == c1) {
+                        tensor_commit(&done[buf]);
+                        ++summed;
+                    }
+                }
+            __syncwarp();
+            if (failed)
+                break;
+        }
+    }
+    __syncthreads();
+    if (failed && threadIdx.x == 0)
+        raise(p.err, EP_ERR_TIMEOUT);
+    if (warp == kFlushWarps + kLoadThreads / 32)
+        tensor_free(tensor, S::kColumns);
+}
+
+// ---------------------------------------------------------------- expand --
+constexpr int kSumWarps = 4, kExpandThreads = kSumWarps * 32 + 32;
+constexpr int kColumns = 32;        // of the output, a stage
+constexpr int kExpandSlots = 2, kBStages = 3;
+
+// KB: runs of 64 ranks.  BASE, OUT: bytes of an element.
+template <int KB, int BASE, int OUT>
+struct Expand {
+    static constexpr int kV = kRows * 128;                                     // a term of v, 64 ranks
+    static constexpr int kB = kExpandSlots * kColumns * 128;                   // a stage of B, 64 ranks
+    static constexpr int kRowBytes = kColumns * (BASE > OUT ? BASE : OUT) + 16;
+    static constexpr int kRowStages = kRowBytes <= 80 ? 3 : 2;
+    static constexpr int kRoom = 32 * kRowBytes;                               // a warp's stage
+    static constexpr int kBytes = kPlanes * KB * kV + kBStages * KB * kB + kSumWarps * kRowStages * kRoom + 1024;
+    static constexpr int kTensor = 2 * kExpandSlots * kColumns;                // columns of tensor memory
+};
+
+template <int KB, int BASE, int OUT>
+__global__ void __launch_bounds__(kExpandThreads)
+lora_expand_many_kernel(Lora p, int span)
+{
+    using S = Expand<KB, BASE, OUT>;
+    extern __shared__ uint8_t dynamic[];
+    __shared__ int ids[kRows];
+    __shared__ uint64_t empty[kBStages], done[2], taken[2];
+    __shared__ uint32_t tensor;
+    __shared__ int failed;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = (int64_t)blockIdx.x * kRows;
+    const uint32_t v_at = (smem_u32(dynamic) + 1023u) & ~1023u, b_at = v_at + kPlanes * KB * S::kV;
+    const uint32_t rows_at = b_at + kBStages * KB * S::kB;
+    const int n_from = blockIdx.y * span, n_to = min(n_from + span, p.N);
+    const int steps = (p.R + 15) / 16;   // of 16 ranks
+    grid_dependency_wait();
+    allow_dependents();
+    if (threadIdx.x < kRows)
+        ids[threadIdx.x] = first + threadIdx.x < p.M ? adapter_of(p, first + threadIdx.x) : kNoRow;
+    if (threadIdx.x == 0) {
+        failed = 0;
+        for (int i = 0; i < kBStages; ++i)
+            mbar_init(&empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&taken[i], kSumWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kSumWarps)
+        tensor_alloc(&tensor, S::kTensor);
+    __syncthreads();
+    {   // v of every row, kBatch pairs of ranks a thread at a time
+        constexpr int kBatch = 4;
+        const int pairs = steps * 8, all = kRows * pairs;
+        for (int i = threadIdx.x; i < all; i += kBatch * kExpandThreads) {
+            float2 f[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int at = i + j * kExpandThreads, row = at / pairs, r = (at - row * pairs) * 2;
+                const int id = at < all ? ids[row] : -1;
+                const bool has = id >= 0 && id != kNoRow;
+                f[j] = ranks_of(p, has ? first + row : -1, r, has ? scaling_of(p, id) : 1.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int at = i + j * kExpandThreads, row = at / pairs, r = (at - row * pairs) * 2;
+                if (at >= all)
+                    break;
+                uint32_t terms[kPlanes];
+                split(f[j], terms);
+#pragma unroll
+                for (int z = 0; z < kPlanes; ++z)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(v_at + (z * KB + (r >> 6)) * S::kV +
+                                                                 tile_offset(row, (r & 63) >> 3) + (r & 7) * 2),
+                                 "r"(terms[z])
+                                 : "memory");
+            }
+        }
+    }
+    fence_async_shared();
+    tensor_fence_before();
+    __syncthreads();
+    tensor_fence_after();
+    int used = 0;   // chunks so far: stages of B, and sums
+    Pass<kExpandSlots> pass;
+    const int begin = adapter_after(ids, -1);
+    if (warp < kSumWarps) {
+        // a row to a thread for the sums; whole rows by neighbouring lanes for the base and the result
+        constexpr int kBasePieces = kColumns * BASE / 16, kOutPieces = kColumns * OUT / 16;
+        const int id = ids[threadIdx.x];
+        const uint32_t room = rows_at + warp * S::kRowStages * S::kRoom;
+        const int64_t row0 = first + warp * 32;
+        bool start = true;
+        for (int now = begin; start || now != kNoRow; now = pass.next) {
+            pass.set(ids, now);
+            // rows without an adapter go along with the first pass
+            const bool row_in = pass.has(id) || (start && id == -1);
+            const uint32_t rows = __ballot_sync(kFull, row_in), mine = pass.mask(id);
+            start = false;
+            auto fetch = [&](int n0, int stage) {
+                if (p.base != nullptr && n0 < n_to)
+#pragma unroll
+                    for (int i = 0; i < kBasePieces; ++i) {
+                        const int q = i * 32 + lane, row = q / kBasePieces, piece = q % kBasePieces;
+                        const int n = n0 + piece * (16 / BASE);
+                        const bool ok = (rows >> row & 1u) && n < p.N;
+                        cp_async16(room + stage * S::kRoom + row * S::kRowBytes + piece * 16,
+                                   ok ? static_cast<const uint8_t *>(p.base) + ((row0 + row) * p.N + n) * BASE : p.x, ok);
+                    }
+                cp_async_commit();
+            };
+#pragma unroll
+            for (int i = 0; i < S::kRowStages - 1; ++i)
+                fetch(n_from + i * kColumns, i);
+            int stage = 0;
+            for (int n0 = n_from; n0 < n_to; n0 += kColumns) {
+                fetch(n0 + (S::kRowStages - 1) * kColumns, stage == 0 ? S::kRowStages - 1 : stage - 1);
+                float d[kColumns];
+#pragma unroll
+                for (int i = 0; i < kColumns; ++i)
+                    d[i] = -0.0f;   // base + -0 is base
+                if (pass.slots > 0) {
+                    const int buf = used & 1;
+                    if (!wait_for(&done[buf], used >> 1, &failed))
+                        break;
+                    ++used;
+                    tensor_fence_after();
+                    for (uint32_t todo = mine; todo != 0; todo &= todo - 1u) {
+                        const int slot = __ffs(todo) - 1;
+                        float f[kColumns];
+                        tensor_load<kColumns>(f, tensor + ((uint32_t)(warp * 32) << 16) + (buf * kExpandSlots + slot) * kColumns);
+                        if (id == pass.id_of(slot))
+#pragma unroll
+                            for (int i = 0; i < kColumns; ++i)
+                                d[i] = f[i];
+                    }
+                    tensor_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&taken[buf]);
+                }
+                cp_async_wait<S::kRowStages - 1>();
+                __syncwarp();
+                const uint32_t own = room + stage * S::kRoom + lane * S::kRowBytes;
+                if (p.base != nullptr && row_in) {
+#pragma unroll
+                    for (int i = 0; i < kBasePieces; ++i) {
+                        const uint4 v = ld_shared16(own + i * 16);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (BASE == 4) {
+                                d[(i * 4 + j) % kColumns] = __fadd_rn(__uint_as_float(w[j]), d[(i * 4 + j) % kColumns]);
+                            } else {
+                                const int at = (i * 8 + j * 2) % kColumns;
+                                d[at] = __fadd_rn(bf16_lo(w[j]), d[at]);
+                                d[at + 1] = __fadd_rn(bf16_hi(w[j]), d[at + 1]);
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kColumns; ++i)
+                        d[i] = __fadd_rn(0.0f, d[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kOutPieces; ++i) {
+                    uint4 v;
+                    if (OUT == 2)
+                        v = make_uint4(pack_bf16x2(d[i * 8 % kColumns], d[(i * 8 + 1) % kColumns]),
+                                       pack_bf16x2(d[(i * 8 + 2) % kColumns], d[(i * 8 + 3) % kColumns]),
+                                       pack_bf16x2(d[(i * 8 + 4) % kColumns], d[(i * 8 + 5) % kColumns]),
+                                       pack_bf16x2(d[(i * 8 + 6) % kColumns], d[(i * 8 + 7) % kColumns]));
+                    else
+                        v = make_uint4(__float_as_uint(d[i * 4 % kColumns]), __float_as_uint(d[(i * 4 + 1) % kColumns]),
+                                       __float_as_uint(d[(i * 4 + 2) % kColumns]), __float_as_uint(d[(i * 4 + 3) % kColumns]));
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(own + i * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kOutPieces; ++i) {
+                    const int q = i * 32 + lane, row = q / kOutPieces, piece = q % kOutPieces;
+                    const int n = n0 + piece * (16 / OUT);
+                    if ((rows >> row & 1u) && n < p.N)
+                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + ((row0 + row) * p.N + n) * OUT) =
+                            ld_shared16(room + stage * S::kRoom + row * S::kRowBytes + piece * 16);
+                }
+                __syncwarp();   // before the stage is filled again
+                stage = stage + 1 == S::kRowStages ? 0 : stage + 1;
+            }
+            cp_async_wait<0>();
+            __syncwarp();
+            if (failed)
+                break;
+        }
+    } else {
+        for (int now = begin; now != kNoRow; now = pass.next) {
+            pass.set(ids, now);
+            const uint32_t kind = step_kind(pass.slots * kColumns);
+            const int chunks = (n_to - n_from + kColumns - 1) / kColumns;
+            // this lane's pieces of a tile of B: of 16 bytes, at `piece` of 64 ranks of rows r0, r0 + 4, ...
+            const int piece = lane & 7, r0 = lane >> 3;
+            for (int c = 0; c < chunks + kBStages - 1; ++c) {
+                if (c < chunks) {
+                    const int use = used + c;
+                    if (use >= kBStages && !wait_for(&empty[use % kBStages], use / kBStages - 1, &failed))
+                        break;
+                    const uint32_t to = b_at + use % kBStages * (KB * S::kB);
+                    const int n0 = n_from + c * kColumns;
+#pragma unroll
+                    for (int i = 0; i < kExpandSlots; ++i)
+                        if (i < pass.slots)
+#pragma unroll
+                            for (int b = 0; b < KB; ++b) {
+                                const int r = b * 64 + piece * 8;
+                                const uint8_t *from = p.b + (((int64_t)pass.slot[i] * p.N + n0 + r0) * p.R + r) * 2;
+                                if (r < steps * 16)
+#pragma unroll
+                                    for (int j = 0; j < kColumns / 4; ++j) {
+                                        const bool ok = r < p.R && n0 + r0 + 4 * j < p.N;
+                                        cp_async16(to + b * S::kB + tile_offset(i * kColumns + r0 + 4 * j, piece),
+                                                   ok ? from + (int64_t)j * 4 * p.R * 2 : p.b, ok);
+                                    }
+                            }
+                }
+                cp_async_commit();
+                cp_async_wait<kBStages - 1>();
+                fence_async_shared();
+                __syncwarp();
+                const int at = c - (kBStages - 1);
+                if (at < 0)
+                    continue;
+                const int use = used + at, buf = use & 1;
+                if (use >= 2 && !wait_for(&taken[buf], (use >> 1) - 1, &failed))
+                    break;
+                if (lane == 0) {
+                    tensor_fence_after();
+                    const uint32_t d = tensor + buf * kExpandSlots * kColumns, stage = b_at + use % kBStages * (KB * S::kB);
+                    bool add = false;
+#pragma unroll
+                    for (int z = kPlanes - 1; z >= 0; --z)
+                        for (int k = 0; k < steps; ++k) {
+                            const uint64_t a = tile_descriptor(v_at + (z * KB + (k >> 2)) * S::kV) + 2 * (k & 3);
+                            const uint64_t b = tile_descriptor(stage + (k >> 2) * S::kB) + 2 * (k & 3);
+                            tensor_step(d, a, b, kind, add);
+                            add = true;
+                        }
+                    tensor_commit(&empty[use % kBStages]);
+                    tensor_commit(&done[buf]);
+                }
+                __syncwarp();
+            }
+            cp_async_wait<0>();
+            if (failed)
+                break;
+            used += chunks;
+        }
+    }
+    __syncthreads();
+    if (failed && threadIdx.x == 0)
+        raise(p.err, EP_ERR_TIMEOUT);
+    if (warp == kSumWarps)
+        tensor_free(tensor, S::kTensor);
+}
+
+// ---------------------------------------------------------------- launch --
+template <int RP, int SLOTS, int STAGES>
+int launch_shrink(const Lora &p, cudaStream_t stream)
+{
+    using S = Shrink<RP, SLOTS, STAGES>;
+    static PerDevice set;
+    const int rc = raise_smem(lora_shrink_many_kernel<RP, SLOTS, STAGES>, S::kBytes, set);
+    if (rc != EP_OK)
+        return rc;
+    return launch_dependent(lora_shrink_many_kernel<RP, SLOTS, STAGES>, dim3((unsigned)ceil_div(p.M, kRows), p.splits),
+                            kShrinkThreads, S::kBytes, stream, p);
+}
+
+template <int KB, int BASE, int OUT>
+int launch_expand(const Lora &p, cudaStream_t stream)
+{
+    using S = Expand<KB, BASE, OUT>;
+    static PerDevice set;
+    const int rc = raise_smem(lora_expand_many_kernel<KB, BASE, OUT>, S::kBytes, set);
+    if (rc != EP_OK)
+        return rc;
+    const int64_t tiles = ceil_div(p.M, kRows);
+    const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(ceil_div(p.N, kColumns), kLoraBlocks / KB / tiles));
+    const int span = (int)(ceil_div(ceil_div(p.N, pieces), kColumns) * kColumns);
+    return launch_dependent(lora_expand_many_kernel<KB, BASE, OUT>, dim3((unsigned)tiles, (unsigned)ceil_div(p.N, span)),
+                            kExpandThreads, S::kBytes, stream, p, span);
+}
+
+template <int KB>
+int launch_expand(const Lora &p, cudaStream_t stream)
+{
+    if (p.base != nullptr && p.base_dtype != 0)
+        return p.out_dtype == 0 ? launch_expand<KB, 4, 2>(p, stream) : launch_expand<KB, 4, 4>(p, stream);
+    return p.out_dtype == 0 ? launch_expand<KB, 2, 2>(p, stream) : launch_expand<KB, 2, 4>(p, stream);
+}
+
+}  // namespace
+
+int launch_lora_many(const Lora &p, cudaStream_t stream)
+{
+    const int rc = p.R <= 16 ? launch_shrink<16, 4, 4>(p, stream) : p.R <= 32 ? launch_shrink<32, 4, 3>(p, stream)
+                   : p.R <= 64 ? launch_shrink<64, 2, 3>(p, stream) : launch_shrink<128, 2, 3>(p, stream);
+    if (rc != EP_OK)
+        return rc;
+    return p.R <= 64 ? launch_expand<1>(p, stream) : launch_expand<2>(p, stream);
+}
+
+}  // namespace ep
