@@ -86,13 +86,21 @@ struct Pass {
     }
 };
 
-// Waits until the n-th use of a barrier that is completed once a use; false (once and for all) after a second.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, int n, volatile int *failed)
+// One thread waits for the n-th use of a barrier that is completed once a use; false (once and for all) after a second.
+__device__ __forceinline__ bool wait_alone(uint64_t *bar, int n, volatile int *failed)
 {
     if (mbar_wait(bar, n & 1, kLimitNs))
         return true;
     *failed = 1;
     return false;
+}
+
+// A whole warp waits.  Lanes may leave the spin one by one, and the way out of a wait that failed leaves the caller's
+// loop, so that they would meet again only behind it: the vote brings them together for the .aligned instructions here.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, int n, volatile int *failed)
+{
+    const bool ok = wait_alone(bar, n, failed);
+    return __all_sync(kFull, ok);
 }
 
 // ---------------------------------------------------------------- shrink --
@@ -142,6 +150,7 @@ lora_shrink_many_kernel(Lora p)
         }
         fence_mbar_init();
     }
+    __syncwarp();
     if (warp == kFlushWarps + kLoadThreads / 32)
         tensor_alloc(&tensor, S::kColumns);
     tensor_fence_before();
@@ -249,8 +258,8 @@ lora_shrink_many_kernel(Lora p)
             if (lane == 0)
                 for (int c = c0; c < c1; ++c, ++used) {
                     const int at = (c - c0) % kGroup, buf = summed & 1;
-                    if ((at == 0 && summed >= 2 && !wait_for(&taken[buf], (summed >> 1) - 1, &failed)) ||
-                        !wait_for(&full[used % STAGES], used / STAGES, &failed))
+                    if ((at == 0 && summed >= 2 && !wait_alone(&taken[buf], (summed >> 1) - 1, &failed)) ||
+                        !wait_alone(&full[used % STAGES], used / STAGES, &failed))
                         break;
                     tensor_fence_after();
                     const uint32_t stage = ring + (used % STAGES) * S::kStage;
@@ -272,34 +281,44 @@ lora_shrink_many_kernel(Lora p)
     __syncthreads();
     if (failed && threadIdx.x == 0)
         raise(p.err, EP_ERR_TIMEOUT);
+    __syncwarp();
     if (warp == kFlushWarps + kLoadThreads / 32)
         tensor_free(tensor, S::kColumns);
 }
 
 // ---------------------------------------------------------------- expand --
-constexpr int kSumWarps = 4, kExpandThreads = kSumWarps * 32 + 32;
-constexpr int kColumns = 32;        // of the output, a stage
-constexpr int kExpandSlots = 2, kBStages = 3;
+constexpr int kSumWarps = 8, kExpandThreads = kSumWarps * 32 + 32;
+constexpr int kColumns = 32;        // of the output, a chunk
+constexpr int kExpandSlots = 2, kBStages = 3, kRowStages = 2;
 
 // KB: runs of 64 ranks.  BASE, OUT: bytes of an element.
 template <int KB, int BASE, int OUT>
 struct Expand {
     static constexpr int kV = kRows * 128;                                     // a term of v, 64 ranks
     static constexpr int kB = kExpandSlots * kColumns * 128;                   // a stage of B, 64 ranks
-    static constexpr int kRowBytes = kColumns * (BASE > OUT ? BASE : OUT) + 16;
-    static constexpr int kRowStages = kRowBytes <= 80 ? 3 : 2;
+    static constexpr int kRowBytes = kColumns * (BASE > OUT ? BASE : OUT);
     static constexpr int kRoom = 32 * kRowBytes;                               // a warp's stage
     static constexpr int kBytes = kPlanes * KB * kV + kBStages * KB * kB + kSumWarps * kRowStages * kRoom + 1024;
     static constexpr int kTensor = 2 * kExpandSlots * kColumns;                // columns of tensor memory
+    static constexpr int kPerSM = KB == 1 && kBytes <= 112 * 1024 ? 2 : 1;     // blocks
+
+    // a 16-byte piece of a row, so that eight rows' meet no bank twice
+    __device__ __forceinline__ static uint32_t piece(int row, int i)
+    {
+        return row * kRowBytes + ((kRowBytes == 64 ? i ^ (row >> 1 & 3) : i ^ (row & 7)) << 4);
+    }
 };
 
+// Warps 0-3 take the even chunks, 4-7 the odd ones, each its own buffer of tensor memory; warp 8 copies B and issues the
+// matrix steps.
 template <int KB, int BASE, int OUT>
-__global__ void __launch_bounds__(kExpandThreads)
+__global__ void __launch_bounds__(kExpandThreads, (Expand<KB, BASE, OUT>::kPerSM))
 lora_expand_many_kernel(Lora p, int span)
 {
     using S = Expand<KB, BASE, OUT>;
     extern __shared__ uint8_t dynamic[];
     __shared__ int ids[kRows];
+    __shared__ float scales[kRows];
     __shared__ uint64_t empty[kBStages], done[2], taken[2];
     __shared__ uint32_t tensor;
     __shared__ int failed;
@@ -308,49 +327,51 @@ lora_expand_many_kernel(Lora p, int span)
     const uint32_t v_at = (smem_u32(dynamic) + 1023u) & ~1023u, b_at = v_at + kPlanes * KB * S::kV;
     const uint32_t rows_at = b_at + kBStages * KB * S::kB;
     const int n_from = blockIdx.y * span, n_to = min(n_from + span, p.N);
+    const int chunks = (n_to - n_from + kColumns - 1) / kColumns;
     const int steps = (p.R + 15) / 16;   // of 16 ranks
     grid_dependency_wait();
     allow_dependents();
-    if (threadIdx.x < kRows)
-        ids[threadIdx.x] = first + threadIdx.x < p.M ? adapter_of(p, first + threadIdx.x) : kNoRow;
+    if (threadIdx.x < kRows) {
+        const int id = first + threadIdx.x < p.M ? adapter_of(p, first + threadIdx.x) : kNoRow;
+        ids[threadIdx.x] = id;
+        scales[threadIdx.x] = id == kNoRow ? 1.0f : scaling_of(p, id);
+    }
     if (threadIdx.x == 0) {
         failed = 0;
         for (int i = 0; i < kBStages; ++i)
             mbar_init(&empty[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
-            mbar_init(&taken[i], kSumWarps);
+            mbar_init(&taken[i], kSumWarps / 2);
         }
         fence_mbar_init();
     }
+    __syncwarp();
     if (warp == kSumWarps)
         tensor_alloc(&tensor, S::kTensor);
     __syncthreads();
-    {   // v of every row, kBatch pairs of ranks a thread at a time
+    if (warp < kSumWarps) {   // v of every row: a thread has a pair of ranks of several rows, kBatch of them at a time
         constexpr int kBatch = 4;
-        const int pairs = steps * 8, all = kRows * pairs;
-        for (int i = threadIdx.x; i < all; i += kBatch * kExpandThreads) {
+        const int log_pairs = p.R <= 16 ? 3 : p.R <= 32 ? 4 : p.R <= 64 ? 5 : 6;
+        const int r = (threadIdx.x & ((1 << log_pairs) - 1)) * 2, apart = kSumWarps * 32 >> log_pairs;
+        for (int row = threadIdx.x >> log_pairs; row < kRows; row += kBatch * apart) {
             float2 f[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int at = i + j * kExpandThreads, row = at / pairs, r = (at - row * pairs) * 2;
-                const int id = at < all ? ids[row] : -1;
-                const bool has = id >= 0 && id != kNoRow;
-                f[j] = ranks_of(p, has ? first + row : -1, r, has ? scaling_of(p, id) : 1.0f);
+                const int at = row + j * apart, id = at < kRows ? ids[at] : -1;
+                f[j] = ranks_of(p, id >= 0 && id != kNoRow ? first + at : -1, r, id >= 0 ? scales[at] : 1.0f);
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int at = i + j * kExpandThreads, row = at / pairs, r = (at - row * pairs) * 2;
-                if (at >= all)
+                const int at = row + j * apart;
+                if (at >= kRows || r >= steps * 16)
                     break;
                 uint32_t terms[kPlanes];
                 split(f[j], terms);
+                const uint32_t to = v_at + (r >> 6) * S::kV + tile_offset(at, (r & 63) >> 3) + (r & 7) * 2;
 #pragma unroll
                 for (int z = 0; z < kPlanes; ++z)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(v_at + (z * KB + (r >> 6)) * S::kV +
-                                                                 tile_offset(row, (r & 63) >> 3) + (r & 7) * 2),
-                                 "r"(terms[z])
-                                 : "memory");
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + z * KB * S::kV), "r"(terms[z]) : "memory");
             }
         }
     }
@@ -358,15 +379,22 @@ lora_expand_many_kernel(Lora p, int span)
     tensor_fence_before();
     __syncthreads();
     tensor_fence_after();
-    int used = 0;   // chunks so far: stages of B, and sums
     Pass<kExpandSlots> pass;
     const int begin = adapter_after(ids, -1);
     if (warp < kSumWarps) {
         // a row to a thread for the sums; whole rows by neighbouring lanes for the base and the result
         constexpr int kBasePieces = kColumns * BASE / 16, kOutPieces = kColumns * OUT / 16;
-        const int id = ids[threadIdx.x];
-        const uint32_t room = rows_at + warp * S::kRowStages * S::kRoom;
-        const int64_t row0 = first + warp * 32;
+        const int group = warp >> 2, mine0 = (warp & 3) * 32, id = ids[mine0 + lane];
+        const uint32_t room = rows_at + warp * kRowStages * S::kRoom;
+        const uint32_t sums = tensor + ((uint32_t)mine0 << 16) + group * kExpandSlots * kColumns;
+        // this lane's pieces: of rows lane / pieces, and so many further
+        const int base_row = lane / kBasePieces, base_piece = lane % kBasePieces;
+        const int out_row = lane / kOutPieces, out_piece = lane % kOutPieces;
+        const uint8_t *const base_at = static_cast<const uint8_t *>(p.base) + (first + mine0 + base_row) * p.N * BASE + base_piece * 16;
+        uint8_t *const out_at = static_cast<uint8_t *>(p.out) + (first + mine0 + out_row) * p.N * OUT + out_piece * 16;
+        const int64_t base_apart = (int64_t)(32 / kBasePieces) * p.N * BASE, out_apart = (int64_t)(32 / kOutPieces) * p.N * OUT;
+        int used = 0;       // sums of this group so far
+        int before = 0;     // chunks of the passes so far
         bool start = true;
         for (int now = begin; start || now != kNoRow; now = pass.next) {
             pass.set(ids, now);
@@ -374,64 +402,75 @@ lora_expand_many_kernel(Lora p, int span)
             const bool row_in = pass.has(id) || (start && id == -1);
             const uint32_t rows = __ballot_sync(kFull, row_in), mine = pass.mask(id);
             start = false;
-            auto fetch = [&](int n0, int stage) {
-                if (p.base != nullptr && n0 < n_to)
+            // the group of a chunk goes on counting through the passes, as the buffers do
+            const int c0 = (before & 1) == group ? 0 : 1;
+            if (pass.slots > 0)
+                before += chunks;
+            auto fetch = [&](int c, int stage) {
+                if (p.base != nullptr && c < chunks) {
+                    const int n0 = n_from + c * kColumns;
+                    const bool in = n0 + base_piece * (16 / BASE) < p.N;
 #pragma unroll
                     for (int i = 0; i < kBasePieces; ++i) {
-                        const int q = i * 32 + lane, row = q / kBasePieces, piece = q % kBasePieces;
-                        const int n = n0 + piece * (16 / BASE);
-                        const bool ok = (rows >> row & 1u) && n < p.N;
-                        cp_async16(room + stage * S::kRoom + row * S::kRowBytes + piece * 16,
-                                   ok ? static_cast<const uint8_t *>(p.base) + ((row0 + row) * p.N + n) * BASE : p.x, ok);
+                        const int row = base_row + i * (32 / kBasePieces);
+                        const bool ok = in && (rows >> row & 1u);
+                        cp_async16(room + stage * S::kRoom + S::piece(row, base_piece),
+                                   ok ? base_at + i * base_apart + (int64_t)n0 * BASE : p.x, ok);
                     }
+                }
                 cp_async_commit();
             };
-#pragma unroll
-            for (int i = 0; i < S::kRowStages - 1; ++i)
-                fetch(n_from + i * kColumns, i);
+            fetch(c0, 0);
             int stage = 0;
-            for (int n0 = n_from; n0 < n_to; n0 += kColumns) {
-                fetch(n0 + (S::kRowStages - 1) * kColumns, stage == 0 ? S::kRowStages - 1 : stage - 1);
+            for (int c = c0; c < chunks; c += 2, stage ^= 1) {
+                fetch(c + 2, stage ^ 1);
+                const int n0 = n_from + c * kColumns;
                 float d[kColumns];
 #pragma unroll
                 for (int i = 0; i < kColumns; ++i)
                     d[i] = -0.0f;   // base + -0 is base
                 if (pass.slots > 0) {
-                    const int buf = used & 1;
-                    if (!wait_for(&done[buf], used >> 1, &failed))
+                    if (!wait_for(&done[group], used++, &failed))
                         break;
-                    ++used;
                     tensor_fence_after();
-                    for (uint32_t todo = mine; todo != 0; todo &= todo - 1u) {
-                        const int slot = __ffs(todo) - 1;
-                        float f[kColumns];
-                        tensor_load<kColumns>(f, tensor + ((uint32_t)(warp * 32) << 16) + (buf * kExpandSlots + slot) * kColumns);
-                        if (id == pass.id_of(slot))
+                    if (mine != 0 && (mine & (mine - 1u)) == 0) {   // rows of one adapter, or of none here
+                        tensor_load<kColumns>(d, sums + (__ffs(mine) - 1) * kColumns);
+                        if (id == -1)
 #pragma unroll
                             for (int i = 0; i < kColumns; ++i)
-                                d[i] = f[i];
+                                d[i] = -0.0f;
+                    } else {
+                        for (uint32_t todo = mine; todo != 0; todo &= todo - 1u) {
+                            const int slot = __ffs(todo) - 1;
+                            float f[kColumns];
+                            tensor_load<kColumns>(f, sums + slot * kColumns);
+                            if (id == pass.id_of(slot))
+#pragma unroll
+                                for (int i = 0; i < kColumns; ++i)
+                                    d[i] = f[i];
+                        }
                     }
                     tensor_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(&taken[buf]);
+                        mbar_arrive(&taken[group]);
                 }
-                cp_async_wait<S::kRowStages - 1>();
+                cp_async_wait<1>();
                 __syncwarp();
-                const uint32_t own = room + stage * S::kRoom + lane * S::kRowBytes;
-                if (p.base != nullptr && row_in) {
+                const uint32_t at = room + stage * S::kRoom;
+                if (p.base != nullptr) {
 #pragma unroll
                     for (int i = 0; i < kBasePieces; ++i) {
-                        const uint4 v = ld_shared16(own + i * 16);
+                        const uint4 v = ld_shared16(at + S::piece(lane, i));
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (BASE == 4) {
                                 d[(i * 4 + j) % kColumns] = __fadd_rn(__uint_as_float(w[j]), d[(i * 4 + j) % kColumns]);
                             } else {
-                                const int at = (i * 8 + j * 2) % kColumns;
-                                d[at] = __fadd_rn(bf16_lo(w[j]), d[at]);
-                                d[at + 1] = __fadd_rn(bf16_hi(w[j]), d[at + 1]);
+                                const int k = (i * 8 + j * 2) % kColumns;
+                                d[k] = __fadd_rn(bf16_lo(w[j]), d[k]);
+                                d[k + 1] = __fadd_rn(bf16_hi(w[j]), d[k + 1]);
                             }
                         }
                     }
@@ -451,20 +490,20 @@ lora_expand_many_kernel(Lora p, int span)
                     else
                         v = make_uint4(__float_as_uint(d[i * 4 % kColumns]), __float_as_uint(d[(i * 4 + 1) % kColumns]),
                                        __float_as_uint(d[(i * 4 + 2) % kColumns]), __float_as_uint(d[(i * 4 + 3) % kColumns]));
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(own + i * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + S::piece(lane, i)), "r"(v.x), "r"(v.y),
+                                 "r"(v.z), "r"(v.w)
                                  : "memory");
                 }
                 __syncwarp();
+                const bool in = n0 + out_piece * (16 / OUT) < p.N;
 #pragma unroll
                 for (int i = 0; i < kOutPieces; ++i) {
-                    const int q = i * 32 + lane, row = q / kOutPieces, piece = q % kOutPieces;
-                    const int n = n0 + piece * (16 / OUT);
-                    if ((rows >> row & 1u) && n < p.N)
-                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + ((row0 + row) * p.N + n) * OUT) =
-                            ld_shared16(room + stage * S::kRoom + row * S::kRowBytes + piece * 16);
+                    const int row = out_row + i * (32 / kOutPieces);
+                    if (in && (rows >> row & 1u))
+                        *reinterpret_cast<uint4 *>(out_at + i * out_apart + (int64_t)n0 * OUT) =
+                            ld_shared16(at + S::piece(row, out_piece));
                 }
                 __syncwarp();   // before the stage is filled again
-                stage = stage + 1 == S::kRowStages ? 0 : stage + 1;
             }
             cp_async_wait<0>();
             __syncwarp();
@@ -472,10 +511,10 @@ lora_expand_many_kernel(Lora p, int span)
                 break;
         }
     } else {
+        int used = 0;   // chunks so far: stages of B, and sums
         for (int now = begin; now != kNoRow; now = pass.next) {
             pass.set(ids, now);
             const uint32_t kind = step_kind(pass.slots * kColumns);
-            const int chunks = (n_to - n_from + kColumns - 1) / kColumns;
             // this lane's pieces of a tile of B: of 16 bytes, at `piece` of 64 ranks of rows r0, r0 + 4, ...
             const int piece = lane & 7, r0 = lane >> 3;
             for (int c = 0; c < chunks + kBStages - 1; ++c) {
@@ -497,7 +536,7 @@ lora_expand_many_kernel(Lora p, int span)
                                     for (int j = 0; j < kColumns / 4; ++j) {
                                         const bool ok = r < p.R && n0 + r0 + 4 * j < p.N;
                                         cp_async16(to + b * S::kB + tile_offset(i * kColumns + r0 + 4 * j, piece),
-                                                   ok ? from + (int64_t)j * 4 * p.R * 2 : p.b, ok);
+                                                   ok ? from + j * 8 * p.R : p.b, ok);
                                     }
                             }
                 }
@@ -529,6 +568,7 @@ lora_expand_many_kernel(Lora p, int span)
                 __syncwarp();
             }
             cp_async_wait<0>();
+            __syncwarp();
             if (failed)
                 break;
             used += chunks;
@@ -537,6 +577,7 @@ lora_expand_many_kernel(Lora p, int span)
     __syncthreads();
     if (failed && threadIdx.x == 0)
         raise(p.err, EP_ERR_TIMEOUT);
+    __syncwarp();
     if (warp == kSumWarps)
         tensor_free(tensor, S::kTensor);
 }
@@ -563,7 +604,7 @@ int launch_expand(const Lora &p, cudaStream_t stream)
     if (rc != EP_OK)
         return rc;
     const int64_t tiles = ceil_div(p.M, kRows);
-    const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(ceil_div(p.N, kColumns), kLoraBlocks / KB / tiles));
+    const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(ceil_div(p.N, kColumns), kLoraBlocks / 2 * S::kPerSM / tiles));
     const int span = (int)(ceil_div(ceil_div(p.N, pieces), kColumns) * kColumns);
     return launch_dependent(lora_expand_many_kernel<KB, BASE, OUT>, dim3((unsigned)tiles, (unsigned)ceil_div(p.N, span)),
                             kExpandThreads, S::kBytes, stream, p, span);

@@ -66,6 +66,7 @@ __device__ __forceinline__ void tensor_load(float (&f)[N], uint32_t at)
 {
     static_assert(N == 16 || N == 32, "columns of a load");
     uint32_t r[N];
+    __syncwarp();   // the warp is together for an .aligned instruction
     if constexpr (N == 32)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
                      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
