@@ -512,6 +512,10 @@ lora_expand_many_kernel(Lora p, int span)
         }
     } else {
         int used = 0;   // chunks so far: stages of B, and sums
+        uint64_t terms[kPlanes];
+#pragma unroll
+        for (int z = 0; z < kPlanes; ++z)
+            terms[z] = tile_descriptor(v_at + z * KB * S::kV);
         for (int now = begin; now != kNoRow; now = pass.next) {
             pass.set(ids, now);
             const uint32_t kind = step_kind(pass.slots * kColumns);
@@ -553,15 +557,26 @@ lora_expand_many_kernel(Lora p, int span)
                 if (lane == 0) {
                     tensor_fence_after();
                     const uint32_t d = tensor + buf * kExpandSlots * kColumns, stage = b_at + use % kBStages * (KB * S::kB);
-                    bool add = false;
+                    if constexpr (KB == 1) {
+                        // few instructions to a step: one thread issues them all
+                        const uint64_t b = tile_descriptor(stage);
 #pragma unroll
-                    for (int z = kPlanes - 1; z >= 0; --z)
-                        for (int k = 0; k < steps; ++k) {
-                            const uint64_t a = tile_descriptor(v_at + (z * KB + (k >> 2)) * S::kV) + 2 * (k & 3);
-                            const uint64_t b = tile_descriptor(stage + (k >> 2) * S::kB) + 2 * (k & 3);
-                            tensor_step(d, a, b, kind, add);
-                            add = true;
-                        }
+                        for (int z = kPlanes - 1; z >= 0; --z)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < steps)
+                                    tensor_step(d, terms[z] + 2 * k, b + 2 * k, kind, z != kPlanes - 1 || k != 0);
+                    } else {
+                        bool add = false;
+#pragma unroll
+                        for (int z = kPlanes - 1; z >= 0; --z)
+                            for (int k = 0; k < steps; ++k) {
+                                const uint64_t a = tile_descriptor(v_at + (z * KB + (k >> 2)) * S::kV) + 2 * (k & 3);
+                                const uint64_t b = tile_descriptor(stage + (k >> 2) * S::kB) + 2 * (k & 3);
+                                tensor_step(d, a, b, kind, add);
+                                add = true;
+                            }
+                    }
                     tensor_commit(&empty[use % kBStages]);
                     tensor_commit(&done[buf]);
                 }
