@@ -13,11 +13,16 @@
 //     memory; B comes 32 columns at a time; the base comes through a ring of each warp's
 //     own, where the sums are added to it and from where they leave in whole rows.
 //
-// Operands are copied by cp.async, which zeroes what is past the edges and takes any
-// alignment of 16 bytes; a thread that has waited for its copies makes them visible to
-// the matrix steps by a proxy fence.  Waits on barriers give up after a second
-// (EP_ERR_TIMEOUT).
+// x, A and B come by TMA (tensor maps of x [M,K], A [L,R,K] and B [L,N,R], whose
+// edges read as zeros) with the 128-byte swizzle that the matrix steps take.  Copied by
+// cp.async instead, with a proxy fence by the threads that copied, both kernels waited
+// at that fence for the copies still in flight.  Waits on barriers give up after a
+// second (EP_ERR_TIMEOUT).
 #include <algorithm>
+#include <atomic>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "ep_device.cuh"
 #include "ep_internal.h"
@@ -104,8 +109,7 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, int n, volatile int *fai
 }
 
 // ---------------------------------------------------------------- shrink --
-constexpr int kFlushWarps = 4, kLoadThreads = 128;
-constexpr int kShrinkThreads = kFlushWarps * 32 + kLoadThreads + 32;
+constexpr int kFlushWarps = 4, kShrinkThreads = kFlushWarps * 32 + 64;
 constexpr int kChunk = 64;      // columns of x a stage
 constexpr int kGroup = 2;       // stages of a sum
 
@@ -118,7 +122,7 @@ struct Shrink {
 
 template <int RP, int SLOTS, int STAGES>
 __global__ void __launch_bounds__(kShrinkThreads, RP <= 64 ? 2 : 1)
-lora_shrink_many_kernel(Lora p)
+lora_shrink_many_kernel(Lora p, const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap a_map)
 {
     using S = Shrink<RP, SLOTS, STAGES>;
     constexpr int kLoad = RP < 32 ? RP : 32;   // columns of tensor memory a load
@@ -141,7 +145,7 @@ lora_shrink_many_kernel(Lora p)
     if (threadIdx.x == 0) {
         failed = 0;
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&full[i], kLoadThreads);
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -151,7 +155,7 @@ lora_shrink_many_kernel(Lora p)
         fence_mbar_init();
     }
     __syncwarp();
-    if (warp == kFlushWarps + kLoadThreads / 32)
+    if (warp == kFlushWarps + 1)
         tensor_alloc(&tensor, S::kColumns);
     tensor_fence_before();
     __syncthreads();
@@ -202,55 +206,26 @@ lora_shrink_many_kernel(Lora p)
                         *reinterpret_cast<float4 *>(to + r) = make_float4(acc[r], acc[r + 1], acc[r + 2], acc[r + 3]);
             }
         }
-    } else if (warp < kFlushWarps + kLoadThreads / 32) {
-        // this thread's pieces: of 16 bytes, at `piece` of rows r0, r0 + 16, ...
-        const int t = threadIdx.x - kFlushWarps * 32, r0 = t >> 3, piece = t & 7;
-        constexpr int kAhead = STAGES - 1;   // stages copied before the first is waited for
-        int arrived = 0;
-        auto arrive = [&]() {
-            fence_async_shared();
-            mbar_arrive(&full[arrived++ % STAGES]);
-        };
+    } else if (warp == kFlushWarps) {
         for (int now = adapter_after(ids, -1); now != kNoRow; now = pass.next) {
             pass.set(ids, now);
-            uint32_t here = 0;   // rows that the pass is for
+            if (lane == 0)
+                for (int c = c0; c < c1; ++c, ++used) {
+                    const int at = used % STAGES;
+                    if (used >= STAGES && !wait_alone(&empty[at], used / STAGES - 1, &failed))
+                        break;
+                    const uint32_t to = ring + at * S::kStage;
+                    mbar_arrive_expect_tx(&full[at], S::kX + pass.slots * RP * 128);
+                    tensor_copy(to, &x_map, c * kChunk, (int)first, 0, &full[at]);
 #pragma unroll
-            for (int i = 0; i < kRows / 16; ++i)
-                here |= (pass.has(ids[r0 + 16 * i]) ? 1u : 0u) << i;
-            const uint8_t *x_at = p.x + ((first + r0) * p.K + piece * 8) * 2;
-            const int64_t step = (int64_t)p.K * 2 * 16;   // from a piece to the next
-            for (int c = c0; c < c1; ++c, ++used) {
-                if (used >= STAGES && !wait_for(&empty[used % STAGES], used / STAGES - 1, &failed))
-                    break;
-                const uint32_t to = ring + (used % STAGES) * S::kStage;
-                const int64_t k = (int64_t)c * kChunk * 2;
-                const bool in = c * kChunk + piece * 8 < p.K;
-#pragma unroll
-                for (int i = 0; i < kRows / 16; ++i) {
-                    const bool ok = in && (here >> i & 1u);
-                    cp_async16(to + tile_offset(r0 + 16 * i, piece), ok ? x_at + i * step + k : p.x, ok);
+                    for (int i = 0; i < SLOTS; ++i)
+                        if (i < pass.slots)
+                            tensor_copy(to + S::kX + i * RP * 128, &a_map, c * kChunk, 0, pass.slot[i], &full[at]);
                 }
-#pragma unroll
-                for (int i = 0; i < SLOTS; ++i)
-                    if (i < pass.slots) {
-                        const uint8_t *a_at = p.a + (((int64_t)pass.slot[i] * p.R + r0) * p.K + piece * 8) * 2;
-#pragma unroll
-                        for (int j = 0; j < RP / 16; ++j) {
-                            const bool ok = in && r0 + 16 * j < p.R;
-                            cp_async16(to + S::kX + tile_offset(i * RP + r0 + 16 * j, piece), ok ? a_at + j * step + k : p.a, ok);
-                        }
-                    }
-                cp_async_commit();
-                cp_async_wait<kAhead>();
-                if (used >= kAhead)
-                    arrive();
-            }
+            __syncwarp();
             if (failed)
                 break;
         }
-        cp_async_wait<0>();
-        while (arrived < used)
-            arrive();
     } else {
         for (int now = adapter_after(ids, -1); now != kNoRow; now = pass.next) {
             pass.set(ids, now);
@@ -282,7 +257,7 @@ lora_shrink_many_kernel(Lora p)
     if (failed && threadIdx.x == 0)
         raise(p.err, EP_ERR_TIMEOUT);
     __syncwarp();
-    if (warp == kFlushWarps + kLoadThreads / 32)
+    if (warp == kFlushWarps + 1)
         tensor_free(tensor, S::kColumns);
 }
 
@@ -313,13 +288,13 @@ struct Expand {
 // matrix steps.
 template <int KB, int BASE, int OUT>
 __global__ void __launch_bounds__(kExpandThreads, (Expand<KB, BASE, OUT>::kPerSM))
-lora_expand_many_kernel(Lora p, int span)
+lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int span)
 {
     using S = Expand<KB, BASE, OUT>;
     extern __shared__ uint8_t dynamic[];
     __shared__ int ids[kRows];
     __shared__ float scales[kRows];
-    __shared__ uint64_t empty[kBStages], done[2], taken[2];
+    __shared__ uint64_t full[kBStages], empty[kBStages], done[2], taken[2];
     __shared__ uint32_t tensor;
     __shared__ int failed;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -338,8 +313,10 @@ lora_expand_many_kernel(Lora p, int span)
     }
     if (threadIdx.x == 0) {
         failed = 0;
-        for (int i = 0; i < kBStages; ++i)
+        for (int i = 0; i < kBStages; ++i) {
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
             mbar_init(&taken[i], kSumWarps / 2);
@@ -519,42 +496,29 @@ lora_expand_many_kernel(Lora p, int span)
         for (int now = begin; now != kNoRow; now = pass.next) {
             pass.set(ids, now);
             const uint32_t kind = step_kind(pass.slots * kColumns);
-            // this lane's pieces of a tile of B: of 16 bytes, at `piece` of 64 ranks of rows r0, r0 + 4, ...
-            const int piece = lane & 7, r0 = lane >> 3;
-            for (int c = 0; c < chunks + kBStages - 1; ++c) {
-                if (c < chunks) {
-                    const int use = used + c;
-                    if (use >= kBStages && !wait_for(&empty[use % kBStages], use / kBStages - 1, &failed))
+            // one thread: chunk c is copied, and the steps of the chunk before those in flight issued
+            if (lane == 0)
+                for (int c = 0; c < chunks + kBStages - 1; ++c) {
+                    if (c < chunks) {
+                        const int use = used + c, at = use % kBStages;
+                        if (use >= kBStages && !wait_alone(&empty[at], use / kBStages - 1, &failed))
+                            break;
+                        const uint32_t to = b_at + at * (KB * S::kB);
+                        mbar_arrive_expect_tx(&full[at], pass.slots * KB * kColumns * 128);
+#pragma unroll
+                        for (int i = 0; i < kExpandSlots; ++i)
+                            if (i < pass.slots)
+#pragma unroll
+                                for (int b = 0; b < KB; ++b)
+                                    tensor_copy(to + b * S::kB + i * kColumns * 128, &b_map, b * 64, n_from + c * kColumns,
+                                                pass.slot[i], &full[at]);
+                    }
+                    if (c < kBStages - 1)
+                        continue;
+                    const int use = used + c - (kBStages - 1), buf = use & 1;
+                    if ((use >= 2 && !wait_alone(&taken[buf], (use >> 1) - 1, &failed)) ||
+                        !wait_alone(&full[use % kBStages], use / kBStages, &failed))
                         break;
-                    const uint32_t to = b_at + use % kBStages * (KB * S::kB);
-                    const int n0 = n_from + c * kColumns;
-#pragma unroll
-                    for (int i = 0; i < kExpandSlots; ++i)
-                        if (i < pass.slots)
-#pragma unroll
-                            for (int b = 0; b < KB; ++b) {
-                                const int r = b * 64 + piece * 8;
-                                const uint8_t *from = p.b + (((int64_t)pass.slot[i] * p.N + n0 + r0) * p.R + r) * 2;
-                                if (r < steps * 16)
-#pragma unroll
-                                    for (int j = 0; j < kColumns / 4; ++j) {
-                                        const bool ok = r < p.R && n0 + r0 + 4 * j < p.N;
-                                        cp_async16(to + b * S::kB + tile_offset(i * kColumns + r0 + 4 * j, piece),
-                                                   ok ? from + j * 8 * p.R : p.b, ok);
-                                    }
-                            }
-                }
-                cp_async_commit();
-                cp_async_wait<kBStages - 1>();
-                fence_async_shared();
-                __syncwarp();
-                const int at = c - (kBStages - 1);
-                if (at < 0)
-                    continue;
-                const int use = used + at, buf = use & 1;
-                if (use >= 2 && !wait_for(&taken[buf], (use >> 1) - 1, &failed))
-                    break;
-                if (lane == 0) {
                     tensor_fence_after();
                     const uint32_t d = tensor + buf * kExpandSlots * kColumns, stage = b_at + use % kBStages * (KB * S::kB);
                     if constexpr (KB == 1) {
@@ -580,9 +544,6 @@ lora_expand_many_kernel(Lora p, int span)
                     tensor_commit(&empty[use % kBStages]);
                     tensor_commit(&done[buf]);
                 }
-                __syncwarp();
-            }
-            cp_async_wait<0>();
             __syncwarp();
             if (failed)
                 break;
@@ -598,16 +559,45 @@ lora_expand_many_kernel(Lora p, int span)
 }
 
 // ---------------------------------------------------------------- launch --
+// A tensor map of bf16 [z, y, x] read in boxes of 64 columns and `rows` rows.
+int make_map(CUtensorMap *map, const void *at, int64_t x, int64_t y, int64_t z, int rows)
+{
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = found.load(std::memory_order_relaxed);
+    if (encode == nullptr) {
+        void *entry = nullptr;
+        cudaDriverEntryPointQueryResult how;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &entry, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+            how != cudaDriverEntryPointSuccess || entry == nullptr) {
+            cudaGetLastError();
+            return EP_ERR_CUDA;
+        }
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(entry);
+        found.store(encode, std::memory_order_relaxed);
+    }
+    const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
+    const cuuint64_t strides[2] = {(cuuint64_t)x * 2, (cuuint64_t)(x * y) * 2};
+    const cuuint32_t box[3] = {kChunk, (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(at), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? EP_OK : EP_ERR_CUDA;
+}
+
 template <int RP, int SLOTS, int STAGES>
 int launch_shrink(const Lora &p, cudaStream_t stream)
 {
     using S = Shrink<RP, SLOTS, STAGES>;
     static PerDevice set;
-    const int rc = raise_smem(lora_shrink_many_kernel<RP, SLOTS, STAGES>, S::kBytes, set);
+    CUtensorMap x, a;
+    int rc = raise_smem(lora_shrink_many_kernel<RP, SLOTS, STAGES>, S::kBytes, set);
+    if (rc == EP_OK)
+        rc = make_map(&x, p.x, p.K, p.M, 1, kRows);
+    if (rc == EP_OK)
+        rc = make_map(&a, p.a, p.K, p.R, p.L, RP);
     if (rc != EP_OK)
         return rc;
     return launch_dependent(lora_shrink_many_kernel<RP, SLOTS, STAGES>, dim3((unsigned)ceil_div(p.M, kRows), p.splits),
-                            kShrinkThreads, S::kBytes, stream, p);
+                            kShrinkThreads, S::kBytes, stream, p, x, a);
 }
 
 template <int KB, int BASE, int OUT>
@@ -615,14 +605,17 @@ int launch_expand(const Lora &p, cudaStream_t stream)
 {
     using S = Expand<KB, BASE, OUT>;
     static PerDevice set;
-    const int rc = raise_smem(lora_expand_many_kernel<KB, BASE, OUT>, S::kBytes, set);
+    CUtensorMap b;
+    int rc = raise_smem(lora_expand_many_kernel<KB, BASE, OUT>, S::kBytes, set);
+    if (rc == EP_OK)
+        rc = make_map(&b, p.b, p.R, p.N, p.L, kColumns);
     if (rc != EP_OK)
         return rc;
     const int64_t tiles = ceil_div(p.M, kRows);
     const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(ceil_div(p.N, kColumns), kLoraBlocks / 2 * S::kPerSM / tiles));
     const int span = (int)(ceil_div(ceil_div(p.N, pieces), kColumns) * kColumns);
     return launch_dependent(lora_expand_many_kernel<KB, BASE, OUT>, dim3((unsigned)tiles, (unsigned)ceil_div(p.N, span)),
-                            kExpandThreads, S::kBytes, stream, p, span);
+                            kExpandThreads, S::kBytes, stream, p, b, span);
 }
 
 template <int KB>

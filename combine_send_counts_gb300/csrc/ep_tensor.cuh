@@ -7,6 +7,8 @@
 // further in the tile.
 #pragma once
 
+#include <cuda.h>
+
 #include "ep_device.cuh"
 
 namespace ep {
@@ -55,6 +57,15 @@ __device__ __forceinline__ void tensor_commit(uint64_t *bar)
 
 __device__ __forceinline__ void tensor_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tensor_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// A box of a tensor map from (x, y, z) on to a tile at shared-memory address `to`, completing its bytes on `bar`; one
+// thread.  x * 2 is a multiple of 16 bytes.
+__device__ __forceinline__ void tensor_copy(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+                 : "memory");
+}
 
 // Makes this thread's writes to shared memory visible to matrix steps (and bulk copies) that are ordered behind it.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
