@@ -260,8 +260,7 @@ lora_expand_few_kernel(Lora p)
     constexpr int kRanks = UNITS * WORDS * 8, kVRow = kRanks * 2 + 16;   // bytes of a row of v
     __shared__ __align__(16) uint8_t v_room[kPlanes][kTile][kVRow];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, m = blockIdx.x;
-    grid_dependency_wait();
-    allow_dependents();
+    // Every block of shrink has waited for what was before it, so that only what shrink itself writes is waited for here.
     const int adapter = adapter_of(p, m);
     const int n0 = (blockIdx.y * kWarps + warp) * 32, n = n0 + 8 * t;
     Ranks<UNITS, WORDS> b[4];
@@ -289,8 +288,10 @@ lora_expand_few_kernel(Lora p)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         d[j][0] = d[j][1] = d[j][2] = d[j][3] = none;
+    const float scaling = scaling_of(p, adapter);
+    grid_dependency_wait();
+    allow_dependents();
     if (adapter >= 0) {
-        const float scaling = scaling_of(p, adapter);
         for (int i = warp; i < kTile; i += kWarps) {   // a warp to a row
             const int row = __shfl_sync(kFull, mine, i);
             for (int r = 2 * lane; r < kRanks; r += 64) {

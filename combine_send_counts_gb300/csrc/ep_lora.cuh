@@ -64,15 +64,54 @@ __device__ __forceinline__ float2 ranks_of(const Lora &p, int64_t m, int r, floa
     return make_float2(__fmul_rn(v.x, scaling), __fmul_rn(v.y, scaling));
 }
 
-// Two values as sums of kPlanes bf16 terms each.
+// Four of them, r % 4 == 0.
+__device__ __forceinline__ float4 four_ranks_of(const Lora &p, int64_t m, int r, float scaling)
+{
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (m < 0 || r >= p.R)
+        return v;
+    const float4 *part = reinterpret_cast<const float4 *>(p.parts + m * p.R + r);
+    const int64_t next = p.M * p.R / 4;
+    for (int z = 0; z < p.splits; z += 4) {
+        float4 u[4];   // loaded together
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u[i] = z + i < p.splits ? part[(z + i) * next] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v.x = __fadd_rn(v.x, u[i].x);
+            v.y = __fadd_rn(v.y, u[i].y);
+            v.z = __fadd_rn(v.z, u[i].z);
+            v.w = __fadd_rn(v.w, u[i].w);
+        }
+    }
+    return make_float4(__fmul_rn(v.x, scaling), __fmul_rn(v.y, scaling), __fmul_rn(v.z, scaling), __fmul_rn(v.w, scaling));
+}
+
+// Two values as sums of kPlanes bf16 terms each: the first eight bits, the next and the last, by cutting, which is
+// exact.  What is left of an infinity or NaN is nothing.
 __device__ __forceinline__ void split(float2 v, uint32_t (&w)[kPlanes])
 {
+    uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
+    if ((a & 0x7f800000u) == 0x7f800000u || (b & 0x7f800000u) == 0x7f800000u) {
+        // a NaN keeps a bit that the first term holds
+        a |= isnan(v.x) ? 0x400000u : 0u;
+        b |= isnan(v.y) ? 0x400000u : 0u;
+        w[0] = a >> 16 | (b & 0xffff0000u);
+        v.x = isfinite(v.x) ? __fsub_rn(v.x, __uint_as_float(a & 0xffff0000u)) : 0.0f;
+        v.y = isfinite(v.y) ? __fsub_rn(v.y, __uint_as_float(b & 0xffff0000u)) : 0.0f;
+    } else {
+        w[0] = a >> 16 | (b & 0xffff0000u);
+        v.x = __fsub_rn(v.x, __uint_as_float(a & 0xffff0000u));
+        v.y = __fsub_rn(v.y, __uint_as_float(b & 0xffff0000u));
+    }
 #pragma unroll
-    for (int i = 0; i < kPlanes; ++i) {
-        w[i] = pack_bf16x2(v.x, v.y);
-        // what is left of an infinity or NaN is nothing
-        v.x = isfinite(v.x) ? __fsub_rn(v.x, bf16_lo(w[i])) : 0.0f;
-        v.y = isfinite(v.y) ? __fsub_rn(v.y, bf16_hi(w[i])) : 0.0f;
+    for (int i = 1; i < kPlanes; ++i) {
+        a = __float_as_uint(v.x);
+        b = __float_as_uint(v.y);
+        w[i] = a >> 16 | (b & 0xffff0000u);
+        v.x = __fsub_rn(v.x, __uint_as_float(a & 0xffff0000u));
+        v.y = __fsub_rn(v.y, __uint_as_float(b & 0xffff0000u));
     }
 }
 

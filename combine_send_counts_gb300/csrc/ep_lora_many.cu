@@ -10,14 +10,14 @@
 //     memory's sums are taken into registers after every 128 columns and added there
 //     with IEEE operations, as a long chain of matrix steps loses bits.
 //   expand: v is made once for a tile, as three bf16 terms, and stays in shared
-//     memory; B comes 32 columns at a time; the base comes through a ring of each warp's
+//     memory; B comes 64 or 128 columns at a time; the base comes through a ring of each warp's
 //     own, where the sums are added to it and from where they leave in whole rows.
 //
 // x, A and B come by TMA (tensor maps of x [M,K], A [L,R,K] and B [L,N,R], whose
 // edges read as zeros) with the 128-byte swizzle that the matrix steps take.  Copied by
 // cp.async instead, with a proxy fence by the threads that copied, both kernels waited
 // at that fence for the copies still in flight.  Waits on barriers give up after a
-// second (EP_ERR_TIMEOUT).
+// second or so (EP_ERR_TIMEOUT).
 #include <algorithm>
 #include <atomic>
 
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kRows = 128;           // of a tile
 constexpr int kNoRow = 0x7fffffff;   // the adapter of a row past the end
-constexpr uint64_t kLimitNs = 1000000000;
+constexpr int kTries = 1 << 16;      // of a wait, each of which may sleep for 20 us
 
 // The least adapter above `last` among a tile's rows, kNoRow if there is none.  The same in every lane.
 __device__ __forceinline__ int adapter_after(const int *ids, int last)
@@ -91,20 +91,31 @@ struct Pass {
     }
 };
 
-// One thread waits for the n-th use of a barrier that is completed once a use; false (once and for all) after a second.
+// One thread waits for the n-th use of a barrier that is completed once a use; false (once and for all) after kTries.
+// It sleeps while it waits: spinning warps take the issue slots of those that they wait for.
 __device__ __forceinline__ bool wait_alone(uint64_t *bar, int n, volatile int *failed)
 {
-    if (mbar_wait(bar, n & 1, kLimitNs))
-        return true;
+    for (int i = 0; i < kTries; ++i) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(smem_u32(bar)), "r"((uint32_t)n & 1u), "r"(20000u)
+                     : "memory");
+        if (ok != 0)
+            return true;
+    }
     *failed = 1;
     return false;
 }
 
-// A whole warp waits.  Lanes may leave the spin one by one, and the way out of a wait that failed leaves the caller's
-// loop, so that they would meet again only behind it: the vote brings them together for the .aligned instructions here.
+// A whole warp waits, by one lane.  The way out of a wait that failed leaves the caller's loop, so that lanes which got
+// through at different times would meet again only behind it: the vote brings them together for the .aligned
+// instructions here.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, int n, volatile int *failed)
 {
-    const bool ok = wait_alone(bar, n, failed);
+    const bool ok = (threadIdx.x & 31) != 0 || wait_alone(bar, n, failed);
     return __all_sync(kFull, ok);
 }
 
@@ -135,7 +146,6 @@ lora_shrink_many_kernel(Lora p, const __grid_constant__ CUtensorMap x_map, const
     const int64_t first = (int64_t)blockIdx.x * kRows;
     const uint32_t ring = (smem_u32(dynamic) + 1023u) & ~1023u;
     grid_dependency_wait();
-    allow_dependents();
     if (threadIdx.x < kRows) {
         const int64_t m = first + threadIdx.x;
         ids[threadIdx.x] = m < p.M ? adapter_of(p, m) : -1;
@@ -160,6 +170,7 @@ lora_shrink_many_kernel(Lora p, const __grid_constant__ CUtensorMap x_map, const
     tensor_fence_before();
     __syncthreads();
     tensor_fence_after();
+    allow_dependents();   // with its tensor memory in hand
     const int chunks = (p.K + kChunk - 1) / kChunk;
     const int c0 = (int)((int64_t)chunks * blockIdx.y / p.splits), c1 = (int)((int64_t)chunks * (blockIdx.y + 1) / p.splits);
     int used = 0, summed = 0;   // stages and sums so far
@@ -262,20 +273,24 @@ lora_shrink_many_kernel(Lora p, const __grid_constant__ CUtensorMap x_map, const
 }
 
 // ---------------------------------------------------------------- expand --
-constexpr int kSumWarps = 8, kExpandThreads = kSumWarps * 32 + 32;
-constexpr int kColumns = 32;        // of the output, a chunk
-constexpr int kExpandSlots = 2, kBStages = 3, kRowStages = 2;
+constexpr int kExpandSlots = 2, kBStages = 2, kRowStages = 2;
 
-// KB: runs of 64 ranks.  BASE, OUT: bytes of an element.
-template <int KB, int BASE, int OUT>
+// STEPS: of 16 ranks, 8 of them in two runs of 64.  BASE, OUT: bytes of an element.
+//
+// A step reads the 128 rows of v, which takes it some 70 cycles whatever its N: chunks are as wide as there is room
+// for.  (Of 32 columns, with two blocks to an SM, the steps alone took 1700 of the 1350 cycles that a pair of
+// chunks' bytes take.)
+template <int STEPS, int BASE, int OUT>
 struct Expand {
+    static constexpr int kRuns = STEPS > 4 ? 2 : 1;
+    static constexpr int kN = kRuns == 1 && BASE == 2 && OUT == 2 ? 128 : 64;  // columns of a chunk
+    static constexpr int kSumWarps = kN / 8, kThreads = kSumWarps * 32 + 32;   // 32 rows and 32 columns to a warp
     static constexpr int kV = kRows * 128;                                     // a term of v, 64 ranks
-    static constexpr int kB = kExpandSlots * kColumns * 128;                   // a stage of B, 64 ranks
-    static constexpr int kRowBytes = kColumns * (BASE > OUT ? BASE : OUT);
+    static constexpr int kB = kExpandSlots * kN * 128;                         // a stage of B, 64 ranks
+    static constexpr int kRowBytes = 32 * (BASE > OUT ? BASE : OUT);
     static constexpr int kRoom = 32 * kRowBytes;                               // a warp's stage
-    static constexpr int kBytes = kPlanes * KB * kV + kBStages * KB * kB + kSumWarps * kRowStages * kRoom + 1024;
-    static constexpr int kTensor = 2 * kExpandSlots * kColumns;                // columns of tensor memory
-    static constexpr int kPerSM = KB == 1 && kBytes <= 112 * 1024 ? 2 : 1;     // blocks
+    static constexpr int kBytes = kPlanes * kRuns * kV + kBStages * kRuns * kB + kSumWarps * kRowStages * kRoom + 1024;
+    static constexpr int kTensor = 2 * kExpandSlots * kN;                      // columns of tensor memory
 
     // a 16-byte piece of a row, so that eight rows' meet no bank twice
     __device__ __forceinline__ static uint32_t piece(int row, int i)
@@ -284,13 +299,14 @@ struct Expand {
     }
 };
 
-// Warps 0-3 take the even chunks, 4-7 the odd ones, each its own buffer of tensor memory; warp 8 copies B and issues the
+// Each of the warps but the last takes 32 rows and 32 columns of every chunk's sums; the last copies B and issues the
 // matrix steps.
-template <int KB, int BASE, int OUT>
-__global__ void __launch_bounds__(kExpandThreads, (Expand<KB, BASE, OUT>::kPerSM))
+template <int STEPS, int BASE, int OUT>
+__global__ void __launch_bounds__((Expand<STEPS, BASE, OUT>::kThreads))
 lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int span)
 {
-    using S = Expand<KB, BASE, OUT>;
+    using S = Expand<STEPS, BASE, OUT>;
+    constexpr int kRuns = S::kRuns, kN = S::kN, kSumWarps = S::kSumWarps;
     extern __shared__ uint8_t dynamic[];
     __shared__ int ids[kRows];
     __shared__ float scales[kRows];
@@ -299,13 +315,11 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
     __shared__ int failed;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t first = (int64_t)blockIdx.x * kRows;
-    const uint32_t v_at = (smem_u32(dynamic) + 1023u) & ~1023u, b_at = v_at + kPlanes * KB * S::kV;
-    const uint32_t rows_at = b_at + kBStages * KB * S::kB;
+    const uint32_t v_at = (smem_u32(dynamic) + 1023u) & ~1023u, b_at = v_at + kPlanes * kRuns * S::kV;
+    const uint32_t rows_at = b_at + kBStages * kRuns * S::kB;
     const int n_from = blockIdx.y * span, n_to = min(n_from + span, p.N);
-    const int chunks = (n_to - n_from + kColumns - 1) / kColumns;
-    const int steps = (p.R + 15) / 16;   // of 16 ranks
-    grid_dependency_wait();
-    allow_dependents();
+    const int chunks = (n_to - n_from + kN - 1) / kN;
+    // Every block of shrink has waited for what was before it, so that only what shrink itself writes is waited for here.
     if (threadIdx.x < kRows) {
         const int id = first + threadIdx.x < p.M ? adapter_of(p, first + threadIdx.x) : kNoRow;
         ids[threadIdx.x] = id;
@@ -319,38 +333,42 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
-            mbar_init(&taken[i], kSumWarps / 2);
+            mbar_init(&taken[i], kSumWarps);
         }
         fence_mbar_init();
     }
-    __syncwarp();
+    __syncthreads();
+    grid_dependency_wait();
+    // not before: a block that held tensor memory while it waits for shrink could keep it from shrink
     if (warp == kSumWarps)
         tensor_alloc(&tensor, S::kTensor);
-    __syncthreads();
-    if (warp < kSumWarps) {   // v of every row: a thread has a pair of ranks of several rows, kBatch of them at a time
-        constexpr int kBatch = 4;
-        const int log_pairs = p.R <= 16 ? 3 : p.R <= 32 ? 4 : p.R <= 64 ? 5 : 6;
-        const int r = (threadIdx.x & ((1 << log_pairs) - 1)) * 2, apart = kSumWarps * 32 >> log_pairs;
-        for (int row = threadIdx.x >> log_pairs; row < kRows; row += kBatch * apart) {
-            float2 f[kBatch];
+    allow_dependents();
+    {   // v of every row: a thread has four ranks of several rows
+        constexpr int kFours = STEPS * 4, kThreads = kSumWarps * 32, kApart = kThreads / kFours;
+        constexpr int kEach = kRows / kApart, kBatch = kEach < 4 ? kEach : 4;
+        const int r = threadIdx.x % kFours * 4, row0 = threadIdx.x / kFours;
+        if (warp < kSumWarps)
+#pragma unroll 1
+            for (int i = 0; i < kEach; i += kBatch) {
+                float4 f[kBatch];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int at = row + j * apart, id = at < kRows ? ids[at] : -1;
-                f[j] = ranks_of(p, id >= 0 && id != kNoRow ? first + at : -1, r, id >= 0 ? scales[at] : 1.0f);
+                for (int j = 0; j < kBatch; ++j) {
+                    const int row = row0 + (i + j) * kApart, id = ids[row];
+                    f[j] = four_ranks_of(p, id >= 0 && id != kNoRow ? first + row : -1, r, scales[row]);
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int row = row0 + (i + j) * kApart;
+                    uint32_t lo[kPlanes], hi[kPlanes];
+                    split(make_float2(f[j].x, f[j].y), lo);
+                    split(make_float2(f[j].z, f[j].w), hi);
+                    const uint32_t to = v_at + (r >> 6) * S::kV + tile_offset(row, (r & 63) >> 3) + (r & 7) * 2;
+#pragma unroll
+                    for (int z = 0; z < kPlanes; ++z)
+                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(to + z * kRuns * S::kV), "r"(lo[z]), "r"(hi[z])
+                                     : "memory");
+                }
             }
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int at = row + j * apart;
-                if (at >= kRows || r >= steps * 16)
-                    break;
-                uint32_t terms[kPlanes];
-                split(f[j], terms);
-                const uint32_t to = v_at + (r >> 6) * S::kV + tile_offset(at, (r & 63) >> 3) + (r & 7) * 2;
-#pragma unroll
-                for (int z = 0; z < kPlanes; ++z)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + z * KB * S::kV), "r"(terms[z]) : "memory");
-            }
-        }
     }
     fence_async_shared();
     tensor_fence_before();
@@ -360,18 +378,17 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
     const int begin = adapter_after(ids, -1);
     if (warp < kSumWarps) {
         // a row to a thread for the sums; whole rows by neighbouring lanes for the base and the result
-        constexpr int kBasePieces = kColumns * BASE / 16, kOutPieces = kColumns * OUT / 16;
-        const int group = warp >> 2, mine0 = (warp & 3) * 32, id = ids[mine0 + lane];
+        constexpr int kBasePieces = 32 * BASE / 16, kOutPieces = 32 * OUT / 16;
+        const int column0 = (warp >> 2) * 32, mine0 = (warp & 3) * 32, id = ids[mine0 + lane];
         const uint32_t room = rows_at + warp * kRowStages * S::kRoom;
-        const uint32_t sums = tensor + ((uint32_t)mine0 << 16) + group * kExpandSlots * kColumns;
+        const uint32_t sums = tensor + ((uint32_t)mine0 << 16);
         // this lane's pieces: of rows lane / pieces, and so many further
         const int base_row = lane / kBasePieces, base_piece = lane % kBasePieces;
         const int out_row = lane / kOutPieces, out_piece = lane % kOutPieces;
         const uint8_t *const base_at = static_cast<const uint8_t *>(p.base) + (first + mine0 + base_row) * p.N * BASE + base_piece * 16;
         uint8_t *const out_at = static_cast<uint8_t *>(p.out) + (first + mine0 + out_row) * p.N * OUT + out_piece * 16;
         const int64_t base_apart = (int64_t)(32 / kBasePieces) * p.N * BASE, out_apart = (int64_t)(32 / kOutPieces) * p.N * OUT;
-        int used = 0;       // sums of this group so far
-        int before = 0;     // chunks of the passes so far
+        int used = 0;   // sums so far
         bool start = true;
         for (int now = begin; start || now != kNoRow; now = pass.next) {
             pass.set(ids, now);
@@ -379,13 +396,9 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
             const bool row_in = pass.has(id) || (start && id == -1);
             const uint32_t rows = __ballot_sync(kFull, row_in), mine = pass.mask(id);
             start = false;
-            // the group of a chunk goes on counting through the passes, as the buffers do
-            const int c0 = (before & 1) == group ? 0 : 1;
-            if (pass.slots > 0)
-                before += chunks;
             auto fetch = [&](int c, int stage) {
                 if (p.base != nullptr && c < chunks) {
-                    const int n0 = n_from + c * kColumns;
+                    const int n0 = n_from + c * kN + column0;
                     const bool in = n0 + base_piece * (16 / BASE) < p.N;
 #pragma unroll
                     for (int i = 0; i < kBasePieces; ++i) {
@@ -397,40 +410,43 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
                 }
                 cp_async_commit();
             };
-            fetch(c0, 0);
+            fetch(0, 0);
             int stage = 0;
-            for (int c = c0; c < chunks; c += 2, stage ^= 1) {
-                fetch(c + 2, stage ^ 1);
-                const int n0 = n_from + c * kColumns;
-                float d[kColumns];
+            for (int c = 0; c < chunks; ++c, stage ^= 1) {
+                fetch(c + 1, stage ^ 1);
+                const int n0 = n_from + c * kN + column0;
+                float d[32];
 #pragma unroll
-                for (int i = 0; i < kColumns; ++i)
+                for (int i = 0; i < 32; ++i)
                     d[i] = -0.0f;   // base + -0 is base
                 if (pass.slots > 0) {
-                    if (!wait_for(&done[group], used++, &failed))
+                    const int buf = used & 1;
+                    if (!wait_for(&done[buf], used >> 1, &failed))
                         break;
+                    ++used;
                     tensor_fence_after();
+                    const uint32_t from = sums + buf * kExpandSlots * kN + column0;
                     if (mine != 0 && (mine & (mine - 1u)) == 0) {   // rows of one adapter, or of none here
-                        tensor_load<kColumns>(d, sums + (__ffs(mine) - 1) * kColumns);
+                        tensor_load<32>(d, from + (__ffs(mine) - 1) * kN);
                         if (id == -1)
 #pragma unroll
-                            for (int i = 0; i < kColumns; ++i)
+                            for (int i = 0; i < 32; ++i)
                                 d[i] = -0.0f;
                     } else {
                         for (uint32_t todo = mine; todo != 0; todo &= todo - 1u) {
                             const int slot = __ffs(todo) - 1;
-                            float f[kColumns];
-                            tensor_load<kColumns>(f, sums + slot * kColumns);
+                            float f[32];
+                            tensor_load<32>(f, from + slot * kN);
                             if (id == pass.id_of(slot))
 #pragma unroll
-                                for (int i = 0; i < kColumns; ++i)
+                                for (int i = 0; i < 32; ++i)
                                     d[i] = f[i];
                         }
                     }
                     tensor_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(&taken[group]);
+                        mbar_arrive(&taken[buf]);
                 }
                 cp_async_wait<1>();
                 __syncwarp();
@@ -443,9 +459,9 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (BASE == 4) {
-                                d[(i * 4 + j) % kColumns] = __fadd_rn(__uint_as_float(w[j]), d[(i * 4 + j) % kColumns]);
+                                d[(i * 4 + j) % 32] = __fadd_rn(__uint_as_float(w[j]), d[(i * 4 + j) % 32]);
                             } else {
-                                const int k = (i * 8 + j * 2) % kColumns;
+                                const int k = (i * 8 + j * 2) % 32;
                                 d[k] = __fadd_rn(bf16_lo(w[j]), d[k]);
                                 d[k + 1] = __fadd_rn(bf16_hi(w[j]), d[k + 1]);
                             }
@@ -453,20 +469,20 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kColumns; ++i)
+                    for (int i = 0; i < 32; ++i)
                         d[i] = __fadd_rn(0.0f, d[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < kOutPieces; ++i) {
                     uint4 v;
                     if (OUT == 2)
-                        v = make_uint4(pack_bf16x2(d[i * 8 % kColumns], d[(i * 8 + 1) % kColumns]),
-                                       pack_bf16x2(d[(i * 8 + 2) % kColumns], d[(i * 8 + 3) % kColumns]),
-                                       pack_bf16x2(d[(i * 8 + 4) % kColumns], d[(i * 8 + 5) % kColumns]),
-                                       pack_bf16x2(d[(i * 8 + 6) % kColumns], d[(i * 8 + 7) % kColumns]));
+                        v = make_uint4(pack_bf16x2(d[i * 8 % 32], d[(i * 8 + 1) % 32]),
+                                       pack_bf16x2(d[(i * 8 + 2) % 32], d[(i * 8 + 3) % 32]),
+                                       pack_bf16x2(d[(i * 8 + 4) % 32], d[(i * 8 + 5) % 32]),
+                                       pack_bf16x2(d[(i * 8 + 6) % 32], d[(i * 8 + 7) % 32]));
                     else
-                        v = make_uint4(__float_as_uint(d[i * 4 % kColumns]), __float_as_uint(d[(i * 4 + 1) % kColumns]),
-                                       __float_as_uint(d[(i * 4 + 2) % kColumns]), __float_as_uint(d[(i * 4 + 3) % kColumns]));
+                        v = make_uint4(__float_as_uint(d[i * 4 % 32]), __float_as_uint(d[(i * 4 + 1) % 32]),
+                                       __float_as_uint(d[(i * 4 + 2) % 32]), __float_as_uint(d[(i * 4 + 3) % 32]));
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + S::piece(lane, i)), "r"(v.x), "r"(v.y),
                                  "r"(v.z), "r"(v.w)
                                  : "memory");
@@ -492,62 +508,55 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
         uint64_t terms[kPlanes];
 #pragma unroll
         for (int z = 0; z < kPlanes; ++z)
-            terms[z] = tile_descriptor(v_at + z * KB * S::kV);
+            terms[z] = tile_descriptor(v_at + z * kRuns * S::kV);
         for (int now = begin; now != kNoRow; now = pass.next) {
             pass.set(ids, now);
-            const uint32_t kind = step_kind(pass.slots * kColumns);
-            // one thread: chunk c is copied, and the steps of the chunk before those in flight issued
-            if (lane == 0)
-                for (int c = 0; c < chunks + kBStages - 1; ++c) {
-                    if (c < chunks) {
-                        const int use = used + c, at = use % kBStages;
-                        if (use >= kBStages && !wait_alone(&empty[at], use / kBStages - 1, &failed))
-                            break;
-                        const uint32_t to = b_at + at * (KB * S::kB);
-                        mbar_arrive_expect_tx(&full[at], pass.slots * KB * kColumns * 128);
+            const uint32_t kind = step_kind(pass.slots * kN);
+            // one thread: the steps of chunk c are issued before the next copy waits for those of the chunk before it,
+            // so that the matrix pipe always has some ahead
+            if (lane == 0) {
+                auto copy = [&](int c) {
+                    const int use = used + c, at = use % kBStages;
+                    if (use >= kBStages && !wait_alone(&empty[at], use / kBStages - 1, &failed))
+                        return false;
+                    const uint32_t to = b_at + at * (kRuns * S::kB);
+                    mbar_arrive_expect_tx(&full[at], pass.slots * kRuns * kN * 128);
 #pragma unroll
-                        for (int i = 0; i < kExpandSlots; ++i)
-                            if (i < pass.slots)
+                    for (int i = 0; i < kExpandSlots; ++i)
+                        if (i < pass.slots)
 #pragma unroll
-                                for (int b = 0; b < KB; ++b)
-                                    tensor_copy(to + b * S::kB + i * kColumns * 128, &b_map, b * 64, n_from + c * kColumns,
-                                                pass.slot[i], &full[at]);
-                    }
-                    if (c < kBStages - 1)
-                        continue;
-                    const int use = used + c - (kBStages - 1), buf = use & 1;
-                    if ((use >= 2 && !wait_alone(&taken[buf], (use >> 1) - 1, &failed)) ||
+                            for (int b = 0; b < kRuns; ++b)
+                                tensor_copy(to + b * S::kB + i * kN * 128, &b_map, b * 64, n_from + c * kN,
+                                            pass.slot[i], &full[at]);
+                    return true;
+                };
+                for (int c = 0; c < min(chunks, kBStages - 1); ++c)
+                    if (!copy(c))
+                        break;
+                for (int c = 0; c < chunks; ++c) {
+                    const int use = used + c, buf = use & 1;
+                    if (failed || (use >= 2 && !wait_alone(&taken[buf], (use >> 1) - 1, &failed)) ||
                         !wait_alone(&full[use % kBStages], use / kBStages, &failed))
                         break;
                     tensor_fence_after();
-                    const uint32_t d = tensor + buf * kExpandSlots * kColumns, stage = b_at + use % kBStages * (KB * S::kB);
-                    if constexpr (KB == 1) {
-                        // few instructions to a step: one thread issues them all
-                        const uint64_t b = tile_descriptor(stage);
+                    const uint32_t d = tensor + buf * kExpandSlots * kN, stage = b_at + use % kBStages * (kRuns * S::kB);
+                    const uint64_t b = tile_descriptor(stage);
 #pragma unroll
-                        for (int z = kPlanes - 1; z >= 0; --z)
+                    for (int z = kPlanes - 1; z >= 0; --z)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (k < steps)
-                                    tensor_step(d, terms[z] + 2 * k, b + 2 * k, kind, z != kPlanes - 1 || k != 0);
-                    } else {
-                        bool add = false;
-#pragma unroll
-                        for (int z = kPlanes - 1; z >= 0; --z)
-                            for (int k = 0; k < steps; ++k) {
-                                const uint64_t a = tile_descriptor(v_at + (z * KB + (k >> 2)) * S::kV) + 2 * (k & 3);
-                                const uint64_t b = tile_descriptor(stage + (k >> 2) * S::kB) + 2 * (k & 3);
-                                tensor_step(d, a, b, kind, add);
-                                add = true;
-                            }
-                    }
+                        for (int k = 0; k < STEPS; ++k)
+                            tensor_step(d, terms[z] + ((k >> 2) * S::kV >> 4) + 2 * (k & 3),
+                                        b + ((k >> 2) * S::kB >> 4) + 2 * (k & 3), kind, z != kPlanes - 1 || k != 0);
                     tensor_commit(&empty[use % kBStages]);
                     tensor_commit(&done[buf]);
+                    if (c + kBStages - 1 < chunks && !copy(c + kBStages - 1))
+                        break;
                 }
+                used += chunks;
+            }
             __syncwarp();
             if (failed)
                 break;
-            used += chunks;
         }
     }
     __syncthreads();
@@ -600,30 +609,31 @@ int launch_shrink(const Lora &p, cudaStream_t stream)
                             kShrinkThreads, S::kBytes, stream, p, x, a);
 }
 
-template <int KB, int BASE, int OUT>
+template <int STEPS, int BASE, int OUT>
 int launch_expand(const Lora &p, cudaStream_t stream)
 {
-    using S = Expand<KB, BASE, OUT>;
+    using S = Expand<STEPS, BASE, OUT>;
     static PerDevice set;
     CUtensorMap b;
-    int rc = raise_smem(lora_expand_many_kernel<KB, BASE, OUT>, S::kBytes, set);
+    int rc = raise_smem(lora_expand_many_kernel<STEPS, BASE, OUT>, S::kBytes, set);
     if (rc == EP_OK)
-        rc = make_map(&b, p.b, p.R, p.N, p.L, kColumns);
+        rc = make_map(&b, p.b, p.R, p.N, p.L, S::kN);
     if (rc != EP_OK)
         return rc;
+    // a block to an SM, with as few columns as that leaves
     const int64_t tiles = ceil_div(p.M, kRows);
-    const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(ceil_div(p.N, kColumns), kLoraBlocks / 2 * S::kPerSM / tiles));
-    const int span = (int)(ceil_div(ceil_div(p.N, pieces), kColumns) * kColumns);
-    return launch_dependent(lora_expand_many_kernel<KB, BASE, OUT>, dim3((unsigned)tiles, (unsigned)ceil_div(p.N, span)),
-                            kExpandThreads, S::kBytes, stream, p, b, span);
+    const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(ceil_div(p.N, S::kN), kLoraBlocks / 2 / tiles));
+    const int span = (int)(ceil_div(ceil_div(p.N, pieces), S::kN) * S::kN);
+    return launch_dependent(lora_expand_many_kernel<STEPS, BASE, OUT>, dim3((unsigned)tiles, (unsigned)ceil_div(p.N, span)),
+                            S::kThreads, S::kBytes, stream, p, b, span);
 }
 
-template <int KB>
+template <int STEPS>
 int launch_expand(const Lora &p, cudaStream_t stream)
 {
     if (p.base != nullptr && p.base_dtype != 0)
-        return p.out_dtype == 0 ? launch_expand<KB, 4, 2>(p, stream) : launch_expand<KB, 4, 4>(p, stream);
-    return p.out_dtype == 0 ? launch_expand<KB, 2, 2>(p, stream) : launch_expand<KB, 2, 4>(p, stream);
+        return p.out_dtype == 0 ? launch_expand<STEPS, 4, 2>(p, stream) : launch_expand<STEPS, 4, 4>(p, stream);
+    return p.out_dtype == 0 ? launch_expand<STEPS, 2, 2>(p, stream) : launch_expand<STEPS, 2, 4>(p, stream);
 }
 
 }  // namespace
@@ -634,7 +644,11 @@ int launch_lora_many(const Lora &p, cudaStream_t stream)
                    : p.R <= 64 ? launch_shrink<64, 2, 3>(p, stream) : launch_shrink<128, 2, 3>(p, stream);
     if (rc != EP_OK)
         return rc;
-    return p.R <= 64 ? launch_expand<1>(p, stream) : launch_expand<2>(p, stream);
+    if (p.R <= 16)
+        return launch_expand<1>(p, stream);
+    if (p.R <= 32)
+        return launch_expand<2>(p, stream);
+    return p.R <= 64 ? launch_expand<4>(p, stream) : launch_expand<8>(p, stream);
 }
 
 }  // namespace ep

@@ -40,7 +40,9 @@ __device__ __forceinline__ void tensor_free(uint32_t at, int columns)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
 }
 
-// D (+)= A B^T, one step of 16 of K; one thread.
+// D (+)= A B^T, one step of 16 of K; one thread, in a warp that is otherwise of one mind: what the operands are made of
+// has to be uniform for the compiler too, as they go by uniform registers (in code that one lane ran alone, a step took
+// 80 cycles to issue, done or skipped).
 __device__ __forceinline__ void tensor_step(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
