@@ -273,7 +273,7 @@ lora_shrink_many_kernel(Lora p, const __grid_constant__ CUtensorMap x_map, const
 }
 
 // ---------------------------------------------------------------- expand --
-constexpr int kExpandSlots = 2, kBStages = 2, kRowStages = 2;
+constexpr int kExpandSlots = 2, kBStages = 2;
 
 // STEPS: of 16 ranks, 8 of them in two runs of 64.  BASE, OUT: bytes of an element.
 //
@@ -289,7 +289,9 @@ struct Expand {
     static constexpr int kB = kExpandSlots * kN * 128;                         // a stage of B, 64 ranks
     static constexpr int kRowBytes = 32 * (BASE > OUT ? BASE : OUT);
     static constexpr int kRoom = 32 * kRowBytes;                               // a warp's stage
-    static constexpr int kBytes = kPlanes * kRuns * kV + kBStages * kRuns * kB + kSumWarps * kRowStages * kRoom + 1024;
+    static constexpr int kFixed = kPlanes * kRuns * kV + kBStages * kRuns * kB + 1024;
+    static constexpr int kRowStages = kFixed + 3 * kSumWarps * kRoom <= 225 * 1024 ? 3 : 2;
+    static constexpr int kBytes = kFixed + kRowStages * kSumWarps * kRoom;
     static constexpr int kTensor = 2 * kExpandSlots * kN;                      // columns of tensor memory
 
     // a 16-byte piece of a row, so that eight rows' meet no bank twice
@@ -380,7 +382,7 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
         // a row to a thread for the sums; whole rows by neighbouring lanes for the base and the result
         constexpr int kBasePieces = 32 * BASE / 16, kOutPieces = 32 * OUT / 16;
         const int column0 = (warp >> 2) * 32, mine0 = (warp & 3) * 32, id = ids[mine0 + lane];
-        const uint32_t room = rows_at + warp * kRowStages * S::kRoom;
+        const uint32_t room = rows_at + warp * S::kRowStages * S::kRoom;
         const uint32_t sums = tensor + ((uint32_t)mine0 << 16);
         // this lane's pieces: of rows lane / pieces, and so many further
         const int base_row = lane / kBasePieces, base_piece = lane % kBasePieces;
@@ -410,10 +412,12 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
                 }
                 cp_async_commit();
             };
-            fetch(0, 0);
+#pragma unroll
+            for (int i = 0; i < S::kRowStages - 1; ++i)
+                fetch(i, i);
             int stage = 0;
-            for (int c = 0; c < chunks; ++c, stage ^= 1) {
-                fetch(c + 1, stage ^ 1);
+            for (int c = 0; c < chunks; ++c, stage = stage + 1 == S::kRowStages ? 0 : stage + 1) {
+                fetch(c + S::kRowStages - 1, stage == 0 ? S::kRowStages - 1 : stage - 1);
                 const int n0 = n_from + c * kN + column0;
                 float d[32];
 #pragma unroll
@@ -448,7 +452,7 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, int s
                     if (lane == 0)
                         mbar_arrive(&taken[buf]);
                 }
-                cp_async_wait<1>();
+                cp_async_wait<S::kRowStages - 1>();
                 __syncwarp();
                 const uint32_t at = room + stage * S::kRoom;
                 if (p.base != nullptr) {
