@@ -42,6 +42,7 @@ The lower-case helpers after them allocate outputs with torch and call the
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -1337,6 +1338,7 @@ def moe_decode(x, topk_idx, topk_weights, w13, w2, *, num_experts: Optional[int]
 
 
 # ------------------------------------------------------- around the routing --
+_BF16 = torch.bfloat16
 _SCORINGS = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
 _FLOATS = {torch.float32: 0, torch.bfloat16: 1}   # of logits
 _SCALE_FMTS = (EP_SCALE_ROW_F32, EP_SCALE_COL_F32, EP_SCALE_COL_UE8M0)
@@ -1349,12 +1351,18 @@ def _matrix(where: str, name: str, t: torch.Tensor) -> tuple:
     return t.shape
 
 
-def _norm_weight(where: str, w: Optional[torch.Tensor], H: int, index: int):
-    if w is None:
-        return None, 0
-    if w.dtype not in _OUT_DTYPES:
-        raise TypeError(f"{where}: weight must be torch.bfloat16 or torch.float32, got {w.dtype}")
-    return _ready(where, "weight", w, w.dtype, (H,), index), _OUT_DTYPES[w.dtype]
+def _good(t: torch.Tensor, dtype, shape, index: int) -> bool:
+    """What _ready checks, for calls whose time is the host's."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and t.is_contiguous()
+
+
+def _norm_weight(where: str, w: torch.Tensor, H: int, index: int):
+    dt = w.dtype
+    if dt not in _OUT_DTYPES:
+        raise TypeError(f"{where}: weight must be torch.bfloat16 or torch.float32, got {dt}")
+    if not _good(w, dt, (H,), index):
+        _ready(where, "weight", w, dt, (H,), index)
+    return w.data_ptr(), _OUT_DTYPES[dt]
 
 
 def _apart(where: str, name: str, t: torch.Tensor, **others):
@@ -1381,39 +1389,54 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Opti
     [H/512,T] int32); round_scale: scales that are powers of two.  inplace: h
     is written over residual."""
     where = "add_rms_norm"
-    T, H = _matrix(where, "x", x)
-    index, dev = x.get_device(), x.device
-    xp = _ready(where, "x", x, torch.bfloat16, (T, H), index)
-    wp, wd = _norm_weight(where, weight, H, index)
+    shape, index = x.shape, x.get_device()
+    if len(shape) != 2 or not _good(x, _BF16, shape, index):
+        _ready(where, "x", x, _BF16, _matrix(where, "x", x))
+    T, H = shape
+    dev, lib = x.device, load()
+    wp, wd = (None, 0) if weight is None else _norm_weight(where, weight, H, index)
     rp, rd, h, hp = None, 0, None, None
     if residual is not None:
-        if residual.dtype not in _OUT_DTYPES:
-            raise TypeError(f"{where}: residual must be torch.bfloat16 or torch.float32, got {residual.dtype}")
-        rd = _OUT_DTYPES[residual.dtype]
-        rp = _ready(where, "residual", residual, residual.dtype, (T, H), index)
+        rt = residual.dtype
+        if rt not in _OUT_DTYPES:
+            raise TypeError(f"{where}: residual must be torch.bfloat16 or torch.float32, got {rt}")
+        if not _good(residual, rt, shape, index):
+            _ready(where, "residual", residual, rt, shape, index)
+        rd, rp = _OUT_DTYPES[rt], residual.data_ptr()
         if inplace:
             _apart(where, "residual", residual, x=x, weight=weight)
-        h = residual if inplace else _empty((T, H), residual.dtype, dev, stream)
+            h = residual
+        else:
+            h = _empty(shape, rt, dev, stream) if stream is not None else torch.empty(shape, dtype=rt, device=dev)
         hp = h.data_ptr()
     elif inplace:
         raise ValueError(f"{where}: inplace needs a residual")
     if not y and not fp8 and residual is None:
         raise ValueError(f"{where}: nothing is asked for")
-    out = _empty((T, H), torch.bfloat16, dev, stream) if y else None
-    q = scale = None
+    out = q = scale = yp = qp = sp = None
+    if y:
+        out = _empty(shape, _BF16, dev, stream) if stream is not None else torch.empty(shape, dtype=_BF16, device=dev)
+        yp = out.data_ptr()
     if fp8:
         if scale_fmt not in _SCALE_FMTS:
             raise ValueError(f"{where}: scale_fmt must be one of EP_SCALE_*, got {scale_fmt!r}")
-        q = _empty((T, H), torch.uint8, dev, stream)
-        scale = (_empty((T, H // 128), torch.float32, dev, stream) if scale_fmt == EP_SCALE_ROW_F32 else
-                 _empty((H // 128, T), torch.float32, dev, stream) if scale_fmt == EP_SCALE_COL_F32 else
-                 _empty((H // 512, T), torch.int32, dev, stream))
-    rc = _call(index, load().ep_add_rms_norm, xp, rp, rd, T, H, wp, wd, eps, hp, None if out is None else out.data_ptr(),
-               None if q is None else q.data_ptr(), None if scale is None else scale.data_ptr(), scale_fmt,
-               int(round_scale), _raw_stream(stream, index))
+        of = (T, H // 128) if scale_fmt == EP_SCALE_ROW_F32 else (H // 128, T) if scale_fmt == EP_SCALE_COL_F32 else (H // 512, T)
+        kind = torch.int32 if scale_fmt == EP_SCALE_COL_UE8M0 else torch.float32
+        if stream is None:
+            q, scale = torch.empty(shape, dtype=torch.uint8, device=dev), torch.empty(of, dtype=kind, device=dev)
+        else:
+            q, scale = _empty(shape, torch.uint8, dev, stream), _empty(of, kind, dev, stream)
+        qp, sp = q.data_ptr(), scale.data_ptr()
+    rc = _call(index, lib.ep_add_rms_norm, x.data_ptr(), rp, rd, T, H, wp, wd, eps, hp, yp, qp, sp, scale_fmt,
+               1 if round_scale else 0, _raw_stream(stream, index))
     if rc:
         _check(rc, where)
-    return dict(y=out, residual=h, q=q, scale=scale)
+    return {"y": out, "residual": h, "q": q, "scale": scale}
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(T: int, H: int) -> int:
+    return ep_rms_norm_backward_workspace_size(T, H)
 
 
 def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor],
@@ -1426,29 +1449,42 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[to
     -> dict(dresidual [T,H] in h's type, dx [T,H] bf16 (the same tensor where h is
     bf16), dweight [H] fp32 or None)."""
     where = "add_rms_norm_backward"
-    T, H = _matrix(where, "dy", dy)
-    index, dev = dy.get_device(), dy.device
-    gp = _ready(where, "dy", dy, torch.bfloat16, (T, H), index)
-    if h.dtype not in _OUT_DTYPES:
-        raise TypeError(f"{where}: h must be torch.bfloat16 or torch.float32, got {h.dtype}")
-    rd = _OUT_DTYPES[h.dtype]
-    hp = _ready(where, "h", h, h.dtype, (T, H), index)
-    rp = None if dresidual is None else _ready(where, "dresidual", dresidual, h.dtype, (T, H), index)
-    wp, wd = _norm_weight(where, weight, H, index)
-    dh = _empty((T, H), h.dtype, dev, stream)
-    dx = dh if rd == 0 else _empty((T, H), torch.bfloat16, dev, stream)
-    dw = ws = None
+    shape, index = dy.shape, dy.get_device()
+    if len(shape) != 2 or not _good(dy, _BF16, shape, index):
+        _ready(where, "dy", dy, _BF16, _matrix(where, "dy", dy))
+    T, H = shape
+    dev, lib, ht = dy.device, load(), h.dtype
+    if ht not in _OUT_DTYPES:
+        raise TypeError(f"{where}: h must be torch.bfloat16 or torch.float32, got {ht}")
+    rd = _OUT_DTYPES[ht]
+    if not _good(h, ht, shape, index):
+        _ready(where, "h", h, ht, shape, index)
+    if dresidual is not None and not _good(dresidual, ht, shape, index):
+        _ready(where, "dresidual", dresidual, ht, shape, index)
+    wp, wd = (None, 0) if weight is None else _norm_weight(where, weight, H, index)
+    dx = dw = wsp = None
     n = 0
     if dweight:
-        dw = _empty((H,), torch.float32, dev, stream)
-        n = ep_rms_norm_backward_workspace_size(T, H)
-        ws = _empty((n,), torch.uint8, dev, stream)
-    rc = _call(index, load().ep_add_rms_norm_backward, gp, hp, rp, rd, T, H, wp, wd, eps, dh.data_ptr(),
-               None if rd == 0 else dx.data_ptr(), None if dw is None else dw.data_ptr(),
-               None if ws is None else ws.data_ptr(), n, _raw_stream(stream, index))
+        n = _norm_workspace(T, H)
+    if stream is None:
+        dh = torch.empty(shape, dtype=ht, device=dev)
+        if dweight:
+            dw, ws = torch.empty((H,), dtype=torch.float32, device=dev), torch.empty((n,), dtype=torch.uint8, device=dev)
+    else:
+        dh = _empty(shape, ht, dev, stream)
+        if dweight:
+            dw, ws = _empty((H,), torch.float32, dev, stream), _empty((n,), torch.uint8, dev, stream)
+    if rd != 0:
+        dx = _empty(shape, _BF16, dev, stream)
+    if dweight:
+        wsp = ws.data_ptr()
+    rc = _call(index, lib.ep_add_rms_norm_backward, dy.data_ptr(), h.data_ptr(),
+               None if dresidual is None else dresidual.data_ptr(), rd, T, H, wp, wd, eps, dh.data_ptr(),
+               None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(), wsp, n,
+               _raw_stream(stream, index))
     if rc:
         _check(rc, where)
-    return dict(dresidual=dh, dx=dx, dweight=dw)
+    return {"dresidual": dh, "dx": dh if dx is None else dx, "dweight": dw}
 
 
 def router_select(logits: torch.Tensor, topk: int, *, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
@@ -1461,22 +1497,32 @@ def router_select(logits: torch.Tensor, topk: int, *, scoring: str = "softmax", 
     num_groups: runs of E / num_groups experts, of which the topk_groups best stay;
     group_score: "max", a group's largest key, or "top2", the sum of its two largest."""
     where = "router_select"
-    T, E = _matrix(where, "logits", logits)
-    dt = logits.dtype
+    shape, index, dt = logits.shape, logits.get_device(), logits.dtype
     if dt not in _FLOATS:
         raise TypeError(f"{where}: logits must be torch.float32 or torch.bfloat16, got {dt}")
+    if len(shape) != 2 or not _good(logits, dt, shape, index):
+        _ready(where, "logits", logits, dt, _matrix(where, "logits", logits))
+    T, E = shape
     if scoring not in _SCORINGS:
         raise ValueError(f"{where}: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
     if not 1 <= topk <= min(E, 32):
         raise ValueError(f"{where}: topk must be 1 .. min(E, 32), got {topk}")
-    groups = _groups(where, E, num_groups, topk_groups, group_score)
-    index = logits.get_device()
-    lp = _ready(where, "logits", logits, dt, (T, E), index)
-    bp = None if bias is None else _ready(where, "bias", bias, torch.float32, (E,), index)
-    idx = _empty((T, topk), torch.int64, logits.device, stream)
-    wts = _empty((T, topk), torch.float32, logits.device, stream)
-    rc = _call(index, load().ep_router_select, lp, _FLOATS[dt], T, E, bp, topk, _SCORINGS[scoring], *groups,
-               int(renormalize), scale, idx.data_ptr(), wts.data_ptr(), _raw_stream(stream, index))
+    g, kept, mark = _groups(where, E, num_groups, topk_groups, group_score)
+    bp = None
+    if bias is not None:
+        if not _good(bias, torch.float32, (E,), index):
+            _ready(where, "bias", bias, torch.float32, (E,), index)
+        bp = bias.data_ptr()
+    if stream is None:
+        dev, raw = logits.device, _current_raw(index)
+        idx = torch.empty((T, topk), dtype=torch.int64, device=dev)
+        wts = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    else:
+        raw = _raw_stream(stream, index)
+        idx = _empty((T, topk), torch.int64, logits.device, stream)
+        wts = _empty((T, topk), torch.float32, logits.device, stream)
+    rc = _call(index, load().ep_router_select, logits.data_ptr(), _FLOATS[dt], T, E, bp, topk, _SCORINGS[scoring], g, kept,
+               mark, 1 if renormalize else 0, scale, idx.data_ptr(), wts.data_ptr(), raw)
     if rc:
         _check(rc, where)
     return idx, wts
@@ -1490,21 +1536,24 @@ def router_select_backward(logits: torch.Tensor, topk_idx: torch.Tensor, dweight
     itself is held fixed.  Slots with an invalid expert id are left out and
     reported in err (an error_word()), so without one unseen."""
     where = "router_select_backward"
-    T, E = _matrix(where, "logits", logits)
-    dt = logits.dtype
+    shape, index, dt = logits.shape, logits.get_device(), logits.dtype
     if dt not in _FLOATS:
         raise TypeError(f"{where}: logits must be torch.float32 or torch.bfloat16, got {dt}")
+    if len(shape) != 2 or not _good(logits, dt, shape, index):
+        _ready(where, "logits", logits, dt, _matrix(where, "logits", logits))
+    T, E = shape
     if scoring not in _SCORINGS:
         raise ValueError(f"{where}: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
     K = _matrix(where, "topk_idx", topk_idx)[1]
-    index = logits.get_device()
-    lp = _ready(where, "logits", logits, dt, (T, E), index)
-    ip = _ready(where, "topk_idx", topk_idx, torch.int64, (T, K), index)
-    gp = _ready(where, "dweights", dweights, torch.float32, (T, K), index)
+    if not _good(topk_idx, torch.int64, (T, K), index):
+        _ready(where, "topk_idx", topk_idx, torch.int64, (T, K), index)
+    if not _good(dweights, torch.float32, (T, K), index):
+        _ready(where, "dweights", dweights, torch.float32, (T, K), index)
     wp = None if err is None else _word(where, err, index)
-    out = _empty((T, E), dt, logits.device, stream)
-    rc = _call(index, load().ep_router_select_backward, lp, _FLOATS[dt], T, E, ip, gp, K, _SCORINGS[scoring],
-               int(renormalize), scale, out.data_ptr(), wp, _raw_stream(stream, index))
+    out = torch.empty(shape, dtype=dt, device=logits.device) if stream is None else _empty(shape, dt, logits.device, stream)
+    rc = _call(index, load().ep_router_select_backward, logits.data_ptr(), _FLOATS[dt], T, E, topk_idx.data_ptr(),
+               dweights.data_ptr(), K, _SCORINGS[scoring], 1 if renormalize else 0, scale, out.data_ptr(), wp,
+               _raw_stream(stream, index))
     if rc:
         _check(rc, where)
     return out
@@ -1544,28 +1593,34 @@ class LoraAdapters(_Kept):
         [M,N].  out may be base if the types are the same.  Device errors go to err, an
         error_word() (default: this object's)."""
         M, index = x.shape[0], self._index
-        xp = _ready("LoraAdapters", "x", x, torch.bfloat16, (M, self.K), index)
-        ip = _ready("LoraAdapters", "ids", ids, torch.int64, (M,), index)
+        if not _good(x, _BF16, (M, self.K), index):
+            _ready("LoraAdapters", "x", x, _BF16, (M, self.K), index)
+        if not _good(ids, torch.int64, (M,), index):
+            _ready("LoraAdapters", "ids", ids, torch.int64, (M,), index)
         if M > self.max_tokens:
             raise ValueError(f"LoraAdapters: at most {self.max_tokens} rows, got {M}")
-        bp, bd = None, 0
+        bp, bd, shape = None, 0, (M, self.N)
         if base is not None:
-            if base.dtype not in _OUT_DTYPES:
-                raise TypeError(f"LoraAdapters: base must be torch.bfloat16 or torch.float32, got {base.dtype}")
-            bd = _OUT_DTYPES[base.dtype]
-            bp = _ready("LoraAdapters", "base", base, base.dtype, (M, self.N), index)
+            bt = base.dtype
+            if bt not in _OUT_DTYPES:
+                raise TypeError(f"LoraAdapters: base must be torch.bfloat16 or torch.float32, got {bt}")
+            if not _good(base, bt, shape, index):
+                _ready("LoraAdapters", "base", base, bt, shape, index)
+            bd, bp = _OUT_DTYPES[bt], base.data_ptr()
         if out is None:
-            out = _empty((M, self.N), self.out_dtype, x.device, stream)
+            out = (torch.empty(shape, dtype=self.out_dtype, device=x.device) if stream is None else
+                   _empty(shape, self.out_dtype, x.device, stream))
             op = out.data_ptr()
         else:
-            op = _ready("LoraAdapters", "out", out, self.out_dtype, (M, self.N), index)
+            op = _ready("LoraAdapters", "out", out, self.out_dtype, shape, index)
             _apart("LoraAdapters", "out", out, x=x, ids=ids, a=self.a, b=self.b, scaling=self.scaling,
                    base=None if op == bp and bd == self._code else base)
         ep = self._err if err is None else _word("LoraAdapters", err, index)
         raw = _current_raw(index) if stream is None else _raw_stream(stream, index)
         if raw != self._home and raw not in self._others:
             self._lend(stream, raw)
-        rc = _call(index, load().ep_lora, xp, M, self.K, ip, *self._mid, bp, bd, op, self._code, *self._ws, ep, raw)
+        rc = _call(index, load().ep_lora, x.data_ptr(), M, self.K, ids.data_ptr(), *self._mid, bp, bd, op, self._code,
+                   *self._ws, ep, raw)
         if rc:
             _check(rc, "LoraAdapters")
         return out

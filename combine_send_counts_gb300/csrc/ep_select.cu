@@ -257,6 +257,7 @@ __device__ __forceinline__ double warp_sum64(double v)
 }
 
 // A token's 64-bit scores, for the comparisons that need them.
+template <int = 0>
 __device__ __noinline__ Score64 scores64(const Choice &c, int64_t t, float mx)
 {
     Score64 s{c.sigmoid, (double)mx, 1.0};
@@ -283,6 +284,7 @@ struct Share {
 
 // Which groups stay, by marks in 64 bits of the experts (bit i of `mask`: this lane's first + i) that a mark may be made
 // of: a bit for each group.
+template <int = 0>
 __device__ __noinline__ uint32_t groups64(const Choice &c, int64_t t, float mx, Share mine, uint32_t mask)
 {
     const Score64 score = scores64(c, t, mx);
@@ -326,6 +328,7 @@ __device__ __forceinline__ int place_of(Key k, int e, int n)
 }
 
 // One candidate a lane, by keys in 64 bits: lane k gets the k-th expert.
+template <int = 0>
 __device__ __noinline__ int order64(const Choice &c, int64_t t, float mx, int e, int n, int *room)
 {
     const int lane = threadIdx.x & 31;
@@ -341,6 +344,7 @@ __device__ __noinline__ int order64(const Choice &c, int64_t t, float mx, int e,
 
 // The K largest of any number of candidates (bit i of `mask`: this lane's expert first + i) by keys in 64 bits, one at a
 // time; lane k gets the k-th, or -1.
+template <int = 0>
 __device__ __noinline__ int choose64(const Choice &c, int64_t t, float mx, Share mine, uint32_t mask)
 {
     const int lane = threadIdx.x & 31;

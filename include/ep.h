@@ -724,11 +724,13 @@ int ep_router_select_backward(const void *logits, int dtype, int64_t T, int E, c
  * Sums are fp32; the result is rounded once.
  *   K, N, R % 8 == 0, R <= 128; M, K, N <= 2^24 (else EP_ERR_UNSUPPORTED).
  *   Up to 1024 rows may name adapters in any order; with more, rows of one adapter
- *   are best neighbours (128 rows are gone over once for each adapter among them).
+ *   are best neighbours (128 rows are gone over once for each two to four adapters
+ *   among them).  An adapter's infinities and NaN stay its own rows'.
  *   ws: ep_lora_workspace_size(M, R) bytes, 256-byte aligned, scratch.  Calls that
  *     overlap on the GPU must not share it.
  * The same call on the same inputs gives the same bits.
- * Device errors: EP_ERR_INVALID_EXPERT (an id outside [-1, L): taken as -1). */
+ * Device errors: EP_ERR_INVALID_EXPERT (an id outside [-1, L): taken as -1),
+ * EP_ERR_TIMEOUT (a bounded wait gave up; out is then undefined). */
 size_t ep_lora_workspace_size(int64_t M, int R);
 int ep_lora(const void *x, int64_t M, int K, const int64_t *ids, const void *a, const void *b, const float *scaling,
             int L, int R, int N, const void *base, int base_dtype, void *out, int out_dtype, void *ws, size_t ws_bytes,

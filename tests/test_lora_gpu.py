@@ -28,7 +28,8 @@ def inputs(M, K, N, L, R, base, how, g):
 SIZES = [(1, 8, 8, 1, 8), (1, 4096, 4096, 4, 16), (3, 264, 72, 5, 24), (24, 2048, 1000, 32, 16), (17, 1024, 264, 2, 64),
          (33, 520, 520, 3, 128), (64, 4104, 256, 40, 32), (257, 256, 512, 7, 8), (1000, 264, 136, 9, 40),
          (1024, 512, 256, 300, 16), (1025, 512, 264, 6, 16), (1100, 264, 520, 3, 128), (1500, 1032, 40, 11, 64),
-         (2000, 136, 2048, 70, 8), (40, 72, 24, 5, 120), (1050, 64, 48, 2, 96)]
+         (2000, 136, 2048, 70, 8), (40, 72, 24, 5, 120), (1050, 64, 48, 2, 96), (1030, 8, 8, 2, 8), (1300, 200, 72, 3, 24),
+         (1040, 72, 264, 5, 40), (1200, 64, 96, 4, 72), (1100, 1000, 40, 2, 120), (1153, 448, 1000, 9, 32)]
 
 
 @pytest.mark.parametrize("M,K,N,L,R", SIZES)
@@ -125,6 +126,20 @@ def test_adapters_past_32_bits():
         got = ep.LoraAdapters(a, b, max_tokens=M, out_dtype=torch.float32)(xs, ids)
         want, tol = r.lora64(xs, ids * 0, a[-1:], b[-1:], None, None)
         r.inside(got, want, tol)
+
+
+def test_rows_past_32_bits():
+    M, K, N = 300001, 7168, 16   # x: 2.15e9 elements
+    g = f.gen(5)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = f.randn((3, K), g)
+    a, b = f.randn((2, 16, K), g, K ** -0.5), f.randn((2, N, 16), g)
+    ids = torch.ones(M, dtype=torch.int64, device="cuda")
+    ids[-1] = 0
+    got = ep.LoraAdapters(a, b, max_tokens=M, out_dtype=torch.float32)(x, ids)
+    want, tol = r.lora64(x[-3:], ids[-3:], a, b, None, None)
+    r.inside(got[-3:], want, tol)
+    assert bool((got[:-3] == 0).all())
 
 
 def test_smaller_batches_than_the_workspace_is_for():

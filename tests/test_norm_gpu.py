@@ -92,6 +92,12 @@ def test_in_place(residual, T, H):
     assert torch.equal(y, want["y"]) and torch.equal(h, want["residual"])
 
 
+def test_the_sum_alone():
+    x, w, res = inputs(5, 1000, "fp32", "bf16")
+    got = ep.add_rms_norm(x, w, res, y=False)
+    assert got["y"] is None and torch.equal(got["residual"], x.float() + res)
+
+
 def test_rows_are_their_own():
     x, w, res = inputs(7, 1024, "bf16", "bf16")
     want = ep.add_rms_norm(x, w, res, fp8=True)

@@ -93,6 +93,23 @@ def test_masks_and_non_finite(E, groups, scoring, bias, mark):
         r.inside(w[rows], w64[rows], r.weights_tol(l[rows], w64[rows]))
 
 
+@pytest.mark.parametrize("E,groups", [(64, 8), (1000, 8), (63, 7)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_fewer_experts_than_slots_and_unaligned_rows(E, groups, dtype):
+    T, g = 9, f.gen(E)
+    room = f.randn((T * E + 8,), g, 1.0, TYPES[dtype])
+    bias = f.randn((E + 4,), g, 0.1, torch.float32)
+    for at in (0, 1, 2, 3):   # starts at any element
+        l, b = room[at:at + T * E].view(T, E), bias[at:at + E]
+        for K in (4, min(32, E // groups + 5)):
+            check(l, K, scoring="sigmoid", bias=b, num_groups=groups, topk_groups=1, group_score="top2")
+            check(l, K, scoring="softmax", num_groups=groups, topk_groups=1, group_score="max", renormalize=False)
+        idx, w = ep.router_select(l, 4)
+        got = ep.router_select_backward(l, idx, w, renormalize=False)
+        want, tol = r.select_backward64(l, idx, w, scoring="softmax", renormalize=False, scale=1.0)
+        r.inside(got, want, tol)
+
+
 def test_uniform_logits_and_no_tokens():
     l = torch.zeros((50, 256), device="cuda")
     idx, w = check(l, 8, scoring="sigmoid", bias=torch.zeros(256, device="cuda"), num_groups=8, topk_groups=4,
