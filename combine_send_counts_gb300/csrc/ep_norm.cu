@@ -153,21 +153,49 @@ __device__ __forceinline__ float half_warp_max(float m)
     return m;
 }
 
-// The scale of a group whose largest magnitude is m, its reciprocal and UE8M0 code.
-__device__ __forceinline__ void group_scale(float m, bool power_of_two, float &scale, float &inverse, uint32_t &code)
-{
-    const float a = fmaxf(m, 1e-4f);
-    scale = __fdiv_rn(a, 448.0f);
-    code = 0;
-    if (power_of_two) {
-        const uint32_t b = __float_as_uint(scale);
-        code = (b >> 23) + ((b & 0x7fffffu) != 0u);
-        scale = __uint_as_float(code << 23);
-        inverse = code < 255u ? __uint_as_float((254u - code) << 23) : 0.0f;
-    } else {
-        inverse = __fdiv_rn(448.0f, a);
+// A group of 128: `top` is the largest magnitude of h w, and y = h w rs.
+struct Group {
+    float scale, of;        // scale; a column's value in codes is about h w * of
+    float top, back;        // top, or 0 where values are y's own; about 1 / top
+    uint32_t code;
+
+    __device__ __forceinline__ Group(float top_, float rs, bool power_of_two)
+    {
+        const float largest = __fmul_rn(top_, rs);
+        const float a = largest > 1e-4f ? largest : 1e-4f;   // also where it is NaN
+        code = 0;
+        if (power_of_two) {
+            const float s = __fdiv_rn(a, 448.0f);
+            const uint32_t b = __float_as_uint(s);
+            code = (b >> 23) + ((b & 0x7fffffu) != 0u);
+            scale = __uint_as_float(code << 23);
+            of = code < 255u ? __uint_as_float((254u - code) << 23) : 0.0f;
+            top = back = 0.0f;
+            return;
+        }
+        scale = __fmul_rn(a, 1.0f / 448.0f);
+        // rs is no part of the quotient 448 h w / top, unless the floor or an infinity is what counts
+        const bool own = largest > 1e-4f && largest < __int_as_float(0x7f800000) && top_ < 1e36f && top_ > 1e-30f;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(back) : "f"(own ? top_ : a));
+        of = __fmul_rn(back, 448.0f);
+        top = own ? top_ : 0.0f;
     }
-}
+
+    // Two columns in units of the scale.  With bf16 h and w their product is exact, and the remainder makes the
+    // quotient so too where it is a number of few bits: halfway between two codes it is rounded as the quotient
+    // itself, not by what rounding left of it.
+    __device__ __forceinline__ float2 value(float2 hw, float2 y) const
+    {
+        if (top == 0.0f)
+            return mul2_rn(y, make_float2(of, of));
+        const float2 q = mul2_rn(hw, make_float2(of, of)), less = make_float2(-top, -top);
+        const float2 left = fma2_rn(q, less, mul2_rn(hw, make_float2(448.0f, 448.0f)));
+        return fma2_rn(left, make_float2(back, back), q);
+    }
+};
+
+// Two columns of eight.
+__device__ __forceinline__ float2 pair(const float (&f)[8], int j) { return make_float2(f[2 * j], f[2 * j + 1]); }
 
 template <int RES, int NV, int SF, int MOST>
 __global__ void __launch_bounds__(MOST)
@@ -201,19 +229,20 @@ norm_kernel(Norm a)
             h[i].set(f);
         }
     }
-    float squares[1] = {0.0f};
+    float2 both = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * 8;
         float f[8];
         h[i].get(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            squares[0] = __fmaf_rn(f[j], f[j], squares[0]);
+        for (int j = 0; j < 4; ++j)
+            both = fma2_rn(pair(f, j), pair(f, j), both);
         if (a.sum != nullptr && c < a.H)
             h[i].store(a.sum, row + c);
     }
     int phase = 0;
+    float squares[1] = {__fadd_rn(both.x, both.y)};
     block_sums(squares, s, phase);
     const float rs = inverse_root(squares[0], a.H, a.eps);
     const int groups = a.H >> 7;
@@ -221,35 +250,33 @@ norm_kernel(Norm a)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * 8;
-        float f[8], w[8];
+        float f[8], w[8], y[8], m = 0.0f;
         h[i].get(f);
         load_weights(a.w, a.w_dtype, c, c < a.H, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = __fmul_rn(__fmul_rn(f[j], rs), w[j]);
+        for (int j = 0; j < 4; ++j) {
+            const float2 hw = mul2_rn(pair(f, j), pair(w, j)), v = mul2_rn(hw, make_float2(rs, rs));   // hw exact of two bf16
+            f[2 * j] = hw.x;
+            f[2 * j + 1] = hw.y;
+            y[2 * j] = v.x;
+            y[2 * j + 1] = v.y;
+            m = fmaxf(m, fmaxf(fabsf(hw.x), fabsf(hw.y)));   // a NaN does not enter it
+        }
         if (a.y != nullptr && c < a.H) {
             Eight<kBf16> o;
-            o.set(f);
+            o.set(y);
             o.store(a.y, row + c);
         }
         if (SF >= 0) {
-            float m = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                m = fmaxf(m, fabsf(f[j]));   // a NaN does not enter it
-            float scale, inverse;
-            uint32_t code;
-            group_scale(half_warp_max(m), a.scale.round != 0, scale, inverse, code);
+            const Group group(half_warp_max(m), rs, a.scale.round != 0);
             uint32_t p[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                p[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(
-                    mul2_rn(make_float2(f[2 * j], f[2 * j + 1]), make_float2(inverse, inverse)), __NV_SATFINITE,
-                    __NV_E4M3);
+                p[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(group.value(pair(f, j), pair(y, j)), __NV_SATFINITE, __NV_E4M3);
             if (c < a.H) {
                 st_stream(reinterpret_cast<uint2 *>(a.q + row + c), make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16));
                 if ((threadIdx.x & 15) == 0)
-                    put_scale<SF < 0 ? 0 : SF>(a.scale, base, c >> 7, scale, code);
+                    put_scale<SF < 0 ? 0 : SF>(a.scale, base, c >> 7, group.scale, group.code);
             }
         }
     }
@@ -352,9 +379,6 @@ struct Slot {
     static constexpr int kPieces = RES == kFp32 ? 5 : 3;   // 16 bytes each: dy, then h, then dres
     static constexpr int kBytes = kPieces * 16;            // of eight columns of a row
 };
-
-// Two roundings at once, on the pairs of eight values.
-__device__ __forceinline__ float2 pair(const float (&f)[8], int j) { return make_float2(f[2 * j], f[2 * j + 1]); }
 
 template <int RES, int NV, int AHEAD, int MOST, int BLOCKS>
 __global__ void __launch_bounds__(MOST, BLOCKS)

@@ -77,6 +77,20 @@ def test_eight_bits(T, H, fmt, residual):
                 assert torch.equal(got["residual"], h)
 
 
+@pytest.mark.parametrize("T,H", [(1, 7168), (300, 2048)])
+def test_codes_halfway_between_two(T, H):
+    # h and w of few bits: their products are exact, and many stand exactly halfway between two codes
+    g = f.gen(H)
+    h = (torch.randint(-31, 32, (T, H), generator=g, device="cuda").float() / 32).to(torch.bfloat16)
+    h[:, ::128] = 7.0 / 8   # the largest after w, so that values in units of the scale are whole 64ths of h w
+    w = torch.ones(H, device="cuda").to(torch.bfloat16)
+    w[::128] = 2.0
+    got = ep.add_rms_norm(h, w, None, fp8=True)
+    d = (h.double() * w.double()).view(T, -1, 128)
+    want = (d * 448 / d.abs().amax(2, keepdim=True)).float().to(torch.float8_e4m3fn).view(T, H)
+    assert torch.equal(got["q"].view(torch.float8_e4m3fn).float(), want.float())
+
+
 @pytest.mark.parametrize("residual", ["bf16", "fp32"])
 @pytest.mark.parametrize("T,H", [(1, 2048), (160, 7168), (160, 10000)])
 def test_in_place(residual, T, H):
