@@ -1390,10 +1390,14 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Opti
     is written over residual."""
     where = "add_rms_norm"
     shape, index = x.shape, x.get_device()
-    if len(shape) != 2 or not _good(x, _BF16, shape, index):
+    if len(shape) != 2 or x.dtype is not _BF16 or index < 0 or not x.is_contiguous():
         _ready(where, "x", x, _BF16, _matrix(where, "x", x))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return add_rms_norm(x, weight, residual, eps=eps, y=y, fp8=fp8, scale_fmt=scale_fmt, round_scale=round_scale,
+                                inplace=inplace, stream=stream)
     T, H = shape
-    dev, lib = x.device, load()
+    dev = x.device
     wp, wd = (None, 0) if weight is None else _norm_weight(where, weight, H, index)
     rp, rd, h, hp = None, 0, None, None
     if residual is not None:
@@ -1407,7 +1411,7 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Opti
             _apart(where, "residual", residual, x=x, weight=weight)
             h = residual
         else:
-            h = _empty(shape, rt, dev, stream) if stream is not None else torch.empty(shape, dtype=rt, device=dev)
+            h = torch.empty_like(residual) if stream is None else _empty(shape, rt, dev, stream)
         hp = h.data_ptr()
     elif inplace:
         raise ValueError(f"{where}: inplace needs a residual")
@@ -1415,7 +1419,7 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Opti
         raise ValueError(f"{where}: nothing is asked for")
     out = q = scale = yp = qp = sp = None
     if y:
-        out = _empty(shape, _BF16, dev, stream) if stream is not None else torch.empty(shape, dtype=_BF16, device=dev)
+        out = torch.empty_like(x) if stream is None else _empty(shape, _BF16, dev, stream)
         yp = out.data_ptr()
     if fp8:
         if scale_fmt not in _SCALE_FMTS:
@@ -1423,12 +1427,12 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Opti
         of = (T, H // 128) if scale_fmt == EP_SCALE_ROW_F32 else (H // 128, T) if scale_fmt == EP_SCALE_COL_F32 else (H // 512, T)
         kind = torch.int32 if scale_fmt == EP_SCALE_COL_UE8M0 else torch.float32
         if stream is None:
-            q, scale = torch.empty(shape, dtype=torch.uint8, device=dev), torch.empty(of, dtype=kind, device=dev)
+            q, scale = torch.empty_like(x, dtype=torch.uint8), torch.empty(of, dtype=kind, device=dev)
         else:
             q, scale = _empty(shape, torch.uint8, dev, stream), _empty(of, kind, dev, stream)
         qp, sp = q.data_ptr(), scale.data_ptr()
-    rc = _call(index, lib.ep_add_rms_norm, x.data_ptr(), rp, rd, T, H, wp, wd, eps, hp, yp, qp, sp, scale_fmt,
-               1 if round_scale else 0, _raw_stream(stream, index))
+    rc = load().ep_add_rms_norm(x.data_ptr(), rp, rd, T, H, wp, wd, eps, hp, yp, qp, sp, scale_fmt, 1 if round_scale else 0,
+                                _current_raw(index) if stream is None else _raw_stream(stream, index))
     if rc:
         _check(rc, where)
     return {"y": out, "residual": h, "q": q, "scale": scale}
@@ -1450,10 +1454,13 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[to
     bf16), dweight [H] fp32 or None)."""
     where = "add_rms_norm_backward"
     shape, index = dy.shape, dy.get_device()
-    if len(shape) != 2 or not _good(dy, _BF16, shape, index):
+    if len(shape) != 2 or dy.dtype is not _BF16 or index < 0 or not dy.is_contiguous():
         _ready(where, "dy", dy, _BF16, _matrix(where, "dy", dy))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return add_rms_norm_backward(dy, h, weight, dresidual, eps=eps, dweight=dweight, stream=stream)
     T, H = shape
-    dev, lib, ht = dy.device, load(), h.dtype
+    dev, ht = dy.device, h.dtype
     if ht not in _OUT_DTYPES:
         raise TypeError(f"{where}: h must be torch.bfloat16 or torch.float32, got {ht}")
     rd = _OUT_DTYPES[ht]
@@ -1467,7 +1474,7 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[to
     if dweight:
         n = _norm_workspace(T, H)
     if stream is None:
-        dh = torch.empty(shape, dtype=ht, device=dev)
+        dh = torch.empty_like(h)
         if dweight:
             dw, ws = torch.empty((H,), dtype=torch.float32, device=dev), torch.empty((n,), dtype=torch.uint8, device=dev)
     else:
@@ -1478,10 +1485,10 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[to
         dx = _empty(shape, _BF16, dev, stream)
     if dweight:
         wsp = ws.data_ptr()
-    rc = _call(index, lib.ep_add_rms_norm_backward, dy.data_ptr(), h.data_ptr(),
-               None if dresidual is None else dresidual.data_ptr(), rd, T, H, wp, wd, eps, dh.data_ptr(),
-               None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(), wsp, n,
-               _raw_stream(stream, index))
+    rc = load().ep_add_rms_norm_backward(
+        dy.data_ptr(), h.data_ptr(), None if dresidual is None else dresidual.data_ptr(), rd, T, H, wp, wd, eps,
+        dh.data_ptr(), None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(), wsp, n,
+        _current_raw(index) if stream is None else _raw_stream(stream, index))
     if rc:
         _check(rc, where)
     return {"dresidual": dh, "dx": dh if dx is None else dx, "dweight": dw}
@@ -1500,8 +1507,12 @@ def router_select(logits: torch.Tensor, topk: int, *, scoring: str = "softmax", 
     shape, index, dt = logits.shape, logits.get_device(), logits.dtype
     if dt not in _FLOATS:
         raise TypeError(f"{where}: logits must be torch.float32 or torch.bfloat16, got {dt}")
-    if len(shape) != 2 or not _good(logits, dt, shape, index):
+    if len(shape) != 2 or index < 0 or not logits.is_contiguous():
         _ready(where, "logits", logits, dt, _matrix(where, "logits", logits))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return router_select(logits, topk, scoring=scoring, bias=bias, num_groups=num_groups, topk_groups=topk_groups,
+                                 group_score=group_score, renormalize=renormalize, scale=scale, stream=stream)
     T, E = shape
     if scoring not in _SCORINGS:
         raise ValueError(f"{where}: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
@@ -1521,8 +1532,8 @@ def router_select(logits: torch.Tensor, topk: int, *, scoring: str = "softmax", 
         raw = _raw_stream(stream, index)
         idx = _empty((T, topk), torch.int64, logits.device, stream)
         wts = _empty((T, topk), torch.float32, logits.device, stream)
-    rc = _call(index, load().ep_router_select, logits.data_ptr(), _FLOATS[dt], T, E, bp, topk, _SCORINGS[scoring], g, kept,
-               mark, 1 if renormalize else 0, scale, idx.data_ptr(), wts.data_ptr(), raw)
+    rc = load().ep_router_select(logits.data_ptr(), _FLOATS[dt], T, E, bp, topk, _SCORINGS[scoring], g, kept, mark,
+                                 1 if renormalize else 0, scale, idx.data_ptr(), wts.data_ptr(), raw)
     if rc:
         _check(rc, where)
     return idx, wts
@@ -1539,8 +1550,12 @@ def router_select_backward(logits: torch.Tensor, topk_idx: torch.Tensor, dweight
     shape, index, dt = logits.shape, logits.get_device(), logits.dtype
     if dt not in _FLOATS:
         raise TypeError(f"{where}: logits must be torch.float32 or torch.bfloat16, got {dt}")
-    if len(shape) != 2 or not _good(logits, dt, shape, index):
+    if len(shape) != 2 or index < 0 or not logits.is_contiguous():
         _ready(where, "logits", logits, dt, _matrix(where, "logits", logits))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return router_select_backward(logits, topk_idx, dweights, scoring=scoring, renormalize=renormalize, scale=scale,
+                                          err=err, stream=stream)
     T, E = shape
     if scoring not in _SCORINGS:
         raise ValueError(f"{where}: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
@@ -1550,10 +1565,11 @@ def router_select_backward(logits: torch.Tensor, topk_idx: torch.Tensor, dweight
     if not _good(dweights, torch.float32, (T, K), index):
         _ready(where, "dweights", dweights, torch.float32, (T, K), index)
     wp = None if err is None else _word(where, err, index)
-    out = torch.empty(shape, dtype=dt, device=logits.device) if stream is None else _empty(shape, dt, logits.device, stream)
-    rc = _call(index, load().ep_router_select_backward, logits.data_ptr(), _FLOATS[dt], T, E, topk_idx.data_ptr(),
-               dweights.data_ptr(), K, _SCORINGS[scoring], 1 if renormalize else 0, scale, out.data_ptr(), wp,
-               _raw_stream(stream, index))
+    out = torch.empty_like(logits) if stream is None else _empty(shape, dt, logits.device, stream)
+    rc = load().ep_router_select_backward(
+        logits.data_ptr(), _FLOATS[dt], T, E, topk_idx.data_ptr(), dweights.data_ptr(), K, _SCORINGS[scoring],
+        1 if renormalize else 0, scale, out.data_ptr(), wp,
+        _current_raw(index) if stream is None else _raw_stream(stream, index))
     if rc:
         _check(rc, where)
     return out
@@ -1593,6 +1609,9 @@ class LoraAdapters(_Kept):
         [M,N].  out may be base if the types are the same.  Device errors go to err, an
         error_word() (default: this object's)."""
         M, index = x.shape[0], self._index
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self(x, ids, base, out, err, stream)
         if not _good(x, _BF16, (M, self.K), index):
             _ready("LoraAdapters", "x", x, _BF16, (M, self.K), index)
         if not _good(ids, torch.int64, (M,), index):
@@ -1619,8 +1638,7 @@ class LoraAdapters(_Kept):
         raw = _current_raw(index) if stream is None else _raw_stream(stream, index)
         if raw != self._home and raw not in self._others:
             self._lend(stream, raw)
-        rc = _call(index, load().ep_lora, x.data_ptr(), M, self.K, ids.data_ptr(), *self._mid, bp, bd, op, self._code,
-                   *self._ws, ep, raw)
+        rc = load().ep_lora(x.data_ptr(), M, self.K, ids.data_ptr(), *self._mid, bp, bd, op, self._code, *self._ws, ep, raw)
         if rc:
             _check(rc, "LoraAdapters")
         return out
