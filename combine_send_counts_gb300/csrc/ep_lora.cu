@@ -4,17 +4,20 @@
 //
 // Two kernels, the second launched while the first drains: `shrink` leaves
 // v = A x in parts of K in the workspace, `expand` adds the parts, multiplies by
-// B and adds to the base.  Both take 16 rows of x as the 16-row operand of
-// m16n8k16 matrix steps, ranks or output columns as its 8 columns.
+// B and adds to the base.  v is kept whole between the two products, as the sum of
+// three bf16 terms (24 bits), because the matrix step takes bf16.
 //
-//   few rows (up to 1024): a tile is up to 16 rows of the batch that name the same
-//   adapter, found by the block from the ids, so that each adapter's weights are
-//   read once for 16 rows wherever they stand;
-//   more rows: a tile is 128 neighbouring rows, gone over once for each adapter that
-//   they name, which is one or two where requests are long.
+// Rows come in one of three ways, by the sizes (Way):
+//   few: a tile is up to 16 rows that name the same adapter, wherever they stand, so that
+//     each adapter's weights are read once for 16 rows.  Up to 64 rows each block finds
+//     its tile by itself; with more, a block makes a list of them first.
+//   many (ep_lora_many.cu): a tile is 128 neighbouring rows, gone over once for each two or
+//     four adapters that they name.
+//   mixed: each 128 rows that name more than eight adapters by the list, the rest as many.
 //
-// v is kept whole between the two products, as the sum of three bf16 terms (24
-// bits), because the matrix step takes bf16.
+// What bounds them: few rows, the chain of two dependent launches (24 rows, rank 16,
+// 4096 x 4096: 6.9 us, of which the bytes are 0.7); 1024 rows of 64 adapters 23 us;
+// many rows, HBM and the start of expand (8192 rows, rank 64, 7168 x 4096: 62 us, 4.1 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -31,13 +34,17 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnit = 32;            // columns of a lane's 16-byte pieces: two k16 steps
 constexpr int kBatch = 4;            // units loaded together, and summed by matrix steps alone
-constexpr int kTile = 16;
+constexpr int kTile = kLoraTile;
+// Most rows of which each block finds its tile by itself: 64 rows of 64 adapters of rank 64 took 18 us so, and 96 took 10
+// to 25 us with a list.  (Of 256 rows of 64 adapters of rank 16, 17.5 us so and 13.2 with a list; of 1024, 55 and 23,
+// most of it for the blocks that look at all ids to find that they have no tile.)
+constexpr int kSearchRows = 64;
 
 // The tile that begins with row m: `mine` is the row index of this lane's slot (lane & 15), or -1; false if no tile
 // does.  A tile begins with every 16th row of an adapter.  All threads of the block.
 __device__ __forceinline__ bool gather_tile(const Lora &p, int m, int adapter, int &mine)
 {
-    __shared__ uint32_t same[kLoraFewRows / 32];
+    __shared__ uint32_t same[kSearchRows / 32];
     const int words = ((int)p.M + 31) / 32;
     for (int r = threadIdx.x; r < words * 32; r += kThreads) {
         const uint32_t bits = __ballot_sync(kFull, r < p.M && adapter_of(p, r) == adapter);
@@ -69,6 +76,114 @@ __device__ __forceinline__ bool gather_tile(const Lora &p, int m, int adapter, i
         bits = same[w];
     }
     return true;
+}
+
+// ------------------------------------------------------------------ list --
+// The tiles of more rows, by one block: the rows of an adapter (or of none) are counted in
+// a table of twice as many places as there are rows, which gives each row its place
+// among them, and each adapter its tiles.  The order of tiles, and of rows in them, is as
+// it comes: a row's sums do not depend on where it stands.
+constexpr int kListThreads = 1024;
+constexpr uint32_t kNowhere = 0xffffffffu;
+
+struct Entry {
+    int key, count;   // adapter, or -1 for none; -2: a free entry.  Rows, and then the first tile
+};
+
+__global__ void __launch_bounds__(kListThreads)
+lora_list_kernel(Lora p, int places)
+{
+    extern __shared__ __align__(16) uint8_t list_room[];
+    Entry *const table = reinterpret_cast<Entry *>(list_room);                      // [places]
+    uint32_t *const where = reinterpret_cast<uint32_t *>(list_room + places * sizeof(Entry));   // [M]: place, and rank above it
+    __shared__ int tiles;
+    const int M = (int)p.M, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < places; i += kListThreads)
+        table[i] = Entry{-2, 0};
+    if (threadIdx.x == 0)
+        tiles = 0;
+    grid_dependency_wait();
+    allow_dependents();
+    __syncthreads();
+    auto add = [&](int r, int key) {   // a whole warp; -2: not in the list
+        const uint32_t same = __match_any_sync(kFull, key);
+        const int leader = __ffs(same) - 1;
+        int at = 0, rank = 0;
+        if (lane == leader && key != -2) {
+            at = (int)((uint32_t)key * 2654435761u >> 16) & (places - 1);
+            for (int i = 0; i < places; ++i) {   // at most half of them are taken
+                const int was = atomicCAS(&table[at].key, -2, key);
+                if (was == -2 || was == key)
+                    break;
+                at = (at + 1) & (places - 1);
+            }
+            rank = atomicAdd(&table[at].count, __popc(same));
+        }
+        at = __shfl_sync(kFull, at, leader);
+        rank = __shfl_sync(kFull, rank, leader) + __popc(same & lanemask_lt());
+        if (r < M)
+            where[r] = key == -2 ? kNowhere : (uint32_t)rank << 14 | (uint32_t)at;
+    };
+    // a warp takes 32 rows, or the 128 of a tile of the other kernels, which it may leave to them
+    constexpr int kEach = kLoraWide / 32;
+    const int warp = threadIdx.x >> 5, each = p.mixed ? kEach : 1;
+    bool some = false;
+    for (int m = warp * each * 32; m < M; m += kListThreads * each) {
+        int keys[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int r = m + i * 32 + lane;
+            keys[i] = i < each && r < M ? adapter_of(p, r) : -2;
+            if (i < each && r < M && bad_id(p, r))
+                raise(p.err, EP_ERR_INVALID_EXPERT);
+        }
+        const bool theirs = p.mixed && !many_adapters(keys);
+        some |= !theirs;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (i < each)
+                add(m + i * 32 + lane, theirs ? -2 : keys[i]);
+    }
+    if (!__syncthreads_or(some)) {
+        if (threadIdx.x == 0)
+            *p.list = 0;
+        return;
+    }
+    int *const adapters = p.list + 1, *const rows = adapters + M;
+    for (int i = threadIdx.x; i < places; i += kListThreads) {
+        const Entry e = table[i];
+        if (e.key == -2)
+            continue;
+        const int n = (e.count + kTile - 1) / kTile, from = atomicAdd(&tiles, n);
+        for (int t = 0; t < n; ++t)
+            adapters[from + t] = e.key;
+        for (int j = e.count; j < n * kTile; ++j)
+            rows[from * kTile + j] = -1;
+        table[i].count = from;
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < M; r += kListThreads)
+        if (where[r] != kNowhere)
+            rows[table[where[r] & 0x3fffu].count * kTile + (int)(where[r] >> 14)] = r;
+    if (threadIdx.x == 0)
+        *p.list = tiles;
+}
+
+// Where a block of the kernels for few rows has its tiles from: each row that begins one, a list of which it takes one, or
+// one of which it takes several.
+enum Source { kSearch, kList, kLists };
+
+// This lane's row (lane & 15) of tile m, or -1; false if there is none.  With a list it is its tile m; without, that
+// which begins with row m.
+template <int FROM>
+__device__ __forceinline__ bool tile_of(const Lora &p, int m, int adapter, int &mine)
+{
+    if (FROM != kSearch) {
+        mine = p.list[1 + p.M + m * kTile + (threadIdx.x & (kTile - 1))];
+        return true;
+    }
+    mine = (threadIdx.x & (kTile - 1)) == 0 ? m : -1;
+    return adapter < 0 || gather_tile(p, m, adapter, mine);
 }
 
 __device__ __forceinline__ uint4 piece(const uint8_t *row, int k, int K)
@@ -129,51 +244,54 @@ __device__ __forceinline__ void leave(const Lora &p, const float (&acc)[NT][4], 
     }
 }
 
-// Few rows: a block per row (where a tile begins) and part of K, its warps an eighth of that each.
-template <int NT>
+// A block takes tiles of a list (or one, without) and a part of K, its warps an eighth of that each.
+template <int NT, int FROM>
 __global__ void __launch_bounds__(kThreads)
 lora_shrink_few_kernel(Lora p)
 {
     __shared__ __align__(16) float kept[kWarps / 2][NT * 32 * 4];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, m = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
     allow_dependents();
-    const int adapter = adapter_of(p, m);
-    if (adapter < 0) {
-        if (threadIdx.x == 0 && blockIdx.y == 0 && bad_id(p, m))
-            raise(p.err, EP_ERR_INVALID_EXPERT);
-        return;
-    }
-    int mine;
-    if (!gather_tile(p, m, adapter, mine))
-        return;
-    const int m0 = __shfl_sync(kFull, mine, lane >> 2), m1 = __shfl_sync(kFull, mine, (lane >> 2) + 8);
     const int units = (p.K + kUnit - 1) / kUnit, all = p.splits * kWarps, part = blockIdx.y * kWarps + warp;
-    float acc[NT][4] = {};
-    product<NT>(acc, m0 < 0 ? nullptr : p.x + (int64_t)m0 * p.K * 2, m1 < 0 ? nullptr : p.x + (int64_t)m1 * p.K * 2,
-                p.a + (int64_t)adapter * p.R * p.K * 2, p.R, p.K, (int)((int64_t)units * part / all),
-                (int)((int64_t)units * (part + 1) / all));
+    const int u0 = (int)((int64_t)units * part / all), u1 = (int)((int64_t)units * (part + 1) / all);
+    const int tiles = FROM != kSearch ? *p.list : (int)p.M;
+    for (int m = blockIdx.x; m < tiles; m = FROM == kLists ? m + gridDim.x : tiles) {
+        const int adapter = FROM != kSearch ? p.list[1 + m] : adapter_of(p, m);
+        if (adapter < 0) {
+            if (FROM == kSearch && threadIdx.x == 0 && blockIdx.y == 0 && bad_id(p, m))
+                raise(p.err, EP_ERR_INVALID_EXPERT);
+            continue;
+        }
+        int mine;
+        if (!tile_of<FROM>(p, m, adapter, mine))
+            continue;
+        const int m0 = __shfl_sync(kFull, mine, lane >> 2), m1 = __shfl_sync(kFull, mine, (lane >> 2) + 8);
+        float acc[NT][4] = {};
+        product<NT>(acc, m0 < 0 ? nullptr : p.x + (int64_t)m0 * p.K * 2, m1 < 0 ? nullptr : p.x + (int64_t)m1 * p.K * 2,
+                    p.a + (int64_t)adapter * p.R * p.K * 2, p.R, p.K, u0, u1);
 #pragma unroll
-    for (int half = kWarps / 2; half >= 1; half /= 2) {
-        if (warp >= half && warp < 2 * half)
+        for (int half = kWarps / 2; half >= 1; half /= 2) {
+            if (warp >= half && warp < 2 * half)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<float4 *>(&kept[warp - half][(n * 32 + lane) * 4]) =
-                    make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-        __syncthreads();
-        if (warp < half)
+                for (int n = 0; n < NT; ++n)
+                    *reinterpret_cast<float4 *>(&kept[warp - half][(n * 32 + lane) * 4]) =
+                        make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            __syncthreads();
+            if (warp < half)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float4 v = *reinterpret_cast<const float4 *>(&kept[warp][(n * 32 + lane) * 4]);
-                acc[n][0] = __fadd_rn(acc[n][0], v.x);
-                acc[n][1] = __fadd_rn(acc[n][1], v.y);
-                acc[n][2] = __fadd_rn(acc[n][2], v.z);
-                acc[n][3] = __fadd_rn(acc[n][3], v.w);
-            }
-        __syncthreads();
+                for (int n = 0; n < NT; ++n) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&kept[warp][(n * 32 + lane) * 4]);
+                    acc[n][0] = __fadd_rn(acc[n][0], v.x);
+                    acc[n][1] = __fadd_rn(acc[n][1], v.y);
+                    acc[n][2] = __fadd_rn(acc[n][2], v.z);
+                    acc[n][3] = __fadd_rn(acc[n][3], v.w);
+                }
+            __syncthreads();
+        }
+        if (warp == 0)
+            leave<NT>(p, acc, m0, m1, blockIdx.y);
     }
-    if (warp == 0)
-        leave<NT>(p, acc, m0, m1, blockIdx.y);
 }
 
 // ---------------------------------------------------------------- expand --
@@ -249,119 +367,191 @@ __device__ __forceinline__ void put(void *out, bool bf16_base, bool bf16_out, co
     }
 }
 
-// Few rows: a block per row (where a tile begins, or without an adapter) and 256
-// columns.  Column g of block j of a warp's 32 stands for column n0 + 8 (g / 2) + 2 j +
-// g % 2, so that a lane ends up with eight neighbouring columns of each of its rows.
-// The block makes v once, in shared memory.
-template <int UNITS, int WORDS>
+// A block takes tiles of a list (or, without, one, or a row without an adapter) and 256 columns.
+// Column g of block j of a warp's 32 stands for column n0 + 8 (g / 2) + 2 j + g % 2, so that a
+// lane ends up with eight neighbouring columns of each of its rows.  The block makes v once, in
+// shared memory.
+template <int UNITS, int WORDS, int FROM>
 __global__ void __launch_bounds__(kThreads)
 lora_expand_few_kernel(Lora p)
 {
     constexpr int kRanks = UNITS * WORDS * 8, kVRow = kRanks * 2 + 16;   // bytes of a row of v
     __shared__ __align__(16) uint8_t v_room[kPlanes][kTile][kVRow];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, m = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // Every block of shrink has waited for what was before it, so that only what shrink itself writes is waited for here.
-    const int adapter = adapter_of(p, m);
     const int n0 = (blockIdx.y * kWarps + warp) * 32, n = n0 + 8 * t;
-    Ranks<UNITS, WORDS> b[4];
-    auto load_b = [&]() {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
-            b[j].load(adapter >= 0 && row < p.N ? p.b + ((int64_t)adapter * p.N + row) * p.R * 2 : nullptr, p.R);
-        }
-    };
-    const bool early = p.M <= 64;   // most blocks have a tile, and nothing waits for the ids
-    if (early)
-        load_b();
-    int mine = (lane & (kTile - 1)) == 0 ? m : -1;
-    if (adapter >= 0 && !gather_tile(p, m, adapter, mine))
-        return;
-    const int m0 = __shfl_sync(kFull, mine, g), m1 = __shfl_sync(kFull, mine, g + 8);
-    Base base0, base1;
-    base0.load(p, m0, n);
-    base1.load(p, m1, n);
-    if (!early)
-        load_b();
-    const float none = adapter >= 0 ? 0.0f : -0.0f;   // base + -0 is base
-    float d[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        d[j][0] = d[j][1] = d[j][2] = d[j][3] = none;
-    const float scaling = scaling_of(p, adapter);
-    grid_dependency_wait();
-    allow_dependents();
-    if (adapter >= 0) {
-        for (int i = warp; i < kTile; i += kWarps) {   // a warp to a row
-            const int row = __shfl_sync(kFull, mine, i);
-            for (int r = 2 * lane; r < kRanks; r += 64) {
-                uint32_t terms[kPlanes];
-                split(ranks_of(p, row, r, scaling), terms);
-#pragma unroll
-                for (int z = 0; z < kPlanes; ++z)
-                    *reinterpret_cast<uint32_t *>(&v_room[z][i][r * 2]) = terms[z];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-            for (int z = kPlanes - 1; z >= 0; --z) {
-                uint32_t v0[WORDS], v1[WORDS];
-                const uint32_t *at0 = reinterpret_cast<const uint32_t *>(&v_room[z][g][(u * 4 + t) * WORDS * 4]);
-                const uint32_t *at1 = reinterpret_cast<const uint32_t *>(&v_room[z][g + 8][(u * 4 + t) * WORDS * 4]);
-#pragma unroll
-                for (int w = 0; w < WORDS; ++w) {
-                    v0[w] = at0[w];
-                    v1[w] = at1[w];
-                }
-#pragma unroll
-                for (int w = 0; w < WORDS; w += 2)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_bf16(d[j], v0[w], v1[w], v0[w + 1], v1[w + 1], b[j].v[u][w], b[j].v[u][w + 1]);
-            }
-    }
-    if (n >= p.N)
-        return;
     const bool bf16_base = p.base_dtype == 0, bf16_out = p.out_dtype == 0;
-    auto at = [&](int m) { return static_cast<uint8_t *>(p.out) + ((int64_t)m * p.N + n) * (bf16_out ? 2 : 4); };
-    if (m0 >= 0)
-        put(at(m0), bf16_base, bf16_out, base0, {d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]});
-    if (m1 >= 0)
-        put(at(m1), bf16_base, bf16_out, base1, {d[0][2], d[0][3], d[1][2], d[1][3], d[2][2], d[2][3], d[3][2], d[3][3]});
+    const int tiles = FROM != kSearch ? *p.list : (int)p.M;
+    for (int m = blockIdx.x; m < tiles; m = FROM == kLists ? m + gridDim.x : tiles) {
+        const int adapter = FROM != kSearch ? p.list[1 + m] : adapter_of(p, m);
+        Ranks<UNITS, WORDS> b[4];
+        auto load_b = [&]() {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
+                b[j].load(adapter >= 0 && row < p.N ? p.b + ((int64_t)adapter * p.N + row) * p.R * 2 : nullptr, p.R);
+            }
+        };
+        load_b();   // nothing waits for the tile's rows
+        int mine;
+        if (!tile_of<FROM>(p, m, adapter, mine))
+            continue;
+        const int m0 = __shfl_sync(kFull, mine, g), m1 = __shfl_sync(kFull, mine, g + 8);
+        Base base0, base1;
+        base0.load(p, m0, n);
+        base1.load(p, m1, n);
+        const float none = adapter >= 0 ? 0.0f : -0.0f;   // base + -0 is base
+        float d[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            d[j][0] = d[j][1] = d[j][2] = d[j][3] = none;
+        const float scaling = scaling_of(p, adapter);
+        grid_dependency_wait();
+        allow_dependents();
+        if (adapter >= 0) {
+            for (int i = warp; i < kTile; i += kWarps) {   // a warp to a row
+                const int row = __shfl_sync(kFull, mine, i);
+                for (int r = 2 * lane; r < kRanks; r += 64) {
+                    uint32_t terms[kPlanes];
+                    split(ranks_of(p, row, r, scaling), terms);
+#pragma unroll
+                    for (int z = 0; z < kPlanes; ++z)
+                        *reinterpret_cast<uint32_t *>(&v_room[z][i][r * 2]) = terms[z];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+                for (int z = kPlanes - 1; z >= 0; --z) {
+                    uint32_t v0[WORDS], v1[WORDS];
+                    const uint32_t *at0 = reinterpret_cast<const uint32_t *>(&v_room[z][g][(u * 4 + t) * WORDS * 4]);
+                    const uint32_t *at1 = reinterpret_cast<const uint32_t *>(&v_room[z][g + 8][(u * 4 + t) * WORDS * 4]);
+#pragma unroll
+                    for (int w = 0; w < WORDS; ++w) {
+                        v0[w] = at0[w];
+                        v1[w] = at1[w];
+                    }
+#pragma unroll
+                    for (int w = 0; w < WORDS; w += 2)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_bf16(d[j], v0[w], v1[w], v0[w + 1], v1[w + 1], b[j].v[u][w], b[j].v[u][w + 1]);
+                }
+        }
+        auto at = [&](int m) { return static_cast<uint8_t *>(p.out) + ((int64_t)m * p.N + n) * (bf16_out ? 2 : 4); };
+        if (m0 >= 0 && n < p.N)
+            put(at(m0), bf16_base, bf16_out, base0, {d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]});
+        if (m1 >= 0 && n < p.N)
+            put(at(m1), bf16_base, bf16_out, base1, {d[0][2], d[0][3], d[1][2], d[1][3], d[2][2], d[2][3], d[3][2], d[3][3]});
+        if (FROM == kLists)
+            __syncthreads();   // before v is made again
+    }
+    grid_dependency_wait();   // also without a tile: what follows waits for all before it through this kernel
 }
 
 // ---------------------------------------------------------------- launch --
+// Kernels for few rows alone, for many alone, or both: each tile of 128 rows by the one or the other.  Measured with
+// 4096 x 4096 in us, few / many: 512 rows of one adapter of rank 16 10.4 / 10.8, of rank 64 17.9 / 16.5, 64 adapters at random
+// 15.7 / 107; 1024 rows of one 14.5 / 12.9 and 25.8 / 19.4, of 8 at random 14.9 / 33, of 64 at random 23 / 143; 8192 rows
+// of one of rank 64 161 / 49.  Both, of 64 adapters: 8192 rows of rank 64 in runs of 256 65 (few 170, many 52), at random
+// 220 (185, 1034); 2048 rows 42 (48, 26) and 113 (74, 298), less than few only where rows are in runs.
+enum Way { kFew, kMany, kMixed };
+
+Way way_of(int64_t M, int L)
+{
+    if (M <= 512 || (M <= 2048 && L > kLoraMostAdapters))
+        return kFew;
+    return L <= kLoraMostAdapters || M > kLoraListRows ? kMany : kMixed;
+}
+
 // Parts of K: as many as fill the GPU, at least a unit to a warp of each, or 256
 // columns of many rows.  Tiles are estimated from the sizes alone.
 int splits_of(int64_t M, int K, int L)
 {
-    const bool few = M <= kLoraFewRows;
-    const int64_t tiles = few ? std::min<int64_t>(M, L + M / kTile) : ceil_div(M, 128);
+    const int64_t tiles = way_of(M, L) == kFew ? std::min<int64_t>(M, L + M / kTile) : ceil_div(M, 128);
     const int64_t most = std::min<int64_t>(kLoraMaxSplits, ceil_div(K, 256));
     return (int)std::max<int64_t>(1, std::min<int64_t>(most, kLoraBlocks / std::max<int64_t>(1, tiles)));
 }
 
-template <int NT, int UNITS, int WORDS>
-int launch_few(const Lora &p, cudaStream_t stream)
+size_t list_bytes(int64_t M)
 {
-    const int rc = launch_dependent(lora_shrink_few_kernel<NT>, dim3((unsigned)p.M, p.splits), kThreads, 0, stream, p);
-    if (rc != EP_OK)
-        return rc;
-    return launch_dependent(lora_expand_few_kernel<UNITS, WORDS>,
-                            dim3((unsigned)p.M, (unsigned)ceil_div(p.N, 32 * kWarps)), kThreads, 0, stream, p);
+    return align_up((1 + (size_t)std::min<int64_t>(M, kLoraListRows) * (1 + kTile)) * sizeof(int), kWsAlign);
 }
 
-int launch_few(const Lora &p, cudaStream_t stream)
+// f with the kernels' shapes of a rank as constants: eights of ranks, and units and words of B's.
+template <class F>
+int with_rank(int R, F &&f)
 {
-    if (p.R <= 8)
-        return launch_few<1, 1, 2>(p, stream);
-    if (p.R <= 16)
-        return launch_few<2, 1, 2>(p, stream);
-    if (p.R <= 32)
-        return launch_few<4, 1, 4>(p, stream);
-    return p.R <= 64 ? launch_few<8, 2, 4>(p, stream) : launch_few<16, 4, 4>(p, stream);
+    using std::integral_constant;
+    if (R <= 8)
+        return f(integral_constant<int, 1>(), integral_constant<int, 1>(), integral_constant<int, 2>());
+    if (R <= 16)
+        return f(integral_constant<int, 2>(), integral_constant<int, 1>(), integral_constant<int, 2>());
+    if (R <= 32)
+        return f(integral_constant<int, 4>(), integral_constant<int, 1>(), integral_constant<int, 4>());
+    if (R <= 64)
+        return f(integral_constant<int, 8>(), integral_constant<int, 2>(), integral_constant<int, 4>());
+    return f(integral_constant<int, 16>(), integral_constant<int, 4>(), integral_constant<int, 4>());
+}
+
+// Blocks for a list's tiles, in `pieces` each: as many as it may have; where it may as well have none, no more than
+// run at a time.
+unsigned blocks_of(const Lora &p, int64_t pieces)
+{
+    const int64_t most = std::min<int64_t>(p.M, (int64_t)p.L + 1 + p.M / kTile);
+    return (unsigned)(p.mixed ? std::min<int64_t>(most, ceil_div(2 * kLoraBlocks, pieces)) : most);
+}
+
+int launch_list(const Lora &p, cudaStream_t stream)
+{
+    static PerDevice set;
+    int places = 2 * kSearchRows;
+    while (places < 2 * p.M)
+        places *= 2;
+    const int rc = raise_smem(lora_list_kernel, kLoraListRows * (2 * sizeof(Entry) + sizeof(int)), set);
+    if (rc != EP_OK)
+        return rc;
+    return launch_dependent(lora_list_kernel, dim3(1), kListThreads, places * sizeof(Entry) + p.M * sizeof(int), stream, p,
+                            places);
+}
+
+int launch_shrink_few(const Lora &p, bool list, cudaStream_t stream)
+{
+    return with_rank(p.R, [&](auto nt, auto, auto) {
+        constexpr int NT = decltype(nt)::value;
+        const dim3 grid(list ? blocks_of(p, p.splits) : (unsigned)p.M, p.splits);
+        return launch_dependent(p.mixed ? lora_shrink_few_kernel<NT, kLists> : list ? lora_shrink_few_kernel<NT, kList>
+                                                                                    : lora_shrink_few_kernel<NT, kSearch>,
+                                grid, kThreads, 0, stream, p);
+    });
+}
+
+int launch_expand_few(const Lora &p, bool list, cudaStream_t stream)
+{
+    return with_rank(p.R, [&](auto, auto units, auto words) {
+        constexpr int U = decltype(units)::value, W = decltype(words)::value;
+        const int64_t pieces = ceil_div(p.N, 32 * kWarps);
+        const dim3 grid(list ? blocks_of(p, pieces) : (unsigned)p.M, (unsigned)pieces);
+        return launch_dependent(p.mixed ? lora_expand_few_kernel<U, W, kLists> : list ? lora_expand_few_kernel<U, W, kList>
+                                                                                      : lora_expand_few_kernel<U, W, kSearch>,
+                                grid, kThreads, 0, stream, p);
+    });
+}
+
+int launch_lora(const Lora &p, Way way, cudaStream_t stream)
+{
+    const bool list = p.M > kSearchRows;
+    int rc = way != kMany && list ? launch_list(p, stream) : EP_OK;
+    if (rc == EP_OK && way != kMany)
+        rc = launch_shrink_few(p, list, stream);
+    if (rc == EP_OK && way != kFew)
+        rc = launch_lora_shrink_many(p, stream);
+    if (rc == EP_OK && way != kMany)
+        rc = launch_expand_few(p, list, stream);
+    if (rc == EP_OK && way != kFew)
+        rc = launch_lora_expand_many(p, stream);
+    return rc;
 }
 
 }  // namespace
@@ -375,7 +565,7 @@ extern "C" size_t ep_lora_workspace_size(int64_t M, int R)
         return 0;
     // splits_of(m) * m is at most this for every m <= M, so that a workspace serves smaller batches too
     const int64_t rows = std::min<int64_t>(kLoraMaxSplits * M, std::max<int64_t>(M, (int64_t)kLoraBlocks * 128));
-    return align_up((size_t)rows * R * sizeof(float), kWsAlign) + kWsAlign;
+    return list_bytes(M) + align_up((size_t)rows * R * sizeof(float), kWsAlign) + kWsAlign;
 }
 
 extern "C" int ep_lora(const void *x, int64_t M, int K, const int64_t *ids, const void *a, const void *b,
@@ -386,7 +576,7 @@ extern "C" int ep_lora(const void *x, int64_t M, int K, const int64_t *ids, cons
     if (M < 0 || K < 8 || K % 8 != 0 || N < 8 || N % 8 != 0 || R < 8 || R % 8 != 0 || L < 1)
         return EP_ERR_INVALID_ARG;
     if ((out_dtype != 0 && out_dtype != 1) || (base != nullptr && base_dtype != 0 && base_dtype != 1) || R > kLoraMaxRank ||
-        K > (1 << 24) || N > (1 << 24) || M > (1 << 24))
+        K > (1 << 23) || N > (1 << 23) || M > (1 << 24))
         return EP_ERR_UNSUPPORTED;
     if (M == 0)
         return EP_OK;
@@ -396,7 +586,8 @@ extern "C" int ep_lora(const void *x, int64_t M, int K, const int64_t *ids, cons
         !aligned(ws, kWsAlign) || ws_bytes < ep_lora_workspace_size(M, R))
         return EP_ERR_INVALID_ARG;
     const Lora p{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(a), static_cast<const uint8_t *>(b), ids,
-                 scaling, base, out, M, K, N, R, L, splits_of(M, K, L), base_dtype, out_dtype, static_cast<float *>(ws),
-                 err};
-    return M <= kLoraFewRows ? launch_few(p, stream) : launch_lora_many(p, stream);
+                 scaling, base, out, M, K, N, R, L, splits_of(M, K, L), base_dtype, out_dtype,
+                 reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + list_bytes(M)), static_cast<int *>(ws),
+                 way_of(M, L) == kMixed, err};
+    return launch_lora(p, way_of(M, L), stream);
 }

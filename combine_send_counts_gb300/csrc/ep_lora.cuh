@@ -9,7 +9,8 @@
 
 namespace ep {
 
-constexpr int kLoraFewRows = 1024;      // most of the kernels for few rows
+constexpr int kLoraListRows = 8192;     // most of the kernels for few rows
+constexpr int kLoraTile = 16;           // rows of their tiles
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxSplits = 16;      // parts of K
 constexpr int kLoraBlocks = 2 * 152;    // that fill the GPU
@@ -24,6 +25,8 @@ struct Lora {
     int64_t M;
     int K, N, R, L, splits, base_dtype, out_dtype;
     float *parts;                    // [splits][M][R]
+    int *list;                       // tiles of few rows: their number; [M] adapters; [M][kLoraTile] rows, or -1
+    int mixed;                       // the 128-row tiles of many adapters are among them
     int32_t *err;
 };
 
@@ -64,30 +67,6 @@ __device__ __forceinline__ float2 ranks_of(const Lora &p, int64_t m, int r, floa
     return make_float2(__fmul_rn(v.x, scaling), __fmul_rn(v.y, scaling));
 }
 
-// Four of them, r % 4 == 0.
-__device__ __forceinline__ float4 four_ranks_of(const Lora &p, int64_t m, int r, float scaling)
-{
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (m < 0 || r >= p.R)
-        return v;
-    const float4 *part = reinterpret_cast<const float4 *>(p.parts + m * p.R + r);
-    const int64_t next = p.M * p.R / 4;
-    for (int z = 0; z < p.splits; z += 4) {
-        float4 u[4];   // loaded together
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = z + i < p.splits ? part[(z + i) * next] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v.x = __fadd_rn(v.x, u[i].x);
-            v.y = __fadd_rn(v.y, u[i].y);
-            v.z = __fadd_rn(v.z, u[i].z);
-            v.w = __fadd_rn(v.w, u[i].w);
-        }
-    }
-    return make_float4(__fmul_rn(v.x, scaling), __fmul_rn(v.y, scaling), __fmul_rn(v.z, scaling), __fmul_rn(v.w, scaling));
-}
-
 // Two values as sums of kPlanes bf16 terms each: the first eight bits, the next and the last, by cutting, which is
 // exact.  What is left of an infinity or NaN is nothing.
 __device__ __forceinline__ void split(float2 v, uint32_t (&w)[kPlanes])
@@ -121,7 +100,31 @@ __device__ __forceinline__ float scaling_of(const Lora &p, int adapter)
                ? 1.0f : __uint_as_float(ld_global(reinterpret_cast<const uint32_t *>(p.scaling) + adapter));
 }
 
-// The two kernels for more than kLoraFewRows rows.
-int launch_lora_many(const Lora &p, cudaStream_t stream);
+constexpr int kLoraWide = 128;        // rows of a tile of the kernels for many rows
+constexpr int kLoraMostAdapters = 8;  // that it may name if p.mixed
+constexpr int kNoRow = 0x7fffffff;    // the adapter of a row past the end
+
+// The least adapter above `last` among a tile's rows, four to a lane; kNoRow if there is none.  The same in every lane.
+__device__ __forceinline__ int next_adapter(const int (&ids)[kLoraWide / 32], int last)
+{
+    int least = kNoRow;
+#pragma unroll
+    for (int i = 0; i < kLoraWide / 32; ++i)
+        least = ids[i] > last ? min(least, ids[i]) : least;
+    return __reduce_min_sync(kFull, least);
+}
+
+// Whether a tile names more than kLoraMostAdapters.
+__device__ __forceinline__ bool many_adapters(const int (&ids)[kLoraWide / 32])
+{
+    int last = -1;
+    for (int i = 0; i <= kLoraMostAdapters && last != kNoRow; ++i)
+        last = next_adapter(ids, last);
+    return last != kNoRow;
+}
+
+// The two kernels for many rows.
+int launch_lora_shrink_many(const Lora &p, cudaStream_t stream);
+int launch_lora_expand_many(const Lora &p, cudaStream_t stream);
 
 }  // namespace ep

@@ -40,9 +40,7 @@ __device__ __forceinline__ void tensor_free(uint32_t at, int columns)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
 }
 
-// D (+)= A B^T, one step of 16 of K; one thread, in a warp that is otherwise of one mind: what the operands are made of
-// has to be uniform for the compiler too, as they go by uniform registers (in code that one lane ran alone, a step took
-// 80 cycles to issue, done or skipped).
+// D (+)= A B^T, one step of 16 of K; one thread.
 __device__ __forceinline__ void tensor_step(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -68,6 +66,23 @@ __device__ __forceinline__ void tensor_copy(uint32_t to, const CUtensorMap *map,
                  ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
                  : "memory");
 }
+
+// A box from a tile at shared-memory address `from` to (x, y, z) on of a tensor map, what lies past its edges left out; one
+// thread, which then commits it to a group of its own.  No coordinate is negative.
+__device__ __forceinline__ void tensor_store(const CUtensorMap *map, uint32_t from, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(from)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+// All but this thread's last N groups of stores have been read from shared memory; or are done.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Makes this thread's writes to shared memory visible to matrix steps (and bulk copies) that are ordered behind it.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

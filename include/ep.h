@@ -722,7 +722,7 @@ int ep_router_select_backward(const void *logits, int dtype, int64_t T, int E, c
  *     zeros.  out [M,N] bf16 (out_dtype 0) or fp32 (1); may be base if the types
  *     are the same.
  * Sums are fp32; the result is rounded once.
- *   K, N, R % 8 == 0, R <= 128; M, K, N <= 2^24 (else EP_ERR_UNSUPPORTED).
+ *   K, N, R % 8 == 0, R <= 128; M <= 2^24, K, N <= 2^23 (else EP_ERR_UNSUPPORTED).
  *   Up to 1024 rows may name adapters in any order; with more, rows of one adapter
  *   are best neighbours (128 rows are gone over once for each two to four adapters
  *   among them).  An adapter's infinities and NaN stay its own rows'.

@@ -151,3 +151,52 @@ def test_smaller_batches_than_the_workspace_is_for():
         want, tol = r.lora64(x[:M], ids[:M], a, b, s, y[:M])
         r.inside(got, want, tol)
     assert plan(x[:0], ids[:0], y[:0]).shape == (0, 128)
+
+
+@pytest.mark.parametrize("M,K,N,L,R", [(65, 72, 264, 40, 16), (130, 264, 40, 130, 24), (513, 64, 72, 9, 8),
+                                       (700, 136, 264, 200, 64), (2048, 72, 40, 3000, 16), (2049, 264, 136, 20, 32),
+                                       (2500, 64, 264, 9, 128), (8192, 72, 136, 70, 16), (8192, 64, 40, 9, 64),
+                                       (8193, 64, 72, 24, 8)])
+@pytest.mark.parametrize("base,out", [("bf16", "bf16"), ("fp32", "bf16")])
+@pytest.mark.parametrize("how", ["both", "turns", "last"])
+def test_long_requests_beside_short_ones(M, K, N, L, R, base, out, how):
+    g = f.gen(M + K + N + R + L)
+    x, ids, a, b, s, y = inputs(M, K, N, L, R, base, "random", g)
+    if how == "both":       # one adapter for a stretch of rows, and another for the next
+        ids[M // 8:M // 2] = L - 1
+        ids[M // 2:M // 2 + 300] = 0
+    elif how == "turns":    # eight adapters in turn, one more in some rows
+        ids = torch.arange(M, device="cuda") % min(8, L)
+        ids[::300] = L - 1
+    else:                   # none but the last rows
+        ids[:M - 5] = -1
+    plan = ep.LoraAdapters(a, b, s, max_tokens=M, out_dtype=TYPES[out])
+    got = plan(x, ids, y)
+    want, tol = r.lora64(x, ids, a, b, s, y)
+    assert int(plan.err.item()) == 0
+    r.inside(got, want, tol)
+    assert torch.equal(plan(x, ids, y), got)   # though a list's order is as it comes
+    if base == out:
+        assert torch.equal(plan(x, ids, y, out=y), got)
+
+
+def test_a_graph_of_long_and_short_requests_with_other_ids():
+    M, L = 3000, 40
+    g = f.gen(5)
+    x, ids, a, b, s, y = inputs(M, 264, 136, L, 16, "bf16", "random", g)
+    plan = ep.LoraAdapters(a, b, s, max_tokens=M)
+    runs = ids[:M // 100 + 1].repeat_interleave(100)[:M].contiguous()
+    want = [plan(x, i, y).clone() for i in (ids, runs)]
+    mine, out = ids.clone(), torch.empty_like(want[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan(x, mine, y, out=out)
+    for i, w in zip((ids, runs, ids), (want[0], want[1], want[0])):
+        mine.copy_(i)
+        graph.replay()
+        assert torch.equal(out, w)
+    bad = runs.clone()
+    bad[2999] = L
+    plan(x, bad, y)
+    assert int(plan.err.item()) == ep.EP_ERR_INVALID_EXPERT
