@@ -6,7 +6,9 @@
 //   with rs = (mean(h^2) + eps)^-1/2, n = h rs, g = dy.
 //
 // Bound by HBM: every element is read once and written once, its row being
-// held in a block's registers between the sum of squares and its use.
+// held in registers between the sum of squares and its use.  Measured (of a copy's 6.78
+// TB/s): 16384 rows of 7168 with a residual to sum, result and codes 163 us (6.5 TB/s), their
+// backward pass 141 us (6.6 TB/s).  Of few rows a call is its launches: 1 row 2.3 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -153,7 +155,8 @@ __device__ __forceinline__ float half_warp_max(float m)
     return m;
 }
 
-// A group of 128: `top` is the largest magnitude of h w, and y = h w rs.
+// A group of 128 columns and its scale, which each of the 16 lanes that hold them makes for itself.  (Made once by one lane,
+// with h w held meanwhile: 195 us instead of 165 for 16384 rows of 7168; with IEEE divisions 169.)  `top` is the largest magnitude of h w, and y = h w rs.
 struct Group {
     float scale, of;        // scale; a column's value in codes is about h w * of
     float top, back;        // top, or 0 where values are y's own; about 1 / top
@@ -197,22 +200,28 @@ struct Group {
 // Two columns of eight.
 __device__ __forceinline__ float2 pair(const float (&f)[8], int j) { return make_float2(f[2 * j], f[2 * j + 1]); }
 
+// A block to a row, or (MOST == 0) a warp, which needs no barrier.
+constexpr int kRowsOfWarps = 8;
+
 template <int RES, int NV, int SF, int MOST>
-__global__ void __launch_bounds__(MOST)
+__global__ void __launch_bounds__(MOST == 0 ? 32 * kRowsOfWarps : MOST)
 norm_kernel(Norm a)
 {
     constexpr int SUM = RES == kNone ? kBf16 : RES;   // what the sum is held in
     __shared__ float s[2 * 32];
-    const int64_t row = (int64_t)blockIdx.x * a.H;
+    const int tid = MOST == 0 ? threadIdx.x & 31 : threadIdx.x, width = MOST == 0 ? 32 : blockDim.x;
+    const int64_t t = MOST == 0 ? (int64_t)blockIdx.x * kRowsOfWarps + (threadIdx.x >> 5) : blockIdx.x, row = t * a.H;
     grid_dependency_wait();
     allow_dependents();
+    if (MOST == 0 && t >= a.T)
+        return;
     Eight<SUM> h[NV];
     {
         Eight<kBf16> x[NV];
         Eight<RES> r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * 8;
+            const int c = (i * width + tid) * 8;
             x[i].load(a.x, row + c, c < a.H);
             r[i].load(a.residual, row + c, c < a.H);
         }
@@ -232,7 +241,7 @@ norm_kernel(Norm a)
     float2 both = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * 8;
+        const int c = (i * width + tid) * 8;
         float f[8];
         h[i].get(f);
 #pragma unroll
@@ -241,15 +250,21 @@ norm_kernel(Norm a)
         if (a.sum != nullptr && c < a.H)
             h[i].store(a.sum, row + c);
     }
-    int phase = 0;
     float squares[1] = {__fadd_rn(both.x, both.y)};
-    block_sums(squares, s, phase);
+    if (MOST == 0) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            squares[0] = __fadd_rn(squares[0], __shfl_xor_sync(kFull, squares[0], o));
+    } else {
+        int phase = 0;
+        block_sums(squares, s, phase);
+    }
     const float rs = inverse_root(squares[0], a.H, a.eps);
     const int groups = a.H >> 7;
-    const int64_t base = SF < 0 ? 0 : scale_row_base<SF < 0 ? 0 : SF>(a.scale, blockIdx.x, groups);
+    const int64_t base = SF < 0 ? 0 : scale_row_base<SF < 0 ? 0 : SF>(a.scale, t, groups);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * 8;
+        const int c = (i * width + tid) * 8;
         float f[8], w[8], y[8], m = 0.0f;
         h[i].get(f);
         load_weights(a.w, a.w_dtype, c, c < a.H, w);
@@ -275,7 +290,7 @@ norm_kernel(Norm a)
                 p[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(group.value(pair(f, j), pair(y, j)), __NV_SATFINITE, __NV_E4M3);
             if (c < a.H) {
                 st_stream(reinterpret_cast<uint2 *>(a.q + row + c), make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16));
-                if ((threadIdx.x & 15) == 0)
+                if ((tid & 15) == 0)
                     put_scale<SF < 0 ? 0 : SF>(a.scale, base, c >> 7, group.scale, group.code);
             }
         }
@@ -292,6 +307,7 @@ struct NormBackward {
 };
 
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ...; the block's part of dw stays in registers.
+// For rows of more than 16384 columns, of which shared memory does not hold two.
 template <int RES, int NV, int MOST>
 __global__ void __launch_bounds__(MOST)
 norm_backward_kernel(NormBackward a)
@@ -373,7 +389,8 @@ norm_backward_kernel(NormBackward a)
 
 // The same for rows of up to 16384 columns: rows are copied ahead of their use into
 // a ring in shared memory, of which each thread fills and reads its own slots, so
-// that the copies go on through the block's sums.
+// that the copies go on through the block's sums.  (With the rows loaded when their turn
+// comes, 16384 rows of 7168 took 240 us instead of 142.)
 template <int RES>
 struct Slot {
     static constexpr int kPieces = RES == kFp32 ? 5 : 3;   // 16 bytes each: dy, then h, then dres
@@ -501,7 +518,8 @@ norm_backward_ring_kernel(NormBackward a)
     }
 }
 
-// dw: the blocks' parts added in their order, 32 columns to a block, 16 runs of parts side by side.
+// dw: the blocks' parts added in their order, 32 columns to a block, 16 runs of parts side by side.  (Parts loaded 4 to 16 at
+// a time: no faster.)
 constexpr int kJoinRuns = 16;
 
 __global__ void __launch_bounds__(32 * kJoinRuns)
@@ -525,53 +543,52 @@ norm_join_kernel(const float *partial, int parts, int H, float *dw)
     }
 }
 
-// Vectors of 8 columns a thread, and threads: one where rows are few or short, as a row's latency is all there.
-struct Shape {
-    int vectors, threads;
-};
-
-Shape shape_of(int H, bool few)
-{
-    const int v = H / 8;
-    const int n = v <= 1024 && (few || v <= 128) ? 1 : kMostVectors;
-    return {n, (int)align_up(ceil_div(v, n), 32)};
-}
-
-// f with the number of vectors and the most threads of its kernel as constants.
+// f with the number of vectors of 8 columns a thread and the most threads of its kernel as constants, and the threads.
+// Where rows are few, as many threads as there are vectors, as a row's latency is all there is: 1 row of 7168 2.3 us, with
+// four vectors a thread 3.3.  With more, four: 16384 rows of 7168 163 us, with one 257.  Rows of up to 512 columns a warp
+// each: 16384 rows of 512 13.4 us, of 256 6.5, with a block to a row 17.1 and 17.0; of 1024 25.0 both ways, 4096 of them
+// 8.6 by warps and 7.9 by blocks of one vector a thread (8.7 of four).
 template <class F>
-int with_shape(const Shape &s, F &&f)
+int with_shape(int H, bool few, F &&f)
 {
-    if (s.vectors == 1)
-        return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1024>());
-    if (s.threads <= 256)
-        return f(std::integral_constant<int, kMostVectors>(), std::integral_constant<int, 256>());
-    return f(std::integral_constant<int, kMostVectors>(), std::integral_constant<int, 1024>());
+    using std::integral_constant;
+    const int v = H / 8;
+    if (v <= 1024 && (few || (v > 64 && v <= 128)))
+        return f(integral_constant<int, 1>(), integral_constant<int, 1024>(), (int)align_up(v, 32));
+    if (v <= 32)
+        return f(integral_constant<int, 1>(), integral_constant<int, 0>(), 32 * kRowsOfWarps);
+    if (v <= 64)
+        return f(integral_constant<int, 2>(), integral_constant<int, 0>(), 32 * kRowsOfWarps);
+    const int threads = (int)align_up(ceil_div(v, kMostVectors), 32);
+    if (threads <= 256)
+        return f(integral_constant<int, kMostVectors>(), integral_constant<int, 256>(), threads);
+    return f(integral_constant<int, kMostVectors>(), integral_constant<int, 1024>(), threads);
 }
 
 template <int RES>
 int launch_norm(const Norm &a, cudaStream_t stream)
 {
-    const Shape s = shape_of(a.H, a.T <= kSMs);
-    return with_shape(s, [&](auto nv, auto most) {
+    return with_shape(a.H, a.T <= kSMs, [&](auto nv, auto most, int threads) {
         constexpr int NV = decltype(nv)::value, MOST = decltype(most)::value;
-        const dim3 grid((unsigned)a.T);
+        const dim3 grid((unsigned)(MOST == 0 ? ceil_div(a.T, kRowsOfWarps) : a.T));
         if (a.q == nullptr)
-            return launch_dependent(norm_kernel<RES, NV, -1, MOST>, grid, s.threads, 0, stream, a);
+            return launch_dependent(norm_kernel<RES, NV, -1, MOST>, grid, threads, 0, stream, a);
         switch (a.scale.fmt) {
         case EP_SCALE_ROW_F32:
-            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_ROW_F32, MOST>, grid, s.threads, 0, stream, a);
+            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_ROW_F32, MOST>, grid, threads, 0, stream, a);
         case EP_SCALE_COL_F32:
-            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_COL_F32, MOST>, grid, s.threads, 0, stream, a);
+            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_COL_F32, MOST>, grid, threads, 0, stream, a);
         default:
-            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_COL_UE8M0, MOST>, grid, s.threads, 0, stream, a);
+            return launch_dependent(norm_kernel<RES, NV, EP_SCALE_COL_UE8M0, MOST>, grid, threads, 0, stream, a);
         }
     });
 }
 
 // The ring's blocks: a thread for each eight columns, or for each sixteen of more
-// than 8192; as many blocks to an SM as make 1024 threads.  (Sixteen columns a
-// thread for 7168, in two blocks, spilled and took 242 us instead of 142.)  Three rows
-// ahead where they fit, or two.
+// than 8192; as many blocks to an SM as make 1024 threads, eight at most (with 16, 3000 rows of
+// 256 took 9.2 us instead of 7.0, for the parts of dw).  Sixteen columns a
+// thread for 7168, in two blocks, spilled and took 242 us instead of 142.  Three rows
+// ahead where they fit, or two: 142 and 151 us.
 struct Ring {
     int vectors, threads, blocks;
 };
@@ -622,7 +639,7 @@ int launch_norm_backward(const NormBackward &a, cudaStream_t stream)
     if (a.H <= 16384 && 2 * row * r.blocks <= kMostShared)
         return launch_ring<RES, 2>(a, r, stream);
     return launch_dependent(norm_backward_kernel<RES, kMostVectors, 1024>, dim3((unsigned)parts_of(a.T, a.H)),
-                            shape_of(a.H, false).threads, 0, stream, a);
+                            (int)align_up(ceil_div(a.H / 8, kMostVectors), 32), 0, stream, a);
 }
 
 bool rows_ok(const void *p) { return p == nullptr || aligned(p, 16); }

@@ -205,3 +205,16 @@ def test_backward_in_place():
         a, b, dw = dy.clone(), dres.clone(), torch.empty(H, device="cuda")
         ep.ep_add_rms_norm_backward(a, h, b, 0, T, H, w, 0, 1e-6, b if over == "dres" else a, None, dw, ws)
         assert torch.equal(b if over == "dres" else a, want["dx"]) and torch.equal(dw, want["dweight"])
+
+
+@pytest.mark.parametrize("T,H", [(153, 8), (161, 256), (1001, 264), (155, 504), (999, 512), (154, 520), (1000, 1024)])
+@pytest.mark.parametrize("residual", [None, "bf16", "fp32"])
+def test_many_short_rows(T, H, residual):
+    test_norm(T, H, residual, "bf16")
+
+
+@pytest.mark.parametrize("T,H", [(153, 128), (999, 384), (1001, 512), (161, 256), (1000, 640)])
+@pytest.mark.parametrize("fmt", [ep.EP_SCALE_ROW_F32, ep.EP_SCALE_COL_F32, ep.EP_SCALE_COL_UE8M0])
+@pytest.mark.parametrize("residual", [None, "fp32"])
+def test_eight_bits_of_many_short_rows(T, H, fmt, residual):
+    test_eight_bits(T, H, fmt, residual)
