@@ -10,10 +10,10 @@
 //     memory's sums are taken into registers after every 128 columns and added there
 //     with IEEE operations, as a long chain of matrix steps loses bits.
 //   expand: v is made once for a tile, as three bf16 terms, and stays in shared
-//     memory; B comes 64 or 128 columns at a time, up to four chunks ahead; the base comes
+//     memory; B comes 64 or 128 columns at a time, up to three chunks ahead; the base comes
 //     in boxes of 32 rows and 32 columns through a ring of each warp's own, where the sums
-//     are added to it and from where they leave as such a box, or row by row where some of
-//     the 32 rows are another pass's.
+//     are added to it and from where they leave as such a box (by tensor maps), or in pieces
+//     of rows where some of the 32 are another pass's.
 //
 // Measured with 8192 rows of 8 adapters of rank 64, 7168 x 4096, bf16: shrink 25 us (the bytes
 // of x alone: 17), expand 37 (base and result: 20), of which making v from its parts takes 4.
@@ -23,8 +23,7 @@
 // 2500.  Eight warps of 64 columns instead of 16 of 32: 66 us in all instead of 62.
 //
 // x, A and B come by TMA (tensor maps of x [M,K], A [L,R,K] and B [L,N,R], whose
-// edges read as zeros) with the 128-byte swizzle that the matrix steps take, and so do base and
-// result (which stay as they are past the edges).  Copied by
+// edges read as zeros) with the 128-byte swizzle that the matrix steps take.  Copied by
 // cp.async instead, with a proxy fence by the threads that copied, both kernels waited
 // at that fence for the copies still in flight.  Waits on barriers give up after a
 // second or so (EP_ERR_TIMEOUT).
@@ -322,7 +321,7 @@ struct Expand {
     static constexpr int kSumWarps = kN / 8, kThreads = kSumWarps * 32 + 32;   // 32 rows and 32 columns to a warp
     static constexpr int kV = kRows * 128;                                     // a term of v, 64 ranks
     static constexpr int kB = kN * 128;                                        // a stage of B, 64 ranks
-    static constexpr int kBaseRow = 32 * BASE, kOutRow = 32 * OUT;       // bytes
+    static constexpr int kBaseRow = 32 * BASE, kOutRow = 32 * OUT;             // bytes
     static constexpr int kRoom = 32 * (BASE > OUT ? kBaseRow : kOutRow);       // a warp's stage
     static constexpr int kFixed = kPlanes * kRuns * kV + kBStages * kRuns * kB + 1024;
     static constexpr int kFit = (225 * 1024 - kFixed) / (kSumWarps * kRoom);

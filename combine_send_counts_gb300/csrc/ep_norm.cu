@@ -155,8 +155,9 @@ __device__ __forceinline__ float half_warp_max(float m)
     return m;
 }
 
-// A group of 128 columns and its scale, which each of the 16 lanes that hold them makes for itself.  (Made once by one lane,
-// with h w held meanwhile: 195 us instead of 165 for 16384 rows of 7168; with IEEE divisions 169.)  `top` is the largest magnitude of h w, and y = h w rs.
+// A group of 128 columns, of which `top` is the largest magnitude of h w; y = h w rs.  Each of the 16 lanes that hold it makes
+// the scale for itself: made once by one lane, with h w held meanwhile, 16384 rows of 7168 took 195 us instead of 165; with
+// IEEE divisions 169.
 struct Group {
     float scale, of;        // scale; a column's value in codes is about h w * of
     float top, back;        // top, or 0 where values are y's own; about 1 / top

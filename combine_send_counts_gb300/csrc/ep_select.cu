@@ -9,6 +9,10 @@
 //
 // Keys and marks are compared as they come out in 64 bits: with a million
 // scores in a batch some two are nearer than fp32 tells apart.
+//
+// Measured: 1 token 3.1 us; 16384 tokens of 256 experts (sigmoid, bias, 4 of 8 groups by the
+// sum of two, 8 chosen) 17.6 us, where the bytes are 2.7: some 870 instructions of a warp
+// a token, issued at 70% of what an SM can; the backward pass of as many (softmax) 9.5 us, 3.7 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -80,7 +84,8 @@ __device__ __forceinline__ double block_reduce64(double v, double *s)
     return v;
 }
 
-// Any number of experts: a block per token, all keys in 64 bits in shared memory.
+// Any number of experts: a block per token, all keys in 64 bits in shared memory.  Bound by the 64-bit exponentials, of which
+// an SM has few units: 16384 tokens of 256 experts took 653 us so, and 17.6 by warps in fp32.
 __global__ void __launch_bounds__(kThreads)
 select_kernel(Choice c)
 {
@@ -433,6 +438,7 @@ __device__ __forceinline__ void ld_share(const void *p, int dtype, int64_t row, 
 __device__ __forceinline__ float most_of(float v, float off) { return __fadd_rn(v, __fmaf_rn(2 * kU, fabsf(v), off)); }
 __device__ __forceinline__ float least_of(float v, float off) { return __fsub_rn(v, __fmaf_rn(2 * kU, fabsf(v), off)); }
 
+// Registers for eight blocks to an SM: 17.5 us for 16384 tokens of 256 experts; for 7, 6 or 5 of them 18.0, 18.8 and 18.7.
 template <int C, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kThreads, C <= 8 ? 8 : 5)
 select_warp_kernel(const __grid_constant__ Choice c, int size, int log_per, int wide)
@@ -703,7 +709,8 @@ __device__ __forceinline__ void st_logit(void *p, int dtype, int64_t at, float v
 
 // A warp per token, lane k with slot k.  First what every logit gets, then the
 // chosen ones over it.  PIECES > 0: the row stays in registers, four neighbours of
-// each 128 to a lane; 0: any number of experts, the row read as often as needed.
+// each 128 to a lane; 0: any number of experts, the row read as often as needed (16384 tokens
+// of 256 experts: 9.5 and 17.2 us).
 template <int PIECES>
 __global__ void __launch_bounds__(kThreads)
 select_backward_kernel(Backward b)
@@ -850,6 +857,7 @@ int launch_choice(const Choice &c, cudaStream_t stream)
     while (log_per > 0 && (c.groups << log_per) > 32)
         --log_per;
     const int size = c.E / c.groups, share = (int)ceil_div(size, 1 << log_per);
+    // sixteen experts to a lane at most, which keeps a lane's keys in registers and its masks in 32 bits
     if ((c.groups << log_per) <= 32 && share <= 16) {
         const dim3 grid((unsigned)ceil_div(c.T, kWarps));
         const int wide = size % 4 != 0 ? 0 : (aligned(c.logits, c.dtype == 0 ? 16 : 8) ? 1 : 0) | (aligned(c.bias, 16) ? 2 : 0);
