@@ -9,7 +9,7 @@
 
 namespace ep {
 
-constexpr int kLoraListRows = 8192;     // most of the kernels for few rows
+constexpr int kLoraListRows = 8192;     // most of a list
 constexpr int kLoraTile = 16;           // rows of their tiles
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxSplits = 16;      // parts of K
