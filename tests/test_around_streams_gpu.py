@@ -203,3 +203,68 @@ def test_a_chain_without_waits_gives_the_bits_of_one_with_them(big):
             chain(q, out, False)
         torch.cuda.synchronize()
         assert all(same(a, b) for a, b in zip(apart, together))
+
+
+def listed(g, M, L, R=16):
+    """Rows of many adapters, in lists; of 3000, half are one adapter's instead."""
+    K, N = 512, 520
+    a, b = f.randn((L, R, K), g, K ** -0.5), f.randn((L, N, R), g, R ** -0.5)
+    x, y = f.randn((M, K), g), f.randn((M, N), g)
+    ids = torch.randint(-1, L, (M,), generator=g, device="cuda")
+    if M == 3000:
+        ids[:M // 2] = 3
+    plan = ep.LoraAdapters(a, b, max_tokens=M)
+    return lambda **kw: (plan(x, ids, y, **kw),)
+
+
+@pytest.mark.parametrize("M,L", [(300, 40), (1500, 12), (3000, 40), (9000, 12)])
+@pytest.mark.parametrize("other", [lora, lora64, lora128, None])
+def test_lists_and_another_stream_at_once(M, L, other):
+    calls = [listed(f.gen(5), M, L), listed(f.gen(6), 3000, 12, 64) if other is None else other(f.gen(7), True)]
+    want = [c() for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(LONG // 20)
+    got = [[], []]
+    for _ in range(10):
+        for i, (c, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(c())
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(same(v, want[i]) for v in got[i])
+
+
+def test_one_workspace_for_a_chain_of_lists():
+    # each call reads what the one before wrote, over the same list and parts, whose tiles are others each time
+    g = f.gen(8)
+    H, L, R = 512, 30, 16
+    a, b = f.randn((L, R, H), g, H ** -0.5), f.randn((L, H, R), g, 0.1)
+    x = f.randn((9000, H), g)
+    plan = ep.LoraAdapters(a, b, max_tokens=9000)
+    sizes = [1, 9000, 64, 65, 3000, 512, 700, 2049, 20, 8193, 100, 2048, 4096, 3]
+    ids = []
+    for i, M in enumerate(sizes):
+        v = torch.randint(-1, L, (M,), generator=g, device="cuda")
+        if i % 3 == 1:
+            v = v[:M // 60 + 1].repeat_interleave(60)[:M].contiguous()
+        elif i % 3 == 2:
+            v[M // 3:] = L - 1
+        ids.append(v)
+
+    def run(wait):   # nothing but the plan's own kernels between two calls
+        h, k = x.clone(), torch.empty_like(x)
+        k.copy_(x)
+        for v in ids * 2:
+            m = v.shape[0]
+            plan(h[:m], v, k[:m], out=k[:m])
+            h, k = k, h
+            if wait:
+                torch.cuda.synchronize()
+        return h, k
+
+    want = run(True)
+    for _ in range(5):
+        assert same(run(False), want)
