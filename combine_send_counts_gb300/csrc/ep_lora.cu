@@ -467,11 +467,13 @@ Way way_of(int64_t M, int L)
 }
 
 // Parts of K: as many as fill the GPU, at least a unit to a warp of each, or 256
-// columns of many rows.  Tiles are estimated from the sizes alone.
-int splits_of(int64_t M, int K, int L)
+// columns of many rows, and no more than are worth reading again by each block of expand:
+// 1 row of rank 16 takes 4.8 us with up to 8 and 5.2 with 16, 1024 rows of rank 64 18.6 and 20.3
+// (20.1 with 4); 4096 rows of rank 128 47 with 4 and 55 with 8.  Tiles are estimated from the sizes alone.
+int splits_of(int64_t M, int K, int L, int R)
 {
     const int64_t tiles = way_of(M, L) == kFew ? std::min<int64_t>(M, L + M / kTile) : ceil_div(M, 128);
-    const int64_t most = std::min<int64_t>(kLoraMaxSplits, ceil_div(K, 256));
+    const int64_t most = std::min<int64_t>(way_of(M, L) != kFew && R > 64 ? 4 : kLoraMaxSplits, ceil_div(K, 256));
     return (int)std::max<int64_t>(1, std::min<int64_t>(most, kLoraBlocks / std::max<int64_t>(1, tiles)));
 }
 
@@ -595,7 +597,7 @@ extern "C" int ep_lora(const void *x, int64_t M, int K, const int64_t *ids, cons
                      static_cast<const uint8_t *>(b), ids + m, scaling,
                      base == nullptr ? nullptr : static_cast<const uint8_t *>(base) + m * N * (base_dtype == 0 ? 2 : 4),
                      static_cast<uint8_t *>(out) + m * N * (out_dtype == 0 ? 2 : 4), rows, K, N, R, L,
-                     splits_of(rows, K, L), base_dtype, out_dtype,
+                     splits_of(rows, K, L, R), base_dtype, out_dtype,
                      reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + list_bytes(rows)), static_cast<int *>(ws),
                      way == kMixed, err};
         const int rc = launch_lora(p, way, stream);

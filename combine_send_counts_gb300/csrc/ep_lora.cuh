@@ -12,7 +12,7 @@ namespace ep {
 constexpr int kLoraListRows = 8192;     // most of a list
 constexpr int kLoraTile = 16;           // rows of their tiles
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraMaxSplits = 16;      // parts of K
+constexpr int kLoraMaxSplits = 8;       // parts of K
 constexpr int kLoraBlocks = 2 * 152;    // that fill the GPU
 constexpr int kPlanes = 3;              // bf16 terms of v
 
