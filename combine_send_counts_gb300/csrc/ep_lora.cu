@@ -246,8 +246,11 @@ __device__ __forceinline__ void leave(const Lora &p, const float (&acc)[NT][4], 
 }
 
 // A block takes tiles of a list (or one, without) and a part of K, its warps an eighth of that each.
+// Registers for two blocks to an SM up to rank 64, which fill it with loads: 2048 rows of 64 adapters of rank 64 in 57 us
+// instead of 76, as the compiler by itself left room for one, and 24 of rank 16 in 5.6 instead of 6.8, where it left
+// some for four.  Lists of long batches, of rank 16, are faster with four: 8192 rows 106 us, with two 131.
 template <int NT, int FROM>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, FROM == kLists && NT <= 2 ? 4 : NT <= 8 ? 2 : 1)
 lora_shrink_few_kernel(Lora p)
 {
     __shared__ __align__(16) float kept[kWarps / 2][NT * 32 * 4];
@@ -372,8 +375,10 @@ __device__ __forceinline__ void put(void *out, bool bf16_base, bool bf16_out, co
 // Column g of block j of a warp's 32 stands for column n0 + 8 (g / 2) + 2 j + g % 2, so that a
 // lane ends up with eight neighbouring columns of each of its rows.  The block makes v once, in
 // shared memory.
+// Registers for three blocks to an SM up to rank 32, two of more: 2048 rows of 9 adapters of rank 16 in 25 us with three and 29
+// with as many as the compiler takes, of rank 128 66 with two and 87; of rank 64 41 either way.
 template <int UNITS, int WORDS, int FROM>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, UNITS == 1 ? (FROM == kLists ? 4 : 3) : UNITS == 2 ? 1 : 2)
 lora_expand_few_kernel(Lora p)
 {
     constexpr int kRanks = UNITS * WORDS * 8, kVRow = kRanks * 2 + 16;   // bytes of a row of v
