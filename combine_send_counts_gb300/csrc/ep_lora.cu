@@ -17,7 +17,7 @@
 //     at a time.
 //
 // What bounds them: few rows, the chain of two dependent launches (24 rows, rank 16,
-// 4096 x 4096: 6.5 us, of which the bytes are 0.7); 1024 rows of 64 adapters 23 us;
+// 4096 x 4096: 5.4 us, of which the bytes are 0.7); 1024 rows of 64 adapters 21 us;
 // many rows, HBM and the start of expand (8192 rows, rank 64, 7168 x 4096: 62 us, 4.1 TB/s).
 #include <algorithm>
 #include <type_traits>
@@ -36,9 +36,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kUnit = 32;            // columns of a lane's 16-byte pieces: two k16 steps
 constexpr int kBatch = 4;            // units loaded together, and summed by matrix steps alone
 constexpr int kTile = kLoraTile;
-// Most rows of which each block finds its tile by itself: 64 rows of 64 adapters of rank 64 took 18 us so, and 96 took 10
-// to 25 us with a list.  (Of 256 rows of 64 adapters of rank 16, 17.5 us so and 13.2 with a list; of 1024, 55 and 23,
-// most of it for the blocks that look at all ids to find that they have no tile.)
+// Most rows of which each block finds its tile by itself.  (Of 256 rows of 64 adapters of rank 16, 17.5 us so and 13.2 with a
+// list; of 1024, 55 and 23, most of it for the blocks that look at all ids to find that they have no tile.  The list is a
+// launch more: 64 rows of 64 adapters 9.0 us without, 96 rows 10.3 with one.)
 constexpr int kSearchRows = 64;
 
 // The tile that begins with row m: `mine` is the row index of this lane's slot (lane & 15), or -1; false if no tile
@@ -458,15 +458,20 @@ lora_expand_few_kernel(Lora p)
 
 // ---------------------------------------------------------------- launch --
 // Kernels for few rows alone, for many alone, or both: each tile of 128 rows by the one or the other.  Measured with
-// 4096 x 4096 in us, few / many: 512 rows of one adapter of rank 16 10.4 / 10.8, of rank 64 17.9 / 16.5, 64 adapters at random
-// 15.7 / 107; 1024 rows of one 14.5 / 12.9 and 25.8 / 19.4, of 8 at random 14.9 / 33, of 64 at random 23 / 143; 8192 rows
-// of one of rank 64 161 / 49.  Both, of 64 adapters: 8192 rows of rank 64 in runs of 256 65 (few 170, many 52), at random
-// 220 (185, 1034); 2048 rows 42 (48, 26) and 113 (74, 298), less than few only where rows are in runs.
+// 4096 x 4096 in us, few / many / both:
+//                        rank 16                          rank 64
+//   rows    1 adapter      64 at random        1 adapter      64 at random
+//   512     11 / 11 / 18   15 / 128 / 22       15 / 15 / 22   29 / 197 / 42
+//   768     12 / 12 / 19   18 / 165 / 24       19 / 17 / 24   33 / 238 / 45
+//   1024    15 / 13 / 19   21 / 164 / 32       23 / 18 / 25   36 / 236 / 55
+//   2048    25 / 18 / 27   31 / 259 / 45       40 / 23 / 32   57 / 333 / 76
+//   8192    82 / 44 / 55   93 / 875 / 106      141 / 50 / 63  156 / 1033 / 189
+// Many alone where no tile can name more than eight (8192 rows of 8 at random: 84 / 165 and 142 / 187).
 enum Way { kFew, kMany, kMixed };
 
 Way way_of(int64_t M, int L)
 {
-    if (M <= 512 || (M <= 2048 && L > kLoraMostAdapters))
+    if (M <= 768 || (M <= 2048 && L > kLoraMostAdapters))
         return kFew;
     return L <= kLoraMostAdapters ? kMany : kMixed;
 }

@@ -723,7 +723,7 @@ int ep_router_select_backward(const void *logits, int dtype, int64_t T, int E, c
  *     are the same.
  * Sums are fp32; the result is rounded once.
  *   K, N, R % 8 == 0, R <= 128; M <= 2^24, K, N <= 2^23 (else EP_ERR_UNSUPPORTED).
- *   Rows may name adapters in any order; with more than 512, those of one adapter
+ *   Rows may name adapters in any order; with more than 768, those of one adapter
  *   are best neighbours.  An adapter's infinities and NaN stay its own rows'.
  *   ws: ep_lora_workspace_size(M, R) bytes, 256-byte aligned, scratch.  Calls that
  *     overlap on the GPU must not share it.

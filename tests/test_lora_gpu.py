@@ -156,7 +156,7 @@ def test_smaller_batches_than_the_workspace_is_for():
 @pytest.mark.parametrize("M,K,N,L,R", [(65, 72, 264, 40, 16), (130, 264, 40, 130, 24), (513, 64, 72, 9, 8),
                                        (700, 136, 264, 200, 64), (2048, 72, 40, 3000, 16), (2049, 264, 136, 20, 32),
                                        (2500, 64, 264, 9, 128), (8192, 72, 136, 70, 16), (8192, 64, 40, 9, 64),
-                                       (8193, 64, 72, 24, 8), (20000, 40, 72, 30, 16)])
+                                       (8193, 64, 72, 24, 8), (20000, 40, 72, 30, 16), (768, 72, 40, 8, 16), (769, 72, 40, 8, 16)])
 @pytest.mark.parametrize("base,out", [("bf16", "bf16"), ("fp32", "bf16")])
 @pytest.mark.parametrize("how", ["both", "turns", "last"])
 def test_long_requests_beside_short_ones(M, K, N, L, R, base, out, how):
