@@ -34,7 +34,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnit = 32;            // columns of a lane's 16-byte pieces: two k16 steps
-constexpr int kBatch = 4;            // units loaded together, and summed by matrix steps alone
 constexpr int kTile = kLoraTile;
 // Most rows of which each block finds its tile by itself.  (Of 256 rows of 64 adapters of rank 16, 17.5 us so and 13.2 with a
 // list; of 1024, 55 and 23, most of it for the blocks that look at all ids to find that they have no tile.  The list is a
@@ -199,6 +198,10 @@ template <int NT>
 __device__ __forceinline__ void product(float (&acc)[NT][4], const uint8_t *x0, const uint8_t *x1, const uint8_t *a,
                                         int R, int K, int u0, int u1)
 {
+    // Units whose x is loaded together, and which are summed by matrix steps alone: as many as leave registers for the
+    // ranks' loads ahead (24 rows of rank 64 8.8 us with one, 9.4 with two and 10.5 with four; of rank 128 13.0 with two, 13.4
+    // with one and 14.5 with four).
+    constexpr int kBatch = NT == 16 ? 2 : NT == 8 ? 1 : 4;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     for (int u = u0; u < u1; u += kBatch) {
         uint4 xa[kBatch], xb[kBatch];
@@ -246,7 +249,7 @@ __device__ __forceinline__ void leave(const Lora &p, const float (&acc)[NT][4], 
 }
 
 // A block takes tiles of a list (or one, without) and a part of K, its warps an eighth of that each.
-// Registers for two blocks to an SM up to rank 64, which fill it with loads: 2048 rows of 64 adapters of rank 64 in 57 us
+// Registers for two blocks to an SM up to rank 64, which fill it with loads: 2048 rows of 64 adapters of rank 64 in 53 us
 // instead of 76, as the compiler by itself left room for one, and 24 of rank 16 in 5.6 instead of 6.8, where it left
 // some for four.  Lists of long batches, of rank 16, are faster with four: 8192 rows 106 us, with two 131.
 template <int NT, int FROM>
