@@ -18,7 +18,7 @@
 //
 // What bounds them: few rows, the chain of two dependent launches (24 rows, rank 16,
 // 4096 x 4096: 5.4 us, of which the bytes are 0.7); 1024 rows of 64 adapters 21 us;
-// many rows, HBM and the start of expand (8192 rows, rank 64, 7168 x 4096: 62 us, 4.1 TB/s).
+// many rows, HBM and the start of expand (8192 rows, rank 64, 7168 x 4096: 61 us, 4.1 TB/s).
 #include <algorithm>
 #include <type_traits>
 

@@ -391,6 +391,7 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, const
     const int column0 = (warp >> 2) * 32, mine0 = (warp & 3) * 32, id = ids[mine0 + lane];
     const uint32_t room = rows_at + warp * kStages * S::kRoom;
     uint32_t rows = 0, mine = 0;   // of the pass: rows of these 32, and the slots that they name
+    bool one = false;              // they name one, and each does
     bool whole = false;            // no other row of the batch is among the 32
     int taken_in = 0, fetched = 0; // stages of the rows so far; of the base copied, by the one lane
     auto fetch = [&](int c, int use) {   // one lane
@@ -410,6 +411,7 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, const
         rows = __ballot_sync(kFull, in);
         whole = __all_sync(kFull, in || id == kNoRow);
         mine = pass.mask(id);
+        one = mine != 0 && (mine & (mine - 1u)) == 0 && !__any_sync(kFull, in && id == -1);
         if (lane == 0 && rows != 0) {
             bulk_wait_read<0>();
             for (int i = 0; i < S::kAhead; ++i)
@@ -525,17 +527,13 @@ lora_expand_many_kernel(Lora p, const __grid_constant__ CUtensorMap b_map, const
                     break;
                 if (rows != 0) {
                     float d[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        d[i] = -0.0f;   // base + -0 is base
                     const uint32_t from = sums + buf * kExpandSlots * kN;
-                    if (mine != 0 && (mine & (mine - 1u)) == 0) {   // rows of one adapter, or of none here
+                    if (one) {
                         tensor_load<32>(d, from + (__ffs(mine) - 1) * kN);
-                        if (id == -1)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                d[i] = -0.0f;
                     } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            d[i] = -0.0f;   // base + -0 is base
                         for (uint32_t todo = mine; todo != 0; todo &= todo - 1u) {
                             const int slot = __ffs(todo) - 1;
                             float f[32];
